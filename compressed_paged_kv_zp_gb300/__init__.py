@@ -31,6 +31,7 @@ EXPORTS = [
     "zp_decode_workspace_size", "zp_paged_decode_attn", "zp_paged_decode_attn_rho", "zp_paged_decode_attn_noalloc",
     "zp_debug_noalloc_preset_ctl", "zp_append_kv", "zp_needs_compression",
     "zp_needs_compression_batch",
+    "zp_build_slots", "zp_write_kv", "zp_prefix_plan", "zp_prefix_decode_workspace_size", "zp_prefix_decode_attn",
     "zp_window_score_workspace_size", "zp_window_score",
     "zp_score_workspace_size", "zp_score_tokens", "zp_select_topk", "zp_compact_pages",
     "zp_compress_workspace_size", "zp_compress_layers", "zp_compress_layers_rho", "zp_compress_rho_supported",
@@ -70,6 +71,11 @@ class ScoreRows(ctypes.Structure):
 class RhoRows(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64), ("layer_stride", ctypes.c_int64),
                 ("rows", ctypes.c_void_p), ("n_rows", ctypes.c_int32), ("threshold", ctypes.c_float)]
+
+
+class _PrefixGroups(ctypes.Structure):
+    _fields_ = [("prefix_lens", ctypes.c_void_p), ("n_groups", ctypes.c_void_p), ("group_start", ctypes.c_void_p),
+                ("members", ctypes.c_void_p), ("group_blocks", ctypes.c_void_p)]
 
 
 def _rho_rows(rho, rows, threshold=0.0):
@@ -122,6 +128,12 @@ def _load() -> ctypes.CDLL:
     lib.zp_paged_decode_attn_noalloc.argtypes = [D, P, P, P, P, I32, P, I32, P, P, P, I32, I32, P]
     lib.zp_debug_noalloc_preset_ctl.argtypes = [I32, ctypes.c_uint64]
     lib.zp_append_kv.argtypes = [D, P, P, P, P, P, I32, P, I32, P]
+    lib.zp_build_slots.argtypes = [D, P, P, I32, P, P, I32, P, I32, P, P, I32, P, P, P]
+    lib.zp_write_kv.argtypes = [D, P, P, I64, I64, P, I32, P, P, I64, I32, P]
+    lib.zp_prefix_plan.argtypes = [D, P, I32, P, I32, I32, I32, P, P]
+    lib.zp_prefix_decode_workspace_size.restype = SZ
+    lib.zp_prefix_decode_workspace_size.argtypes = [D, I32, I32]
+    lib.zp_prefix_decode_attn.argtypes = [D, P, P, P, P, I32, P, I32, P, P, P, P, I32, I32, P, SZ, P]
     lib.zp_needs_compression.argtypes = [I32, I32, I32]
     lib.zp_needs_compression_batch.argtypes = [P, P, I32, I32, I32, P, P, P]
     lib.zp_score_workspace_size.restype = SZ
@@ -250,6 +262,168 @@ def zp_append_kv(desc, k_new, v_new, k_cache, v_cache, block_table, seq_lens, st
                             _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
                             _dev(block_table, "block_table"), table_stride, _dev(seq_lens, "seq_lens"),
                             B, _stream(stream)))
+
+
+# ----------------------------------------------------------------------------- shared prompts
+def _ints(t, name: str, numel=None):
+    """Pointer of an int32 CUDA tensor (None stays None) of `numel` elements, on the current device."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32:
+        raise ValueError("%s must be int32" % name)
+    if numel is not None and t.numel() != numel:
+        raise ValueError("%s must have %d elements, has %d" % (name, numel, t.numel()))
+    return _here(t, name)
+
+
+def _here(t, name: str):
+    """Pointer of a contiguous CUDA tensor on the current device (None stays None)."""
+    if t is None:
+        return None
+    p = _dev(t, name)
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, torch.cuda.current_device()))
+    return p
+
+
+def _table(block_table):
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B][table_stride]")
+    return int(block_table.shape[0]), int(block_table.shape[1])
+
+
+def _cache_dtype(desc, t, name: str):
+    if _DTYPES.get(t.dtype) != desc.dtype:
+        raise ValueError("%s is %s, not the cache's type" % (name, t.dtype))
+
+
+def _cache_shape(desc, t, name: str):
+    if tuple(t.shape[-4:]) != (desc.n_total_blocks, desc.block_size, desc.h_kv, desc.head_dim):
+        raise ValueError("%s must be [N_total][b][h_kv][d] (or one of these per layer), is %s" % (name, tuple(t.shape)))
+
+
+def zp_build_slots(desc, block_table, old_lens, new_lens, slots, cu_tokens, fresh=None, table_out=None, positions=None,
+                   n_used=None, stream=None) -> None:
+    """Grow the block table from old_lens to new_lens with the blocks of `fresh`
+    (int32, in the order they go out) and write the slot map of the new tokens:
+    slots and positions int32 [max_tokens] (padded with -1), cu_tokens [B+1],
+    n_used [1].  table_out: a separate table for the result (None: in place)."""
+    B, table_stride = _table(block_table)
+    if table_out is None:
+        table_out = block_table
+    elif table_out.shape != block_table.shape:
+        raise ValueError("table_out must have block_table's shape")
+    _check(lib.zp_build_slots(ctypes.byref(desc), _ints(block_table, "block_table"), _ints(table_out, "table_out"),
+                              table_stride, _ints(old_lens, "old_lens", B), _ints(new_lens, "new_lens", B), B,
+                              _ints(fresh, "fresh"), 0 if fresh is None else fresh.numel(), _ints(slots, "slots"),
+                              _ints(positions, "positions", slots.numel()), slots.numel(),
+                              _ints(cu_tokens, "cu_tokens", B + 1), _ints(n_used, "n_used", 1), _stream(stream)))
+
+
+def zp_write_kv(desc, k_new, v_new, slots, k_cache, v_cache, stream=None) -> None:
+    """Store the rows of n tokens into their slots (int32 [n]; negative: skipped).
+    k_new, v_new: [n][h_kv][d] for one layer, or [layers][n][h_kv][d] with caches
+    [layers][N_total][b][h_kv][d].  The rows [h_kv][d] are contiguous; the token
+    and layer strides are free (a slice of a fused projection)."""
+    row = (desc.h_kv, desc.head_dim)
+    layers = int(k_cache.shape[0]) if k_cache.dim() == 5 else 1
+    lead = (layers,) if k_cache.dim() == 5 else ()
+    n = int(slots.numel())
+    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
+        if tuple(t.shape) != lead + (n,) + row:
+            raise ValueError("%s must be %s, is %s" % (name, lead + (n,) + row, tuple(t.shape)))
+        _cache_dtype(desc, t, name)
+        if not t.is_cuda or t.device.index != torch.cuda.current_device():
+            raise ValueError("%s must be a CUDA tensor on the current device" % name)
+        if n and t.stride()[-2:] != (desc.head_dim, 1):
+            raise ValueError("%s: the row of a token must be contiguous" % name)
+    if n and k_new.stride() != v_new.stride():
+        raise ValueError("k_new and v_new must have the same strides")
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _cache_dtype(desc, t, name)
+        _cache_shape(desc, t, name)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same shape")
+    if n == 0:
+        return
+    token_stride = int(k_new.stride(-3)) if n > 1 else max(int(k_new.stride(-3)), row[0] * row[1])
+    _check(lib.zp_write_kv(ctypes.byref(desc), ctypes.c_void_p(k_new.data_ptr()), ctypes.c_void_p(v_new.data_ptr()),
+                           token_stride, int(k_new.stride(0)) if layers > 1 else 0, _ints(slots, "slots"), n,
+                           _here(k_cache, "k_cache"), _here(v_cache, "v_cache"),
+                           int(k_cache.stride(0)) if layers > 1 else 0, layers, _stream(stream)))
+
+
+class PrefixPlan:
+    """Groups of batch entries that share leading blocks: int32 CUDA tensors
+    prefix_lens [B], n_groups [1], group_start [B+1], members [B], group_blocks
+    [B] (see zp_prefix_groups in zp.h).  zp_prefix_plan fills them from the block
+    table; a scheduler that knows its groups may fill them itself."""
+
+    def __init__(self, prefix_lens, n_groups, group_start, members, group_blocks):
+        B = int(prefix_lens.numel())
+        self.B = B
+        self.prefix_lens, self.n_groups, self.group_start = prefix_lens, n_groups, group_start
+        self.members, self.group_blocks = members, group_blocks
+        self._c = _PrefixGroups(*(None if p is None else p.value for p in (
+            _ints(prefix_lens, "prefix_lens", B), _ints(n_groups, "n_groups", 1), _ints(group_start, "group_start", B + 1),
+            _ints(members, "members", B), _ints(group_blocks, "group_blocks", B))))
+
+
+def prefix_plan(B: int, device="cuda") -> PrefixPlan:
+    """An empty plan (no groups) for B batch entries."""
+    buf = torch.zeros(4 * B + 2, dtype=torch.int32, device=device)
+    buf[2 * B + 2:3 * B + 2] = -1
+    return PrefixPlan(buf[:B], buf[B:B + 1], buf[B + 1:2 * B + 2], buf[2 * B + 2:3 * B + 2], buf[3 * B + 2:])
+
+
+def zp_prefix_plan(desc, block_table, seq_lens, plan: PrefixPlan, min_blocks=1, min_members=2, stream=None) -> None:
+    """Find the groups that share at least min_blocks leading blocks among at least min_members entries."""
+    B, table_stride = _table(block_table)
+    if plan.B != B:
+        raise ValueError("the plan is for %d batch entries, the table has %d" % (plan.B, B))
+    _check(lib.zp_prefix_plan(ctypes.byref(desc), _ints(block_table, "block_table"), table_stride,
+                              _ints(seq_lens, "seq_lens", B), B, int(min_blocks), int(min_members),
+                              ctypes.byref(plan._c), _stream(stream)))
+
+
+def zp_prefix_decode_workspace_size(desc: CacheDesc, B: int, table_stride: int) -> int:
+    n = lib.zp_prefix_decode_workspace_size(ctypes.byref(desc), int(B), int(table_stride))
+    if n == 0 and B > 0:
+        raise ZPError(2, lib.zp_last_error().decode() or "unsupported decode shape")
+    return int(n)
+
+
+def zp_prefix_decode_attn(desc, q, k_cache, v_cache, block_table, seq_lens, plan: PrefixPlan, out, score_accum=None,
+                          window=0, workspace=None, stream=None, score_rows=None) -> None:
+    """zp_paged_decode_attn with every group's shared prefix computed once for all its members."""
+    B, table_stride = _table(block_table)
+    if plan.B != B:
+        raise ValueError("the plan is for %d batch entries, the table has %d" % (plan.B, B))
+    for t, name in ((q, "q"), (out, "out")):
+        if tuple(t.shape) != (B, desc.h_q, desc.head_dim):
+            raise ValueError("%s must be [B][h_q][d], is %s" % (name, tuple(t.shape)))
+        _cache_dtype(desc, t, name)
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _cache_dtype(desc, t, name)
+        _cache_shape(desc, t, name)
+    rows_p, n_rows = _slot_map(score_accum, score_rows)
+    if score_accum is not None and (score_accum.dtype != torch.float32 or score_accum.dim() != 3 or
+                                    tuple(score_accum.shape[1:]) != (desc.h_kv, table_stride * desc.block_size) or
+                                    (score_rows is None and score_accum.shape[0] < B)):
+        raise ValueError("score_accum must be float32 [R][h_kv][table_stride*b] with a row per batch entry or a slot map")
+    if score_rows is not None and score_rows.numel() != B:
+        raise ValueError("score_rows must have one entry per batch entry")
+    if workspace is None:
+        workspace = torch.empty(zp_prefix_decode_workspace_size(desc, B, table_stride), dtype=torch.uint8,
+                                device=q.device)
+        if stream is not None:
+            workspace.record_stream(stream)  # not reused before this call's work on that stream
+    _check(lib.zp_prefix_decode_attn(ctypes.byref(desc), _here(q, "q"), _here(k_cache, "k_cache"),
+                                     _here(v_cache, "v_cache"), _ints(block_table, "block_table"), table_stride,
+                                     _ints(seq_lens, "seq_lens", B), B, ctypes.byref(plan._c), _here(out, "out"),
+                                     _here(score_accum, "score_accum"), rows_p, n_rows, int(window),
+                                     _here(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+                                     _stream(stream)))
 
 
 # ----------------------------------------------------------------------------- compression
@@ -496,6 +670,8 @@ class Pool:
 __all__ = ["lib", "LIB_PATH", "EXPORTS", "ZPError", "CacheDesc", "ScoreParams", "ScoreRows", "RhoRows", "score_params",
            "cache_desc", "zp_decode_workspace_size", "zp_paged_decode_attn",
            "zp_paged_decode_attn_noalloc", "zp_append_kv",
+           "zp_build_slots", "zp_write_kv", "PrefixPlan", "prefix_plan", "zp_prefix_plan",
+           "zp_prefix_decode_workspace_size", "zp_prefix_decode_attn",
            "zp_needs_compression", "zp_needs_compression_batch", "zp_window_score_workspace_size", "zp_window_score",
            "zp_score_workspace_size", "zp_score_tokens", "zp_select_topk",
            "zp_compact_pages", "zp_compress_workspace_size", "zp_compress_layers", "zp_compress_rho_supported", "zp_plan_capacity", "zp_device_status", "Pool",

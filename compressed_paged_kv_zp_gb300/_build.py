@@ -20,7 +20,8 @@ OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libzp.so")
 
 SOURCES = ["zp_api.cu", "decode_attn.cu", "append_kv.cu", "window_score.cu", "score.cu", "redundancy.cu", "topk.cu",
-           "compact.cu", "pool.cpp", "sched.cpp"]
+           "compact.cu", "slots.cu", "prefix_plan.cu", "prefix_attn.cu", "decode_attn_prefix.cu", "pool.cpp", "sched.cpp"]
+INCLUDED = {"decode_attn_prefix.cu": ["decode_attn.cu"]}  # sources that a source includes
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -40,6 +41,7 @@ def _compile(src: str, verbose: bool) -> str:
     path = os.path.join(CSRC, src)
     headers = [os.path.join(CSRC, h) for h in os.listdir(CSRC) if h.endswith((".h", ".cuh"))]
     headers += [os.path.join(INCLUDE, h) for h in ("zp.h", "zp_sched.h")]
+    headers += [os.path.join(CSRC, s) for s in INCLUDED.get(src, [])]
     newest = max(os.path.getmtime(p) for p in [path, __file__] + headers)
     if os.path.exists(obj) and os.path.getmtime(obj) >= newest:
         return obj

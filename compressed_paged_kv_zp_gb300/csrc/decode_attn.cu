@@ -39,9 +39,21 @@
 #include "lightning.cuh"
 #include "zp_common.cuh"
 
+// decode_attn_prefix.cu compiles this file once more with ZP_DECODE_PREFIX 1:
+// the decode of the tokens behind a shared prefix.  A sequence with a prefix of
+// p tokens (a multiple of b) is then the sequence of its other L - p tokens:
+// its table row starts p/b entries later, its score row p tokens later, and its
+// online softmax starts from the prefix's record (max, sum, accumulator) where
+// a CTA takes its first unit, instead of from nothing.  Everything else (the
+// split, the merges, the score) is unchanged.
+#ifndef ZP_DECODE_PREFIX
+#define ZP_DECODE_PREFIX 0
+#endif
+
 namespace zp {
 namespace {
 
+constexpr bool kPrefix = ZP_DECODE_PREFIX != 0;
 constexpr int kMaxConsumerWarps = 16;
 constexpr int kStageBytesCap = 32768;  // per tensor and stage
 constexpr int kMaxB = 4096;
@@ -90,7 +102,25 @@ struct DecodeArgs {
     float rho_p;              // similarity threshold p
     int rho_weight16;         // stream-K weight of a unit with row sums, in sixteenths of a plain unit
     unsigned *err;
+    // shared prefix (kPrefix): tokens per batch entry and the records its softmax starts from
+    const int32_t *prefix_lens;  // [B]
+    const float *init_acc;       // [B][h_q][D] unnormalised accumulator
+    const float2 *init_ml;       // [B][h_q] (max, sum), log2 units
 };
+
+// Tokens of sequence s (of L) that its prefix record covers: none when the plan
+// names more than the L - 1 that precede the newest token (the sequence is then
+// decoded from its first token).
+__device__ __forceinline__ int prefix_of(const DecodeArgs &a, int s, int L) {
+    if constexpr (!kPrefix) return 0;
+    const int p = __ldg(&a.prefix_lens[s]);
+    return p > 0 && p < L && p % a.b == 0 ? p : 0;
+}
+// The same from the sequence's index alone.
+__device__ __forceinline__ int prefix_of(const DecodeArgs &a, int s) {
+    if constexpr (!kPrefix) return 0;
+    return prefix_of(a, s, min(__ldg(&a.seq_lens[s]), a.table_stride * a.b));
+}
 
 // Reduce-scatter of V per-lane values over the 16 lanes of a half-warp (lane
 // bits 3..0, high bit first).  Afterwards lane l holds in v[0..max(V/16,1))
@@ -271,7 +301,7 @@ __global__ void __launch_bounds__(kMaxConsumerWarps * 32, 1)
             record_error(a.err, ZP_ERR_DEVICE, 2);
             L = maxL;
         }
-        lens[s] = L;
+        lens[s] = kPrefix ? L - prefix_of(a, s, L) : L;
     }
     if (tid == 0) {
         abort_flag[0] = 0;
@@ -345,7 +375,7 @@ __global__ void __launch_bounds__(kMaxConsumerWarps * 32, 1)
         const int tok0 = j * TU;
         int valid = lens[ps] - tok0;
         if (valid > TU) valid = TU;
-        const int blk = __ldg(&a.table[(size_t)ps * a.table_stride + tok0 / a.b]);
+        const int blk = __ldg(&a.table[(size_t)ps * a.table_stride + (prefix_of(a, ps) + tok0) / a.b]);
         if (a.want_score) a.unit_info[u] = unit_record(a, ps, tok0, lens[ps]);
         unsigned char *ks = stage_base + (size_t)st * 2 * stage_bytes;
         unsigned char *vs = ks + stage_bytes;
@@ -407,6 +437,29 @@ __global__ void __launch_bounds__(kMaxConsumerWarps * 32, 1)
 #pragma unroll
         for (int i = 0; i < NV; ++i) l_own[i] = 0.f;
     };
+    // the state a sequence starts from: its prefix's record when this CTA takes
+    // its first unit (accumulator in the first half-warp of the head's first
+    // warp, the sum in the lanes that own it), else nothing
+    auto start_state = [&](int s, bool first_unit) {
+        reset_state();
+        if constexpr (kPrefix) {
+            if (!first_unit || wih != 0 || prefix_of(a, s) == 0) return;
+            const float2 *iml = a.init_ml + (size_t)s * a.h_q + h0;
+#pragma unroll
+            for (int j = 0; j < G; ++j) m[j] = __ldg(&iml[j]).x;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (owner) l_own[i] = __ldg(&iml[jv[i]]).y;
+            if (half == 0) {
+                const float *ia = a.init_acc + ((size_t)s * a.h_q + h0) * D + lane16 * DPL;
+#pragma unroll
+                for (int j = 0; j < G; ++j)
+#pragma unroll
+                    for (int p = 0; p < DPL / 2; ++p)
+                        acc[j][p] = __ldg(reinterpret_cast<const float2 *>(ia + (size_t)j * D) + p);
+            }
+        }
+    };
     auto load_q = [&](int s) {
         const T *qg = static_cast<const T *>(a.q) + ((size_t)s * a.h_q + h0) * D + lane16 * DPL;
 #pragma unroll
@@ -421,7 +474,7 @@ __global__ void __launch_bounds__(kMaxConsumerWarps * 32, 1)
 
     int s = s_first;
     long long seg_begin = u0;
-    reset_state();
+    start_state(s, u0 == prefix[s]);
     load_q(s);
     bool window_step = false;
     auto compute_window = [&](int seq) {
@@ -639,7 +692,7 @@ __global__ void __launch_bounds__(kMaxConsumerWarps * 32, 1)
             if (u + 1 < u1) {
                 while (u + 1 >= prefix[s + 1]) ++s;
                 seg_begin = u + 1;
-                reset_state();
+                start_state(s, true);
                 load_q(s);
                 window_step = compute_window(s);
             }
@@ -695,7 +748,7 @@ __global__ void __launch_bounds__(128) decode_score_kernel(const DecodeArgs a) {
 #pragma unroll
         for (int j = 0; j < G; ++j) best = fmaxf(best, exp2f(x[j] - ml[j].x) / ml[j].y);
         const float c = best * inv_w;
-        float *dst = a.score + ((size_t)score_row_of(a, s) * a.h_kv + kvh) * a.score_stride + tok;
+        float *dst = a.score + ((size_t)score_row_of(a, s) * a.h_kv + kvh) * a.score_stride + prefix_of(a, s) + tok;
         *dst = (first_row || tok == P) ? c : (*dst + c);
     }
 }
@@ -898,6 +951,9 @@ __device__ void part_stats(const DecodeArgs &a, int s, const int *prefix, const 
             M = Mn;
         }
         out[h] = Lsum > 0.f ? M + log2f(Lsum) : INFINITY;
+        // the prefix's score pass reads every sequence's final statistics (each
+        // part-holder writes the same value)
+        if constexpr (kPrefix) a.stats[(size_t)s * h_q + h] = make_float2(M, Lsum);
     }
 }
 
@@ -1064,7 +1120,7 @@ __device__ void score_segment(const DecodeArgs &a, int s, int L, long long p0, i
     const int RSF = CT + 4;  // score piece stride in floats (bank shift of 4 per kv head)
     float *lg_s = reinterpret_cast<float *>(buf);
     float *sc_s = lg_s + (size_t)CT * HQ;
-    float *srow0 = a.score + (size_t)score_row_of(a, s) * HKV * a.score_stride;
+    float *srow0 = a.score + (size_t)score_row_of(a, s) * HKV * a.score_stride + prefix_of(a, s);
     const float *lg_g = a.logits + ((size_t)p0 * kTcTokens) * HQ;
     fence_proxy_async_smem();  // earlier ordinary writes to buf precede the copies into it
     named_bar_sync(1, nthr);
@@ -1113,7 +1169,7 @@ __device__ void score_prefetched(const DecodeArgs &a, int s, int L, int tb, int 
     fence_proxy_async_smem();
     named_bar_sync_id<BAR>(nthr);
     if (ctid == 0) {
-        float *srow0 = a.score + (size_t)score_row_of(a, s) * HKV * a.score_stride;
+        float *srow0 = a.score + (size_t)score_row_of(a, s) * HKV * a.score_stride + prefix_of(a, s);
 #pragma unroll
         for (int kvh = 0; kvh < HKV; ++kvh)
             bulk_s2g(srow0 + (size_t)kvh * a.score_stride + tb, sc_s + kvh * RSF, (unsigned)(n16 * 4));
@@ -1183,7 +1239,7 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
             record_error(a.err, ZP_ERR_DEVICE, 2);
             L = maxL;
         }
-        lens[s] = L;
+        lens[s] = kPrefix ? L - prefix_of(a, s, L) : L;
         if (weighted) wgt[s] = a.rho_rows[s] >= 0 ? a.rho_weight16 : 16;
     }
     if (tid == 0) {
@@ -1290,15 +1346,19 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
         while (u0 >= prefix[ns + 1]) ++ns;
         int cur_s = ns;
         int ntok0 = (int)(u0 - prefix[ns]) * kTcTokens;
-        int nblk = __ldg(&a.table[(size_t)ns * a.table_stride + ntok0 / a.b]);
+        int npre = prefix_of(a, ns);  // tokens of the sequence before its first unit
+        int nblk = __ldg(&a.table[(size_t)ns * a.table_stride + (npre + ntok0) / a.b]);
         for (long long u = u0, i = 0; u < u1; ++u, ++i) {
             const int tok0 = ntok0;
             const int blk = nblk;
             const int useq = cur_s;
             if (u + 1 < u1) {
-                while (u + 1 >= prefix[ns + 1]) ++ns;
+                if (u + 1 >= prefix[ns + 1]) {
+                    while (u + 1 >= prefix[ns + 1]) ++ns;
+                    npre = prefix_of(a, ns);
+                }
                 ntok0 = (int)(u + 1 - prefix[ns]) * kTcTokens;
-                nblk = __ldg(&a.table[(size_t)ns * a.table_stride + ntok0 / a.b]);
+                nblk = __ldg(&a.table[(size_t)ns * a.table_stride + (npre + ntok0) / a.b]);
             }
             cur_s = ns;
             const int st = (int)(i % a.stages);
@@ -1317,7 +1377,7 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
                     int te = (int)(ue - prefix[useq]) * kTcTokens;
                     if (te > L) te = L;
                     const unsigned bytes = (unsigned)(((te - tok0) * 4 + 15) & ~15);
-                    bulk_prefetch_l2(a.score + ((size_t)row * h_kv + lane) * a.score_stride + tok0, bytes);
+                    bulk_prefetch_l2(a.score + ((size_t)row * h_kv + lane) * a.score_stride + prefix_of(a, useq) + tok0, bytes);
                 }
             }
             if (lane == 0) {
@@ -1362,6 +1422,32 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
     };
+    // the state a sequence starts from: its prefix's record when this CTA takes
+    // its first unit, in the lanes that hold the rows and columns of each head
+    auto start_state = [&](int s, bool first_unit) {
+        reset_state();
+        if constexpr (kPrefix) {
+            if (!first_unit || prefix_of(a, s) == 0) return;
+            if (g < G) {
+                const float2 ml = __ldg(&a.init_ml[(size_t)s * a.h_q + h0 + g]);
+                m_run = ml.x;
+                l_run = ml.y;
+            }
+            const float *ia = a.init_acc + ((size_t)s * a.h_q + h0) * D;
+#pragma unroll
+            for (int t = 0; t < KS; ++t) {
+                const int d0 = 16 * t + g;
+                if (2 * tig < G) {
+                    acc[t][0] = __ldg(ia + (size_t)(2 * tig) * D + d0);
+                    acc[t][2] = __ldg(ia + (size_t)(2 * tig) * D + d0 + 8);
+                }
+                if (2 * tig + 1 < G) {
+                    acc[t][1] = __ldg(ia + (size_t)(2 * tig + 1) * D + d0);
+                    acc[t][3] = __ldg(ia + (size_t)(2 * tig + 1) * D + d0 + 8);
+                }
+            }
+        }
+    };
     auto load_q = [&](int s) {
         const uint32_t *qg = reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(a.q) +
                                                               ((size_t)s * a.h_q + h0 + g) * D);
@@ -1389,7 +1475,7 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
     int s = s_first;
     long long seg_begin = u0;
     const uint64_t keep_pol = l2_evict_last_policy();
-    reset_state();
+    start_state(s, u0 == prefix[s]);
     load_q(s);
     bool window_step = compute_window(s);
     int rho_row = rho_row_of(s);
@@ -1562,7 +1648,7 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
             if (u + 1 < u1) {
                 while (u + 1 >= prefix[s + 1]) ++s;
                 seg_begin = u + 1;
-                reset_state();
+                start_state(s, true);
                 load_q(s);
                 window_step = compute_window(s);
                 rho_row = rho_row_of(s);
@@ -1620,7 +1706,8 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
                     float *sc_s = lg_s + (size_t)n16 * HQ;
                     bulk_g2s_plain(lg_s, a.logits + ((size_t)prefix[g.x] * kTcTokens + g.y) * HQ,
                                    (unsigned)(n16 * HQ * 4), ebar);
-                    const float *srow0 = a.score + (size_t)score_row_of(a, g.x) * h_kv * a.score_stride + g.y;
+                    const float *srow0 =
+                        a.score + (size_t)score_row_of(a, g.x) * h_kv * a.score_stride + prefix_of(a, g.x) + g.y;
                     for (int kvh = 0; kvh < h_kv; ++kvh)
                         bulk_g2s_plain(sc_s + kvh * (n16 + 4), srow0 + (size_t)kvh * a.score_stride,
                                        (unsigned)(n16 * 4), ebar);
@@ -2045,6 +2132,7 @@ zp_status launch_t(const DecodeArgs &a, const Plan &p, const DeviceInfo &dev, cu
 
 using namespace zp;
 
+#if !ZP_DECODE_PREFIX
 extern "C" size_t zp_decode_workspace_size(const zp_cache_desc *D, int32_t B, int32_t table_stride) {
     if (check_desc(D) != ZP_OK || B < 0 || table_stride < 0) return 0;
     DeviceInfo dev;
@@ -2054,11 +2142,13 @@ extern "C" size_t zp_decode_workspace_size(const zp_cache_desc *D, int32_t B, in
     return p.total;
 }
 
+#endif
+
 static zp_status decode_impl(const zp_cache_desc *D, const void *q, const void *k_cache, const void *v_cache,
                              const int32_t *block_table, int32_t table_stride, const int32_t *seq_lens, int32_t B,
                              void *out, float *score_accum, const int32_t *score_rows, int32_t n_score_rows,
                              int32_t window, void *workspace, size_t workspace_bytes, void *stream,
-                             const zp_rho_rows *rho) {
+                             const zp_rho_rows *rho, const PrefixRecords *pre) {
     zp_status rc = check_desc(D);
     if (rc != ZP_OK) return rc;
     if (B < 0 || table_stride < 0) return fail(ZP_ERR_INVALID_ARG, "decode: B or table_stride negative");
@@ -2134,6 +2224,9 @@ static zp_status decode_impl(const zp_cache_desc *D, const void *q, const void *
     a.rho_weight16 = (rho && p.tc && max_units * kRhoUnitWeight16 < 2.0e9 && (2LL * B + 1) * 4 <= stage_area)
                          ? kRhoUnitWeight16 : 16;
     a.err = dev.error_word;
+    a.prefix_lens = pre ? pre->prefix_lens : nullptr;
+    a.init_acc = pre ? pre->acc : nullptr;
+    a.init_ml = pre ? pre->ml : nullptr;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int G = D->h_q / D->h_kv;
     const int d = D->head_dim;
@@ -2161,6 +2254,23 @@ static zp_status decode_impl(const zp_cache_desc *D, const void *q, const void *
     return fail(ZP_ERR_SHAPE, "decode: no kernel for d=%d, group=%d", d, G);
 }
 
+#if ZP_DECODE_PREFIX
+zp_status zp::decode_after_prefix(const zp_cache_desc *D, const void *q, const void *k_cache, const void *v_cache,
+                                  const int32_t *block_table, int32_t table_stride, const int32_t *seq_lens, int32_t B,
+                                  void *out, float *score_accum, const int32_t *score_rows, int32_t n_score_rows,
+                                  int32_t window, const PrefixRecords &pre, void *workspace, size_t workspace_bytes,
+                                  void *stream, const float2 **stats) {
+    DeviceInfo dev;
+    zp_status rc = device_info(&dev);
+    if (rc != ZP_OK) return rc;
+    Plan p;
+    rc = make_plan(D, B, table_stride, dev, &p);
+    if (rc != ZP_OK) return rc;
+    *stats = reinterpret_cast<const float2 *>(static_cast<unsigned char *>(workspace) + p.off_stats);
+    return decode_impl(D, q, k_cache, v_cache, block_table, table_stride, seq_lens, B, out, score_accum, score_rows,
+                       n_score_rows, window, workspace, workspace_bytes, stream, nullptr, &pre);
+}
+#else
 extern "C" zp_status zp_paged_decode_attn(const zp_cache_desc *D, const void *q, const void *k_cache,
                                           const void *v_cache, const int32_t *block_table,
                                           int32_t table_stride, const int32_t *seq_lens, int32_t B,
@@ -2168,7 +2278,7 @@ extern "C" zp_status zp_paged_decode_attn(const zp_cache_desc *D, const void *q,
                                           int32_t n_score_rows, int32_t window, void *workspace,
                                           size_t workspace_bytes, void *stream) {
     return decode_impl(D, q, k_cache, v_cache, block_table, table_stride, seq_lens, B, out, score_accum, score_rows,
-                       n_score_rows, window, workspace, workspace_bytes, stream, nullptr);
+                       n_score_rows, window, workspace, workspace_bytes, stream, nullptr, nullptr);
 }
 
 extern "C" zp_status zp_paged_decode_attn_rho(const zp_cache_desc *D, const void *q, const void *k_cache,
@@ -2178,7 +2288,7 @@ extern "C" zp_status zp_paged_decode_attn_rho(const zp_cache_desc *D, const void
                                               int32_t n_score_rows, int32_t window, const zp_rho_rows *rho,
                                               void *workspace, size_t workspace_bytes, void *stream) {
     return decode_impl(D, q, k_cache, v_cache, block_table, table_stride, seq_lens, B, out, score_accum, score_rows,
-                       n_score_rows, window, workspace, workspace_bytes, stream, rho);
+                       n_score_rows, window, workspace, workspace_bytes, stream, rho, nullptr);
 }
 
 // ---------------------------------------------------------------------------
@@ -2258,3 +2368,4 @@ extern "C" zp_status zp_debug_noalloc_preset_ctl(int32_t seq, uint64_t word) {
     if (e != cudaSuccess) return cuda_fail(e, "noalloc_preset_ctl: cudaMemcpyToSymbol");
     return ok();
 }
+#endif  // !ZP_DECODE_PREFIX

@@ -1,0 +1,716 @@
+// prefix_attn.cu -- decode attention of a batch whose sequences share prefixes:
+// the shared part computed once per group for all its members.
+//
+// For a group of n sequences that share p prefix tokens, the G query rows of a
+// kv head of every member form one matrix of n*G rows, and its attention to the
+// shared keys and values is a dense product:
+//     x = log2(e)/sqrt(d) Q K^T,  m_r = max_t x_rt,  l_r = sum_t 2^(x_rt - m_r),
+//     acc_r = sum_t 2^(x_rt - m_r) v_t.
+// (m, l, acc) of every (sequence, q head) is the state from which the decode of
+// the sequence's other tokens starts (decode_attn_prefix.cu), so the result is
+// the softmax over all tokens and the shared keys and values are read once per
+// group instead of once per sequence.  With the window score, the final (m, l)
+// of every sequence that is on a window step give a second pass over the shared
+// keys: S[t] (+)= (1/w) max_{h in group} 2^(x_ht - m_h) / l_h.
+//
+// Work: an item is (group, kv head, tile of query rows), its length the group's
+// tiles of prefix tokens.  The tiles of all items are concatenated and every CTA
+// takes an equal contiguous range (as the decode does with its units), so any
+// mix of group sizes and prefix lengths fills the GPU.  The first piece of an
+// item goes to its rows' place in the main records, a piece that begins inside
+// an item (at most one per CTA) to the CTA's extra records; a merge kernel joins
+// the pieces of each row.
+#include <math.h>
+
+#include "zp_common.cuh"
+
+namespace zp {
+namespace {
+
+constexpr int kPfxMaxB = 4096;
+constexpr int kPfxThreads = 256;
+constexpr int kPfxRows = 64;    // query rows per item (CUDA-core kernel)
+constexpr int kPfxTokens = 64;  // prefix tokens per tile (CUDA-core kernel)
+
+struct PfxArgs {
+    const void *q, *k, *v;
+    const int32_t *table;
+    int stride;
+    const int32_t *seq_lens;
+    int B, h_q, h_kv, b, n_total;
+    // the plan
+    const int32_t *n_groups, *group_start, *members, *group_blocks;
+    int rt, kt;          // rows per item, tokens per tile
+    int parts;           // CTAs of the prefix kernel (split of the tiles)
+    float qscale;        // log2(e) / sqrt(d)
+    int *wpre;           // [B+1] tiles before each group
+    int32_t *prefix;     // [B] prefix tokens of every batch entry, 0 = none
+    float *rec_acc;      // [B*h_q + parts*rt][d] pieces: main records, then extra records
+    float2 *rec_ml;      // same rows
+    float *init_acc;     // [B][h_q][d]
+    float2 *init_ml;     // [B][h_q]
+    // score
+    float *score;
+    long long score_stride;
+    const int32_t *score_rows;
+    int n_score_rows, window;
+    const float2 *stats;  // [B][h_q] final (max, sum)
+    unsigned *err;
+};
+
+// Group g of the plan, with every index the plan gives bounded.
+struct PfxGroup {
+    int m0, n;    // first member, members
+    int tokens;   // prefix tokens
+    int rts, kts; // row tiles, token tiles
+};
+
+__device__ __forceinline__ int pfx_groups(const PfxArgs &a) { return min(max(__ldg(a.n_groups), 0), a.B); }
+
+__device__ __forceinline__ PfxGroup pfx_group(const PfxArgs &a, int g) {
+    PfxGroup r;
+    r.m0 = min(max(__ldg(a.group_start + g), 0), a.B);
+    r.n = min(max(__ldg(a.group_start + g + 1), r.m0), a.B) - r.m0;
+    r.tokens = min(max(__ldg(a.group_blocks + g), 0), a.stride) * a.b;
+    r.rts = (r.n * (a.h_q / a.h_kv) + a.rt - 1) / a.rt;
+    r.kts = (r.tokens + a.kt - 1) / a.kt;
+    return r;
+}
+
+// Batch entry of member i; an entry outside the batch is recorded, -1.
+__device__ __forceinline__ int pfx_member(const PfxArgs &a, int i) {
+    const int s = __ldg(a.members + i);
+    if (s < 0 || s >= a.B) {
+        record_error(a.err, ZP_ERR_DEVICE, 0x142);
+        return -1;
+    }
+    return s;
+}
+
+__device__ __forceinline__ int pfx_start(int c, int W, int parts) { return (int)((long long)c * W / parts); }
+
+// last g in [0, n) with pre[g] <= x
+__device__ __forceinline__ int pfx_find(const int *pre, int n, int x) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (pre[mid] <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// CTA whose range holds tile w
+__device__ __forceinline__ int pfx_owner(int w, int W, int parts) {
+    int c = (int)((long long)w * parts / W);
+    while (c + 1 < parts && pfx_start(c + 1, W, parts) <= w) ++c;
+    while (c > 0 && pfx_start(c, W, parts) > w) --c;
+    return c;
+}
+
+// Tiles before each group (whole CTA; pre: n_groups + 1 ints of shared memory);
+// returns the total.
+__device__ int pfx_scan(const PfxArgs &a, int ng, int *pre) {
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int carry = 0;
+        for (int base = 0; base < ng; base += 32) {
+            int x = 0;
+            if (base + lane < ng) {
+                const PfxGroup g = pfx_group(a, base + lane);
+                x = a.h_kv * g.rts * g.kts;
+            }
+            int v = x;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xFFFFFFFFu, v, o);
+                if (lane >= o) v += y;
+            }
+            if (base + lane < ng) pre[base + lane] = carry + v - x;
+            carry += __shfl_sync(0xFFFFFFFFu, v, 31);
+        }
+        if (lane == 0) pre[ng] = carry;
+    }
+    __syncthreads();
+    return pre[ng];
+}
+
+// Item of a group: row tile fastest, so that CTAs that run together read the
+// same keys.
+struct PfxItem {
+    int head, rt;
+};
+__device__ __forceinline__ PfxItem pfx_item(const PfxGroup &g, int item) {
+    return {item / g.rts, item - item / g.rts * g.rts};
+}
+
+// Row of the main records: rows of a group are (kv head, member, q head of the
+// group), after the rows of the members before it.
+__device__ __forceinline__ long long pfx_main_row(const PfxArgs &a, const PfxGroup &g, int head, int r) {
+    return (long long)g.m0 * a.h_q + (long long)head * g.n * (a.h_q / a.h_kv) + r;
+}
+
+// Physical row (block * b + slot) of token t of the group's prefix, by its first
+// member's table row; -1 for a bad block id (recorded).
+__device__ __forceinline__ long long pfx_slot(const PfxArgs &a, const int32_t *row, int t) {
+    const int blk = __ldg(row + t / a.b);
+    if (blk < 0 || blk >= a.n_total) {
+        record_error(a.err, ZP_ERR_DEVICE, 0x143);
+        return -1;
+    }
+    return (long long)blk * a.b + t % a.b;
+}
+
+// Eight (bf16) or four (fp32) consecutive elements as floats.
+__device__ __forceinline__ void load_vec(const float *p, float *o) {
+    const float4 v = *reinterpret_cast<const float4 *>(p);
+    o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
+}
+__device__ __forceinline__ void load_vec(const __nv_bfloat16 *p, float *o) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = bf2_to_f2(w[i]);
+        o[2 * i] = f.x, o[2 * i + 1] = f.y;
+    }
+}
+
+// ===========================================================================
+// CUDA-core kernels (fp32 caches; bf16 shapes without a tensor-core tile).
+// 64 query rows x 64 prefix tokens per tile, everything in fp32 in shared
+// memory; a thread holds 4 rows x 4 tokens of the logits and 4 rows x d/16 dims
+// of the accumulator, and the 16 threads of a row (a half-warp) share its
+// softmax statistics by shuffles.
+template <int D>
+struct PfxSmem {
+    float q[kPfxRows][D + 4];
+    float k[kPfxTokens][D + 4];
+    float v[kPfxTokens][D];
+    float p[kPfxRows][kPfxTokens + 4];
+};
+
+// Query rows [r0, r0 + 64) of the group into shared memory, zero beyond the last.
+template <typename T, int D, int G>
+__device__ void pfx_load_q(const PfxArgs &a, const PfxGroup &g, int head, int r0, PfxSmem<D> &sm) {
+    constexpr int V = 16 / (int)sizeof(T);
+    for (int i = threadIdx.x; i < kPfxRows * (D / V); i += kPfxThreads) {
+        const int r = i / (D / V), c = (i % (D / V)) * V;
+        float x[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) x[e] = 0.f;
+        if (r0 + r < g.n * G) {
+            const int s = pfx_member(a, g.m0 + (r0 + r) / G);
+            if (s >= 0)
+                load_vec(static_cast<const T *>(a.q) + ((size_t)s * a.h_q + head * G + (r0 + r) % G) * D + c, x);
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) sm.q[r][c + e] = x[e] * a.qscale;
+    }
+}
+
+// 64 prefix tokens from t0 (zero beyond the prefix and for bad blocks).
+template <typename T, int D>
+__device__ void pfx_load_kv(const PfxArgs &a, const PfxGroup &g, const int32_t *row, int head, int t0, PfxSmem<D> &sm,
+                            bool with_v) {
+    constexpr int V = 16 / (int)sizeof(T);
+    for (int i = threadIdx.x; i < kPfxTokens * (D / V); i += kPfxThreads) {
+        const int t = i / (D / V), c = (i % (D / V)) * V;
+        float x[V], y[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) x[e] = y[e] = 0.f;
+        if (t0 + t < g.tokens) {
+            const long long slot = pfx_slot(a, row, t0 + t);
+            if (slot >= 0) {
+                const size_t at = ((size_t)slot * a.h_kv + head) * D + c;
+                load_vec(static_cast<const T *>(a.k) + at, x);
+                if (with_v) load_vec(static_cast<const T *>(a.v) + at, y);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) sm.k[t][c + e] = x[e];
+        if (with_v) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) sm.v[t][c + e] = y[e];
+        }
+    }
+}
+
+// Logits of rows ty*4 + i, tokens tx + 16 j (log2 units).
+template <int D>
+__device__ __forceinline__ void pfx_logits(const PfxSmem<D> &sm, int ty, int tx, float (&x)[4][4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[i][j] = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < D; c += 4) {
+        float4 qv[4], kv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4 *>(&sm.q[ty * 4 + i][c]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4 *>(&sm.k[tx + 16 * j][c]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[i][j] = fmaf(qv[i].x, kv[j].x, x[i][j]);
+                x[i][j] = fmaf(qv[i].y, kv[j].y, x[i][j]);
+                x[i][j] = fmaf(qv[i].z, kv[j].z, x[i][j]);
+                x[i][j] = fmaf(qv[i].w, kv[j].w, x[i][j]);
+            }
+    }
+}
+
+// The table row every member's prefix agrees with: the first member's.
+__device__ __forceinline__ const int32_t *pfx_row(const PfxArgs &a, const PfxGroup &g) {
+    const int s = pfx_member(a, g.m0);
+    return a.table + (size_t)(s < 0 ? 0 : s) * a.stride;
+}
+
+template <typename T, int D, int G>
+__global__ void __launch_bounds__(kPfxThreads) prefix_part_kernel(const PfxArgs a) {
+    extern __shared__ __align__(16) unsigned char pfx_raw[];
+    PfxSmem<D> &sm = *reinterpret_cast<PfxSmem<D> *>(pfx_raw);
+    int *pre = reinterpret_cast<int *>(pfx_raw + sizeof(PfxSmem<D>));
+    constexpr int DV = D / 64;  // float4 groups of dims per thread
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int ng = pfx_groups(a);
+    const int W = pfx_scan(a, ng, pre);
+    if (blockIdx.x == 0) {
+        for (int i = tid; i <= ng; i += kPfxThreads) a.wpre[i] = pre[i];
+        for (int s = tid; s < a.B; s += kPfxThreads) a.prefix[s] = 0;
+        __syncthreads();
+        for (int g = 0; g < ng; ++g) {
+            const PfxGroup gr = pfx_group(a, g);
+            for (int i = tid; i < gr.n; i += kPfxThreads) {
+                const int s = pfx_member(a, gr.m0 + i);
+                if (s >= 0) a.prefix[s] = gr.tokens;
+            }
+        }
+    }
+    const int w0 = pfx_start(blockIdx.x, W, a.parts), w1 = pfx_start(blockIdx.x + 1, W, a.parts);
+    for (int w = w0; w < w1;) {
+        const int gi = pfx_find(pre, ng, w);
+        const PfxGroup g = pfx_group(a, gi);
+        const int item = (w - pre[gi]) / g.kts, t_b = (w - pre[gi]) % g.kts;
+        const int t_e = min(g.kts, t_b + (w1 - w));
+        const PfxItem it = pfx_item(g, item);
+        const int r0 = it.rt * kPfxRows;
+        const int32_t *row = pfx_row(a, g);
+        __syncthreads();  // the last segment's reads of shared memory
+        pfx_load_q<T, D, G>(a, g, it.head, r0, sm);
+        float m[4], l[4], acc[4][4 * DV];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4 * DV; ++e) acc[i][e] = 0.f;
+        }
+        for (int t = t_b; t < t_e; ++t) {
+            const int t0 = t * kPfxTokens;
+            __syncthreads();
+            pfx_load_kv<T, D>(a, g, row, it.head, t0, sm, true);
+            __syncthreads();
+            float x[4][4];
+            pfx_logits<D>(sm, ty, tx, x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float mx = m[i];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (t0 + tx + 16 * j >= g.tokens) x[i][j] = -INFINITY;
+                    mx = fmaxf(mx, x[i][j]);
+                }
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+                // (the tile's first token is in the prefix: the maximum is that of at least one logit)
+                const float al = mx == -INFINITY ? 1.f : exp2f(m[i] - mx);
+                m[i] = mx;
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float p = x[i][j] == -INFINITY ? 0.f : exp2f(x[i][j] - mx);
+                    sum += p;
+                    sm.p[ty * 4 + i][tx + 16 * j] = p;
+                }
+                l[i] = l[i] * al + sum;  // this thread's tokens only; joined at the end
+#pragma unroll
+                for (int e = 0; e < 4 * DV; ++e) acc[i][e] *= al;
+            }
+            __syncwarp();  // the rows of a half-warp's p are its own
+#pragma unroll 2
+            for (int t4 = 0; t4 < kPfxTokens; t4 += 4) {
+                float4 pv[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) pv[i] = *reinterpret_cast<const float4 *>(&sm.p[ty * 4 + i][t4]);
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int dv = 0; dv < DV; ++dv) {
+                        const float4 vv = *reinterpret_cast<const float4 *>(&sm.v[t4 + u][dv * 64 + tx * 4]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float p = u == 0 ? pv[i].x : (u == 1 ? pv[i].y : (u == 2 ? pv[i].z : pv[i].w));
+                            acc[i][4 * dv] = fmaf(p, vv.x, acc[i][4 * dv]);
+                            acc[i][4 * dv + 1] = fmaf(p, vv.y, acc[i][4 * dv + 1]);
+                            acc[i][4 * dv + 2] = fmaf(p, vv.z, acc[i][4 * dv + 2]);
+                            acc[i][4 * dv + 3] = fmaf(p, vv.w, acc[i][4 * dv + 3]);
+                        }
+                    }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], o);
+            const int r = r0 + ty * 4 + i;
+            if (r < g.n * G) {
+                const long long at = t_b == 0 ? pfx_main_row(a, g, it.head, r)
+                                              : (long long)a.B * a.h_q + (long long)blockIdx.x * a.rt + ty * 4 + i;
+                if (tx == 0) a.rec_ml[at] = make_float2(m[i], l[i]);
+#pragma unroll
+                for (int dv = 0; dv < DV; ++dv)
+                    *reinterpret_cast<float4 *>(a.rec_acc + at * D + dv * 64 + tx * 4) =
+                        make_float4(acc[i][4 * dv], acc[i][4 * dv + 1], acc[i][4 * dv + 2], acc[i][4 * dv + 3]);
+            }
+        }
+        w += t_e - t_b;
+    }
+}
+
+// One warp per (member, q head): the pieces of its row joined,
+//     M = max_j m_j,  l = sum_j 2^(m_j - M) l_j,  acc = sum_j 2^(m_j - M) acc_j.
+template <int D>
+__global__ void __launch_bounds__(256) prefix_merge_kernel(const PfxArgs a) {
+    const int lane = threadIdx.x & 31;
+    const long long wi = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int ng = pfx_groups(a);
+    if (ng == 0) return;
+    const int mi = (int)(wi / a.h_q), h = (int)(wi - (long long)mi * a.h_q);
+    const int W = a.wpre[ng];
+    // the group of member mi: the last that starts at or before it (empty ones hold none)
+    int lo = 0, hi = ng - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (__ldg(a.group_start + mid) <= mi) lo = mid;
+        else hi = mid - 1;
+    }
+    const PfxGroup g = pfx_group(a, lo);
+    if (mi < g.m0 || mi >= g.m0 + g.n || g.tokens == 0) return;
+    const int s = pfx_member(a, mi);
+    if (s < 0) return;
+    const int G = a.h_q / a.h_kv, head = h / G;
+    const int r = (mi - g.m0) * G + h % G;
+    const int i0 = a.wpre[lo] + (head * g.rts + r / a.rt) * g.kts;
+    const int c0 = pfx_owner(i0, W, a.parts), c1 = pfx_owner(i0 + g.kts - 1, W, a.parts);
+    constexpr int V = D / 32;
+    float M = -INFINITY, L = 0.f, acc[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = 0.f;
+    for (int c = c0; c <= c1; ++c) {
+        if (pfx_start(c, W, a.parts) == pfx_start(c + 1, W, a.parts)) continue;  // a CTA without tiles
+        const long long at = c == c0 ? pfx_main_row(a, g, head, r)
+                                     : (long long)a.B * a.h_q + (long long)c * a.rt + r % a.rt;
+        const float2 ml = a.rec_ml[at];
+        const float Mn = fmaxf(M, ml.x);
+        if (Mn == -INFINITY) continue;
+        const float f0 = M == -INFINITY ? 0.f : exp2f(M - Mn), f1 = ml.x == -INFINITY ? 0.f : exp2f(ml.x - Mn);
+        L = L * f0 + ml.y * f1;
+        M = Mn;
+        const float *src = a.rec_acc + at * D + lane * V;
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = acc[e] * f0 + src[e] * f1;
+    }
+    float *dst = a.init_acc + ((size_t)s * a.h_q + h) * D + lane * V;
+#pragma unroll
+    for (int e = 0; e < V; ++e) dst[e] = acc[e];
+    if (lane == 0) a.init_ml[(size_t)s * a.h_q + h] = make_float2(M, L);
+}
+
+// Row of the score that batch entry s adds to in this step, -1: none (no prefix,
+// not on a window step, no score row).  first: the window's first row, written.
+__device__ __forceinline__ int pfx_score_row(const PfxArgs &a, int s, bool *first) {
+    const int L = min(__ldg(a.seq_lens + s), a.stride * a.b);
+    const int p = a.prefix[s];
+    *first = false;
+    if (p <= 0 || p >= L) return -1;
+    const int ph = (L - 1) % a.b;
+    if (ph < a.b - a.window) return -1;
+    *first = ph == a.b - a.window;
+    if (!a.score_rows) return s;
+    const int r = __ldg(a.score_rows + s);
+    return r >= a.n_score_rows ? -1 : r;  // (the decode records a row out of range)
+}
+
+// Window score of the prefix tokens from the final statistics: the logits again,
+// the maximum of x - (m + log2 l) over the q heads of the kv head, one
+// exponential per (sequence, kv head, token).
+template <typename T, int D, int G>
+__global__ void __launch_bounds__(kPfxThreads) prefix_score_kernel(const PfxArgs a) {
+    extern __shared__ __align__(16) unsigned char pfx_raw[];
+    PfxSmem<D> &sm = *reinterpret_cast<PfxSmem<D> *>(pfx_raw);
+    int *pre = reinterpret_cast<int *>(pfx_raw + sizeof(PfxSmem<D>));
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int ng = pfx_groups(a);
+    const int W = pfx_scan(a, ng, pre);
+    const int w0 = pfx_start(blockIdx.x, W, gridDim.x), w1 = pfx_start(blockIdx.x + 1, W, gridDim.x);
+    const float inv_w = 1.f / (float)a.window;
+    for (int w = w0; w < w1;) {
+        const int gi = pfx_find(pre, ng, w);
+        const PfxGroup g = pfx_group(a, gi);
+        const int item = (w - pre[gi]) / g.kts, t_b = (w - pre[gi]) % g.kts;
+        const int t_e = min(g.kts, t_b + (w1 - w));
+        const PfxItem it = pfx_item(g, item);
+        const int r0 = it.rt * kPfxRows;
+        const int32_t *row = pfx_row(a, g);
+        __syncthreads();
+        pfx_load_q<T, D, G>(a, g, it.head, r0, sm);
+        // score row and c = m + log2 l of this thread's rows
+        float c[4];
+        int srow[4];
+        bool first[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = r0 + ty * 4 + i;
+            c[i] = INFINITY;
+            srow[i] = -1;
+            first[i] = false;
+            if (r < g.n * G) {
+                const int s = pfx_member(a, g.m0 + r / G);
+                if (s >= 0) {
+                    srow[i] = pfx_score_row(a, s, &first[i]);
+                    if (srow[i] >= 0) {
+                        const float2 ml = a.stats[(size_t)s * a.h_q + it.head * G + r % G];
+                        c[i] = ml.y > 0.f ? ml.x + log2f(ml.y) : INFINITY;
+                    }
+                }
+            }
+        }
+        for (int t = t_b; t < t_e; ++t) {
+            const int t0 = t * kPfxTokens;
+            __syncthreads();
+            pfx_load_kv<T, D>(a, g, row, it.head, t0, sm, false);
+            __syncthreads();
+            float x[4][4];
+            pfx_logits<D>(sm, ty, tx, x);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int tok = t0 + tx + 16 * j;
+                float e[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) e[i] = x[i][j] - c[i];
+                // maximum over the group's rows: inside the thread for G <= 4, with the
+                // other half-warp (the next four rows) for G = 8
+                if constexpr (G >= 2) {
+                    e[0] = fmaxf(e[0], e[1]);
+                    e[2] = fmaxf(e[2], e[3]);
+                }
+                if constexpr (G >= 4) e[0] = fmaxf(e[0], e[2]);
+                if constexpr (G == 8) e[0] = fmaxf(e[0], __shfl_xor_sync(0xFFFFFFFFu, e[0], 16));
+                if (tok < g.tokens) {
+#pragma unroll
+                    for (int i = 0; i < 4; i += (G >= 4 ? 4 : G)) {
+                        if (srow[i] < 0 || (G == 8 && (ty & 1))) continue;
+                        float *dst = a.score + ((size_t)srow[i] * a.h_kv + it.head) * a.score_stride + tok;
+                        const float val = exp2f(e[i]) * inv_w;
+                        *dst = first[i] ? val : *dst + val;
+                    }
+                }
+            }
+        }
+        w += t_e - t_b;
+    }
+}
+
+struct PfxPlan {
+    int rt, kt, parts;
+    size_t off_wpre, off_prefix, off_rml, off_racc, off_iml, off_iacc, total;
+};
+
+zp_status pfx_plan(const zp_cache_desc *D, int B, const DeviceInfo &dev, PfxPlan *p) {
+    const int d = D->head_dim, G = D->h_q / D->h_kv;
+    if (!(d == 64 || d == 128)) return fail(ZP_ERR_SHAPE, "prefix_decode: head_dim %d not in {64,128}", d);
+    if (!(G == 1 || G == 2 || G == 4 || G == 8)) return fail(ZP_ERR_SHAPE, "prefix_decode: group size %d", G);
+    if (B > kPfxMaxB) return fail(ZP_ERR_SHAPE, "prefix_decode: B %d > %d", B, kPfxMaxB);
+    p->rt = kPfxRows;
+    p->kt = kPfxTokens;
+    p->parts = dev.sm_count;
+    const size_t rows = (size_t)B * D->h_q, recs = rows + (size_t)p->parts * p->rt;
+    size_t off = 0;
+    p->off_wpre = off;
+    off = align_up(off + (size_t)(B + 1) * 4, 256);
+    p->off_prefix = off;
+    off = align_up(off + (size_t)B * 4, 256);
+    p->off_rml = off;
+    off = align_up(off + recs * 8, 256);
+    p->off_racc = off;
+    off = align_up(off + recs * d * 4, 256);
+    p->off_iml = off;
+    off = align_up(off + rows * 8, 256);
+    p->off_iacc = off;
+    off = align_up(off + rows * d * 4, 256);
+    p->total = off;
+    return ZP_OK;
+}
+
+template <typename T, int D, int G>
+zp_status launch_part(const PfxArgs &a, cudaStream_t st) {
+    const size_t smem = sizeof(PfxSmem<D>) + (size_t)(a.B + 1) * 4;
+    zp_status rc = set_max_dynamic_smem(reinterpret_cast<const void *>(prefix_part_kernel<T, D, G>), smem,
+                                        "prefix_decode: shared-memory attribute");
+    if (rc != ZP_OK) return rc;
+    prefix_part_kernel<T, D, G><<<a.parts, kPfxThreads, smem, st>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "prefix_decode: prefix kernel launch");
+    const long long warps = (long long)a.B * a.h_q;
+    prefix_merge_kernel<D><<<(unsigned)((warps + 7) / 8), 256, 0, st>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "prefix_decode: merge kernel launch");
+    return ZP_OK;
+}
+
+template <typename T, int D, int G>
+zp_status launch_score(const PfxArgs &a, cudaStream_t st) {
+    const size_t smem = sizeof(PfxSmem<D>) + (size_t)(a.B + 1) * 4;
+    zp_status rc = set_max_dynamic_smem(reinterpret_cast<const void *>(prefix_score_kernel<T, D, G>), smem,
+                                        "prefix_decode: shared-memory attribute");
+    if (rc != ZP_OK) return rc;
+    prefix_score_kernel<T, D, G><<<a.parts, kPfxThreads, smem, st>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "prefix_decode: score kernel launch");
+    return ZP_OK;
+}
+
+// Calls f.template operator()<T, D, G>() for the cache's type and geometry.
+template <typename F>
+zp_status pfx_dispatch(const zp_cache_desc *D, F &&f) {
+    const int G = D->h_q / D->h_kv, d = D->head_dim;
+#define ZP_PFX_CASE(T, DD)                                          \
+    if (G == 1) return f.template operator()<T, DD, 1>();           \
+    if (G == 2) return f.template operator()<T, DD, 2>();           \
+    if (G == 4) return f.template operator()<T, DD, 4>();           \
+    if (G == 8) return f.template operator()<T, DD, 8>();
+    if (D->dtype == ZP_BF16 && d == 64) {
+        ZP_PFX_CASE(__nv_bfloat16, 64)
+    } else if (D->dtype == ZP_BF16) {
+        ZP_PFX_CASE(__nv_bfloat16, 128)
+    } else if (d == 64) {
+        ZP_PFX_CASE(float, 64)
+    } else {
+        ZP_PFX_CASE(float, 128)
+    }
+#undef ZP_PFX_CASE
+    return fail(ZP_ERR_SHAPE, "prefix_decode: no kernel for d=%d, group=%d", d, G);
+}
+
+struct LaunchPart {
+    const PfxArgs &a;
+    cudaStream_t st;
+    template <typename T, int D, int G>
+    zp_status operator()() const { return launch_part<T, D, G>(a, st); }
+};
+struct LaunchScore {
+    const PfxArgs &a;
+    cudaStream_t st;
+    template <typename T, int D, int G>
+    zp_status operator()() const { return launch_score<T, D, G>(a, st); }
+};
+
+}  // namespace
+}  // namespace zp
+
+using namespace zp;
+
+extern "C" size_t zp_prefix_decode_workspace_size(const zp_cache_desc *D, int32_t B, int32_t table_stride) {
+    if (check_desc(D) != ZP_OK || B < 0 || table_stride < 0) return 0;
+    const size_t dec = zp_decode_workspace_size(D, B, table_stride);
+    DeviceInfo dev;
+    PfxPlan p;
+    if (dec == 0 || device_info(&dev) != ZP_OK || pfx_plan(D, B, dev, &p) != ZP_OK) return 0;
+    return align_up(dec, 256) + p.total;
+}
+
+extern "C" zp_status zp_prefix_decode_attn(const zp_cache_desc *D, const void *q, const void *k_cache,
+                                           const void *v_cache, const int32_t *block_table, int32_t table_stride,
+                                           const int32_t *seq_lens, int32_t B, const zp_prefix_groups *plan, void *out,
+                                           float *score_accum, const int32_t *score_rows, int32_t n_score_rows,
+                                           int32_t window, void *workspace, size_t workspace_bytes, void *stream) {
+    zp_status rc = check_desc(D);
+    if (rc != ZP_OK) return rc;
+    if (B < 0 || table_stride < 0) return fail(ZP_ERR_INVALID_ARG, "prefix_decode: B or table_stride negative");
+    if (B == 0) return ok();
+    if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !out || !workspace || !plan || !plan->n_groups ||
+        !plan->group_start || !plan->members || !plan->group_blocks)
+        return fail(ZP_ERR_INVALID_ARG, "prefix_decode: NULL buffer");
+    if (table_stride < 1) return fail(ZP_ERR_INVALID_ARG, "prefix_decode: table_stride < 1");
+    if (score_accum && (window < 1 || window > D->block_size))
+        return fail(ZP_ERR_INVALID_ARG, "prefix_decode: window %d outside [1, b=%d]", window, D->block_size);
+    if (score_accum && score_rows && n_score_rows < 1)
+        return fail(ZP_ERR_INVALID_ARG, "prefix_decode: a slot map needs n_score_rows >= 1");
+    const uintptr_t al = (uintptr_t)q | (uintptr_t)k_cache | (uintptr_t)v_cache | (uintptr_t)out |
+                         (uintptr_t)score_accum | (uintptr_t)workspace;
+    if (al % 16) return fail(ZP_ERR_INVALID_ARG, "prefix_decode: buffers must be 16-byte aligned");
+    const int G = D->h_q / D->h_kv;
+    // tile counts are 32-bit: kv heads * query rows * tokens of a row bounds them
+    if ((double)D->h_kv * ((double)B * G) * ((double)table_stride * D->block_size / kPfxTokens + 1) > 2147483647.0 ||
+        (long long)table_stride * D->block_size > INT32_MAX)
+        return fail(ZP_ERR_SHAPE, "prefix_decode: B=%d rows of %d blocks", B, table_stride);
+    DeviceInfo dev;
+    rc = device_info(&dev);
+    if (rc != ZP_OK) return rc;
+    PfxPlan p;
+    rc = pfx_plan(D, B, dev, &p);
+    if (rc != ZP_OK) return rc;
+    const size_t dec = zp_decode_workspace_size(D, B, table_stride);
+    if (dec == 0) return fail(ZP_ERR_SHAPE, "prefix_decode: %s", zp_last_error());
+    if (workspace_bytes < align_up(dec, 256) + p.total)
+        return fail(ZP_ERR_CAPACITY, "prefix_decode: workspace %zu < %zu bytes", workspace_bytes,
+                    align_up(dec, 256) + p.total);
+    unsigned char *ws = static_cast<unsigned char *>(workspace) + align_up(dec, 256);
+    PfxArgs a = {};
+    a.q = q;
+    a.k = k_cache;
+    a.v = v_cache;
+    a.table = block_table;
+    a.stride = table_stride;
+    a.seq_lens = seq_lens;
+    a.B = B;
+    a.h_q = D->h_q;
+    a.h_kv = D->h_kv;
+    a.b = D->block_size;
+    a.n_total = D->n_total_blocks;
+    a.n_groups = plan->n_groups;
+    a.group_start = plan->group_start;
+    a.members = plan->members;
+    a.group_blocks = plan->group_blocks;
+    a.rt = p.rt;
+    a.kt = p.kt;
+    a.parts = p.parts;
+    a.qscale = (float)(1.4426950408889634 / sqrt((double)D->head_dim));
+    a.wpre = reinterpret_cast<int *>(ws + p.off_wpre);
+    a.prefix = reinterpret_cast<int32_t *>(ws + p.off_prefix);
+    a.rec_acc = reinterpret_cast<float *>(ws + p.off_racc);
+    a.rec_ml = reinterpret_cast<float2 *>(ws + p.off_rml);
+    a.init_acc = reinterpret_cast<float *>(ws + p.off_iacc);
+    a.init_ml = reinterpret_cast<float2 *>(ws + p.off_iml);
+    a.score = score_accum;
+    a.score_stride = (long long)table_stride * D->block_size;
+    a.score_rows = score_accum ? score_rows : nullptr;
+    a.n_score_rows = n_score_rows;
+    a.window = window;
+    a.err = dev.error_word;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    rc = pfx_dispatch(D, LaunchPart{a, st});
+    if (rc != ZP_OK) return rc;
+    const PrefixRecords pre = {a.prefix, a.init_acc, a.init_ml};
+    rc = decode_after_prefix(D, q, k_cache, v_cache, block_table, table_stride, seq_lens, B, out, score_accum, score_rows,
+                             n_score_rows, window, pre, workspace, dec, stream, &a.stats);
+    if (rc != ZP_OK) return rc;
+    if (score_accum) {
+        rc = pfx_dispatch(D, LaunchScore{a, st});
+        if (rc != ZP_OK) return rc;
+    }
+    return ok();
+}

@@ -59,4 +59,22 @@ struct AllPairsArgs {
 size_t all_pairs_workspace_size(int n, int h_kv, int d, int Lmax);
 zp_status launch_all_pairs(const AllPairsArgs &a, cudaStream_t st);
 
+// Softmax records of the shared prefixes, per batch entry and query head, that
+// the decode of the remaining tokens starts from (log2 units; read only for
+// entries with prefix_lens > 0).
+struct PrefixRecords {
+    const int32_t *prefix_lens;  // [B] tokens, multiples of b
+    const float *acc;            // [B][h_q][d] unnormalised accumulator
+    const float2 *ml;            // [B][h_q] (max, sum)
+};
+
+// zp_paged_decode_attn of the tokens behind the prefixes (arguments checked as
+// there; the workspace is the decode's).  *stats: the workspace's [B][h_q]
+// final (max, sum) of every entry that is on a window step, when scoring.
+zp_status decode_after_prefix(const zp_cache_desc *D, const void *q, const void *k_cache, const void *v_cache,
+                              const int32_t *block_table, int32_t table_stride, const int32_t *seq_lens, int32_t B,
+                              void *out, float *score_accum, const int32_t *score_rows, int32_t n_score_rows,
+                              int32_t window, const PrefixRecords &pre, void *workspace, size_t workspace_bytes,
+                              void *stream, const float2 **stats);
+
 }  // namespace zp

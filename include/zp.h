@@ -222,6 +222,96 @@ zp_status zp_append_kv(const zp_cache_desc *D, const void *k_new, const void *v_
                        void *k_cache, void *v_cache, const int32_t *block_table,
                        int32_t table_stride, const int32_t *seq_lens, int32_t B, void *stream);
 
+/* Block tables and slot maps from request lengths [Zipage §3: the block table
+ * records where each block is written].  Sequence s grows from old_lens[s] to
+ * new_lens[s] tokens (device int32 [B]; equal: no new token).  Every column c in
+ * [ceil(old/b), ceil(new/b)) whose table entry is negative takes the next block
+ * of fresh[0..n_fresh) in (sequence, column) order; entries already >= 0 (a
+ * reserved block, a shared prefix) are kept.  Outputs:
+ *   table_out   the grown table [B][table_stride]: block_table itself (in place)
+ *               or a separate buffer, which then receives every entry
+ *   cu_tokens   [B+1] new tokens before each sequence
+ *   slots       [max_tokens] slot (block * b + t % b) of new token i =
+ *               cu_tokens[s] + (t - old_lens[s]); -1 behind the last token
+ *   positions   nullable [max_tokens]: t; -1 behind the last token
+ *   n_used      nullable [1]: fresh blocks needed
+ * Recorded as ZP_ERR_DEVICE: old < 0, new < old or new > table_stride * b (detail
+ * 0x120; the sequence counts as not growing), too few fresh blocks (0x121;
+ * their entries and slots are -1), a block id outside [0, N_total) under a new
+ * token (0x122; slot -1), more than max_tokens new tokens (0x123; the rest are
+ * not written).  Limits: B <= 4096, N_total * b and B * table_stride * b below
+ * 2^31 (ZP_ERR_SHAPE). */
+zp_status zp_build_slots(const zp_cache_desc *D, const int32_t *block_table, int32_t *table_out,
+                         int32_t table_stride, const int32_t *old_lens, const int32_t *new_lens, int32_t B,
+                         const int32_t *fresh, int32_t n_fresh, int32_t *slots, int32_t *positions,
+                         int32_t max_tokens, int32_t *cu_tokens, int32_t *n_used, void *stream);
+
+/* Writes the keys and values of n_tokens tokens into their slots, for
+ * layer_count layers in one call [Zipage §3] (a prompt; zp_append_kv is the form
+ * for one token per sequence).  The row [h_kv][d] of token i of layer l is
+ * contiguous at k_new / v_new + l*new_layer_stride + i*token_stride elements (a
+ * slice of a fused projection has token_stride > h_kv*d) and goes to slot
+ * slots[i] (device int32) of layer l at k_base / v_base + l*layer_stride.  A
+ * negative slot is skipped; one >= N_total * b is recorded as ZP_ERR_DEVICE
+ * (detail 0x130) and skipped.  A slot named twice receives either row, or a mix
+ * of both.  Addresses and strides are multiples of 16 bytes. */
+zp_status zp_write_kv(const zp_cache_desc *D, const void *k_new, const void *v_new, int64_t token_stride,
+                      int64_t new_layer_stride, const int32_t *slots, int32_t n_tokens, void *k_base, void *v_base,
+                      int64_t layer_stride, int32_t layer_count, void *stream);
+
+/* ---- decode behind a shared prefix --------------------------------------- */
+
+/* Groups of batch entries that share leading blocks (prefix blocks [Zipage
+ * §4.4]), device int32 arrays owned by the caller:
+ *   prefix_lens  [B] tokens shared by the entry's group (a multiple of b), 0 = none
+ *   n_groups     [1]
+ *   group_start  [B+1] group g's members are members[group_start[g] ..
+ *                group_start[g+1]); entries behind n_groups repeat the end
+ *   members      [B] batch entries, ascending inside a group; -1 behind the last
+ *   group_blocks [B] leading table entries the members share; 0 behind n_groups
+ * An entry is in one group at most. */
+typedef struct zp_prefix_groups {
+    int32_t *prefix_lens;
+    int32_t *n_groups;
+    int32_t *group_start;
+    int32_t *members;
+    int32_t *group_blocks;
+} zp_prefix_groups;
+
+/* Finds the groups in the block table, on the GPU.  Entry s may share the
+ * u = floor((L-1)/b) blocks before the one that holds its newest token.  Entries
+ * with the same first block are compared with the one of them that has the
+ * largest u (the lowest index on ties); of the common lengths c found, the group
+ * shares the p that maximises p * (#{c >= p} - 1), the blocks not read again
+ * (the longer p on ties), and has the entries with c >= p.  No group where
+ * p < min_blocks or fewer than min_members entries have it.  Groups are ordered
+ * by their lowest entry.  The plan holds while its members' leading table
+ * entries stay (sequences may grow); the call writes all of its arrays.
+ * Limits: B <= 4096, min_blocks >= 1, min_members >= 2. */
+zp_status zp_prefix_plan(const zp_cache_desc *D, const int32_t *block_table, int32_t table_stride,
+                         const int32_t *seq_lens, int32_t B, int32_t min_blocks, int32_t min_members,
+                         const zp_prefix_groups *plan, void *stream);
+
+/* zp_paged_decode_attn (output, window score, arguments, skipping of L = 0) with
+ * each group's shared tokens attended once for all its members: their query rows
+ * form one dense product with the shared keys and values, whose softmax state
+ * the decode of the members' other tokens continues.  plan->prefix_lens is not
+ * read.  A member whose L does not exceed its group's prefix is decoded alone.
+ * The members' leading group_blocks table entries must be equal (the first
+ * member's are used).  A member outside [0, B) (detail 0x142) and a block id
+ * outside [0, N_total) (0x143) are recorded as ZP_ERR_DEVICE and skipped.  The
+ * sum over the tokens has another order than zp_paged_decode_attn's, so results
+ * agree to rounding, not bit for bit; a call with the same arguments gives the
+ * same bits.  Two calls that may overlap need a workspace each.
+ * Limits: those of zp_paged_decode_attn and h_q/h_kv in {1,2,4,8} (1 and 2 with
+ * bf16 caches). */
+size_t zp_prefix_decode_workspace_size(const zp_cache_desc *D, int32_t B, int32_t table_stride);
+zp_status zp_prefix_decode_attn(const zp_cache_desc *D, const void *q, const void *k_cache, const void *v_cache,
+                                const int32_t *block_table, int32_t table_stride, const int32_t *seq_lens, int32_t B,
+                                const zp_prefix_groups *plan, void *out, float *score_accum,
+                                const int32_t *score_rows, int32_t n_score_rows, int32_t window, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
 /* ---- compression -------------------------------------------------------- */
 
 /* Compression trigger [Zipage §4.1]: 1 iff ceil(L/b) >= max_blocks and L%b == 0. */
