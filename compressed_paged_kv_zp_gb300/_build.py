@@ -20,7 +20,8 @@ OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libzp.so")
 
 SOURCES = ["zp_api.cu", "decode_attn.cu", "append_kv.cu", "window_score.cu", "score.cu", "redundancy.cu", "topk.cu",
-           "compact.cu", "slots.cu", "prefix_plan.cu", "prefix_attn.cu", "decode_attn_prefix.cu", "pool.cpp", "sched.cpp"]
+           "compact.cu", "slots.cu", "prefix_plan.cu", "prefix_attn.cu", "prefix_tc.cu",
+           "decode_attn_prefix.cu", "pool.cpp", "sched.cpp"]
 INCLUDED = {"decode_attn_prefix.cu": ["decode_attn.cu"]}  # sources that a source includes
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

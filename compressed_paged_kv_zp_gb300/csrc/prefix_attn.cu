@@ -22,162 +22,23 @@
 // the pieces of each row.
 #include <math.h>
 
-#include "zp_common.cuh"
+#include "prefix_tc.h"
 
 namespace zp {
 namespace {
 
-constexpr int kPfxMaxB = 4096;
 constexpr int kPfxThreads = 256;
-constexpr int kPfxRows = 64;    // query rows per item (CUDA-core kernel)
-constexpr int kPfxTokens = 64;  // prefix tokens per tile (CUDA-core kernel)
+constexpr int kPfxRows = 64;    // query rows per item
+constexpr int kPfxTokens = 64;  // prefix tokens per tile
 
-struct PfxArgs {
-    const void *q, *k, *v;
-    const int32_t *table;
-    int stride;
-    const int32_t *seq_lens;
-    int B, h_q, h_kv, b, n_total;
-    // the plan
-    const int32_t *n_groups, *group_start, *members, *group_blocks;
-    int rt, kt;          // rows per item, tokens per tile
-    int parts;           // CTAs of the prefix kernel (split of the tiles)
-    float qscale;        // log2(e) / sqrt(d)
-    int *wpre;           // [B+1] tiles before each group
-    int32_t *prefix;     // [B] prefix tokens of every batch entry, 0 = none
-    float *rec_acc;      // [B*h_q + parts*rt][d] pieces: main records, then extra records
-    float2 *rec_ml;      // same rows
-    float *init_acc;     // [B][h_q][d]
-    float2 *init_ml;     // [B][h_q]
-    // score
-    float *score;
-    long long score_stride;
-    const int32_t *score_rows;
-    int n_score_rows, window;
-    const float2 *stats;  // [B][h_q] final (max, sum)
-    unsigned *err;
-};
-
-// Group g of the plan, with every index the plan gives bounded.
-struct PfxGroup {
-    int m0, n;    // first member, members
-    int tokens;   // prefix tokens
-    int rts, kts; // row tiles, token tiles
-};
-
-__device__ __forceinline__ int pfx_groups(const PfxArgs &a) { return min(max(__ldg(a.n_groups), 0), a.B); }
-
-__device__ __forceinline__ PfxGroup pfx_group(const PfxArgs &a, int g) {
-    PfxGroup r;
-    r.m0 = min(max(__ldg(a.group_start + g), 0), a.B);
-    r.n = min(max(__ldg(a.group_start + g + 1), r.m0), a.B) - r.m0;
-    r.tokens = min(max(__ldg(a.group_blocks + g), 0), a.stride) * a.b;
-    r.rts = (r.n * (a.h_q / a.h_kv) + a.rt - 1) / a.rt;
-    r.kts = (r.tokens + a.kt - 1) / a.kt;
-    return r;
-}
-
-// Batch entry of member i; an entry outside the batch is recorded, -1.
-__device__ __forceinline__ int pfx_member(const PfxArgs &a, int i) {
-    const int s = __ldg(a.members + i);
-    if (s < 0 || s >= a.B) {
-        record_error(a.err, ZP_ERR_DEVICE, 0x142);
-        return -1;
-    }
-    return s;
-}
-
-__device__ __forceinline__ int pfx_start(int c, int W, int parts) { return (int)((long long)c * W / parts); }
-
-// last g in [0, n) with pre[g] <= x
-__device__ __forceinline__ int pfx_find(const int *pre, int n, int x) {
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (pre[mid] <= x) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
-}
-
-// CTA whose range holds tile w
-__device__ __forceinline__ int pfx_owner(int w, int W, int parts) {
-    int c = (int)((long long)w * parts / W);
-    while (c + 1 < parts && pfx_start(c + 1, W, parts) <= w) ++c;
-    while (c > 0 && pfx_start(c, W, parts) > w) --c;
-    return c;
-}
-
-// Tiles before each group (whole CTA; pre: n_groups + 1 ints of shared memory);
-// returns the total.
-__device__ int pfx_scan(const PfxArgs &a, int ng, int *pre) {
-    if (threadIdx.x < 32) {
-        const int lane = threadIdx.x;
-        int carry = 0;
-        for (int base = 0; base < ng; base += 32) {
-            int x = 0;
-            if (base + lane < ng) {
-                const PfxGroup g = pfx_group(a, base + lane);
-                x = a.h_kv * g.rts * g.kts;
-            }
-            int v = x;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xFFFFFFFFu, v, o);
-                if (lane >= o) v += y;
-            }
-            if (base + lane < ng) pre[base + lane] = carry + v - x;
-            carry += __shfl_sync(0xFFFFFFFFu, v, 31);
-        }
-        if (lane == 0) pre[ng] = carry;
-    }
-    __syncthreads();
-    return pre[ng];
-}
-
-// Item of a group: row tile fastest, so that CTAs that run together read the
-// same keys.
-struct PfxItem {
-    int head, rt;
-};
-__device__ __forceinline__ PfxItem pfx_item(const PfxGroup &g, int item) {
-    return {item / g.rts, item - item / g.rts * g.rts};
-}
-
-// Row of the main records: rows of a group are (kv head, member, q head of the
-// group), after the rows of the members before it.
-__device__ __forceinline__ long long pfx_main_row(const PfxArgs &a, const PfxGroup &g, int head, int r) {
-    return (long long)g.m0 * a.h_q + (long long)head * g.n * (a.h_q / a.h_kv) + r;
-}
-
-// Physical row (block * b + slot) of token t of the group's prefix, by its first
-// member's table row; -1 for a bad block id (recorded).
-__device__ __forceinline__ long long pfx_slot(const PfxArgs &a, const int32_t *row, int t) {
-    const int blk = __ldg(row + t / a.b);
-    if (blk < 0 || blk >= a.n_total) {
-        record_error(a.err, ZP_ERR_DEVICE, 0x143);
-        return -1;
-    }
-    return (long long)blk * a.b + t % a.b;
-}
-
-// Eight (bf16) or four (fp32) consecutive elements as floats.
+// Four consecutive elements.
 __device__ __forceinline__ void load_vec(const float *p, float *o) {
     const float4 v = *reinterpret_cast<const float4 *>(p);
     o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
 }
-__device__ __forceinline__ void load_vec(const __nv_bfloat16 *p, float *o) {
-    const uint4 v = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = bf2_to_f2(w[i]);
-        o[2 * i] = f.x, o[2 * i + 1] = f.y;
-    }
-}
 
 // ===========================================================================
-// CUDA-core kernels (fp32 caches; bf16 shapes without a tensor-core tile).
+// CUDA-core kernels (fp32 caches; bf16 caches: prefix_tc.cu).
 // 64 query rows x 64 prefix tokens per tile, everything in fp32 in shared
 // memory; a thread holds 4 rows x 4 tokens of the logits and 4 rows x d/16 dims
 // of the accumulator, and the 16 threads of a row (a half-warp) share its
@@ -191,9 +52,9 @@ struct PfxSmem {
 };
 
 // Query rows [r0, r0 + 64) of the group into shared memory, zero beyond the last.
-template <typename T, int D, int G>
+template <int D, int G>
 __device__ void pfx_load_q(const PfxArgs &a, const PfxGroup &g, int head, int r0, PfxSmem<D> &sm) {
-    constexpr int V = 16 / (int)sizeof(T);
+    constexpr int V = 4;
     for (int i = threadIdx.x; i < kPfxRows * (D / V); i += kPfxThreads) {
         const int r = i / (D / V), c = (i % (D / V)) * V;
         float x[V];
@@ -202,7 +63,7 @@ __device__ void pfx_load_q(const PfxArgs &a, const PfxGroup &g, int head, int r0
         if (r0 + r < g.n * G) {
             const int s = pfx_member(a, g.m0 + (r0 + r) / G);
             if (s >= 0)
-                load_vec(static_cast<const T *>(a.q) + ((size_t)s * a.h_q + head * G + (r0 + r) % G) * D + c, x);
+                load_vec(static_cast<const float *>(a.q) + ((size_t)s * a.h_q + head * G + (r0 + r) % G) * D + c, x);
         }
 #pragma unroll
         for (int e = 0; e < V; ++e) sm.q[r][c + e] = x[e] * a.qscale;
@@ -210,10 +71,10 @@ __device__ void pfx_load_q(const PfxArgs &a, const PfxGroup &g, int head, int r0
 }
 
 // 64 prefix tokens from t0 (zero beyond the prefix and for bad blocks).
-template <typename T, int D>
+template <int D>
 __device__ void pfx_load_kv(const PfxArgs &a, const PfxGroup &g, const int32_t *row, int head, int t0, PfxSmem<D> &sm,
                             bool with_v) {
-    constexpr int V = 16 / (int)sizeof(T);
+    constexpr int V = 4;
     for (int i = threadIdx.x; i < kPfxTokens * (D / V); i += kPfxThreads) {
         const int t = i / (D / V), c = (i % (D / V)) * V;
         float x[V], y[V];
@@ -223,8 +84,8 @@ __device__ void pfx_load_kv(const PfxArgs &a, const PfxGroup &g, const int32_t *
             const long long slot = pfx_slot(a, row, t0 + t);
             if (slot >= 0) {
                 const size_t at = ((size_t)slot * a.h_kv + head) * D + c;
-                load_vec(static_cast<const T *>(a.k) + at, x);
-                if (with_v) load_vec(static_cast<const T *>(a.v) + at, y);
+                load_vec(static_cast<const float *>(a.k) + at, x);
+                if (with_v) load_vec(static_cast<const float *>(a.v) + at, y);
             }
         }
 #pragma unroll
@@ -262,13 +123,7 @@ __device__ __forceinline__ void pfx_logits(const PfxSmem<D> &sm, int ty, int tx,
     }
 }
 
-// The table row every member's prefix agrees with: the first member's.
-__device__ __forceinline__ const int32_t *pfx_row(const PfxArgs &a, const PfxGroup &g) {
-    const int s = pfx_member(a, g.m0);
-    return a.table + (size_t)(s < 0 ? 0 : s) * a.stride;
-}
-
-template <typename T, int D, int G>
+template <int D, int G>
 __global__ void __launch_bounds__(kPfxThreads) prefix_part_kernel(const PfxArgs a) {
     extern __shared__ __align__(16) unsigned char pfx_raw[];
     PfxSmem<D> &sm = *reinterpret_cast<PfxSmem<D> *>(pfx_raw);
@@ -277,18 +132,7 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_part_kernel(const PfxArgs 
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int ng = pfx_groups(a);
     const int W = pfx_scan(a, ng, pre);
-    if (blockIdx.x == 0) {
-        for (int i = tid; i <= ng; i += kPfxThreads) a.wpre[i] = pre[i];
-        for (int s = tid; s < a.B; s += kPfxThreads) a.prefix[s] = 0;
-        __syncthreads();
-        for (int g = 0; g < ng; ++g) {
-            const PfxGroup gr = pfx_group(a, g);
-            for (int i = tid; i < gr.n; i += kPfxThreads) {
-                const int s = pfx_member(a, gr.m0 + i);
-                if (s >= 0) a.prefix[s] = gr.tokens;
-            }
-        }
-    }
+    if (blockIdx.x == 0) pfx_publish(a, ng, pre);
     const int w0 = pfx_start(blockIdx.x, W, a.parts), w1 = pfx_start(blockIdx.x + 1, W, a.parts);
     for (int w = w0; w < w1;) {
         const int gi = pfx_find(pre, ng, w);
@@ -299,7 +143,7 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_part_kernel(const PfxArgs 
         const int r0 = it.rt * kPfxRows;
         const int32_t *row = pfx_row(a, g);
         __syncthreads();  // the last segment's reads of shared memory
-        pfx_load_q<T, D, G>(a, g, it.head, r0, sm);
+        pfx_load_q<D, G>(a, g, it.head, r0, sm);
         float m[4], l[4], acc[4][4 * DV];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -311,7 +155,7 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_part_kernel(const PfxArgs 
         for (int t = t_b; t < t_e; ++t) {
             const int t0 = t * kPfxTokens;
             __syncthreads();
-            pfx_load_kv<T, D>(a, g, row, it.head, t0, sm, true);
+            pfx_load_kv<D>(a, g, row, it.head, t0, sm, true);
             __syncthreads();
             float x[4][4];
             pfx_logits<D>(sm, ty, tx, x);
@@ -368,7 +212,7 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_part_kernel(const PfxArgs 
             const int r = r0 + ty * 4 + i;
             if (r < g.n * G) {
                 const long long at = t_b == 0 ? pfx_main_row(a, g, it.head, r)
-                                              : (long long)a.B * a.h_q + (long long)blockIdx.x * a.rt + ty * 4 + i;
+                                              : a.extra0 + (long long)blockIdx.x * a.rt + ty * 4 + i;
                 if (tx == 0) a.rec_ml[at] = make_float2(m[i], l[i]);
 #pragma unroll
                 for (int dv = 0; dv < DV; ++dv)
@@ -390,13 +234,7 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const PfxArgs a) {
     if (ng == 0) return;
     const int mi = (int)(wi / a.h_q), h = (int)(wi - (long long)mi * a.h_q);
     const int W = a.wpre[ng];
-    // the group of member mi: the last that starts at or before it (empty ones hold none)
-    int lo = 0, hi = ng - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (__ldg(a.group_start + mid) <= mi) lo = mid;
-        else hi = mid - 1;
-    }
+    const int lo = pfx_group_of(a, ng, mi);
     const PfxGroup g = pfx_group(a, lo);
     if (mi < g.m0 || mi >= g.m0 + g.n || g.tokens == 0) return;
     const int s = pfx_member(a, mi);
@@ -409,19 +247,24 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const PfxArgs a) {
     float M = -INFINITY, L = 0.f, acc[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) acc[e] = 0.f;
+    // an item of at most 128 rows has a record per stream
+    const int row = r % a.rt;
+    const bool two = a.tc && min(a.rt, g.n * G - (r - row)) <= a.rt / 2;
     for (int c = c0; c <= c1; ++c) {
         if (pfx_start(c, W, a.parts) == pfx_start(c + 1, W, a.parts)) continue;  // a CTA without tiles
-        const long long at = c == c0 ? pfx_main_row(a, g, head, r)
-                                     : (long long)a.B * a.h_q + (long long)c * a.rt + r % a.rt;
-        const float2 ml = a.rec_ml[at];
-        const float Mn = fmaxf(M, ml.x);
-        if (Mn == -INFINITY) continue;
-        const float f0 = M == -INFINITY ? 0.f : exp2f(M - Mn), f1 = ml.x == -INFINITY ? 0.f : exp2f(ml.x - Mn);
-        L = L * f0 + ml.y * f1;
-        M = Mn;
-        const float *src = a.rec_acc + at * D + lane * V;
+        for (int x = 0; x < (two ? 2 : 1); ++x) {
+            const long long at = c == c0 ? pfx_main_row(a, g, head, r) + x * (long long)a.B * a.h_q
+                                         : a.extra0 + (long long)c * a.rt + x * (a.rt / 2) + row;
+            const float2 ml = a.rec_ml[at];
+            if (ml.x == -INFINITY) continue;  // no tile, no accumulator
+            const float Mn = fmaxf(M, ml.x);
+            const float f0 = M == -INFINITY ? 0.f : exp2f(M - Mn), f1 = exp2f(ml.x - Mn);
+            L = L * f0 + ml.y * f1;
+            M = Mn;
+            const float *src = a.rec_acc + at * D + lane * V;
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = acc[e] * f0 + src[e] * f1;
+            for (int e = 0; e < V; ++e) acc[e] = acc[e] * f0 + src[e] * f1;
+        }
     }
     float *dst = a.init_acc + ((size_t)s * a.h_q + h) * D + lane * V;
 #pragma unroll
@@ -429,25 +272,10 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const PfxArgs a) {
     if (lane == 0) a.init_ml[(size_t)s * a.h_q + h] = make_float2(M, L);
 }
 
-// Row of the score that batch entry s adds to in this step, -1: none (no prefix,
-// not on a window step, no score row).  first: the window's first row, written.
-__device__ __forceinline__ int pfx_score_row(const PfxArgs &a, int s, bool *first) {
-    const int L = min(__ldg(a.seq_lens + s), a.stride * a.b);
-    const int p = a.prefix[s];
-    *first = false;
-    if (p <= 0 || p >= L) return -1;
-    const int ph = (L - 1) % a.b;
-    if (ph < a.b - a.window) return -1;
-    *first = ph == a.b - a.window;
-    if (!a.score_rows) return s;
-    const int r = __ldg(a.score_rows + s);
-    return r >= a.n_score_rows ? -1 : r;  // (the decode records a row out of range)
-}
-
 // Window score of the prefix tokens from the final statistics: the logits again,
 // the maximum of x - (m + log2 l) over the q heads of the kv head, one
 // exponential per (sequence, kv head, token).
-template <typename T, int D, int G>
+template <int D, int G>
 __global__ void __launch_bounds__(kPfxThreads) prefix_score_kernel(const PfxArgs a) {
     extern __shared__ __align__(16) unsigned char pfx_raw[];
     PfxSmem<D> &sm = *reinterpret_cast<PfxSmem<D> *>(pfx_raw);
@@ -466,7 +294,7 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_score_kernel(const PfxArgs
         const int r0 = it.rt * kPfxRows;
         const int32_t *row = pfx_row(a, g);
         __syncthreads();
-        pfx_load_q<T, D, G>(a, g, it.head, r0, sm);
+        pfx_load_q<D, G>(a, g, it.head, r0, sm);
         // score row and c = m + log2 l of this thread's rows
         float c[4];
         int srow[4];
@@ -491,7 +319,7 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_score_kernel(const PfxArgs
         for (int t = t_b; t < t_e; ++t) {
             const int t0 = t * kPfxTokens;
             __syncthreads();
-            pfx_load_kv<T, D>(a, g, row, it.head, t0, sm, false);
+            pfx_load_kv<D>(a, g, row, it.head, t0, sm, false);
             __syncthreads();
             float x[4][4];
             pfx_logits<D>(sm, ty, tx, x);
@@ -525,7 +353,9 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_score_kernel(const PfxArgs
 }
 
 struct PfxPlan {
+    bool tc;
     int rt, kt, parts;
+    long long extra0;
     size_t off_wpre, off_prefix, off_rml, off_racc, off_iml, off_iacc, total;
 };
 
@@ -534,10 +364,13 @@ zp_status pfx_plan(const zp_cache_desc *D, int B, const DeviceInfo &dev, PfxPlan
     if (!(d == 64 || d == 128)) return fail(ZP_ERR_SHAPE, "prefix_decode: head_dim %d not in {64,128}", d);
     if (!(G == 1 || G == 2 || G == 4 || G == 8)) return fail(ZP_ERR_SHAPE, "prefix_decode: group size %d", G);
     if (B > kPfxMaxB) return fail(ZP_ERR_SHAPE, "prefix_decode: B %d > %d", B, kPfxMaxB);
-    p->rt = kPfxRows;
-    p->kt = kPfxTokens;
+    p->tc = D->dtype == ZP_BF16;
+    p->rt = p->tc ? kPtRows : kPfxRows;
+    p->kt = p->tc ? 128 : kPfxTokens;
     p->parts = dev.sm_count;
-    const size_t rows = (size_t)B * D->h_q, recs = rows + (size_t)p->parts * p->rt;
+    const size_t rows = (size_t)B * D->h_q;
+    p->extra0 = (long long)(p->tc ? 2 * rows : rows);
+    const size_t recs = (size_t)p->extra0 + (size_t)p->parts * p->rt;
     size_t off = 0;
     p->off_wpre = off;
     off = align_up(off + (size_t)(B + 1) * 4, 256);
@@ -555,68 +388,54 @@ zp_status pfx_plan(const zp_cache_desc *D, int B, const DeviceInfo &dev, PfxPlan
     return ZP_OK;
 }
 
-template <typename T, int D, int G>
+template <int D, int G>
 zp_status launch_part(const PfxArgs &a, cudaStream_t st) {
     const size_t smem = sizeof(PfxSmem<D>) + (size_t)(a.B + 1) * 4;
-    zp_status rc = set_max_dynamic_smem(reinterpret_cast<const void *>(prefix_part_kernel<T, D, G>), smem,
+    zp_status rc = set_max_dynamic_smem(reinterpret_cast<const void *>(prefix_part_kernel<D, G>), smem,
                                         "prefix_decode: shared-memory attribute");
     if (rc != ZP_OK) return rc;
-    prefix_part_kernel<T, D, G><<<a.parts, kPfxThreads, smem, st>>>(a);
-    cudaError_t e = cudaGetLastError();
+    prefix_part_kernel<D, G><<<a.parts, kPfxThreads, smem, st>>>(a);
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "prefix_decode: prefix kernel launch");
-    const long long warps = (long long)a.B * a.h_q;
-    prefix_merge_kernel<D><<<(unsigned)((warps + 7) / 8), 256, 0, st>>>(a);
-    e = cudaGetLastError();
+    return ZP_OK;
+}
+
+zp_status launch_merge(const PfxArgs &a, int d, cudaStream_t st) {
+    const unsigned grid = (unsigned)(((long long)a.B * a.h_q + 7) / 8);
+    if (d == 64) prefix_merge_kernel<64><<<grid, 256, 0, st>>>(a);
+    else prefix_merge_kernel<128><<<grid, 256, 0, st>>>(a);
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "prefix_decode: merge kernel launch");
     return ZP_OK;
 }
 
-template <typename T, int D, int G>
+template <int D, int G>
 zp_status launch_score(const PfxArgs &a, cudaStream_t st) {
     const size_t smem = sizeof(PfxSmem<D>) + (size_t)(a.B + 1) * 4;
-    zp_status rc = set_max_dynamic_smem(reinterpret_cast<const void *>(prefix_score_kernel<T, D, G>), smem,
+    zp_status rc = set_max_dynamic_smem(reinterpret_cast<const void *>(prefix_score_kernel<D, G>), smem,
                                         "prefix_decode: shared-memory attribute");
     if (rc != ZP_OK) return rc;
-    prefix_score_kernel<T, D, G><<<a.parts, kPfxThreads, smem, st>>>(a);
+    prefix_score_kernel<D, G><<<a.parts, kPfxThreads, smem, st>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "prefix_decode: score kernel launch");
     return ZP_OK;
 }
 
-// Calls f.template operator()<T, D, G>() for the cache's type and geometry.
-template <typename F>
-zp_status pfx_dispatch(const zp_cache_desc *D, F &&f) {
-    const int G = D->h_q / D->h_kv, d = D->head_dim;
-#define ZP_PFX_CASE(T, DD)                                          \
-    if (G == 1) return f.template operator()<T, DD, 1>();           \
-    if (G == 2) return f.template operator()<T, DD, 2>();           \
-    if (G == 4) return f.template operator()<T, DD, 4>();           \
-    if (G == 8) return f.template operator()<T, DD, 8>();
-    if (D->dtype == ZP_BF16 && d == 64) {
-        ZP_PFX_CASE(__nv_bfloat16, 64)
-    } else if (D->dtype == ZP_BF16) {
-        ZP_PFX_CASE(__nv_bfloat16, 128)
-    } else if (d == 64) {
-        ZP_PFX_CASE(float, 64)
-    } else {
-        ZP_PFX_CASE(float, 128)
-    }
-#undef ZP_PFX_CASE
-    return fail(ZP_ERR_SHAPE, "prefix_decode: no kernel for d=%d, group=%d", d, G);
+// fp32 caches: the kernel of the head dimension and group size.
+template <int D>
+zp_status launch_part_f32(const PfxArgs &a, int G, cudaStream_t st) {
+    if (G == 1) return launch_part<D, 1>(a, st);
+    if (G == 2) return launch_part<D, 2>(a, st);
+    if (G == 4) return launch_part<D, 4>(a, st);
+    return launch_part<D, 8>(a, st);
 }
-
-struct LaunchPart {
-    const PfxArgs &a;
-    cudaStream_t st;
-    template <typename T, int D, int G>
-    zp_status operator()() const { return launch_part<T, D, G>(a, st); }
-};
-struct LaunchScore {
-    const PfxArgs &a;
-    cudaStream_t st;
-    template <typename T, int D, int G>
-    zp_status operator()() const { return launch_score<T, D, G>(a, st); }
-};
+template <int D>
+zp_status launch_score_f32(const PfxArgs &a, int G, cudaStream_t st) {
+    if (G == 1) return launch_score<D, 1>(a, st);
+    if (G == 2) return launch_score<D, 2>(a, st);
+    if (G == 4) return launch_score<D, 4>(a, st);
+    return launch_score<D, 8>(a, st);
+}
 
 }  // namespace
 }  // namespace zp
@@ -688,6 +507,8 @@ extern "C" zp_status zp_prefix_decode_attn(const zp_cache_desc *D, const void *q
     a.rt = p.rt;
     a.kt = p.kt;
     a.parts = p.parts;
+    a.extra0 = p.extra0;
+    a.tc = p.tc;
     a.qscale = (float)(1.4426950408889634 / sqrt((double)D->head_dim));
     a.wpre = reinterpret_cast<int *>(ws + p.off_wpre);
     a.prefix = reinterpret_cast<int32_t *>(ws + p.off_prefix);
@@ -702,14 +523,18 @@ extern "C" zp_status zp_prefix_decode_attn(const zp_cache_desc *D, const void *q
     a.window = window;
     a.err = dev.error_word;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    rc = pfx_dispatch(D, LaunchPart{a, st});
+    const int d = D->head_dim;
+    if (p.tc) rc = prefix_part_tc(a, d, st);
+    else rc = d == 64 ? launch_part_f32<64>(a, G, st) : launch_part_f32<128>(a, G, st);
+    if (rc == ZP_OK) rc = launch_merge(a, d, st);
     if (rc != ZP_OK) return rc;
     const PrefixRecords pre = {a.prefix, a.init_acc, a.init_ml};
     rc = decode_after_prefix(D, q, k_cache, v_cache, block_table, table_stride, seq_lens, B, out, score_accum, score_rows,
                              n_score_rows, window, pre, workspace, dec, stream, &a.stats);
     if (rc != ZP_OK) return rc;
     if (score_accum) {
-        rc = pfx_dispatch(D, LaunchScore{a, st});
+        if (p.tc) rc = prefix_score_tc(a, d, st);
+        else rc = d == 64 ? launch_score_f32<64>(a, G, st) : launch_score_f32<128>(a, G, st);
         if (rc != ZP_OK) return rc;
     }
     return ok();

@@ -1,0 +1,705 @@
+// prefix_tc.cu -- the shared prefix on the fifth-generation tensor cores (bf16
+// caches): the dense product of a group's query rows with its prefix, and the
+// window score of the prefix tokens.  See prefix_attn.cu for the formulas and
+// the split of the work.
+//
+// prefix_part_tc_kernel: one persistent CTA per SM.  An item has up to 256 query
+// rows, two streams of 128 (one softmax warpgroup each, a thread per row):
+//   S_w = Q_w K^T   (tcgen05.mma, both operands in shared memory, 128 x 128)
+//   P_w = 2^(x - m) rounded to bf16, written over S_w in tensor memory
+//   O_w += P_w V    (A = P_w from tensor memory, B = V as it lies, d contiguous)
+// so that the tensor cores work on one stream while the other's softmax runs.
+// An item with at most 128 rows gives both streams the same rows and every
+// other tile of prefix tokens each; its pieces are joined like any others.
+// Tensor memory: S_0, S_1 (128 columns each), O_0, O_1 (d columns each).  The
+// running maximum m of a row is raised, and O_w rescaled, only when a tile
+// exceeds it by more than 2^8 (the result does not depend on m, and P stays
+// below 2^8); S_w of the next tile is complete only after O_w's last product,
+// so the rescaling needs no wait of its own.
+// K and V tiles of 128 tokens arrive by TMA as boxes of 16 token rows (a part of
+// one block) x 64 elements with the 128-byte swizzle, through a ring of stages.
+#include <math.h>
+
+#include "prefix_common.cuh"
+#include "prefix_tc.h"
+#include "tc05.cuh"
+
+namespace zp {
+namespace {
+
+constexpr int kPtTile = 128;                // prefix tokens per tile
+constexpr int kPtThreads = 32 * (2 + 8);    // TMA, MMA, two warpgroups
+constexpr float kPtRaise = 8.f;             // log2 units a tile may exceed the running maximum by
+
+// tcgen05.mma with A in tensor memory (bf16 pairs, one row per lane).
+__device__ __forceinline__ void tc_mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Shared-memory descriptor of a B operand that is contiguous along N (V: 64 dims
+// per 128-byte row, rows are tokens): groups of 8 tokens 1024 bytes apart
+// (stride offset), the next 64 dims `half` bytes further (leading offset).
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t half) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(half >> 4) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// Stores to the warp's 32 TMEM lanes, waited for in the same statement.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+template <int D>
+struct PtCfg {
+    static constexpr int KH = D / 64;
+    static constexpr int KS = D / 16;
+    static constexpr int HALF = kPtTile * 128;        // bytes of 128 rows x 64 elements
+    static constexpr int TILE = KH * HALF;            // a Q, K or V tile
+    static constexpr int STAGES = D == 128 ? 4 : 8;   // K and V tiles in flight
+    static constexpr int Q_OFF = 0;                   // two query tiles
+    static constexpr int ST_OFF = 2 * TILE;
+    static constexpr int BAR_OFF = ST_OFF + STAGES * TILE;
+    static constexpr int PRE_OFF = BAR_OFF + 512;
+    static constexpr int smem(int B) { return PRE_OFF + (B + 1) * 4 + 1024; }
+    static constexpr uint32_t TMEM_COLS = 512;
+    static constexpr uint32_t S_COL = 0, O_COL = 256;
+    static constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, 128);
+    static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D) | (1u << 16);  // B contiguous along N
+};
+
+// One CTA's share of an item.
+struct PtSeg {
+    PfxGroup g;
+    int head, rt;
+    int t_b, t_e;  // token tiles
+    int rows;      // query rows of the item (<= 256)
+    bool split;    // at most 128 rows: the streams take alternate tiles
+};
+
+__device__ __forceinline__ PtSeg pt_segment(const PfxArgs &a, const int *pre, int ng, int w, int w1) {
+    PtSeg s;
+    const int gi = pfx_find(pre, ng, w);
+    s.g = pfx_group(a, gi);
+    const int x = w - pre[gi], item = x / s.g.kts;
+    const PfxItem it = pfx_item(s.g, item);
+    s.head = it.head;
+    s.rt = it.rt;
+    s.t_b = x - item * s.g.kts;
+    s.t_e = min(s.g.kts, s.t_b + (w1 - w));
+    s.rows = min(kPtRows, s.g.n * (a.h_q / a.h_kv) - s.rt * kPtRows);
+    s.split = s.rows <= kPtRows / 2;
+    return s;
+}
+
+// Tiles of stream w in a segment.
+__device__ __forceinline__ int pt_tiles(const PtSeg &s, int w) {
+    const int n = s.t_e - s.t_b;
+    return s.split ? (n - w + 1) / 2 : n;
+}
+
+// First row (block * b + slot) of the 16 tokens from `tok`; a row outside the
+// tensor (zeros are read) beyond the prefix and for a bad block.
+__device__ __forceinline__ int pt_rows16(const PfxArgs &a, const PfxGroup &g, const int32_t *row, int tok) {
+    if (tok >= g.tokens) return -16;
+    const long long s = pfx_slot(a, row, tok);
+    return s < 0 ? -16 : (int)s;
+}
+
+// This thread's query row into a swizzled tile (zeros beyond the last row).
+template <int D>
+__device__ __forceinline__ void pt_load_q(const PfxArgs &a, const PtSeg &s, int r, int row_in_tile, unsigned char *tile) {
+    const int G = a.h_q / a.h_kv;
+    const uint4 *src = nullptr;
+    const int rr = s.rt * kPtRows + r;
+    if (r < s.rows) {
+        const int e = pfx_member(a, s.g.m0 + rr / G);
+        if (e >= 0)
+            src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
+                                                  ((size_t)e * a.h_q + s.head * G + rr % G) * D);
+    }
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+        const uint4 v = src ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>(tile + (c >> 3) * PtCfg<D>::HALF + row_in_tile * 128 +
+                                   (((c & 7) ^ (row_in_tile & 7)) << 4)) = v;
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPtThreads, 1)
+    prefix_part_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                          const PfxArgs a) {
+    using C = PtCfg<D>;
+    extern __shared__ unsigned char pt_raw[];
+    unsigned char *smem =
+        reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(pt_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);
+    uint64_t *empty = full + C::STAGES;
+    uint64_t *q_full = empty + C::STAGES;  // [2] query tile written
+    uint64_t *s_full = q_full + 2;         // [2] logits complete
+    uint64_t *p_full = s_full + 2;         // [2] probabilities written
+    uint64_t *o_full = p_full + 2;         // [2] last product of the segment complete
+    uint64_t *drain = o_full + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int *pre = reinterpret_cast<int *>(smem + C::PRE_OFF);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::STAGES; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], 4);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&o_full[i], 1);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    const int ng = pfx_groups(a);
+    const int W = pfx_scan(a, ng, pre);  // (ends with a barrier)
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    if (blockIdx.x == 0) pfx_publish(a, ng, pre);
+    const int w0 = pfx_start(blockIdx.x, W, a.parts), w1 = pfx_start(blockIdx.x + 1, W, a.parts);
+
+    if (warp == 0) {
+        // ---------------- producer: K and V tiles in order
+        uint32_t fill = 0;
+        const int q = lane >> 1, half = lane & 1;  // lanes 0..15: 16-token group, 64-element half
+        bool ok_all = true;
+        if (lane == 0) {
+            prefetch_tensormap(&kmap);
+            prefetch_tensormap(&vmap);
+        }
+        for (int w = w0; w < w1 && ok_all;) {
+            const PtSeg s = pt_segment(a, pre, ng, w, w1);
+            const int32_t *row = pfx_row(a, s.g);
+            int z_next = lane < 16 ? pt_rows16(a, s.g, row, s.t_b * kPtTile + 16 * q) : 0;
+            for (int t = s.t_b; t < s.t_e && ok_all; ++t) {
+                const int z = z_next;
+                if (t + 1 < s.t_e) z_next = lane < 16 ? pt_rows16(a, s.g, row, (t + 1) * kPtTile + 16 * q) : 0;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    const uint32_t st = fill % C::STAGES;
+                    bool got = true;
+                    if (lane == 0) {
+                        got = mbar_wait_bounded(&empty[st], ((fill / C::STAGES) & 1) ^ 1, a.err, abort_flag, 0x601);
+                        if (got) mbar_arrive_expect_tx(&full[st], C::TILE);
+                    }
+                    got = __shfl_sync(0xFFFFFFFFu, got ? 1 : 0, 0) != 0;
+                    if (!got) {
+                        ok_all = false;
+                        break;
+                    }
+                    ++fill;
+                    unsigned char *dst = smem + C::ST_OFF + st * C::TILE;
+                    if (lane < 16 && half < C::KH)
+                        tma_load_3d(dst + half * C::HALF + q * 2048, kv ? &vmap : &kmap, half * 64, s.head, z, &full[st]);
+                    __syncwarp();
+                }
+            }
+            w += s.t_e - s.t_b;
+        }
+        if (lane == 0 && *abort_flag) {  // copies in flight land before the CTA ends
+            volatile int never = 0;
+            for (uint32_t f = fill > C::STAGES ? fill - C::STAGES : 0; f < fill; ++f)
+                mbar_wait_bounded(&full[f % C::STAGES], (f / C::STAGES) & 1, a.err, &never, 0x602);
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer (one thread)
+        if (lane == 0) {
+            uint32_t base = 0, n_p[2] = {0, 0}, n_q[2] = {0, 0};
+            const uint32_t q_addr = smem_u32(smem + C::Q_OFF), st_addr = smem_u32(smem + C::ST_OFF);
+            bool ok_all = true;
+            for (int w = w0; w < w1 && ok_all;) {
+                const PtSeg s = pt_segment(a, pre, ng, w, w1);
+                const int n_t[2] = {pt_tiles(s, 0), pt_tiles(s, 1)};
+                // logits of stream x, its tile j
+                auto qk = [&](int x, int j) -> bool {
+                    const uint32_t f = base + 2 * (s.split ? 2 * j + x : j);
+                    const uint32_t st = f % C::STAGES;
+                    if (!mbar_wait_bounded(&full[st], (f / C::STAGES) & 1, a.err, abort_flag, 0x603)) return false;
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < C::KS; ++ks) {
+                        const uint32_t o = (ks >> 2) * C::HALF + (ks & 3) * 32;
+                        tc_mma_bf16(tmem + C::S_COL + x * 128, sdesc_k_sw128(q_addr + x * C::TILE + o),
+                                    sdesc_k_sw128(st_addr + st * C::TILE + o), C::IDESC_QK, ks > 0 ? 1u : 0u);
+                    }
+                    if (s.split || x == 1) tc_commit(&empty[st]);
+                    tc_commit(&s_full[x]);
+                    return true;
+                };
+                auto pv = [&](int x, int j) -> bool {
+                    const uint32_t f = base + 2 * (s.split ? 2 * j + x : j) + 1;
+                    const uint32_t st = f % C::STAGES;
+                    if (!mbar_wait_bounded(&full[st], (f / C::STAGES) & 1, a.err, abort_flag, 0x604)) return false;
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < kPtTile / 16; ++ks)
+                        tc_mma_bf16_ta(tmem + C::O_COL + x * D, tmem + C::S_COL + x * 128 + ks * 8,
+                                       sdesc_mn_sw128(st_addr + st * C::TILE + ks * 2048, C::HALF), C::IDESC_PV,
+                                       j > 0 || ks > 0 ? 1u : 0u);
+                    if (s.split || x == 1) tc_commit(&empty[st]);
+                    return true;
+                };
+                for (int x = 0; x < 2 && ok_all; ++x) {
+                    if (n_t[x] == 0) continue;
+                    ok_all = mbar_wait_bounded(&q_full[x], n_q[x] & 1, a.err, abort_flag, 0x605);
+                    ++n_q[x];
+                    ok_all = ok_all && qk(x, 0);
+                }
+                for (int j = 0; j < n_t[0] && ok_all; ++j)  // n_t[0] >= n_t[1]
+                    for (int x = 0; x < 2 && ok_all; ++x) {
+                        if (j >= n_t[x]) continue;
+                        ok_all = mbar_wait_bounded(&p_full[x], n_p[x] & 1, a.err, abort_flag, 0x606);
+                        ++n_p[x];
+                        if (!ok_all) break;
+                        tc_fence_after();
+                        ok_all = pv(x, j);
+                        if (!ok_all) break;
+                        if (j + 1 < n_t[x]) ok_all = qk(x, j + 1);
+                        else tc_commit(&o_full[x]);
+                    }
+                base += 2 * (s.t_e - s.t_b);
+                w += s.t_e - s.t_b;
+            }
+        }
+    } else {
+        // ---------------- softmax: warpgroup x = stream, thread = query row (TMEM lane)
+        const int x = (warp - 2) >> 2;
+        const int quarter = warp & 3;
+        const int tr = quarter * 32 + lane;  // row of the tile
+        const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16);
+        const uint32_t s_t = lane_base + C::S_COL + x * 128, o_t = lane_base + C::O_COL + x * D;
+        uint32_t n_s = 0, n_o = 0;
+        bool ok_all = true;
+        for (int w = w0; w < w1 && ok_all;) {
+            const PtSeg s = pt_segment(a, pre, ng, w, w1);
+            const int n_t = pt_tiles(s, x);
+            const int r = s.split ? tr : x * 128 + tr;  // row of the item
+            float m = -INFINITY, l = 0.f;
+            if (n_t > 0) {
+                pt_load_q<D>(a, s, r, tr, smem + C::Q_OFF + x * C::TILE);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&q_full[x]);
+            }
+            for (int j = 0; j < n_t; ++j) {
+                if (!mbar_wait_bounded(&s_full[x], n_s & 1, a.err, abort_flag, 0x607)) {
+                    ok_all = false;
+                    break;
+                }
+                ++n_s;
+                tc_fence_after();
+                const int t = s.t_b + (s.split ? 2 * j + x : j);
+                const int valid = min(kPtTile, s.g.tokens - t * kPtTile);  // a multiple of 16
+                uint32_t v0[64], v1[64];
+                tmem_ld64(s_t, v0);
+                tmem_ld64(s_t + 64, v1);
+                if (valid < kPtTile) {
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) {
+                        if (c >= valid) v0[c] = 0xFF800000u;  // -inf
+                        if (c + 64 >= valid) v1[c] = 0xFF800000u;
+                    }
+                }
+                float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 64; ++c) {
+                    mx0 = fmaxf(mx0, __uint_as_float(v0[c]));
+                    mx1 = fmaxf(mx1, __uint_as_float(v1[c]));
+                }
+                const float mx = fmaxf(mx0, mx1) * a.qscale;
+                // raise the maximum (and rescale what is summed) only beyond 2^8
+                const bool raise = mx > m + kPtRaise;  // true at the first tile (m = -inf)
+                if (__any_sync(0xFFFFFFFFu, raise)) {
+                    const float al = raise ? (j == 0 ? 0.f : ex2_approx(m - mx)) : 1.f;
+                    if (raise) m = mx;
+                    l *= al;
+                    if (j > 0) {
+#pragma unroll 1
+                        for (int c0 = 0; c0 < D; c0 += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(o_t + c0, o);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * al);
+                            tmem_st32(o_t + c0, o);
+                        }
+                    }
+                }
+                const float2 sc = make_float2(a.qscale, a.qscale), nm = make_float2(-m, -m);
+                float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+                uint32_t p[32];
+                auto half_tile = [&](const uint32_t(&v)[64], uint32_t col) {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        float2 y = ffma2(make_float2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])), sc, nm);
+                        y.x = ex2_approx(y.x);
+                        y.y = ex2_approx(y.y);
+                        float2 &sum = c & 1 ? sum1 : sum0;
+                        sum.x += y.x;
+                        sum.y += y.y;
+                        p[c] = f2_to_bf2(y.x, y.y);
+                    }
+                    tmem_st32(s_t + col, p);
+                };
+                half_tile(v0, 0);
+                half_tile(v1, 32);
+                l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[x]);
+            }
+            if (!ok_all) break;
+            // the piece's record
+            long long at = -1;
+            if (r < s.rows)
+                at = s.t_b == 0 ? pfx_main_row(a, s.g, s.head, s.rt * kPtRows + r) + (s.split && x ? (long long)a.B * a.h_q : 0)
+                                : a.extra0 + (long long)blockIdx.x * kPtRows + x * 128 + tr;
+            if (n_t > 0) {
+                if (!mbar_wait_bounded(&o_full[x], n_o & 1, a.err, abort_flag, 0x608)) break;
+                ++n_o;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(o_t + c0, o);
+                    if (at >= 0) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(a.rec_acc + at * D + c0);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) dst[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                    }
+                }
+                tc_fence_before();
+            }
+            if (at >= 0) a.rec_ml[at] = make_float2(m, l);
+            w += s.t_e - s.t_b;
+        }
+    }
+
+    __syncthreads();
+    if (*abort_flag && threadIdx.x == 32) {
+        volatile int never = 0;
+        tc_commit(drain);
+        mbar_wait_bounded(drain, 0, a.err, &never, 0x609);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
+}
+
+// ===========================================================================
+// Window score of the prefix tokens: the 128 tokens of a tile are the M operand
+// (a thread per token), the item's query rows the N operand, so the maximum over
+// a kv head's q heads is taken in registers and consecutive lanes write
+// consecutive tokens of a score row.  Accumulators of two tiles (256 columns
+// each); per (token, sequence) one exponential of max_h (x_h - c_h),
+// c = m + log2 l.
+template <int D>
+struct PsCfg {
+    static constexpr int KH = D / 64;
+    static constexpr int KS = D / 16;
+    static constexpr int A_HALF = kPtTile * 128;
+    static constexpr int TILE = KH * A_HALF;           // K tile
+    static constexpr int B_HALF = kPtRows * 128;       // 256 query rows x 64 elements
+    static constexpr int B_BYTES = KH * B_HALF;
+    static constexpr int STAGES = 4;
+    static constexpr int ST_OFF = B_BYTES;
+    static constexpr int BAR_OFF = ST_OFF + STAGES * TILE;
+    static constexpr int C_OFF = BAR_OFF + 256;        // c of every row
+    static constexpr int M_OFF = C_OFF + kPtRows * 4;  // score row of every member: row * 2 + first, -1 none
+    static constexpr int PRE_OFF = M_OFF + kPtRows * 4;
+    static constexpr int smem(int B) { return PRE_OFF + (B + 1) * 4 + 1024; }
+};
+
+template <int D, int G>
+__global__ void __launch_bounds__(kPtThreads, 1)
+    prefix_score_tc_kernel(const __grid_constant__ CUtensorMap kmap, const PfxArgs a) {
+    using C = PsCfg<D>;
+    extern __shared__ unsigned char pt_raw[];
+    unsigned char *smem =
+        reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(pt_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);
+    uint64_t *empty = full + C::STAGES;
+    uint64_t *q_full = empty + C::STAGES;  // the item's rows and statistics written (every epilogue warp)
+    uint64_t *q_done = q_full + 1;         // the item finished by every epilogue warp
+    uint64_t *acc_full = q_done + 1;       // [2]
+    uint64_t *acc_empty = acc_full + 2;  // [2]
+    uint64_t *drain = acc_empty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    float *cs = reinterpret_cast<float *>(smem + C::C_OFF);
+    int *ms = reinterpret_cast<int *>(smem + C::M_OFF);
+    int *pre = reinterpret_cast<int *>(smem + C::PRE_OFF);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::STAGES; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        mbar_init(q_full, 8);
+        mbar_init(q_done, 8);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], 8);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    const int ng = pfx_groups(a);
+    const int W = pfx_scan(a, ng, pre);
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int w0 = pfx_start(blockIdx.x, W, gridDim.x), w1 = pfx_start(blockIdx.x + 1, W, gridDim.x);
+
+    if (warp == 0) {
+        uint32_t fill = 0;
+        const int q = lane >> 1, half = lane & 1;
+        bool ok_all = true;
+        if (lane == 0) prefetch_tensormap(&kmap);
+        for (int w = w0; w < w1 && ok_all;) {
+            const PtSeg s = pt_segment(a, pre, ng, w, w1);
+            const int32_t *row = pfx_row(a, s.g);
+            for (int t = s.t_b; t < s.t_e; ++t, ++fill) {
+                const int z = lane < 16 ? pt_rows16(a, s.g, row, t * kPtTile + 16 * q) : 0;
+                const uint32_t st = fill % C::STAGES;
+                bool got = true;
+                if (lane == 0) {
+                    got = mbar_wait_bounded(&empty[st], ((fill / C::STAGES) & 1) ^ 1, a.err, abort_flag, 0x611);
+                    if (got) mbar_arrive_expect_tx(&full[st], C::TILE);
+                }
+                got = __shfl_sync(0xFFFFFFFFu, got ? 1 : 0, 0) != 0;
+                if (!got) {
+                    ok_all = false;
+                    break;
+                }
+                if (lane < 16 && half < C::KH)
+                    tma_load_3d(smem + C::ST_OFF + st * C::TILE + half * C::A_HALF + q * 2048, &kmap, half * 64, s.head, z,
+                                &full[st]);
+                __syncwarp();
+            }
+            w += s.t_e - s.t_b;
+        }
+        if (lane == 0 && *abort_flag) {
+            volatile int never = 0;
+            for (uint32_t f = fill > C::STAGES ? fill - C::STAGES : 0; f < fill; ++f)
+                mbar_wait_bounded(&full[f % C::STAGES], (f / C::STAGES) & 1, a.err, &never, 0x612);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            uint32_t fill = 0, n_q = 0;
+            const uint32_t b_addr = smem_u32(smem), st_addr = smem_u32(smem + C::ST_OFF);
+            bool ok_all = true;
+            for (int w = w0; w < w1 && ok_all;) {
+                const PtSeg s = pt_segment(a, pre, ng, w, w1);
+                const uint32_t idesc = idesc_bf16_f32(128, (s.rows + 15) / 16 * 16);
+                ok_all = mbar_wait_bounded(q_full, n_q & 1, a.err, abort_flag, 0x613);
+                ++n_q;
+                for (int t = s.t_b; t < s.t_e && ok_all; ++t, ++fill) {
+                    const uint32_t st = fill % C::STAGES, ab = fill & 1;
+                    ok_all = mbar_wait_bounded(&full[st], (fill / C::STAGES) & 1, a.err, abort_flag, 0x614) &&
+                             mbar_wait_bounded(&acc_empty[ab], ((fill >> 1) & 1) ^ 1, a.err, abort_flag, 0x615);
+                    if (!ok_all) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < C::KS; ++ks)
+                        tc_mma_bf16(tmem + ab * 256,
+                                    sdesc_k_sw128(st_addr + st * C::TILE + (ks >> 2) * C::A_HALF + (ks & 3) * 32),
+                                    sdesc_k_sw128(b_addr + (ks >> 2) * C::B_HALF + (ks & 3) * 32), idesc, ks > 0 ? 1u : 0u);
+                    tc_commit(&empty[st]);
+                    tc_commit(&acc_full[ab]);
+                }
+                w += s.t_e - s.t_b;
+            }
+        }
+    } else {
+        const int et = threadIdx.x - 64;          // 0..255: query row while loading
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const float inv_w = 1.f / (float)a.window;
+        uint32_t tile = 0, item = 0;
+        bool ok_all = true;
+        // (every wait is bounded, so a warp that stops cannot leave another waiting for ever)
+        for (int w = w0; w < w1 && ok_all; ++item) {
+            const PtSeg s = pt_segment(a, pre, ng, w, w1);
+            // the item's rows and statistics: once every warp has finished the last
+            // item (whose products are then complete)
+            if (!mbar_wait_bounded(q_done, (item & 1) ^ 1, a.err, abort_flag, 0x618)) break;
+            {
+                const int r = et, rr = s.rt * kPtRows + r;
+                const uint4 *src = nullptr;
+                float c = INFINITY;
+                int mrow = -1;
+                if (r < s.rows) {
+                    const int e = pfx_member(a, s.g.m0 + rr / G);
+                    if (e >= 0) {
+                        src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
+                                                              ((size_t)e * a.h_q + s.head * G + rr % G) * D);
+                        bool first;
+                        mrow = pfx_score_row(a, e, &first);
+                        if (mrow >= 0) {
+                            const float2 ml = a.stats[(size_t)e * a.h_q + s.head * G + rr % G];
+                            c = ml.y > 0.f ? ml.x + log2f(ml.y) : INFINITY;
+                            mrow = mrow * 2 + (first ? 1 : 0);
+                        }
+                    }
+                }
+                cs[r] = c;
+                if (r % G == 0) ms[r / G] = mrow;
+#pragma unroll
+                for (int ch = 0; ch < D / 8; ++ch) {
+                    const uint4 v = src ? __ldg(src + ch) : make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(smem + (ch >> 3) * C::B_HALF + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+            if (!mbar_wait_bounded(q_full, item & 1, a.err, abort_flag, 0x619)) break;
+            for (int t = s.t_b; t < s.t_e; ++t, ++tile) {
+                const uint32_t ab = tile & 1;
+                if (!mbar_wait_bounded(&acc_full[ab], (tile >> 1) & 1, a.err, abort_flag, 0x616)) {
+                    ok_all = false;
+                    break;
+                }
+                tc_fence_after();
+                const int tok = t * kPtTile + 32 * quarter + lane;
+                const uint32_t acc = tmem + ((uint32_t)(32 * quarter) << 16) + ab * 256 + half * 128;
+                const bool live = tok < s.g.tokens;
+#pragma unroll 1
+                for (int c0 = 0; c0 < 128; c0 += 32) {
+                    if (half * 128 + c0 >= s.rows) break;
+                    uint32_t v[32];
+                    tmem_ld32(acc + c0, v);
+#pragma unroll
+                    for (int i = 0; i < 32 / G; ++i) {
+                        const int mi = (half * 128 + c0) / G + i;
+                        const int mr = ms[mi];
+                        float e = -INFINITY;
+#pragma unroll
+                        for (int j = 0; j < G; ++j)
+                            e = fmaxf(e, fmaf(__uint_as_float(v[i * G + j]), a.qscale, -cs[half * 128 + c0 + i * G + j]));
+                        if (mr >= 0 && live) {
+                            float *dst = a.score + ((size_t)(mr >> 1) * a.h_kv + s.head) * a.score_stride + tok;
+                            const float val = ex2_approx(e) * inv_w;
+                            *dst = (mr & 1) ? val : *dst + val;
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&acc_empty[ab]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_done);
+            w += s.t_e - s.t_b;
+        }
+    }
+    __syncthreads();
+    if (*abort_flag && threadIdx.x == 32) {
+        volatile int never = 0;
+        tc_commit(drain);
+        mbar_wait_bounded(drain, 0, a.err, &never, 0x617);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+zp_status pt_map(CUtensorMap *map, const void *base, const PfxArgs &a, int d) {
+    const uint64_t dims[3] = {(uint64_t)d, (uint64_t)a.h_kv, (uint64_t)a.n_total * a.b};
+    const uint64_t strides[2] = {(uint64_t)d * 2, (uint64_t)a.h_kv * d * 2};
+    const uint32_t box[3] = {64, 1, 16};
+    return encode_tmap_bf16_3d(map, base, dims, strides, box, "prefix_decode");
+}
+
+template <int D>
+zp_status launch_part_tc(const PfxArgs &a, cudaStream_t st) {
+    CUtensorMap km, vm;
+    zp_status rc = pt_map(&km, a.k, a, D);
+    if (rc != ZP_OK) return rc;
+    rc = pt_map(&vm, a.v, a, D);
+    if (rc != ZP_OK) return rc;
+    const size_t smem = PtCfg<D>::smem(a.B);
+    rc = set_max_dynamic_smem(reinterpret_cast<const void *>(prefix_part_tc_kernel<D>), smem,
+                              "prefix_decode: shared-memory attribute");
+    if (rc != ZP_OK) return rc;
+    prefix_part_tc_kernel<D><<<a.parts, kPtThreads, smem, st>>>(km, vm, a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "prefix_decode: prefix kernel launch");
+    return ZP_OK;
+}
+
+template <int D, int G>
+zp_status launch_score_tc(const PfxArgs &a, cudaStream_t st) {
+    CUtensorMap km;
+    zp_status rc = pt_map(&km, a.k, a, D);
+    if (rc != ZP_OK) return rc;
+    const size_t smem = PsCfg<D>::smem(a.B);
+    rc = set_max_dynamic_smem(reinterpret_cast<const void *>(prefix_score_tc_kernel<D, G>), smem,
+                              "prefix_decode: shared-memory attribute");
+    if (rc != ZP_OK) return rc;
+    prefix_score_tc_kernel<D, G><<<a.parts, kPtThreads, smem, st>>>(km, a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "prefix_decode: score kernel launch");
+    return ZP_OK;
+}
+
+}  // namespace
+
+zp_status prefix_part_tc(const PfxArgs &a, int d, cudaStream_t st) {
+    return d == 64 ? launch_part_tc<64>(a, st) : launch_part_tc<128>(a, st);
+}
+
+zp_status prefix_score_tc(const PfxArgs &a, int d, cudaStream_t st) {
+    const int G = a.h_q / a.h_kv;
+    if (d == 64) {
+        if (G == 1) return launch_score_tc<64, 1>(a, st);
+        if (G == 2) return launch_score_tc<64, 2>(a, st);
+        if (G == 4) return launch_score_tc<64, 4>(a, st);
+        return launch_score_tc<64, 8>(a, st);
+    }
+    if (G == 1) return launch_score_tc<128, 1>(a, st);
+    if (G == 2) return launch_score_tc<128, 2>(a, st);
+    if (G == 4) return launch_score_tc<128, 4>(a, st);
+    return launch_score_tc<128, 8>(a, st);
+}
+
+}  // namespace zp
