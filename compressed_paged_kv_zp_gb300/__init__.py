@@ -128,12 +128,13 @@ def _load() -> ctypes.CDLL:
     lib.zp_paged_decode_attn_noalloc.argtypes = [D, P, P, P, P, I32, P, I32, P, P, P, I32, I32, P]
     lib.zp_debug_noalloc_preset_ctl.argtypes = [I32, ctypes.c_uint64]
     lib.zp_append_kv.argtypes = [D, P, P, P, P, P, I32, P, I32, P]
+    G = ctypes.POINTER(_PrefixGroups)
     lib.zp_build_slots.argtypes = [D, P, P, I32, P, P, I32, P, I32, P, P, I32, P, P, P]
     lib.zp_write_kv.argtypes = [D, P, P, I64, I64, P, I32, P, P, I64, I32, P]
-    lib.zp_prefix_plan.argtypes = [D, P, I32, P, I32, I32, I32, P, P]
+    lib.zp_prefix_plan.argtypes = [D, P, I32, P, I32, I32, I32, G, P]
     lib.zp_prefix_decode_workspace_size.restype = SZ
     lib.zp_prefix_decode_workspace_size.argtypes = [D, I32, I32]
-    lib.zp_prefix_decode_attn.argtypes = [D, P, P, P, P, I32, P, I32, P, P, P, P, I32, I32, P, SZ, P]
+    lib.zp_prefix_decode_attn.argtypes = [D, P, P, P, P, I32, P, I32, G, P, P, P, I32, I32, P, SZ, P]
     lib.zp_needs_compression.argtypes = [I32, I32, I32]
     lib.zp_needs_compression_batch.argtypes = [P, P, I32, I32, I32, P, P, P]
     lib.zp_score_workspace_size.restype = SZ
@@ -265,40 +266,52 @@ def zp_append_kv(desc, k_new, v_new, k_cache, v_cache, block_table, seq_lens, st
 
 
 # ----------------------------------------------------------------------------- shared prompts
-def _ints(t, name: str, numel=None):
-    """Pointer of an int32 CUDA tensor (None stays None) of `numel` elements, on the current device."""
+# These calls run before or inside every decode step, so their checks are kept to
+# a few attribute reads per tensor: pointers go to ctypes as ints.
+def _ptr_on(t, dev: int, name: str):
+    """Address of a contiguous tensor on CUDA device `dev`, the current one (None stays None)."""
     if t is None:
         return None
-    if t.dtype != torch.int32:
+    if t.get_device() != dev:
+        raise ValueError("%s must be a CUDA tensor on the current device, is on %s" % (name, t.device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _ints(t, dev: int, name: str, numel=None):
+    """_ptr_on of an int32 tensor, of `numel` elements where given."""
+    if t is None:
+        return None
+    if t.dtype is not torch.int32:
         raise ValueError("%s must be int32" % name)
     if numel is not None and t.numel() != numel:
         raise ValueError("%s must have %d elements, has %d" % (name, numel, t.numel()))
-    return _here(t, name)
+    return _ptr_on(t, dev, name)
 
 
-def _here(t, name: str):
-    """Pointer of a contiguous CUDA tensor on the current device (None stays None)."""
-    if t is None:
-        return None
-    p = _dev(t, name)
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, torch.cuda.current_device()))
-    return p
+def _device() -> int:
+    return torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -2
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _table(block_table):
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B][table_stride]")
-    return int(block_table.shape[0]), int(block_table.shape[1])
+    return block_table.shape
 
 
-def _cache_dtype(desc, t, name: str):
+def _like_cache(desc, t, name: str):
     if _DTYPES.get(t.dtype) != desc.dtype:
         raise ValueError("%s is %s, not the cache's type" % (name, t.dtype))
 
 
-def _cache_shape(desc, t, name: str):
-    if tuple(t.shape[-4:]) != (desc.n_total_blocks, desc.block_size, desc.h_kv, desc.head_dim):
+def _cache(desc, t, name: str):
+    _like_cache(desc, t, name)
+    if t.shape[-4:] != (desc.n_total_blocks, desc.block_size, desc.h_kv, desc.head_dim):
         raise ValueError("%s must be [N_total][b][h_kv][d] (or one of these per layer), is %s" % (name, tuple(t.shape)))
 
 
@@ -309,15 +322,18 @@ def zp_build_slots(desc, block_table, old_lens, new_lens, slots, cu_tokens, fres
     slots and positions int32 [max_tokens] (padded with -1), cu_tokens [B+1],
     n_used [1].  table_out: a separate table for the result (None: in place)."""
     B, table_stride = _table(block_table)
-    if table_out is None:
-        table_out = block_table
-    elif table_out.shape != block_table.shape:
+    dev, room = _device(), slots.numel()
+    table = _ints(block_table, dev, "block_table")
+    if table_out is not None and table_out.shape != block_table.shape:
         raise ValueError("table_out must have block_table's shape")
-    _check(lib.zp_build_slots(ctypes.byref(desc), _ints(block_table, "block_table"), _ints(table_out, "table_out"),
-                              table_stride, _ints(old_lens, "old_lens", B), _ints(new_lens, "new_lens", B), B,
-                              _ints(fresh, "fresh"), 0 if fresh is None else fresh.numel(), _ints(slots, "slots"),
-                              _ints(positions, "positions", slots.numel()), slots.numel(),
-                              _ints(cu_tokens, "cu_tokens", B + 1), _ints(n_used, "n_used", 1), _stream(stream)))
+    rc = lib.zp_build_slots(desc, table, table if table_out is None else _ints(table_out, dev, "table_out"),
+                            table_stride, _ints(old_lens, dev, "old_lens", B), _ints(new_lens, dev, "new_lens", B), B,
+                            _ints(fresh, dev, "fresh"), 0 if fresh is None else fresh.numel(),
+                            _ints(slots, dev, "slots"), _ints(positions, dev, "positions", room), room,
+                            _ints(cu_tokens, dev, "cu_tokens", B + 1), _ints(n_used, dev, "n_used", 1),
+                            _raw_stream(stream, dev))
+    if rc:
+        _check(rc)
 
 
 def zp_write_kv(desc, k_new, v_new, slots, k_cache, v_cache, stream=None) -> None:
@@ -325,32 +341,32 @@ def zp_write_kv(desc, k_new, v_new, slots, k_cache, v_cache, stream=None) -> Non
     k_new, v_new: [n][h_kv][d] for one layer, or [layers][n][h_kv][d] with caches
     [layers][N_total][b][h_kv][d].  The rows [h_kv][d] are contiguous; the token
     and layer strides are free (a slice of a fused projection)."""
-    row = (desc.h_kv, desc.head_dim)
-    layers = int(k_cache.shape[0]) if k_cache.dim() == 5 else 1
-    lead = (layers,) if k_cache.dim() == 5 else ()
-    n = int(slots.numel())
+    n, h_kv, d = slots.numel(), desc.h_kv, desc.head_dim
+    several = k_cache.dim() == 5
+    layers = k_cache.shape[0] if several else 1
+    shape = (layers, n, h_kv, d) if several else (n, h_kv, d)
+    dev = _device()
     for t, name in ((k_new, "k_new"), (v_new, "v_new")):
-        if tuple(t.shape) != lead + (n,) + row:
-            raise ValueError("%s must be %s, is %s" % (name, lead + (n,) + row, tuple(t.shape)))
-        _cache_dtype(desc, t, name)
-        if not t.is_cuda or t.device.index != torch.cuda.current_device():
-            raise ValueError("%s must be a CUDA tensor on the current device" % name)
-        if n and t.stride()[-2:] != (desc.head_dim, 1):
-            raise ValueError("%s: the row of a token must be contiguous" % name)
-    if n and k_new.stride() != v_new.stride():
-        raise ValueError("k_new and v_new must have the same strides")
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _cache_dtype(desc, t, name)
-        _cache_shape(desc, t, name)
+        _like_cache(desc, t, name)
+        if t.shape != shape:
+            raise ValueError("%s must be %s, is %s" % (name, shape, tuple(t.shape)))
+        if t.get_device() != dev:
+            raise ValueError("%s must be a CUDA tensor on the current device, is on %s" % (name, t.device))
+    strides = k_new.stride()
+    if n and (strides[-2:] != (d, 1) or v_new.stride() != strides):
+        raise ValueError("the row [h_kv][d] of a token must be contiguous, and k_new and v_new must have the same strides")
+    _cache(desc, k_cache, "k_cache")
+    _cache(desc, v_cache, "v_cache")
     if v_cache.shape != k_cache.shape:
         raise ValueError("k_cache and v_cache must have the same shape")
     if n == 0:
         return
-    token_stride = int(k_new.stride(-3)) if n > 1 else max(int(k_new.stride(-3)), row[0] * row[1])
-    _check(lib.zp_write_kv(ctypes.byref(desc), ctypes.c_void_p(k_new.data_ptr()), ctypes.c_void_p(v_new.data_ptr()),
-                           token_stride, int(k_new.stride(0)) if layers > 1 else 0, _ints(slots, "slots"), n,
-                           _here(k_cache, "k_cache"), _here(v_cache, "v_cache"),
-                           int(k_cache.stride(0)) if layers > 1 else 0, layers, _stream(stream)))
+    rc = lib.zp_write_kv(desc, k_new.data_ptr(), v_new.data_ptr(), strides[-3] if n > 1 else max(strides[-3], h_kv * d),
+                         strides[0] if layers > 1 else 0, _ints(slots, dev, "slots"), n, _ptr_on(k_cache, dev, "k_cache"),
+                         _ptr_on(v_cache, dev, "v_cache"), k_cache.stride(0) if layers > 1 else 0, layers,
+                         _raw_stream(stream, dev))
+    if rc:
+        _check(rc)
 
 
 class PrefixPlan:
@@ -360,13 +376,13 @@ class PrefixPlan:
     table; a scheduler that knows its groups may fill them itself."""
 
     def __init__(self, prefix_lens, n_groups, group_start, members, group_blocks):
-        B = int(prefix_lens.numel())
-        self.B = B
+        self.B = B = prefix_lens.numel()
         self.prefix_lens, self.n_groups, self.group_start = prefix_lens, n_groups, group_start
         self.members, self.group_blocks = members, group_blocks
-        self._c = _PrefixGroups(*(None if p is None else p.value for p in (
-            _ints(prefix_lens, "prefix_lens", B), _ints(n_groups, "n_groups", 1), _ints(group_start, "group_start", B + 1),
-            _ints(members, "members", B), _ints(group_blocks, "group_blocks", B))))
+        dev = _device()
+        self._c = _PrefixGroups(_ints(prefix_lens, dev, "prefix_lens", B), _ints(n_groups, dev, "n_groups", 1),
+                                _ints(group_start, dev, "group_start", B + 1), _ints(members, dev, "members", B),
+                                _ints(group_blocks, dev, "group_blocks", B))
 
 
 def prefix_plan(B: int, device="cuda") -> PrefixPlan:
@@ -381,16 +397,18 @@ def zp_prefix_plan(desc, block_table, seq_lens, plan: PrefixPlan, min_blocks=1, 
     B, table_stride = _table(block_table)
     if plan.B != B:
         raise ValueError("the plan is for %d batch entries, the table has %d" % (plan.B, B))
-    _check(lib.zp_prefix_plan(ctypes.byref(desc), _ints(block_table, "block_table"), table_stride,
-                              _ints(seq_lens, "seq_lens", B), B, int(min_blocks), int(min_members),
-                              ctypes.byref(plan._c), _stream(stream)))
+    dev = _device()
+    rc = lib.zp_prefix_plan(desc, _ints(block_table, dev, "block_table"), table_stride, _ints(seq_lens, dev, "seq_lens", B),
+                            B, min_blocks, min_members, plan._c, _raw_stream(stream, dev))
+    if rc:
+        _check(rc)
 
 
 def zp_prefix_decode_workspace_size(desc: CacheDesc, B: int, table_stride: int) -> int:
-    n = lib.zp_prefix_decode_workspace_size(ctypes.byref(desc), int(B), int(table_stride))
+    n = lib.zp_prefix_decode_workspace_size(desc, B, table_stride)
     if n == 0 and B > 0:
         raise ZPError(2, lib.zp_last_error().decode() or "unsupported decode shape")
-    return int(n)
+    return n
 
 
 def zp_prefix_decode_attn(desc, q, k_cache, v_cache, block_table, seq_lens, plan: PrefixPlan, out, score_accum=None,
@@ -399,31 +417,34 @@ def zp_prefix_decode_attn(desc, q, k_cache, v_cache, block_table, seq_lens, plan
     B, table_stride = _table(block_table)
     if plan.B != B:
         raise ValueError("the plan is for %d batch entries, the table has %d" % (plan.B, B))
+    dev = _device()
+    shape = (B, desc.h_q, desc.head_dim)
     for t, name in ((q, "q"), (out, "out")):
-        if tuple(t.shape) != (B, desc.h_q, desc.head_dim):
-            raise ValueError("%s must be [B][h_q][d], is %s" % (name, tuple(t.shape)))
-        _cache_dtype(desc, t, name)
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _cache_dtype(desc, t, name)
-        _cache_shape(desc, t, name)
-    rows_p, n_rows = _slot_map(score_accum, score_rows)
-    if score_accum is not None and (score_accum.dtype != torch.float32 or score_accum.dim() != 3 or
-                                    tuple(score_accum.shape[1:]) != (desc.h_kv, table_stride * desc.block_size) or
-                                    (score_rows is None and score_accum.shape[0] < B)):
-        raise ValueError("score_accum must be float32 [R][h_kv][table_stride*b] with a row per batch entry or a slot map")
-    if score_rows is not None and score_rows.numel() != B:
-        raise ValueError("score_rows must have one entry per batch entry")
+        _like_cache(desc, t, name)
+        if t.shape != shape:
+            raise ValueError("%s must be [B][h_q][d] = %s, is %s" % (name, shape, tuple(t.shape)))
+    _cache(desc, k_cache, "k_cache")
+    _cache(desc, v_cache, "v_cache")
+    n_rows = 0
+    if score_accum is not None:
+        n_rows = score_accum.shape[0]
+        if (score_accum.dtype is not torch.float32 or score_accum.dim() != 3 or (score_rows is None and n_rows < B) or
+                score_accum.shape[1:] != (desc.h_kv, table_stride * desc.block_size)):
+            raise ValueError("score_accum must be float32 [R][h_kv][table_stride*b] with a row per batch entry or a slot map")
+    elif score_rows is not None:
+        raise ValueError("score_rows needs score_accum")
     if workspace is None:
         workspace = torch.empty(zp_prefix_decode_workspace_size(desc, B, table_stride), dtype=torch.uint8,
                                 device=q.device)
         if stream is not None:
             workspace.record_stream(stream)  # not reused before this call's work on that stream
-    _check(lib.zp_prefix_decode_attn(ctypes.byref(desc), _here(q, "q"), _here(k_cache, "k_cache"),
-                                     _here(v_cache, "v_cache"), _ints(block_table, "block_table"), table_stride,
-                                     _ints(seq_lens, "seq_lens", B), B, ctypes.byref(plan._c), _here(out, "out"),
-                                     _here(score_accum, "score_accum"), rows_p, n_rows, int(window),
-                                     _here(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-                                     _stream(stream)))
+    rc = lib.zp_prefix_decode_attn(desc, _ptr_on(q, dev, "q"), _ptr_on(k_cache, dev, "k_cache"),
+                                   _ptr_on(v_cache, dev, "v_cache"), _ints(block_table, dev, "block_table"), table_stride,
+                                   _ints(seq_lens, dev, "seq_lens", B), B, plan._c, _ptr_on(out, dev, "out"),
+                                   _ptr_on(score_accum, dev, "score_accum"), _ints(score_rows, dev, "score_rows", B), n_rows,
+                                   window, _ptr_on(workspace, dev, "workspace"), workspace.nbytes, _raw_stream(stream, dev))
+    if rc:
+        _check(rc)
 
 
 # ----------------------------------------------------------------------------- compression

@@ -13,13 +13,14 @@
 // of every sequence that is on a window step give a second pass over the shared
 // keys: S[t] (+)= (1/w) max_{h in group} 2^(x_ht - m_h) / l_h.
 //
-// Work: an item is (group, kv head, tile of query rows), its length the group's
-// tiles of prefix tokens.  The tiles of all items are concatenated and every CTA
-// takes an equal contiguous range (as the decode does with its units), so any
-// mix of group sizes and prefix lengths fills the GPU.  The first piece of an
-// item goes to its rows' place in the main records, a piece that begins inside
-// an item (at most one per CTA) to the CTA's extra records; a merge kernel joins
-// the pieces of each row.
+// Work: an item is (group, tile of query rows), its length the group's tiles of
+// prefix tokens.  The tiles of all items are concatenated and every set of h_kv
+// CTAs takes an equal contiguous range (as the decode does with its units), one
+// kv head per CTA, so any mix of group sizes and prefix lengths fills the GPU
+// and the CTAs of a set read the heads of the same token rows at the same time.
+// The first piece of an item goes to its rows' place in the main records, a
+// piece that begins inside an item (at most one per CTA) to the CTA's extra
+// records; a merge kernel joins the pieces of each row.
 #include <math.h>
 
 #include "prefix_tc.h"
@@ -133,17 +134,17 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_part_kernel(const PfxArgs 
     const int ng = pfx_groups(a);
     const int W = pfx_scan(a, ng, pre);
     if (blockIdx.x == 0) pfx_publish(a, ng, pre);
-    const int w0 = pfx_start(blockIdx.x, W, a.parts), w1 = pfx_start(blockIdx.x + 1, W, a.parts);
+    const int head = blockIdx.x % a.h_kv, set = blockIdx.x / a.h_kv;
+    const int w0 = pfx_start(set, W, a.parts), w1 = pfx_start(set + 1, W, a.parts);
     for (int w = w0; w < w1;) {
         const int gi = pfx_find(pre, ng, w);
         const PfxGroup g = pfx_group(a, gi);
         const int item = (w - pre[gi]) / g.kts, t_b = (w - pre[gi]) % g.kts;
         const int t_e = min(g.kts, t_b + (w1 - w));
-        const PfxItem it = pfx_item(g, item);
-        const int r0 = it.rt * kPfxRows;
+        const int r0 = item * kPfxRows;
         const int32_t *row = pfx_row(a, g);
         __syncthreads();  // the last segment's reads of shared memory
-        pfx_load_q<D, G>(a, g, it.head, r0, sm);
+        pfx_load_q<D, G>(a, g, head, r0, sm);
         float m[4], l[4], acc[4][4 * DV];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -155,7 +156,7 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_part_kernel(const PfxArgs 
         for (int t = t_b; t < t_e; ++t) {
             const int t0 = t * kPfxTokens;
             __syncthreads();
-            pfx_load_kv<D>(a, g, row, it.head, t0, sm, true);
+            pfx_load_kv<D>(a, g, row, head, t0, sm, true);
             __syncthreads();
             float x[4][4];
             pfx_logits<D>(sm, ty, tx, x);
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_part_kernel(const PfxArgs 
             for (int o = 1; o < 16; o <<= 1) l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], o);
             const int r = r0 + ty * 4 + i;
             if (r < g.n * G) {
-                const long long at = t_b == 0 ? pfx_main_row(a, g, it.head, r)
+                const long long at = t_b == 0 ? pfx_main_row(a, g, head, r)
                                               : a.extra0 + (long long)blockIdx.x * a.rt + ty * 4 + i;
                 if (tx == 0) a.rec_ml[at] = make_float2(m[i], l[i]);
 #pragma unroll
@@ -226,6 +227,8 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_part_kernel(const PfxArgs 
 
 // One warp per (member, q head): the pieces of its row joined,
 //     M = max_j m_j,  l = sum_j 2^(m_j - M) l_j,  acc = sum_j 2^(m_j - M) acc_j.
+// Lane j finds piece j and its (m, l) (32 pieces at a time), so that the loads
+// of the statistics, and then of the accumulators, are all in flight together.
 template <int D>
 __global__ void __launch_bounds__(256) prefix_merge_kernel(const PfxArgs a) {
     const int lane = threadIdx.x & 31;
@@ -234,36 +237,57 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const PfxArgs a) {
     if (ng == 0) return;
     const int mi = (int)(wi / a.h_q), h = (int)(wi - (long long)mi * a.h_q);
     const int W = a.wpre[ng];
-    const int lo = pfx_group_of(a, ng, mi);
-    const PfxGroup g = pfx_group(a, lo);
+    const int gi = pfx_group_of(a, ng, mi);
+    const PfxGroup g = pfx_group(a, gi);
     if (mi < g.m0 || mi >= g.m0 + g.n || g.tokens == 0) return;
     const int s = pfx_member(a, mi);
     if (s < 0) return;
     const int G = a.h_q / a.h_kv, head = h / G;
     const int r = (mi - g.m0) * G + h % G;
-    const int i0 = a.wpre[lo] + (head * g.rts + r / a.rt) * g.kts;
-    const int c0 = pfx_owner(i0, W, a.parts), c1 = pfx_owner(i0 + g.kts - 1, W, a.parts);
+    const int i0 = a.wpre[gi] + r / a.rt * g.kts, i1 = i0 + g.kts;
+    const int c0 = pfx_owner(i0, W, a.parts);
+    // pieces: consecutive sets when each has a tile, one tile each otherwise
+    const int n = W >= a.parts ? pfx_owner(i1 - 1, W, a.parts) - c0 + 1 : g.kts;
+    // an item of at most 128 rows has a record per stream
+    const int row = r % a.rt;
+    const int two = a.tc && min(a.rt, g.n * G - (r - row)) <= a.rt / 2 ? 2 : 1;
     constexpr int V = D / 32;
     float M = -INFINITY, L = 0.f, acc[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) acc[e] = 0.f;
-    // an item of at most 128 rows has a record per stream
-    const int row = r % a.rt;
-    const bool two = a.tc && min(a.rt, g.n * G - (r - row)) <= a.rt / 2;
-    for (int c = c0; c <= c1; ++c) {
-        if (pfx_start(c, W, a.parts) == pfx_start(c + 1, W, a.parts)) continue;  // a CTA without tiles
-        for (int x = 0; x < (two ? 2 : 1); ++x) {
-            const long long at = c == c0 ? pfx_main_row(a, g, head, r) + x * (long long)a.B * a.h_q
-                                         : a.extra0 + (long long)c * a.rt + x * (a.rt / 2) + row;
-            const float2 ml = a.rec_ml[at];
-            if (ml.x == -INFINITY) continue;  // no tile, no accumulator
-            const float Mn = fmaxf(M, ml.x);
-            const float f0 = M == -INFINITY ? 0.f : exp2f(M - Mn), f1 = exp2f(ml.x - Mn);
-            L = L * f0 + ml.y * f1;
-            M = Mn;
-            const float *src = a.rec_acc + at * D + lane * V;
+    for (int p0 = 0; p0 < n * two; p0 += 32) {
+        const int p = p0 + lane, j = p / two, x = p - j * two;
+        long long at = 0;
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (j < n) {
+            const int c = W >= a.parts ? c0 + j : pfx_owner(i0 + j, W, a.parts);
+            at = j == 0 ? pfx_main_row(a, g, head, r) + x * (long long)a.B * a.h_q
+                        : a.extra0 + ((long long)c * a.h_kv + head) * a.rt + x * (a.rt / 2) + row;
+            ml = a.rec_ml[at];
+        }
+        float Mn = fmaxf(M, ml.x);
 #pragma unroll
-            for (int e = 0; e < V; ++e) acc[e] = acc[e] * f0 + src[e] * f1;
+        for (int o = 16; o; o >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(0xFFFFFFFFu, Mn, o));
+        if (Mn == -INFINITY) continue;
+        const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - Mn);  // 0: no tile, no accumulator
+        float ls = f * ml.y;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) ls += __shfl_xor_sync(0xFFFFFFFFu, ls, o);
+        const float old = M == -INFINITY ? 0.f : exp2f(M - Mn);
+        L = L * old + ls;
+        M = Mn;
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] *= old;
+        const int n_here = min(32, n * two - p0);
+#pragma unroll 4
+        for (int k = 0; k < n_here; ++k) {
+            const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
+            const long long ak = __shfl_sync(0xFFFFFFFFu, at, k);
+            if (fk != 0.f) {
+                const float *src = a.rec_acc + ak * D + lane * V;
+#pragma unroll
+                for (int e = 0; e < V; ++e) acc[e] = fmaf(src[e], fk, acc[e]);
+            }
         }
     }
     float *dst = a.init_acc + ((size_t)s * a.h_q + h) * D + lane * V;
@@ -283,18 +307,18 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_score_kernel(const PfxArgs
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int ng = pfx_groups(a);
     const int W = pfx_scan(a, ng, pre);
-    const int w0 = pfx_start(blockIdx.x, W, gridDim.x), w1 = pfx_start(blockIdx.x + 1, W, gridDim.x);
+    const int head = blockIdx.x % a.h_kv, set = blockIdx.x / a.h_kv;
+    const int w0 = pfx_start(set, W, a.parts), w1 = pfx_start(set + 1, W, a.parts);
     const float inv_w = 1.f / (float)a.window;
     for (int w = w0; w < w1;) {
         const int gi = pfx_find(pre, ng, w);
         const PfxGroup g = pfx_group(a, gi);
         const int item = (w - pre[gi]) / g.kts, t_b = (w - pre[gi]) % g.kts;
         const int t_e = min(g.kts, t_b + (w1 - w));
-        const PfxItem it = pfx_item(g, item);
-        const int r0 = it.rt * kPfxRows;
+        const int r0 = item * kPfxRows;
         const int32_t *row = pfx_row(a, g);
         __syncthreads();
-        pfx_load_q<D, G>(a, g, it.head, r0, sm);
+        pfx_load_q<D, G>(a, g, head, r0, sm);
         // score row and c = m + log2 l of this thread's rows
         float c[4];
         int srow[4];
@@ -310,7 +334,7 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_score_kernel(const PfxArgs
                 if (s >= 0) {
                     srow[i] = pfx_score_row(a, s, &first[i]);
                     if (srow[i] >= 0) {
-                        const float2 ml = a.stats[(size_t)s * a.h_q + it.head * G + r % G];
+                        const float2 ml = a.stats[(size_t)s * a.h_q + head * G + r % G];
                         c[i] = ml.y > 0.f ? ml.x + log2f(ml.y) : INFINITY;
                     }
                 }
@@ -319,7 +343,7 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_score_kernel(const PfxArgs
         for (int t = t_b; t < t_e; ++t) {
             const int t0 = t * kPfxTokens;
             __syncthreads();
-            pfx_load_kv<D>(a, g, row, it.head, t0, sm, false);
+            pfx_load_kv<D>(a, g, row, head, t0, sm, false);
             __syncthreads();
             float x[4][4];
             pfx_logits<D>(sm, ty, tx, x);
@@ -341,7 +365,7 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_score_kernel(const PfxArgs
 #pragma unroll
                     for (int i = 0; i < 4; i += (G >= 4 ? 4 : G)) {
                         if (srow[i] < 0 || (G == 8 && (ty & 1))) continue;
-                        float *dst = a.score + ((size_t)srow[i] * a.h_kv + it.head) * a.score_stride + tok;
+                        float *dst = a.score + ((size_t)srow[i] * a.h_kv + head) * a.score_stride + tok;
                         const float val = exp2f(e[i]) * inv_w;
                         *dst = first[i] ? val : *dst + val;
                     }
@@ -367,10 +391,11 @@ zp_status pfx_plan(const zp_cache_desc *D, int B, const DeviceInfo &dev, PfxPlan
     p->tc = D->dtype == ZP_BF16;
     p->rt = p->tc ? kPtRows : kPfxRows;
     p->kt = p->tc ? 128 : kPfxTokens;
-    p->parts = dev.sm_count;
+    p->parts = dev.sm_count / D->h_kv;
+    if (p->parts < 1) return fail(ZP_ERR_SHAPE, "prefix_decode: h_kv %d above %d", D->h_kv, dev.sm_count);
     const size_t rows = (size_t)B * D->h_q;
     p->extra0 = (long long)(p->tc ? 2 * rows : rows);
-    const size_t recs = (size_t)p->extra0 + (size_t)p->parts * p->rt;
+    const size_t recs = (size_t)p->extra0 + (size_t)p->parts * D->h_kv * p->rt;
     size_t off = 0;
     p->off_wpre = off;
     off = align_up(off + (size_t)(B + 1) * 4, 256);
@@ -394,7 +419,7 @@ zp_status launch_part(const PfxArgs &a, cudaStream_t st) {
     zp_status rc = set_max_dynamic_smem(reinterpret_cast<const void *>(prefix_part_kernel<D, G>), smem,
                                         "prefix_decode: shared-memory attribute");
     if (rc != ZP_OK) return rc;
-    prefix_part_kernel<D, G><<<a.parts, kPfxThreads, smem, st>>>(a);
+    prefix_part_kernel<D, G><<<a.parts * a.h_kv, kPfxThreads, smem, st>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "prefix_decode: prefix kernel launch");
     return ZP_OK;
@@ -415,7 +440,7 @@ zp_status launch_score(const PfxArgs &a, cudaStream_t st) {
     zp_status rc = set_max_dynamic_smem(reinterpret_cast<const void *>(prefix_score_kernel<D, G>), smem,
                                         "prefix_decode: shared-memory attribute");
     if (rc != ZP_OK) return rc;
-    prefix_score_kernel<D, G><<<a.parts, kPfxThreads, smem, st>>>(a);
+    prefix_score_kernel<D, G><<<a.parts * a.h_kv, kPfxThreads, smem, st>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "prefix_decode: score kernel launch");
     return ZP_OK;
@@ -472,8 +497,8 @@ extern "C" zp_status zp_prefix_decode_attn(const zp_cache_desc *D, const void *q
                          (uintptr_t)score_accum | (uintptr_t)workspace;
     if (al % 16) return fail(ZP_ERR_INVALID_ARG, "prefix_decode: buffers must be 16-byte aligned");
     const int G = D->h_q / D->h_kv;
-    // tile counts are 32-bit: kv heads * query rows * tokens of a row bounds them
-    if ((double)D->h_kv * ((double)B * G) * ((double)table_stride * D->block_size / kPfxTokens + 1) > 2147483647.0 ||
+    // tile counts are 32-bit: query rows * tiles of a table row bounds them
+    if (((double)B * G) * ((double)table_stride * D->block_size / kPfxTokens + 1) > 2147483647.0 ||
         (long long)table_stride * D->block_size > INT32_MAX)
         return fail(ZP_ERR_SHAPE, "prefix_decode: B=%d rows of %d blocks", B, table_stride);
     DeviceInfo dev;

@@ -18,13 +18,14 @@ struct PfxArgs {
     // the plan
     const int32_t *n_groups, *group_start, *members, *group_blocks;
     int rt, kt;          // rows per item, tokens per tile
-    int parts;           // CTAs of the prefix kernel (split of the tiles)
+    int parts;           // sets of CTAs (split of the tiles); a set has a CTA per kv head
     float qscale;        // log2(e) / sqrt(d)
     int *wpre;           // [B+1] tiles before each group
     int32_t *prefix;     // [B] prefix tokens of every batch entry, 0 = none
     float *rec_acc;      // [extra0 + parts*rt][d] pieces: main records, then extra records
     float2 *rec_ml;      // same rows
-    long long extra0;    // first extra record: B*h_q, twice that on the tensor cores (second streams)
+    long long extra0;    // first extra record: B*h_q, twice that on the tensor cores (second streams);
+                         // then rt rows per CTA (set * h_kv + head)
     int tc;              // tensor-core kernels: 256 rows x 128 tokens, two streams
     float *init_acc;     // [B][h_q][d]
     float2 *init_ml;     // [B][h_q]
@@ -91,12 +92,9 @@ __device__ __forceinline__ int pfx_find(const int *pre, int n, int x) {
     return lo;
 }
 
-// CTA whose range holds tile w
+// Set whose range holds tile w: the largest c with floor(c W / parts) <= w.
 __device__ __forceinline__ int pfx_owner(int w, int W, int parts) {
-    int c = (int)((long long)w * parts / W);
-    while (c + 1 < parts && pfx_start(c + 1, W, parts) <= w) ++c;
-    while (c > 0 && pfx_start(c, W, parts) > w) --c;
-    return c;
+    return (int)(((long long)(w + 1) * parts - 1) / W);
 }
 
 // Tiles before each group (whole CTA; pre: n_groups + 1 ints of shared memory);
@@ -104,7 +102,7 @@ __device__ __forceinline__ int pfx_owner(int w, int W, int parts) {
 inline __device__ int pfx_scan(const PfxArgs &a, int ng, int *pre) {
     for (int i = threadIdx.x; i < ng; i += blockDim.x) {
         const PfxGroup g = pfx_group(a, i);
-        pre[i] = a.h_kv * g.rts * g.kts;
+        pre[i] = g.rts * g.kts;
     }
     __syncthreads();
     if (threadIdx.x < 32) {
@@ -125,15 +123,6 @@ inline __device__ int pfx_scan(const PfxArgs &a, int ng, int *pre) {
     }
     __syncthreads();
     return pre[ng];
-}
-
-// Item of a group: row tile fastest, so that CTAs that run together read the
-// same keys.
-struct PfxItem {
-    int head, rt;
-};
-__device__ __forceinline__ PfxItem pfx_item(const PfxGroup &g, int item) {
-    return {item / g.rts, item - item / g.rts * g.rts};
 }
 
 // Row of the main records: rows of a group are (kv head, member, q head of the

@@ -48,6 +48,7 @@ struct PlanSmem {
     int aux[kPlanMaxB];                  // members with at least this lcp, then the rank inside the group
     int gid[kPlanMaxB];                  // by leader: lowest member, then group number
     int size[kPlanMaxB];                 // by leader: members
+    int full[kPlanMaxB];                 // blocks before the newest token's
     unsigned char member[kPlanMaxB];
     int warp_sums[32];
     int total;
@@ -105,6 +106,7 @@ __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanThre
     // leaders: every CTA hashes every sequence's first block
     for (int s = tid; s < B; s += kPlanThreads) {
         const int u = plan_full(a, s);
+        sm.full[s] = u;
         const int first = u >= 1 ? a.table[(size_t)s * a.stride] : -1;
         int h = -1;
         if (first >= 0 && first < a.n_total) {
@@ -125,41 +127,72 @@ __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanThre
         sm.lcp[s] = 0;
     }
     cluster.sync();  // every CTA's arrays are ready for the others' writes
-    // lcp of this CTA's sequences, given to every CTA
-    for (int s = e0 + warp; s < e1; s += kPlanThreads / 32) {
-        const int ld = sm.leader[s];
-        int n = 0;
-        if (ld >= 0) {
-            const int lim = min(plan_full(a, s), plan_full(a, ld));
-            const int32_t *r0 = a.table + (size_t)s * a.stride, *r1 = a.table + (size_t)ld * a.stride;
-            n = lim;
-            for (int c0 = 0; c0 < lim; c0 += 128) {  // four entries of each row in flight per lane
-                bool same = true;
+    // lcp of this CTA's sequences, given to every CTA: a warp compares kEach rows
+    // with their leaders' at a time, 64 entries each, all loads in flight
+    constexpr int kWarps = kPlanThreads / 32, kEach = 4;
+    for (int s0 = e0 + warp * kEach; s0 < e1; s0 += kWarps * kEach) {
+        int lim[kEach], n[kEach], far = 0;
+        const int32_t *r0[kEach], *r1[kEach];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+        for (int i = 0; i < kEach; ++i) {
+            const int s = s0 + i, ld = s < e1 ? sm.leader[s] : -1;
+            lim[i] = ld >= 0 ? min(sm.full[s], sm.full[ld]) : 0;
+            n[i] = lim[i];
+            far = max(far, lim[i]);
+            r0[i] = a.table + (size_t)(ld >= 0 ? s : 0) * a.stride;
+            r1[i] = a.table + (size_t)(ld >= 0 ? ld : 0) * a.stride;
+        }
+        for (int c0 = 0; c0 < far; c0 += 64) {
+            int x[kEach][2], y[kEach][2];
+#pragma unroll
+            for (int i = 0; i < kEach; ++i)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
                     const int c = c0 + 32 * q + lane;
-                    const int x = c < lim ? r0[c] : 0, y = c < lim ? r1[c] : 0;
-                    const bool ok = x == y && x >= 0 && x < a.n_total;
-                    const unsigned bad = __ballot_sync(0xFFFFFFFFu, !ok);
-                    if (bad && same) {
-                        n = min(lim, c0 + 32 * q + __ffs(bad) - 1);
-                        same = false;
-                    }
+                    const bool in = c < n[i];  // (a row that has differed reads no further)
+                    x[i][q] = in ? r0[i][c] : 0;
+                    y[i][q] = in ? r1[i][c] : 0;
                 }
-                if (!same) break;
+            far = 0;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const unsigned bad =
+                        __ballot_sync(0xFFFFFFFFu, !(x[i][q] == y[i][q] && x[i][q] >= 0 && x[i][q] < a.n_total));
+                    if (bad) n[i] = min(n[i], c0 + 32 * q + __ffs(bad) - 1);
+                }
+                far = max(far, n[i]);
             }
         }
-        if (lane < kPlanCluster) *cluster.map_shared_rank(&sm.lcp[s], lane) = n;
+        if (lane < kPlanCluster) {
+#pragma unroll
+            for (int i = 0; i < kEach; ++i)
+                if (s0 + i < e1) *cluster.map_shared_rank(&sm.lcp[s0 + i], lane) = n[i];
+        }
     }
     cluster.sync();
     // members of the class with at least this lcp, given to the first CTA
-    for (int s = e0 + warp; s < e1; s += kPlanThreads / 32) {
-        const int ld = sm.leader[s], n = sm.lcp[s];
-        int cnt = 0;
-        if (ld >= 0)
-            for (int j = lane; j < B; j += 32) cnt += (sm.leader[j] == ld && sm.lcp[j] >= n) ? 1 : 0;
-        cnt = __reduce_add_sync(0xFFFFFFFFu, cnt);
-        if (lane == 0) *cluster.map_shared_rank(&sm.aux[s], 0) = cnt;
+    constexpr int kMany = 8;  // sequences a warp counts for together
+    for (int s0 = e0 + warp * kMany; s0 < e1; s0 += kWarps * kMany) {
+        int ld[kMany], n[kMany], cnt[kMany];
+#pragma unroll
+        for (int i = 0; i < kMany; ++i) {
+            ld[i] = s0 + i < e1 ? sm.leader[s0 + i] : -1;
+            n[i] = s0 + i < e1 ? sm.lcp[s0 + i] : 0;
+            if (ld[i] < 0) ld[i] = -2;  // equal to no leader
+            cnt[i] = 0;
+        }
+        for (int j = lane; j < B; j += 32) {
+            const int lj = sm.leader[j], nj = sm.lcp[j];
+#pragma unroll
+            for (int i = 0; i < kMany; ++i) cnt[i] += lj == ld[i] && nj >= n[i] ? 1 : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < kMany; ++i) {
+            const int c = __reduce_add_sync(0xFFFFFFFFu, cnt[i]);
+            if (lane == 0 && s0 + i < e1) *cluster.map_shared_rank(&sm.aux[s0 + i], 0) = c;
+        }
     }
     cluster.sync();
     if (rank == 0) {
@@ -226,13 +259,24 @@ __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanThre
         for (int s = tid; s < e1; s += kPlanThreads) sm.member[s] = first->member[s];
         __syncthreads();
     }
-    for (int s = e0 + warp; s < e1; s += kPlanThreads / 32) {
-        if (!sm.member[s]) continue;
-        const int ld = sm.leader[s];
-        int r = 0;
-        for (int j = lane; j < s; j += 32) r += (sm.member[j] && sm.leader[j] == ld) ? 1 : 0;
-        r = __reduce_add_sync(0xFFFFFFFFu, r);
-        if (lane == 0) a.members[first->aux[ld] + r] = s;
+    for (int s0 = e0 + warp * kMany; s0 < e1; s0 += kWarps * kMany) {
+        int ld[kMany], r[kMany];
+#pragma unroll
+        for (int i = 0; i < kMany; ++i) {
+            ld[i] = s0 + i < e1 && sm.member[s0 + i] ? sm.leader[s0 + i] : -2;
+            r[i] = 0;
+        }
+        const int end = min(e1, s0 + kMany);
+        for (int j = lane; j < end; j += 32) {
+            const int lj = sm.member[j] ? sm.leader[j] : -1;
+#pragma unroll
+            for (int i = 0; i < kMany; ++i) r[i] += lj == ld[i] && j < s0 + i ? 1 : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < kMany; ++i) {
+            const int c = __reduce_add_sync(0xFFFFFFFFu, r[i]);
+            if (lane == 0 && ld[i] >= 0) a.members[first->aux[ld[i]] + c] = s0 + i;
+        }
     }
     cluster.sync();  // the first CTA's shared memory outlives the others' reads
 }

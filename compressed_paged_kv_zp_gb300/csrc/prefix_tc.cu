@@ -16,8 +16,11 @@
 // exceeds it by more than 2^8 (the result does not depend on m, and P stays
 // below 2^8); S_w of the next tile is complete only after O_w's last product,
 // so the rescaling needs no wait of its own.
-// K and V tiles of 128 tokens arrive by TMA as boxes of 16 token rows (a part of
-// one block) x 64 elements with the 128-byte swizzle, through a ring of stages.
+// K and V tiles of 128 tokens arrive by TMA with the 128-byte swizzle through a
+// ring of stages, one copy per 16 token rows (a part of one block): the box is
+// {64 elements, 8 tokens, d/64 halves, one head, 2 groups of 8 tokens}, so that
+// in shared memory the halves of 8 tokens are 1024 bytes apart and the groups
+// d/64 * 1024, a uniform stride for either operand.
 #include <math.h>
 
 #include "prefix_common.cuh"
@@ -42,14 +45,15 @@ __device__ __forceinline__ void tc_mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem,
         : "memory");
 }
 
-// Shared-memory descriptor of a B operand that is contiguous along N (V: 64 dims
-// per 128-byte row, rows are tokens): groups of 8 tokens 1024 bytes apart
-// (stride offset), the next 64 dims `half` bytes further (leading offset).
-__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t half) {
+// Shared-memory descriptor of a K or V tile as the copies leave it: groups of 8
+// tokens `group` bytes apart (stride offset).  K is contiguous along the product's
+// K dimension; V along its N dimension, whose next 64 dims are 1024 bytes further
+// (leading offset; not used by K).
+__device__ __forceinline__ uint64_t sdesc_kv_sw128(uint32_t saddr, uint32_t group) {
     uint64_t d = 0;
     d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)(half >> 4) << 16;
-    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)(1024u >> 4) << 16;
+    d |= (uint64_t)(group >> 4) << 32;
     d |= (uint64_t)1 << 46;
     d |= (uint64_t)2 << 61;
     return d;
@@ -75,6 +79,7 @@ struct PtCfg {
     static constexpr int KS = D / 16;
     static constexpr int HALF = kPtTile * 128;        // bytes of 128 rows x 64 elements
     static constexpr int TILE = KH * HALF;            // a Q, K or V tile
+    static constexpr int GROUP = KH * 1024;           // 8 tokens of a K or V tile
     static constexpr int STAGES = D == 128 ? 4 : 8;   // K and V tiles in flight
     static constexpr int Q_OFF = 0;                   // two query tiles
     static constexpr int ST_OFF = 2 * TILE;
@@ -90,7 +95,7 @@ struct PtCfg {
 // One CTA's share of an item.
 struct PtSeg {
     PfxGroup g;
-    int head, rt;
+    int rt;
     int t_b, t_e;  // token tiles
     int rows;      // query rows of the item (<= 256)
     bool split;    // at most 128 rows: the streams take alternate tiles
@@ -101,9 +106,7 @@ __device__ __forceinline__ PtSeg pt_segment(const PfxArgs &a, const int *pre, in
     const int gi = pfx_find(pre, ng, w);
     s.g = pfx_group(a, gi);
     const int x = w - pre[gi], item = x / s.g.kts;
-    const PfxItem it = pfx_item(s.g, item);
-    s.head = it.head;
-    s.rt = it.rt;
+    s.rt = item;
     s.t_b = x - item * s.g.kts;
     s.t_e = min(s.g.kts, s.t_b + (w1 - w));
     s.rows = min(kPtRows, s.g.n * (a.h_q / a.h_kv) - s.rt * kPtRows);
@@ -117,31 +120,42 @@ __device__ __forceinline__ int pt_tiles(const PtSeg &s, int w) {
     return s.split ? (n - w + 1) / 2 : n;
 }
 
-// First row (block * b + slot) of the 16 tokens from `tok`; a row outside the
-// tensor (zeros are read) beyond the prefix and for a bad block.
+// First group of 8 rows ((block * b + slot) / 8) of the 16 tokens from `tok`; one
+// outside the tensor (zeros are read) beyond the prefix and for a bad block.
 __device__ __forceinline__ int pt_rows16(const PfxArgs &a, const PfxGroup &g, const int32_t *row, int tok) {
-    if (tok >= g.tokens) return -16;
+    if (tok >= g.tokens) return -2;
     const long long s = pfx_slot(a, row, tok);
-    return s < 0 ? -16 : (int)s;
+    return s < 0 ? -2 : (int)(s / 8);
 }
 
-// This thread's query row into a swizzled tile (zeros beyond the last row).
+// Address of row r of the item's queries, nullptr beyond the last row.
 template <int D>
-__device__ __forceinline__ void pt_load_q(const PfxArgs &a, const PtSeg &s, int r, int row_in_tile, unsigned char *tile) {
-    const int G = a.h_q / a.h_kv;
-    const uint4 *src = nullptr;
-    const int rr = s.rt * kPtRows + r;
-    if (r < s.rows) {
-        const int e = pfx_member(a, s.g.m0 + rr / G);
-        if (e >= 0)
-            src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
-                                                  ((size_t)e * a.h_q + s.head * G + rr % G) * D);
+__device__ __forceinline__ const uint4 *pt_query(const PfxArgs &a, const PtSeg &s, int head, int r, int *entry) {
+    const int G = a.h_q / a.h_kv, rr = s.rt * kPtRows + r;
+    *entry = r < s.rows ? pfx_member(a, s.g.m0 + rr / G) : -1;
+    if (*entry < 0) return nullptr;
+    return reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
+                                           ((size_t)*entry * a.h_q + head * G + rr % G) * D);
+}
+
+// The warp's 32 query rows (lane i holds the address of row row0 + i of the
+// tile) into a swizzled tile of 64-element halves `half` bytes apart, a whole
+// row per D/8 lanes; zeros for rows without an address.
+template <int D>
+__device__ __forceinline__ void pt_load_q(const uint4 *src, int row0, unsigned char *tile, int half) {
+    constexpr int PER = D / 8;  // 16-byte chunks of a row
+    const int lane = threadIdx.x & 31;
+    uint4 v[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(
+            __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(src), i * (32 / PER) + lane / PER));
+        v[i] = p ? __ldg(p + lane % PER) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int c = 0; c < D / 8; ++c) {
-        const uint4 v = src ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4 *>(tile + (c >> 3) * PtCfg<D>::HALF + row_in_tile * 128 +
-                                   (((c & 7) ^ (row_in_tile & 7)) << 4)) = v;
+    for (int i = 0; i < PER; ++i) {
+        const int r = row0 + i * (32 / PER) + lane / PER, c = lane % PER;
+        *reinterpret_cast<uint4 *>(tile + (c >> 3) * half + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v[i];
     }
 }
 
@@ -157,8 +171,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     uint64_t *empty = full + C::STAGES;
     uint64_t *q_full = empty + C::STAGES;  // [2] query tile written
     uint64_t *s_full = q_full + 2;         // [2] logits complete
-    uint64_t *p_full = s_full + 2;         // [2] probabilities written
-    uint64_t *o_full = p_full + 2;         // [2] last product of the segment complete
+    uint64_t *p_full = s_full + 2;         // [2][2] probabilities of the tile's first and last 64 tokens written
+    uint64_t *o_full = p_full + 4;         // [2] last product of the segment complete
     uint64_t *drain = o_full + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -173,7 +187,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 4);
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);
+            mbar_init(&p_full[2 * i], 4);
+            mbar_init(&p_full[2 * i + 1], 4);
             mbar_init(&o_full[i], 1);
         }
         mbar_init(drain, 1);
@@ -190,12 +205,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     if (blockIdx.x == 0) pfx_publish(a, ng, pre);
-    const int w0 = pfx_start(blockIdx.x, W, a.parts), w1 = pfx_start(blockIdx.x + 1, W, a.parts);
+    const int head = blockIdx.x % a.h_kv, set = blockIdx.x / a.h_kv;
+    const int w0 = pfx_start(set, W, a.parts), w1 = pfx_start(set + 1, W, a.parts);
 
     if (warp == 0) {
         // ---------------- producer: K and V tiles in order
         uint32_t fill = 0;
-        const int q = lane >> 1, half = lane & 1;  // lanes 0..15: 16-token group, 64-element half
+        const int q = lane;  // lanes 0..7: 16 tokens each
         bool ok_all = true;
         if (lane == 0) {
             prefetch_tensormap(&kmap);
@@ -204,10 +220,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         for (int w = w0; w < w1 && ok_all;) {
             const PtSeg s = pt_segment(a, pre, ng, w, w1);
             const int32_t *row = pfx_row(a, s.g);
-            int z_next = lane < 16 ? pt_rows16(a, s.g, row, s.t_b * kPtTile + 16 * q) : 0;
+            int z_next = lane < 8 ? pt_rows16(a, s.g, row, s.t_b * kPtTile + 16 * q) : 0;
             for (int t = s.t_b; t < s.t_e && ok_all; ++t) {
                 const int z = z_next;
-                if (t + 1 < s.t_e) z_next = lane < 16 ? pt_rows16(a, s.g, row, (t + 1) * kPtTile + 16 * q) : 0;
+                if (t + 1 < s.t_e) z_next = lane < 8 ? pt_rows16(a, s.g, row, (t + 1) * kPtTile + 16 * q) : 0;
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
                     const uint32_t st = fill % C::STAGES;
@@ -223,8 +239,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     }
                     ++fill;
                     unsigned char *dst = smem + C::ST_OFF + st * C::TILE;
-                    if (lane < 16 && half < C::KH)
-                        tma_load_3d(dst + half * C::HALF + q * 2048, kv ? &vmap : &kmap, half * 64, s.head, z, &full[st]);
+                    if (lane < 8) tma_load_5d(dst + q * 2 * C::GROUP, kv ? &vmap : &kmap, 0, 0, 0, head, z, &full[st]);
                     __syncwarp();
                 }
             }
@@ -237,7 +252,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         }
     } else if (warp == 1) {
         // ---------------- MMA issuer (one thread)
-        if (lane == 0) {
+        if (elect_one()) {
             uint32_t base = 0, n_p[2] = {0, 0}, n_q[2] = {0, 0};
             const uint32_t q_addr = smem_u32(smem + C::Q_OFF), st_addr = smem_u32(smem + C::ST_OFF);
             bool ok_all = true;
@@ -252,24 +267,32 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     tc_fence_after();
 #pragma unroll
                     for (int ks = 0; ks < C::KS; ++ks) {
-                        const uint32_t o = (ks >> 2) * C::HALF + (ks & 3) * 32;
-                        tc_mma_bf16(tmem + C::S_COL + x * 128, sdesc_k_sw128(q_addr + x * C::TILE + o),
-                                    sdesc_k_sw128(st_addr + st * C::TILE + o), C::IDESC_QK, ks > 0 ? 1u : 0u);
+                        tc_mma_bf16(tmem + C::S_COL + x * 128,
+                                    sdesc_k_sw128(q_addr + x * C::TILE + (ks >> 2) * C::HALF + (ks & 3) * 32),
+                                    sdesc_kv_sw128(st_addr + st * C::TILE + (ks >> 2) * 1024 + (ks & 3) * 32, C::GROUP),
+                                    C::IDESC_QK, ks > 0 ? 1u : 0u);
                     }
                     if (s.split || x == 1) tc_commit(&empty[st]);
                     tc_commit(&s_full[x]);
                     return true;
                 };
+                // the product of stream x's tile j with V, 64 tokens at a time as their
+                // probabilities are written
                 auto pv = [&](int x, int j) -> bool {
                     const uint32_t f = base + 2 * (s.split ? 2 * j + x : j) + 1;
                     const uint32_t st = f % C::STAGES;
                     if (!mbar_wait_bounded(&full[st], (f / C::STAGES) & 1, a.err, abort_flag, 0x604)) return false;
-                    tc_fence_after();
 #pragma unroll
-                    for (int ks = 0; ks < kPtTile / 16; ++ks)
-                        tc_mma_bf16_ta(tmem + C::O_COL + x * D, tmem + C::S_COL + x * 128 + ks * 8,
-                                       sdesc_mn_sw128(st_addr + st * C::TILE + ks * 2048, C::HALF), C::IDESC_PV,
-                                       j > 0 || ks > 0 ? 1u : 0u);
+                    for (int hf = 0; hf < 2; ++hf) {
+                        if (!mbar_wait_bounded(&p_full[2 * x + hf], n_p[x] & 1, a.err, abort_flag, 0x606)) return false;
+                        tc_fence_after();
+#pragma unroll
+                        for (int ks = hf * 4; ks < hf * 4 + 4; ++ks)
+                            tc_mma_bf16_ta(tmem + C::O_COL + x * D, tmem + C::S_COL + x * 128 + ks * 8,
+                                           sdesc_kv_sw128(st_addr + st * C::TILE + ks * 2 * C::GROUP, C::GROUP), C::IDESC_PV,
+                                           j > 0 || ks > 0 ? 1u : 0u);
+                    }
+                    ++n_p[x];
                     if (s.split || x == 1) tc_commit(&empty[st]);
                     return true;
                 };
@@ -282,10 +305,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 for (int j = 0; j < n_t[0] && ok_all; ++j)  // n_t[0] >= n_t[1]
                     for (int x = 0; x < 2 && ok_all; ++x) {
                         if (j >= n_t[x]) continue;
-                        ok_all = mbar_wait_bounded(&p_full[x], n_p[x] & 1, a.err, abort_flag, 0x606);
-                        ++n_p[x];
-                        if (!ok_all) break;
-                        tc_fence_after();
                         ok_all = pv(x, j);
                         if (!ok_all) break;
                         if (j + 1 < n_t[x]) ok_all = qk(x, j + 1);
@@ -294,7 +313,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 base += 2 * (s.t_e - s.t_b);
                 w += s.t_e - s.t_b;
             }
+            // every product has been carried out before the CTA ends, also after a timeout
+            volatile int never = 0;
+            tc_commit(drain);
+            mbar_wait_bounded(drain, 0, a.err, &never, 0x609);
         }
+        __syncwarp();
     } else {
         // ---------------- softmax: warpgroup x = stream, thread = query row (TMEM lane)
         const int x = (warp - 2) >> 2;
@@ -310,7 +334,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             const int r = s.split ? tr : x * 128 + tr;  // row of the item
             float m = -INFINITY, l = 0.f;
             if (n_t > 0) {
-                pt_load_q<D>(a, s, r, tr, smem + C::Q_OFF + x * C::TILE);
+                int entry;
+                pt_load_q<D>(pt_query<D>(a, s, head, r, &entry), quarter * 32, smem + C::Q_OFF + x * C::TILE, C::HALF);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&q_full[x]);
@@ -334,13 +359,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                         if (c + 64 >= valid) v1[c] = 0xFF800000u;
                     }
                 }
-                float mx0 = -INFINITY, mx1 = -INFINITY;
+                float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 64; ++c) {
-                    mx0 = fmaxf(mx0, __uint_as_float(v0[c]));
-                    mx1 = fmaxf(mx1, __uint_as_float(v1[c]));
+                for (int c = 0; c < 64; c += 2) {
+                    mx4[c & 2] = fmaxf(mx4[c & 2], fmaxf(__uint_as_float(v0[c]), __uint_as_float(v0[c + 1])));
+                    mx4[(c & 2) + 1] = fmaxf(mx4[(c & 2) + 1], fmaxf(__uint_as_float(v1[c]), __uint_as_float(v1[c + 1])));
                 }
-                const float mx = fmaxf(mx0, mx1) * a.qscale;
+                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.qscale;
                 // raise the maximum (and rescale what is summed) only beyond 2^8
                 const bool raise = mx > m + kPtRaise;  // true at the first tile (m = -inf)
                 if (__any_sync(0xFFFFFFFFu, raise)) {
@@ -373,33 +398,48 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                         p[c] = f2_to_bf2(y.x, y.y);
                     }
                     tmem_st32(s_t + col, p);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[2 * x + col / 32]);
                 };
                 half_tile(v0, 0);
                 half_tile(v1, 32);
                 l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[x]);
             }
             if (!ok_all) break;
-            // the piece's record
+            // the piece's record: 64 dims of the warp's 32 rows at a time through the
+            // stream's query tile (its products are complete), so that stores are
+            // whole 128-byte lines; chunk c of row i sits at c ^ (i & 7)
             long long at = -1;
             if (r < s.rows)
-                at = s.t_b == 0 ? pfx_main_row(a, s.g, s.head, s.rt * kPtRows + r) + (s.split && x ? (long long)a.B * a.h_q : 0)
+                at = s.t_b == 0 ? pfx_main_row(a, s.g, head, s.rt * kPtRows + r) + (s.split && x ? (long long)a.B * a.h_q : 0)
                                 : a.extra0 + (long long)blockIdx.x * kPtRows + x * 128 + tr;
             if (n_t > 0) {
                 if (!mbar_wait_bounded(&o_full[x], n_o & 1, a.err, abort_flag, 0x608)) break;
                 ++n_o;
                 tc_fence_after();
+                uint4 *buf = reinterpret_cast<uint4 *>(smem + C::Q_OFF + x * C::TILE + quarter * (C::TILE / 4));
+                constexpr int COLS = D == 128 ? 64 : 32;  // what fits: 32 rows in a quarter of the tile
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(o_t + c0, o);
-                    if (at >= 0) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(a.rec_acc + at * D + c0);
+                for (int c0 = 0; c0 < D; c0 += COLS) {
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) dst[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                    for (int c1 = 0; c1 < COLS; c1 += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(o_t + c0 + c1, o);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            buf[lane * (COLS / 4) + ((c1 / 4 + c) ^ (lane & 7))] =
+                                make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
                     }
+                    __syncwarp();
+                    constexpr int PER = COLS / 4;  // chunks per row
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) {
+                        const int row = i * (32 / PER) + lane / PER, c = lane % PER;
+                        const long long ra = __shfl_sync(0xFFFFFFFFu, at, row);
+                        if (ra >= 0) *reinterpret_cast<uint4 *>(a.rec_acc + ra * D + c0 + 4 * c) = buf[row * PER + (c ^ (row & 7))];
+                    }
+                    __syncwarp();
                 }
                 tc_fence_before();
             }
@@ -409,11 +449,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     }
 
     __syncthreads();
-    if (*abort_flag && threadIdx.x == 32) {
-        volatile int never = 0;
-        tc_commit(drain);
-        mbar_wait_bounded(drain, 0, a.err, &never, 0x609);
-    }
     tc_fence_before();
     __syncthreads();
     if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
@@ -430,8 +465,8 @@ template <int D>
 struct PsCfg {
     static constexpr int KH = D / 64;
     static constexpr int KS = D / 16;
-    static constexpr int A_HALF = kPtTile * 128;
-    static constexpr int TILE = KH * A_HALF;           // K tile
+    static constexpr int GROUP = KH * 1024;            // 8 tokens of a K tile
+    static constexpr int TILE = kPtTile / 8 * GROUP;   // K tile
     static constexpr int B_HALF = kPtRows * 128;       // 256 query rows x 64 elements
     static constexpr int B_BYTES = KH * B_HALF;
     static constexpr int STAGES = 4;
@@ -488,18 +523,19 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     const int W = pfx_scan(a, ng, pre);
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int w0 = pfx_start(blockIdx.x, W, gridDim.x), w1 = pfx_start(blockIdx.x + 1, W, gridDim.x);
+    const int head = blockIdx.x % a.h_kv, set = blockIdx.x / a.h_kv;
+    const int w0 = pfx_start(set, W, a.parts), w1 = pfx_start(set + 1, W, a.parts);
 
     if (warp == 0) {
         uint32_t fill = 0;
-        const int q = lane >> 1, half = lane & 1;
+        const int q = lane;
         bool ok_all = true;
         if (lane == 0) prefetch_tensormap(&kmap);
         for (int w = w0; w < w1 && ok_all;) {
             const PtSeg s = pt_segment(a, pre, ng, w, w1);
             const int32_t *row = pfx_row(a, s.g);
             for (int t = s.t_b; t < s.t_e; ++t, ++fill) {
-                const int z = lane < 16 ? pt_rows16(a, s.g, row, t * kPtTile + 16 * q) : 0;
+                const int z = lane < 8 ? pt_rows16(a, s.g, row, t * kPtTile + 16 * q) : 0;
                 const uint32_t st = fill % C::STAGES;
                 bool got = true;
                 if (lane == 0) {
@@ -511,9 +547,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     ok_all = false;
                     break;
                 }
-                if (lane < 16 && half < C::KH)
-                    tma_load_3d(smem + C::ST_OFF + st * C::TILE + half * C::A_HALF + q * 2048, &kmap, half * 64, s.head, z,
-                                &full[st]);
+                if (lane < 8)
+                    tma_load_5d(smem + C::ST_OFF + st * C::TILE + q * 2 * C::GROUP, &kmap, 0, 0, 0, head, z, &full[st]);
                 __syncwarp();
             }
             w += s.t_e - s.t_b;
@@ -524,7 +559,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 mbar_wait_bounded(&full[f % C::STAGES], (f / C::STAGES) & 1, a.err, &never, 0x612);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             uint32_t fill = 0, n_q = 0;
             const uint32_t b_addr = smem_u32(smem), st_addr = smem_u32(smem + C::ST_OFF);
             bool ok_all = true;
@@ -542,14 +577,18 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 #pragma unroll
                     for (int ks = 0; ks < C::KS; ++ks)
                         tc_mma_bf16(tmem + ab * 256,
-                                    sdesc_k_sw128(st_addr + st * C::TILE + (ks >> 2) * C::A_HALF + (ks & 3) * 32),
+                                    sdesc_kv_sw128(st_addr + st * C::TILE + (ks >> 2) * 1024 + (ks & 3) * 32, C::GROUP),
                                     sdesc_k_sw128(b_addr + (ks >> 2) * C::B_HALF + (ks & 3) * 32), idesc, ks > 0 ? 1u : 0u);
                     tc_commit(&empty[st]);
                     tc_commit(&acc_full[ab]);
                 }
                 w += s.t_e - s.t_b;
             }
+            volatile int never = 0;
+            tc_commit(drain);
+            mbar_wait_bounded(drain, 0, a.err, &never, 0x617);
         }
+        __syncwarp();
     } else {
         const int et = threadIdx.x - 64;          // 0..255: query row while loading
         const int quarter = warp & 3, half = (warp - 2) >> 2;
@@ -563,31 +602,22 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             // item (whose products are then complete)
             if (!mbar_wait_bounded(q_done, (item & 1) ^ 1, a.err, abort_flag, 0x618)) break;
             {
-                const int r = et, rr = s.rt * kPtRows + r;
-                const uint4 *src = nullptr;
+                const int r = et;
+                int e, mrow = -1;
+                const uint4 *src = pt_query<D>(a, s, head, r, &e);
                 float c = INFINITY;
-                int mrow = -1;
-                if (r < s.rows) {
-                    const int e = pfx_member(a, s.g.m0 + rr / G);
-                    if (e >= 0) {
-                        src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
-                                                              ((size_t)e * a.h_q + s.head * G + rr % G) * D);
-                        bool first;
-                        mrow = pfx_score_row(a, e, &first);
-                        if (mrow >= 0) {
-                            const float2 ml = a.stats[(size_t)e * a.h_q + s.head * G + rr % G];
-                            c = ml.y > 0.f ? ml.x + log2f(ml.y) : INFINITY;
-                            mrow = mrow * 2 + (first ? 1 : 0);
-                        }
+                if (e >= 0) {
+                    bool first;
+                    mrow = pfx_score_row(a, e, &first);
+                    if (mrow >= 0) {
+                        const float2 ml = a.stats[(size_t)e * a.h_q + head * G + (s.rt * kPtRows + r) % G];
+                        c = ml.y > 0.f ? ml.x + log2f(ml.y) : INFINITY;
+                        mrow = mrow * 2 + (first ? 1 : 0);
                     }
                 }
                 cs[r] = c;
                 if (r % G == 0) ms[r / G] = mrow;
-#pragma unroll
-                for (int ch = 0; ch < D / 8; ++ch) {
-                    const uint4 v = src ? __ldg(src + ch) : make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4 *>(smem + (ch >> 3) * C::B_HALF + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
-                }
+                pt_load_q<D>(src, r & ~31, smem, C::B_HALF);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -617,7 +647,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                         for (int j = 0; j < G; ++j)
                             e = fmaxf(e, fmaf(__uint_as_float(v[i * G + j]), a.qscale, -cs[half * 128 + c0 + i * G + j]));
                         if (mr >= 0 && live) {
-                            float *dst = a.score + ((size_t)(mr >> 1) * a.h_kv + s.head) * a.score_stride + tok;
+                            float *dst = a.score + ((size_t)(mr >> 1) * a.h_kv + head) * a.score_stride + tok;
                             const float val = ex2_approx(e) * inv_w;
                             *dst = (mr & 1) ? val : *dst + val;
                         }
@@ -633,21 +663,17 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         }
     }
     __syncthreads();
-    if (*abort_flag && threadIdx.x == 32) {
-        volatile int never = 0;
-        tc_commit(drain);
-        mbar_wait_bounded(drain, 0, a.err, &never, 0x617);
-    }
     tc_fence_before();
     __syncthreads();
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
 zp_status pt_map(CUtensorMap *map, const void *base, const PfxArgs &a, int d) {
-    const uint64_t dims[3] = {(uint64_t)d, (uint64_t)a.h_kv, (uint64_t)a.n_total * a.b};
-    const uint64_t strides[2] = {(uint64_t)d * 2, (uint64_t)a.h_kv * d * 2};
-    const uint32_t box[3] = {64, 1, 16};
-    return encode_tmap_bf16_3d(map, base, dims, strides, box, "prefix_decode");
+    const uint64_t row = (uint64_t)a.h_kv * d * 2;  // bytes of a token, every kv head
+    const uint64_t dims[5] = {64, 8, (uint64_t)d / 64, (uint64_t)a.h_kv, (uint64_t)a.n_total * a.b / 8};
+    const uint64_t strides[4] = {row, 128, (uint64_t)d * 2, 8 * row};
+    const uint32_t box[5] = {64, 8, (uint32_t)d / 64, 1, 2};
+    return encode_tmap_bf16(map, 5, base, dims, strides, box, "prefix_decode");
 }
 
 template <int D>
@@ -661,7 +687,7 @@ zp_status launch_part_tc(const PfxArgs &a, cudaStream_t st) {
     rc = set_max_dynamic_smem(reinterpret_cast<const void *>(prefix_part_tc_kernel<D>), smem,
                               "prefix_decode: shared-memory attribute");
     if (rc != ZP_OK) return rc;
-    prefix_part_tc_kernel<D><<<a.parts, kPtThreads, smem, st>>>(km, vm, a);
+    prefix_part_tc_kernel<D><<<a.parts * a.h_kv, kPtThreads, smem, st>>>(km, vm, a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "prefix_decode: prefix kernel launch");
     return ZP_OK;
@@ -676,7 +702,7 @@ zp_status launch_score_tc(const PfxArgs &a, cudaStream_t st) {
     rc = set_max_dynamic_smem(reinterpret_cast<const void *>(prefix_score_tc_kernel<D, G>), smem,
                               "prefix_decode: shared-memory attribute");
     if (rc != ZP_OK) return rc;
-    prefix_score_tc_kernel<D, G><<<a.parts, kPtThreads, smem, st>>>(km, a);
+    prefix_score_tc_kernel<D, G><<<a.parts * a.h_kv, kPtThreads, smem, st>>>(km, a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "prefix_decode: score kernel launch");
     return ZP_OK;

@@ -133,9 +133,22 @@ __global__ void __launch_bounds__(kSlotThreads) build_slots_kernel(const SlotArg
         return c >= (old_s[s] + a.b - 1) / a.b && a.table[(size_t)s * a.stride + c] < 0;
     };
     int before = 0;
-    for (int x = tid; x < x0; x += kSlotThreads) {
-        const int s = find_seq(ccol, a.B, x);
-        before += missing(s, old_s[s] / a.b + (x - ccol[s])) ? 1 : 0;
+    constexpr int kAhead = 8;  // table entries in flight per thread
+    for (int xb = tid; xb < x0; xb += kAhead * kSlotThreads) {
+        int c[kAhead], e[kAhead], lo[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int x = xb + k * kSlotThreads;
+            e[k] = 0;
+            if (x < x0) {
+                const int s = find_seq(ccol, a.B, x), o = old_s[s];
+                c[k] = o / a.b + (x - ccol[s]);
+                lo[k] = (o + a.b - 1) / a.b;
+                e[k] = a.table[(size_t)s * a.stride + c[k]];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) before += e[k] < 0 && c[k] >= lo[k] ? 1 : 0;
     }
     int mine;
     block_scan(before, warp_sums, &mine);

@@ -73,8 +73,8 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 }  // namespace
 
-zp_status encode_tmap_bf16_3d(void *map, const void *base, const uint64_t dims[3], const uint64_t strides[2],
-                              const uint32_t box[3], const char *what) {
+zp_status encode_tmap_bf16(void *map, int rank, const void *base, const uint64_t *dims, const uint64_t *strides,
+                           const uint32_t *box, const char *what) {
     std::call_once(g_encode_once, [] {
         cudaDriverEntryPointQueryResult q;
         void *fn = nullptr;
@@ -84,16 +84,26 @@ zp_status encode_tmap_bf16_3d(void *map, const void *base, const uint64_t dims[3
             g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     });
     if (!g_encode) return fail(ZP_ERR_CUDA, "%s: cuTensorMapEncodeTiled unavailable", what);
-    const cuuint64_t d[3] = {dims[0], dims[1], dims[2]};
-    const cuuint64_t st[2] = {strides[0], strides[1]};
-    const cuuint32_t bx[3] = {box[0], box[1], box[2]};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    const CUresult r = g_encode(static_cast<CUtensorMap *>(map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+    cuuint64_t d[5], st[4];
+    cuuint32_t bx[5], estr[5];
+    if (rank < 2 || rank > 5) return fail(ZP_ERR_CUDA, "%s: tensor map of rank %d", what, rank);
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        bx[i] = box[i];
+        estr[i] = 1;
+        if (i + 1 < rank) st[i] = strides[i];
+    }
+    const CUresult r = g_encode(static_cast<CUtensorMap *>(map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
                                 const_cast<void *>(base), d, st, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(ZP_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", what, (int)r);
     return ZP_OK;
+}
+
+zp_status encode_tmap_bf16_3d(void *map, const void *base, const uint64_t dims[3], const uint64_t strides[2],
+                              const uint32_t box[3], const char *what) {
+    return encode_tmap_bf16(map, 3, base, dims, strides, box, what);
 }
 
 namespace {

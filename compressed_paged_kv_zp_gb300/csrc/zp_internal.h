@@ -42,6 +42,10 @@ zp_status check_desc(const zp_cache_desc *D);
 zp_status encode_tmap_bf16_3d(void *map /* CUtensorMap */, const void *base, const uint64_t dims[3],
                               const uint64_t strides[2], const uint32_t box[3], const char *what);
 
+// The same of any rank from 2 to 5 (rank - 1 strides).
+zp_status encode_tmap_bf16(void *map, int rank, const void *base, const uint64_t *dims, const uint64_t *strides,
+                           const uint32_t *box, const char *what);
+
 // All-pairs key redundancy of one layer (redundancy.cu): rho [n][h_kv][Lmax]
 // receives the row sums of the thresholded cosine matrix of every sequence and
 // kv head (overwritten).  Lengths are clamped to Lcap.
