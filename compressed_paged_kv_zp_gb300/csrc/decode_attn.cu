@@ -49,6 +49,9 @@
 #ifndef ZP_DECODE_PREFIX
 #define ZP_DECODE_PREFIX 0
 #endif
+#if ZP_DECODE_PREFIX
+#include "prefix_common.cuh"
+#endif
 
 namespace zp {
 namespace {
@@ -289,6 +292,7 @@ __global__ void __launch_bounds__(kMaxConsumerWarps * 32, 1)
     const int warp = tid >> 5;
     const int lane = tid & 31;
 
+    if constexpr (kPrefix) pdl_trigger();
     // ---- unit prefix over sequences: n_units(s) = ceil(L_s / T)
     for (int s = tid; s < B; s += blockDim.x) {
         int L = a.seq_lens[s];
@@ -337,12 +341,16 @@ __global__ void __launch_bounds__(kMaxConsumerWarps * 32, 1)
     }
     if (a.want_score && U > a.logits_units) {
         if (tid == 0) record_error(a.err, ZP_ERR_DEVICE, 3);
+        if constexpr (kPrefix) pdl_wait();
         return;
     }
     const int Gd = gridDim.x;
     const long long u0 = cta_start(blockIdx.x, U, Gd);
     const long long u1 = cta_start(blockIdx.x + 1, U, Gd);
-    if (u0 >= u1) return;
+    if (u0 >= u1) {
+        if constexpr (kPrefix) pdl_wait();
+        return;
+    }
 
     // first sequence of the range: largest s with prefix[s] <= u0
     int s_first = 0;
@@ -446,17 +454,17 @@ __global__ void __launch_bounds__(kMaxConsumerWarps * 32, 1)
             if (!first_unit || wih != 0 || prefix_of(a, s) == 0) return;
             const float2 *iml = a.init_ml + (size_t)s * a.h_q + h0;
 #pragma unroll
-            for (int j = 0; j < G; ++j) m[j] = __ldg(&iml[j]).x;
+            for (int j = 0; j < G; ++j) m[j] = __ldcg(&iml[j]).x;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (owner) l_own[i] = __ldg(&iml[jv[i]]).y;
+                if (owner) l_own[i] = __ldcg(&iml[jv[i]]).y;
             if (half == 0) {
                 const float *ia = a.init_acc + ((size_t)s * a.h_q + h0) * D + lane16 * DPL;
 #pragma unroll
                 for (int j = 0; j < G; ++j)
 #pragma unroll
                     for (int p = 0; p < DPL / 2; ++p)
-                        acc[j][p] = __ldg(reinterpret_cast<const float2 *>(ia + (size_t)j * D) + p);
+                        acc[j][p] = __ldcg(reinterpret_cast<const float2 *>(ia + (size_t)j * D) + p);
             }
         }
     };
@@ -474,6 +482,7 @@ __global__ void __launch_bounds__(kMaxConsumerWarps * 32, 1)
 
     int s = s_first;
     long long seg_begin = u0;
+    if constexpr (kPrefix) pdl_wait();  // the prefix records
     start_state(s, u0 == prefix[s]);
     load_q(s);
     bool window_step = false;
@@ -1315,12 +1324,16 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
     __syncthreads();
     if (a.want_score && U > a.logits_units) {
         if (tid == 0) record_error(a.err, ZP_ERR_DEVICE, 3);
+        if constexpr (kPrefix) pdl_wait();
         return;
     }
     const int Gd = gridDim.x;
     const long long u0 = cst[blockIdx.x];
     const long long u1 = cst[blockIdx.x + 1];
-    if (u0 >= u1) return;
+    if (u0 >= u1) {
+        if constexpr (kPrefix) pdl_wait();
+        return;
+    }
     int s_first = 0;
     {
         int lo = 0, hi = B - 1;
@@ -1429,7 +1442,7 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
         if constexpr (kPrefix) {
             if (!first_unit || prefix_of(a, s) == 0) return;
             if (g < G) {
-                const float2 ml = __ldg(&a.init_ml[(size_t)s * a.h_q + h0 + g]);
+                const float2 ml = __ldcg(&a.init_ml[(size_t)s * a.h_q + h0 + g]);
                 m_run = ml.x;
                 l_run = ml.y;
             }
@@ -1438,12 +1451,12 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
             for (int t = 0; t < KS; ++t) {
                 const int d0 = 16 * t + g;
                 if (2 * tig < G) {
-                    acc[t][0] = __ldg(ia + (size_t)(2 * tig) * D + d0);
-                    acc[t][2] = __ldg(ia + (size_t)(2 * tig) * D + d0 + 8);
+                    acc[t][0] = __ldcg(ia + (size_t)(2 * tig) * D + d0);
+                    acc[t][2] = __ldcg(ia + (size_t)(2 * tig) * D + d0 + 8);
                 }
                 if (2 * tig + 1 < G) {
-                    acc[t][1] = __ldg(ia + (size_t)(2 * tig + 1) * D + d0);
-                    acc[t][3] = __ldg(ia + (size_t)(2 * tig + 1) * D + d0 + 8);
+                    acc[t][1] = __ldcg(ia + (size_t)(2 * tig + 1) * D + d0);
+                    acc[t][3] = __ldcg(ia + (size_t)(2 * tig + 1) * D + d0 + 8);
                 }
             }
         }
@@ -1475,6 +1488,7 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
     int s = s_first;
     long long seg_begin = u0;
     const uint64_t keep_pol = l2_evict_last_policy();
+    if constexpr (kPrefix) pdl_wait();  // the prefix records (the producer reads only inputs)
     start_state(s, u0 == prefix[s]);
     load_q(s);
     bool window_step = compute_window(s);
@@ -1925,6 +1939,10 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
 template <typename T, int D>
 __global__ void __launch_bounds__(256) decode_merge_kernel(const DecodeArgs a, int grid_main) {
     extern __shared__ float2 msm[];  // [grid_main][h_q] (m, l) then weights; then slots, L
+    if constexpr (kPrefix) {
+        pdl_trigger();
+        pdl_wait();
+    }
     const int c = blockIdx.x;
     const int B = a.B;
     const int *pre = a.unit_prefix;
@@ -2014,8 +2032,13 @@ zp_status launch_finish(const DecodeArgs &a, int grid, long long units_cap, cuda
     zp_status rs = set_max_dynamic_smem(reinterpret_cast<const void *>(decode_merge_kernel<T, D>), smem,
                                         "decode: merge shared-memory attribute");
     if (rs != ZP_OK) return rs;
-    decode_merge_kernel<T, D><<<grid, 256, smem, st>>>(a, grid);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = cudaSuccess;
+    if constexpr (kPrefix) {
+        e = launch_dependent(decode_merge_kernel<T, D>, dim3(grid), dim3(256), smem, st, false, a, grid);
+    } else {
+        decode_merge_kernel<T, D><<<grid, 256, smem, st>>>(a, grid);
+        e = cudaGetLastError();
+    }
     if (e != cudaSuccess) return cuda_fail(e, "decode: merge kernel launch");
     if (a.want_score) {
         decode_score_kernel<G><<<(unsigned)units_cap, 128, 0, st>>>(a);
@@ -2109,7 +2132,11 @@ zp_status launch_tc(const DecodeArgs &a, const Plan &p, const DeviceInfo &dev, c
     // cooperative: CTAs wait (bounded) for the merges of other CTAs
     DecodeArgs args = a;
     void *params[] = {&args};
-    cudaError_t e = cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(kmain), dim3(p.grid), dim3(p.threads), params,
+    cudaError_t e = cudaSuccess;
+    if constexpr (kPrefix)
+        e = launch_dependent(kmain, dim3(p.grid), dim3(p.threads), (size_t)p.smem, st, true, a);
+    else
+        e = cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(kmain), dim3(p.grid), dim3(p.threads), params,
                                     (size_t)p.smem, st);
     if (e != cudaSuccess) return cuda_fail(e, "decode: tensor-core kernel launch");
     return ok();  // merges and the window score run inside the kernel
@@ -2121,8 +2148,13 @@ zp_status launch_t(const DecodeArgs &a, const Plan &p, const DeviceInfo &dev, cu
     zp_status rs = set_max_dynamic_smem(reinterpret_cast<const void *>(kmain), (size_t)p.smem,
                                         "decode: shared-memory attribute");
     if (rs != ZP_OK) return rs;
-    kmain<<<p.grid, p.threads, p.smem, st>>>(a);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = cudaSuccess;
+    if constexpr (kPrefix) {
+        e = launch_dependent(kmain, dim3(p.grid), dim3(p.threads), (size_t)p.smem, st, false, a);
+    } else {
+        kmain<<<p.grid, p.threads, p.smem, st>>>(a);
+        e = cudaGetLastError();
+    }
     if (e != cudaSuccess) return cuda_fail(e, "decode: main kernel launch");
     return launch_finish<T, Dd, G>(a, p.grid, p.logits_units, st);
 }
@@ -2148,7 +2180,7 @@ static zp_status decode_impl(const zp_cache_desc *D, const void *q, const void *
                              const int32_t *block_table, int32_t table_stride, const int32_t *seq_lens, int32_t B,
                              void *out, float *score_accum, const int32_t *score_rows, int32_t n_score_rows,
                              int32_t window, void *workspace, size_t workspace_bytes, void *stream,
-                             const zp_rho_rows *rho, const PrefixRecords *pre) {
+                             const zp_rho_rows *rho, const PfxArgs *pfx) {
     zp_status rc = check_desc(D);
     if (rc != ZP_OK) return rc;
     if (B < 0 || table_stride < 0) return fail(ZP_ERR_INVALID_ARG, "decode: B or table_stride negative");
@@ -2224,9 +2256,15 @@ static zp_status decode_impl(const zp_cache_desc *D, const void *q, const void *
     a.rho_weight16 = (rho && p.tc && max_units * kRhoUnitWeight16 < 2.0e9 && (2LL * B + 1) * 4 <= stage_area)
                          ? kRhoUnitWeight16 : 16;
     a.err = dev.error_word;
-    a.prefix_lens = pre ? pre->prefix_lens : nullptr;
-    a.init_acc = pre ? pre->acc : nullptr;
-    a.init_ml = pre ? pre->ml : nullptr;
+#if ZP_DECODE_PREFIX
+    a.prefix_lens = pfx->prefix;
+    a.init_acc = pfx->init_acc;
+    a.init_ml = pfx->init_ml;
+#else
+    a.prefix_lens = nullptr;
+    a.init_acc = nullptr;
+    a.init_ml = nullptr;
+#endif
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int G = D->h_q / D->h_kv;
     const int d = D->head_dim;
@@ -2258,7 +2296,7 @@ static zp_status decode_impl(const zp_cache_desc *D, const void *q, const void *
 zp_status zp::decode_after_prefix(const zp_cache_desc *D, const void *q, const void *k_cache, const void *v_cache,
                                   const int32_t *block_table, int32_t table_stride, const int32_t *seq_lens, int32_t B,
                                   void *out, float *score_accum, const int32_t *score_rows, int32_t n_score_rows,
-                                  int32_t window, const PrefixRecords &pre, void *workspace, size_t workspace_bytes,
+                                  int32_t window, const PfxArgs &pfx, void *workspace, size_t workspace_bytes,
                                   void *stream, const float2 **stats) {
     DeviceInfo dev;
     zp_status rc = device_info(&dev);
@@ -2268,7 +2306,7 @@ zp_status zp::decode_after_prefix(const zp_cache_desc *D, const void *q, const v
     if (rc != ZP_OK) return rc;
     *stats = reinterpret_cast<const float2 *>(static_cast<unsigned char *>(workspace) + p.off_stats);
     return decode_impl(D, q, k_cache, v_cache, block_table, table_stride, seq_lens, B, out, score_accum, score_rows,
-                       n_score_rows, window, workspace, workspace_bytes, stream, nullptr, &pre);
+                       n_score_rows, window, workspace, workspace_bytes, stream, nullptr, &pfx);
 }
 #else
 extern "C" zp_status zp_paged_decode_attn(const zp_cache_desc *D, const void *q, const void *k_cache,

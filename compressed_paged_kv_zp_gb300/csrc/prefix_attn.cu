@@ -20,7 +20,9 @@
 // and the CTAs of a set read the heads of the same token rows at the same time.
 // The first piece of an item goes to its rows' place in the main records, a
 // piece that begins inside an item (at most one per CTA) to the CTA's extra
-// records; a merge kernel joins the pieces of each row.
+// records; a merge kernel joins the pieces of each row.  (Joined by the decode
+// where it starts a sequence instead, the scored 256 x 4k batch took 186 us, not
+// 174: a chain of dependent loads against its own K and V traffic.)
 #include <math.h>
 
 #include "prefix_tc.h"
@@ -133,7 +135,9 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_part_kernel(const PfxArgs 
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int ng = pfx_groups(a);
     const int W = pfx_scan(a, ng, pre);
-    if (blockIdx.x == 0) pfx_publish(a, ng, pre);
+    pdl_trigger();
+    if (blockIdx.x == 0)
+        for (int i = tid; i <= ng; i += kPfxThreads) a.wpre[i] = pre[i];  // for the merge
     const int head = blockIdx.x % a.h_kv, set = blockIdx.x / a.h_kv;
     const int w0 = pfx_start(set, W, a.parts), w1 = pfx_start(set + 1, W, a.parts);
     for (int w = w0; w < w1;) {
@@ -225,75 +229,106 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_part_kernel(const PfxArgs 
     }
 }
 
-// One warp per (member, q head): the pieces of its row joined,
+// One warp per (member, kv head): the pieces of its G rows joined,
 //     M = max_j m_j,  l = sum_j 2^(m_j - M) l_j,  acc = sum_j 2^(m_j - M) acc_j.
-// Lane j finds piece j and its (m, l) (32 pieces at a time), so that the loads
-// of the statistics, and then of the accumulators, are all in flight together.
-template <int D>
-__global__ void __launch_bounds__(256) prefix_merge_kernel(const PfxArgs a) {
+// Lane i finds record i and its (m, l), 32 at a time, so that these loads, and
+// then those of the accumulators, are in flight together.  What depends on the
+// plan alone is done before the wait for the prefix kernel.
+template <int V>
+__device__ __forceinline__ void ld_row(const float *p, float (&v)[V]) {
+    if constexpr (V == 4) {
+        const float4 w = __ldcg(reinterpret_cast<const float4 *>(p));
+        v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+    } else {
+        const float2 w = __ldcg(reinterpret_cast<const float2 *>(p));
+        v[0] = w.x, v[1] = w.y;
+    }
+}
+constexpr int kMergeScan = 256;  // groups up to which a warp sums the tiles itself
+template <int D, int G>
+__global__ void __launch_bounds__(128) prefix_merge_kernel(const PfxArgs a) {
+    pdl_trigger();
     const int lane = threadIdx.x & 31;
-    const long long wi = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const long long wi = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
     const int ng = pfx_groups(a);
-    if (ng == 0) return;
-    const int mi = (int)(wi / a.h_q), h = (int)(wi - (long long)mi * a.h_q);
-    const int W = a.wpre[ng];
-    const int gi = pfx_group_of(a, ng, mi);
-    const PfxGroup g = pfx_group(a, gi);
-    if (mi < g.m0 || mi >= g.m0 + g.n || g.tokens == 0) return;
-    const int s = pfx_member(a, mi);
-    if (s < 0) return;
-    const int G = a.h_q / a.h_kv, head = h / G;
-    const int r = (mi - g.m0) * G + h % G;
-    const int i0 = a.wpre[gi] + r / a.rt * g.kts, i1 = i0 + g.kts;
-    const int c0 = pfx_owner(i0, W, a.parts);
-    // pieces: consecutive sets when each has a tile, one tile each otherwise
-    const int n = W >= a.parts ? pfx_owner(i1 - 1, W, a.parts) - c0 + 1 : g.kts;
-    // an item of at most 128 rows has a record per stream
-    const int row = r % a.rt;
-    const int two = a.tc && min(a.rt, g.n * G - (r - row)) <= a.rt / 2 ? 2 : 1;
-    constexpr int V = D / 32;
-    float M = -INFINITY, L = 0.f, acc[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = 0.f;
-    for (int p0 = 0; p0 < n * two; p0 += 32) {
-        const int p = p0 + lane, j = p / two, x = p - j * two;
-        long long at = 0;
-        float2 ml = make_float2(-INFINITY, 0.f);
-        if (j < n) {
-            const int c = W >= a.parts ? c0 + j : pfx_owner(i0 + j, W, a.parts);
-            at = j == 0 ? pfx_main_row(a, g, head, r) + x * (long long)a.B * a.h_q
-                        : a.extra0 + ((long long)c * a.h_kv + head) * a.rt + x * (a.rt / 2) + row;
-            ml = a.rec_ml[at];
+    const int mi = (int)(wi / a.h_kv), head = (int)(wi - (long long)mi * a.h_kv);
+    int gi = 0, s = -1, before = 0, W = 0;
+    PfxGroup g = {};
+    if (ng > 0 && mi < a.B) {
+        gi = pfx_group_of(a, ng, mi);
+        g = pfx_group(a, gi);
+        if (mi >= g.m0 && mi < g.m0 + g.n && g.tokens > 0) s = pfx_member(a, mi);
+    }
+    if (s >= 0 && ng <= kMergeScan) {
+        for (int i = lane; i < ng; i += 32) {
+            const PfxGroup o = pfx_group(a, i);
+            W += o.rts * o.kts;
+            if (i < gi) before += o.rts * o.kts;
         }
-        float Mn = fmaxf(M, ml.x);
+        W = __reduce_add_sync(0xFFFFFFFFu, W);
+        before = __reduce_add_sync(0xFFFFFFFFu, before);
+    }
+    pdl_wait();
+    if (s < 0) return;
+    if (ng > kMergeScan) {
+        W = __ldcg(a.wpre + ng);
+        before = __ldcg(a.wpre + gi);
+    }
+    const PfxPieces pc = pfx_pieces(a, g, mi, head, before, W);
+    constexpr int V = D / 32;
+    float M[G], L[G], x[G][V];
 #pragma unroll
-        for (int o = 16; o; o >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(0xFFFFFFFFu, Mn, o));
-        if (Mn == -INFINITY) continue;
-        const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - Mn);  // 0: no tile, no accumulator
-        float ls = f * ml.y;
+    for (int j = 0; j < G; ++j) {
+        M[j] = -INFINITY;
+        L[j] = 0.f;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) ls += __shfl_xor_sync(0xFFFFFFFFu, ls, o);
-        const float old = M == -INFINITY ? 0.f : exp2f(M - Mn);
-        L = L * old + ls;
-        M = Mn;
+        for (int e = 0; e < V; ++e) x[j][e] = 0.f;
+    }
+    const int n = pc.n * pc.two;
+    for (int p0 = 0; p0 < n; p0 += 32) {
+        const bool has = p0 + lane < n;
+        const long long at = has ? pfx_record(a, pc, p0 + lane) : 0;
+        float f[G];
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] *= old;
-        const int n_here = min(32, n * two - p0);
+        for (int j = 0; j < G; ++j) {
+            const float2 ml = has ? __ldcg(a.rec_ml + at + j) : make_float2(-INFINITY, 0.f);
+            float Mn = fmaxf(M[j], ml.x);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(0xFFFFFFFFu, Mn, o));
+            f[j] = ml.x == -INFINITY ? 0.f : exp2f(ml.x - Mn);  // 0: a stream without a tile wrote no accumulator
+            float ls = f[j] * ml.y;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) ls += __shfl_xor_sync(0xFFFFFFFFu, ls, o);
+            const float old = M[j] == -INFINITY ? 0.f : exp2f(M[j] - Mn);
+            L[j] = L[j] * old + ls;
+            M[j] = Mn;
+#pragma unroll
+            for (int e = 0; e < V; ++e) x[j][e] *= old;
+        }
+        const int here = min(32, n - p0);
 #pragma unroll 4
-        for (int k = 0; k < n_here; ++k) {
-            const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
+        for (int k = 0; k < here; ++k) {
             const long long ak = __shfl_sync(0xFFFFFFFFu, at, k);
-            if (fk != 0.f) {
-                const float *src = a.rec_acc + ak * D + lane * V;
 #pragma unroll
-                for (int e = 0; e < V; ++e) acc[e] = fmaf(src[e], fk, acc[e]);
+            for (int j = 0; j < G; ++j) {
+                const float fk = __shfl_sync(0xFFFFFFFFu, f[j], k);
+                if (fk != 0.f) {
+                    float v[V];
+                    ld_row<V>(a.rec_acc + (ak + j) * D + lane * V, v);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) x[j][e] = fmaf(fk, v[e], x[j][e]);
+                }
             }
         }
     }
-    float *dst = a.init_acc + ((size_t)s * a.h_q + h) * D + lane * V;
+    const size_t row = (size_t)s * a.h_q + head * G;
 #pragma unroll
-    for (int e = 0; e < V; ++e) dst[e] = acc[e];
-    if (lane == 0) a.init_ml[(size_t)s * a.h_q + h] = make_float2(M, L);
+    for (int j = 0; j < G; ++j) {
+        float *dst = a.init_acc + (row + j) * D + lane * V;
+        if constexpr (V == 4) *reinterpret_cast<float4 *>(dst) = make_float4(x[j][0], x[j][1], x[j][2], x[j][3]);
+        else *reinterpret_cast<float2 *>(dst) = make_float2(x[j][0], x[j][1]);
+        if (lane == 0) a.init_ml[row + j] = make_float2(M[j], L[j]);
+    }
 }
 
 // Window score of the prefix tokens from the final statistics: the logits again,
@@ -309,6 +344,7 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_score_kernel(const PfxArgs
     const int W = pfx_scan(a, ng, pre);
     const int head = blockIdx.x % a.h_kv, set = blockIdx.x / a.h_kv;
     const int w0 = pfx_start(set, W, a.parts), w1 = pfx_start(set + 1, W, a.parts);
+    pdl_wait();  // the decode's statistics
     const float inv_w = 1.f / (float)a.window;
     for (int w = w0; w < w1;) {
         const int gi = pfx_find(pre, ng, w);
@@ -380,7 +416,7 @@ struct PfxPlan {
     bool tc;
     int rt, kt, parts;
     long long extra0;
-    size_t off_wpre, off_prefix, off_rml, off_racc, off_iml, off_iacc, total;
+    size_t off_wpre, off_rml, off_racc, off_iml, off_iacc, total;
 };
 
 zp_status pfx_plan(const zp_cache_desc *D, int B, const DeviceInfo &dev, PfxPlan *p) {
@@ -399,8 +435,6 @@ zp_status pfx_plan(const zp_cache_desc *D, int B, const DeviceInfo &dev, PfxPlan
     size_t off = 0;
     p->off_wpre = off;
     off = align_up(off + (size_t)(B + 1) * 4, 256);
-    p->off_prefix = off;
-    off = align_up(off + (size_t)B * 4, 256);
     p->off_rml = off;
     off = align_up(off + recs * 8, 256);
     p->off_racc = off;
@@ -425,24 +459,26 @@ zp_status launch_part(const PfxArgs &a, cudaStream_t st) {
     return ZP_OK;
 }
 
-zp_status launch_merge(const PfxArgs &a, int d, cudaStream_t st) {
-    const unsigned grid = (unsigned)(((long long)a.B * a.h_q + 7) / 8);
-    if (d == 64) prefix_merge_kernel<64><<<grid, 256, 0, st>>>(a);
-    else prefix_merge_kernel<128><<<grid, 256, 0, st>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_fail(e, "prefix_decode: merge kernel launch");
-    return ZP_OK;
-}
-
 template <int D, int G>
 zp_status launch_score(const PfxArgs &a, cudaStream_t st) {
     const size_t smem = sizeof(PfxSmem<D>) + (size_t)(a.B + 1) * 4;
     zp_status rc = set_max_dynamic_smem(reinterpret_cast<const void *>(prefix_score_kernel<D, G>), smem,
                                         "prefix_decode: shared-memory attribute");
     if (rc != ZP_OK) return rc;
-    prefix_score_kernel<D, G><<<a.parts * a.h_kv, kPfxThreads, smem, st>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_dependent(prefix_score_kernel<D, G>, dim3(a.parts * a.h_kv), dim3(kPfxThreads), smem, st,
+                                           false, a);
     if (e != cudaSuccess) return cuda_fail(e, "prefix_decode: score kernel launch");
+    return ZP_OK;
+}
+
+template <int D>
+zp_status launch_merge(const PfxArgs &a, int G, cudaStream_t st) {
+    const auto kernel = G == 1 ? prefix_merge_kernel<D, 1>
+                      : G == 2 ? prefix_merge_kernel<D, 2>
+                      : G == 4 ? prefix_merge_kernel<D, 4> : prefix_merge_kernel<D, 8>;
+    const cudaError_t e = launch_dependent(kernel, dim3((unsigned)(((long long)a.B * a.h_kv + 3) / 4)), dim3(128), 0, st,
+                                           false, a);
+    if (e != cudaSuccess) return cuda_fail(e, "prefix_decode: merge kernel launch");
     return ZP_OK;
 }
 
@@ -485,7 +521,7 @@ extern "C" zp_status zp_prefix_decode_attn(const zp_cache_desc *D, const void *q
     if (rc != ZP_OK) return rc;
     if (B < 0 || table_stride < 0) return fail(ZP_ERR_INVALID_ARG, "prefix_decode: B or table_stride negative");
     if (B == 0) return ok();
-    if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !out || !workspace || !plan || !plan->n_groups ||
+    if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !out || !workspace || !plan || !plan->prefix_lens || !plan->n_groups ||
         !plan->group_start || !plan->members || !plan->group_blocks)
         return fail(ZP_ERR_INVALID_ARG, "prefix_decode: NULL buffer");
     if (table_stride < 1) return fail(ZP_ERR_INVALID_ARG, "prefix_decode: table_stride < 1");
@@ -525,6 +561,7 @@ extern "C" zp_status zp_prefix_decode_attn(const zp_cache_desc *D, const void *q
     a.h_kv = D->h_kv;
     a.b = D->block_size;
     a.n_total = D->n_total_blocks;
+    a.prefix = plan->prefix_lens;
     a.n_groups = plan->n_groups;
     a.group_start = plan->group_start;
     a.members = plan->members;
@@ -536,7 +573,6 @@ extern "C" zp_status zp_prefix_decode_attn(const zp_cache_desc *D, const void *q
     a.tc = p.tc;
     a.qscale = (float)(1.4426950408889634 / sqrt((double)D->head_dim));
     a.wpre = reinterpret_cast<int *>(ws + p.off_wpre);
-    a.prefix = reinterpret_cast<int32_t *>(ws + p.off_prefix);
     a.rec_acc = reinterpret_cast<float *>(ws + p.off_racc);
     a.rec_ml = reinterpret_cast<float2 *>(ws + p.off_rml);
     a.init_acc = reinterpret_cast<float *>(ws + p.off_iacc);
@@ -551,11 +587,10 @@ extern "C" zp_status zp_prefix_decode_attn(const zp_cache_desc *D, const void *q
     const int d = D->head_dim;
     if (p.tc) rc = prefix_part_tc(a, d, st);
     else rc = d == 64 ? launch_part_f32<64>(a, G, st) : launch_part_f32<128>(a, G, st);
-    if (rc == ZP_OK) rc = launch_merge(a, d, st);
+    if (rc == ZP_OK) rc = d == 64 ? launch_merge<64>(a, G, st) : launch_merge<128>(a, G, st);
     if (rc != ZP_OK) return rc;
-    const PrefixRecords pre = {a.prefix, a.init_acc, a.init_ml};
     rc = decode_after_prefix(D, q, k_cache, v_cache, block_table, table_stride, seq_lens, B, out, score_accum, score_rows,
-                             n_score_rows, window, pre, workspace, dec, stream, &a.stats);
+                             n_score_rows, window, a, workspace, dec, stream, &a.stats);
     if (rc != ZP_OK) return rc;
     if (score_accum) {
         if (p.tc) rc = prefix_score_tc(a, d, st);

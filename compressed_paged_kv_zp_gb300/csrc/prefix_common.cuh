@@ -16,19 +16,18 @@ struct PfxArgs {
     const int32_t *seq_lens;
     int B, h_q, h_kv, b, n_total;
     // the plan
-    const int32_t *n_groups, *group_start, *members, *group_blocks;
+    const int32_t *prefix, *n_groups, *group_start, *members, *group_blocks;
     int rt, kt;          // rows per item, tokens per tile
     int parts;           // sets of CTAs (split of the tiles); a set has a CTA per kv head
     float qscale;        // log2(e) / sqrt(d)
     int *wpre;           // [B+1] tiles before each group
-    int32_t *prefix;     // [B] prefix tokens of every batch entry, 0 = none
     float *rec_acc;      // [extra0 + parts*rt][d] pieces: main records, then extra records
     float2 *rec_ml;      // same rows
     long long extra0;    // first extra record: B*h_q, twice that on the tensor cores (second streams);
                          // then rt rows per CTA (set * h_kv + head)
     int tc;              // tensor-core kernels: 256 rows x 128 tokens, two streams
-    float *init_acc;     // [B][h_q][d]
-    float2 *init_ml;     // [B][h_q]
+    float *init_acc;     // [B][h_q][d] joined accumulators
+    float2 *init_ml;     // [B][h_q] joined (max, sum)
     // score
     float *score;
     long long score_stride;
@@ -152,9 +151,9 @@ __device__ __forceinline__ const int32_t *pfx_row(const PfxArgs &a, const PfxGro
 // not on a window step, no score row).  first: the window's first row, written.
 __device__ __forceinline__ int pfx_score_row(const PfxArgs &a, int s, bool *first) {
     const int L = min(__ldg(a.seq_lens + s), a.stride * a.b);
-    const int p = a.prefix[s];
+    const int p = __ldg(a.prefix + s);
     *first = false;
-    if (p <= 0 || p >= L) return -1;
+    if (p <= 0 || p >= L || p % a.b) return -1;
     const int ph = (L - 1) % a.b;
     if (ph < a.b - a.window) return -1;
     *first = ph == a.b - a.window;
@@ -163,18 +162,38 @@ __device__ __forceinline__ int pfx_score_row(const PfxArgs &a, int s, bool *firs
     return r >= a.n_score_rows ? -1 : r;  // (the decode records a row out of range)
 }
 
-// The first CTA's outputs for the kernels that follow: the tiles before each
-// group and the prefix tokens of every batch entry (whole CTA).
-inline __device__ void pfx_publish(const PfxArgs &a, int ng, const int *pre) {
-    for (int i = threadIdx.x; i <= ng; i += blockDim.x) a.wpre[i] = pre[i];
-    for (int s = threadIdx.x; s < a.B; s += blockDim.x) a.prefix[s] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.B && ng > 0; i += blockDim.x) {
-        const PfxGroup g = pfx_group(a, pfx_group_of(a, ng, i));
-        if (i < g.m0 || i >= g.m0 + g.n) continue;
-        const int s = pfx_member(a, i);
-        if (s >= 0) a.prefix[s] = g.tokens;
-    }
+// Records of the rows of one (member, kv head): the G rows of a piece are
+// consecutive.
+struct PfxPieces {
+    long long main, main2, extra;  // first piece, its second stream; row of CTA 0's extra records
+    int n, two;                    // pieces, records of each (one per stream); n = 0: none
+    int c0, i0, W;                 // set of the first piece; its first tile; all tiles
+};
+
+// before, W: the tiles before the member's group and of all groups.
+__device__ __forceinline__ PfxPieces pfx_pieces(const PfxArgs &a, const PfxGroup &g, int mi, int head, int before, int W) {
+    PfxPieces p = {};
+    if (mi < g.m0 || mi >= g.m0 + g.n || g.tokens == 0) return p;
+    const int G = a.h_q / a.h_kv;
+    const int r = (mi - g.m0) * G, row = r % a.rt;
+    p.W = W;
+    p.i0 = before + r / a.rt * g.kts;
+    p.c0 = pfx_owner(p.i0, W, a.parts);
+    // consecutive sets when each has a tile, one tile each otherwise
+    p.n = W >= a.parts ? pfx_owner(p.i0 + g.kts - 1, W, a.parts) - p.c0 + 1 : g.kts;
+    p.two = a.tc && min(a.rt, g.n * G - (r - row)) <= a.rt / 2 ? 2 : 1;  // at most 128 rows: a record per stream
+    p.main = pfx_main_row(a, g, head, r);
+    p.main2 = p.main + (long long)a.B * a.h_q;
+    p.extra = a.extra0 + (long long)head * a.rt + row;
+    return p;
+}
+
+// First row of record i in [0, n * two).
+__device__ __forceinline__ long long pfx_record(const PfxArgs &a, const PfxPieces &p, int i) {
+    const int j = i / p.two, x = i - j * p.two;
+    if (j == 0) return x ? p.main2 : p.main;
+    const int c = p.W >= a.parts ? p.c0 + j : pfx_owner(p.i0 + j, p.W, a.parts);
+    return p.extra + (long long)c * a.h_kv * a.rt + x * (a.rt / 2);
 }
 
 }  // namespace zp

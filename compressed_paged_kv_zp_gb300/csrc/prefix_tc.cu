@@ -204,7 +204,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     const int W = pfx_scan(a, ng, pre);  // (ends with a barrier)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    if (blockIdx.x == 0) pfx_publish(a, ng, pre);
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i <= ng; i += kPtThreads) a.wpre[i] = pre[i];  // for the merge
     const int head = blockIdx.x % a.h_kv, set = blockIdx.x / a.h_kv;
     const int w0 = pfx_start(set, W, a.parts), w1 = pfx_start(set + 1, W, a.parts);
 
@@ -595,6 +596,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         const float inv_w = 1.f / (float)a.window;
         uint32_t tile = 0, item = 0;
         bool ok_all = true;
+        pdl_wait();  // the decode's statistics (the other warps read only inputs)
         // (every wait is bounded, so a warp that stops cannot leave another waiting for ever)
         for (int w = w0; w < w1 && ok_all; ++item) {
             const PtSeg s = pt_segment(a, pre, ng, w, w1);
@@ -702,8 +704,8 @@ zp_status launch_score_tc(const PfxArgs &a, cudaStream_t st) {
     rc = set_max_dynamic_smem(reinterpret_cast<const void *>(prefix_score_tc_kernel<D, G>), smem,
                               "prefix_decode: shared-memory attribute");
     if (rc != ZP_OK) return rc;
-    prefix_score_tc_kernel<D, G><<<a.parts * a.h_kv, kPtThreads, smem, st>>>(km, a);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_dependent(prefix_score_tc_kernel<D, G>, dim3(a.parts * a.h_kv), dim3(kPtThreads), smem, st,
+                                           false, km, a);
     if (e != cudaSuccess) return cuda_fail(e, "prefix_decode: score kernel launch");
     return ZP_OK;
 }

@@ -234,6 +234,14 @@ __device__ __forceinline__ void named_bar_sync_id(int threads) {
     asm volatile("bar.sync %0, %1;" ::"n"(ID), "r"(threads) : "memory");
 }
 
+// ---------------------------------------------------------------- programmatic dependent launch
+// The kernel launched after this one as its programmatic dependent may start.
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// The kernel before this one has completed and its writes are visible (at once
+// without a programmatic launch).  Every CTA of such a kernel executes it, so
+// that kernels after it in the stream are also after the one before it.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------- misc
 __device__ __forceinline__ float warp_max_xor(float v, int mask) {
     return fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, mask));

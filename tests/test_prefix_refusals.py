@@ -74,7 +74,7 @@ def test_prefix_decode(zp):
     for kw in (dict(B=-1), dict(stride=-1), dict(stride=0), dict(q=None), dict(k=None), dict(v=None), dict(table=None),
                dict(lens=None), dict(out=None), dict(ws=None), dict(S=P, w=0), dict(S=P, w=17), dict(S=P, w=4, rows=P, nr=0),
                dict(q=ctypes.c_void_p(4104)), dict(S=ctypes.c_void_p(4100), w=4), dict(ws=ctypes.c_void_p(4100)),
-               *(dict(plan=_groups(zp, **{k: None})) for k in ("n_groups", "group_start", "members", "group_blocks"))):
+               *(dict(plan=_groups(zp, **{k: None})) for k in ("prefix_lens", "n_groups", "group_start", "members", "group_blocks"))):
         assert call(**kw) == 1, kw
     assert call(B=4096, stride=1 << 20) == 2
     assert call(B=0, q=None) == 0
