@@ -65,6 +65,7 @@ constexpr int kMaxB = 4096;
 // the 64-sequence Qwen3-8B layer fit 1.15-1.18); the stream-K split weighs
 // such units accordingly so that the CTAs holding them finish with the rest.
 constexpr int kRhoUnitWeight16 = 19;
+constexpr int kAlignUnits = 4;  // behind a prefix: units of the longest sequence up to which none is cut
 
 struct DecodeArgs {
     const void *q;
@@ -117,7 +118,7 @@ struct DecodeArgs {
 __device__ __forceinline__ int prefix_of(const DecodeArgs &a, int s, int L) {
     if constexpr (!kPrefix) return 0;
     const int p = __ldg(&a.prefix_lens[s]);
-    return p > 0 && p < L && p % a.b == 0 ? p : 0;
+    return p > 0 && p < L && (p & (a.b - 1)) == 0 ? p : 0;  // (b is a power of two)
 }
 // The same from the sequence's index alone.
 __device__ __forceinline__ int prefix_of(const DecodeArgs &a, int s) {
@@ -201,14 +202,9 @@ __device__ __forceinline__ long long cta_start(int c, long long U, int G) {
     return (long long)c * U / G;
 }
 
-// CTA whose range [start(c), start(c+1)) holds unit u.
-__device__ __forceinline__ int cta_of(long long u, long long U, int G) {
-    int c = (int)((u * G) / U);
-    if (c >= G) c = G - 1;
-    while (c + 1 < G && cta_start(c + 1, U, G) <= u) ++c;
-    while (c > 0 && cta_start(c, U, G) > u) --c;
-    return c;
-}
+// CTA whose range [start(c), start(c+1)) holds unit u: the largest c with
+// floor(c U / G) <= u.
+__device__ __forceinline__ int cta_of(long long u, long long U, int G) { return (int)(((u + 1) * G - 1) / U); }
 
 // Row of S that batch entry s scores into: its query slot when a slot map is
 // given (-1: the entry holds no slot and is not scored), else s.  A slot
@@ -1264,7 +1260,42 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
         fence_barrier_init();
     }
     __syncthreads();
-    if (warp == 0) {
+    int longest = 0;  // units of the longest sequence (kPrefix)
+    if constexpr (kPrefix) {
+        // unit prefix by every warp, a chunk of 32 sequences each: sums, then the
+        // sums before each chunk
+        const int warps = blockDim.x >> 5, chunks = (B + 31) / 32;
+        int *sums = reinterpret_cast<int *>(smem + lay.stage_off);  // [chunks] sums, [chunks] maxima (no copy yet)
+        for (int ch = warp; ch < chunks; ch += warps) {
+            const int q = ch * 32 + lane;
+            const int n = q < B ? (lens[q] + kTcTokens - 1) / kTcTokens : 0;
+            const int sum = __reduce_add_sync(0xFFFFFFFFu, n), mx = __reduce_max_sync(0xFFFFFFFFu, n);
+            if (lane == 0) {
+                sums[ch] = sum;
+                sums[chunks + ch] = mx;
+            }
+        }
+        __syncthreads();
+        int mx = 0;
+        for (int i = lane; i < chunks; i += 32) mx = max(mx, sums[chunks + i]);
+        longest = __reduce_max_sync(0xFFFFFFFFu, mx);
+        for (int ch = warp; ch < chunks; ch += warps) {
+            int before = 0;
+            for (int i = lane; i < ch; i += 32) before += sums[i];
+            before = __reduce_add_sync(0xFFFFFFFFu, before);
+            const int q = ch * 32 + lane;
+            const int n = q < B ? (lens[q] + kTcTokens - 1) / kTcTokens : 0;
+            int x = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+                if (lane >= o) x += y;
+            }
+            if (q < B) prefix[q] = before + x - n;
+            if (q == B - 1) prefix[B] = before + x;
+        }
+        fence_proxy_async_smem();  // these accesses of the stage area precede the copies into it
+    } else if (warp == 0) {
         // unit prefix, and with a weighted split the weighted prefix, in one pass
         int carry = 0, wcarry = 0;
         for (int base = 0; base < B; base += 32) {
@@ -1318,6 +1349,20 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
             cst[c] = v;
         }
         fence_proxy_async_smem();  // these reads of the stage area precede the copies into it
+    } else if (kPrefix && longest <= kAlignUnits) {
+        // Behind a prefix the sequences may have just begun.  While none has more
+        // than a few units, a CTA takes whole sequences (those that start in its
+        // equal share): the cuts' merge costs more than a share off by a few units.
+        for (int c = tid; c <= (int)gridDim.x; c += blockDim.x) {
+            const long long target = cta_start(c, U, gridDim.x);
+            int lo = 0, hi = B;  // the first sequence that starts at or after it
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (prefix[mid] >= target) hi = mid;
+                else lo = mid + 1;
+            }
+            cst[c] = prefix[lo];
+        }
     } else {
         for (int c = tid; c <= (int)gridDim.x; c += blockDim.x) cst[c] = cta_start(c, U, gridDim.x);
     }
@@ -2129,12 +2174,15 @@ zp_status launch_tc(const DecodeArgs &a, const Plan &p, const DeviceInfo &dev, c
     if (rs != ZP_OK) return rs;
     if ((reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v)) % 16)
         return fail(ZP_ERR_INVALID_ARG, "decode: caches must be 16-byte aligned");
-    // cooperative: CTAs wait (bounded) for the merges of other CTAs
+    // cooperative: CTAs wait (bounded) for the merges of other CTAs.  Behind a
+    // prefix and without the score no CTA waits for another (the last arrival
+    // merges), and an ordinary launch may start while the kernel before it ends;
+    // a cooperative one never does (8 sequences behind 2k tokens: 39 -> 35 us).
     DecodeArgs args = a;
     void *params[] = {&args};
     cudaError_t e = cudaSuccess;
     if constexpr (kPrefix)
-        e = launch_dependent(kmain, dim3(p.grid), dim3(p.threads), (size_t)p.smem, st, true, a);
+        e = launch_dependent(kmain, dim3(p.grid), dim3(p.threads), (size_t)p.smem, st, a.want_score != 0, a);
     else
         e = cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(kmain), dim3(p.grid), dim3(p.threads), params,
                                     (size_t)p.smem, st);

@@ -229,11 +229,7 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_part_kernel(const PfxArgs 
     }
 }
 
-// One warp per (member, kv head): the pieces of its G rows joined,
-//     M = max_j m_j,  l = sum_j 2^(m_j - M) l_j,  acc = sum_j 2^(m_j - M) acc_j.
-// Lane i finds record i and its (m, l), 32 at a time, so that these loads, and
-// then those of the accumulators, are in flight together.  What depends on the
-// plan alone is done before the wait for the prefix kernel.
+// V consecutive floats through L2.
 template <int V>
 __device__ __forceinline__ void ld_row(const float *p, float (&v)[V]) {
     if constexpr (V == 4) {
@@ -244,14 +240,31 @@ __device__ __forceinline__ void ld_row(const float *p, float (&v)[V]) {
         v[0] = w.x, v[1] = w.y;
     }
 }
+
+// The records of the G rows of a (member, kv head) pair joined by SPLIT warps,
+//     M = max_j m_j,  l = sum_j 2^(m_j - M) l_j,  acc = sum_j 2^(m_j - M) acc_j:
+// a share of the records per warp and, for SPLIT > 1, the warps' results joined in
+// shared memory.  Lane i finds record i and its (m, l), 32 at a time, and lists
+// those that hold anything, so that the loads of the statistics, and then of the
+// accumulators, are in flight together: bound by the latency of these two.  What
+// depends on the plan alone is done before the wait for the prefix kernel.
+// Few pairs have many records each, many pairs few: a CTA of four warps takes one
+// pair while the pairs fill the GPU at most once (64 pairs of 16 records: 2.6 us
+// after the wait, 7.4 us with a warp each), else four (2048 pairs of 6: 3.6 us;
+// 13 us with four warps each).
 constexpr int kMergeScan = 256;  // groups up to which a warp sums the tiles itself
-template <int D, int G>
-__global__ void __launch_bounds__(128) prefix_merge_kernel(const PfxArgs a) {
+constexpr int kMergeWarps = 4;
+template <int D, int G, int SPLIT>
+__global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const PfxArgs a) {
     pdl_trigger();
-    const int lane = threadIdx.x & 31;
-    const long long wi = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    __shared__ long long at_s[kMergeWarps][32];
+    __shared__ float f_s[kMergeWarps][32][G];
+    __shared__ float acc_s[SPLIT > 1 ? SPLIT : 1][G][D];
+    __shared__ float2 ml_s[SPLIT > 1 ? SPLIT : 1][G];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int ng = pfx_groups(a);
-    const int mi = (int)(wi / a.h_kv), head = (int)(wi - (long long)mi * a.h_kv);
+    const int pair = SPLIT > 1 ? blockIdx.x : blockIdx.x * kMergeWarps + warp;
+    const int mi = pair / a.h_kv, head = pair - mi * a.h_kv;
     int gi = 0, s = -1, before = 0, W = 0;
     PfxGroup g = {};
     if (ng > 0 && mi < a.B) {
@@ -268,13 +281,11 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PfxArgs a) {
         W = __reduce_add_sync(0xFFFFFFFFu, W);
         before = __reduce_add_sync(0xFFFFFFFFu, before);
     }
+    PfxPieces pc = {};
+    if (s >= 0 && ng <= kMergeScan) pc = pfx_pieces(a, g, mi, head, before, W);
     pdl_wait();
     if (s < 0) return;
-    if (ng > kMergeScan) {
-        W = __ldcg(a.wpre + ng);
-        before = __ldcg(a.wpre + gi);
-    }
-    const PfxPieces pc = pfx_pieces(a, g, mi, head, before, W);
+    if (ng > kMergeScan) pc = pfx_pieces(a, g, mi, head, __ldcg(a.wpre + gi), __ldcg(a.wpre + ng));
     constexpr int V = D / 32;
     float M[G], L[G], x[G][V];
 #pragma unroll
@@ -285,18 +296,27 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PfxArgs a) {
         for (int e = 0; e < V; ++e) x[j][e] = 0.f;
     }
     const int n = pc.n * pc.two;
-    for (int p0 = 0; p0 < n; p0 += 32) {
-        const bool has = p0 + lane < n;
+    const int part = SPLIT > 1 ? warp : 0;
+    const int n_b = n * part / SPLIT, n_e = n * (part + 1) / SPLIT;
+    for (int p0 = n_b; p0 < n_e; p0 += 32) {
+        const bool has = p0 + lane < n_e;
         const long long at = has ? pfx_record(a, pc, p0 + lane) : 0;
-        float f[G];
+        float2 ml[G];
+#pragma unroll
+        for (int j = 0; j < G; ++j) ml[j] = has ? __ldcg(a.rec_ml + at + j) : make_float2(-INFINITY, 0.f);
+        const bool holds = ml[0].x != -INFINITY;  // else a stream without a tile: no accumulator either
+        const unsigned mask = __ballot_sync(0xFFFFFFFFu, holds);
+        if (mask == 0) continue;
+        const int at_i = __popc(mask & ((1u << lane) - 1));
+        if (holds) at_s[warp][at_i] = at;
 #pragma unroll
         for (int j = 0; j < G; ++j) {
-            const float2 ml = has ? __ldcg(a.rec_ml + at + j) : make_float2(-INFINITY, 0.f);
-            float Mn = fmaxf(M[j], ml.x);
+            float Mn = fmaxf(M[j], ml[j].x);
 #pragma unroll
             for (int o = 16; o; o >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(0xFFFFFFFFu, Mn, o));
-            f[j] = ml.x == -INFINITY ? 0.f : exp2f(ml.x - Mn);  // 0: a stream without a tile wrote no accumulator
-            float ls = f[j] * ml.y;
+            const float f = holds ? exp2f(ml[j].x - Mn) : 0.f;
+            if (holds) f_s[warp][at_i][j] = f;
+            float ls = f * ml[j].y;
 #pragma unroll
             for (int o = 16; o; o >>= 1) ls += __shfl_xor_sync(0xFFFFFFFFu, ls, o);
             const float old = M[j] == -INFINITY ? 0.f : exp2f(M[j] - Mn);
@@ -305,29 +325,60 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PfxArgs a) {
 #pragma unroll
             for (int e = 0; e < V; ++e) x[j][e] *= old;
         }
-        const int here = min(32, n - p0);
-#pragma unroll 4
-        for (int k = 0; k < here; ++k) {
-            const long long ak = __shfl_sync(0xFFFFFFFFu, at, k);
+        __syncwarp();
+        const int here = __popc(mask);
+        constexpr int U = G <= 4 ? 4 : 2;  // records in flight
+#pragma unroll 1
+        for (int k0 = 0; k0 < here; k0 += U) {
+            float v[U][G][V];
 #pragma unroll
-            for (int j = 0; j < G; ++j) {
-                const float fk = __shfl_sync(0xFFFFFFFFu, f[j], k);
-                if (fk != 0.f) {
-                    float v[V];
-                    ld_row<V>(a.rec_acc + (ak + j) * D + lane * V, v);
+            for (int u = 0; u < U; ++u) {  // behind the last: the first record with weight 0
+                const float *src = a.rec_acc + at_s[warp][k0 + u < here ? k0 + u : 0] * D + lane * V;
 #pragma unroll
-                    for (int e = 0; e < V; ++e) x[j][e] = fmaf(fk, v[e], x[j][e]);
-                }
+                for (int j = 0; j < G; ++j) ld_row<V>(src + j * D, v[u][j]);
             }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int j = 0; j < G; ++j) {
+                    const float f = k0 + u < here ? f_s[warp][k0 + u][j] : 0.f;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) x[j][e] = fmaf(f, v[u][j][e], x[j][e]);
+                }
         }
+        __syncwarp();
     }
     const size_t row = (size_t)s * a.h_q + head * G;
+    if constexpr (SPLIT == 1) {
 #pragma unroll
-    for (int j = 0; j < G; ++j) {
-        float *dst = a.init_acc + (row + j) * D + lane * V;
-        if constexpr (V == 4) *reinterpret_cast<float4 *>(dst) = make_float4(x[j][0], x[j][1], x[j][2], x[j][3]);
-        else *reinterpret_cast<float2 *>(dst) = make_float2(x[j][0], x[j][1]);
-        if (lane == 0) a.init_ml[row + j] = make_float2(M[j], L[j]);
+        for (int j = 0; j < G; ++j) {
+            float *dst = a.init_acc + (row + j) * D + lane * V;
+            if constexpr (V == 4) *reinterpret_cast<float4 *>(dst) = make_float4(x[j][0], x[j][1], x[j][2], x[j][3]);
+            else *reinterpret_cast<float2 *>(dst) = make_float2(x[j][0], x[j][1]);
+            if (lane == 0) a.init_ml[row + j] = make_float2(M[j], L[j]);
+        }
+    } else {  // (s is the CTA's: every warp is here)
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc_s[warp][j][lane * V + e] = x[j][e];
+            if (lane == 0) ml_s[warp][j] = make_float2(M[j], L[j]);
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < G * D; i += 32 * SPLIT) {
+            const int j = i / D, c = i % D;
+            float Mj = -INFINITY, Lj = 0.f, y = 0.f;
+#pragma unroll
+            for (int w = 0; w < SPLIT; ++w) Mj = fmaxf(Mj, ml_s[w][j].x);
+#pragma unroll
+            for (int w = 0; w < SPLIT; ++w) {
+                const float f = ml_s[w][j].x == -INFINITY ? 0.f : exp2f(ml_s[w][j].x - Mj);
+                Lj += f * ml_s[w][j].y;
+                y = fmaf(f, acc_s[w][j][c], y);
+            }
+            a.init_acc[(row + j) * D + c] = y;
+            if (c == 0) a.init_ml[row + j] = make_float2(Mj, Lj);
+        }
     }
 }
 
@@ -471,15 +522,25 @@ zp_status launch_score(const PfxArgs &a, cudaStream_t st) {
     return ZP_OK;
 }
 
-template <int D>
-zp_status launch_merge(const PfxArgs &a, int G, cudaStream_t st) {
-    const auto kernel = G == 1 ? prefix_merge_kernel<D, 1>
-                      : G == 2 ? prefix_merge_kernel<D, 2>
-                      : G == 4 ? prefix_merge_kernel<D, 4> : prefix_merge_kernel<D, 8>;
-    const cudaError_t e = launch_dependent(kernel, dim3((unsigned)(((long long)a.B * a.h_kv + 3) / 4)), dim3(128), 0, st,
-                                           false, a);
+template <int D, int G>
+zp_status launch_merge_g(const PfxArgs &a, cudaStream_t st) {
+    const long long pairs = (long long)a.B * a.h_kv;
+    const bool split = pairs <= 8LL * a.parts * a.h_kv;  // CTAs per SM that fit at once
+    const cudaError_t e =
+        split ? launch_dependent(prefix_merge_kernel<D, G, kMergeWarps>, dim3((unsigned)pairs), dim3(32 * kMergeWarps), 0,
+                                 st, false, a)
+              : launch_dependent(prefix_merge_kernel<D, G, 1>, dim3((unsigned)((pairs + kMergeWarps - 1) / kMergeWarps)),
+                                 dim3(32 * kMergeWarps), 0, st, false, a);
     if (e != cudaSuccess) return cuda_fail(e, "prefix_decode: merge kernel launch");
     return ZP_OK;
+}
+
+template <int D>
+zp_status launch_merge(const PfxArgs &a, int G, cudaStream_t st) {
+    if (G == 1) return launch_merge_g<D, 1>(a, st);
+    if (G == 2) return launch_merge_g<D, 2>(a, st);
+    if (G == 4) return launch_merge_g<D, 4>(a, st);
+    return launch_merge_g<D, 8>(a, st);
 }
 
 // fp32 caches: the kernel of the head dimension and group size.

@@ -13,8 +13,9 @@
 //
 // One cluster of CTAs, a slice of the batch per CTA: a shared-memory hash of the
 // first blocks finds the leaders (each CTA builds it from all B first entries),
-// a warp per sequence compares table rows, lcp and counts are exchanged through
-// distributed shared memory, and the first CTA numbers the groups.  Bound by
+// a warp compares table rows, lcp and counts are exchanged through distributed
+// shared memory (a sequence is counted against its own class only, whose members
+// are listed together), and the first CTA numbers the groups.  Bound by
 // latency (four cluster barriers and the gather of the first column); the rows
 // are read only up to their first difference.
 #include <cooperative_groups.h>
@@ -40,9 +41,26 @@ struct PlanArgs {
 };
 
 // Shared memory of one CTA.
+static_assert(kPlanHash >= 2 * kPlanMaxB && kPlanMaxB == 1 << 12, "arrays over the hash; 12 bits of an index");
 struct PlanSmem {
-    int key[kPlanHash];                  // first block id, -1 = free
-    unsigned long long lead[kPlanHash];  // (u << 32) | ~index of the leader; later (gain, lcp) of the class
+    union {
+        int key[kPlanHash];              // first block id, -1 = free
+        struct {                         // once the leaders are known:
+            unsigned gain[kPlanMaxB];    // by leader: most blocks saved
+            int shared[kPlanMaxB];       // by leader: the longest lcp that saves them
+        };
+    };
+    union {
+        struct {
+            int most[kPlanHash];         // largest u of the class
+            int lead[kPlanHash];         // its leader: the lowest index with that u
+        };
+        struct {                         // once the leaders are known, by leader:
+            int cls_n[kPlanMaxB];        // sequences of the class
+            int cls_at[kPlanMaxB];       // its first place in seg
+            unsigned seg[kPlanMaxB];     // the classes one after another: (lcp << 12) | index
+        };
+    };
     int leader[kPlanMaxB];               // leader of each sequence, -1 = no class
     int lcp[kPlanMaxB];
     int aux[kPlanMaxB];                  // members with at least this lcp, then the rank inside the group
@@ -88,6 +106,56 @@ __device__ __forceinline__ int plan_full(const PlanArgs &a, int s) {
     return L > 0 ? (L - 1) / a.b : 0;
 }
 
+constexpr int kWarps = kPlanThreads / 32;
+
+// lcp of sequences [e0, e1) with their leaders, written to every CTA: EACH rows per
+// warp at a time, 64 entries of each, all loads in flight.
+template <int EACH>
+__device__ __forceinline__ void plan_lcp(const PlanArgs &a, PlanSmem &sm, cooperative_groups::cluster_group &cluster, int e0,
+                                         int e1) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int s0 = e0 + warp * EACH; s0 < e1; s0 += kWarps * EACH) {
+        int n[EACH], far = 0;
+        const int32_t *r0[EACH], *r1[EACH];
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            const int s = s0 + i, ld = s < e1 ? sm.leader[s] : -1;
+            n[i] = ld >= 0 ? min(sm.full[s], sm.full[ld]) : 0;
+            far = max(far, n[i]);
+            r0[i] = a.table + (size_t)(ld >= 0 ? s : 0) * a.stride;
+            r1[i] = a.table + (size_t)(ld >= 0 ? ld : 0) * a.stride;
+        }
+        for (int c0 = 0; c0 < far; c0 += 64) {
+            int x[EACH][2], y[EACH][2];
+#pragma unroll
+            for (int i = 0; i < EACH; ++i)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int c = c0 + 32 * q + lane;
+                    const bool in = c < n[i];  // (a row that has differed reads no further)
+                    x[i][q] = in ? r0[i][c] : 0;
+                    y[i][q] = in ? r1[i][c] : 0;
+                }
+            far = 0;
+#pragma unroll
+            for (int i = 0; i < EACH; ++i) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const unsigned bad =
+                        __ballot_sync(0xFFFFFFFFu, !(x[i][q] == y[i][q] && x[i][q] >= 0 && x[i][q] < a.n_total));
+                    if (bad) n[i] = min(n[i], c0 + 32 * q + __ffs(bad) - 1);
+                }
+                far = max(far, n[i]);
+            }
+        }
+        if (lane < kPlanCluster) {
+#pragma unroll
+            for (int i = 0; i < EACH; ++i)
+                if (s0 + i < e1) *cluster.map_shared_rank(&sm.lcp[s0 + i], lane) = n[i];
+        }
+    }
+}
+
 __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanThreads, 1)
     prefix_plan_kernel(const PlanArgs a) {
     extern __shared__ __align__(16) unsigned char plan_smem_raw[];
@@ -100,7 +168,8 @@ __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanThre
 
     for (int i = tid; i < kPlanHash; i += kPlanThreads) {
         sm.key[i] = -1;
-        sm.lead[i] = 0;
+        sm.most[i] = 0;
+        sm.lead[i] = kPlanMaxB;
     }
     __syncthreads();
     // leaders: every CTA hashes every sequence's first block
@@ -116,106 +185,82 @@ __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanThre
                 if (k == -1 || k == first) break;
                 h = (h + 1) % kPlanHash;
             }
-            atomicMax(&sm.lead[h], ((unsigned long long)u << 32) | (unsigned)(~s));
+            atomicMax(&sm.most[h], u);
         }
         sm.leader[s] = h;  // hash slot for now
     }
     __syncthreads();
     for (int s = tid; s < B; s += kPlanThreads) {
         const int h = sm.leader[s];
-        sm.leader[s] = h < 0 ? -1 : (int)~(unsigned)(sm.lead[h] & 0xFFFFFFFFull);
+        if (h >= 0 && sm.full[s] == sm.most[h]) atomicMin(&sm.lead[h], s);
+    }
+    __syncthreads();
+    for (int s = tid; s < B; s += kPlanThreads) {
+        const int h = sm.leader[s];
+        sm.leader[s] = h < 0 ? -1 : sm.lead[h];
         sm.lcp[s] = 0;
     }
     cluster.sync();  // every CTA's arrays are ready for the others' writes
-    // lcp of this CTA's sequences, given to every CTA: a warp compares kEach rows
-    // with their leaders' at a time, 64 entries each, all loads in flight
-    constexpr int kWarps = kPlanThreads / 32, kEach = 4;
-    for (int s0 = e0 + warp * kEach; s0 < e1; s0 += kWarps * kEach) {
-        int lim[kEach], n[kEach], far = 0;
-        const int32_t *r0[kEach], *r1[kEach];
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            const int s = s0 + i, ld = s < e1 ? sm.leader[s] : -1;
-            lim[i] = ld >= 0 ? min(sm.full[s], sm.full[ld]) : 0;
-            n[i] = lim[i];
-            far = max(far, lim[i]);
-            r0[i] = a.table + (size_t)(ld >= 0 ? s : 0) * a.stride;
-            r1[i] = a.table + (size_t)(ld >= 0 ? ld : 0) * a.stride;
-        }
-        for (int c0 = 0; c0 < far; c0 += 64) {
-            int x[kEach][2], y[kEach][2];
-#pragma unroll
-            for (int i = 0; i < kEach; ++i)
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int c = c0 + 32 * q + lane;
-                    const bool in = c < n[i];  // (a row that has differed reads no further)
-                    x[i][q] = in ? r0[i][c] : 0;
-                    y[i][q] = in ? r1[i][c] : 0;
-                }
-            far = 0;
-#pragma unroll
-            for (int i = 0; i < kEach; ++i) {
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const unsigned bad =
-                        __ballot_sync(0xFFFFFFFFu, !(x[i][q] == y[i][q] && x[i][q] >= 0 && x[i][q] < a.n_total));
-                    if (bad) n[i] = min(n[i], c0 + 32 * q + __ffs(bad) - 1);
-                }
-                far = max(far, n[i]);
-            }
-        }
-        if (lane < kPlanCluster) {
-#pragma unroll
-            for (int i = 0; i < kEach; ++i)
-                if (s0 + i < e1) *cluster.map_shared_rank(&sm.lcp[s0 + i], lane) = n[i];
-        }
-    }
+    // lcp of this CTA's sequences, given to every CTA; every sequence a warp has
+    // is compared at the same time (their loads overlap)
+    const int per_warp = (e1 - e0 + kWarps - 1) / kWarps;
+    if (per_warp <= 1) plan_lcp<1>(a, sm, cluster, e0, e1);
+    else if (per_warp <= 4) plan_lcp<4>(a, sm, cluster, e0, e1);
+    else plan_lcp<8>(a, sm, cluster, e0, e1);
+    for (int s = tid; s < B; s += kPlanThreads) sm.cls_n[s] = 0;  // (the hash is no longer needed)
     cluster.sync();
+    // the classes one after another, so that a sequence is compared with its own
+    for (int s = tid; s < B; s += kPlanThreads)
+        if (sm.leader[s] >= 0) atomicAdd(&sm.cls_n[sm.leader[s]], 1);
+    __syncthreads();
+    for (int base = 0, at = 0; base < B; base += kPlanThreads) {
+        const int s = base + tid;
+        const int n = s < B ? sm.cls_n[s] : 0;
+        const int p = at + plan_scan(n, sm);
+        if (s < B) sm.cls_at[s] = p;
+        at += sm.total;
+        __syncthreads();
+    }
+    for (int s = tid; s < B; s += kPlanThreads) {
+        const int ld = sm.leader[s];
+        if (ld >= 0) sm.seg[atomicAdd(&sm.cls_at[ld], 1)] = ((unsigned)sm.lcp[s] << 12) | (unsigned)s;
+    }
+    __syncthreads();  // (cls_at is now the class's end)
     // members of the class with at least this lcp, given to the first CTA
-    constexpr int kMany = 8;  // sequences a warp counts for together
-    for (int s0 = e0 + warp * kMany; s0 < e1; s0 += kWarps * kMany) {
-        int ld[kMany], n[kMany], cnt[kMany];
-#pragma unroll
-        for (int i = 0; i < kMany; ++i) {
-            ld[i] = s0 + i < e1 ? sm.leader[s0 + i] : -1;
-            n[i] = s0 + i < e1 ? sm.lcp[s0 + i] : 0;
-            if (ld[i] < 0) ld[i] = -2;  // equal to no leader
-            cnt[i] = 0;
+    for (int s = e0 + warp; s < e1; s += kWarps) {
+        const int ld = sm.leader[s];
+        int cnt = 0;
+        if (ld >= 0) {
+            const unsigned mine = (unsigned)sm.lcp[s] << 12;
+            for (int j = sm.cls_at[ld] - sm.cls_n[ld] + lane; j < sm.cls_at[ld]; j += 32) cnt += sm.seg[j] >= mine ? 1 : 0;
         }
-        for (int j = lane; j < B; j += 32) {
-            const int lj = sm.leader[j], nj = sm.lcp[j];
-#pragma unroll
-            for (int i = 0; i < kMany; ++i) cnt[i] += lj == ld[i] && nj >= n[i] ? 1 : 0;
-        }
-#pragma unroll
-        for (int i = 0; i < kMany; ++i) {
-            const int c = __reduce_add_sync(0xFFFFFFFFu, cnt[i]);
-            if (lane == 0 && s0 + i < e1) *cluster.map_shared_rank(&sm.aux[s0 + i], 0) = c;
-        }
+        cnt = __reduce_add_sync(0xFFFFFFFFu, cnt);
+        if (lane == 0) *cluster.map_shared_rank(&sm.aux[s], 0) = cnt;
     }
     cluster.sync();
     if (rank == 0) {
-        // best (blocks saved, lcp) and its member count per class
-        for (int s = tid; s < B; s += kPlanThreads) sm.lead[s] = 0;
+        // per class the most blocks saved, then the longest lcp that saves them
+        for (int s = tid; s < B; s += kPlanThreads) {
+            sm.gain[s] = 0;
+            sm.shared[s] = 0;
+            sm.gid[s] = B;
+            sm.size[s] = 0;
+        }
+        __syncthreads();
+        for (int s = tid; s < B; s += kPlanThreads)
+            if (sm.leader[s] >= 0) atomicMax(&sm.gain[sm.leader[s]], (unsigned)sm.lcp[s] * (unsigned)(sm.aux[s] - 1));
         __syncthreads();
         for (int s = tid; s < B; s += kPlanThreads) {
             const int ld = sm.leader[s];
-            if (ld < 0) continue;
-            const unsigned long long gain = (unsigned long long)sm.lcp[s] * (unsigned)(sm.aux[s] - 1);
-            // gain < 2^31 * 2^12, lcp < 2^31 but at most the row length: 21 bits are left for it
-            atomicMax(&sm.lead[ld], (gain << 21) | (unsigned)min(sm.lcp[s], (1 << 21) - 1));
-            sm.gid[ld] = B;
-            sm.size[ld] = 0;
+            if (ld >= 0 && (unsigned)sm.lcp[s] * (unsigned)(sm.aux[s] - 1) == sm.gain[ld]) atomicMax(&sm.shared[ld], sm.lcp[s]);
         }
         __syncthreads();
         for (int s = tid; s < B; s += kPlanThreads) {
             const int ld = sm.leader[s];
             bool in = false;
             if (ld >= 0) {
-                const int p = (int)(sm.lead[ld] & ((1u << 21) - 1));
-                const unsigned long long gain = sm.lead[ld] >> 21;
-                const unsigned long long cnt = gain / (unsigned)p + 1;  // p >= 1: the first blocks are equal
+                const int p = sm.shared[ld];
+                const unsigned cnt = sm.gain[ld] / (unsigned)p + 1;  // p >= 1: the first blocks are equal
                 in = sm.lcp[s] >= p && p >= a.min_blocks && cnt >= (unsigned)a.min_members;
                 if (in) {
                     atomicMin(&sm.gid[ld], s);
@@ -242,7 +287,7 @@ __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanThre
             __syncthreads();
             if (head) {
                 a.group_start[g] = at;
-                a.group_blocks[g] = (int)(sm.lead[ld] & ((1u << 21) - 1));
+                a.group_blocks[g] = sm.shared[ld];
                 sm.aux[ld] = at;  // the class's first place (the counts are no longer needed)
             }
         }
@@ -256,27 +301,20 @@ __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanThre
     // rank of each member inside its group: same leader, lower index
     const PlanSmem *first = cluster.map_shared_rank(&sm, 0);
     if (rank != 0) {
-        for (int s = tid; s < e1; s += kPlanThreads) sm.member[s] = first->member[s];
+        for (int s = tid * 4; s < B; s += kPlanThreads * 4)
+            *reinterpret_cast<unsigned *>(sm.member + s) = *reinterpret_cast<const unsigned *>(first->member + s);
         __syncthreads();
     }
-    for (int s0 = e0 + warp * kMany; s0 < e1; s0 += kWarps * kMany) {
-        int ld[kMany], r[kMany];
-#pragma unroll
-        for (int i = 0; i < kMany; ++i) {
-            ld[i] = s0 + i < e1 && sm.member[s0 + i] ? sm.leader[s0 + i] : -2;
-            r[i] = 0;
+    for (int s = e0 + warp; s < e1; s += kWarps) {
+        if (!sm.member[s]) continue;
+        const int ld = sm.leader[s];
+        int r = 0;
+        for (int j = sm.cls_at[ld] - sm.cls_n[ld] + lane; j < sm.cls_at[ld]; j += 32) {
+            const int o = (int)(sm.seg[j] & (kPlanMaxB - 1));
+            r += o < s && sm.member[o] ? 1 : 0;
         }
-        const int end = min(e1, s0 + kMany);
-        for (int j = lane; j < end; j += 32) {
-            const int lj = sm.member[j] ? sm.leader[j] : -1;
-#pragma unroll
-            for (int i = 0; i < kMany; ++i) r[i] += lj == ld[i] && j < s0 + i ? 1 : 0;
-        }
-#pragma unroll
-        for (int i = 0; i < kMany; ++i) {
-            const int c = __reduce_add_sync(0xFFFFFFFFu, r[i]);
-            if (lane == 0 && ld[i] >= 0) a.members[first->aux[ld[i]] + c] = s0 + i;
-        }
+        r = __reduce_add_sync(0xFFFFFFFFu, r);
+        if (lane == 0) a.members[first->aux[ld] + r] = s;
     }
     cluster.sync();  // the first CTA's shared memory outlives the others' reads
 }
@@ -298,7 +336,8 @@ extern "C" zp_status zp_prefix_plan(const zp_cache_desc *D, const int32_t *block
         (B > 0 && (!block_table || !seq_lens || !plan->prefix_lens || !plan->members || !plan->group_blocks)))
         return fail(ZP_ERR_INVALID_ARG, "prefix_plan: NULL buffer");
     if (B > kPlanMaxB) return fail(ZP_ERR_SHAPE, "prefix_plan: B %d > %d", B, kPlanMaxB);
-    if (table_stride >= 1 << 21 || (long long)table_stride * D->block_size > INT32_MAX)
+    // (blocks saved by a class, stride * (B - 1), fit 32 bits)
+    if (table_stride >= 1 << 20 || (long long)table_stride * D->block_size > INT32_MAX)
         return fail(ZP_ERR_SHAPE, "prefix_plan: table rows of %d blocks", table_stride);
     DeviceInfo dev;
     rc = device_info(&dev);

@@ -474,8 +474,8 @@ struct PsCfg {
     static constexpr int ST_OFF = B_BYTES;
     static constexpr int BAR_OFF = ST_OFF + STAGES * TILE;
     static constexpr int C_OFF = BAR_OFF + 256;        // c of every row
-    static constexpr int M_OFF = C_OFF + kPtRows * 4;  // score row of every member: row * 2 + first, -1 none
-    static constexpr int PRE_OFF = M_OFF + kPtRows * 4;
+    static constexpr int M_OFF = C_OFF + kPtRows * 4;  // score row of every member: offset * 2 + first, -1 none
+    static constexpr int PRE_OFF = M_OFF + kPtRows * 8;
     static constexpr int smem(int B) { return PRE_OFF + (B + 1) * 4 + 1024; }
 };
 
@@ -488,15 +488,16 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(pt_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);
     uint64_t *empty = full + C::STAGES;
-    uint64_t *q_full = empty + C::STAGES;  // the item's rows and statistics written (every epilogue warp)
-    uint64_t *q_done = q_full + 1;         // the item finished by every epilogue warp
+    uint64_t *q_full = empty + C::STAGES;  // the item's rows written (every epilogue warp)
+    uint64_t *c_full = q_full + 1;         // its statistics and score rows too
+    uint64_t *q_done = c_full + 1;         // the item finished by every epilogue warp
     uint64_t *acc_full = q_done + 1;       // [2]
     uint64_t *acc_empty = acc_full + 2;  // [2]
     uint64_t *drain = acc_empty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     float *cs = reinterpret_cast<float *>(smem + C::C_OFF);
-    int *ms = reinterpret_cast<int *>(smem + C::M_OFF);
+    long long *ms = reinterpret_cast<long long *>(smem + C::M_OFF);
     int *pre = reinterpret_cast<int *>(smem + C::PRE_OFF);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -506,6 +507,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             mbar_init(&empty[i], 1);
         }
         mbar_init(q_full, 8);
+        mbar_init(c_full, 8);
         mbar_init(q_done, 8);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
@@ -595,36 +597,35 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         const float inv_w = 1.f / (float)a.window;
         uint32_t tile = 0, item = 0;
-        bool ok_all = true;
-        pdl_wait();  // the decode's statistics (the other warps read only inputs)
+        bool ok_all = true, waited = false;
         // (every wait is bounded, so a warp that stops cannot leave another waiting for ever)
         for (int w = w0; w < w1 && ok_all; ++item) {
             const PtSeg s = pt_segment(a, pre, ng, w, w1);
-            // the item's rows and statistics: once every warp has finished the last
-            // item (whose products are then complete)
+            // the item's rows: once every warp has finished the last item (whose
+            // products are then complete)
             if (!mbar_wait_bounded(q_done, (item & 1) ^ 1, a.err, abort_flag, 0x618)) break;
-            {
-                const int r = et;
-                int e, mrow = -1;
-                const uint4 *src = pt_query<D>(a, s, head, r, &e);
-                float c = INFINITY;
-                if (e >= 0) {
-                    bool first;
-                    mrow = pfx_score_row(a, e, &first);
-                    if (mrow >= 0) {
-                        const float2 ml = a.stats[(size_t)e * a.h_q + head * G + (s.rt * kPtRows + r) % G];
-                        c = ml.y > 0.f ? ml.x + log2f(ml.y) : INFINITY;
-                        mrow = mrow * 2 + (first ? 1 : 0);
-                    }
-                }
-                cs[r] = c;
-                if (r % G == 0) ms[r / G] = mrow;
-                pt_load_q<D>(src, r & ~31, smem, C::B_HALF);
-            }
+            int e;
+            pt_load_q<D>(pt_query<D>(a, s, head, et, &e), et & ~31, smem, C::B_HALF);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
-            if (!mbar_wait_bounded(q_full, item & 1, a.err, abort_flag, 0x619)) break;
+            bool first = false;
+            const int row = e >= 0 ? pfx_score_row(a, e, &first) : -1;
+            // only the statistics and the score rows wait for the decode: the first
+            // products run while it ends
+            if (!waited) pdl_wait();
+            waited = true;
+            float c = INFINITY;
+            if (row >= 0) {
+                const float2 ml = __ldcg(a.stats + (size_t)e * a.h_q + head * G + (s.rt * kPtRows + et) % G);
+                c = ml.y > 0.f ? ml.x + log2f(ml.y) : INFINITY;
+            }
+            cs[et] = c;
+            if (et % G == 0)
+                ms[et / G] = row >= 0 ? ((long long)row * a.h_kv + head) * a.score_stride * 2 + (first ? 1 : 0) : -1;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(c_full);
+            if (!mbar_wait_bounded(c_full, item & 1, a.err, abort_flag, 0x619)) break;
             for (int t = s.t_b; t < s.t_e; ++t, ++tile) {
                 const uint32_t ab = tile & 1;
                 if (!mbar_wait_bounded(&acc_full[ab], (tile >> 1) & 1, a.err, abort_flag, 0x616)) {
@@ -635,24 +636,32 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 const int tok = t * kPtTile + 32 * quarter + lane;
                 const uint32_t acc = tmem + ((uint32_t)(32 * quarter) << 16) + ab * 256 + half * 128;
                 const bool live = tok < s.g.tokens;
+                float *col = a.score + tok;
 #pragma unroll 1
                 for (int c0 = 0; c0 < 128; c0 += 32) {
                     if (half * 128 + c0 >= s.rows) break;
                     uint32_t v[32];
                     tmem_ld32(acc + c0, v);
+                    const float *cc = cs + half * 128 + c0;
+                    float val[32 / G];
 #pragma unroll
                     for (int i = 0; i < 32 / G; ++i) {
-                        const int mi = (half * 128 + c0) / G + i;
-                        const int mr = ms[mi];
-                        float e = -INFINITY;
+                        float x[G];
 #pragma unroll
-                        for (int j = 0; j < G; ++j)
-                            e = fmaxf(e, fmaf(__uint_as_float(v[i * G + j]), a.qscale, -cs[half * 128 + c0 + i * G + j]));
-                        if (mr >= 0 && live) {
-                            float *dst = a.score + ((size_t)(mr >> 1) * a.h_kv + head) * a.score_stride + tok;
-                            const float val = ex2_approx(e) * inv_w;
-                            *dst = (mr & 1) ? val : *dst + val;
-                        }
+                        for (int j = 0; j < G; ++j) x[j] = fmaf(__uint_as_float(v[i * G + j]), a.qscale, -cc[i * G + j]);
+#pragma unroll
+                        for (int o = 1; o < G; o <<= 1)
+#pragma unroll
+                            for (int j = 0; j < G; j += 2 * o) x[j] = fmaxf(x[j], x[j + o]);
+                        val[i] = ex2_approx(x[0]) * inv_w;
+                    }
+                    const long long *mm = ms + (half * 128 + c0) / G;
+#pragma unroll
+                    for (int i = 0; i < 32 / G; ++i) {
+                        const long long mr = mm[i];
+                        if (mr < 0 || !live) continue;
+                        float *dst = col + (mr >> 1);
+                        *dst = (mr & 1) ? val[i] : *dst + val[i];
                     }
                 }
                 tc_fence_before();
@@ -663,6 +672,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             if (lane == 0) mbar_arrive(q_done);
             w += s.t_e - s.t_b;
         }
+        if (!waited) pdl_wait();
     }
     __syncthreads();
     tc_fence_before();

@@ -9,13 +9,14 @@
 //
 // One launch: every CTA scans the lengths of all sequences (B <= 4096, 32 KB)
 // into shared memory, takes an equal contiguous share of the touched columns,
-// counts the missing entries before its share (the table entries of touched
-// columns only: B of them in a decode step, new tokens / b in a prefill) and
-// then deals blocks and writes slots for its own columns, whose tokens are
-// contiguous in the output.  Latency bound: the redundant scan costs less than
-// a second launch.  In place (table_out = block_table) one cluster of CTAs
-// does the same with a cluster barrier between counting and writing, since the
-// counts read entries that other CTAs write.
+// needs the number of missing entries before its share, and then deals blocks
+// and writes slots for its own columns, whose tokens are contiguous in the
+// output.  A CTA counts what lies before it from the table entries of the touched
+// columns (B of them in a decode step, new tokens / b in a prefill).  Beyond a few
+// entries per thread a cluster of 8 CTAs counts together and exchanges the counts
+// in distributed shared memory.  Latency bound: the redundant scan and count cost
+// less than a second launch.  In place (table_out = block_table) there is one
+// cluster, since the counts read entries that other clusters would write.
 #include <cooperative_groups.h>
 
 #include "zp_common.cuh"
@@ -25,7 +26,7 @@ namespace {
 
 constexpr int kSlotThreads = 512;
 constexpr int kSlotMaxB = 4096;
-constexpr int kSlotCluster = 8;  // CTAs of the in-place form
+constexpr int kSlotCluster = 8;  // CTAs of a cluster
 
 struct SlotArgs {
     const int32_t *table;
@@ -78,24 +79,30 @@ __device__ __forceinline__ int2 slot_lens(const SlotArgs &a, int s, bool record)
     return make_int2(o, n);
 }
 
-// last s in [0, B) with start[s] <= x
-__device__ __forceinline__ int find_seq(const int *start, int B, int x) {
-    int lo = 0, hi = B - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (start[mid] <= x) lo = mid;
-        else hi = mid - 1;
+// last s in [0, B) with start[s] <= x[k], for N values at once (their loads
+// overlap); top: the largest power of two below B (0 for one sequence)
+template <int N>
+__device__ __forceinline__ void find_seq(const int *start, int B, int top, const int (&x)[N], int (&s)[N]) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) s[k] = 0;
+    for (int step = top; step; step >>= 1) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int t = s[k] + step;
+            if (t < B && start[t] <= x[k]) s[k] = t;
+        }
     }
-    return lo;
 }
 
-template <bool kInPlace>
+template <bool kCluster>
 __global__ void __launch_bounds__(kSlotThreads) build_slots_kernel(const SlotArgs a) {
     extern __shared__ int slot_smem[];
     int *ccol = slot_smem;              // [B+1] touched columns before s
     int *ctok = ccol + a.B + 1;         // [B+1] new tokens before s
-    int *old_s = ctok + a.B + 1;        // [B]
+    int *old_s = ctok + a.B + 1;        // [B] old length
+    int *col_s = old_s + a.B;           // [B] first touched column * 2 + (it holds old tokens: never missing)
     __shared__ int warp_sums[kSlotThreads / 32];
+    __shared__ int counts[2];  // missing entries this CTA counted before its cluster, and in its own share
     __shared__ int blk_s[kSlotThreads], tok_s[kSlotThreads], n_s[kSlotThreads], pos_s[kSlotThreads];
     const int tid = threadIdx.x;
     const bool lead = blockIdx.x == 0;
@@ -108,6 +115,8 @@ __global__ void __launch_bounds__(kSlotThreads) build_slots_kernel(const SlotArg
             t = l.y - l.x;
             c = t ? (l.y + a.b - 1) / a.b - l.x / a.b : 0;
             old_s[s] = l.x;
+            const int c0 = l.x / a.b;
+            col_s[s] = 2 * c0 + (l.x > c0 * a.b ? 1 : 0);
         }
         int ct, tt;
         const int ce = block_scan(c, warp_sums, &ct), te = block_scan(t, warp_sums, &tt);
@@ -128,49 +137,77 @@ __global__ void __launch_bounds__(kSlotThreads) build_slots_kernel(const SlotArg
     const int G = gridDim.x;
     const int x0 = (int)((long long)cols * blockIdx.x / G), x1 = (int)((long long)cols * (blockIdx.x + 1) / G);
 
-    // column c of sequence s is missing: at or beyond ceil(old/b), no block yet
-    auto missing = [&](int s, int c) {
-        return c >= (old_s[s] + a.b - 1) / a.b && a.table[(size_t)s * a.stride + c] < 0;
-    };
-    int before = 0;
+    int top = 1;
+    while (2 * top < a.B) top *= 2;
+    if (a.B < 2) top = 0;
+    // Missing entries (no block yet, and not the column of old tokens) of the
+    // touched columns [xb, xe): those of group `which` of every `every`.
     constexpr int kAhead = 8;  // table entries in flight per thread
-    for (int xb = tid; xb < x0; xb += kAhead * kSlotThreads) {
-        int c[kAhead], e[kAhead], lo[kAhead];
+    auto count = [&](int xb, int xe, int which, int every) {
+        int found = 0;
+        for (int g0 = xb + which * kSlotThreads * kAhead; g0 < xe; g0 += every * kSlotThreads * kAhead) {
+            int e[kAhead];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int x = xb + k * kSlotThreads;
-            e[k] = 0;
-            if (x < x0) {
-                const int s = find_seq(ccol, a.B, x), o = old_s[s];
-                c[k] = o / a.b + (x - ccol[s]);
-                lo[k] = (o + a.b - 1) / a.b;
-                e[k] = a.table[(size_t)s * a.stride + c[k]];
+            for (int k0 = 0; k0 < kAhead; k0 += 2) {  // (two searches at a time; none beyond the range)
+                e[k0] = e[k0 + 1] = 0;
+                if (g0 + k0 * kSlotThreads >= xe) continue;
+                const int x[2] = {g0 + k0 * kSlotThreads + tid, g0 + (k0 + 1) * kSlotThreads + tid};
+                int s[2];
+                find_seq<2>(ccol, a.B, top, x, s);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int i = x[k] - ccol[s[k]], c = col_s[s[k]];
+                    if (x[k] < xe && !(i == 0 && (c & 1))) e[k0 + k] = a.table[(size_t)s[k] * a.stride + (c >> 1) + i];
+                }
             }
-        }
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) before += e[k] < 0 && c[k] >= lo[k] ? 1 : 0;
-    }
-    int mine;
-    block_scan(before, warp_sums, &mine);
-    before = mine;
-    if (kInPlace) {
-        cooperative_groups::this_cluster().sync();
+            for (int k = 0; k < kAhead; ++k) found += e[k] < 0 ? 1 : 0;
+        }
+        return found;
+    };
+    int before;
+    if constexpr (kCluster) {
+        auto cluster = cooperative_groups::this_cluster();
+        const int rank = (int)cluster.block_rank(), c_first = blockIdx.x - rank;
+        const int xc = (int)((long long)cols * c_first / G);  // the cluster's first column
+        int n_before, n_own;
+        block_scan(count(0, xc, rank, kSlotCluster), warp_sums, &n_before);
+        block_scan(count(x0, x1, 0, 1), warp_sums, &n_own);
+        if (tid == 0) {
+            counts[0] = n_before;
+            counts[1] = n_own;
+        }
+        cluster.sync();
+        int n = 0;
+        if (tid < kSlotCluster) {
+            const int *c = cluster.map_shared_rank(counts, tid);
+            n = c[0] + (tid < rank ? c[1] : 0);
+        }
+        block_scan(n, warp_sums, &before);
+        cluster.sync();  // the counts have been read (and, in place, every table entry that the counts need)
     } else {
+        block_scan(count(0, x0, 0, 1), warp_sums, &before);
+    }
+    if (a.table_out != a.table) {
         // copy of the table; the touched columns are written by their owners
-        const long long n_table = (long long)a.B * a.stride;
-        for (long long i = (long long)blockIdx.x * kSlotThreads + tid; i < n_table; i += (long long)G * kSlotThreads) {
-            const int s = (int)(i / a.stride), c = (int)(i - (long long)s * a.stride);
-            const int n_cols = ccol[s + 1] - ccol[s], c0 = old_s[s] / a.b;
+        const int n_table = a.B * a.stride;  // (below 2^31 by the limits)
+        for (int i = blockIdx.x * kSlotThreads + tid; i < n_table; i += G * kSlotThreads) {
+            const int s = i / a.stride, c = i - s * a.stride;
+            const int n_cols = ccol[s + 1] - ccol[s], c0 = col_s[s] >> 1;
             if (n_cols == 0 || c < c0 || c >= c0 + n_cols) a.table_out[i] = a.table[i];
         }
     }
     for (int base = x0; base < x1; base += kSlotThreads) {
         const int x = base + tid;
-        int s = 0, c = 0, miss = 0;
+        int s = 0, c = 0, miss = 0, entry = 0;
         if (x < x1) {
-            s = find_seq(ccol, a.B, x);
-            c = old_s[s] / a.b + (x - ccol[s]);
-            miss = missing(s, c) ? 1 : 0;
+            const int xs[1] = {x};
+            int found[1];
+            find_seq<1>(ccol, a.B, top, xs, found);
+            s = found[0];
+            c = (col_s[s] >> 1) + (x - ccol[s]);
+            entry = a.table[(size_t)s * a.stride + c];
+            miss = entry < 0 && !(x == ccol[s] && (col_s[s] & 1)) ? 1 : 0;
         }
         int total;
         const int rank = before + block_scan(miss, warp_sums, &total);
@@ -182,7 +219,7 @@ __global__ void __launch_bounds__(kSlotThreads) build_slots_kernel(const SlotArg
                 blk = rank < a.n_fresh ? a.fresh[rank] : -1;
                 if (rank >= a.n_fresh) record_error(a.err, ZP_ERR_DEVICE, 0x121);
             } else {
-                blk = a.table[(size_t)s * a.stride + c];
+                blk = entry;
             }
             a.table_out[(size_t)s * a.stride + c] = blk;
             if ((blk < 0 || blk >= a.n_total) && !(miss && rank >= a.n_fresh))
@@ -296,31 +333,28 @@ extern "C" zp_status zp_build_slots(const zp_cache_desc *D, const int32_t *block
     if (rc != ZP_OK) return rc;
     SlotArgs a = {block_table, table_out, table_stride, old_lens, new_lens, B, D->block_size, D->n_total_blocks, fresh,
                   n_fresh, slots, positions, max_tokens, cu_tokens, n_used, dev.error_word};
-    const size_t smem = (size_t)(3 * B + 2) * 4;
+    // the columns that new tokens can touch, at most: per sequence one, and one
+    // per b tokens.  Up to 4096 of them a CTA counts alone (512 sequences, one
+    // token each: 6 us; in clusters 18), beyond that in clusters (16 prompts of 32k
+    // tokens: 17 us; alone 36).
+    const long long most = (long long)B + max_tokens / D->block_size;
+    const bool in_place = table_out == block_table, clusters = in_place || most > 4096;
+    const size_t smem = (size_t)(4 * B + 2) * 4;
+    const auto kernel = clusters ? build_slots_kernel<true> : build_slots_kernel<false>;
+    rc = set_max_dynamic_smem(reinterpret_cast<const void *>(kernel), smem, "build_slots: shared-memory attribute");
+    if (rc != ZP_OK) return rc;
     cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(in_place ? kSlotCluster : (unsigned)align_up(dev.sm_count, kSlotCluster));
     cfg.blockDim = dim3(kSlotThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
-    cudaError_t e;
-    if (table_out == block_table) {
-        rc = set_max_dynamic_smem(reinterpret_cast<const void *>(build_slots_kernel<true>), smem,
-                                  "build_slots: shared-memory attribute");
-        if (rc != ZP_OK) return rc;
-        cfg.gridDim = dim3(kSlotCluster);
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = kSlotCluster;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, build_slots_kernel<true>, a);
-    } else {
-        rc = set_max_dynamic_smem(reinterpret_cast<const void *>(build_slots_kernel<false>), smem,
-                                  "build_slots: shared-memory attribute");
-        if (rc != ZP_OK) return rc;
-        cfg.gridDim = dim3(dev.sm_count);
-        e = cudaLaunchKernelEx(&cfg, build_slots_kernel<false>, a);
-    }
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kSlotCluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = clusters ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
     if (e != cudaSuccess) return cuda_fail(e, "build_slots: launch");
     return ok();
 }

@@ -287,7 +287,8 @@ typedef struct zp_prefix_groups {
  * p < min_blocks or fewer than min_members entries have it.  Groups are ordered
  * by their lowest entry.  The plan holds while its members' leading table
  * entries stay (sequences may grow); the call writes all of its arrays.
- * Limits: B <= 4096, min_blocks >= 1, min_members >= 2. */
+ * Limits: B <= 4096, table_stride < 2^20 (ZP_ERR_SHAPE), min_blocks >= 1,
+ * min_members >= 2. */
 zp_status zp_prefix_plan(const zp_cache_desc *D, const int32_t *block_table, int32_t table_stride,
                          const int32_t *seq_lens, int32_t B, int32_t min_blocks, int32_t min_members,
                          const zp_prefix_groups *plan, void *stream);

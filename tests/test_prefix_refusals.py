@@ -62,7 +62,7 @@ def test_prefix_plan(zp):
     for kw in (dict(B=-1), dict(stride=0), dict(mb=0), dict(mm=1), dict(table=None), dict(lens=None),
                *(dict(plan=_groups(zp, **{k: None})) for k in ("prefix_lens", "n_groups", "group_start", "members", "group_blocks"))):
         assert call(**kw) == 1, kw
-    assert call(B=4097) == 2 and call(stride=1 << 21) == 2
+    assert call(B=4097) == 2 and call(stride=1 << 20) == 2
 
 
 def test_prefix_decode(zp):
