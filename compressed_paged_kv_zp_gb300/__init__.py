@@ -21,6 +21,7 @@ LIB_PATH = os.path.join(_HERE, "libzp.so")
 ZP_BF16 = 0
 ZP_F32 = 1
 _DTYPES = {torch.bfloat16: ZP_BF16, torch.float32: ZP_F32}
+_TORCH = {code: t for t, code in _DTYPES.items()}
 
 STATUS = {0: "ZP_OK", 1: "ZP_ERR_INVALID_ARG", 2: "ZP_ERR_SHAPE", 3: "ZP_ERR_DTYPE",
           4: "ZP_ERR_CAPACITY", 5: "ZP_ERR_CUDA", 6: "ZP_ERR_TIMEOUT", 7: "ZP_ERR_DEVICE"}
@@ -304,15 +305,11 @@ def _table(block_table):
     return block_table.shape
 
 
-def _like_cache(desc, t, name: str):
-    if _DTYPES.get(t.dtype) != desc.dtype:
-        raise ValueError("%s is %s, not the cache's type" % (name, t.dtype))
-
-
-def _cache(desc, t, name: str):
-    _like_cache(desc, t, name)
-    if t.shape[-4:] != (desc.n_total_blocks, desc.block_size, desc.h_kv, desc.head_dim):
-        raise ValueError("%s must be [N_total][b][h_kv][d] (or one of these per layer), is %s" % (name, tuple(t.shape)))
+def _check_cache(desc, k_cache, v_cache, layers=1) -> None:
+    n = layers * desc.n_total_blocks * desc.block_size * desc.h_kv * desc.head_dim
+    if k_cache.numel() != n or v_cache.numel() != n:
+        raise ValueError("k_cache and v_cache must be [N_total][b][h_kv][d] (or one of these per layer), are %s and %s"
+                         % (tuple(k_cache.shape), tuple(v_cache.shape)))
 
 
 def zp_build_slots(desc, block_table, old_lens, new_lens, slots, cu_tokens, fresh=None, table_out=None, positions=None,
@@ -345,20 +342,17 @@ def zp_write_kv(desc, k_new, v_new, slots, k_cache, v_cache, stream=None) -> Non
     several = k_cache.dim() == 5
     layers = k_cache.shape[0] if several else 1
     shape = (layers, n, h_kv, d) if several else (n, h_kv, d)
-    dev = _device()
-    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
-        _like_cache(desc, t, name)
-        if t.shape != shape:
-            raise ValueError("%s must be %s, is %s" % (name, shape, tuple(t.shape)))
-        if t.get_device() != dev:
-            raise ValueError("%s must be a CUDA tensor on the current device, is on %s" % (name, t.device))
+    dev, dt = _device(), _TORCH.get(desc.dtype)
+    if k_new.shape != shape or v_new.shape != shape:
+        raise ValueError("k_new and v_new must be %s, are %s and %s" % (shape, tuple(k_new.shape), tuple(v_new.shape)))
+    if not (k_new.dtype is v_new.dtype is k_cache.dtype is v_cache.dtype is dt):
+        raise ValueError("k_new, v_new, k_cache and v_cache must have the cache's type")
+    if k_new.get_device() != dev or v_new.get_device() != dev:
+        raise ValueError("k_new and v_new must be CUDA tensors on the current device")
     strides = k_new.stride()
     if n and (strides[-2:] != (d, 1) or v_new.stride() != strides):
         raise ValueError("the row [h_kv][d] of a token must be contiguous, and k_new and v_new must have the same strides")
-    _cache(desc, k_cache, "k_cache")
-    _cache(desc, v_cache, "v_cache")
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must have the same shape")
+    _check_cache(desc, k_cache, v_cache, layers)
     if n == 0:
         return
     rc = lib.zp_write_kv(desc, k_new.data_ptr(), v_new.data_ptr(), strides[-3] if n > 1 else max(strides[-3], h_kv * d),
@@ -418,13 +412,12 @@ def zp_prefix_decode_attn(desc, q, k_cache, v_cache, block_table, seq_lens, plan
     if plan.B != B:
         raise ValueError("the plan is for %d batch entries, the table has %d" % (plan.B, B))
     dev = _device()
-    shape = (B, desc.h_q, desc.head_dim)
-    for t, name in ((q, "q"), (out, "out")):
-        _like_cache(desc, t, name)
-        if t.shape != shape:
-            raise ValueError("%s must be [B][h_q][d] = %s, is %s" % (name, shape, tuple(t.shape)))
-    _cache(desc, k_cache, "k_cache")
-    _cache(desc, v_cache, "v_cache")
+    shape, dt = (B, desc.h_q, desc.head_dim), _TORCH.get(desc.dtype)
+    if q.shape != shape or out.shape != shape:
+        raise ValueError("q and out must be [B][h_q][d] = %s, are %s and %s" % (shape, tuple(q.shape), tuple(out.shape)))
+    if not (q.dtype is out.dtype is k_cache.dtype is v_cache.dtype is dt):
+        raise ValueError("q, out, k_cache and v_cache must have the cache's type")
+    _check_cache(desc, k_cache, v_cache)
     n_rows = 0
     if score_accum is not None:
         n_rows = score_accum.shape[0]
@@ -434,8 +427,7 @@ def zp_prefix_decode_attn(desc, q, k_cache, v_cache, block_table, seq_lens, plan
     elif score_rows is not None:
         raise ValueError("score_rows needs score_accum")
     if workspace is None:
-        workspace = torch.empty(zp_prefix_decode_workspace_size(desc, B, table_stride), dtype=torch.uint8,
-                                device=q.device)
+        workspace = q.new_empty(zp_prefix_decode_workspace_size(desc, B, table_stride), dtype=torch.uint8)
         if stream is not None:
             workspace.record_stream(stream)  # not reused before this call's work on that stream
     rc = lib.zp_prefix_decode_attn(desc, _ptr_on(q, dev, "q"), _ptr_on(k_cache, dev, "k_cache"),

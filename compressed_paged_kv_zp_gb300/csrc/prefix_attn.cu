@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_part_kernel(const PfxArgs 
             const int r = r0 + ty * 4 + i;
             if (r < g.n * G) {
                 const long long at = t_b == 0 ? pfx_main_row(a, g, head, r)
-                                              : a.extra0 + (long long)blockIdx.x * a.rt + ty * 4 + i;
+                                              : a.extra0 + (long long)blockIdx.x * kPfxRows + ty * 4 + i;
                 if (tx == 0) a.rec_ml[at] = make_float2(m[i], l[i]);
 #pragma unroll
                 for (int dv = 0; dv < DV; ++dv)
@@ -448,14 +448,11 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_score_kernel(const PfxArgs
                 }
                 if constexpr (G >= 4) e[0] = fmaxf(e[0], e[2]);
                 if constexpr (G == 8) e[0] = fmaxf(e[0], __shfl_xor_sync(0xFFFFFFFFu, e[0], 16));
-                if (tok < g.tokens) {
 #pragma unroll
-                    for (int i = 0; i < 4; i += (G >= 4 ? 4 : G)) {
-                        if (srow[i] < 0 || (G == 8 && (ty & 1))) continue;
-                        float *dst = a.score + ((size_t)srow[i] * a.h_kv + head) * a.score_stride + tok;
-                        const float val = exp2f(e[i]) * inv_w;
-                        *dst = first[i] ? val : *dst + val;
-                    }
+                for (int i = 0; i < 4; i += (G >= 4 ? 4 : G)) {
+                    const bool on = tok < g.tokens && srow[i] >= 0 && !(G == 8 && (ty & 1));
+                    float *dst = a.score + ((size_t)max(srow[i], 0) * a.h_kv + head) * a.score_stride + tok;
+                    st_if(dst, exp2f(e[i]) * inv_w + ld_if(dst, on && !first[i]), on);
                 }
             }
         }
@@ -621,14 +618,17 @@ extern "C" zp_status zp_prefix_decode_attn(const zp_cache_desc *D, const void *q
     a.h_q = D->h_q;
     a.h_kv = D->h_kv;
     a.b = D->block_size;
+    a.b_log = __builtin_ctz((unsigned)D->block_size);  // (a power of two: the decode's plan checked it)
+    a.G = G;
+    a.G_log = __builtin_ctz((unsigned)G);
     a.n_total = D->n_total_blocks;
     a.prefix = plan->prefix_lens;
     a.n_groups = plan->n_groups;
     a.group_start = plan->group_start;
     a.members = plan->members;
     a.group_blocks = plan->group_blocks;
-    a.rt = p.rt;
-    a.kt = p.kt;
+    a.rt_log = __builtin_ctz((unsigned)p.rt);
+    a.kt_log = __builtin_ctz((unsigned)p.kt);
     a.parts = p.parts;
     a.extra0 = p.extra0;
     a.tc = p.tc;

@@ -14,10 +14,12 @@ struct PfxArgs {
     const int32_t *table;
     int stride;
     const int32_t *seq_lens;
-    int B, h_q, h_kv, b, n_total;
+    int B, h_q, h_kv, n_total;
+    int b, b_log;        // tokens per block, a power of two
+    int G, G_log;        // q heads per kv head, a power of two
     // the plan
     const int32_t *prefix, *n_groups, *group_start, *members, *group_blocks;
-    int rt, kt;          // rows per item, tokens per tile
+    int rt_log, kt_log;  // rows per item, tokens per tile (powers of two)
     int parts;           // sets of CTAs (split of the tiles); a set has a CTA per kv head
     float qscale;        // log2(e) / sqrt(d)
     int *wpre;           // [B+1] tiles before each group
@@ -50,9 +52,9 @@ __device__ __forceinline__ PfxGroup pfx_group(const PfxArgs &a, int g) {
     PfxGroup r;
     r.m0 = min(max(__ldg(a.group_start + g), 0), a.B);
     r.n = min(max(__ldg(a.group_start + g + 1), r.m0), a.B) - r.m0;
-    r.tokens = min(max(__ldg(a.group_blocks + g), 0), a.stride) * a.b;
-    r.rts = (r.n * (a.h_q / a.h_kv) + a.rt - 1) / a.rt;
-    r.kts = (r.tokens + a.kt - 1) / a.kt;
+    r.tokens = min(max(__ldg(a.group_blocks + g), 0), a.stride) << a.b_log;
+    r.rts = ((r.n << a.G_log) + (1 << a.rt_log) - 1) >> a.rt_log;
+    r.kts = (r.tokens + (1 << a.kt_log) - 1) >> a.kt_log;
     return r;
 }
 
@@ -127,18 +129,18 @@ inline __device__ int pfx_scan(const PfxArgs &a, int ng, int *pre) {
 // Row of the main records: rows of a group are (kv head, member, q head of the
 // group), after the rows of the members before it.
 __device__ __forceinline__ long long pfx_main_row(const PfxArgs &a, const PfxGroup &g, int head, int r) {
-    return (long long)g.m0 * a.h_q + (long long)head * g.n * (a.h_q / a.h_kv) + r;
+    return (long long)g.m0 * a.h_q + (long long)head * (g.n << a.G_log) + r;
 }
 
 // Physical row (block * b + slot) of token t of the group's prefix, by its first
 // member's table row; -1 for a bad block id (recorded).
 __device__ __forceinline__ long long pfx_slot(const PfxArgs &a, const int32_t *row, int t) {
-    const int blk = __ldg(row + t / a.b);
+    const int blk = __ldg(row + (t >> a.b_log));
     if (blk < 0 || blk >= a.n_total) {
         record_error(a.err, ZP_ERR_DEVICE, 0x143);
         return -1;
     }
-    return (long long)blk * a.b + t % a.b;
+    return ((long long)blk << a.b_log) + (t & (a.b - 1));
 }
 
 // The table row every member's prefix agrees with: the first member's.
@@ -153,8 +155,8 @@ __device__ __forceinline__ int pfx_score_row(const PfxArgs &a, int s, bool *firs
     const int L = min(__ldg(a.seq_lens + s), a.stride * a.b);
     const int p = __ldg(a.prefix + s);
     *first = false;
-    if (p <= 0 || p >= L || p % a.b) return -1;
-    const int ph = (L - 1) % a.b;
+    if (p <= 0 || p >= L || (p & (a.b - 1))) return -1;
+    const int ph = (L - 1) & (a.b - 1);
     if (ph < a.b - a.window) return -1;
     *first = ph == a.b - a.window;
     if (!a.score_rows) return s;
@@ -174,17 +176,16 @@ struct PfxPieces {
 __device__ __forceinline__ PfxPieces pfx_pieces(const PfxArgs &a, const PfxGroup &g, int mi, int head, int before, int W) {
     PfxPieces p = {};
     if (mi < g.m0 || mi >= g.m0 + g.n || g.tokens == 0) return p;
-    const int G = a.h_q / a.h_kv;
-    const int r = (mi - g.m0) * G, row = r % a.rt;
+    const int rt = 1 << a.rt_log, r = (mi - g.m0) << a.G_log, row = r & (rt - 1);
     p.W = W;
-    p.i0 = before + r / a.rt * g.kts;
+    p.i0 = before + (r >> a.rt_log) * g.kts;
     p.c0 = pfx_owner(p.i0, W, a.parts);
     // consecutive sets when each has a tile, one tile each otherwise
     p.n = W >= a.parts ? pfx_owner(p.i0 + g.kts - 1, W, a.parts) - p.c0 + 1 : g.kts;
-    p.two = a.tc && min(a.rt, g.n * G - (r - row)) <= a.rt / 2 ? 2 : 1;  // at most 128 rows: a record per stream
+    p.two = a.tc && min(rt, (g.n << a.G_log) - (r - row)) <= rt / 2 ? 2 : 1;  // at most 128 rows: a record per stream
     p.main = pfx_main_row(a, g, head, r);
     p.main2 = p.main + (long long)a.B * a.h_q;
-    p.extra = a.extra0 + (long long)head * a.rt + row;
+    p.extra = a.extra0 + ((long long)head << a.rt_log) + row;
     return p;
 }
 
@@ -193,7 +194,7 @@ __device__ __forceinline__ long long pfx_record(const PfxArgs &a, const PfxPiece
     const int j = i / p.two, x = i - j * p.two;
     if (j == 0) return x ? p.main2 : p.main;
     const int c = p.W >= a.parts ? p.c0 + j : pfx_owner(p.i0 + j, p.W, a.parts);
-    return p.extra + (long long)c * a.h_kv * a.rt + x * (a.rt / 2);
+    return p.extra + (((long long)c * a.h_kv) << a.rt_log) + (x << (a.rt_log - 1));
 }
 
 }  // namespace zp

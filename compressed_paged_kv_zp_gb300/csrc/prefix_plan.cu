@@ -63,11 +63,11 @@ struct PlanSmem {
     };
     int leader[kPlanMaxB];               // leader of each sequence, -1 = no class
     int lcp[kPlanMaxB];
-    int aux[kPlanMaxB];                  // members with at least this lcp, then the rank inside the group
+    alignas(16) int aux[kPlanMaxB];      // members with at least this lcp, then the rank inside the group
     int gid[kPlanMaxB];                  // by leader: lowest member, then group number
     int size[kPlanMaxB];                 // by leader: members
     int full[kPlanMaxB];                 // blocks before the newest token's
-    unsigned char member[kPlanMaxB];
+    alignas(4) unsigned char member[kPlanMaxB];
     int warp_sums[32];
     int total;
 };
@@ -109,10 +109,13 @@ __device__ __forceinline__ int plan_full(const PlanArgs &a, int s) {
 constexpr int kWarps = kPlanThreads / 32;
 
 // lcp of sequences [e0, e1) with their leaders, written to every CTA: EACH rows per
-// warp at a time, 64 entries of each, all loads in flight.
+// warp at a time, 128 entries of each, all loads in flight.  Bound by the
+// instructions per entry, so a column beyond the row's limit reads the last one
+// again instead of being tested, and a chunk is searched only if it differs.
 template <int EACH>
 __device__ __forceinline__ void plan_lcp(const PlanArgs &a, PlanSmem &sm, cooperative_groups::cluster_group &cluster, int e0,
                                          int e1) {
+    constexpr int Q = 4;  // columns per lane and chunk
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int s0 = e0 + warp * EACH; s0 < e1; s0 += kWarps * EACH) {
         int n[EACH], far = 0;
@@ -125,27 +128,33 @@ __device__ __forceinline__ void plan_lcp(const PlanArgs &a, PlanSmem &sm, cooper
             r0[i] = a.table + (size_t)(ld >= 0 ? s : 0) * a.stride;
             r1[i] = a.table + (size_t)(ld >= 0 ? ld : 0) * a.stride;
         }
-        for (int c0 = 0; c0 < far; c0 += 64) {
-            int x[EACH][2], y[EACH][2];
+        for (int c0 = 0; c0 < far; c0 += 32 * Q) {
+            int x[EACH][Q], y[EACH][Q];
 #pragma unroll
             for (int i = 0; i < EACH; ++i)
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int c = c0 + 32 * q + lane;
-                    const bool in = c < n[i];  // (a row that has differed reads no further)
-                    x[i][q] = in ? r0[i][c] : 0;
-                    y[i][q] = in ? r1[i][c] : 0;
+                for (int q = 0; q < Q; ++q) {
+                    const int c = max(min(c0 + 32 * q + lane, n[i] - 1), 0);
+                    x[i][q] = r0[i][c];
+                    y[i][q] = r1[i][c];
                 }
             far = 0;
 #pragma unroll
             for (int i = 0; i < EACH; ++i) {
+                bool bad[Q], any = false;
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const unsigned bad =
-                        __ballot_sync(0xFFFFFFFFu, !(x[i][q] == y[i][q] && x[i][q] >= 0 && x[i][q] < a.n_total));
-                    if (bad) n[i] = min(n[i], c0 + 32 * q + __ffs(bad) - 1);
+                for (int q = 0; q < Q; ++q) {
+                    bad[q] = x[i][q] != y[i][q] || (unsigned)x[i][q] >= (unsigned)a.n_total;
+                    any |= bad[q];
                 }
-                far = max(far, n[i]);
+                if (c0 < n[i] && __any_sync(0xFFFFFFFFu, any)) {
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) {
+                        const unsigned m = __ballot_sync(0xFFFFFFFFu, bad[q]);
+                        if (m) n[i] = min(n[i], c0 + 32 * q + __ffs(m) - 1);
+                    }
+                }
+                if (n[i] > c0 + 32 * Q) far = max(far, n[i]);  // (a row that has differed reads no further)
             }
         }
         if (lane < kPlanCluster) {
@@ -205,8 +214,7 @@ __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanThre
     // is compared at the same time (their loads overlap)
     const int per_warp = (e1 - e0 + kWarps - 1) / kWarps;
     if (per_warp <= 1) plan_lcp<1>(a, sm, cluster, e0, e1);
-    else if (per_warp <= 4) plan_lcp<4>(a, sm, cluster, e0, e1);
-    else plan_lcp<8>(a, sm, cluster, e0, e1);
+    else plan_lcp<4>(a, sm, cluster, e0, e1);
     for (int s = tid; s < B; s += kPlanThreads) sm.cls_n[s] = 0;  // (the hash is no longer needed)
     cluster.sync();
     // the classes one after another, so that a sequence is compared with its own
@@ -273,23 +281,23 @@ __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanThre
             sm.member[s] = in ? 1 : 0;
         }
         __syncthreads();
-        // group numbers by lowest member; starts by a scan of the sizes
+        // group numbers by lowest member, starts by the sizes: both in one scan
         int groups = 0, members = 0;
         for (int base = 0; base < B; base += kPlanThreads) {
             const int s = base + tid;
             const int ld = s < B ? sm.leader[s] : -1;
             const bool head = s < B && sm.member[s] && sm.gid[ld] == s;
-            const int g = groups + plan_scan(head ? 1 : 0, sm);
-            groups += sm.total;
-            __syncthreads();
-            const int at = members + plan_scan(head ? sm.size[ld] : 0, sm);
-            members += sm.total;
-            __syncthreads();
+            const int at = plan_scan(head ? (1 << 16) + sm.size[ld] : 0, sm);  // (at most 4096 members)
+            const int total = sm.total;
             if (head) {
-                a.group_start[g] = at;
+                const int g = groups + (at >> 16);
+                a.group_start[g] = members + (at & 0xFFFF);
                 a.group_blocks[g] = sm.shared[ld];
-                sm.aux[ld] = at;  // the class's first place (the counts are no longer needed)
+                sm.aux[ld] = members + (at & 0xFFFF);  // the class's first place (the counts are no longer needed)
             }
+            groups += total >> 16;
+            members += total & 0xFFFF;
+            __syncthreads();
         }
         if (tid == 0) *a.n_groups = groups;
         for (int i = groups + tid; i <= B; i += kPlanThreads) a.group_start[i] = members;
@@ -299,10 +307,14 @@ __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanThre
     }
     cluster.sync();  // the first CTA's member flags and places
     // rank of each member inside its group: same leader, lower index
-    const PlanSmem *first = cluster.map_shared_rank(&sm, 0);
     if (rank != 0) {
-        for (int s = tid * 4; s < B; s += kPlanThreads * 4)
-            *reinterpret_cast<unsigned *>(sm.member + s) = *reinterpret_cast<const unsigned *>(first->member + s);
+        const PlanSmem *first = cluster.map_shared_rank(&sm, 0);
+        for (int s = tid * 4; s < B; s += kPlanThreads * 4) {
+            const unsigned m = *reinterpret_cast<const unsigned *>(first->member + s);
+            const int4 p = *reinterpret_cast<const int4 *>(first->aux + s);
+            *reinterpret_cast<unsigned *>(sm.member + s) = m;
+            *reinterpret_cast<int4 *>(sm.aux + s) = p;
+        }
         __syncthreads();
     }
     for (int s = e0 + warp; s < e1; s += kWarps) {
@@ -314,7 +326,7 @@ __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanThre
             r += o < s && sm.member[o] ? 1 : 0;
         }
         r = __reduce_add_sync(0xFFFFFFFFu, r);
-        if (lane == 0) a.members[first->aux[ld] + r] = s;
+        if (lane == 0) a.members[sm.aux[ld] + r] = s;
     }
     cluster.sync();  // the first CTA's shared memory outlives the others' reads
 }

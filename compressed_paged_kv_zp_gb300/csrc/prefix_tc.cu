@@ -105,11 +105,11 @@ __device__ __forceinline__ PtSeg pt_segment(const PfxArgs &a, const int *pre, in
     PtSeg s;
     const int gi = pfx_find(pre, ng, w);
     s.g = pfx_group(a, gi);
-    const int x = w - pre[gi], item = x / s.g.kts;
+    const int x = w - pre[gi], item = (int)((unsigned)x / (unsigned)s.g.kts);
     s.rt = item;
     s.t_b = x - item * s.g.kts;
     s.t_e = min(s.g.kts, s.t_b + (w1 - w));
-    s.rows = min(kPtRows, s.g.n * (a.h_q / a.h_kv) - s.rt * kPtRows);
+    s.rows = min(kPtRows, (s.g.n << a.G_log) - s.rt * kPtRows);
     s.split = s.rows <= kPtRows / 2;
     return s;
 }
@@ -131,11 +131,11 @@ __device__ __forceinline__ int pt_rows16(const PfxArgs &a, const PfxGroup &g, co
 // Address of row r of the item's queries, nullptr beyond the last row.
 template <int D>
 __device__ __forceinline__ const uint4 *pt_query(const PfxArgs &a, const PtSeg &s, int head, int r, int *entry) {
-    const int G = a.h_q / a.h_kv, rr = s.rt * kPtRows + r;
-    *entry = r < s.rows ? pfx_member(a, s.g.m0 + rr / G) : -1;
+    const int rr = s.rt * kPtRows + r;
+    *entry = r < s.rows ? pfx_member(a, s.g.m0 + (rr >> a.G_log)) : -1;
     if (*entry < 0) return nullptr;
     return reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
-                                           ((size_t)*entry * a.h_q + head * G + rr % G) * D);
+                                           ((size_t)*entry * a.h_q + (head << a.G_log) + (rr & (a.G - 1))) * D);
 }
 
 // The warp's 32 query rows (lane i holds the address of row row0 + i of the
@@ -655,14 +655,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                             for (int j = 0; j < G; j += 2 * o) x[j] = fmaxf(x[j], x[j + o]);
                         val[i] = ex2_approx(x[0]) * inv_w;
                     }
+                    // (the old scores' loads, where there are any, are in flight together)
                     const long long *mm = ms + (half * 128 + c0) / G;
 #pragma unroll
-                    for (int i = 0; i < 32 / G; ++i) {
-                        const long long mr = mm[i];
-                        if (mr < 0 || !live) continue;
-                        float *dst = col + (mr >> 1);
-                        *dst = (mr & 1) ? val[i] : *dst + val[i];
-                    }
+                    for (int i = 0; i < 32 / G; ++i)
+                        val[i] += ld_if(col + (mm[i] >> 1), live && mm[i] >= 0 && !(mm[i] & 1));
+#pragma unroll
+                    for (int i = 0; i < 32 / G; ++i) st_if(col + (mm[i] >> 1), val[i], live && mm[i] >= 0);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -727,7 +726,7 @@ zp_status prefix_part_tc(const PfxArgs &a, int d, cudaStream_t st) {
 }
 
 zp_status prefix_score_tc(const PfxArgs &a, int d, cudaStream_t st) {
-    const int G = a.h_q / a.h_kv;
+    const int G = a.G;
     if (d == 64) {
         if (G == 1) return launch_score_tc<64, 1>(a, st);
         if (G == 2) return launch_score_tc<64, 2>(a, st);

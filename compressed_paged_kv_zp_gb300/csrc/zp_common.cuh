@@ -69,6 +69,24 @@ __device__ __forceinline__ float ex2_approx(float x) {
     return y;
 }
 
+// ---------------------------------------------------------------- predicated access
+// A float where `on`, else 0; and the store.  (A plain "written ? v : *p + v" is
+// compiled into a load in either case.)
+__device__ __forceinline__ float ld_if(const float *p, bool on) {
+    float v;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\tmov.f32 %0, 0f00000000;\n\t@q ld.global.f32 %0, [%1];\n\t}"
+        : "=&f"(v)
+        : "l"(p), "r"((int)on)
+        : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_if(float *p, float v, bool on) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q st.global.f32 [%0], %1;\n\t}" ::"l"(p), "f"(v),
+                 "r"((int)on)
+                 : "memory");
+}
+
 // ---------------------------------------------------------------- mbarrier
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
