@@ -642,26 +642,30 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     if (half * 128 + c0 >= s.rows) break;
                     uint32_t v[32];
                     tmem_ld32(acc + c0, v);
-                    const float *cc = cs + half * 128 + c0;
-                    float val[32 / G];
+                    // statistics and score rows first, then the old scores where there are
+                    // any: the loads of a chunk are in flight together
+                    constexpr int N = 32 / G;
+                    float c[32];
 #pragma unroll
-                    for (int i = 0; i < 32 / G; ++i) {
+                    for (int j = 0; j < 8; ++j)
+                        *reinterpret_cast<float4 *>(c + 4 * j) = reinterpret_cast<const float4 *>(cs + half * 128 + c0)[j];
+                    long long mr[N];
+#pragma unroll
+                    for (int i = 0; i < N; ++i) mr[i] = ms[(half * 128 + c0) / G + i];
+                    float old[N];
+#pragma unroll
+                    for (int i = 0; i < N; ++i) old[i] = ld_if(col + (mr[i] >> 1), live && mr[i] >= 0 && !(mr[i] & 1));
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
                         float x[G];
 #pragma unroll
-                        for (int j = 0; j < G; ++j) x[j] = fmaf(__uint_as_float(v[i * G + j]), a.qscale, -cc[i * G + j]);
+                        for (int j = 0; j < G; ++j) x[j] = fmaf(__uint_as_float(v[i * G + j]), a.qscale, -c[i * G + j]);
 #pragma unroll
                         for (int o = 1; o < G; o <<= 1)
 #pragma unroll
                             for (int j = 0; j < G; j += 2 * o) x[j] = fmaxf(x[j], x[j + o]);
-                        val[i] = ex2_approx(x[0]) * inv_w;
+                        st_if(col + (mr[i] >> 1), fmaf(ex2_approx(x[0]), inv_w, old[i]), live && mr[i] >= 0);
                     }
-                    // (the old scores' loads, where there are any, are in flight together)
-                    const long long *mm = ms + (half * 128 + c0) / G;
-#pragma unroll
-                    for (int i = 0; i < 32 / G; ++i)
-                        val[i] += ld_if(col + (mm[i] >> 1), live && mm[i] >= 0 && !(mm[i] & 1));
-#pragma unroll
-                    for (int i = 0; i < 32 / G; ++i) st_if(col + (mm[i] >> 1), val[i], live && mm[i] >= 0);
                 }
                 tc_fence_before();
                 __syncwarp();
