@@ -17,7 +17,11 @@ The host side of the hot path around the libzp kernels:
     completed, then rejoin with their new block table, while everybody else
     keeps decoding;
   * the blocks a compressed sequence no longer holds go back to the pool only
-    after the compaction that reads them has completed.
+    after the compaction that reads them has completed;
+  * with prefix_decode, sequences whose tables share leading blocks (§4.4) attend
+    to those once per group: the groups are found on the device whenever tables
+    or blocks change, for all layers (the compression then forms the row sums
+    itself).
 All device work is libzp calls; torch provides memory, streams and events.
 """
 from __future__ import annotations
@@ -25,9 +29,9 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (Pool, cache_desc, score_params, zp_append_kv, zp_compress_layers, zp_compress_rho_supported,
+from . import (Pool, cache_desc, prefix_plan, score_params, zp_append_kv, zp_compress_layers, zp_compress_rho_supported,
                zp_compress_workspace_size, zp_needs_compression_batch, zp_decode_workspace_size,
-               zp_paged_decode_attn)
+               zp_paged_decode_attn, zp_prefix_decode_attn, zp_prefix_decode_workspace_size, zp_prefix_plan)
 
 
 def upload(arr: np.ndarray, dev) -> torch.Tensor:
@@ -61,7 +65,7 @@ class DecodeLoop:
 
     def __init__(self, h_q, h_kv, d, b, n_total, max_blocks, table_stride, layers=1, dtype=torch.bfloat16,
                  window=None, params=None, async_compress=False, layer_stride=None, device="cuda",
-                 decode_rho=True):
+                 decode_rho=True, prefix_decode=False, prefix_min_blocks=4):
         self.h_q, self.h_kv, self.d, self.b = h_q, h_kv, d, b
         self.n_total, self.N_max, self.stride, self.layers = n_total, max_blocks, table_stride, layers
         self.k = (max_blocks - 1) * b
@@ -71,7 +75,10 @@ class DecodeLoop:
         self.desc = cache_desc(h_q, h_kv, d, b, n_total, dtype)
         self.params = params or score_params(window=self.window)
         self.async_compress = async_compress
-        self.decode_rho = decode_rho
+        # prefix_decode: groups of at least prefix_min_blocks shared blocks are
+        # attended to once for all their members
+        self.prefix_decode, self.prefix_min_blocks = prefix_decode, prefix_min_blocks
+        self.decode_rho = decode_rho and not prefix_decode
         # layers compressed per call (App. C.1's layer stride): bounds the
         # scoring scratch to layer_stride layers
         self.layer_stride = max(1, min(layer_stride or layers, layers))
@@ -134,8 +141,10 @@ class DecodeLoop:
         # position, so sequences sharing prefix blocks keep their own scores
         self.S = torch.zeros(self.layers, B, self.h_kv, self.stride * self.b, dtype=torch.float32,
                              device=self.dev)
-        self.ws = torch.empty(zp_decode_workspace_size(self.desc, B, self.stride), dtype=torch.uint8,
-                              device=self.dev)
+        ws_size = zp_prefix_decode_workspace_size if self.prefix_decode else zp_decode_workspace_size
+        self.ws = torch.empty(ws_size(self.desc, B, self.stride), dtype=torch.uint8, device=self.dev)
+        self.plan = prefix_plan(B, self.dev) if self.prefix_decode else None
+        self._plan_stale = True
         Lmax = self.stride * self.b
         self.Lmax = Lmax
         self.use_rho = bool(self.decode_rho and zp_compress_rho_supported(self.desc, self.params, Lmax, self.k))
@@ -164,10 +173,14 @@ class DecodeLoop:
             if int(self.lens[need].max()) // self.b >= self.stride:
                 raise RuntimeError("a sequence outgrew table_stride blocks")
             self.table[need, self.lens[need] // self.b] = self.pool.alloc(len(need))
+            self._plan_stale = True
         self.lens[act] += 1
         self.table_dev.copy_(torch.from_numpy(self.table).pin_memory(), non_blocking=True)
         step_lens = upload(np.where(act, self.lens, 0).astype(np.int32), self.dev)
         main = torch.cuda.current_stream(self.dev)
+        if self.prefix_decode and self._plan_stale:
+            zp_prefix_plan(self.desc, self.table_dev, step_lens, self.plan, min_blocks=self.prefix_min_blocks)
+            self._plan_stale = False
         # the sequences that compress after this step: their decode also forms
         # the lightning row sums (row i of rho for the i-th of them)
         trig = zp_needs_compression_batch(self.lens, self.b, self.N_max, active=act, max_blocks_seq=self.N_seq)
@@ -183,6 +196,10 @@ class DecodeLoop:
             extra = dict(rho_rows=buf["rows"], rho_threshold=self.params.threshold)
         for l in range(self.layers):
             zp_append_kv(self.desc, k_new[l], v_new[l], self.K[l], self.V[l], self.table_dev, step_lens)
+            if self.prefix_decode:
+                zp_prefix_decode_attn(self.desc, q[l], self.K[l], self.V[l], self.table_dev, step_lens, self.plan,
+                                      self.out[l], score_accum=self.S[l], window=self.window, workspace=self.ws)
+                continue
             zp_paged_decode_attn(self.desc, q[l], self.K[l], self.V[l], self.table_dev, step_lens, self.out[l],
                                  score_accum=self.S[l], window=self.window, workspace=self.ws,
                                  rho=None if rho is None else rho[l], **extra)
@@ -259,6 +276,7 @@ class DecodeLoop:
                 nd = int(plan["n_dropped"][i])
                 if nd:
                     self.pool.release(plan["dropped"][i, :nd].tolist())
+            self._plan_stale = True
         self.pending = still
 
     def drain(self):

@@ -5,10 +5,15 @@ engine-level throughput -- tokens per second (TPS) and time per output token
 
 Per step the scheduler [§4.3, §4.4] picks either a prefill step (admitted
 requests) or a decode step (the running requests that can go on); then:
-  * prefill: the prompt's keys and values are written into the request's
-    blocks (synthetic values: prefill attention is not part of this path);
+  * prefill: the prompts' slots are built on the device from the request
+    lengths (zp_build_slots) and their keys and values written through them,
+    every layer in one call (zp_write_kv; synthetic values: prefill attention is
+    not part of this path);
   * decode: per layer zp_append_kv + zp_paged_decode_attn, the window score
-    accumulated into the request's query slot (a row of S) [§4.2];
+    accumulated into the request's query slot (a row of S) [§4.2]; with
+    prefix_decode the requests that share prompt blocks [§4.4] are grouped on the
+    device (zp_prefix_plan) and attend to the shared blocks once per group
+    (zp_prefix_decode_attn);
   * compression of the triggered requests on a side stream with
     zp_compress_layers (per-request budgets, slot rows) [§4.1, §4.5, App. C.1];
     a compressing request sits out until its event has completed, then the
@@ -25,16 +30,18 @@ import time
 import numpy as np
 import torch
 
-from . import (cache_desc, score_params, zp_append_kv, zp_compress_layers, zp_compress_workspace_size,
-               zp_decode_workspace_size, zp_paged_decode_attn)
-from .engine import upload
+from . import (PrefixPlan, cache_desc, score_params, zp_append_kv, zp_build_slots, zp_compress_layers,
+               zp_compress_workspace_size, zp_decode_workspace_size, zp_paged_decode_attn, zp_prefix_decode_attn,
+               zp_prefix_decode_workspace_size, zp_prefix_plan, zp_write_kv)
+from .engine import upload, upload_packed
 from .sched import CONSTRAINED, HYBRID, Scheduler
 
 
 class ServeLoop:
     def __init__(self, h_q, h_kv, d, b, n_total, max_blocks, query_slots, table_stride, layers=1,
                  dtype=torch.bfloat16, window=None, params=None, policy=HYBRID, prefix_sharing=False,
-                 max_running=256, max_prefill_tokens=16384, layer_stride=None, seed=0, device="cuda"):
+                 max_running=256, max_prefill_tokens=16384, layer_stride=None, seed=0, device="cuda",
+                 prefix_decode=False, prefix_min_blocks=4):
         self.h_q, self.h_kv, self.d, self.b = h_q, h_kv, d, b
         self.n_total, self.N_max, self.M, self.stride, self.layers = n_total, max_blocks, query_slots, table_stride, layers
         self.window = window or b
@@ -52,8 +59,11 @@ class ServeLoop:
         self.Lmax = table_stride * b
         # one score row per query slot and kv head [§4.2]
         self.S = torch.zeros(layers, query_slots, h_kv, self.Lmax, dtype=torch.float32, device=self.dev)
-        self.ws = torch.empty(zp_decode_workspace_size(self.desc, max_running, table_stride), dtype=torch.uint8,
-                              device=self.dev)
+        self.prefix_decode, self.prefix_min_blocks = prefix_decode, prefix_min_blocks
+        ws_size = zp_prefix_decode_workspace_size if prefix_decode else zp_decode_workspace_size
+        self.ws = torch.empty(ws_size(self.desc, max_running, table_stride), dtype=torch.uint8, device=self.dev)
+        # groups of requests that share prompt blocks, rebuilt every decode step
+        self._plan_buf = torch.zeros(5, max_running + 1, dtype=torch.int32, device=self.dev)
         self.score_ws = torch.empty(
             max(zp_compress_workspace_size(self.desc, min(max_running, query_slots), self.Lmax, self.layer_stride), 1),
             dtype=torch.uint8, device=self.dev)
@@ -79,19 +89,17 @@ class ServeLoop:
         return torch.randn(*shape, generator=self.gen, device=self.dev, dtype=torch.float32).to(self.dtype)
 
     def _prefill(self, st):
-        b = self.b
-        pos, blk = [], []
-        for i in range(len(st["ids"])):
-            p = np.arange(int(st["start"][i]), int(st["lens"][i]))
-            pos.append(p)
-            blk.append(st["tables"][i][p // b] * b + p % b)
-        phys = upload(np.concatenate(blk).astype(np.int64), self.dev)
-        n = int(phys.numel())
+        n = int((st["lens"] - st["start"]).sum())
         if n:
-            kf = self.K.view(self.layers, -1, self.h_kv, self.d)
-            vf = self.V.view(self.layers, -1, self.h_kv, self.d)
-            kf[:, phys] = self._randn(self.layers, n, self.h_kv, self.d)
-            vf[:, phys] = self._randn(self.layers, n, self.h_kv, self.d)
+            # the scheduler has placed every block: the slots of the new tokens
+            table, start, lens = upload_packed([np.ascontiguousarray(st[k], dtype=np.int32)
+                                                for k in ("tables", "start", "lens")], self.dev)
+            slots = torch.empty(n, dtype=torch.int32, device=self.dev)
+            cu = torch.empty(len(st["ids"]) + 1, dtype=torch.int32, device=self.dev)
+            zp_build_slots(self.desc, table, start, lens, slots, cu)
+            k = self._randn(self.layers, n, self.h_kv, self.d)
+            v = self._randn(self.layers, n, self.h_kv, self.d)
+            zp_write_kv(self.desc, k, v, slots, self.K, self.V)
         self.last_step = ("prefill", st["ids"], None, st["tables"])
 
     def _decode(self, st):
@@ -103,8 +111,17 @@ class ServeLoop:
         kn = self._randn(self.layers, B, self.h_kv, self.d)
         vn = self._randn(self.layers, B, self.h_kv, self.d)
         out = torch.empty(self.layers, B, self.h_q, self.d, dtype=self.dtype, device=self.dev)
+        plan = None
+        if self.prefix_decode:
+            p = self._plan_buf
+            plan = PrefixPlan(p[0, :B], p[1, :1], p[2, :B + 1], p[3, :B], p[4, :B])
+            zp_prefix_plan(self.desc, table, lens, plan, min_blocks=self.prefix_min_blocks)
         for l in range(self.layers):
             zp_append_kv(self.desc, kn[l], vn[l], self.K[l], self.V[l], table, lens)
+            if plan is not None:
+                zp_prefix_decode_attn(self.desc, q[l], self.K[l], self.V[l], table, lens, plan, out[l],
+                                      score_accum=self.S[l], window=self.window, workspace=self.ws, score_rows=rows)
+                continue
             zp_paged_decode_attn(self.desc, q[l], self.K[l], self.V[l], table, lens, out[l], score_accum=self.S[l],
                                  window=self.window, workspace=self.ws, score_rows=rows)
         self.out = out
@@ -238,6 +255,8 @@ def main(argv=None):
     ap = argparse.ArgumentParser(description="engine-level throughput of the scheduler + kernels on a synthetic trace")
     ap.add_argument("--policy", choices=["constrained", "hybrid"], default="hybrid")
     ap.add_argument("--prefix-sharing", action="store_true")
+    ap.add_argument("--prefix-decode", action="store_true",
+                    help="attend to shared prompt blocks once per group of requests")
     ap.add_argument("--requests", type=int, default=256)
     ap.add_argument("--prompt", type=int, nargs=2, default=[64, 512])
     ap.add_argument("--output", type=int, nargs=2, default=[512, 4096])
@@ -254,11 +273,11 @@ def main(argv=None):
     stride = (a.prompt[1] + a.output[1]) // b + 2
     loop = ServeLoop(h_q, h_kv, d, b, a.blocks, a.max_blocks, a.query_slots, stride, layers=a.layers,
                      policy=CONSTRAINED if a.policy == "constrained" else HYBRID, prefix_sharing=a.prefix_sharing,
-                     max_running=a.max_running, seed=a.seed)
+                     max_running=a.max_running, seed=a.seed, prefix_decode=a.prefix_decode)
     for r in synthetic_trace(a.requests, a.seed, tuple(a.prompt), tuple(a.output), a.prefix_groups, a.prefix_len):
         loop.add_request(*r)
     m = loop.run()
-    m.update(policy=a.policy, prefix_sharing=a.prefix_sharing, requests=a.requests, layers=a.layers,
+    m.update(policy=a.policy, prefix_sharing=a.prefix_sharing, prefix_decode=a.prefix_decode, requests=a.requests, layers=a.layers,
              heads="%dq/%dkv" % (h_q, h_kv), head_dim=d, block=b, max_blocks=a.max_blocks, query_slots=a.query_slots,
              blocks=a.blocks, prompt=a.prompt, output=a.output)
     print(json.dumps(m))
