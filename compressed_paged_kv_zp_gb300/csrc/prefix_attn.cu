@@ -73,32 +73,38 @@ __device__ void pfx_load_q(const PfxArgs &a, const PfxGroup &g, int head, int r0
     }
 }
 
-// 64 prefix tokens from t0 (zero beyond the prefix and for bad blocks).
-template <int D>
-__device__ void pfx_load_kv(const PfxArgs &a, const PfxGroup &g, const int32_t *row, int head, int t0, PfxSmem<D> &sm,
-                            bool with_v) {
-    constexpr int V = 4;
-    for (int i = threadIdx.x; i < kPfxTokens * (D / V); i += kPfxThreads) {
-        const int t = i / (D / V), c = (i % (D / V)) * V;
-        float x[V], y[V];
+// 64 prefix tokens from t0 (zero beyond the prefix and for bad blocks): fetched
+// into registers while the tile before is computed, then put in shared memory.
+template <int D, bool WITH_V>
+struct PfxFetch {
+    static constexpr int N = kPfxTokens * (D / 4) / kPfxThreads;
+    float4 k[N], v[WITH_V ? N : 1];
+
+    __device__ __forceinline__ void load(const PfxArgs &a, const PfxGroup &g, const int32_t *row, int head, int t0) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) x[e] = y[e] = 0.f;
-        if (t0 + t < g.tokens) {
-            const long long slot = pfx_slot(a, row, t0 + t);
-            if (slot >= 0) {
-                const size_t at = ((size_t)slot * a.h_kv + head) * D + c;
-                load_vec(static_cast<const float *>(a.k) + at, x);
-                if (with_v) load_vec(static_cast<const float *>(a.v) + at, y);
+        for (int n = 0; n < N; ++n) {
+            const int i = n * kPfxThreads + threadIdx.x, t = i / (D / 4), c = (i % (D / 4)) * 4;
+            k[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (WITH_V) v[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (t0 + t < g.tokens) {
+                const long long slot = pfx_slot(a, row, t0 + t);
+                if (slot >= 0) {
+                    const size_t at = ((size_t)slot * a.h_kv + head) * D + c;
+                    k[n] = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(a.k) + at));
+                    if (WITH_V) v[n] = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(a.v) + at));
+                }
             }
         }
+    }
+    __device__ __forceinline__ void store(PfxSmem<D> &sm) const {
 #pragma unroll
-        for (int e = 0; e < V; ++e) sm.k[t][c + e] = x[e];
-        if (with_v) {
-#pragma unroll
-            for (int e = 0; e < V; ++e) sm.v[t][c + e] = y[e];
+        for (int n = 0; n < N; ++n) {
+            const int i = n * kPfxThreads + threadIdx.x, t = i / (D / 4), c = (i % (D / 4)) * 4;
+            *reinterpret_cast<float4 *>(&sm.k[t][c]) = k[n];
+            if (WITH_V) *reinterpret_cast<float4 *>(&sm.v[t][c]) = v[n];
         }
     }
-}
+};
 
 // Logits of rows ty*4 + i, tokens tx + 16 j (log2 units).
 template <int D>
@@ -157,11 +163,16 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_part_kernel(const PfxArgs 
 #pragma unroll
             for (int e = 0; e < 4 * DV; ++e) acc[i][e] = 0.f;
         }
+        PfxFetch<D, true> next;
+        next.load(a, g, row, head, t_b * kPfxTokens);
+        const bool live = r0 + (ty & ~1) * 4 < g.n * G;  // the warp has a query row
         for (int t = t_b; t < t_e; ++t) {
             const int t0 = t * kPfxTokens;
             __syncthreads();
-            pfx_load_kv<D>(a, g, row, head, t0, sm, true);
+            next.store(sm);
             __syncthreads();
+            if (t + 1 < t_e) next.load(a, g, row, head, t0 + kPfxTokens);
+            if (!live) continue;
             float x[4][4];
             pfx_logits<D>(sm, ty, tx, x);
 #pragma unroll
@@ -427,11 +438,16 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_score_kernel(const PfxArgs
                 }
             }
         }
+        PfxFetch<D, false> next;
+        next.load(a, g, row, head, t_b * kPfxTokens);
+        const bool live = r0 + (ty & ~1) * 4 < g.n * G;  // the warp has a query row
         for (int t = t_b; t < t_e; ++t) {
             const int t0 = t * kPfxTokens;
             __syncthreads();
-            pfx_load_kv<D>(a, g, row, head, t0, sm, false);
+            next.store(sm);
             __syncthreads();
+            if (t + 1 < t_e) next.load(a, g, row, head, t0 + kPfxTokens);
+            if (!live) continue;
             float x[4][4];
             pfx_logits<D>(sm, ty, tx, x);
 #pragma unroll

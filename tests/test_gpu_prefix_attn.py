@@ -228,3 +228,51 @@ def test_bad_members_and_blocks_are_recorded(zp):
     zp.zp_prefix_decode_attn(c.desc, c.qd, c.Kd, c.Vd, c.td, c.ld, c.plan, out)
     assert zp.zp_device_status() == (7, 0x143)
     assert torch.equal(out[lone], good[lone]) and bool(torch.isfinite(out.float()).all())
+
+
+@pytest.mark.parametrize("heads", ["qwen", "g8d64", "tiny32", "wide"])
+def test_rows_outside_the_sequences_do_not_matter(zp, heads):
+    """NaN and infinities in every cache row that holds no token (unused blocks, the rest of last blocks)."""
+    c = Case(zp, 101, HEADS[heads], [5, 3], [3, 9], (1, 90), 2, 1)
+    used = np.zeros((c.n_total, c.b), bool)
+    for s, L in enumerate(c.lens):
+        t = np.arange(int(L))
+        used[c.table[s, t // c.b], t % c.b] = True
+    clean = (c.K.clone(), c.V.clone())
+    bad = torch.from_numpy(~used)
+    c.K[bad] = float("nan")
+    c.V[bad] = float("inf")
+    c.Kd, c.Vd = c.K.to(DEV), c.V.to(DEV)
+    c.score_rows(102, c.b)
+    out, S = c.run(zp)
+    c.K, c.V = clean
+    c.check(out, S)
+
+
+def test_blocks_far_into_a_large_cache(zp):
+    """Byte offsets beyond 32 bits: the sequences' blocks are the last of a 4.9 GB layer."""
+    c = Case(zp, 111, HEADS["qwen"], [6], [20], (1, 60), 2)
+    far = 150000
+    K = torch.zeros(far, c.b, c.h_kv, c.d, dtype=BF16, device=DEV)
+    V = torch.zeros_like(K)
+    off = far - c.n_total
+    K[off:], V[off:] = c.Kd, c.Vd
+    c.score_rows(112, 16)
+    td = torch.where(c.td >= 0, c.td + off, c.td)
+    desc = zp.cache_desc(c.h_q, c.h_kv, c.d, c.b, far, BF16)
+    out = torch.full_like(c.qd, 7.0)
+    S = torch.from_numpy(c.S0).to(DEV)
+    zp.zp_prefix_plan(desc, td, c.ld, c.plan)
+    zp.zp_prefix_decode_attn(desc, c.qd, K, V, td, c.ld, c.plan, out, score_accum=S, window=16, score_rows=_d(c.rows))
+    torch.cuda.synchronize()
+    assert zp.zp_device_status() == (0, 0)
+    near, S2 = c.run(zp)
+    assert torch.equal(out, near) and torch.equal(S, S2)  # the same work on the same values
+    c.check(out, S)
+
+
+def test_full_batch(zp):
+    """The largest batch: 4096 entries, groups and lone entries, some without a token."""
+    c = Case(zp, 121, (4, 1, 64, 16, BF16), [1500, 700, 2] + [3] * 400, [3, 2, 5] + [1] * 400, (1, 20), 600, 94)
+    assert c.B == 4096
+    c.check(*c.run(zp))
