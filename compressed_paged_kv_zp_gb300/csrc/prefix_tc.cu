@@ -209,6 +209,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     const int head = blockIdx.x % a.h_kv, set = blockIdx.x / a.h_kv;
     const int w0 = pfx_start(set, W, a.parts), w1 = pfx_start(set + 1, W, a.parts);
 
+    if (warp < 2) pdl_trigger();
     if (warp == 0) {
         // ---------------- producer: K and V tiles in order
         uint32_t fill = 0;
@@ -408,6 +409,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
             }
             if (!ok_all) break;
+            pdl_trigger();  // (the merge waits for this kernel's end)
             // the piece's record: 64 dims of the warp's 32 rows at a time through the
             // stream's query tile (its products are complete), so that stores are
             // whole 128-byte lines; chunk c of row i sits at c ^ (i & 7)
