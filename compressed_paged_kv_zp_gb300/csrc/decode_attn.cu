@@ -44,7 +44,8 @@
 // p tokens (a multiple of b) is then the sequence of its other L - p tokens:
 // its table row starts p/b entries later, its score row p tokens later, and its
 // online softmax starts from the prefix's record (max, sum, accumulator) where
-// a CTA takes its first unit, instead of from nothing.  Everything else (the
+// a CTA takes its first unit, instead of from nothing; without the score it starts
+// from nothing and prefix_tail_kernel joins its records with the prefix's.  Everything else (the
 // split, the merges, the score) is unchanged.
 #ifndef ZP_DECODE_PREFIX
 #define ZP_DECODE_PREFIX 0
@@ -93,7 +94,7 @@ struct DecodeArgs {
     float2 *stats;     // [B][h_q] final (max, sum), log2 units
     float *part_acc;   // [2*grid][h_q][D]
     float2 *part_ml;   // [2*grid][h_q]
-    int *unit_prefix;  // [B+1]
+    int *unit_prefix;  // [B+1]; behind a prefix [B+2]: whether no sequence is cut
     int4 *unit_info;   // [units]: (sequence, first token, length, window flags) of every unit
     long long logits_units;  // capacity of `logits` in units
     unsigned long long *ctl;  // [B] per-sequence control words of the in-kernel merge (tensor-core path)
@@ -108,8 +109,9 @@ struct DecodeArgs {
     unsigned *err;
     // shared prefix (kPrefix): tokens per batch entry and the records its softmax starts from
     const int32_t *prefix_lens;  // [B]
-    const float *init_acc;       // [B][h_q][D] unnormalised accumulator
-    const float2 *init_ml;       // [B][h_q] (max, sum), log2 units
+    float *init_acc;             // [B][h_q][D] unnormalised accumulator
+    float2 *init_ml;             // [B][h_q] (max, sum), log2 units
+    int detached;  // no score: start from nothing and leave the records of sequences behind a prefix there
 };
 
 // Tokens of sequence s (of L) that its prefix record covers: none when the plan
@@ -334,6 +336,7 @@ __global__ void __launch_bounds__(kMaxConsumerWarps * 32, 1)
     const long long U = prefix[B];
     if (blockIdx.x == 0) {
         for (int s = tid; s <= B; s += blockDim.x) a.unit_prefix[s] = prefix[s];
+        if (kPrefix && tid == 0) a.unit_prefix[B + 1] = 0;
     }
     if (a.want_score && U > a.logits_units) {
         if (tid == 0) record_error(a.err, ZP_ERR_DEVICE, 3);
@@ -447,7 +450,7 @@ __global__ void __launch_bounds__(kMaxConsumerWarps * 32, 1)
     auto start_state = [&](int s, bool first_unit) {
         reset_state();
         if constexpr (kPrefix) {
-            if (!first_unit || wih != 0 || prefix_of(a, s) == 0) return;
+            if (a.detached || !first_unit || wih != 0 || prefix_of(a, s) == 0) return;
             const float2 *iml = a.init_ml + (size_t)s * a.h_q + h0;
 #pragma unroll
             for (int j = 0; j < G; ++j) m[j] = __ldcg(&iml[j]).x;
@@ -478,7 +481,8 @@ __global__ void __launch_bounds__(kMaxConsumerWarps * 32, 1)
 
     int s = s_first;
     long long seg_begin = u0;
-    if constexpr (kPrefix) pdl_wait();  // the prefix records
+    if constexpr (kPrefix)
+        if (!a.detached) pdl_wait();  // the prefix records
     start_state(s, u0 == prefix[s]);
     load_q(s);
     bool window_step = false;
@@ -663,7 +667,8 @@ __global__ void __launch_bounds__(kMaxConsumerWarps * 32, 1)
             }
 
             const bool whole = (prefix[s] >= seg_begin) && seq_ends;
-            if (whole) {
+            const bool leave = kPrefix && whole && a.detached && prefix_of(a, s) > 0;  // a record all the same
+            if (whole && !leave) {
                 if (wih == 0 && lane < 16) {
                     T *og = static_cast<T *>(a.out) + ((size_t)s * a.h_q + h0) * D + lane16 * DPL;
 #pragma unroll
@@ -680,7 +685,8 @@ __global__ void __launch_bounds__(kMaxConsumerWarps * 32, 1)
                 // partial record of this CTA for sequence s
                 const int slot = 2 * blockIdx.x + ((prefix[s] <= u0) ? 0 : 1);
                 if (wih == 0 && lane < 16) {
-                    float *pa = a.part_acc + ((size_t)slot * a.h_q + h0) * D + lane16 * DPL;
+                    const size_t row = (size_t)(leave ? s : slot) * a.h_q + h0;
+                    float *pa = (leave ? a.init_acc : a.part_acc) + row * D + lane16 * DPL;
 #pragma unroll
                     for (int j = 0; j < G; ++j)
 #pragma unroll
@@ -689,7 +695,7 @@ __global__ void __launch_bounds__(kMaxConsumerWarps * 32, 1)
                     if (lane == 0) {
 #pragma unroll
                         for (int j = 0; j < G; ++j)
-                            a.part_ml[(size_t)slot * a.h_q + h0 + j] = make_float2(m[j], l[j]);
+                            (leave ? a.init_ml : a.part_ml)[row + j] = make_float2(m[j], l[j]);
                     }
                 }
             }
@@ -703,7 +709,8 @@ __global__ void __launch_bounds__(kMaxConsumerWarps * 32, 1)
             }
         }
     }
-
+    if constexpr (kPrefix)
+        if (a.detached) pdl_wait();  // the next kernel is then also behind the prefix kernel
 }
 
 // Window-score epilogue: one block per unit, one thread per (kv head, token)
@@ -1328,6 +1335,7 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
     const long long U = prefix[B];
     if (blockIdx.x == 0)
         for (int s = tid; s <= B; s += blockDim.x) a.unit_prefix[s] = prefix[s];
+    if (kPrefix && blockIdx.x == 0 && tid == 0) a.unit_prefix[B + 1] = longest <= kAlignUnits;
     if (weighted) {
         // Stream-K over weighted units: a unit of a sequence with row sums
         // weighs rho_weight16, a plain one 16.
@@ -1485,7 +1493,7 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
     auto start_state = [&](int s, bool first_unit) {
         reset_state();
         if constexpr (kPrefix) {
-            if (!first_unit || prefix_of(a, s) == 0) return;
+            if (a.detached || !first_unit || prefix_of(a, s) == 0) return;
             if (g < G) {
                 const float2 ml = __ldcg(&a.init_ml[(size_t)s * a.h_q + h0 + g]);
                 m_run = ml.x;
@@ -1533,7 +1541,8 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
     int s = s_first;
     long long seg_begin = u0;
     const uint64_t keep_pol = l2_evict_last_policy();
-    if constexpr (kPrefix) pdl_wait();  // the prefix records (the producer reads only inputs)
+    if constexpr (kPrefix)
+        if (!a.detached) pdl_wait();  // the prefix records (the producer reads only inputs)
     start_state(s, u0 == prefix[s]);
     load_q(s);
     bool window_step = compute_window(s);
@@ -1668,7 +1677,8 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
             const float l_hi = __shfl_sync(0xFFFFFFFFu, l_run, (2 * tig + 1) * 4);
             const int hc0 = 2 * tig, hc1 = 2 * tig + 1;  // column heads
             const bool whole = (prefix[s] >= seg_begin) && seq_ends;
-            if (whole) {
+            const bool leave = kPrefix && whole && a.detached && prefix_of(a, s) > 0;  // a record all the same
+            if (whole && !leave) {
                 __nv_bfloat16 *og = static_cast<__nv_bfloat16 *>(a.out) + ((size_t)s * a.h_q + h0) * D;
                 const float i0 = l_lo > 0.f ? 1.f / l_lo : 0.f;
                 const float i1 = l_hi > 0.f ? 1.f / l_hi : 0.f;
@@ -1688,7 +1698,8 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
                     a.stats[(size_t)s * a.h_q + h0 + g] = make_float2(m_run, l_run);
             } else {
                 const int slot = 2 * blockIdx.x + ((prefix[s] <= u0) ? 0 : 1);
-                float *pa = a.part_acc + ((size_t)slot * a.h_q + h0) * D;
+                const size_t row = (size_t)(leave ? s : slot) * a.h_q + h0;
+                float *pa = (leave ? a.init_acc : a.part_acc) + row * D;
 #pragma unroll
                 for (int t = 0; t < KS; ++t) {
                     const int d0 = 16 * t + g;
@@ -1701,7 +1712,7 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
                         pa[(size_t)hc1 * D + d0 + 8] = acc[t][3];
                     }
                 }
-                if (g < G && tig == 0) a.part_ml[(size_t)slot * a.h_q + h0 + g] = make_float2(m_run, l_run);
+                if (g < G && tig == 0) (leave ? a.init_ml : a.part_ml)[row + g] = make_float2(m_run, l_run);
                 if (tid == 0) mlist[5 + mlist[4]++] = s;  // announced after the loop
             }
             if (u + 1 < u1) {
@@ -1715,6 +1726,11 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
         }
     }
 
+    if constexpr (kPrefix)
+        if (a.detached) {  // the records are joined by the next kernel
+            pdl_wait();    // (which is then also behind the prefix kernel)
+            return;
+        }
     // =====================================================================
     // epilogue (consumer warps; the producer has returned and every stage has
     // been consumed, so the stage area is free scratch)
@@ -2069,6 +2085,83 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(const DecodeArgs a, i
     }
 }
 
+#if ZP_DECODE_PREFIX
+// Output of every sequence that has more than one record: those of its prefix and
+// of the decode (one that it saw whole, else one per CTA that took units of it).
+template <typename T, int D, int G, int SPLIT>
+__global__ void __launch_bounds__(32 * kJoinWarps) prefix_tail_kernel(const DecodeArgs a, const PfxArgs p, int grid_main) {
+    using Join = PfxJoin<D, G, SPLIT>;
+    __shared__ typename Join::Smem sm;
+    const int pair = SPLIT > 1 ? blockIdx.x : blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+    const int s = pair / a.h_kv, head = pair - s * a.h_kv;
+    const int ng = pfx_groups(p);
+    const int pre = s < a.B ? prefix_of(a, s) : 0;
+    pdl_wait();
+    if (s >= a.B) return;
+    const int u_b = __ldcg(a.unit_prefix + s), u_e = __ldcg(a.unit_prefix + s + 1);
+    const int U = __ldcg(a.unit_prefix + a.B);
+    const bool aligned = __ldcg(a.unit_prefix + a.B + 1) != 0;
+    const int mi = pre > 0 && ng > 0 ? __ldcg(p.place + s) : -1;
+    if (u_b == u_e) return;  // no token
+    const int c_lo = aligned ? 0 : cta_of(u_b, U, grid_main), c_hi = aligned ? 0 : cta_of(u_e - 1, U, grid_main);
+    const bool whole = c_lo == c_hi;
+    if (whole && pre == 0) return;  // the decode wrote the output
+    PfxPieces pc = {};
+    if (mi >= 0) {
+        const int gi = pfx_group_of(p, ng, mi);
+        pc = pfx_pieces(p, pfx_group(p, gi), mi, head, __ldcg(p.wpre + gi), __ldcg(p.wpre + ng));
+    }
+    const int n_pre = pc.n * pc.two;
+    // consecutive CTAs when each has a unit, one unit each otherwise
+    const bool dense = U >= grid_main;
+    const int n_own = whole ? 1 : (dense ? c_hi - c_lo + 1 : u_e - u_b);
+    const size_t row = (size_t)s * a.h_q + head * G;
+    Join::run(
+        sm, n_pre + n_own,
+        [&](int i, const float2 *&ml, const float *&acc) {
+            if (i < n_pre) {
+                const long long at = pfx_record(p, pc, i);
+                ml = p.rec_ml + at;
+                acc = p.rec_acc + at * D;
+            } else if (whole) {
+                ml = a.init_ml + row;
+                acc = a.init_acc + row * D;
+            } else {
+                const int c = dense ? c_lo + i - n_pre : cta_of(u_b + i - n_pre, U, grid_main);
+                const size_t at = (size_t)(2 * c + (u_b > cta_start(c, U, grid_main) ? 1 : 0)) * a.h_q + head * G;
+                ml = a.part_ml + at;
+                acc = a.part_acc + at * D;
+            }
+        },
+        [&](int j, int c, const auto &y, float, float L) {
+            constexpr int N = sizeof(y) / 4;
+            const float inv = L > 0.f ? 1.f / L : 0.f;
+            T *dst = static_cast<T *>(a.out) + (row + j) * D + c;
+            if constexpr (sizeof(T) == 2) {
+                if constexpr (N == 4)
+                    *reinterpret_cast<uint2 *>(dst) = make_uint2(f2_to_bf2(y[0] * inv, y[1] * inv), f2_to_bf2(y[2] * inv, y[3] * inv));
+                else if constexpr (N == 2) *reinterpret_cast<uint32_t *>(dst) = f2_to_bf2(y[0] * inv, y[1] * inv);
+                else *dst = __float2bfloat16_rn(y[0] * inv);
+            } else {
+#pragma unroll
+                for (int e = 0; e < N; ++e) dst[e] = y[e] * inv;
+            }
+        });
+}
+
+template <typename T, int D, int G>
+zp_status launch_tail(const DecodeArgs &a, const PfxArgs &p, int grid, cudaStream_t st) {
+    const long long pairs = (long long)a.B * a.h_kv;
+    const cudaError_t e =
+        pfx_join_split(p) ? launch_dependent(prefix_tail_kernel<T, D, G, kJoinWarps>, dim3((unsigned)pairs),
+                                             dim3(32 * kJoinWarps), 0, st, false, a, p, grid)
+                          : launch_dependent(prefix_tail_kernel<T, D, G, 1>, dim3((unsigned)((pairs + kJoinWarps - 1) / kJoinWarps)),
+                                             dim3(32 * kJoinWarps), 0, st, false, a, p, grid);
+    if (e != cudaSuccess) return cuda_fail(e, "prefix_decode: tail kernel launch");
+    return ok();
+}
+#endif
+
 // Merge kernel, then (window steps) the score epilogue.  (Programmatic
 // dependent launches of these two were measured slightly slower.)
 template <typename T, int D, int G>
@@ -2150,7 +2243,7 @@ zp_status make_plan(const zp_cache_desc *D, int B, int table_stride, const Devic
     p->off_count = off;  // per-sequence arrival counters (tensor-core path)
     off = align_up(off + (size_t)B * 8, 256);
     p->off_prefix = off;
-    off = align_up(off + (size_t)(B + 1) * 4, 256);
+    off = align_up(off + (size_t)(B + 2) * 4, 256);
     p->off_stats = off;
     off = align_up(off + (size_t)B * D->h_q * 8, 256);
     p->off_pml = off;
@@ -2166,8 +2259,7 @@ zp_status make_plan(const zp_cache_desc *D, int B, int table_stride, const Devic
 }
 
 template <int Dd, int G>
-zp_status launch_tc(const DecodeArgs &a, const Plan &p, const DeviceInfo &dev, cudaStream_t st,
-                    const zp_cache_desc *D) {
+zp_status launch_tc(const DecodeArgs &a, const Plan &p, const PfxArgs *pfx, cudaStream_t st) {
     auto kmain = decode_tc_kernel<Dd, G>;
     zp_status rs = set_max_dynamic_smem(reinterpret_cast<const void *>(kmain), (size_t)p.smem,
                                         "decode: shared-memory attribute");
@@ -2175,9 +2267,9 @@ zp_status launch_tc(const DecodeArgs &a, const Plan &p, const DeviceInfo &dev, c
     if ((reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v)) % 16)
         return fail(ZP_ERR_INVALID_ARG, "decode: caches must be 16-byte aligned");
     // cooperative: CTAs wait (bounded) for the merges of other CTAs.  Behind a
-    // prefix and without the score no CTA waits for another (the last arrival
-    // merges), and an ordinary launch may start while the kernel before it ends;
-    // a cooperative one never does (8 sequences behind 2k tokens: 39 -> 35 us).
+    // prefix and without the score there is no such wait, and an ordinary launch may
+    // start while the kernel before it ends; a cooperative one never does (8
+    // sequences behind 2k tokens: 39 -> 35 us).
     DecodeArgs args = a;
     void *params[] = {&args};
     cudaError_t e = cudaSuccess;
@@ -2187,11 +2279,14 @@ zp_status launch_tc(const DecodeArgs &a, const Plan &p, const DeviceInfo &dev, c
         e = cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(kmain), dim3(p.grid), dim3(p.threads), params,
                                     (size_t)p.smem, st);
     if (e != cudaSuccess) return cuda_fail(e, "decode: tensor-core kernel launch");
+#if ZP_DECODE_PREFIX
+    if (a.detached) return launch_tail<__nv_bfloat16, Dd, G>(a, *pfx, p.grid, st);
+#endif
     return ok();  // merges and the window score run inside the kernel
 }
 
 template <typename T, int Dd, int G>
-zp_status launch_t(const DecodeArgs &a, const Plan &p, const DeviceInfo &dev, cudaStream_t st) {
+zp_status launch_t(const DecodeArgs &a, const Plan &p, const PfxArgs *pfx, cudaStream_t st) {
     auto kmain = decode_main_kernel<T, Dd, G>;
     zp_status rs = set_max_dynamic_smem(reinterpret_cast<const void *>(kmain), (size_t)p.smem,
                                         "decode: shared-memory attribute");
@@ -2204,6 +2299,9 @@ zp_status launch_t(const DecodeArgs &a, const Plan &p, const DeviceInfo &dev, cu
         e = cudaGetLastError();
     }
     if (e != cudaSuccess) return cuda_fail(e, "decode: main kernel launch");
+#if ZP_DECODE_PREFIX
+    if (a.detached) return launch_tail<T, Dd, G>(a, *pfx, p.grid, st);
+#endif
     return launch_finish<T, Dd, G>(a, p.grid, p.logits_units, st);
 }
 
@@ -2308,34 +2406,36 @@ static zp_status decode_impl(const zp_cache_desc *D, const void *q, const void *
     a.prefix_lens = pfx->prefix;
     a.init_acc = pfx->init_acc;
     a.init_ml = pfx->init_ml;
+    a.detached = !a.want_score;
 #else
     a.prefix_lens = nullptr;
     a.init_acc = nullptr;
     a.init_ml = nullptr;
+    a.detached = 0;
 #endif
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int G = D->h_q / D->h_kv;
     const int d = D->head_dim;
     if (p.tc) {
-        if (d == 128 && G == 4) return launch_tc<128, 4>(a, p, dev, st, D);
-        if (d == 128 && G == 8) return launch_tc<128, 8>(a, p, dev, st, D);
-        if (d == 128 && G == 2) return launch_tc<128, 2>(a, p, dev, st, D);
-        if (d == 128 && G == 1) return launch_tc<128, 1>(a, p, dev, st, D);
-        if (d == 64 && G == 4) return launch_tc<64, 4>(a, p, dev, st, D);
-        if (d == 64 && G == 8) return launch_tc<64, 8>(a, p, dev, st, D);
-        if (d == 64 && G == 2) return launch_tc<64, 2>(a, p, dev, st, D);
-        if (d == 64 && G == 1) return launch_tc<64, 1>(a, p, dev, st, D);
+        if (d == 128 && G == 4) return launch_tc<128, 4>(a, p, pfx, st);
+        if (d == 128 && G == 8) return launch_tc<128, 8>(a, p, pfx, st);
+        if (d == 128 && G == 2) return launch_tc<128, 2>(a, p, pfx, st);
+        if (d == 128 && G == 1) return launch_tc<128, 1>(a, p, pfx, st);
+        if (d == 64 && G == 4) return launch_tc<64, 4>(a, p, pfx, st);
+        if (d == 64 && G == 8) return launch_tc<64, 8>(a, p, pfx, st);
+        if (d == 64 && G == 2) return launch_tc<64, 2>(a, p, pfx, st);
+        if (d == 64 && G == 1) return launch_tc<64, 1>(a, p, pfx, st);
     }
     if (D->dtype == ZP_BF16) {
-        if (d == 128 && G == 4) return launch_t<__nv_bfloat16, 128, 4>(a, p, dev, st);
-        if (d == 128 && G == 8) return launch_t<__nv_bfloat16, 128, 8>(a, p, dev, st);
-        if (d == 64 && G == 4) return launch_t<__nv_bfloat16, 64, 4>(a, p, dev, st);
-        if (d == 64 && G == 8) return launch_t<__nv_bfloat16, 64, 8>(a, p, dev, st);
+        if (d == 128 && G == 4) return launch_t<__nv_bfloat16, 128, 4>(a, p, pfx, st);
+        if (d == 128 && G == 8) return launch_t<__nv_bfloat16, 128, 8>(a, p, pfx, st);
+        if (d == 64 && G == 4) return launch_t<__nv_bfloat16, 64, 4>(a, p, pfx, st);
+        if (d == 64 && G == 8) return launch_t<__nv_bfloat16, 64, 8>(a, p, pfx, st);
     } else {
-        if (d == 128 && G == 4) return launch_t<float, 128, 4>(a, p, dev, st);
-        if (d == 128 && G == 8) return launch_t<float, 128, 8>(a, p, dev, st);
-        if (d == 64 && G == 4) return launch_t<float, 64, 4>(a, p, dev, st);
-        if (d == 64 && G == 8) return launch_t<float, 64, 8>(a, p, dev, st);
+        if (d == 128 && G == 4) return launch_t<float, 128, 4>(a, p, pfx, st);
+        if (d == 128 && G == 8) return launch_t<float, 128, 8>(a, p, pfx, st);
+        if (d == 64 && G == 4) return launch_t<float, 64, 4>(a, p, pfx, st);
+        if (d == 64 && G == 8) return launch_t<float, 64, 8>(a, p, pfx, st);
     }
     return fail(ZP_ERR_SHAPE, "decode: no kernel for d=%d, group=%d", d, G);
 }

@@ -6,12 +6,15 @@
 // shared keys and values is a dense product:
 //     x = log2(e)/sqrt(d) Q K^T,  m_r = max_t x_rt,  l_r = sum_t 2^(x_rt - m_r),
 //     acc_r = sum_t 2^(x_rt - m_r) v_t.
-// (m, l, acc) of every (sequence, q head) is the state from which the decode of
-// the sequence's other tokens starts (decode_attn_prefix.cu), so the result is
-// the softmax over all tokens and the shared keys and values are read once per
-// group instead of once per sequence.  With the window score, the final (m, l)
-// of every sequence that is on a window step give a second pass over the shared
-// keys: S[t] (+)= (1/w) max_{h in group} 2^(x_ht - m_h) / l_h.
+// (m, l, acc) of every (sequence, q head) and the decode's of the sequence's other
+// tokens (decode_attn_prefix.cu) join to the softmax over all tokens, so the shared
+// keys and values are read once per group instead of once per sequence.  Without
+// the window score the decode leaves records and one kernel joins them with the
+// prefix's; the decode then needs nothing of the prefix kernel and follows it
+// without a gap.  With the score the decode itself starts from the joined prefix
+// records, since its epilogue needs the final (m, l), and these give a second pass
+// over the shared keys for the sequences on a window step:
+//     S[t] (+)= (1/w) max_{h in group} 2^(x_ht - m_h) / l_h.
 //
 // Work: an item is (group, tile of query rows), its length the group's tiles of
 // prefix tokens.  The tiles of all items are concatenated and every set of h_kv
@@ -20,9 +23,8 @@
 // and the CTAs of a set read the heads of the same token rows at the same time.
 // The first piece of an item goes to its rows' place in the main records, a
 // piece that begins inside an item (at most one per CTA) to the CTA's extra
-// records; a merge kernel joins the pieces of each row.  (Joined by the decode
-// where it starts a sequence instead, the scored 256 x 4k batch took 186 us, not
-// 174: a chain of dependent loads against its own K and V traffic.)
+// records.  (Joined by the decode where it starts a sequence, the scored 256 x 4k
+// batch took 186 us, not 174: a chain of dependent loads against its own traffic.)
 #include <math.h>
 
 #include "prefix_tc.h"
@@ -142,8 +144,7 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_part_kernel(const PfxArgs 
     const int ng = pfx_groups(a);
     const int W = pfx_scan(a, ng, pre);
     pdl_trigger();
-    if (blockIdx.x == 0)
-        for (int i = tid; i <= ng; i += kPfxThreads) a.wpre[i] = pre[i];  // for the merge
+    if (blockIdx.x == 0) pfx_publish(a, ng, pre);
     const int head = blockIdx.x % a.h_kv, set = blockIdx.x / a.h_kv;
     const int w0 = pfx_start(set, W, a.parts), w1 = pfx_start(set + 1, W, a.parts);
     for (int w = w0; w < w1;) {
@@ -240,41 +241,18 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_part_kernel(const PfxArgs 
     }
 }
 
-// V consecutive floats through L2.
-template <int V>
-__device__ __forceinline__ void ld_row(const float *p, float (&v)[V]) {
-    if constexpr (V == 4) {
-        const float4 w = __ldcg(reinterpret_cast<const float4 *>(p));
-        v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
-    } else {
-        const float2 w = __ldcg(reinterpret_cast<const float2 *>(p));
-        v[0] = w.x, v[1] = w.y;
-    }
-}
-
-// The records of the G rows of a (member, kv head) pair joined by SPLIT warps,
-//     M = max_j m_j,  l = sum_j 2^(m_j - M) l_j,  acc = sum_j 2^(m_j - M) acc_j:
-// a share of the records per warp and, for SPLIT > 1, the warps' results joined in
-// shared memory.  Lane i finds record i and its (m, l), 32 at a time, and lists
-// those that hold anything, so that the loads of the statistics, and then of the
-// accumulators, are in flight together: bound by the latency of these two.  What
-// depends on the plan alone is done before the wait for the prefix kernel.
-// Few pairs have many records each, many pairs few: a CTA of four warps takes one
-// pair while the pairs fill the GPU at most once (64 pairs of 16 records: 2.6 us
-// after the wait, 7.4 us with a warp each), else four (2048 pairs of 6: 3.6 us;
-// 13 us with four warps each).
+// The pieces of every (member, kv head) pair joined, for a decode that starts from
+// them (the scored call).  What depends on the plan alone is done before the wait
+// for the prefix kernel.
 constexpr int kMergeScan = 256;  // groups up to which a warp sums the tiles itself
-constexpr int kMergeWarps = 4;
 template <int D, int G, int SPLIT>
-__global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const PfxArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps) prefix_merge_kernel(const PfxArgs a) {
     pdl_trigger();
-    __shared__ long long at_s[kMergeWarps][32];
-    __shared__ float f_s[kMergeWarps][32][G];
-    __shared__ float acc_s[SPLIT > 1 ? SPLIT : 1][G][D];
-    __shared__ float2 ml_s[SPLIT > 1 ? SPLIT : 1][G];
+    using Join = PfxJoin<D, G, SPLIT>;
+    __shared__ typename Join::Smem sm;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int ng = pfx_groups(a);
-    const int pair = SPLIT > 1 ? blockIdx.x : blockIdx.x * kMergeWarps + warp;
+    const int pair = SPLIT > 1 ? blockIdx.x : blockIdx.x * kJoinWarps + warp;
     const int mi = pair / a.h_kv, head = pair - mi * a.h_kv;
     int gi = 0, s = -1, before = 0, W = 0;
     PfxGroup g = {};
@@ -297,100 +275,22 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const Pf
     pdl_wait();
     if (s < 0) return;
     if (ng > kMergeScan) pc = pfx_pieces(a, g, mi, head, __ldcg(a.wpre + gi), __ldcg(a.wpre + ng));
-    constexpr int V = D / 32;
-    float M[G], L[G], x[G][V];
-#pragma unroll
-    for (int j = 0; j < G; ++j) {
-        M[j] = -INFINITY;
-        L[j] = 0.f;
-#pragma unroll
-        for (int e = 0; e < V; ++e) x[j][e] = 0.f;
-    }
-    const int n = pc.n * pc.two;
-    const int part = SPLIT > 1 ? warp : 0;
-    const int n_b = n * part / SPLIT, n_e = n * (part + 1) / SPLIT;
-    for (int p0 = n_b; p0 < n_e; p0 += 32) {
-        const bool has = p0 + lane < n_e;
-        const long long at = has ? pfx_record(a, pc, p0 + lane) : 0;
-        float2 ml[G];
-#pragma unroll
-        for (int j = 0; j < G; ++j) ml[j] = has ? __ldcg(a.rec_ml + at + j) : make_float2(-INFINITY, 0.f);
-        const bool holds = ml[0].x != -INFINITY;  // else a stream without a tile: no accumulator either
-        const unsigned mask = __ballot_sync(0xFFFFFFFFu, holds);
-        if (mask == 0) continue;
-        const int at_i = __popc(mask & ((1u << lane) - 1));
-        if (holds) at_s[warp][at_i] = at;
-#pragma unroll
-        for (int j = 0; j < G; ++j) {
-            float Mn = fmaxf(M[j], ml[j].x);
-#pragma unroll
-            for (int o = 16; o; o >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(0xFFFFFFFFu, Mn, o));
-            const float f = holds ? exp2f(ml[j].x - Mn) : 0.f;
-            if (holds) f_s[warp][at_i][j] = f;
-            float ls = f * ml[j].y;
-#pragma unroll
-            for (int o = 16; o; o >>= 1) ls += __shfl_xor_sync(0xFFFFFFFFu, ls, o);
-            const float old = M[j] == -INFINITY ? 0.f : exp2f(M[j] - Mn);
-            L[j] = L[j] * old + ls;
-            M[j] = Mn;
-#pragma unroll
-            for (int e = 0; e < V; ++e) x[j][e] *= old;
-        }
-        __syncwarp();
-        const int here = __popc(mask);
-        constexpr int U = G <= 4 ? 4 : 2;  // records in flight
-#pragma unroll 1
-        for (int k0 = 0; k0 < here; k0 += U) {
-            float v[U][G][V];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {  // behind the last: the first record with weight 0
-                const float *src = a.rec_acc + at_s[warp][k0 + u < here ? k0 + u : 0] * D + lane * V;
-#pragma unroll
-                for (int j = 0; j < G; ++j) ld_row<V>(src + j * D, v[u][j]);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int j = 0; j < G; ++j) {
-                    const float f = k0 + u < here ? f_s[warp][k0 + u][j] : 0.f;
-#pragma unroll
-                    for (int e = 0; e < V; ++e) x[j][e] = fmaf(f, v[u][j][e], x[j][e]);
-                }
-        }
-        __syncwarp();
-    }
     const size_t row = (size_t)s * a.h_q + head * G;
-    if constexpr (SPLIT == 1) {
-#pragma unroll
-        for (int j = 0; j < G; ++j) {
-            float *dst = a.init_acc + (row + j) * D + lane * V;
-            if constexpr (V == 4) *reinterpret_cast<float4 *>(dst) = make_float4(x[j][0], x[j][1], x[j][2], x[j][3]);
-            else *reinterpret_cast<float2 *>(dst) = make_float2(x[j][0], x[j][1]);
-            if (lane == 0) a.init_ml[row + j] = make_float2(M[j], L[j]);
-        }
-    } else {  // (s is the CTA's: every warp is here)
-#pragma unroll
-        for (int j = 0; j < G; ++j) {
-#pragma unroll
-            for (int e = 0; e < V; ++e) acc_s[warp][j][lane * V + e] = x[j][e];
-            if (lane == 0) ml_s[warp][j] = make_float2(M[j], L[j]);
-        }
-        __syncthreads();
-        for (int i = threadIdx.x; i < G * D; i += 32 * SPLIT) {
-            const int j = i / D, c = i % D;
-            float Mj = -INFINITY, Lj = 0.f, y = 0.f;
-#pragma unroll
-            for (int w = 0; w < SPLIT; ++w) Mj = fmaxf(Mj, ml_s[w][j].x);
-#pragma unroll
-            for (int w = 0; w < SPLIT; ++w) {
-                const float f = ml_s[w][j].x == -INFINITY ? 0.f : exp2f(ml_s[w][j].x - Mj);
-                Lj += f * ml_s[w][j].y;
-                y = fmaf(f, acc_s[w][j][c], y);
-            }
-            a.init_acc[(row + j) * D + c] = y;
-            if (c == 0) a.init_ml[row + j] = make_float2(Mj, Lj);
-        }
-    }
+    Join::run(
+        sm, pc.n * pc.two,
+        [&](int i, const float2 *&ml, const float *&acc) {
+            const long long at = pfx_record(a, pc, i);
+            ml = a.rec_ml + at;
+            acc = a.rec_acc + at * D;
+        },
+        [&](int j, int c, const auto &y, float M, float L) {
+            constexpr int N = sizeof(y) / 4;
+            float *dst = a.init_acc + (row + j) * D + c;
+            if constexpr (N == 4) *reinterpret_cast<float4 *>(dst) = make_float4(y[0], y[1], y[2], y[3]);
+            else if constexpr (N == 2) *reinterpret_cast<float2 *>(dst) = make_float2(y[0], y[1]);
+            else *dst = y[0];
+            if (c == 0) a.init_ml[row + j] = make_float2(M, L);
+        });
 }
 
 // Window score of the prefix tokens from the final statistics: the logits again,
@@ -480,7 +380,7 @@ struct PfxPlan {
     bool tc;
     int rt, kt, parts;
     long long extra0;
-    size_t off_wpre, off_rml, off_racc, off_iml, off_iacc, total;
+    size_t off_wpre, off_place, off_rml, off_racc, off_iml, off_iacc, total;
 };
 
 zp_status pfx_plan(const zp_cache_desc *D, int B, const DeviceInfo &dev, PfxPlan *p) {
@@ -499,6 +399,8 @@ zp_status pfx_plan(const zp_cache_desc *D, int B, const DeviceInfo &dev, PfxPlan
     size_t off = 0;
     p->off_wpre = off;
     off = align_up(off + (size_t)(B + 1) * 4, 256);
+    p->off_place = off;
+    off = align_up(off + (size_t)B * 4, 256);
     p->off_rml = off;
     off = align_up(off + recs * 8, 256);
     p->off_racc = off;
@@ -538,12 +440,11 @@ zp_status launch_score(const PfxArgs &a, cudaStream_t st) {
 template <int D, int G>
 zp_status launch_merge_g(const PfxArgs &a, cudaStream_t st) {
     const long long pairs = (long long)a.B * a.h_kv;
-    const bool split = pairs <= 8LL * a.parts * a.h_kv;  // CTAs per SM that fit at once
     const cudaError_t e =
-        split ? launch_dependent(prefix_merge_kernel<D, G, kMergeWarps>, dim3((unsigned)pairs), dim3(32 * kMergeWarps), 0,
-                                 st, false, a)
-              : launch_dependent(prefix_merge_kernel<D, G, 1>, dim3((unsigned)((pairs + kMergeWarps - 1) / kMergeWarps)),
-                                 dim3(32 * kMergeWarps), 0, st, false, a);
+        pfx_join_split(a) ? launch_dependent(prefix_merge_kernel<D, G, kJoinWarps>, dim3((unsigned)pairs),
+                                             dim3(32 * kJoinWarps), 0, st, false, a)
+                          : launch_dependent(prefix_merge_kernel<D, G, 1>, dim3((unsigned)((pairs + kJoinWarps - 1) / kJoinWarps)),
+                                             dim3(32 * kJoinWarps), 0, st, false, a);
     if (e != cudaSuccess) return cuda_fail(e, "prefix_decode: merge kernel launch");
     return ZP_OK;
 }
@@ -652,6 +553,7 @@ extern "C" zp_status zp_prefix_decode_attn(const zp_cache_desc *D, const void *q
     a.wpre = reinterpret_cast<int *>(ws + p.off_wpre);
     a.rec_acc = reinterpret_cast<float *>(ws + p.off_racc);
     a.rec_ml = reinterpret_cast<float2 *>(ws + p.off_rml);
+    a.place = reinterpret_cast<int *>(ws + p.off_place);
     a.init_acc = reinterpret_cast<float *>(ws + p.off_iacc);
     a.init_ml = reinterpret_cast<float2 *>(ws + p.off_iml);
     a.score = score_accum;
@@ -664,7 +566,7 @@ extern "C" zp_status zp_prefix_decode_attn(const zp_cache_desc *D, const void *q
     const int d = D->head_dim;
     if (p.tc) rc = prefix_part_tc(a, d, st);
     else rc = d == 64 ? launch_part_f32<64>(a, G, st) : launch_part_f32<128>(a, G, st);
-    if (rc == ZP_OK) rc = d == 64 ? launch_merge<64>(a, G, st) : launch_merge<128>(a, G, st);
+    if (rc == ZP_OK && score_accum) rc = d == 64 ? launch_merge<64>(a, G, st) : launch_merge<128>(a, G, st);
     if (rc != ZP_OK) return rc;
     rc = decode_after_prefix(D, q, k_cache, v_cache, block_table, table_stride, seq_lens, B, out, score_accum, score_rows,
                              n_score_rows, window, a, workspace, dec, stream, &a.stats);

@@ -23,6 +23,7 @@ struct PfxArgs {
     int parts;           // sets of CTAs (split of the tiles); a set has a CTA per kv head
     float qscale;        // log2(e) / sqrt(d)
     int *wpre;           // [B+1] tiles before each group
+    int *place;          // [B] place of every batch entry in the member list, -1 = in no group
     float *rec_acc;      // [extra0 + parts*rt][d] pieces: main records, then extra records
     float2 *rec_ml;      // same rows
     long long extra0;    // first extra record: B*h_q, twice that on the tensor cores (second streams);
@@ -196,5 +197,151 @@ __device__ __forceinline__ long long pfx_record(const PfxArgs &a, const PfxPiece
     const int c = p.W >= a.parts ? p.c0 + j : pfx_owner(p.i0 + j, p.W, a.parts);
     return p.extra + (((long long)c * a.h_kv) << a.rt_log) + (x << (a.rt_log - 1));
 }
+
+// The first CTA's outputs for the kernels that join records (whole CTA).
+inline __device__ void pfx_publish(const PfxArgs &a, int ng, const int *pre) {
+    for (int i = threadIdx.x; i <= ng; i += blockDim.x) a.wpre[i] = pre[i];
+    for (int s = threadIdx.x; s < a.B; s += blockDim.x) a.place[s] = -1;
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.B && ng > 0; i += blockDim.x) {
+        const PfxGroup g = pfx_group(a, pfx_group_of(a, ng, i));
+        if (i < g.m0 || i >= g.m0 + g.n) continue;
+        const int s = pfx_member(a, i);
+        if (s >= 0) a.place[s] = i;
+    }
+}
+
+// V consecutive floats through L2.
+template <int V>
+__device__ __forceinline__ void ld_row(const float *p, float (&v)[V]) {
+    if constexpr (V == 4) {
+        const float4 w = __ldcg(reinterpret_cast<const float4 *>(p));
+        v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+    } else {
+        const float2 w = __ldcg(reinterpret_cast<const float2 *>(p));
+        v[0] = w.x, v[1] = w.y;
+    }
+}
+
+// Softmax records of the G rows of a (sequence, kv head) pair joined by SPLIT
+// warps of a CTA of four,
+//     M = max_j m_j,  L = sum_j 2^(m_j - M) l_j,  acc = sum_j 2^(m_j - M) acc_j.
+// A share of the records per warp and, for SPLIT > 1, the warps' results joined in
+// shared memory.  Lane i finds record i and its (m, l), 32 at a time, and lists
+// those that hold anything, so that the loads of the statistics, and then of the
+// accumulators, are in flight together: bound by the latency of these two.
+//   rec(i, ml, acc)  the first row of record i in [0, n): statistics, accumulator
+//   put(j, c, y, M, L)  takes V consecutive dims from c of row j (SPLIT 1: V = D/32,
+//                       else 1), unnormalised
+// Few pairs have many records each, many pairs few: four warps per pair while the
+// pairs fill the GPU at most once (64 pairs of 16 records: 2.6 us, 7.4 us with a warp
+// each), else one (2048 pairs of 6: 3.6 us; 13 us with four warps each).
+constexpr int kJoinWarps = 4;
+
+template <int D, int G, int SPLIT>
+struct PfxJoin {
+    static constexpr int V = D / 32;
+    struct Smem {
+        const float *src[kJoinWarps][32];
+        float f[kJoinWarps][32][G];
+        float acc[SPLIT > 1 ? SPLIT : 1][G][D];
+        float2 ml[SPLIT > 1 ? SPLIT : 1][G];
+    };
+
+    template <typename Rec, typename Put>
+    static __device__ __forceinline__ void run(Smem &sm, int n, Rec &&rec, Put &&put) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        float M[G], L[G], x[G][V];
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+            M[j] = -INFINITY;
+            L[j] = 0.f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) x[j][e] = 0.f;
+        }
+        const int part = SPLIT > 1 ? warp : 0;
+        const int n_b = n * part / SPLIT, n_e = n * (part + 1) / SPLIT;
+        for (int p0 = n_b; p0 < n_e; p0 += 32) {
+            const bool has = p0 + lane < n_e;
+            const float2 *ml_p = nullptr;
+            const float *acc_p = nullptr;
+            if (has) rec(p0 + lane, ml_p, acc_p);
+            float2 ml[G];
+#pragma unroll
+            for (int j = 0; j < G; ++j) ml[j] = has ? __ldcg(ml_p + j) : make_float2(-INFINITY, 0.f);
+            const bool holds = ml[0].x != -INFINITY;  // else a stream without a tile: no accumulator either
+            const unsigned mask = __ballot_sync(0xFFFFFFFFu, holds);
+            if (mask == 0) continue;
+            const int at_i = __popc(mask & ((1u << lane) - 1));
+            if (holds) sm.src[warp][at_i] = acc_p;
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+                float Mn = fmaxf(M[j], ml[j].x);
+#pragma unroll
+                for (int o = 16; o; o >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(0xFFFFFFFFu, Mn, o));
+                const float f = holds ? exp2f(ml[j].x - Mn) : 0.f;
+                if (holds) sm.f[warp][at_i][j] = f;
+                float ls = f * ml[j].y;
+#pragma unroll
+                for (int o = 16; o; o >>= 1) ls += __shfl_xor_sync(0xFFFFFFFFu, ls, o);
+                const float old = M[j] == -INFINITY ? 0.f : exp2f(M[j] - Mn);
+                L[j] = L[j] * old + ls;
+                M[j] = Mn;
+#pragma unroll
+                for (int e = 0; e < V; ++e) x[j][e] *= old;
+            }
+            __syncwarp();
+            const int here = __popc(mask);
+            constexpr int U = G <= 4 ? 4 : 2;  // records in flight
+#pragma unroll 1
+            for (int k0 = 0; k0 < here; k0 += U) {
+                float v[U][G][V];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {  // behind the last: the first record with weight 0
+                    const float *src = sm.src[warp][k0 + u < here ? k0 + u : 0] + lane * V;
+#pragma unroll
+                    for (int j = 0; j < G; ++j) ld_row<V>(src + j * D, v[u][j]);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int j = 0; j < G; ++j) {
+                        const float f = k0 + u < here ? sm.f[warp][k0 + u][j] : 0.f;
+#pragma unroll
+                        for (int e = 0; e < V; ++e) x[j][e] = fmaf(f, v[u][j][e], x[j][e]);
+                    }
+            }
+            __syncwarp();
+        }
+        if constexpr (SPLIT == 1) {
+#pragma unroll
+            for (int j = 0; j < G; ++j) put(j, lane * V, x[j], M[j], L[j]);
+        } else {  // (the pair is the CTA's: every warp is here)
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) sm.acc[warp][j][lane * V + e] = x[j][e];
+                if (lane == 0) sm.ml[warp][j] = make_float2(M[j], L[j]);
+            }
+            __syncthreads();
+            for (int i = threadIdx.x; i < G * D; i += 32 * SPLIT) {
+                const int j = i / D, c = i % D;
+                float Mj = -INFINITY, Lj = 0.f, y[1] = {0.f};
+#pragma unroll
+                for (int w = 0; w < SPLIT; ++w) Mj = fmaxf(Mj, sm.ml[w][j].x);
+#pragma unroll
+                for (int w = 0; w < SPLIT; ++w) {
+                    const float f = sm.ml[w][j].x == -INFINITY ? 0.f : exp2f(sm.ml[w][j].x - Mj);
+                    Lj += f * sm.ml[w][j].y;
+                    y[0] = fmaf(f, sm.acc[w][j][c], y[0]);
+                }
+                put(j, c, y, Mj, Lj);
+            }
+        }
+    }
+};
+
+// Host: four warps per pair while the pairs' CTAs are resident at once.
+inline bool pfx_join_split(const PfxArgs &a) { return (long long)a.B * a.h_kv <= 8LL * a.parts * a.h_kv; }
 
 }  // namespace zp

@@ -204,8 +204,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     const int W = pfx_scan(a, ng, pre);  // (ends with a barrier)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    if (blockIdx.x == 0)
-        for (int i = threadIdx.x; i <= ng; i += kPtThreads) a.wpre[i] = pre[i];  // for the merge
+    if (blockIdx.x == 0) pfx_publish(a, ng, pre);
     const int head = blockIdx.x % a.h_kv, set = blockIdx.x / a.h_kv;
     const int w0 = pfx_start(set, W, a.parts), w1 = pfx_start(set + 1, W, a.parts);
 
