@@ -2088,29 +2088,80 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(const DecodeArgs a, i
 #if ZP_DECODE_PREFIX
 // Output of every sequence that has more than one record: those of its prefix and
 // of the decode (one that it saw whole, else one per CTA that took units of it).
+// The split follows from the lengths and the plan, so up to kTailScanB entries a
+// warp works it out before the wait for the decode, and only the records are read
+// after it (64 sequences behind 32k tokens: 3 us after the wait, not 8); beyond,
+// it is read from what the kernels before left in the workspace.
+constexpr int kTailScanB = 512;
+constexpr int kTailScanGroups = 256;
 template <typename T, int D, int G, int SPLIT>
-__global__ void __launch_bounds__(32 * kJoinWarps) prefix_tail_kernel(const DecodeArgs a, const PfxArgs p, int grid_main) {
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    prefix_tail_kernel(const DecodeArgs a, const PfxArgs p, int grid_main, bool may_align) {
     using Join = PfxJoin<D, G, SPLIT>;
     __shared__ typename Join::Smem sm;
+    const int lane = threadIdx.x & 31;
     const int pair = SPLIT > 1 ? blockIdx.x : blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
     const int s = pair / a.h_kv, head = pair - s * a.h_kv;
     const int ng = pfx_groups(p);
     const int pre = s < a.B ? prefix_of(a, s) : 0;
+    const bool scan = a.B <= kTailScanB && ng <= kTailScanGroups;
+    int u_b = 0, u_e = 0, U = 0, mi = -1, c_lo = 0, c_hi = 0;
+    bool aligned = false;
+    PfxPieces pc = {};
+    auto cuts = [&]() {
+        if (!aligned && u_e > u_b) {
+            c_lo = cta_of(u_b, U, grid_main);
+            c_hi = cta_of(u_e - 1, U, grid_main);
+        }
+    };
+    if (scan) {
+        const int t_log = 31 - __clz(a.T);
+        int longest = 0, mine = 0, before = 0, tiles = 0;
+#pragma unroll 4
+        for (int i = lane; i < a.B; i += 32) {
+            const int L = min(max(__ldg(a.seq_lens + i), 0), a.table_stride * a.b);
+            const int n = (L - prefix_of(a, i, L) + a.T - 1) >> t_log;
+            U += n;
+            if (i < s) u_b += n;
+            if (i == s) mine = n;
+            longest = max(longest, n);
+            if (__ldg(p.members + i) == s) mi = i;  // (places behind the last member hold -1)
+        }
+        U = __reduce_add_sync(0xFFFFFFFFu, U);
+        u_b = __reduce_add_sync(0xFFFFFFFFu, u_b);
+        u_e = u_b + __reduce_add_sync(0xFFFFFFFFu, mine);
+        aligned = may_align && __reduce_max_sync(0xFFFFFFFFu, longest) <= kAlignUnits;
+        mi = __reduce_max_sync(0xFFFFFFFFu, mi);
+        cuts();
+        if (pre > 0 && mi >= 0 && ng > 0) {
+            const int gi = pfx_group_of(p, ng, mi);
+            for (int i = lane; i < ng; i += 32) {
+                const PfxGroup o = pfx_group(p, i);
+                tiles += o.rts * o.kts;
+                if (i < gi) before += o.rts * o.kts;
+            }
+            tiles = __reduce_add_sync(0xFFFFFFFFu, tiles);
+            before = __reduce_add_sync(0xFFFFFFFFu, before);
+            pc = pfx_pieces(p, pfx_group(p, gi), mi, head, before, tiles);
+        }
+    }
     pdl_wait();
     if (s >= a.B) return;
-    const int u_b = __ldcg(a.unit_prefix + s), u_e = __ldcg(a.unit_prefix + s + 1);
-    const int U = __ldcg(a.unit_prefix + a.B);
-    const bool aligned = __ldcg(a.unit_prefix + a.B + 1) != 0;
-    const int mi = pre > 0 && ng > 0 ? __ldcg(p.place + s) : -1;
+    if (!scan) {
+        u_b = __ldcg(a.unit_prefix + s);
+        u_e = __ldcg(a.unit_prefix + s + 1);
+        U = __ldcg(a.unit_prefix + a.B);
+        aligned = __ldcg(a.unit_prefix + a.B + 1) != 0;
+        mi = pre > 0 && ng > 0 ? __ldcg(p.place + s) : -1;
+        cuts();
+        if (mi >= 0) {
+            const int gi = pfx_group_of(p, ng, mi);
+            pc = pfx_pieces(p, pfx_group(p, gi), mi, head, __ldcg(p.wpre + gi), __ldcg(p.wpre + ng));
+        }
+    }
     if (u_b == u_e) return;  // no token
-    const int c_lo = aligned ? 0 : cta_of(u_b, U, grid_main), c_hi = aligned ? 0 : cta_of(u_e - 1, U, grid_main);
     const bool whole = c_lo == c_hi;
     if (whole && pre == 0) return;  // the decode wrote the output
-    PfxPieces pc = {};
-    if (mi >= 0) {
-        const int gi = pfx_group_of(p, ng, mi);
-        pc = pfx_pieces(p, pfx_group(p, gi), mi, head, __ldcg(p.wpre + gi), __ldcg(p.wpre + ng));
-    }
     const int n_pre = pc.n * pc.two;
     // consecutive CTAs when each has a unit, one unit each otherwise
     const bool dense = U >= grid_main;
@@ -2150,13 +2201,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prefix_tail_kernel(const Deco
 }
 
 template <typename T, int D, int G>
-zp_status launch_tail(const DecodeArgs &a, const PfxArgs &p, int grid, cudaStream_t st) {
+zp_status launch_tail(const DecodeArgs &a, const PfxArgs &p, int grid, bool may_align, cudaStream_t st) {
     const long long pairs = (long long)a.B * a.h_kv;
     const cudaError_t e =
         pfx_join_split(p) ? launch_dependent(prefix_tail_kernel<T, D, G, kJoinWarps>, dim3((unsigned)pairs),
-                                             dim3(32 * kJoinWarps), 0, st, false, a, p, grid)
+                                             dim3(32 * kJoinWarps), 0, st, false, a, p, grid, may_align)
                           : launch_dependent(prefix_tail_kernel<T, D, G, 1>, dim3((unsigned)((pairs + kJoinWarps - 1) / kJoinWarps)),
-                                             dim3(32 * kJoinWarps), 0, st, false, a, p, grid);
+                                             dim3(32 * kJoinWarps), 0, st, false, a, p, grid, may_align);
     if (e != cudaSuccess) return cuda_fail(e, "prefix_decode: tail kernel launch");
     return ok();
 }
@@ -2280,7 +2331,7 @@ zp_status launch_tc(const DecodeArgs &a, const Plan &p, const PfxArgs *pfx, cuda
                                     (size_t)p.smem, st);
     if (e != cudaSuccess) return cuda_fail(e, "decode: tensor-core kernel launch");
 #if ZP_DECODE_PREFIX
-    if (a.detached) return launch_tail<__nv_bfloat16, Dd, G>(a, *pfx, p.grid, st);
+    if (a.detached) return launch_tail<__nv_bfloat16, Dd, G>(a, *pfx, p.grid, true, st);
 #endif
     return ok();  // merges and the window score run inside the kernel
 }
@@ -2300,7 +2351,7 @@ zp_status launch_t(const DecodeArgs &a, const Plan &p, const PfxArgs *pfx, cudaS
     }
     if (e != cudaSuccess) return cuda_fail(e, "decode: main kernel launch");
 #if ZP_DECODE_PREFIX
-    if (a.detached) return launch_tail<T, Dd, G>(a, *pfx, p.grid, st);
+    if (a.detached) return launch_tail<T, Dd, G>(a, *pfx, p.grid, false, st);
 #endif
     return launch_finish<T, Dd, G>(a, p.grid, p.logits_units, st);
 }
