@@ -1359,9 +1359,15 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
         fence_proxy_async_smem();  // these reads of the stage area precede the copies into it
     } else if (kPrefix && longest <= kAlignUnits) {
         // Behind a prefix the sequences may have just begun.  While none has more
-        // than a few units, a CTA takes whole sequences (those that start in its
-        // equal share): the cuts' merge costs more than a share off by a few units.
+        // than a few units, a CTA takes whole sequences -- one each from the first
+        // CTA on while there are as many (those may start beside the prefix kernel's
+        // last CTAs), else those that start in its equal share: the cuts' merge
+        // costs more than a share off by a few units.
         for (int c = tid; c <= (int)gridDim.x; c += blockDim.x) {
+            if (B <= (int)gridDim.x) {
+                cst[c] = prefix[min(c, B)];
+                continue;
+            }
             const long long target = cta_start(c, U, gridDim.x);
             int lo = 0, hi = B;  // the first sequence that starts at or after it
             while (lo < hi) {
