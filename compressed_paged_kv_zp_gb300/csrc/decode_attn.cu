@@ -41,12 +41,12 @@
 
 // decode_attn_prefix.cu compiles this file once more with ZP_DECODE_PREFIX 1:
 // the decode of the tokens behind a shared prefix.  A sequence with a prefix of
-// p tokens (a multiple of b) is then the sequence of its other L - p tokens:
-// its table row starts p/b entries later, its score row p tokens later, and its
-// online softmax starts from the prefix's record (max, sum, accumulator) where
-// a CTA takes its first unit, instead of from nothing; without the score it starts
-// from nothing and prefix_tail_kernel joins its records with the prefix's.  Everything else (the
-// split, the merges, the score) is unchanged.
+// p tokens (a multiple of b) is then the sequence of its other L - p tokens: its
+// table row starts p/b entries later, its score row p tokens later.  The kernels
+// end after their main loop: every sequence that has a prefix or was cut leaves
+// records, prefix_tail_kernel joins them with the prefix's, and the score of all
+// tokens is formed behind that (prefix_attn.cu).  So the decode needs nothing of
+// the prefix kernel and no CTA waits for another.
 #ifndef ZP_DECODE_PREFIX
 #define ZP_DECODE_PREFIX 0
 #endif
@@ -107,14 +107,14 @@ struct DecodeArgs {
     float rho_p;              // similarity threshold p
     int rho_weight16;         // stream-K weight of a unit with row sums, in sixteenths of a plain unit
     unsigned *err;
-    // shared prefix (kPrefix): tokens per batch entry and the records its softmax starts from
+    // shared prefix (kPrefix): tokens per batch entry, and the records of the
+    // sequences behind one that a CTA sees whole
     const int32_t *prefix_lens;  // [B]
-    float *init_acc;             // [B][h_q][D] unnormalised accumulator
-    float2 *init_ml;             // [B][h_q] (max, sum), log2 units
-    int detached;  // no score: start from nothing and leave the records of sequences behind a prefix there
+    float *whole_acc;            // [B][h_q][D] unnormalised accumulator
+    float2 *whole_ml;            // [B][h_q] (max, sum), log2 units
 };
 
-// Tokens of sequence s (of L) that its prefix record covers: none when the plan
+// Tokens of sequence s (of L) that its prefix records cover: none when the plan
 // names more than the L - 1 that precede the newest token (the sequence is then
 // decoded from its first token).
 __device__ __forceinline__ int prefix_of(const DecodeArgs &a, int s, int L) {
@@ -444,29 +444,6 @@ __global__ void __launch_bounds__(kMaxConsumerWarps * 32, 1)
 #pragma unroll
         for (int i = 0; i < NV; ++i) l_own[i] = 0.f;
     };
-    // the state a sequence starts from: its prefix's record when this CTA takes
-    // its first unit (accumulator in the first half-warp of the head's first
-    // warp, the sum in the lanes that own it), else nothing
-    auto start_state = [&](int s, bool first_unit) {
-        reset_state();
-        if constexpr (kPrefix) {
-            if (a.detached || !first_unit || wih != 0 || prefix_of(a, s) == 0) return;
-            const float2 *iml = a.init_ml + (size_t)s * a.h_q + h0;
-#pragma unroll
-            for (int j = 0; j < G; ++j) m[j] = __ldcg(&iml[j]).x;
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (owner) l_own[i] = __ldcg(&iml[jv[i]]).y;
-            if (half == 0) {
-                const float *ia = a.init_acc + ((size_t)s * a.h_q + h0) * D + lane16 * DPL;
-#pragma unroll
-                for (int j = 0; j < G; ++j)
-#pragma unroll
-                    for (int p = 0; p < DPL / 2; ++p)
-                        acc[j][p] = __ldcg(reinterpret_cast<const float2 *>(ia + (size_t)j * D) + p);
-            }
-        }
-    };
     auto load_q = [&](int s) {
         const T *qg = static_cast<const T *>(a.q) + ((size_t)s * a.h_q + h0) * D + lane16 * DPL;
 #pragma unroll
@@ -481,9 +458,7 @@ __global__ void __launch_bounds__(kMaxConsumerWarps * 32, 1)
 
     int s = s_first;
     long long seg_begin = u0;
-    if constexpr (kPrefix)
-        if (!a.detached) pdl_wait();  // the prefix records
-    start_state(s, u0 == prefix[s]);
+    reset_state();
     load_q(s);
     bool window_step = false;
     auto compute_window = [&](int seq) {
@@ -667,7 +642,7 @@ __global__ void __launch_bounds__(kMaxConsumerWarps * 32, 1)
             }
 
             const bool whole = (prefix[s] >= seg_begin) && seq_ends;
-            const bool leave = kPrefix && whole && a.detached && prefix_of(a, s) > 0;  // a record all the same
+            const bool leave = kPrefix && whole && prefix_of(a, s) > 0;  // a record all the same
             if (whole && !leave) {
                 if (wih == 0 && lane < 16) {
                     T *og = static_cast<T *>(a.out) + ((size_t)s * a.h_q + h0) * D + lane16 * DPL;
@@ -686,7 +661,7 @@ __global__ void __launch_bounds__(kMaxConsumerWarps * 32, 1)
                 const int slot = 2 * blockIdx.x + ((prefix[s] <= u0) ? 0 : 1);
                 if (wih == 0 && lane < 16) {
                     const size_t row = (size_t)(leave ? s : slot) * a.h_q + h0;
-                    float *pa = (leave ? a.init_acc : a.part_acc) + row * D + lane16 * DPL;
+                    float *pa = (leave ? a.whole_acc : a.part_acc) + row * D + lane16 * DPL;
 #pragma unroll
                     for (int j = 0; j < G; ++j)
 #pragma unroll
@@ -695,7 +670,7 @@ __global__ void __launch_bounds__(kMaxConsumerWarps * 32, 1)
                     if (lane == 0) {
 #pragma unroll
                         for (int j = 0; j < G; ++j)
-                            (leave ? a.init_ml : a.part_ml)[row + j] = make_float2(m[j], l[j]);
+                            (leave ? a.whole_ml : a.part_ml)[row + j] = make_float2(m[j], l[j]);
                     }
                 }
             }
@@ -703,14 +678,13 @@ __global__ void __launch_bounds__(kMaxConsumerWarps * 32, 1)
             if (u + 1 < u1) {
                 while (u + 1 >= prefix[s + 1]) ++s;
                 seg_begin = u + 1;
-                start_state(s, true);
+                reset_state();
                 load_q(s);
                 window_step = compute_window(s);
             }
         }
     }
-    if constexpr (kPrefix)
-        if (a.detached) pdl_wait();  // the next kernel is then also behind the prefix kernel
+    if constexpr (kPrefix) pdl_wait();  // the next kernel is then also behind the prefix kernel
 }
 
 // Window-score epilogue: one block per unit, one thread per (kv head, token)
@@ -760,7 +734,7 @@ __global__ void __launch_bounds__(128) decode_score_kernel(const DecodeArgs a) {
 #pragma unroll
         for (int j = 0; j < G; ++j) best = fmaxf(best, exp2f(x[j] - ml[j].x) / ml[j].y);
         const float c = best * inv_w;
-        float *dst = a.score + ((size_t)score_row_of(a, s) * a.h_kv + kvh) * a.score_stride + prefix_of(a, s) + tok;
+        float *dst = a.score + ((size_t)score_row_of(a, s) * a.h_kv + kvh) * a.score_stride + tok;
         *dst = (first_row || tok == P) ? c : (*dst + c);
     }
 }
@@ -963,9 +937,6 @@ __device__ void part_stats(const DecodeArgs &a, int s, const int *prefix, const 
             M = Mn;
         }
         out[h] = Lsum > 0.f ? M + log2f(Lsum) : INFINITY;
-        // the prefix's score pass reads every sequence's final statistics (each
-        // part-holder writes the same value)
-        if constexpr (kPrefix) a.stats[(size_t)s * h_q + h] = make_float2(M, Lsum);
     }
 }
 
@@ -1132,7 +1103,7 @@ __device__ void score_segment(const DecodeArgs &a, int s, int L, long long p0, i
     const int RSF = CT + 4;  // score piece stride in floats (bank shift of 4 per kv head)
     float *lg_s = reinterpret_cast<float *>(buf);
     float *sc_s = lg_s + (size_t)CT * HQ;
-    float *srow0 = a.score + (size_t)score_row_of(a, s) * HKV * a.score_stride + prefix_of(a, s);
+    float *srow0 = a.score + (size_t)score_row_of(a, s) * HKV * a.score_stride;
     const float *lg_g = a.logits + ((size_t)p0 * kTcTokens) * HQ;
     fence_proxy_async_smem();  // earlier ordinary writes to buf precede the copies into it
     named_bar_sync(1, nthr);
@@ -1181,7 +1152,7 @@ __device__ void score_prefetched(const DecodeArgs &a, int s, int L, int tb, int 
     fence_proxy_async_smem();
     named_bar_sync_id<BAR>(nthr);
     if (ctid == 0) {
-        float *srow0 = a.score + (size_t)score_row_of(a, s) * HKV * a.score_stride + prefix_of(a, s);
+        float *srow0 = a.score + (size_t)score_row_of(a, s) * HKV * a.score_stride;
 #pragma unroll
         for (int kvh = 0; kvh < HKV; ++kvh)
             bulk_s2g(srow0 + (size_t)kvh * a.score_stride + tb, sc_s + kvh * RSF, (unsigned)(n16 * 4));
@@ -1453,6 +1424,7 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
                 }
             }
             if (lane == 0) {
+                if (kPrefix && a.want_score) a.unit_info[u] = unit_record(a, useq, tok0, lens[useq]);
                 if (bad) record_error(a.err, ZP_ERR_DEVICE, 4);
                 mbar_arrive_expect_tx(&full[st], bad ? 0u : 2u * valid * row_bytes);
             }
@@ -1494,32 +1466,6 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
     };
-    // the state a sequence starts from: its prefix's record when this CTA takes
-    // its first unit, in the lanes that hold the rows and columns of each head
-    auto start_state = [&](int s, bool first_unit) {
-        reset_state();
-        if constexpr (kPrefix) {
-            if (a.detached || !first_unit || prefix_of(a, s) == 0) return;
-            if (g < G) {
-                const float2 ml = __ldcg(&a.init_ml[(size_t)s * a.h_q + h0 + g]);
-                m_run = ml.x;
-                l_run = ml.y;
-            }
-            const float *ia = a.init_acc + ((size_t)s * a.h_q + h0) * D;
-#pragma unroll
-            for (int t = 0; t < KS; ++t) {
-                const int d0 = 16 * t + g;
-                if (2 * tig < G) {
-                    acc[t][0] = __ldcg(ia + (size_t)(2 * tig) * D + d0);
-                    acc[t][2] = __ldcg(ia + (size_t)(2 * tig) * D + d0 + 8);
-                }
-                if (2 * tig + 1 < G) {
-                    acc[t][1] = __ldcg(ia + (size_t)(2 * tig + 1) * D + d0);
-                    acc[t][3] = __ldcg(ia + (size_t)(2 * tig + 1) * D + d0 + 8);
-                }
-            }
-        }
-    };
     auto load_q = [&](int s) {
         const uint32_t *qg = reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(a.q) +
                                                               ((size_t)s * a.h_q + h0 + g) * D);
@@ -1547,9 +1493,7 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
     int s = s_first;
     long long seg_begin = u0;
     const uint64_t keep_pol = l2_evict_last_policy();
-    if constexpr (kPrefix)
-        if (!a.detached) pdl_wait();  // the prefix records (the producer reads only inputs)
-    start_state(s, u0 == prefix[s]);
+    reset_state();
     load_q(s);
     bool window_step = compute_window(s);
     int rho_row = rho_row_of(s);
@@ -1683,7 +1627,7 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
             const float l_hi = __shfl_sync(0xFFFFFFFFu, l_run, (2 * tig + 1) * 4);
             const int hc0 = 2 * tig, hc1 = 2 * tig + 1;  // column heads
             const bool whole = (prefix[s] >= seg_begin) && seq_ends;
-            const bool leave = kPrefix && whole && a.detached && prefix_of(a, s) > 0;  // a record all the same
+            const bool leave = kPrefix && whole && prefix_of(a, s) > 0;  // a record all the same
             if (whole && !leave) {
                 __nv_bfloat16 *og = static_cast<__nv_bfloat16 *>(a.out) + ((size_t)s * a.h_q + h0) * D;
                 const float i0 = l_lo > 0.f ? 1.f / l_lo : 0.f;
@@ -1705,7 +1649,7 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
             } else {
                 const int slot = 2 * blockIdx.x + ((prefix[s] <= u0) ? 0 : 1);
                 const size_t row = (size_t)(leave ? s : slot) * a.h_q + h0;
-                float *pa = (leave ? a.init_acc : a.part_acc) + row * D;
+                float *pa = (leave ? a.whole_acc : a.part_acc) + row * D;
 #pragma unroll
                 for (int t = 0; t < KS; ++t) {
                     const int d0 = 16 * t + g;
@@ -1718,13 +1662,13 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
                         pa[(size_t)hc1 * D + d0 + 8] = acc[t][3];
                     }
                 }
-                if (g < G && tig == 0) (leave ? a.init_ml : a.part_ml)[row + g] = make_float2(m_run, l_run);
+                if (g < G && tig == 0) (leave ? a.whole_ml : a.part_ml)[row + g] = make_float2(m_run, l_run);
                 if (tid == 0) mlist[5 + mlist[4]++] = s;  // announced after the loop
             }
             if (u + 1 < u1) {
                 while (u + 1 >= prefix[s + 1]) ++s;
                 seg_begin = u + 1;
-                start_state(s, true);
+                reset_state();
                 load_q(s);
                 window_step = compute_window(s);
                 rho_row = rho_row_of(s);
@@ -1732,11 +1676,10 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
         }
     }
 
-    if constexpr (kPrefix)
-        if (a.detached) {  // the records are joined by the next kernel
-            pdl_wait();    // (which is then also behind the prefix kernel)
-            return;
-        }
+    if constexpr (kPrefix) {  // the records are joined by the next kernel
+        pdl_wait();           // (which is then also behind the prefix kernel)
+        return;
+    }
     // =====================================================================
     // epilogue (consumer warps; the producer has returned and every stage has
     // been consumed, so the stage area is free scratch)
@@ -1787,8 +1730,7 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
                     float *sc_s = lg_s + (size_t)n16 * HQ;
                     bulk_g2s_plain(lg_s, a.logits + ((size_t)prefix[g.x] * kTcTokens + g.y) * HQ,
                                    (unsigned)(n16 * HQ * 4), ebar);
-                    const float *srow0 =
-                        a.score + (size_t)score_row_of(a, g.x) * h_kv * a.score_stride + prefix_of(a, g.x) + g.y;
+                    const float *srow0 = a.score + (size_t)score_row_of(a, g.x) * h_kv * a.score_stride + g.y;
                     for (int kvh = 0; kvh < h_kv; ++kvh)
                         bulk_g2s_plain(sc_s + kvh * (n16 + 4), srow0 + (size_t)kvh * a.score_stride,
                                        (unsigned)(n16 * 4), ebar);
@@ -2006,10 +1948,6 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
 template <typename T, int D>
 __global__ void __launch_bounds__(256) decode_merge_kernel(const DecodeArgs a, int grid_main) {
     extern __shared__ float2 msm[];  // [grid_main][h_q] (m, l) then weights; then slots, L
-    if constexpr (kPrefix) {
-        pdl_trigger();
-        pdl_wait();
-    }
     const int c = blockIdx.x;
     const int B = a.B;
     const int *pre = a.unit_prefix;
@@ -2105,6 +2043,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     prefix_tail_kernel(const DecodeArgs a, const PfxArgs p, int grid_main, bool may_align) {
     using Join = PfxJoin<D, G, SPLIT>;
     __shared__ typename Join::Smem sm;
+    pdl_trigger();
     const int lane = threadIdx.x & 31;
     const int pair = SPLIT > 1 ? blockIdx.x : blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
     const int s = pair / a.h_kv, head = pair - s * a.h_kv;
@@ -2181,8 +2120,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
                 ml = p.rec_ml + at;
                 acc = p.rec_acc + at * D;
             } else if (whole) {
-                ml = a.init_ml + row;
-                acc = a.init_acc + row * D;
+                ml = a.whole_ml + row;
+                acc = a.whole_acc + row * D;
             } else {
                 const int c = dense ? c_lo + i - n_pre : cta_of(u_b + i - n_pre, U, grid_main);
                 const size_t at = (size_t)(2 * c + (u_b > cta_start(c, U, grid_main) ? 1 : 0)) * a.h_q + head * G;
@@ -2190,9 +2129,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
                 acc = a.part_acc + at * D;
             }
         },
-        [&](int j, int c, const auto &y, float, float L) {
+        [&](int j, int c, const auto &y, float M, float L) {
             constexpr int N = sizeof(y) / 4;
             const float inv = L > 0.f ? 1.f / L : 0.f;
+            if (a.want_score && c == 0) a.stats[row + j] = make_float2(M, L);
             T *dst = static_cast<T *>(a.out) + (row + j) * D + c;
             if constexpr (sizeof(T) == 2) {
                 if constexpr (N == 4)
@@ -2211,14 +2151,15 @@ zp_status launch_tail(const DecodeArgs &a, const PfxArgs &p, int grid, bool may_
     const long long pairs = (long long)a.B * a.h_kv;
     const cudaError_t e =
         pfx_join_split(p) ? launch_dependent(prefix_tail_kernel<T, D, G, kJoinWarps>, dim3((unsigned)pairs),
-                                             dim3(32 * kJoinWarps), 0, st, false, a, p, grid, may_align)
+                                             dim3(32 * kJoinWarps), 0, st, a, p, grid, may_align)
                           : launch_dependent(prefix_tail_kernel<T, D, G, 1>, dim3((unsigned)((pairs + kJoinWarps - 1) / kJoinWarps)),
-                                             dim3(32 * kJoinWarps), 0, st, false, a, p, grid, may_align);
+                                             dim3(32 * kJoinWarps), 0, st, a, p, grid, may_align);
     if (e != cudaSuccess) return cuda_fail(e, "prefix_decode: tail kernel launch");
     return ok();
 }
 #endif
 
+#if !ZP_DECODE_PREFIX
 // Merge kernel, then (window steps) the score epilogue.  (Programmatic
 // dependent launches of these two were measured slightly slower.)
 template <typename T, int D, int G>
@@ -2227,13 +2168,8 @@ zp_status launch_finish(const DecodeArgs &a, int grid, long long units_cap, cuda
     zp_status rs = set_max_dynamic_smem(reinterpret_cast<const void *>(decode_merge_kernel<T, D>), smem,
                                         "decode: merge shared-memory attribute");
     if (rs != ZP_OK) return rs;
-    cudaError_t e = cudaSuccess;
-    if constexpr (kPrefix) {
-        e = launch_dependent(decode_merge_kernel<T, D>, dim3(grid), dim3(256), smem, st, false, a, grid);
-    } else {
-        decode_merge_kernel<T, D><<<grid, 256, smem, st>>>(a, grid);
-        e = cudaGetLastError();
-    }
+    decode_merge_kernel<T, D><<<grid, 256, smem, st>>>(a, grid);
+    cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "decode: merge kernel launch");
     if (a.want_score) {
         decode_score_kernel<G><<<(unsigned)units_cap, 128, 0, st>>>(a);
@@ -2242,6 +2178,7 @@ zp_status launch_finish(const DecodeArgs &a, int grid, long long units_cap, cuda
     }
     return ZP_OK;
 }
+#endif  // !ZP_DECODE_PREFIX
 
 struct Plan {
     bool tc;  // tensor-core kernel (bf16) or CUDA-core kernel
@@ -2323,23 +2260,19 @@ zp_status launch_tc(const DecodeArgs &a, const Plan &p, const PfxArgs *pfx, cuda
     if (rs != ZP_OK) return rs;
     if ((reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v)) % 16)
         return fail(ZP_ERR_INVALID_ARG, "decode: caches must be 16-byte aligned");
-    // cooperative: CTAs wait (bounded) for the merges of other CTAs.  Behind a
-    // prefix and without the score there is no such wait, and an ordinary launch may
-    // start while the kernel before it ends; a cooperative one never does (8
-    // sequences behind 2k tokens: 39 -> 35 us).
+#if ZP_DECODE_PREFIX
+    const cudaError_t e = launch_dependent(kmain, dim3(p.grid), dim3(p.threads), (size_t)p.smem, st, a);
+    if (e != cudaSuccess) return cuda_fail(e, "prefix_decode: decode kernel launch");
+    return launch_tail<__nv_bfloat16, Dd, G>(a, *pfx, p.grid, true, st);
+#else
+    // cooperative: CTAs wait (bounded) for the merges of other CTAs
     DecodeArgs args = a;
     void *params[] = {&args};
-    cudaError_t e = cudaSuccess;
-    if constexpr (kPrefix)
-        e = launch_dependent(kmain, dim3(p.grid), dim3(p.threads), (size_t)p.smem, st, a.want_score != 0, a);
-    else
-        e = cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(kmain), dim3(p.grid), dim3(p.threads), params,
+    cudaError_t e = cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(kmain), dim3(p.grid), dim3(p.threads), params,
                                     (size_t)p.smem, st);
     if (e != cudaSuccess) return cuda_fail(e, "decode: tensor-core kernel launch");
-#if ZP_DECODE_PREFIX
-    if (a.detached) return launch_tail<__nv_bfloat16, Dd, G>(a, *pfx, p.grid, true, st);
-#endif
     return ok();  // merges and the window score run inside the kernel
+#endif
 }
 
 template <typename T, int Dd, int G>
@@ -2348,18 +2281,16 @@ zp_status launch_t(const DecodeArgs &a, const Plan &p, const PfxArgs *pfx, cudaS
     zp_status rs = set_max_dynamic_smem(reinterpret_cast<const void *>(kmain), (size_t)p.smem,
                                         "decode: shared-memory attribute");
     if (rs != ZP_OK) return rs;
-    cudaError_t e = cudaSuccess;
-    if constexpr (kPrefix) {
-        e = launch_dependent(kmain, dim3(p.grid), dim3(p.threads), (size_t)p.smem, st, false, a);
-    } else {
-        kmain<<<p.grid, p.threads, p.smem, st>>>(a);
-        e = cudaGetLastError();
-    }
-    if (e != cudaSuccess) return cuda_fail(e, "decode: main kernel launch");
 #if ZP_DECODE_PREFIX
-    if (a.detached) return launch_tail<T, Dd, G>(a, *pfx, p.grid, false, st);
-#endif
+    const cudaError_t e = launch_dependent(kmain, dim3(p.grid), dim3(p.threads), (size_t)p.smem, st, a);
+    if (e != cudaSuccess) return cuda_fail(e, "prefix_decode: decode kernel launch");
+    return launch_tail<T, Dd, G>(a, *pfx, p.grid, false, st);
+#else
+    kmain<<<p.grid, p.threads, p.smem, st>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "decode: main kernel launch");
     return launch_finish<T, Dd, G>(a, p.grid, p.logits_units, st);
+#endif
 }
 
 }  // namespace
@@ -2461,14 +2392,12 @@ static zp_status decode_impl(const zp_cache_desc *D, const void *q, const void *
     a.err = dev.error_word;
 #if ZP_DECODE_PREFIX
     a.prefix_lens = pfx->prefix;
-    a.init_acc = pfx->init_acc;
-    a.init_ml = pfx->init_ml;
-    a.detached = !a.want_score;
+    a.whole_acc = pfx->whole_acc;
+    a.whole_ml = pfx->whole_ml;
 #else
     a.prefix_lens = nullptr;
-    a.init_acc = nullptr;
-    a.init_ml = nullptr;
-    a.detached = 0;
+    a.whole_acc = nullptr;
+    a.whole_ml = nullptr;
 #endif
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int G = D->h_q / D->h_kv;
@@ -2501,15 +2430,19 @@ static zp_status decode_impl(const zp_cache_desc *D, const void *q, const void *
 zp_status zp::decode_after_prefix(const zp_cache_desc *D, const void *q, const void *k_cache, const void *v_cache,
                                   const int32_t *block_table, int32_t table_stride, const int32_t *seq_lens, int32_t B,
                                   void *out, float *score_accum, const int32_t *score_rows, int32_t n_score_rows,
-                                  int32_t window, const PfxArgs &pfx, void *workspace, size_t workspace_bytes,
-                                  void *stream, const float2 **stats) {
+                                  int32_t window, PfxArgs &pfx, void *workspace, size_t workspace_bytes, void *stream) {
     DeviceInfo dev;
     zp_status rc = device_info(&dev);
     if (rc != ZP_OK) return rc;
     Plan p;
     rc = make_plan(D, B, table_stride, dev, &p);
     if (rc != ZP_OK) return rc;
-    *stats = reinterpret_cast<const float2 *>(static_cast<unsigned char *>(workspace) + p.off_stats);
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    pfx.stats = reinterpret_cast<const float2 *>(ws + p.off_stats);
+    pfx.logits = reinterpret_cast<const float *>(ws + p.off_logits);
+    pfx.units = reinterpret_cast<const int4 *>(ws + p.off_info);
+    pfx.n_units = reinterpret_cast<const int *>(ws + p.off_prefix) + B;
+    pfx.unit_log = __builtin_ctz((unsigned)p.T);
     return decode_impl(D, q, k_cache, v_cache, block_table, table_stride, seq_lens, B, out, score_accum, score_rows,
                        n_score_rows, window, workspace, workspace_bytes, stream, nullptr, &pfx);
 }

@@ -8,13 +8,15 @@
 //     acc_r = sum_t 2^(x_rt - m_r) v_t.
 // (m, l, acc) of every (sequence, q head) and the decode's of the sequence's other
 // tokens (decode_attn_prefix.cu) join to the softmax over all tokens, so the shared
-// keys and values are read once per group instead of once per sequence.  Without
-// the window score the decode leaves records and one kernel joins them with the
-// prefix's; the decode then needs nothing of the prefix kernel and follows it
-// without a gap.  With the score the decode itself starts from the joined prefix
-// records, since its epilogue needs the final (m, l), and these give a second pass
-// over the shared keys for the sequences on a window step:
+// keys and values are read once per group instead of once per sequence.  With the
+// window score, the final (m, l) give a second pass over the shared keys for the
+// sequences on a window step, and over the decode's logits:
 //     S[t] (+)= (1/w) max_{h in group} 2^(x_ht - m_h) / l_h.
+// Chain of launches: the prefix kernel; the decode, which needs nothing of it and
+// follows without a gap; the kernel that joins the records; the score.  (With the
+// decode starting from the joined prefix instead, and its own cooperative merge
+// and score: 8 sequences behind 2k tokens 24 us, not 19; 64 behind 32k 73, not 63;
+// scored 256 behind 4k 157, not 132.)
 //
 // Work: an item is (group, tile of query rows), its length the group's tiles of
 // prefix tokens.  The tiles of all items are concatenated and every set of h_kv
@@ -23,8 +25,7 @@
 // and the CTAs of a set read the heads of the same token rows at the same time.
 // The first piece of an item goes to its rows' place in the main records, a
 // piece that begins inside an item (at most one per CTA) to the CTA's extra
-// records.  (Joined by the decode where it starts a sequence, the scored 256 x 4k
-// batch took 186 us, not 174: a chain of dependent loads against its own traffic.)
+// records.
 #include <math.h>
 
 #include "prefix_tc.h"
@@ -241,58 +242,6 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_part_kernel(const PfxArgs 
     }
 }
 
-// The pieces of every (member, kv head) pair joined, for a decode that starts from
-// them (the scored call).  What depends on the plan alone is done before the wait
-// for the prefix kernel.
-constexpr int kMergeScan = 256;  // groups up to which a warp sums the tiles itself
-template <int D, int G, int SPLIT>
-__global__ void __launch_bounds__(32 * kJoinWarps) prefix_merge_kernel(const PfxArgs a) {
-    pdl_trigger();
-    using Join = PfxJoin<D, G, SPLIT>;
-    __shared__ typename Join::Smem sm;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int ng = pfx_groups(a);
-    const int pair = SPLIT > 1 ? blockIdx.x : blockIdx.x * kJoinWarps + warp;
-    const int mi = pair / a.h_kv, head = pair - mi * a.h_kv;
-    int gi = 0, s = -1, before = 0, W = 0;
-    PfxGroup g = {};
-    if (ng > 0 && mi < a.B) {
-        gi = pfx_group_of(a, ng, mi);
-        g = pfx_group(a, gi);
-        if (mi >= g.m0 && mi < g.m0 + g.n && g.tokens > 0) s = pfx_member(a, mi);
-    }
-    if (s >= 0 && ng <= kMergeScan) {
-        for (int i = lane; i < ng; i += 32) {
-            const PfxGroup o = pfx_group(a, i);
-            W += o.rts * o.kts;
-            if (i < gi) before += o.rts * o.kts;
-        }
-        W = __reduce_add_sync(0xFFFFFFFFu, W);
-        before = __reduce_add_sync(0xFFFFFFFFu, before);
-    }
-    PfxPieces pc = {};
-    if (s >= 0 && ng <= kMergeScan) pc = pfx_pieces(a, g, mi, head, before, W);
-    pdl_wait();
-    if (s < 0) return;
-    if (ng > kMergeScan) pc = pfx_pieces(a, g, mi, head, __ldcg(a.wpre + gi), __ldcg(a.wpre + ng));
-    const size_t row = (size_t)s * a.h_q + head * G;
-    Join::run(
-        sm, pc.n * pc.two,
-        [&](int i, const float2 *&ml, const float *&acc) {
-            const long long at = pfx_record(a, pc, i);
-            ml = a.rec_ml + at;
-            acc = a.rec_acc + at * D;
-        },
-        [&](int j, int c, const auto &y, float M, float L) {
-            constexpr int N = sizeof(y) / 4;
-            float *dst = a.init_acc + (row + j) * D + c;
-            if constexpr (N == 4) *reinterpret_cast<float4 *>(dst) = make_float4(y[0], y[1], y[2], y[3]);
-            else if constexpr (N == 2) *reinterpret_cast<float2 *>(dst) = make_float2(y[0], y[1]);
-            else *dst = y[0];
-            if (c == 0) a.init_ml[row + j] = make_float2(M, L);
-        });
-}
-
 // Window score of the prefix tokens from the final statistics: the logits again,
 // the maximum of x - (m + log2 l) over the q heads of the kv head, one
 // exponential per (sequence, kv head, token).
@@ -306,7 +255,7 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_score_kernel(const PfxArgs
     const int W = pfx_scan(a, ng, pre);
     const int head = blockIdx.x % a.h_kv, set = blockIdx.x / a.h_kv;
     const int w0 = pfx_start(set, W, a.parts), w1 = pfx_start(set + 1, W, a.parts);
-    pdl_wait();  // the decode's statistics
+    pdl_wait();  // the final statistics
     const float inv_w = 1.f / (float)a.window;
     for (int w = w0; w < w1;) {
         const int gi = pfx_find(pre, ng, w);
@@ -374,13 +323,14 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_score_kernel(const PfxArgs
         }
         w += t_e - t_b;
     }
+    pfx_own_scores<G>(a, tid);
 }
 
 struct PfxPlan {
     bool tc;
     int rt, kt, parts;
     long long extra0;
-    size_t off_wpre, off_place, off_rml, off_racc, off_iml, off_iacc, total;
+    size_t off_wpre, off_place, off_rml, off_racc, off_wml, off_wacc, total;
 };
 
 zp_status pfx_plan(const zp_cache_desc *D, int B, const DeviceInfo &dev, PfxPlan *p) {
@@ -405,9 +355,9 @@ zp_status pfx_plan(const zp_cache_desc *D, int B, const DeviceInfo &dev, PfxPlan
     off = align_up(off + recs * 8, 256);
     p->off_racc = off;
     off = align_up(off + recs * d * 4, 256);
-    p->off_iml = off;
+    p->off_wml = off;
     off = align_up(off + rows * 8, 256);
-    p->off_iacc = off;
+    p->off_wacc = off;
     off = align_up(off + rows * d * 4, 256);
     p->total = off;
     return ZP_OK;
@@ -431,30 +381,9 @@ zp_status launch_score(const PfxArgs &a, cudaStream_t st) {
     zp_status rc = set_max_dynamic_smem(reinterpret_cast<const void *>(prefix_score_kernel<D, G>), smem,
                                         "prefix_decode: shared-memory attribute");
     if (rc != ZP_OK) return rc;
-    const cudaError_t e = launch_dependent(prefix_score_kernel<D, G>, dim3(a.parts * a.h_kv), dim3(kPfxThreads), smem, st,
-                                           false, a);
+    const cudaError_t e = launch_dependent(prefix_score_kernel<D, G>, dim3(a.parts * a.h_kv), dim3(kPfxThreads), smem, st, a);
     if (e != cudaSuccess) return cuda_fail(e, "prefix_decode: score kernel launch");
     return ZP_OK;
-}
-
-template <int D, int G>
-zp_status launch_merge_g(const PfxArgs &a, cudaStream_t st) {
-    const long long pairs = (long long)a.B * a.h_kv;
-    const cudaError_t e =
-        pfx_join_split(a) ? launch_dependent(prefix_merge_kernel<D, G, kJoinWarps>, dim3((unsigned)pairs),
-                                             dim3(32 * kJoinWarps), 0, st, false, a)
-                          : launch_dependent(prefix_merge_kernel<D, G, 1>, dim3((unsigned)((pairs + kJoinWarps - 1) / kJoinWarps)),
-                                             dim3(32 * kJoinWarps), 0, st, false, a);
-    if (e != cudaSuccess) return cuda_fail(e, "prefix_decode: merge kernel launch");
-    return ZP_OK;
-}
-
-template <int D>
-zp_status launch_merge(const PfxArgs &a, int G, cudaStream_t st) {
-    if (G == 1) return launch_merge_g<D, 1>(a, st);
-    if (G == 2) return launch_merge_g<D, 2>(a, st);
-    if (G == 4) return launch_merge_g<D, 4>(a, st);
-    return launch_merge_g<D, 8>(a, st);
 }
 
 // fp32 caches: the kernel of the head dimension and group size.
@@ -554,8 +483,8 @@ extern "C" zp_status zp_prefix_decode_attn(const zp_cache_desc *D, const void *q
     a.rec_acc = reinterpret_cast<float *>(ws + p.off_racc);
     a.rec_ml = reinterpret_cast<float2 *>(ws + p.off_rml);
     a.place = reinterpret_cast<int *>(ws + p.off_place);
-    a.init_acc = reinterpret_cast<float *>(ws + p.off_iacc);
-    a.init_ml = reinterpret_cast<float2 *>(ws + p.off_iml);
+    a.whole_acc = reinterpret_cast<float *>(ws + p.off_wacc);
+    a.whole_ml = reinterpret_cast<float2 *>(ws + p.off_wml);
     a.score = score_accum;
     a.score_stride = (long long)table_stride * D->block_size;
     a.score_rows = score_accum ? score_rows : nullptr;
@@ -566,10 +495,9 @@ extern "C" zp_status zp_prefix_decode_attn(const zp_cache_desc *D, const void *q
     const int d = D->head_dim;
     if (p.tc) rc = prefix_part_tc(a, d, st);
     else rc = d == 64 ? launch_part_f32<64>(a, G, st) : launch_part_f32<128>(a, G, st);
-    if (rc == ZP_OK && score_accum) rc = d == 64 ? launch_merge<64>(a, G, st) : launch_merge<128>(a, G, st);
     if (rc != ZP_OK) return rc;
     rc = decode_after_prefix(D, q, k_cache, v_cache, block_table, table_stride, seq_lens, B, out, score_accum, score_rows,
-                             n_score_rows, window, a, workspace, dec, stream, &a.stats);
+                             n_score_rows, window, a, workspace, dec, stream);
     if (rc != ZP_OK) return rc;
     if (score_accum) {
         if (p.tc) rc = prefix_score_tc(a, d, st);

@@ -29,14 +29,18 @@ struct PfxArgs {
     long long extra0;    // first extra record: B*h_q, twice that on the tensor cores (second streams);
                          // then rt rows per CTA (set * h_kv + head)
     int tc;              // tensor-core kernels: 256 rows x 128 tokens, two streams
-    float *init_acc;     // [B][h_q][d] joined accumulators
-    float2 *init_ml;     // [B][h_q] joined (max, sum)
+    float *whole_acc;    // [B][h_q][d] the decode's records of sequences that one CTA saw whole
+    float2 *whole_ml;    // [B][h_q]
     // score
     float *score;
     long long score_stride;
     const int32_t *score_rows;
     int n_score_rows, window;
     const float2 *stats;  // [B][h_q] final (max, sum)
+    const float *logits;  // the decode's: [units][tokens of a unit][h_q], log2 units
+    const int4 *units;    // [units] (sequence, first token, length behind the prefix, window flags)
+    const int *n_units;   // [1]
+    int unit_log;         // tokens of a unit, a power of two
     unsigned *err;
 };
 
@@ -340,6 +344,69 @@ struct PfxJoin {
         }
     }
 };
+
+// Window score of the tokens behind the prefixes, from the decode's logits and the
+// final statistics: S[t] (+)= (1/w) max_{h in group} 2^(x_ht - m_h) / l_h, written
+// instead of added at the first window row and for the newest token.  A share of
+// the units per CTA, a thread per (token, kv head) of a unit (at most 256 of them:
+// the units' bytes bound it); consecutive threads take consecutive tokens, and a
+// thread's kv head stays, so its statistics are read when the sequence changes.
+template <int G>
+__device__ __forceinline__ void pfx_own_scores(const PfxArgs &a, int tid) {
+    const int U = __ldcg(a.n_units);
+    const int u0 = (int)((long long)U * blockIdx.x / gridDim.x), u1 = (int)((long long)U * (blockIdx.x + 1) / gridDim.x);
+    const int items = a.h_kv << a.unit_log, per = 256 / items;
+    const int q = tid / items, kvh = (tid >> a.unit_log) % a.h_kv, tl = tid & ((1 << a.unit_log) - 1);
+    const float inv_w = 1.f / (float)a.window;
+    constexpr int K = G <= 4 ? 8 : 4;  // units in flight per thread
+    int last = -1;
+    float *row = nullptr;
+    float c[G];
+#pragma unroll
+    for (int j = 0; j < G; ++j) c[j] = INFINITY;
+    for (int ub = u0 + q; ub < u1; ub += K * per) {
+        int4 info[K];
+        float x[K][G], old[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int u = ub + k * per;
+            info[k] = u < u1 ? __ldcg(a.units + u) : make_int4(0, 0, 0, 0);
+            // (logits of units that are not on a window step hold anything)
+            const float *lg = a.logits + (((size_t)min(u, u1 - 1) << a.unit_log) + tl) * a.h_q + kvh * G;
+            if constexpr (G >= 4) {
+#pragma unroll
+                for (int j = 0; j < G; j += 4)
+                    *reinterpret_cast<float4 *>(&x[k][j]) = __ldcg(reinterpret_cast<const float4 *>(lg + j));
+            } else {
+#pragma unroll
+                for (int j = 0; j < G; ++j) x[k][j] = __ldcg(lg + j);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int tok = info[k].y + tl;
+            const bool on = (info[k].w & 1) && tok < info[k].z;
+            if (on && info[k].x != last) {
+                last = info[k].x;
+#pragma unroll
+                for (int j = 0; j < G; ++j) {
+                    const float2 ml = __ldcg(a.stats + (size_t)last * a.h_q + kvh * G + j);
+                    c[j] = ml.y > 0.f ? ml.x + log2f(ml.y) : INFINITY;
+                }
+                // the row was checked by the decode (a unit without one carries no window flag)
+                const int r = a.score_rows ? __ldg(a.score_rows + last) : last;
+                const int first_tok = min(__ldg(a.seq_lens + last), a.stride * a.b) - info[k].z;
+                row = a.score + ((size_t)r * a.h_kv + kvh) * a.score_stride + first_tok;
+            }
+            const bool add = on && !(info[k].w & 2) && tok != info[k].z - 1;
+            old[k] = ld_if(row + tok, add);
+            float e = x[k][0] - c[0];
+#pragma unroll
+            for (int j = 1; j < G; ++j) e = fmaxf(e, x[k][j] - c[j]);
+            st_if(row + tok, fmaf(exp2f(e), inv_w, old[k]), on);
+        }
+    }
+}
 
 // Host: four warps per pair while the pairs' CTAs are resident at once.
 inline bool pfx_join_split(const PfxArgs &a) { return (long long)a.B * a.h_kv <= 8LL * a.parts * a.h_kv; }

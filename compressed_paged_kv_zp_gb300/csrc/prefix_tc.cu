@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
             }
             if (!ok_all) break;
-            pdl_trigger();  // (the merge waits for this kernel's end)
+            pdl_trigger();  // (the decode does not read the records)
             // the piece's record: 64 dims of the warp's 32 rows at a time through the
             // stream's query tile (its products are complete), so that stores are
             // whole 128-byte lines; chunk c of row i sits at c ^ (i & 7)
@@ -471,7 +471,7 @@ struct PsCfg {
     static constexpr int TILE = kPtTile / 8 * GROUP;   // K tile
     static constexpr int B_HALF = kPtRows * 128;       // 256 query rows x 64 elements
     static constexpr int B_BYTES = KH * B_HALF;
-    static constexpr int STAGES = 4;
+    static constexpr int STAGES = 3;  // (leaves room for CTAs of the kernel before, so that this one starts beside it)
     static constexpr int ST_OFF = B_BYTES;
     static constexpr int BAR_OFF = ST_OFF + STAGES * TILE;
     static constexpr int C_OFF = BAR_OFF + 256;        // c of every row
@@ -612,8 +612,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             if (lane == 0) mbar_arrive(q_full);
             bool first = false;
             const int row = e >= 0 ? pfx_score_row(a, e, &first) : -1;
-            // only the statistics and the score rows wait for the decode: the first
-            // products run while it ends
+            // only the statistics wait for the kernel that joins the records: the first
+            // products run before it ends
             if (!waited) pdl_wait();
             waited = true;
             float c = INFINITY;
@@ -677,6 +677,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             w += s.t_e - s.t_b;
         }
         if (!waited) pdl_wait();
+        if (ok_all) pfx_own_scores<G>(a, et);
     }
     __syncthreads();
     tc_fence_before();
@@ -719,7 +720,7 @@ zp_status launch_score_tc(const PfxArgs &a, cudaStream_t st) {
                               "prefix_decode: shared-memory attribute");
     if (rc != ZP_OK) return rc;
     const cudaError_t e = launch_dependent(prefix_score_tc_kernel<D, G>, dim3(a.parts * a.h_kv), dim3(kPtThreads), smem, st,
-                                           false, km, a);
+                                           km, a);
     if (e != cudaSuccess) return cuda_fail(e, "prefix_decode: score kernel launch");
     return ZP_OK;
 }

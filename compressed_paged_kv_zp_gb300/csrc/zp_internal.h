@@ -66,32 +66,29 @@ zp_status launch_all_pairs(const AllPairsArgs &a, cudaStream_t st);
 // Host: launch as a programmatic dependent of the kernel before it on the stream
 // (the kernel calls pdl_wait() before it reads what that one writes).
 template <typename... P, typename... A>
-inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                                    bool cooperative, A &&...args) {
+inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A &&...args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeCooperative;
-    attr[1].val.cooperative = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = cooperative ? 2 : 1;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
-// zp_paged_decode_attn of the tokens behind the prefixes (arguments checked as
-// there; the workspace is the decode's), each sequence continuing from its
-// records of the prefix kernels (pfx).  *stats: the workspace's [B][h_q] final
-// (max, sum) of every entry that is on a window step, when scoring.
+// The decode of the tokens behind the prefixes (arguments checked as for
+// zp_paged_decode_attn; the workspace is the decode's), its records joined with
+// those of the prefix kernel (pfx) into the outputs.  With score_accum it leaves,
+// and tells pfx, what the score of all tokens needs: the final statistics of every
+// entry, the logits of the entries on a window step and the units they lie in.
 struct PfxArgs;
 zp_status decode_after_prefix(const zp_cache_desc *D, const void *q, const void *k_cache, const void *v_cache,
                               const int32_t *block_table, int32_t table_stride, const int32_t *seq_lens, int32_t B,
                               void *out, float *score_accum, const int32_t *score_rows, int32_t n_score_rows,
-                              int32_t window, const PfxArgs &pfx, void *workspace, size_t workspace_bytes,
-                              void *stream, const float2 **stats);
+                              int32_t window, PfxArgs &pfx, void *workspace, size_t workspace_bytes, void *stream);
 
 }  // namespace zp
