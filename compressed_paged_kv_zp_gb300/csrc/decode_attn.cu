@@ -128,6 +128,14 @@ __device__ __forceinline__ int prefix_of(const DecodeArgs &a, int s) {
     return prefix_of(a, s, min(__ldg(&a.seq_lens[s]), a.table_stride * a.b));
 }
 
+// Final statistics of q head h of sequence s: (max, sum), or behind a prefix, where
+// only the score reads them, c = max + log2(sum) (+inf for an empty sum).
+__device__ __forceinline__ void put_stats(const DecodeArgs &a, int s, int h, float m, float l) {
+    const size_t i = (size_t)s * a.h_q + h;
+    if constexpr (kPrefix) reinterpret_cast<float *>(a.stats)[i] = l > 0.f ? m + log2f(l) : INFINITY;
+    else a.stats[i] = make_float2(m, l);
+}
+
 // Reduce-scatter of V per-lane values over the 16 lanes of a half-warp (lane
 // bits 3..0, high bit first).  Afterwards lane l holds in v[0..max(V/16,1))
 // the full sums of indices l*(V/16)+i (V >= 16) or l/(16/V) (V < 16).
@@ -653,7 +661,7 @@ __global__ void __launch_bounds__(kMaxConsumerWarps * 32, 1)
                     }
                     if (a.want_score && lane == 0) {
 #pragma unroll
-                        for (int j = 0; j < G; ++j) a.stats[(size_t)s * a.h_q + h0 + j] = make_float2(m[j], l[j]);
+                        for (int j = 0; j < G; ++j) put_stats(a, s, h0 + j, m[j], l[j]);
                     }
                 }
             } else {
@@ -1644,8 +1652,7 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
                         og[(size_t)hc1 * D + d0 + 8] = __float2bfloat16_rn(acc[t][3] * i1);
                     }
                 }
-                if (a.want_score && g < G && tig == 0)
-                    a.stats[(size_t)s * a.h_q + h0 + g] = make_float2(m_run, l_run);
+                if (a.want_score && g < G && tig == 0) put_stats(a, s, h0 + g, m_run, l_run);
             } else {
                 const int slot = 2 * blockIdx.x + ((prefix[s] <= u0) ? 0 : 1);
                 const size_t row = (size_t)(leave ? s : slot) * a.h_q + h0;
@@ -2132,7 +2139,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
         [&](int j, int c, const auto &y, float M, float L) {
             constexpr int N = sizeof(y) / 4;
             const float inv = L > 0.f ? 1.f / L : 0.f;
-            if (a.want_score && c == 0) a.stats[row + j] = make_float2(M, L);
+            if (a.want_score && c == 0) put_stats(a, s, head * G + j, M, L);
             T *dst = static_cast<T *>(a.out) + (row + j) * D + c;
             if constexpr (sizeof(T) == 2) {
                 if constexpr (N == 4)
@@ -2438,7 +2445,7 @@ zp_status zp::decode_after_prefix(const zp_cache_desc *D, const void *q, const v
     rc = make_plan(D, B, table_stride, dev, &p);
     if (rc != ZP_OK) return rc;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
-    pfx.stats = reinterpret_cast<const float2 *>(ws + p.off_stats);
+    pfx.stats = reinterpret_cast<const float *>(ws + p.off_stats);
     pfx.logits = reinterpret_cast<const float *>(ws + p.off_logits);
     pfx.units = reinterpret_cast<const int4 *>(ws + p.off_info);
     pfx.n_units = reinterpret_cast<const int *>(ws + p.off_prefix) + B;

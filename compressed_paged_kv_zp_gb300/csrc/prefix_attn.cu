@@ -280,10 +280,7 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_score_kernel(const PfxArgs
                 const int s = pfx_member(a, g.m0 + r / G);
                 if (s >= 0) {
                     srow[i] = pfx_score_row(a, s, &first[i]);
-                    if (srow[i] >= 0) {
-                        const float2 ml = a.stats[(size_t)s * a.h_q + head * G + r % G];
-                        c[i] = ml.y > 0.f ? ml.x + log2f(ml.y) : INFINITY;
-                    }
+                    if (srow[i] >= 0) c[i] = __ldcg(a.stats + (size_t)s * a.h_q + head * G + r % G);
                 }
             }
         }
@@ -323,7 +320,7 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_score_kernel(const PfxArgs
         }
         w += t_e - t_b;
     }
-    pfx_own_scores<G>(a, tid);
+    pfx_own_scores<G, kPfxThreads>(a, tid);
 }
 
 struct PfxPlan {

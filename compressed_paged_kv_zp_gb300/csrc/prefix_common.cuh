@@ -36,7 +36,7 @@ struct PfxArgs {
     long long score_stride;
     const int32_t *score_rows;
     int n_score_rows, window;
-    const float2 *stats;  // [B][h_q] final (max, sum)
+    const float *stats;   // [B][h_q] final max + log2(sum)
     const float *logits;  // the decode's: [units][tokens of a unit][h_q], log2 units
     const int4 *units;    // [units] (sequence, first token, length behind the prefix, window flags)
     const int *n_units;   // [1]
@@ -351,14 +351,14 @@ struct PfxJoin {
 // the units per CTA, a thread per (token, kv head) of a unit (at most 256 of them:
 // the units' bytes bound it); consecutive threads take consecutive tokens, and a
 // thread's kv head stays, so its statistics are read when the sequence changes.
-template <int G>
+template <int G, int THREADS>
 __device__ __forceinline__ void pfx_own_scores(const PfxArgs &a, int tid) {
     const int U = __ldcg(a.n_units);
     const int u0 = (int)((long long)U * blockIdx.x / gridDim.x), u1 = (int)((long long)U * (blockIdx.x + 1) / gridDim.x);
-    const int items = a.h_kv << a.unit_log, per = 256 / items;
+    const int items = a.h_kv << a.unit_log, per = THREADS / items;
     const int q = tid / items, kvh = (tid >> a.unit_log) % a.h_kv, tl = tid & ((1 << a.unit_log) - 1);
     const float inv_w = 1.f / (float)a.window;
-    constexpr int K = G <= 4 ? 8 : 4;  // units in flight per thread
+    constexpr int K = G <= 4 && THREADS <= 256 ? 8 : 4;  // units in flight per thread
     int last = -1;
     float *row = nullptr;
     float c[G];
@@ -389,10 +389,7 @@ __device__ __forceinline__ void pfx_own_scores(const PfxArgs &a, int tid) {
             if (on && info[k].x != last) {
                 last = info[k].x;
 #pragma unroll
-                for (int j = 0; j < G; ++j) {
-                    const float2 ml = __ldcg(a.stats + (size_t)last * a.h_q + kvh * G + j);
-                    c[j] = ml.y > 0.f ? ml.x + log2f(ml.y) : INFINITY;
-                }
+                for (int j = 0; j < G; ++j) c[j] = __ldcg(a.stats + (size_t)last * a.h_q + kvh * G + j);
                 // the row was checked by the decode (a unit without one carries no window flag)
                 const int r = a.score_rows ? __ldg(a.score_rows + last) : last;
                 const int first_tok = min(__ldg(a.seq_lens + last), a.stride * a.b) - info[k].z;

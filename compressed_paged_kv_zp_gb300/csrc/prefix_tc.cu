@@ -32,6 +32,8 @@ namespace {
 
 constexpr int kPtTile = 128;                // prefix tokens per tile
 constexpr int kPtThreads = 32 * (2 + 8);    // TMA, MMA, two warpgroups
+constexpr int kPsEpi = 16;                  // epilogue warps of the score kernel
+constexpr int kPsThreads = 32 * (2 + kPsEpi);
 constexpr float kPtRaise = 8.f;             // log2 units a tile may exceed the running maximum by
 
 // tcgen05.mma with A in tensor memory (bf16 pairs, one row per lane).
@@ -481,7 +483,7 @@ struct PsCfg {
 };
 
 template <int D, int G>
-__global__ void __launch_bounds__(kPtThreads, 1)
+__global__ void __launch_bounds__(kPsThreads, 1)
     prefix_score_tc_kernel(const __grid_constant__ CUtensorMap kmap, const PfxArgs a) {
     using C = PsCfg<D>;
     extern __shared__ unsigned char pt_raw[];
@@ -507,12 +509,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
-        mbar_init(q_full, 8);
+        mbar_init(q_full, 8);  // (the first eight epilogue warps, a row per thread)
         mbar_init(c_full, 8);
-        mbar_init(q_done, 8);
+        mbar_init(q_done, kPsEpi);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], 8);
+            mbar_init(&acc_empty[i], kPsEpi);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -594,8 +596,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         }
         __syncwarp();
     } else {
-        const int et = threadIdx.x - 64;          // 0..255: query row while loading
-        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const int et = threadIdx.x - 64;  // below 256: query row while loading
+        const int quarter = warp & 3, col0 = ((warp - 2) >> 2) * (kPtRows * 4 / kPsEpi);  // lanes, 64 columns
         const float inv_w = 1.f / (float)a.window;
         uint32_t tile = 0, item = 0;
         bool ok_all = true, waited = false;
@@ -605,27 +607,28 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             // the item's rows: once every warp has finished the last item (whose
             // products are then complete)
             if (!mbar_wait_bounded(q_done, (item & 1) ^ 1, a.err, abort_flag, 0x618)) break;
-            int e;
-            pt_load_q<D>(pt_query<D>(a, s, head, et, &e), et & ~31, smem, C::B_HALF);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_full);
+            int e = -1, row = -1;
             bool first = false;
-            const int row = e >= 0 ? pfx_score_row(a, e, &first) : -1;
+            if (et < kPtRows) {
+                pt_load_q<D>(pt_query<D>(a, s, head, et, &e), et & ~31, smem, C::B_HALF);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full);
+                row = e >= 0 ? pfx_score_row(a, e, &first) : -1;
+            }
             // only the statistics wait for the kernel that joins the records: the first
             // products run before it ends
             if (!waited) pdl_wait();
             waited = true;
-            float c = INFINITY;
-            if (row >= 0) {
-                const float2 ml = __ldcg(a.stats + (size_t)e * a.h_q + head * G + (s.rt * kPtRows + et) % G);
-                c = ml.y > 0.f ? ml.x + log2f(ml.y) : INFINITY;
+            if (et < kPtRows) {
+                float c = INFINITY;
+                if (row >= 0) c = __ldcg(a.stats + (size_t)e * a.h_q + head * G + (s.rt * kPtRows + et) % G);
+                cs[et] = c;
+                if (et % G == 0)
+                    ms[et / G] = row >= 0 ? ((long long)row * a.h_kv + head) * a.score_stride * 2 + (first ? 1 : 0) : -1;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(c_full);
             }
-            cs[et] = c;
-            if (et % G == 0)
-                ms[et / G] = row >= 0 ? ((long long)row * a.h_kv + head) * a.score_stride * 2 + (first ? 1 : 0) : -1;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(c_full);
             if (!mbar_wait_bounded(c_full, item & 1, a.err, abort_flag, 0x619)) break;
             for (int t = s.t_b; t < s.t_e; ++t, ++tile) {
                 const uint32_t ab = tile & 1;
@@ -635,24 +638,24 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 }
                 tc_fence_after();
                 const int tok = t * kPtTile + 32 * quarter + lane;
-                const uint32_t acc = tmem + ((uint32_t)(32 * quarter) << 16) + ab * 256 + half * 128;
+                const uint32_t acc = tmem + ((uint32_t)(32 * quarter) << 16) + ab * 256 + col0;
                 const bool live = tok < s.g.tokens;
                 float *col = a.score + tok;
 #pragma unroll 1
-                for (int c0 = 0; c0 < 128; c0 += 32) {
-                    if (half * 128 + c0 >= s.rows) break;
-                    uint32_t v[32];
-                    tmem_ld32(acc + c0, v);
+                for (int c0 = 0; c0 < kPtRows * 4 / kPsEpi; c0 += 16) {
+                    if (col0 + c0 >= s.rows) break;
+                    uint32_t v[16];
+                    tmem_ld16(acc + c0, v);
                     // statistics and score rows first, then the old scores where there are
                     // any: the loads of a chunk are in flight together
-                    constexpr int N = 32 / G;
-                    float c[32];
+                    constexpr int N = 16 / G;
+                    float c[16];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        *reinterpret_cast<float4 *>(c + 4 * j) = reinterpret_cast<const float4 *>(cs + half * 128 + c0)[j];
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<float4 *>(c + 4 * j) = reinterpret_cast<const float4 *>(cs + col0 + c0)[j];
                     long long mr[N];
 #pragma unroll
-                    for (int i = 0; i < N; ++i) mr[i] = ms[(half * 128 + c0) / G + i];
+                    for (int i = 0; i < N; ++i) mr[i] = ms[(col0 + c0) / G + i];
                     float old[N];
 #pragma unroll
                     for (int i = 0; i < N; ++i) old[i] = ld_if(col + (mr[i] >> 1), live && mr[i] >= 0 && !(mr[i] & 1));
@@ -677,7 +680,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             w += s.t_e - s.t_b;
         }
         if (!waited) pdl_wait();
-        if (ok_all) pfx_own_scores<G>(a, et);
+        if (ok_all) pfx_own_scores<G, 32 * kPsEpi>(a, et);
     }
     __syncthreads();
     tc_fence_before();
@@ -719,7 +722,7 @@ zp_status launch_score_tc(const PfxArgs &a, cudaStream_t st) {
     rc = set_max_dynamic_smem(reinterpret_cast<const void *>(prefix_score_tc_kernel<D, G>), smem,
                               "prefix_decode: shared-memory attribute");
     if (rc != ZP_OK) return rc;
-    const cudaError_t e = launch_dependent(prefix_score_tc_kernel<D, G>, dim3(a.parts * a.h_kv), dim3(kPtThreads), smem, st,
+    const cudaError_t e = launch_dependent(prefix_score_tc_kernel<D, G>, dim3(a.parts * a.h_kv), dim3(kPsThreads), smem, st,
                                            km, a);
     if (e != cudaSuccess) return cuda_fail(e, "prefix_decode: score kernel launch");
     return ZP_OK;
