@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_score_kernel(const PfxArgs
     const int W = pfx_scan(a, ng, pre);
     const int head = blockIdx.x % a.h_kv, set = blockIdx.x / a.h_kv;
     const int w0 = pfx_start(set, W, a.parts), w1 = pfx_start(set + 1, W, a.parts);
-    pdl_wait();  // the final statistics
+    bool waited = false;
     const float inv_w = 1.f / (float)a.window;
     for (int w = w0; w < w1;) {
         const int gi = pfx_find(pre, ng, w);
@@ -266,21 +266,23 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_score_kernel(const PfxArgs
         const int32_t *row = pfx_row(a, g);
         __syncthreads();
         pfx_load_q<D, G>(a, g, head, r0, sm);
-        // score row and c = m + log2 l of this thread's rows
+        // score row of this thread's rows, and where their c = m + log2 l stands
         float c[4];
+        const float *c_at[4];
         int srow[4];
         bool first[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = r0 + ty * 4 + i;
             c[i] = INFINITY;
+            c_at[i] = a.stats;
             srow[i] = -1;
             first[i] = false;
             if (r < g.n * G) {
                 const int s = pfx_member(a, g.m0 + r / G);
                 if (s >= 0) {
                     srow[i] = pfx_score_row(a, s, &first[i]);
-                    if (srow[i] >= 0) c[i] = __ldcg(a.stats + (size_t)s * a.h_q + head * G + r % G);
+                    c_at[i] = a.stats + (size_t)s * a.h_q + head * G + r % G;
                 }
             }
         }
@@ -294,11 +296,27 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_score_kernel(const PfxArgs
             __syncthreads();
             if (t + 1 < t_e) next.load(a, g, row, head, t0 + kPfxTokens);
             if (!live) continue;
+            constexpr int S = G >= 4 ? 4 : G;  // a score per S rows
+            auto at = [&](int i, int j) {
+                return a.score + ((size_t)max(srow[i], 0) * a.h_kv + head) * a.score_stride + t0 + tx + 16 * j;
+            };
+            auto on = [&](int i, int j) { return t0 + tx + 16 * j < g.tokens && srow[i] >= 0 && !(G == 8 && (ty & 1)); };
+            float old[4][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; i += S) old[i][j] = ld_if(at(i, j), on(i, j) && !first[i]);
             float x[4][4];
             pfx_logits<D>(sm, ty, tx, x);
+            if (t == t_b) {  // the final statistics: the first logits are formed before they are
+                if (!waited) pdl_wait();
+                waited = true;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (srow[i] >= 0) c[i] = __ldcg(c_at[i]);
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int tok = t0 + tx + 16 * j;
                 float e[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) e[i] = x[i][j] - c[i];
@@ -311,15 +329,12 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_score_kernel(const PfxArgs
                 if constexpr (G >= 4) e[0] = fmaxf(e[0], e[2]);
                 if constexpr (G == 8) e[0] = fmaxf(e[0], __shfl_xor_sync(0xFFFFFFFFu, e[0], 16));
 #pragma unroll
-                for (int i = 0; i < 4; i += (G >= 4 ? 4 : G)) {
-                    const bool on = tok < g.tokens && srow[i] >= 0 && !(G == 8 && (ty & 1));
-                    float *dst = a.score + ((size_t)max(srow[i], 0) * a.h_kv + head) * a.score_stride + tok;
-                    st_if(dst, exp2f(e[i]) * inv_w + ld_if(dst, on && !first[i]), on);
-                }
+                for (int i = 0; i < 4; i += S) st_if(at(i, j), exp2f(e[i]) * inv_w + old[i][j], on(i, j));
             }
         }
         w += t_e - t_b;
     }
+    if (!waited) pdl_wait();
     pfx_own_scores<G, kPfxThreads>(a, tid);
 }
 

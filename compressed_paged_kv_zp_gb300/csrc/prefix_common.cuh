@@ -231,9 +231,10 @@ __device__ __forceinline__ void ld_row(const float *p, float (&v)[V]) {
 // warps of a CTA of four,
 //     M = max_j m_j,  L = sum_j 2^(m_j - M) l_j,  acc = sum_j 2^(m_j - M) acc_j.
 // A share of the records per warp and, for SPLIT > 1, the warps' results joined in
-// shared memory.  Lane i finds record i and its (m, l), 32 at a time, and lists
-// those that hold anything, so that the loads of the statistics, and then of the
-// accumulators, are in flight together: bound by the latency of these two.
+// shared memory.  Lane i finds record i and its (m, l), 32 at a time; the first
+// accumulators are fetched beside the statistics, the others, once it is known which
+// records hold anything, U at a time: bound by the latency of these loads.  (With the
+// first accumulators behind the statistics: a chain 1 to 2 us longer.)
 //   rec(i, ml, acc)  the first row of record i in [0, n): statistics, accumulator
 //   put(j, c, y, M, L)  takes V consecutive dims from c of row j (SPLIT 1: V = D/32,
 //                       else 1), unnormalised
@@ -245,6 +246,7 @@ constexpr int kJoinWarps = 4;
 template <int D, int G, int SPLIT>
 struct PfxJoin {
     static constexpr int V = D / 32;
+    static constexpr int U = G <= 4 ? 4 : 2;  // records in flight per warp (twice as many: fewer CTAs, 64 x 32k 64 us, not 60)
     struct Smem {
         const float *src[kJoinWarps][32];
         float f[kJoinWarps][32][G];
@@ -270,21 +272,35 @@ struct PfxJoin {
             const float2 *ml_p = nullptr;
             const float *acc_p = nullptr;
             if (has) rec(p0 + lane, ml_p, acc_p);
+            sm.src[warp][lane] = acc_p;
             float2 ml[G];
 #pragma unroll
             for (int j = 0; j < G; ++j) ml[j] = has ? __ldcg(ml_p + j) : make_float2(-INFINITY, 0.f);
+            __syncwarp();
+            // the first records' accumulators do not wait for the statistics (those of a
+            // record that holds nothing are never written: read, and left out)
+            float v[U][G][V];
+            const int last = min(n_e - p0, 32) - 1;
+            auto fetch = [&](int u, int i) {
+                const float *src = sm.src[warp][i] + lane * V;
+#pragma unroll
+                for (int j = 0; j < G; ++j) ld_row<V>(src + j * D, v[u][j]);
+            };
+#pragma unroll
+            for (int u = 0; u < U; ++u) fetch(u, min(u, last));
             const bool holds = ml[0].x != -INFINITY;  // else a stream without a tile: no accumulator either
-            const unsigned mask = __ballot_sync(0xFFFFFFFFu, holds);
-            if (mask == 0) continue;
-            const int at_i = __popc(mask & ((1u << lane) - 1));
-            if (holds) sm.src[warp][at_i] = acc_p;
+            unsigned mask = __ballot_sync(0xFFFFFFFFu, holds);
+            if (mask == 0) {
+                __syncwarp();
+                continue;
+            }
 #pragma unroll
             for (int j = 0; j < G; ++j) {
                 float Mn = fmaxf(M[j], ml[j].x);
 #pragma unroll
                 for (int o = 16; o; o >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(0xFFFFFFFFu, Mn, o));
                 const float f = holds ? exp2f(ml[j].x - Mn) : 0.f;
-                if (holds) sm.f[warp][at_i][j] = f;
+                sm.f[warp][lane][j] = f;
                 float ls = f * ml[j].y;
 #pragma unroll
                 for (int o = 16; o; o >>= 1) ls += __shfl_xor_sync(0xFFFFFFFFu, ls, o);
@@ -295,25 +311,28 @@ struct PfxJoin {
                 for (int e = 0; e < V; ++e) x[j][e] *= old;
             }
             __syncwarp();
-            const int here = __popc(mask);
-            constexpr int U = G <= 4 ? 4 : 2;  // records in flight
-#pragma unroll 1
-            for (int k0 = 0; k0 < here; k0 += U) {
-                float v[U][G][V];
+            int at[U];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {  // behind the last: the first record with weight 0
-                    const float *src = sm.src[warp][k0 + u < here ? k0 + u : 0] + lane * V;
-#pragma unroll
-                    for (int j = 0; j < G; ++j) ld_row<V>(src + j * D, v[u][j]);
-                }
+            for (int u = 0; u < U; ++u) at[u] = (mask >> u) & 1 ? u : -1;
+            mask &= ~((1u << U) - 1);
+            while (true) {
 #pragma unroll
                 for (int u = 0; u < U; ++u)
+                    if (at[u] >= 0) {
 #pragma unroll
-                    for (int j = 0; j < G; ++j) {
-                        const float f = k0 + u < here ? sm.f[warp][k0 + u][j] : 0.f;
+                        for (int j = 0; j < G; ++j) {
+                            const float f = sm.f[warp][at[u]][j];
 #pragma unroll
-                        for (int e = 0; e < V; ++e) x[j][e] = fmaf(f, v[u][j][e], x[j][e]);
+                            for (int e = 0; e < V; ++e) x[j][e] = fmaf(f, v[u][j][e], x[j][e]);
+                        }
                     }
+                if (mask == 0) break;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    at[u] = __ffs(mask) - 1;  // -1: none left
+                    mask &= mask - 1;
+                    if (at[u] >= 0) fetch(u, at[u]);
+                }
             }
             __syncwarp();
         }
