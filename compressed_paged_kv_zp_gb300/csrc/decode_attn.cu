@@ -2039,14 +2039,17 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(const DecodeArgs a, i
 #if ZP_DECODE_PREFIX
 // Output of every sequence that has more than one record: those of its prefix and
 // of the decode (one that it saw whole, else one per CTA that took units of it).
+// Four CTAs per SM (at most 128 registers): 512 of them, the usual number, are on the
+// GPU at once, and the score, which starts when all have, can begin with its products.
 // The split follows from the lengths and the plan, so up to kTailScanB entries a
 // warp works it out before the wait for the decode, and only the records are read
-// after it (64 sequences behind 32k tokens: 3 us after the wait, not 8); beyond,
-// it is read from what the kernels before left in the workspace.
+// after it (64 sequences behind 32k tokens: 63 us in all, not 65); beyond, it is read
+// from what the kernels before left in the workspace.  Bound by latency: 4 to 7 us
+// after the wait, of which the records' bytes (42 MB through L2 there) are 3.
 constexpr int kTailScanB = 512;
 constexpr int kTailScanGroups = 256;
 template <typename T, int D, int G, int SPLIT>
-__global__ void __launch_bounds__(32 * kJoinWarps)
+__global__ void __launch_bounds__(32 * kJoinWarps, G <= 4 ? 4 : 3)
     prefix_tail_kernel(const DecodeArgs a, const PfxArgs p, int grid_main, bool may_align) {
     using Join = PfxJoin<D, G, SPLIT>;
     __shared__ typename Join::Smem sm;

@@ -301,11 +301,6 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_score_kernel(const PfxArgs
                 return a.score + ((size_t)max(srow[i], 0) * a.h_kv + head) * a.score_stride + t0 + tx + 16 * j;
             };
             auto on = [&](int i, int j) { return t0 + tx + 16 * j < g.tokens && srow[i] >= 0 && !(G == 8 && (ty & 1)); };
-            float old[4][4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; i += S) old[i][j] = ld_if(at(i, j), on(i, j) && !first[i]);
             float x[4][4];
             pfx_logits<D>(sm, ty, tx, x);
             if (t == t_b) {  // the final statistics: the first logits are formed before they are
@@ -329,7 +324,7 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_score_kernel(const PfxArgs
                 if constexpr (G >= 4) e[0] = fmaxf(e[0], e[2]);
                 if constexpr (G == 8) e[0] = fmaxf(e[0], __shfl_xor_sync(0xFFFFFFFFu, e[0], 16));
 #pragma unroll
-                for (int i = 0; i < 4; i += S) st_if(at(i, j), exp2f(e[i]) * inv_w + old[i][j], on(i, j));
+                for (int i = 0; i < 4; i += S) pfx_put_score(at(i, j), exp2f(e[i]) * inv_w, on(i, j), first[i]);
             }
         }
         w += t_e - t_b;

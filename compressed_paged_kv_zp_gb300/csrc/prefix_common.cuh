@@ -364,6 +364,13 @@ struct PfxJoin {
     }
 };
 
+// One score: written, or added to what the window's earlier steps left.  Every score
+// has one thread, so that the order of the additions is that of the steps.
+__device__ __forceinline__ void pfx_put_score(float *p, float v, bool on, bool write) {
+    st_if(p, v, on && write);
+    add_if(p, v, on && !write);
+}
+
 // Window score of the tokens behind the prefixes, from the decode's logits and the
 // final statistics: S[t] (+)= (1/w) max_{h in group} 2^(x_ht - m_h) / l_h, written
 // instead of added at the first window row and for the newest token.  A share of
@@ -377,7 +384,7 @@ __device__ __forceinline__ void pfx_own_scores(const PfxArgs &a, int tid) {
     const int items = a.h_kv << a.unit_log, per = THREADS / items;
     const int q = tid / items, kvh = (tid >> a.unit_log) % a.h_kv, tl = tid & ((1 << a.unit_log) - 1);
     const float inv_w = 1.f / (float)a.window;
-    constexpr int K = G <= 4 && THREADS <= 256 ? 8 : 4;  // units in flight per thread
+    constexpr int K = G <= 4 ? 8 : 4;  // units in flight per thread
     int last = -1;
     float *row = nullptr;
     float c[G];
@@ -385,7 +392,7 @@ __device__ __forceinline__ void pfx_own_scores(const PfxArgs &a, int tid) {
     for (int j = 0; j < G; ++j) c[j] = INFINITY;
     for (int ub = u0 + q; ub < u1; ub += K * per) {
         int4 info[K];
-        float x[K][G], old[K];
+        float x[K][G];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int u = ub + k * per;
@@ -414,12 +421,10 @@ __device__ __forceinline__ void pfx_own_scores(const PfxArgs &a, int tid) {
                 const int first_tok = min(__ldg(a.seq_lens + last), a.stride * a.b) - info[k].z;
                 row = a.score + ((size_t)r * a.h_kv + kvh) * a.score_stride + first_tok;
             }
-            const bool add = on && !(info[k].w & 2) && tok != info[k].z - 1;
-            old[k] = ld_if(row + tok, add);
             float e = x[k][0] - c[0];
 #pragma unroll
             for (int j = 1; j < G; ++j) e = fmaxf(e, x[k][j] - c[j]);
-            st_if(row + tok, fmaf(exp2f(e), inv_w, old[k]), on);
+            pfx_put_score(row + tok, exp2f(e) * inv_w, on, (info[k].w & 2) || tok == info[k].z - 1);
         }
     }
 }

@@ -615,6 +615,11 @@ __global__ void __launch_bounds__(kPsThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(q_full);
                 row = e >= 0 ? pfx_score_row(a, e, &first) : -1;
+                // the scores that are added to, towards L2 while the records are joined
+                if (et % G == 0 && row >= 0 && !first) {
+                    const float *at = a.score + ((size_t)row * a.h_kv + head) * a.score_stride;
+                    for (int tok = s.t_b * kPtTile; tok < min(s.t_e * kPtTile, s.g.tokens); tok += 32) prefetch_l2(at + tok);
+                }
             }
             // only the statistics wait for the kernel that joins the records: the first
             // products run before it ends
@@ -646,8 +651,6 @@ __global__ void __launch_bounds__(kPsThreads, 1)
                     if (col0 + c0 >= s.rows) break;
                     uint32_t v[16];
                     tmem_ld16(acc + c0, v);
-                    // statistics and score rows first, then the old scores where there are
-                    // any: the loads of a chunk are in flight together
                     constexpr int N = 16 / G;
                     float c[16];
 #pragma unroll
@@ -656,9 +659,6 @@ __global__ void __launch_bounds__(kPsThreads, 1)
                     long long mr[N];
 #pragma unroll
                     for (int i = 0; i < N; ++i) mr[i] = ms[(col0 + c0) / G + i];
-                    float old[N];
-#pragma unroll
-                    for (int i = 0; i < N; ++i) old[i] = ld_if(col + (mr[i] >> 1), live && mr[i] >= 0 && !(mr[i] & 1));
 #pragma unroll
                     for (int i = 0; i < N; ++i) {
                         float x[G];
@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(kPsThreads, 1)
                         for (int o = 1; o < G; o <<= 1)
 #pragma unroll
                             for (int j = 0; j < G; j += 2 * o) x[j] = fmaxf(x[j], x[j + o]);
-                        st_if(col + (mr[i] >> 1), fmaf(ex2_approx(x[0]), inv_w, old[i]), live && mr[i] >= 0);
+                        pfx_put_score(col + (mr[i] >> 1), ex2_approx(x[0]) * inv_w, live && mr[i] >= 0, mr[i] & 1);
                     }
                 }
                 tc_fence_before();

@@ -70,21 +70,20 @@ __device__ __forceinline__ float ex2_approx(float x) {
 }
 
 // ---------------------------------------------------------------- predicated access
-// A float where `on`, else 0; and the store.  (A plain "written ? v : *p + v" is
-// compiled into a load in either case.)  Not ordered with other memory accesses:
-// for addresses that the kernel touches in no other way.
-__device__ __forceinline__ float ld_if(const float *p, bool on) {
-    float v;
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\tmov.f32 %0, 0f00000000;\n\t@q ld.global.f32 %0, [%1];\n\t}"
-        : "=&f"(v)
-        : "l"(p), "r"((int)on));
-    return v;
-}
+// *p = v, and *p += v with nothing read back (a subnormal sum becomes 0), where
+// `on`.  (A plain "write ? v : *p + v" is compiled into a load in either case.)  Not
+// ordered with other memory accesses: for addresses that the kernel touches in no
+// other way.
 __device__ __forceinline__ void st_if(float *p, float v, bool on) {
     asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q st.global.f32 [%0], %1;\n\t}" ::"l"(p), "f"(v),
                  "r"((int)on));
 }
+__device__ __forceinline__ void add_if(float *p, float v, bool on) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q red.global.add.f32 [%0], %1;\n\t}" ::"l"(p), "f"(v),
+                 "r"((int)on));
+}
+
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // ---------------------------------------------------------------- mbarrier
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
