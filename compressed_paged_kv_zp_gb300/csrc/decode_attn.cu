@@ -2071,7 +2071,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, G <= 4 ? 4 : 3)
     };
     if (scan) {
         const int t_log = 31 - __clz(a.T);
-        int longest = 0, mine = 0, before = 0, tiles = 0;
+        int longest = 0, mine = 0, before = 0, places = 0;
 #pragma unroll 4
         for (int i = lane; i < a.B; i += 32) {
             const int L = min(max(__ldg(a.seq_lens + i), 0), a.table_stride * a.b);
@@ -2092,12 +2092,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps, G <= 4 ? 4 : 3)
             const int gi = pfx_group_of(p, ng, mi);
             for (int i = lane; i < ng; i += 32) {
                 const PfxGroup o = pfx_group(p, i);
-                tiles += o.rts * o.kts;
-                if (i < gi) before += o.rts * o.kts;
+                places += pfx_places(o);
+                if (i < gi) before += pfx_places(o);
             }
-            tiles = __reduce_add_sync(0xFFFFFFFFu, tiles);
+            places = __reduce_add_sync(0xFFFFFFFFu, places);
             before = __reduce_add_sync(0xFFFFFFFFu, before);
-            pc = pfx_pieces(p, pfx_group(p, gi), mi, head, before, tiles);
+            pc = pfx_pieces(p, pfx_group(p, gi), mi, head, before, places);
         }
     }
     pdl_wait();

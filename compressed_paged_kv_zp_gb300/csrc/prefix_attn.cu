@@ -149,11 +149,11 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_part_kernel(const PfxArgs 
     const int head = blockIdx.x % a.h_kv, set = blockIdx.x / a.h_kv;
     const int w0 = pfx_start(set, W, a.parts), w1 = pfx_start(set + 1, W, a.parts);
     for (int w = w0; w < w1;) {
-        const int gi = pfx_find(pre, ng, w);
-        const PfxGroup g = pfx_group(a, gi);
-        const int item = (w - pre[gi]) / g.kts, t_b = (w - pre[gi]) % g.kts;
-        const int t_e = min(g.kts, t_b + (w1 - w));
-        const int r0 = item * kPfxRows;
+        const PfxSeg seg = pfx_segment(a, pre, ng, w, w1);
+        const PfxGroup &g = seg.g;
+        const int t_b = seg.t_b, t_e = seg.t_e, r0 = seg.item * kPfxRows;
+        w = seg.w_e;
+        if (t_b == t_e) continue;
         const int32_t *row = pfx_row(a, g);
         __syncthreads();  // the last segment's reads of shared memory
         pfx_load_q<D, G>(a, g, head, r0, sm);
@@ -238,7 +238,6 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_part_kernel(const PfxArgs 
                         make_float4(acc[i][4 * dv], acc[i][4 * dv + 1], acc[i][4 * dv + 2], acc[i][4 * dv + 3]);
             }
         }
-        w += t_e - t_b;
     }
 }
 
@@ -258,11 +257,11 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_score_kernel(const PfxArgs
     bool waited = false;
     const float inv_w = 1.f / (float)a.window;
     for (int w = w0; w < w1;) {
-        const int gi = pfx_find(pre, ng, w);
-        const PfxGroup g = pfx_group(a, gi);
-        const int item = (w - pre[gi]) / g.kts, t_b = (w - pre[gi]) % g.kts;
-        const int t_e = min(g.kts, t_b + (w1 - w));
-        const int r0 = item * kPfxRows;
+        const PfxSeg seg = pfx_segment(a, pre, ng, w, w1);
+        const PfxGroup &g = seg.g;
+        const int t_b = seg.t_b, t_e = seg.t_e, r0 = seg.item * kPfxRows;
+        w = seg.w_e;
+        if (t_b == t_e) continue;
         const int32_t *row = pfx_row(a, g);
         __syncthreads();
         pfx_load_q<D, G>(a, g, head, r0, sm);
@@ -327,7 +326,6 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_score_kernel(const PfxArgs
                 for (int i = 0; i < 4; i += S) pfx_put_score(at(i, j), exp2f(e[i]) * inv_w, on(i, j), first[i]);
             }
         }
-        w += t_e - t_b;
     }
     if (!waited) pdl_wait();
     pfx_own_scores<G, kPfxThreads>(a, tid);

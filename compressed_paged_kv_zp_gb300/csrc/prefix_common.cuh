@@ -22,7 +22,7 @@ struct PfxArgs {
     int rt_log, kt_log;  // rows per item, tokens per tile (powers of two)
     int parts;           // sets of CTAs (split of the tiles); a set has a CTA per kv head
     float qscale;        // log2(e) / sqrt(d)
-    int *wpre;           // [B+1] tiles before each group
+    int *wpre;           // [B+1] places before each group
     int *place;          // [B] place of every batch entry in the member list, -1 = in no group
     float *rec_acc;      // [extra0 + parts*rt][d] pieces: main records, then extra records
     float2 *rec_ml;      // same rows
@@ -49,7 +49,17 @@ struct PfxGroup {
     int m0, n;    // first member, members
     int tokens;   // prefix tokens
     int rts, kts; // row tiles, token tiles
+    int lead;     // places that an item's start takes in the split, beside its tiles'
 };
+
+// An item's start (its queries fetched with nothing to compute meanwhile, and the
+// records of the item before written) costs a CTA as much as about five tiles on the
+// tensor cores, so in the split of the work it has places of its own ahead of the
+// tiles, at most one per eight tiles: a CTA that begins a second item gets fewer
+// tiles.  (256 sequences behind two prefixes of 4k, four items of 32 tiles on 19 CTAs:
+// the slowest CTA 22 us, 29 us without; scored in all 145, 151 us without.)  In fp32 a
+// tile costs more than a start.
+constexpr int kPfxLead = 4;
 
 __device__ __forceinline__ int pfx_groups(const PfxArgs &a) { return min(max(__ldg(a.n_groups), 0), a.B); }
 
@@ -60,8 +70,12 @@ __device__ __forceinline__ PfxGroup pfx_group(const PfxArgs &a, int g) {
     r.tokens = min(max(__ldg(a.group_blocks + g), 0), a.stride) << a.b_log;
     r.rts = ((r.n << a.G_log) + (1 << a.rt_log) - 1) >> a.rt_log;
     r.kts = (r.tokens + (1 << a.kt_log) - 1) >> a.kt_log;
+    r.lead = a.tc ? min(kPfxLead, r.kts >> 3) : 0;
     return r;
 }
+
+// Places of a group in the split.
+__device__ __forceinline__ int pfx_places(const PfxGroup &g) { return g.rts * (g.lead + g.kts); }
 
 // Group of place i of the member list: the last that starts at or before it
 // (ng > 0; the place may lie behind its end).
@@ -103,12 +117,12 @@ __device__ __forceinline__ int pfx_owner(int w, int W, int parts) {
     return (int)(((long long)(w + 1) * parts - 1) / W);
 }
 
-// Tiles before each group (whole CTA; pre: n_groups + 1 ints of shared memory);
+// Places before each group (whole CTA; pre: n_groups + 1 ints of shared memory);
 // returns the total.
 inline __device__ int pfx_scan(const PfxArgs &a, int ng, int *pre) {
     for (int i = threadIdx.x; i < ng; i += blockDim.x) {
         const PfxGroup g = pfx_group(a, i);
-        pre[i] = g.rts * g.kts;
+        pre[i] = pfx_places(g);
     }
     __syncthreads();
     if (threadIdx.x < 32) {
@@ -129,6 +143,27 @@ inline __device__ int pfx_scan(const PfxArgs &a, int ng, int *pre) {
     }
     __syncthreads();
     return pre[ng];
+}
+
+// What a CTA does from place w of its range, which ends at w1: tiles [t_b, t_e) of row
+// tile `item` of group g (none where its places end ahead of the first), up to place
+// w_e.
+struct PfxSeg {
+    PfxGroup g;
+    int item, t_b, t_e, w_e;
+};
+
+__device__ __forceinline__ PfxSeg pfx_segment(const PfxArgs &a, const int *pre, int ng, int w, int w1) {
+    PfxSeg s;
+    const int gi = pfx_find(pre, ng, w);
+    s.g = pfx_group(a, gi);
+    const int x = w - pre[gi], len = s.g.lead + s.g.kts;
+    s.item = (int)((unsigned)x / (unsigned)len);
+    const int at = x - s.item * len, end = min(len, at + (w1 - w));
+    s.t_b = max(at - s.g.lead, 0);
+    s.t_e = max(end - s.g.lead, 0);
+    s.w_e = w + (end - at);
+    return s;
 }
 
 // Row of the main records: rows of a group are (kv head, member, q head of the
@@ -174,18 +209,18 @@ __device__ __forceinline__ int pfx_score_row(const PfxArgs &a, int s, bool *firs
 struct PfxPieces {
     long long main, main2, extra;  // first piece, its second stream; row of CTA 0's extra records
     int n, two;                    // pieces, records of each (one per stream); n = 0: none
-    int c0, i0, W;                 // set of the first piece; its first tile; all tiles
+    int c0, i0, W;                 // set of the first piece; place of its first tile; all places
 };
 
-// before, W: the tiles before the member's group and of all groups.
+// before, W: the places before the member's group and of all groups.
 __device__ __forceinline__ PfxPieces pfx_pieces(const PfxArgs &a, const PfxGroup &g, int mi, int head, int before, int W) {
     PfxPieces p = {};
     if (mi < g.m0 || mi >= g.m0 + g.n || g.tokens == 0) return p;
     const int rt = 1 << a.rt_log, r = (mi - g.m0) << a.G_log, row = r & (rt - 1);
     p.W = W;
-    p.i0 = before + (r >> a.rt_log) * g.kts;
+    p.i0 = before + (r >> a.rt_log) * (g.lead + g.kts) + g.lead;
     p.c0 = pfx_owner(p.i0, W, a.parts);
-    // consecutive sets when each has a tile, one tile each otherwise
+    // consecutive sets when each has a place, one tile each otherwise
     p.n = W >= a.parts ? pfx_owner(p.i0 + g.kts - 1, W, a.parts) - p.c0 + 1 : g.kts;
     p.two = a.tc && min(rt, (g.n << a.G_log) - (r - row)) <= rt / 2 ? 2 : 1;  // at most 128 rows: a record per stream
     p.main = pfx_main_row(a, g, head, r);

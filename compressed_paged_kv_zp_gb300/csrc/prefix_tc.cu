@@ -95,23 +95,15 @@ struct PtCfg {
 };
 
 // One CTA's share of an item.
-struct PtSeg {
-    PfxGroup g;
-    int rt;
-    int t_b, t_e;  // token tiles
-    int rows;      // query rows of the item (<= 256)
-    bool split;    // at most 128 rows: the streams take alternate tiles
+struct PtSeg : PfxSeg {
+    int rows;    // query rows of the item (<= 256)
+    bool split;  // at most 128 rows: the streams take alternate tiles
 };
 
 __device__ __forceinline__ PtSeg pt_segment(const PfxArgs &a, const int *pre, int ng, int w, int w1) {
     PtSeg s;
-    const int gi = pfx_find(pre, ng, w);
-    s.g = pfx_group(a, gi);
-    const int x = w - pre[gi], item = (int)((unsigned)x / (unsigned)s.g.kts);
-    s.rt = item;
-    s.t_b = x - item * s.g.kts;
-    s.t_e = min(s.g.kts, s.t_b + (w1 - w));
-    s.rows = min(kPtRows, (s.g.n << a.G_log) - s.rt * kPtRows);
+    static_cast<PfxSeg &>(s) = pfx_segment(a, pre, ng, w, w1);
+    s.rows = min(kPtRows, (s.g.n << a.G_log) - s.item * kPtRows);
     s.split = s.rows <= kPtRows / 2;
     return s;
 }
@@ -133,7 +125,7 @@ __device__ __forceinline__ int pt_rows16(const PfxArgs &a, const PfxGroup &g, co
 // Address of row r of the item's queries, nullptr beyond the last row.
 template <int D>
 __device__ __forceinline__ const uint4 *pt_query(const PfxArgs &a, const PtSeg &s, int head, int r, int *entry) {
-    const int rr = s.rt * kPtRows + r;
+    const int rr = s.item * kPtRows + r;
     *entry = r < s.rows ? pfx_member(a, s.g.m0 + (rr >> a.G_log)) : -1;
     if (*entry < 0) return nullptr;
     return reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
@@ -222,6 +214,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         }
         for (int w = w0; w < w1 && ok_all;) {
             const PtSeg s = pt_segment(a, pre, ng, w, w1);
+            w = s.w_e;
+            if (s.t_b == s.t_e) continue;
             const int32_t *row = pfx_row(a, s.g);
             int z_next = lane < 8 ? pt_rows16(a, s.g, row, s.t_b * kPtTile + 16 * q) : 0;
             for (int t = s.t_b; t < s.t_e && ok_all; ++t) {
@@ -246,7 +240,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     __syncwarp();
                 }
             }
-            w += s.t_e - s.t_b;
         }
         if (lane == 0 && *abort_flag) {  // copies in flight land before the CTA ends
             volatile int never = 0;
@@ -261,6 +254,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             bool ok_all = true;
             for (int w = w0; w < w1 && ok_all;) {
                 const PtSeg s = pt_segment(a, pre, ng, w, w1);
+                w = s.w_e;
+                if (s.t_b == s.t_e) continue;
                 const int n_t[2] = {pt_tiles(s, 0), pt_tiles(s, 1)};
                 // logits of stream x, its tile j
                 auto qk = [&](int x, int j) -> bool {
@@ -314,7 +309,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                         else tc_commit(&o_full[x]);
                     }
                 base += 2 * (s.t_e - s.t_b);
-                w += s.t_e - s.t_b;
             }
             // every product has been carried out before the CTA ends, also after a timeout
             volatile int never = 0;
@@ -333,6 +327,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         bool ok_all = true;
         for (int w = w0; w < w1 && ok_all;) {
             const PtSeg s = pt_segment(a, pre, ng, w, w1);
+            w = s.w_e;
+            if (s.t_b == s.t_e) continue;
             const int n_t = pt_tiles(s, x);
             const int r = s.split ? tr : x * 128 + tr;  // row of the item
             float m = -INFINITY, l = 0.f;
@@ -416,7 +412,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             // whole 128-byte lines; chunk c of row i sits at c ^ (i & 7)
             long long at = -1;
             if (r < s.rows)
-                at = s.t_b == 0 ? pfx_main_row(a, s.g, head, s.rt * kPtRows + r) + (s.split && x ? (long long)a.B * a.h_q : 0)
+                at = s.t_b == 0 ? pfx_main_row(a, s.g, head, s.item * kPtRows + r) + (s.split && x ? (long long)a.B * a.h_q : 0)
                                 : a.extra0 + (long long)blockIdx.x * kPtRows + x * 128 + tr;
             if (n_t > 0) {
                 if (!mbar_wait_bounded(&o_full[x], n_o & 1, a.err, abort_flag, 0x608)) break;
@@ -448,7 +444,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 tc_fence_before();
             }
             if (at >= 0) a.rec_ml[at] = make_float2(m, l);
-            w += s.t_e - s.t_b;
         }
     }
 
@@ -539,6 +534,8 @@ __global__ void __launch_bounds__(kPsThreads, 1)
         if (lane == 0) prefetch_tensormap(&kmap);
         for (int w = w0; w < w1 && ok_all;) {
             const PtSeg s = pt_segment(a, pre, ng, w, w1);
+            w = s.w_e;
+            if (s.t_b == s.t_e) continue;
             const int32_t *row = pfx_row(a, s.g);
             for (int t = s.t_b; t < s.t_e; ++t, ++fill) {
                 const int z = lane < 8 ? pt_rows16(a, s.g, row, t * kPtTile + 16 * q) : 0;
@@ -557,7 +554,6 @@ __global__ void __launch_bounds__(kPsThreads, 1)
                     tma_load_5d(smem + C::ST_OFF + st * C::TILE + q * 2 * C::GROUP, &kmap, 0, 0, 0, head, z, &full[st]);
                 __syncwarp();
             }
-            w += s.t_e - s.t_b;
         }
         if (lane == 0 && *abort_flag) {
             volatile int never = 0;
@@ -571,6 +567,8 @@ __global__ void __launch_bounds__(kPsThreads, 1)
             bool ok_all = true;
             for (int w = w0; w < w1 && ok_all;) {
                 const PtSeg s = pt_segment(a, pre, ng, w, w1);
+                w = s.w_e;
+                if (s.t_b == s.t_e) continue;
                 const uint32_t idesc = idesc_bf16_f32(128, (s.rows + 15) / 16 * 16);
                 ok_all = mbar_wait_bounded(q_full, n_q & 1, a.err, abort_flag, 0x613);
                 ++n_q;
@@ -588,7 +586,6 @@ __global__ void __launch_bounds__(kPsThreads, 1)
                     tc_commit(&empty[st]);
                     tc_commit(&acc_full[ab]);
                 }
-                w += s.t_e - s.t_b;
             }
             volatile int never = 0;
             tc_commit(drain);
@@ -602,8 +599,10 @@ __global__ void __launch_bounds__(kPsThreads, 1)
         uint32_t tile = 0, item = 0;
         bool ok_all = true, waited = false;
         // (every wait is bounded, so a warp that stops cannot leave another waiting for ever)
-        for (int w = w0; w < w1 && ok_all; ++item) {
+        for (int w = w0; w < w1 && ok_all;) {
             const PtSeg s = pt_segment(a, pre, ng, w, w1);
+            w = s.w_e;
+            if (s.t_b == s.t_e) continue;
             // the item's rows: once every warp has finished the last item (whose
             // products are then complete)
             if (!mbar_wait_bounded(q_done, (item & 1) ^ 1, a.err, abort_flag, 0x618)) break;
@@ -627,7 +626,7 @@ __global__ void __launch_bounds__(kPsThreads, 1)
             waited = true;
             if (et < kPtRows) {
                 float c = INFINITY;
-                if (row >= 0) c = __ldcg(a.stats + (size_t)e * a.h_q + head * G + (s.rt * kPtRows + et) % G);
+                if (row >= 0) c = __ldcg(a.stats + (size_t)e * a.h_q + head * G + (s.item * kPtRows + et) % G);
                 cs[et] = c;
                 if (et % G == 0)
                     ms[et / G] = row >= 0 ? ((long long)row * a.h_kv + head) * a.score_stride * 2 + (first ? 1 : 0) : -1;
@@ -677,7 +676,7 @@ __global__ void __launch_bounds__(kPsThreads, 1)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(q_done);
-            w += s.t_e - s.t_b;
+            ++item;
         }
         if (!waited) pdl_wait();
         if (ok_all) pfx_own_scores<G, 32 * kPsEpi>(a, et);

@@ -98,6 +98,21 @@ def test_matches_oracle(zp, heads, shape):
     c.check(*c.run(zp))
 
 
+@pytest.mark.parametrize("scored", [False, True])
+@pytest.mark.parametrize("heads,sizes,blocks", [
+    ("wide", [66, 2, 3], [257, 70, 1]),  # few CTAs per head: two items of many tiles, and starts that a cut falls into
+    ("qwen", [65, 9], [129, 64]),
+    ("g8d64", [33, 40], [35, 150]),
+    ("qwen32", [17, 5], [40, 70]),
+])
+def test_long_items(zp, heads, sizes, blocks, scored):
+    """Prefixes of many tiles in several row tiles: CTAs that end one item and begin another."""
+    c = Case(zp, 23, HEADS[heads], sizes, blocks, (1, 40), 1, 0)
+    if scored:
+        c.score_rows(3, HEADS[heads][3])
+    c.check(*c.run(zp))
+
+
 @pytest.mark.parametrize("window", [1, 5, 16])
 @pytest.mark.parametrize("heads", HEADS)
 def test_scored(zp, heads, window):
