@@ -66,7 +66,9 @@ constexpr int kMaxB = 4096;
 // the 64-sequence Qwen3-8B layer fit 1.15-1.18); the stream-K split weighs
 // such units accordingly so that the CTAs holding them finish with the rest.
 constexpr int kRhoUnitWeight16 = 19;
-constexpr int kAlignUnits = 4;  // behind a prefix: units of the longest sequence up to which none is cut
+// Behind a prefix: units of the longest sequence up to which none is cut between CTAs
+// (8 sequences of up to 64 tokens behind 2k: 16 us in all; 18 with cuts).
+constexpr int kAlignUnits = 4;
 
 struct DecodeArgs {
     const void *q;

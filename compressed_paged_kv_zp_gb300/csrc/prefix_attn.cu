@@ -13,10 +13,10 @@
 // sequences on a window step, and over the decode's logits:
 //     S[t] (+)= (1/w) max_{h in group} 2^(x_ht - m_h) / l_h.
 // Chain of launches: the prefix kernel; the decode, which needs nothing of it and
-// follows without a gap; the kernel that joins the records; the score.  (With the
-// decode starting from the joined prefix instead, and its own cooperative merge
-// and score: 8 sequences behind 2k tokens 24 us, not 19; 64 behind 32k 73, not 63;
-// scored 256 behind 4k 157, not 132.)
+// follows without a gap; the kernel that joins the records; the score.  8 sequences
+// behind 2k tokens 16 us, 64 behind 32k 59, scored 256 behind 4k 145 (bf16, 32 q and 8
+// kv heads of 128).  With the decode starting from the joined prefix instead, and its
+// own cooperative merge and score, the first two took 24 and 73.
 //
 // Work: an item is (group, tile of query rows), its length the group's tiles of
 // prefix tokens.  The tiles of all items are concatenated and every set of h_kv
@@ -48,7 +48,10 @@ __device__ __forceinline__ void load_vec(const float *p, float *o) {
 // 64 query rows x 64 prefix tokens per tile, everything in fp32 in shared
 // memory; a thread holds 4 rows x 4 tokens of the logits and 4 rows x d/16 dims
 // of the accumulator, and the 16 threads of a row (a half-warp) share its
-// softmax statistics by shuffles.
+// softmax statistics by shuffles.  Bound by the fp32 pipe and shared memory: eight
+// 16-byte loads per 64 FMAs.  The next tile waits in registers while one is computed.
+// (61 sequences in 7 groups behind 672 tokens, 16 q and 4 kv heads of 64: 10 us for two
+// tiles per CTA, scored in all 39 us.)
 template <int D>
 struct PfxSmem {
     float q[kPfxRows][D + 4];
@@ -243,7 +246,8 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_part_kernel(const PfxArgs 
 
 // Window score of the prefix tokens from the final statistics: the logits again,
 // the maximum of x - (m + log2 l) over the q heads of the kv head, one
-// exponential per (sequence, kv head, token).
+// exponential per (sequence, kv head, token).  The first tile's logits do not wait for
+// the statistics (39 us where all of it waits: 45).
 template <int D, int G>
 __global__ void __launch_bounds__(kPfxThreads) prefix_score_kernel(const PfxArgs a) {
     extern __shared__ __align__(16) unsigned char pfx_raw[];

@@ -273,9 +273,10 @@ __device__ __forceinline__ void ld_row(const float *p, float (&v)[V]) {
 //   rec(i, ml, acc)  the first row of record i in [0, n): statistics, accumulator
 //   put(j, c, y, M, L)  takes V consecutive dims from c of row j (SPLIT 1: V = D/32,
 //                       else 1), unnormalised
-// Few pairs have many records each, many pairs few: four warps per pair while the
-// pairs fill the GPU at most once (64 pairs of 16 records: 2.6 us, 7.4 us with a warp
-// each), else one (2048 pairs of 6: 3.6 us; 13 us with four warps each).
+// Few pairs have many records each, many pairs few: four warps per pair while there are
+// at most eight pairs per SM (64 pairs of 17 records, 8 sequences behind 2k tokens: 16 us
+// in all, 18 with a warp each; 512 pairs of 20, 64 behind 32k: 59 and 66), else one (2048
+// pairs of 7, 256 scored behind 4k: 145 us in all, 159 with four).
 constexpr int kJoinWarps = 4;
 
 template <int D, int G, int SPLIT>

@@ -15,7 +15,8 @@
 // columns (B of them in a decode step, new tokens / b in a prefill).  Beyond a few
 // entries per thread a cluster of 8 CTAs counts together and exchanges the counts
 // in distributed shared memory.  Latency bound: the redundant scan and count cost
-// less than a second launch.  In place (table_out = block_table) there is one
+// less than a second launch (512 sequences of a token each 6.0 us, 16 prompts of 32k
+// tokens, half a million slots, 12.6 us).  In place (table_out = block_table) there is one
 // cluster, since the counts read entries that other clusters would write.
 #include <cooperative_groups.h>
 
@@ -191,8 +192,8 @@ __global__ void __launch_bounds__(kSlotThreads) build_slots_kernel(const SlotArg
     if (a.table_out != a.table) {
         // copy of the table; the touched columns are written by their owners
         const int n_table = a.B * a.stride;  // (below 2^31 by the limits)
-        for (int i = blockIdx.x * kSlotThreads + tid; i < n_table; i += G * kSlotThreads) {
-            const int s = i / a.stride, c = i - s * a.stride;
+        for (long long i = (long long)blockIdx.x * kSlotThreads + tid; i < n_table; i += (long long)G * kSlotThreads) {
+            const int s = (int)((unsigned)i / (unsigned)a.stride), c = (int)i - s * a.stride;
             const int n_cols = ccol[s + 1] - ccol[s], c0 = col_s[s] >> 1;
             if (n_cols == 0 || c < c0 || c >= c0 + n_cols) a.table_out[i] = a.table[i];
         }
@@ -260,7 +261,11 @@ __global__ void __launch_bounds__(kSlotThreads) build_slots_kernel(const SlotArg
 
 // ---------------------------------------------------------------------------
 // zp_write_kv: row i (one token, every kv head) of layer l goes to slot
-// slots[i] of that layer.  A copy: bound by HBM.
+// slots[i] of that layer.  A copy, bound by HBM: a thread has kWriteUnroll vectors of
+// 16 bytes in flight, a CTA's vectors are consecutive.  16k tokens of 4 layers, 8 heads
+// of 128 in bf16, 528 MB read and written: 76 us, 6.9 TB/s (with 8 vectors 78, with one
+// 86).  Few tokens are bound by the latency of slot and row: 509 tokens of 2 fp32 heads of
+// 64 2.1 us (with 8 vectors, so a quarter of the CTAs, 4.4).
 struct WriteArgs {
     const uint4 *k, *v;
     long long token_vec, new_layer_vec;  // strides of k, v in 16-byte vectors
@@ -272,7 +277,7 @@ struct WriteArgs {
     unsigned *err;
 };
 
-constexpr int kWriteThreads = 256, kWriteUnroll = 8;
+constexpr int kWriteThreads = 256, kWriteUnroll = 2;
 
 __global__ void __launch_bounds__(kWriteThreads) write_kv_kernel(const WriteArgs a) {
     const uint4 *src = (blockIdx.z ? a.v : a.k) + (long long)blockIdx.y * a.new_layer_vec;
@@ -335,8 +340,8 @@ extern "C" zp_status zp_build_slots(const zp_cache_desc *D, const int32_t *block
                   n_fresh, slots, positions, max_tokens, cu_tokens, n_used, dev.error_word};
     // the columns that new tokens can touch, at most: per sequence one, and one
     // per b tokens.  Up to 4096 of them a CTA counts alone (512 sequences, one
-    // token each: 6 us; in clusters 18), beyond that in clusters (16 prompts of 32k
-    // tokens: 17 us; alone 36).
+    // token each: 6.0 us; in clusters 10.5), beyond that in clusters (16 prompts of
+    // 32k tokens: 12.6 us; alone 22.5).
     const long long most = (long long)B + max_tokens / D->block_size;
     const bool in_place = table_out == block_table, clusters = in_place || most > 4096;
     const size_t smem = (size_t)(4 * B + 2) * 4;

@@ -295,9 +295,11 @@ zp_status zp_prefix_plan(const zp_cache_desc *D, const int32_t *block_table, int
 
 /* zp_paged_decode_attn (output, window score, arguments, skipping of L = 0) with
  * each group's shared tokens attended once for all its members: their query rows
- * form one dense product with the shared keys and values, whose softmax state
- * the decode of the members' other tokens continues.  The plan's arrays agree
- * (prefix_lens[s] = group_blocks * b of the group that lists s, 0 if none).  A member whose L does not exceed its group's prefix is decoded alone.
+ * form one dense product with the shared keys and values, and its softmax
+ * statistics are joined with those of the decode of the members' other tokens.
+ * The plan's arrays agree (prefix_lens[s] = group_blocks * b of the group that
+ * lists s, 0 if none).  A member whose L does not exceed its group's prefix is
+ * decoded alone.
  * The members' leading group_blocks table entries must be equal (the first
  * member's are used).  A member outside [0, B) (detail 0x142) and a block id
  * outside [0, N_total) (0x143) are recorded as ZP_ERR_DEVICE and skipped.  The
