@@ -427,7 +427,7 @@ def zp_prefix_decode_attn(desc, q, k_cache, v_cache, block_table, seq_lens, plan
     elif score_rows is not None:
         raise ValueError("score_rows needs score_accum")
     if workspace is None:
-        workspace = q.new_empty(zp_prefix_decode_workspace_size(desc, B, table_stride), dtype=torch.uint8)
+        workspace = torch.empty(zp_prefix_decode_workspace_size(desc, B, table_stride), dtype=torch.uint8, device=q.device)
         if stream is not None:
             workspace.record_stream(stream)  # not reused before this call's work on that stream
     rc = lib.zp_prefix_decode_attn(desc, _ptr_on(q, dev, "q"), _ptr_on(k_cache, dev, "k_cache"),

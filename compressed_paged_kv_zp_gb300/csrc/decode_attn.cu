@@ -2046,10 +2046,8 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(const DecodeArgs a, i
 // The split follows from the lengths and the plan, so up to kTailScanB entries a
 // warp works it out before the wait for the decode, and only the records are read
 // after it (64 sequences behind 32k tokens: 63 us in all, not 65); beyond, it is read
-// from what the kernels before left in the workspace.  Bound by latency: 4 to 7 us
-// after the wait, of which the records' bytes (42 MB through L2 there) are 3.
-constexpr int kTailScanB = 512;
-constexpr int kTailScanGroups = 256;
+// from what the kernels before left in the workspace.  Bound by latency: 3 to 6 us
+// after the wait, of which the records' bytes (32 MB through L2 there) are 2.
 template <typename T, int D, int G, int SPLIT>
 __global__ void __launch_bounds__(32 * kJoinWarps, G <= 4 ? 4 : 3)
     prefix_tail_kernel(const DecodeArgs a, const PfxArgs p, int grid_main, bool may_align) {
@@ -2061,7 +2059,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, G <= 4 ? 4 : 3)
     const int s = pair / a.h_kv, head = pair - s * a.h_kv;
     const int ng = pfx_groups(p);
     const int pre = s < a.B ? prefix_of(a, s) : 0;
-    const bool scan = a.B <= kTailScanB && ng <= kTailScanGroups;
+    const bool scan = pfx_tail_scans(p, ng);
     int u_b = 0, u_e = 0, U = 0, mi = -1, c_lo = 0, c_hi = 0;
     bool aligned = false;
     PfxPieces pc = {};

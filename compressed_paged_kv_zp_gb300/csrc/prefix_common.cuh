@@ -120,10 +120,7 @@ __device__ __forceinline__ int pfx_owner(int w, int W, int parts) {
 // Places before each group (whole CTA; pre: n_groups + 1 ints of shared memory);
 // returns the total.
 inline __device__ int pfx_scan(const PfxArgs &a, int ng, int *pre) {
-    for (int i = threadIdx.x; i < ng; i += blockDim.x) {
-        const PfxGroup g = pfx_group(a, i);
-        pre[i] = pfx_places(g);
-    }
+    for (int i = threadIdx.x; i < ng; i += blockDim.x) pre[i] = pfx_places(pfx_group(a, i));
     __syncthreads();
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
@@ -237,8 +234,16 @@ __device__ __forceinline__ long long pfx_record(const PfxArgs &a, const PfxPiece
     return p.extra + (((long long)c * a.h_kv) << a.rt_log) + (x << (a.rt_log - 1));
 }
 
-// The first CTA's outputs for the kernels that join records (whole CTA).
+// Up to these sizes the kernel that joins the records works out where they are.
+constexpr int kTailScanB = 512;
+constexpr int kTailScanGroups = 256;
+__device__ __forceinline__ bool pfx_tail_scans(const PfxArgs &a, int ng) {
+    return a.B <= kTailScanB && ng <= kTailScanGroups;
+}
+
+// The first CTA's outputs for that kernel beyond (whole CTA).
 inline __device__ void pfx_publish(const PfxArgs &a, int ng, const int *pre) {
+    if (pfx_tail_scans(a, ng)) return;
     for (int i = threadIdx.x; i <= ng; i += blockDim.x) a.wpre[i] = pre[i];
     for (int s = threadIdx.x; s < a.B; s += blockDim.x) a.place[s] = -1;
     __syncthreads();
