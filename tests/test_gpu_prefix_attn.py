@@ -291,3 +291,24 @@ def test_full_batch(zp):
     c = Case(zp, 121, (4, 1, 64, 16, BF16), [1500, 700, 2] + [3] * 400, [3, 2, 5] + [1] * 400, (1, 20), 600, 94)
     assert c.B == 4096
     c.check(*c.run(zp))
+
+
+@pytest.mark.parametrize("heads", [(8, 2, 128, 16, BF16), (8, 2, 64, 16, F32)], ids=["bf16", "f32"])
+def test_scored_batch_beyond_512(zp, heads):
+    """More entries than the joining kernel scans itself: the split is read from the workspace."""
+    c = Case(zp, 131, heads, [300, 250, 40], [9, 3, 20], (1, 60), 20, 5)
+    c.score_rows(132, 11)
+    c.check(*c.run(zp))
+
+
+@pytest.mark.parametrize("heads", HEADS)
+def test_what_the_workspace_held_does_not_matter(zp, heads):
+    """Records that a call leaves unwritten (streams and CTAs without tiles) are not used: a workspace of NaN."""
+    for sizes, blocks in (([3], [30]), ([40, 7], [9, 70])):
+        c = Case(zp, 141, HEADS[heads], sizes, blocks, (1, 120), 2, 1)
+        c.score_rows(142, c.b)
+        n = zp.zp_prefix_decode_workspace_size(c.desc, c.B, c.td.shape[1])
+        out, S = c.run(zp, workspace=torch.zeros(n, dtype=torch.uint8, device=DEV))
+        out2, S2 = c.run(zp, workspace=torch.full((n,), 255, dtype=torch.uint8, device=DEV))
+        assert torch.equal(out, out2) and torch.equal(S, S2)
+        c.check(out, S)
