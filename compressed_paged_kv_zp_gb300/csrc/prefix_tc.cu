@@ -466,10 +466,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 // a kv head's q heads is taken in registers and consecutive lanes write
 // consecutive tokens of a score row.  Accumulators of two tiles (256 columns
 // each); per (token, sequence) one exponential of max_h (x_h - c_h),
-// c = m + log2 l.  Bound by the epilogue's instructions (sixteen warps; a tile's
-// 32768 logits take 1.4 us, its product 0.7) and by the scores' bytes: 253 sequences
-// behind 4k tokens 12 us from the statistics on, 66 MB of scores, then 7 us for the
-// 17 MB of logits of the private tokens.  Eight warps: 4 us more in all.
+// c = m + log2 l.  Bound by the scores' bytes: 253 sequences behind 4k tokens 12 us
+// from the statistics on for 33 MB read and 33 MB written (5.5 TB/s; packed products and
+// three-way maxima in the epilogue change nothing), then 7 us for the 17 MB of logits of
+// the private tokens.  With eight epilogue warps, not sixteen, 4 us more in all.
 template <int D>
 struct PsCfg {
     static constexpr int KH = D / 64;
