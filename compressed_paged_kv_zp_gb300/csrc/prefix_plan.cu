@@ -18,7 +18,8 @@
 // are listed together), and the first CTA numbers the groups.  Bound by
 // latency (four cluster barriers and the gather of the first column); the rows
 // are read only up to their first difference.  256 entries behind a prefix of 64
-// blocks: 11.7 us; 2048 in many classes: 31 us.
+// blocks: 11.5 us; 2048 behind 16 prefixes of up to 256: 28.6 us, of which hashing 3.4,
+// the rows 7.5, counting and ranking 5.
 #include <cooperative_groups.h>
 
 #include "zp_common.cuh"
@@ -166,12 +167,35 @@ __device__ __forceinline__ void plan_lcp(const PlanArgs &a, PlanSmem &sm, cooper
     }
 }
 
+// For each of the sequences [e0, e1) with a leader (and, MEMBERS, in a group), how many
+// entries e of its class's part of seg count(e, s) holds for: done(s, leader, number).
+// LANES lanes per sequence: a whole warp while a warp has one sequence, else 8, so that
+// a warp's sequences are counted at the same time (2048 entries: 28.6 us in all, 31.2
+// with 32).
+template <int LANES, bool MEMBERS, typename Count, typename Done>
+__device__ __forceinline__ void plan_per_class(const PlanSmem &sm, int e0, int e1, Count &&count, Done &&done) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int base = e0 + warp * (32 / LANES); base < e1; base += kPlanThreads / LANES) {
+        const int s = base + lane / LANES;
+        const int ld = s < e1 && (!MEMBERS || sm.member[s]) ? sm.leader[s] : -1;
+        int n = 0;
+        if (ld >= 0) {
+            const int end = sm.cls_at[ld];
+#pragma unroll 4
+            for (int j = end - sm.cls_n[ld] + lane % LANES; j < end; j += LANES) n += count(sm.seg[j], s) ? 1 : 0;
+        }
+#pragma unroll
+        for (int o = 1; o < LANES; o <<= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
+        if (s < e1 && lane % LANES == 0) done(s, ld, n);
+    }
+}
+
 __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanThreads, 1)
     prefix_plan_kernel(const PlanArgs a) {
     extern __shared__ __align__(16) unsigned char plan_smem_raw[];
     PlanSmem &sm = *reinterpret_cast<PlanSmem *>(plan_smem_raw);
     auto cluster = cooperative_groups::this_cluster();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x;
     const int rank = (int)cluster.block_rank();
     const int B = a.B;
     const int e0 = (int)((long long)B * rank / kPlanCluster), e1 = (int)((long long)B * (rank + 1) / kPlanCluster);
@@ -236,15 +260,11 @@ __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanThre
     }
     __syncthreads();  // (cls_at is now the class's end)
     // members of the class with at least this lcp, given to the first CTA
-    for (int s = e0 + warp; s < e1; s += kWarps) {
-        const int ld = sm.leader[s];
-        int cnt = 0;
-        if (ld >= 0) {
-            const unsigned mine = (unsigned)sm.lcp[s] << 12;
-            for (int j = sm.cls_at[ld] - sm.cls_n[ld] + lane; j < sm.cls_at[ld]; j += 32) cnt += sm.seg[j] >= mine ? 1 : 0;
-        }
-        cnt = __reduce_add_sync(0xFFFFFFFFu, cnt);
-        if (lane == 0) *cluster.map_shared_rank(&sm.aux[s], 0) = cnt;
+    {
+        auto at_least = [&](unsigned e, int s) { return e >= (unsigned)sm.lcp[s] << 12; };
+        auto give = [&](int s, int, int n) { *cluster.map_shared_rank(&sm.aux[s], 0) = n; };
+        if (per_warp <= 1) plan_per_class<32, false>(sm, e0, e1, at_least, give);
+        else plan_per_class<8, false>(sm, e0, e1, at_least, give);
     }
     cluster.sync();
     if (rank == 0) {
@@ -318,16 +338,16 @@ __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanThre
         }
         __syncthreads();
     }
-    for (int s = e0 + warp; s < e1; s += kWarps) {
-        if (!sm.member[s]) continue;
-        const int ld = sm.leader[s];
-        int r = 0;
-        for (int j = sm.cls_at[ld] - sm.cls_n[ld] + lane; j < sm.cls_at[ld]; j += 32) {
-            const int o = (int)(sm.seg[j] & (kPlanMaxB - 1));
-            r += o < s && sm.member[o] ? 1 : 0;
-        }
-        r = __reduce_add_sync(0xFFFFFFFFu, r);
-        if (lane == 0) a.members[sm.aux[ld] + r] = s;
+    {
+        auto before = [&](unsigned e, int s) {
+            const int o = (int)(e & (kPlanMaxB - 1));
+            return o < s && sm.member[o];
+        };
+        auto put = [&](int s, int ld, int n) {
+            if (ld >= 0) a.members[sm.aux[ld] + n] = s;
+        };
+        if (per_warp <= 1) plan_per_class<32, true>(sm, e0, e1, before, put);
+        else plan_per_class<8, true>(sm, e0, e1, before, put);
     }
     cluster.sync();  // the first CTA's shared memory outlives the others' reads
 }
