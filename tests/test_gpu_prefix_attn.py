@@ -312,3 +312,34 @@ def test_what_the_workspace_held_does_not_matter(zp, heads):
         out2, S2 = c.run(zp, workspace=torch.full((n,), 255, dtype=torch.uint8, device=DEV))
         assert torch.equal(out, out2) and torch.equal(S, S2)
         c.check(out, S)
+
+
+def test_captured_without_a_workspace(zp):
+    """Captured calls that take their own workspaces, replayed between eager calls and allocations; two on two streams."""
+    cs = [Case(zp, 151 + i, HEADS["qwen"], [12, 5], [20 + i, 9], (1, 100), 2) for i in range(2)]
+    outs, graphs = [], []
+    for c in cs:
+        c.run(zp)
+        out = torch.full_like(c.qd, 7.0)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(2):
+                zp.zp_prefix_decode_attn(c.desc, c.qd, c.Kd, c.Vd, c.td, c.ld, c.plan, out)
+        outs.append(out)
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in cs]
+    for _ in range(3):
+        for out in outs:
+            out.fill_(7.0)
+        torch.cuda.synchronize()
+        for g, st, c in zip(graphs, streams, cs):
+            with torch.cuda.stream(st):
+                g.replay()
+        junk = [torch.full((1 << 24,), 255, dtype=torch.uint8, device=DEV) for _ in range(4)]
+        eager, _ = cs[0].run(zp)
+        torch.cuda.synchronize()
+        del junk
+        cs[0].check(eager)
+        for c, out in zip(cs, outs):
+            c.check(out)
+    assert zp.zp_device_status() == (0, 0)
