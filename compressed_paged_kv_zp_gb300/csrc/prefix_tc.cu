@@ -31,6 +31,7 @@
 #include <math.h>
 
 #include "prefix_common.cuh"
+#include "prefix_layout.h"
 #include "prefix_tc.h"
 #include "tc05.cuh"
 
@@ -156,7 +157,7 @@ __device__ __forceinline__ void pt_load_q(const uint4 *src, int row0, unsigned c
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int r = row0 + i * (32 / PER) + lane / PER, c = lane % PER;
-        *reinterpret_cast<uint4 *>(tile + (c >> 3) * half + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v[i];
+        *reinterpret_cast<uint4 *>(tile + pt_chunk(r, c, half)) = v[i];
     }
 }
 
@@ -414,9 +415,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             }
             if (!ok_all) break;
             pdl_trigger();  // (the decode does not read the records)
-            // the piece's record: 64 dims of the warp's 32 rows at a time through the
-            // stream's query tile (its products are complete), so that stores are
-            // whole 128-byte lines; chunk c of row i sits at c ^ (i & 7)
+            // the piece's record: D/2 dims of the warp's 32 rows at a time through the bytes
+            // of its own query rows (whose products are complete; the next item's queries
+            // go to the same bytes), so that stores are whole 128-byte lines
             long long at = -1;
             if (r < s.rows)
                 at = s.t_b == 0 ? pfx_main_row(a, s.g, head, s.item * kPtRows + r) + (s.split && x ? (long long)a.B * a.h_q : 0)
@@ -425,8 +426,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 if (!mbar_wait_bounded(&o_full[x], n_o & 1, a.err, abort_flag, 0x608)) break;
                 ++n_o;
                 tc_fence_after();
-                uint4 *buf = reinterpret_cast<uint4 *>(smem + C::Q_OFF + x * C::TILE + quarter * (C::TILE / 4));
-                constexpr int COLS = D == 128 ? 64 : 32;  // what fits: 32 rows in a quarter of the tile
+                unsigned char *buf = smem + C::Q_OFF + x * C::TILE;
+                constexpr int COLS = pt_record_cols(D);
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += COLS) {
 #pragma unroll
@@ -435,7 +436,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                         tmem_ld32(o_t + c0 + c1, o);
 #pragma unroll
                         for (int c = 0; c < 8; ++c)
-                            buf[lane * (COLS / 4) + ((c1 / 4 + c) ^ (lane & 7))] =
+                            *reinterpret_cast<uint4 *>(buf + pt_chunk(tr, c1 / 4 + c, C::HALF)) =
                                 make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
                     }
                     __syncwarp();
@@ -444,7 +445,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     for (int i = 0; i < PER; ++i) {
                         const int row = i * (32 / PER) + lane / PER, c = lane % PER;
                         const long long ra = __shfl_sync(0xFFFFFFFFu, at, row);
-                        if (ra >= 0) *reinterpret_cast<uint4 *>(a.rec_acc + ra * D + c0 + 4 * c) = buf[row * PER + (c ^ (row & 7))];
+                        if (ra >= 0)
+                            *reinterpret_cast<uint4 *>(a.rec_acc + ra * D + c0 + 4 * c) =
+                                *reinterpret_cast<const uint4 *>(buf + pt_chunk(quarter * 32 + row, c, C::HALF));
                     }
                     __syncwarp();
                 }
