@@ -1672,7 +1672,9 @@ __global__ void __launch_bounds__(9 * 32, 1) decode_tc_kernel(const DecodeArgs a
                     }
                 }
                 if (g < G && tig == 0) (leave ? a.whole_ml : a.part_ml)[row + g] = make_float2(m_run, l_run);
-                if (tid == 0) mlist[5 + mlist[4]++] = s;  // announced after the loop
+                // announced after the loop: one of at most two cut sequences (behind a prefix
+                // there is no such list: any number of whole sequences leave a record)
+                if (!kPrefix && tid == 0) mlist[5 + mlist[4]++] = s;
             }
             if (u + 1 < u1) {
                 while (u + 1 >= prefix[s + 1]) ++s;
