@@ -43,6 +43,7 @@ constexpr int kPtThreads = 32 * (2 + 8);    // TMA, MMA, two warpgroups
 constexpr int kPsEpi = 16;                  // epilogue warps of the score kernel
 constexpr int kPsThreads = 32 * (2 + kPsEpi);
 constexpr float kPtRaise = 8.f;             // log2 units a tile may exceed the running maximum by
+constexpr float kPtFar = 67108864.f;        // 2^26: beyond, a maximum's rounding (half a step) passes 4 log2 units
 
 // tcgen05.mma with A in tensor memory (bf16 pairs, one row per lane).
 __device__ __forceinline__ void tc_mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
@@ -332,6 +333,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16);
         const uint32_t s_t = lane_base + C::S_COL + x * 128, o_t = lane_base + C::O_COL + x * D;
         uint32_t n_s = 0, n_o = 0;
+        const float raise_by = kPtRaise / a.qscale;
         bool ok_all = true;
         for (int w = w0; w < w1 && ok_all;) {
             const PtSeg s = pt_segment(a, pre, ng, w, w1);
@@ -339,7 +341,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             if (s.t_b == s.t_e) continue;
             const int n_t = pt_tiles(s, x);
             const int r = s.split ? tr : x * 128 + tr;  // row of the item
-            float m = -INFINITY, l = 0.f;
+            float vm = -INFINITY, l = 0.f;  // maximum of the products (logits / qscale), sum
             if (n_t > 0) {
                 int entry;
                 pt_load_q<D>(pt_query<D>(a, s, head, r, &entry), quarter * 32, smem + C::Q_OFF + x * C::TILE, C::HALF);
@@ -372,12 +374,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     mx4[c & 2] = fmaxf(mx4[c & 2], fmaxf(__uint_as_float(v0[c]), __uint_as_float(v0[c + 1])));
                     mx4[(c & 2) + 1] = fmaxf(mx4[(c & 2) + 1], fmaxf(__uint_as_float(v1[c]), __uint_as_float(v1[c + 1])));
                 }
-                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.qscale;
+                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
                 // raise the maximum (and rescale what is summed) only beyond 2^8
-                const bool raise = mx > m + kPtRaise;  // true at the first tile (m = -inf)
+                const bool raise = mx > vm + raise_by;  // true at the first tile (vm = -inf)
                 if (__any_sync(0xFFFFFFFFu, raise)) {
-                    const float al = raise ? (j == 0 ? 0.f : ex2_approx(m - mx)) : 1.f;
-                    if (raise) m = mx;
+                    const float al = raise ? (j == 0 ? 0.f : ex2_approx((vm - mx) * a.qscale)) : 1.f;
+                    if (raise) vm = mx;
                     l *= al;
                     if (j > 0) {
 #pragma unroll 1
@@ -390,7 +392,20 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                         }
                     }
                 }
-                const float2 sc = make_float2(a.qscale, a.qscale), nm = make_float2(-m, -m);
+                // x - m in one rounding, m = vm qscale rounded.  Far from zero the rounding of m
+                // alone would scale every probability: there the maximum is taken off first.
+                float neg = -(vm * a.qscale);
+                const bool far = fabsf(neg) > kPtFar;
+                if (__any_sync(0xFFFFFFFFu, far)) {
+                    const float off = far ? vm : 0.f;
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) {
+                        v0[c] = __float_as_uint(__uint_as_float(v0[c]) - off);
+                        v1[c] = __float_as_uint(__uint_as_float(v1[c]) - off);
+                    }
+                    if (far) neg = 0.f;
+                }
+                const float2 sc = make_float2(a.qscale, a.qscale), nm = make_float2(neg, neg);
                 float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
                 uint32_t p[32];
                 auto half_tile = [&](const uint32_t(&v)[64], uint32_t col) {
@@ -453,7 +468,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 }
                 tc_fence_before();
             }
-            if (at >= 0) a.rec_ml[at] = make_float2(m, l);
+            if (at >= 0) a.rec_ml[at] = make_float2(vm * a.qscale, l);
         }
     }
 
@@ -675,7 +690,8 @@ __global__ void __launch_bounds__(kPsThreads, 1)
                     for (int i = 0; i < N; ++i) {
                         float x[G];
 #pragma unroll
-                        for (int j = 0; j < G; ++j) x[j] = fmaf(__uint_as_float(v[i * G + j]), a.qscale, -c[i * G + j]);
+                        for (int j = 0; j < G; ++j)  // (x rounded as in the statistics: a maximum's x - c is never above -log2 l)
+                            x[j] = __fmul_rn(__uint_as_float(v[i * G + j]), a.qscale) - c[i * G + j];
 #pragma unroll
                         for (int o = 1; o < G; o <<= 1)
 #pragma unroll
