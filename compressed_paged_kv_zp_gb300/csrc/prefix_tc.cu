@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 }
                 const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
                 // raise the maximum (and rescale what is summed) only beyond 2^8
-                const bool raise = mx > vm + raise_by;  // true at the first tile (vm = -inf)
+                const bool raise = mx > vm + raise_by;  // true at the first tile with a logit above -inf
                 if (__any_sync(0xFFFFFFFFu, raise)) {
                     const float al = raise ? (j == 0 ? 0.f : ex2_approx((vm - mx) * a.qscale)) : 1.f;
                     if (raise) vm = mx;
@@ -392,9 +392,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                         }
                     }
                 }
-                // x - m in one rounding, m = vm qscale rounded.  Far from zero the rounding of m
+                // x - m in one rounding, m = vm qscale rounded.  No logit above -inf yet: every
+                // probability is 2^(-inf), not 2^(-inf + inf).  Far from zero the rounding of m
                 // alone would scale every probability: there the maximum is taken off first.
-                float neg = -(vm * a.qscale);
+                float neg = vm == -INFINITY ? 0.f : -(vm * a.qscale);
                 const bool far = fabsf(neg) > kPtFar;
                 if (__any_sync(0xFFFFFFFFu, far)) {
                     const float off = far ? vm : 0.f;

@@ -62,3 +62,44 @@ def test_equal_logits_far_from_zero(zp, heads, big):  # noqa: F811
         tol = (2 * L + 8) * 2.0 ** -24 * absv + torch.finfo(c.dtype).eps / 2 * 1.01 * np.abs(want)
         assert (np.abs(out[int(s)].double().cpu().numpy() - want) <= tol).all()
     assert bool(torch.isfinite(S).all()) and float(S.max()) <= 1.0 + (c.b - 1)  # S0 < 1, one step's share of at most 1
+
+
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("blocks", BLOCKS)
+def test_logits_of_minus_infinity(zp, heads, blocks):  # noqa: F811
+    """Shared tokens with a logit of -infinity, from the first tile on or in the middle of it, or all of them:
+    the bits of the same call with logits so low that their weights are 0."""
+    c = _case(zp, heads)
+    c.qd[..., 0] = 1.0
+    g2 = int(np.nonzero(c.group == 2)[0][0])
+    at = _d(c.table[g2, list(BLOCKS[blocks])]).long()
+    got = []
+    for low in (-1e30, -INF):
+        c.Kd[at, :, :, 0] = low
+        got.append(c.run(zp))
+    (out_low, S_low), (out, S) = got
+    assert bool(torch.isfinite(out.float()).all()) and bool(torch.isfinite(S).all())
+    assert torch.equal(out, out_low) and torch.equal(S, S_low)
+
+
+@pytest.mark.parametrize("heads", HEADS)
+def test_a_sequence_with_nothing_but_minus_infinity(zp, heads):  # noqa: F811
+    """Every logit of a sequence -infinity: zeros, as the decode of the sequence alone gives; the others are not touched."""
+    c = _case(zp, heads)
+    c.qd[..., 0] = 1.0
+    good, _ = c.run(zp)
+    s = int(np.nonzero(c.group == 1)[0][1])
+    c.qd[s] = 0.0
+    c.qd[s, :, 0] = 1.0
+    L, p = int(c.lens[s]), 3 * c.b
+    for t in range(p, L):
+        c.Kd[int(c.table[s, t // c.b]), t % c.b, :, 0] = -INF
+    others = torch.arange(c.B, device=DEV) != s
+    c.Kd[_d(c.table[s, :3]).long(), :, :, 0] = -INF
+    mates = torch.from_numpy(np.nonzero(c.group == 1)[0]).to(DEV)
+    others[mates] = False  # they lose the prefix
+    out, _ = c.run(zp)
+    alone, _ = _alone(zp, c)
+    assert torch.equal(out[s], alone[s]) and not bool(out[s].any())
+    assert torch.equal(out[others], good[others])
+    torch.testing.assert_close(out[mates].float(), alone[mates].float(), rtol=2.0 ** -7, atol=6 * 2.0 ** -7)
