@@ -329,7 +329,12 @@ struct PfxJoin {
             };
 #pragma unroll
             for (int u = 0; u < U; ++u) fetch(u, min(u, last));
-            const bool holds = ml[0].x != -INFINITY;  // else a stream without a tile: no accumulator either
+            // else a stream without a tile (or of weightless tokens only): no accumulator
+            // either.  A row whose logits are all NaN has l = NaN: its record counts, and
+            // every row decides for itself.
+            bool holds = false;
+#pragma unroll
+            for (int j = 0; j < G; ++j) holds |= !(ml[j].y == 0.f);
             unsigned mask = __ballot_sync(0xFFFFFFFFu, holds);
             if (mask == 0) {
                 __syncwarp();
@@ -340,7 +345,7 @@ struct PfxJoin {
                 float Mn = fmaxf(M[j], ml[j].x);
 #pragma unroll
                 for (int o = 16; o; o >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(0xFFFFFFFFu, Mn, o));
-                const float f = holds ? exp2f(ml[j].x - Mn) : 0.f;
+                const float f = ml[j].x == Mn ? 1.f : exp2f(ml[j].x - Mn);  // (both -inf: a sum of 0, or NaN)
                 sm.f[warp][lane][j] = f;
                 float ls = f * ml[j].y;
 #pragma unroll

@@ -65,6 +65,40 @@ def test_equal_logits_far_from_zero(zp, heads, big):  # noqa: F811
 
 
 @pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("which", ["first", "last"])
+def test_a_bad_query_head_stays_alone(zp, heads, which):  # noqa: F811
+    """NaN in one q head of a kv head: its own output is NaN, every other head keeps its bits."""
+    c = _case(zp, heads)
+    good, _ = c.run(zp)
+    G = c.h_q // c.h_kv
+    h = 0 if which == "first" else G - 1
+    for s in np.nonzero(c.group >= 0)[0][::3]:
+        c.qd[int(s), h] = float("nan")
+    bad = torch.isnan(c.qd).any(-1)
+    out, _ = c.run(zp)
+    assert bool(torch.isnan(out[bad]).all())
+    assert torch.equal(out[~bad], good[~bad])
+
+
+@pytest.mark.parametrize("heads", HEADS)
+def test_bad_keys_reach_their_readers(zp, heads):  # noqa: F811
+    """NaN in the keys of one kv head, in a whole prefix and in one private token: NaN where the decode of every
+    sequence alone has it, and the other heads keep their bits."""
+    c = _case(zp, heads)
+    good, _ = c.run(zp)
+    g0 = np.nonzero(c.group == 0)[0]
+    lone = int(np.nonzero(c.group == 2)[0][1])
+    c.Kd[_d(c.table[g0[0], :20]).long(), :, 0] = float("nan")
+    L = int(c.lens[lone])
+    c.Kd[int(c.table[lone, (L - 1) // c.b]), (L - 1) % c.b, c.h_kv - 1] = float("nan")
+    out, _ = c.run(zp)
+    ref, _ = _alone(zp, c)
+    nan = torch.isnan(ref.float())
+    assert bool(nan.any()) and torch.equal(torch.isnan(out.float()), nan)
+    assert torch.equal(out[~nan], good[~nan])
+
+
+@pytest.mark.parametrize("heads", HEADS)
 @pytest.mark.parametrize("blocks", BLOCKS)
 def test_logits_of_minus_infinity(zp, heads, blocks):  # noqa: F811
     """Shared tokens with a logit of -infinity, from the first tile on or in the middle of it, or all of them:
