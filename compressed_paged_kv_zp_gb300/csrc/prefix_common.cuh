@@ -180,10 +180,12 @@ __device__ __forceinline__ long long pfx_slot(const PfxArgs &a, const int32_t *r
     return ((long long)blk << a.b_log) + (t & (a.b - 1));
 }
 
-// The table row every member's prefix agrees with: the first member's.
+// The table row every member's prefix agrees with: that of the first member inside
+// the batch (row 0 if there is none: nobody reads the group's records then).
 __device__ __forceinline__ const int32_t *pfx_row(const PfxArgs &a, const PfxGroup &g) {
-    const int s = pfx_member(a, g.m0);
-    return a.table + (size_t)(s < 0 ? 0 : s) * a.stride;
+    int s = -1;
+    for (int i = g.m0; s < 0 && i < g.m0 + g.n; ++i) s = pfx_member(a, i);
+    return a.table + (size_t)max(s, 0) * a.stride;
 }
 
 // Row of the score that batch entry s adds to in this step, -1: none (no prefix,

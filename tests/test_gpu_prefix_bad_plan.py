@@ -1,0 +1,46 @@
+"""Plans and tables that name what is not there, in prefix-shared decode: recorded, and
+what the bad entry does not touch keeps its value."""
+import numpy as np
+import pytest
+import torch
+
+from tests.test_gpu_prefix_attn import DEV, HEADS, Case, _d, zp  # noqa: F401 (zp is a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def _case(zp, heads, scored=True):  # noqa: F811
+    c = Case(zp, 401, HEADS[heads], [6, 9, 3], [7, 12, 5], (1, 40), 3)
+    if scored:
+        c.score_rows(402, c.b)
+    return c
+
+
+def _call(zp, c):  # noqa: F811
+    out, S = torch.full_like(c.qd, 7.0), torch.from_numpy(c.S0).to(DEV)
+    zp.zp_prefix_decode_attn(c.desc, c.qd, c.Kd, c.Vd, c.td, c.ld, c.plan, out, score_accum=S, window=c.window,
+                             score_rows=_d(c.rows))
+    torch.cuda.synchronize()
+    return out, S, zp.zp_device_status()
+
+
+@pytest.mark.parametrize("heads", ["qwen", "g8d64", "tiny32"])
+@pytest.mark.parametrize("place", ["first", "second", "last"])
+def test_the_other_members_of_a_bad_one(zp, heads, place):  # noqa: F811
+    """A member outside the batch, wherever it stands in its group: every other entry keeps its bits."""
+    c = _case(zp, heads)
+    good, S_good, status = _call(zp, c)
+    assert status == (0, 0)
+    start = c.plan.group_start.tolist()
+    g = 1  # neither the first group nor the last
+    at = {"first": start[g], "second": start[g] + 1, "last": start[g + 1] - 1}[place]
+    lost = int(c.plan.members[at])
+    c.plan.members[at] = -3 if place == "last" else c.B + 7
+    out, S, status = _call(zp, c)
+    assert status == (7, 0x142)
+    rest = torch.arange(c.B, device=DEV) != lost
+    assert torch.equal(out[rest], good[rest])
+    kept = torch.ones(S.shape[0], dtype=torch.bool)
+    if c.rows[lost] >= 0:
+        kept[int(c.rows[lost])] = False
+    assert torch.equal(S[kept.to(DEV)], S_good[kept.to(DEV)])
