@@ -301,8 +301,11 @@ zp_status zp_prefix_plan(const zp_cache_desc *D, const int32_t *block_table, int
  * lists s, 0 if none).  A member whose L does not exceed its group's prefix is
  * decoded alone.
  * The members' leading group_blocks table entries must be equal (the first
- * member's are used).  A member outside [0, B) (detail 0x142) and a block id
- * outside [0, N_total) (0x143) are recorded as ZP_ERR_DEVICE and skipped.  The
+ * member's are used).  A member outside [0, B) is recorded as ZP_ERR_DEVICE
+ * (detail 0x142) and skipped.  A block id outside [0, N_total) among a group's
+ * shared blocks is recorded (0x143) and nothing outside the cache is read; the
+ * outputs and scores of that group's members are then undefined, those of other
+ * entries are not affected.  The
  * sum over the tokens has another order than zp_paged_decode_attn's, so results
  * agree to rounding, not bit for bit; a call with the same arguments gives the
  * same bits.  Two calls that may overlap need a workspace each.

@@ -44,3 +44,19 @@ def test_the_other_members_of_a_bad_one(zp, heads, place):  # noqa: F811
     if c.rows[lost] >= 0:
         kept[int(c.rows[lost])] = False
     assert torch.equal(S[kept.to(DEV)], S_good[kept.to(DEV)])
+
+
+@pytest.mark.parametrize("heads", ["qwen", "g8d64", "tiny32"])
+def test_a_bad_shared_block_stays_in_its_group(zp, heads):  # noqa: F811
+    """A block id outside the cache in one group's prefix: the entries outside that group keep their bits."""
+    c = _case(zp, heads)
+    good, S_good, _ = _call(zp, c)
+    bad = np.nonzero(c.group == 1)[0]
+    for s, block in zip(bad, [-1, c.n_total, 2 ** 31 - 1, -2 ** 31] * 3):
+        c.td[int(s), 4] = block
+    out, S, status = _call(zp, c)
+    assert status == (7, 0x143)
+    rest = np.setdiff1d(np.arange(c.B), bad)
+    assert torch.equal(out[_d(rest).long()], good[_d(rest).long()])
+    rows = np.setdiff1d(np.arange(S.shape[0]), c.rows[bad])
+    assert torch.equal(S[_d(rows).long()], S_good[_d(rows).long()])
