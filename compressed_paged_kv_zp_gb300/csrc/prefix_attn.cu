@@ -299,11 +299,9 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_score_kernel(const PfxArgs
             __syncthreads();
             if (t + 1 < t_e) next.load(a, g, row, head, t0 + kPfxTokens);
             if (!live) continue;
-            constexpr int S = G >= 4 ? 4 : G;  // a score per S rows
-            auto at = [&](int i, int j) {
-                return a.score + ((size_t)max(srow[i], 0) * a.h_kv + head) * a.score_stride + t0 + tx + 16 * j;
-            };
-            auto on = [&](int i, int j) { return t0 + tx + 16 * j < g.tokens && srow[i] >= 0 && !(G == 8 && (ty & 1)); };
+            // a score per four rows (the thread's are of one entry), for G = 8 per eight
+            const bool scores = srow[0] >= 0 && !(G == 8 && (ty & 1));
+            float *at = a.score + ((size_t)max(srow[0], 0) * a.h_kv + head) * a.score_stride + t0 + tx;
             float x[4][4];
             pfx_logits<D>(sm, ty, tx, x);
             if (t == t_b) {  // the final statistics: the first logits are formed before they are
@@ -318,16 +316,11 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_score_kernel(const PfxArgs
                 float e[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) e[i] = x[i][j] - c[i];
-                // maximum over the group's rows: inside the thread for G <= 4, with the
-                // other half-warp (the next four rows) for G = 8
-                if constexpr (G >= 2) {
-                    e[0] = fmaxf(e[0], e[1]);
-                    e[2] = fmaxf(e[2], e[3]);
-                }
-                if constexpr (G >= 4) e[0] = fmaxf(e[0], e[2]);
+                // maximum over the group's rows: four inside the thread, for G = 8 with the
+                // other half-warp's (the next four rows)
+                e[0] = fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3]));
                 if constexpr (G == 8) e[0] = fmaxf(e[0], __shfl_xor_sync(0xFFFFFFFFu, e[0], 16));
-#pragma unroll
-                for (int i = 0; i < 4; i += S) pfx_put_score(at(i, j), exp2f(e[i]) * inv_w, on(i, j), first[i]);
+                pfx_put_score(at + 16 * j, exp2f(e[0]) * inv_w, scores && t0 + tx + 16 * j < g.tokens, first[0]);
             }
         }
     }
@@ -395,18 +388,14 @@ zp_status launch_score(const PfxArgs &a, cudaStream_t st) {
     return ZP_OK;
 }
 
-// fp32 caches: the kernel of the head dimension and group size.
+// fp32 caches: the kernel of the head dimension and group size (4 or 8, as the decode's).
 template <int D>
 zp_status launch_part_f32(const PfxArgs &a, int G, cudaStream_t st) {
-    if (G == 1) return launch_part<D, 1>(a, st);
-    if (G == 2) return launch_part<D, 2>(a, st);
     if (G == 4) return launch_part<D, 4>(a, st);
     return launch_part<D, 8>(a, st);
 }
 template <int D>
 zp_status launch_score_f32(const PfxArgs &a, int G, cudaStream_t st) {
-    if (G == 1) return launch_score<D, 1>(a, st);
-    if (G == 2) return launch_score<D, 2>(a, st);
     if (G == 4) return launch_score<D, 4>(a, st);
     return launch_score<D, 8>(a, st);
 }

@@ -39,7 +39,6 @@ struct PlanArgs {
     int B, b, n_total;
     int min_blocks, min_members;
     int32_t *prefix_lens, *n_groups, *group_start, *members, *group_blocks;
-    unsigned *err;
 };
 
 // Shared memory of one CTA.
@@ -372,12 +371,8 @@ extern "C" zp_status zp_prefix_plan(const zp_cache_desc *D, const int32_t *block
     // (blocks saved by a class, stride * (B - 1), fit 32 bits)
     if (table_stride >= 1 << 20 || (long long)table_stride * D->block_size > INT32_MAX)
         return fail(ZP_ERR_SHAPE, "prefix_plan: table rows of %d blocks", table_stride);
-    DeviceInfo dev;
-    rc = device_info(&dev);
-    if (rc != ZP_OK) return rc;
     const PlanArgs a = {block_table, table_stride, seq_lens, B, D->block_size, D->n_total_blocks, min_blocks, min_members,
-                        plan->prefix_lens, plan->n_groups, plan->group_start, plan->members, plan->group_blocks,
-                        dev.error_word};
+                        plan->prefix_lens, plan->n_groups, plan->group_start, plan->members, plan->group_blocks};
     rc = set_max_dynamic_smem(reinterpret_cast<const void *>(prefix_plan_kernel), sizeof(PlanSmem),
                               "prefix_plan: shared-memory attribute");
     if (rc != ZP_OK) return rc;

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_prefix_attn import DEV, HEADS, Case, _d, zp  # noqa: F401 (zp is a fixture)
+from tests.test_gpu_prefix_attn import BF16, DEV, F32, HEADS, Case, _d, zp  # noqa: F401 (zp is a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +60,19 @@ def test_a_bad_shared_block_stays_in_its_group(zp, heads):  # noqa: F811
     assert torch.equal(out[_d(rest).long()], good[_d(rest).long()])
     rows = np.setdiff1d(np.arange(S.shape[0]), c.rows[bad])
     assert torch.equal(S[_d(rows).long()], S_good[_d(rows).long()])
+
+
+@pytest.mark.parametrize("h_q,h_kv,dtype", [(8, 8, F32), (8, 4, F32), (16, 16, BF16), (32, 16, BF16), (12, 4, BF16), (4, 1, F32)])
+def test_head_layouts_that_are_refused(zp, h_q, h_kv, dtype):  # noqa: F811
+    """The decode's limits: groups of 1 and 2 with bf16 caches of up to 8 kv heads only."""
+    desc = zp.cache_desc(h_q, h_kv, 64, 16, 8, dtype)
+    with pytest.raises(zp.ZPError) as e:
+        zp.zp_prefix_decode_workspace_size(desc, 2, 4)
+    assert e.value.status == 2
+    q = torch.zeros(2, h_q, 64, dtype=dtype, device=DEV)
+    K = torch.zeros(8, 16, h_kv, 64, dtype=dtype, device=DEV)
+    ws = torch.empty(1 << 22, dtype=torch.uint8, device=DEV)
+    with pytest.raises(zp.ZPError) as e:
+        zp.zp_prefix_decode_attn(desc, q, K, K, _d(np.zeros((2, 4))), _d([3, 3]), zp.prefix_plan(2), torch.empty_like(q),
+                                 workspace=ws)
+    assert e.value.status == 2
