@@ -434,6 +434,10 @@ extern "C" zp_status zp_prefix_decode_attn(const zp_cache_desc *D, const void *q
     const uintptr_t al = (uintptr_t)q | (uintptr_t)k_cache | (uintptr_t)v_cache | (uintptr_t)out |
                          (uintptr_t)score_accum | (uintptr_t)workspace;
     if (al % 16) return fail(ZP_ERR_INVALID_ARG, "prefix_decode: buffers must be 16-byte aligned");
+    // the score forms the prefix's logits again, from the queries, when the outputs are written
+    const uintptr_t rows = (uintptr_t)B * D->h_q * D->head_dim * elem_bytes(D->dtype);
+    if (score_accum && (uintptr_t)q < (uintptr_t)out + rows && (uintptr_t)out < (uintptr_t)q + rows)
+        return fail(ZP_ERR_INVALID_ARG, "prefix_decode: out overlaps q in a scored call");
     const int G = D->h_q / D->h_kv;
     // tile counts are 32-bit: query rows * tiles of a table row bounds them
     if (((double)B * G) * ((double)table_stride * D->block_size / kPfxTokens + 1) > 2147483647.0 ||

@@ -305,10 +305,11 @@ zp_status zp_prefix_plan(const zp_cache_desc *D, const int32_t *block_table, int
  * (detail 0x142) and skipped.  A block id outside [0, N_total) among a group's
  * shared blocks is recorded (0x143) and nothing outside the cache is read; the
  * outputs and scores of that group's members are then undefined, those of other
- * entries are not affected.  The
- * sum over the tokens has another order than zp_paged_decode_attn's, so results
- * agree to rounding, not bit for bit; a call with the same arguments gives the
- * same bits.  Two calls that may overlap need a workspace each.
+ * entries are not affected.  With score_accum set, out must not overlap q
+ * (ZP_ERR_INVALID_ARG): the score reads the queries after the outputs are written.
+ * The sum over the tokens has another order than zp_paged_decode_attn's, so
+ * results agree to rounding, not bit for bit; a call with the same arguments gives
+ * the same bits.  Two calls that may overlap need a workspace each.
  * Limits: those of zp_paged_decode_attn and h_q/h_kv in {1,2,4,8} (1 and 2 with
  * bf16 caches). */
 size_t zp_prefix_decode_workspace_size(const zp_cache_desc *D, int32_t B, int32_t table_stride);

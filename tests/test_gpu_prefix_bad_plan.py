@@ -76,3 +76,17 @@ def test_head_layouts_that_are_refused(zp, h_q, h_kv, dtype):  # noqa: F811
         zp.zp_prefix_decode_attn(desc, q, K, K, _d(np.zeros((2, 4))), _d([3, 3]), zp.prefix_plan(2), torch.empty_like(q),
                                  workspace=ws)
     assert e.value.status == 2
+
+
+@pytest.mark.parametrize("heads", ["qwen", "tiny32"])
+def test_outputs_over_the_queries(zp, heads):  # noqa: F811
+    """Unscored calls may write their outputs over q; scored ones are refused."""
+    c = _case(zp, heads)
+    S = torch.from_numpy(c.S0).to(DEV)
+    good = torch.empty_like(c.qd)
+    zp.zp_prefix_decode_attn(c.desc, c.qd, c.Kd, c.Vd, c.td, c.ld, c.plan, good)
+    with pytest.raises(zp.ZPError):
+        zp.zp_prefix_decode_attn(c.desc, c.qd, c.Kd, c.Vd, c.td, c.ld, c.plan, c.qd, score_accum=S, window=c.b, score_rows=_d(c.rows))
+    zp.zp_prefix_decode_attn(c.desc, c.qd, c.Kd, c.Vd, c.td, c.ld, c.plan, c.qd)
+    torch.cuda.synchronize()
+    assert zp.zp_device_status() == (0, 0) and torch.equal(c.qd, good)

@@ -1,0 +1,33 @@
+"""Calls of the prefix operators that are refused because they could not be answered
+rightly (no GPU needed: the checks come before any device work)."""
+import ctypes
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def zp():
+    import compressed_paged_kv_zp_gb300 as m
+    return m
+
+
+def test_scored_output_over_the_queries(zp):
+    """The score reads q after out is written: a scored call must not write its outputs there."""
+    desc = ctypes.byref(zp.cache_desc(32, 8, 128, 16, 100, torch.bfloat16))
+    plan = ctypes.byref(zp._PrefixGroups(*[4096] * 5))
+    P, rows = ctypes.c_void_p(1 << 20), 2 * 32 * 128 * 2
+
+    def call(out, S):
+        return zp.lib.zp_prefix_decode_attn(desc, ctypes.c_void_p(1 << 24), P, P, P, 4, P, 2, plan, ctypes.c_void_p(out), S,
+                                            None, 0, 16, P, 0, None)
+
+    S = ctypes.c_void_p(1 << 26)
+    for out in (1 << 24, (1 << 24) + 16, (1 << 24) - rows + 16):
+        assert call(out, S) == 1
+        assert b"overlaps" in zp.lib.zp_last_error()
+    for out in ((1 << 24) + rows, (1 << 24) - rows):
+        call(out, S)
+        assert b"overlaps" not in zp.lib.zp_last_error()
+    call(1 << 24, None)  # not scored: each row is read before it is written
+    assert b"overlaps" not in zp.lib.zp_last_error()
