@@ -373,10 +373,19 @@ class PrefixPlan:
         self.B = B = prefix_lens.numel()
         self.prefix_lens, self.n_groups, self.group_start = prefix_lens, n_groups, group_start
         self.members, self.group_blocks = members, group_blocks
-        dev = _device()
+        self._dev = dev = _device()
         self._c = _PrefixGroups(_ints(prefix_lens, dev, "prefix_lens", B), _ints(n_groups, dev, "n_groups", 1),
                                 _ints(group_start, dev, "group_start", B + 1), _ints(members, dev, "members", B),
                                 _ints(group_blocks, dev, "group_blocks", B))
+
+
+def _groups_for(plan: PrefixPlan, B: int, dev: int):
+    """The plan's arrays for a call on device `dev` with B batch entries."""
+    if plan.B != B:
+        raise ValueError("the plan is for %d batch entries, the table has %d" % (plan.B, B))
+    if plan._dev != dev:
+        raise ValueError("the plan is on CUDA device %d, the current one is %d" % (plan._dev, dev))
+    return plan._c
 
 
 def prefix_plan(B: int, device="cuda") -> PrefixPlan:
@@ -389,11 +398,10 @@ def prefix_plan(B: int, device="cuda") -> PrefixPlan:
 def zp_prefix_plan(desc, block_table, seq_lens, plan: PrefixPlan, min_blocks=1, min_members=2, stream=None) -> None:
     """Find the groups that share at least min_blocks leading blocks among at least min_members entries."""
     B, table_stride = _table(block_table)
-    if plan.B != B:
-        raise ValueError("the plan is for %d batch entries, the table has %d" % (plan.B, B))
     dev = _device()
+    groups = _groups_for(plan, B, dev)
     rc = lib.zp_prefix_plan(desc, _ints(block_table, dev, "block_table"), table_stride, _ints(seq_lens, dev, "seq_lens", B),
-                            B, min_blocks, min_members, plan._c, _raw_stream(stream, dev))
+                            B, min_blocks, min_members, groups, _raw_stream(stream, dev))
     if rc:
         _check(rc)
 
@@ -409,9 +417,8 @@ def zp_prefix_decode_attn(desc, q, k_cache, v_cache, block_table, seq_lens, plan
                           window=0, workspace=None, stream=None, score_rows=None) -> None:
     """zp_paged_decode_attn with every group's shared prefix computed once for all its members."""
     B, table_stride = _table(block_table)
-    if plan.B != B:
-        raise ValueError("the plan is for %d batch entries, the table has %d" % (plan.B, B))
     dev = _device()
+    groups = _groups_for(plan, B, dev)
     shape, dt = (B, desc.h_q, desc.head_dim), _TORCH.get(desc.dtype)
     if q.shape != shape or out.shape != shape:
         raise ValueError("q and out must be [B][h_q][d] = %s, are %s and %s" % (shape, tuple(q.shape), tuple(out.shape)))
@@ -427,7 +434,7 @@ def zp_prefix_decode_attn(desc, q, k_cache, v_cache, block_table, seq_lens, plan
     elif score_rows is not None:
         raise ValueError("score_rows needs score_accum")
     args = (desc, _ptr_on(q, dev, "q"), _ptr_on(k_cache, dev, "k_cache"), _ptr_on(v_cache, dev, "v_cache"),
-            _ints(block_table, dev, "block_table"), table_stride, _ints(seq_lens, dev, "seq_lens", B), B, plan._c,
+            _ints(block_table, dev, "block_table"), table_stride, _ints(seq_lens, dev, "seq_lens", B), B, groups,
             _ptr_on(out, dev, "out"), _ptr_on(score_accum, dev, "score_accum"), _ints(score_rows, dev, "score_rows", B),
             n_rows, window)
     on = _raw_stream(stream, dev)

@@ -31,3 +31,24 @@ def test_scored_output_over_the_queries(zp):
         assert b"overlaps" not in zp.lib.zp_last_error()
     call(1 << 24, None)  # not scored: each row is read before it is written
     assert b"overlaps" not in zp.lib.zp_last_error()
+
+
+def test_plan_of_another_device(zp, monkeypatch):
+    """A plan's arrays are checked when it is made; a call with another device current must not hand them to its kernels."""
+    class On0(torch.Tensor):  # stands in for a tensor of device 0
+        def get_device(self):
+            return 0
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32).as_subclass(On0)  # noqa: E731
+    monkeypatch.setattr(zp, "_device", lambda: 0)
+    plan = zp.PrefixPlan(i(2), i(1), i(3), i(2), i(2))
+    desc = zp.cache_desc(32, 8, 128, 16, 10, torch.bfloat16)
+    q = torch.zeros(2, 32, 128, dtype=torch.bfloat16)
+    K = torch.zeros(10, 16, 8, 128, dtype=torch.bfloat16)
+    monkeypatch.setattr(zp, "_device", lambda: 1)
+    monkeypatch.setattr(zp, "_ptr_on", lambda t, dev, name: None if t is None else t.data_ptr())  # every other tensor is there
+    monkeypatch.setattr(zp, "_raw_stream", lambda stream, dev: 0)
+    monkeypatch.setattr(zp, "lib", None)  # nothing is launched
+    with pytest.raises(ValueError, match="device"):
+        zp.zp_prefix_plan(desc, i(2, 4), i(2), plan)
+    with pytest.raises(ValueError, match="device"):
+        zp.zp_prefix_decode_attn(desc, q, K, K, i(2, 4), i(2), plan, q.clone())
