@@ -367,16 +367,19 @@ class PrefixPlan:
     """Groups of batch entries that share leading blocks: int32 CUDA tensors
     prefix_lens [B], n_groups [1], group_start [B+1], members [B], group_blocks
     [B] (see zp_prefix_groups in zp.h).  zp_prefix_plan fills them from the block
-    table; a scheduler that knows its groups may fill them itself."""
+    table; a scheduler that knows its groups may fill them itself, in place: the
+    library is given their addresses when the plan is made."""
 
     def __init__(self, prefix_lens, n_groups, group_start, members, group_blocks):
-        self.B = B = prefix_lens.numel()
-        self.prefix_lens, self.n_groups, self.group_start = prefix_lens, n_groups, group_start
-        self.members, self.group_blocks = members, group_blocks
-        self._dev = dev = _device()
-        self._c = _PrefixGroups(_ints(prefix_lens, dev, "prefix_lens", B), _ints(n_groups, dev, "n_groups", 1),
-                                _ints(group_start, dev, "group_start", B + 1), _ints(members, dev, "members", B),
-                                _ints(group_blocks, dev, "group_blocks", B))
+        B, dev = prefix_lens.numel(), _device()
+        c = _PrefixGroups(_ints(prefix_lens, dev, "prefix_lens", B), _ints(n_groups, dev, "n_groups", 1),
+                          _ints(group_start, dev, "group_start", B + 1), _ints(members, dev, "members", B),
+                          _ints(group_blocks, dev, "group_blocks", B))
+        self.__dict__.update(B=B, prefix_lens=prefix_lens, n_groups=n_groups, group_start=group_start, members=members,
+                             group_blocks=group_blocks, _dev=dev, _c=c)
+
+    def __setattr__(self, name, value):
+        raise AttributeError("a plan's arrays are filled in place, not replaced (%s)" % name)
 
 
 def _groups_for(plan: PrefixPlan, B: int, dev: int):

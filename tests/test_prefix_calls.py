@@ -52,3 +52,17 @@ def test_plan_of_another_device(zp, monkeypatch):
         zp.zp_prefix_plan(desc, i(2, 4), i(2), plan)
     with pytest.raises(ValueError, match="device"):
         zp.zp_prefix_decode_attn(desc, q, K, K, i(2, 4), i(2), plan, q.clone())
+
+
+def test_a_plans_arrays_are_not_replaced(zp, monkeypatch):
+    """The library holds the arrays' addresses: another tensor under the same name would not be seen, and the old one's
+    memory would be read after it is gone."""
+    monkeypatch.setattr(zp, "_device", lambda: -1)  # (tensors of the host)
+    i = lambda n: torch.zeros(n, dtype=torch.int32)  # noqa: E731
+    plan = zp.PrefixPlan(i(2), i(1), i(3), i(2), i(2))
+    at = plan.members.data_ptr()
+    for name in ("prefix_lens", "n_groups", "group_start", "members", "group_blocks"):
+        with pytest.raises(AttributeError):
+            setattr(plan, name, i(2))
+    plan.members[:] = i(2) + 1
+    assert plan.members.data_ptr() == at == plan._c.members and plan.members.tolist() == [1, 1]
