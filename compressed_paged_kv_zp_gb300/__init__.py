@@ -442,14 +442,14 @@ def zp_prefix_decode_attn(desc, q, k_cache, v_cache, block_table, seq_lens, plan
             n_rows, window)
     on = _raw_stream(stream, dev)
     if workspace is None:
-        # memory of the stream that the work runs on, given back behind it (a tensor
-        # for it costs the host 5 us of the call's 19)
+        # memory of the stream that the work runs on, given back behind it: torch's
+        # allocator hands it to later work of that stream only
         n = max(zp_prefix_decode_workspace_size(desc, B, table_stride), 16)
-        at = torch._C._cuda_cudaCachingAllocator_raw_alloc(n, on)
+        at = torch.cuda.caching_allocator_alloc(n, dev, on)
         try:
             rc = lib.zp_prefix_decode_attn(*args, at, n, on)
         finally:
-            torch._C._cuda_cudaCachingAllocator_raw_delete(at)
+            torch.cuda.caching_allocator_delete(at)
     else:
         rc = lib.zp_prefix_decode_attn(*args, _ptr_on(workspace, dev, "workspace"), workspace.nbytes, on)
     if rc:

@@ -66,3 +66,33 @@ def test_a_plans_arrays_are_not_replaced(zp, monkeypatch):
             setattr(plan, name, i(2))
     plan.members[:] = i(2) + 1
     assert plan.members.data_ptr() == at == plan._c.members and plan.members.tolist() == [1, 1]
+
+
+def test_default_workspace(zp, monkeypatch):
+    """The default workspace comes from torch's public allocator calls, for the stream of the work, and is given back
+    also when the call fails."""
+    log = []
+
+    class Lib:
+        def zp_prefix_decode_workspace_size(self, *a):
+            return 1000
+
+        def zp_prefix_decode_attn(self, *a):
+            log.append(("call", a[-3:]))
+            raise RuntimeError("stop")
+
+    class Stream:
+        cuda_stream = 77
+
+    monkeypatch.setattr(zp, "lib", Lib())
+    monkeypatch.setattr(zp, "_device", lambda: -1)  # (tensors of the host)
+    monkeypatch.setattr(torch.cuda, "caching_allocator_alloc", lambda n, dev, st: log.append(("alloc", n, dev, st)) or 4096)
+    monkeypatch.setattr(torch.cuda, "caching_allocator_delete", lambda at: log.append(("delete", at)))
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    plan = zp.PrefixPlan(i(2), i(1), i(3), i(2), i(2))
+    q = torch.zeros(2, 32, 128, dtype=torch.bfloat16)
+    K = torch.zeros(10, 16, 8, 128, dtype=torch.bfloat16)
+    with pytest.raises(RuntimeError, match="stop"):
+        zp.zp_prefix_decode_attn(zp.cache_desc(32, 8, 128, 16, 10, torch.bfloat16), q, K, K, i(2, 4), i(2), plan,
+                                 torch.zeros_like(q), stream=Stream())
+    assert log == [("alloc", 1000, -1, 77), ("call", (4096, 1000, 77)), ("delete", 4096)]
