@@ -61,7 +61,14 @@ def upload_packed(arrays, dev):
 
 
 class DecodeLoop:
-    """Batch of sequences decoding over `layers` paged layers of one pool."""
+    """Batch of sequences decoding over `layers` paged layers of one pool.
+
+    prefix_decode: leading blocks that at least two sequences share, from
+    prefix_min_blocks on, are attended to once per group.  It takes the place of
+    decode_rho, which is then off (`use_rho` tells): behind a prefix a decode does
+    not read the shared keys sequence by sequence and forms no row sums of them, so
+    a compression reads its sequence's keys itself, as with decode_rho=False.
+    """
 
     def __init__(self, h_q, h_kv, d, b, n_total, max_blocks, table_stride, layers=1, dtype=torch.bfloat16,
                  window=None, params=None, async_compress=False, layer_stride=None, device="cuda",
@@ -75,8 +82,6 @@ class DecodeLoop:
         self.desc = cache_desc(h_q, h_kv, d, b, n_total, dtype)
         self.params = params or score_params(window=self.window)
         self.async_compress = async_compress
-        # prefix_decode: groups of at least prefix_min_blocks shared blocks are
-        # attended to once for all their members
         self.prefix_decode, self.prefix_min_blocks = prefix_decode, prefix_min_blocks
         self.decode_rho = decode_rho and not prefix_decode
         # layers compressed per call (App. C.1's layer stride): bounds the

@@ -309,7 +309,11 @@ zp_status zp_prefix_plan(const zp_cache_desc *D, const int32_t *block_table, int
  * (ZP_ERR_INVALID_ARG): the score reads the queries after the outputs are written.
  * The sum over the tokens has another order than zp_paged_decode_attn's, so
  * results agree to rounding, not bit for bit; a call with the same arguments gives
- * the same bits.  Two calls that may overlap need a workspace each.
+ * the same bits.  With bf16 caches the probabilities of the shared tokens are
+ * rounded to bf16 for the product with the values (with 16 kv heads too, where
+ * zp_paged_decode_attn keeps them in 32 bits).  For the score, the maximum and the
+ * logarithm of the sum are held as one 32-bit number, and an addition to a row of S
+ * whose sum is subnormal leaves 0.  Two calls that may overlap need a workspace each.
  * Limits: those of zp_paged_decode_attn and h_q/h_kv in {1,2,4,8} (1 and 2 with
  * bf16 caches). */
 size_t zp_prefix_decode_workspace_size(const zp_cache_desc *D, int32_t B, int32_t table_stride);
