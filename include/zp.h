@@ -254,7 +254,8 @@ zp_status zp_build_slots(const zp_cache_desc *D, const int32_t *block_table, int
  * slots[i] (device int32) of layer l at k_base / v_base + l*layer_stride.  A
  * negative slot is skipped; one >= N_total * b is recorded as ZP_ERR_DEVICE
  * (detail 0x130) and skipped.  A slot named twice receives either row, or a mix
- * of both.  Addresses and strides are multiples of 16 bytes. */
+ * of both; rows read from slots that the same call writes are undefined too.
+ * Addresses and strides are multiples of 16 bytes. */
 zp_status zp_write_kv(const zp_cache_desc *D, const void *k_new, const void *v_new, int64_t token_stride,
                       int64_t new_layer_stride, const int32_t *slots, int32_t n_tokens, void *k_base, void *v_base,
                       int64_t layer_stride, int32_t layer_count, void *stream);
