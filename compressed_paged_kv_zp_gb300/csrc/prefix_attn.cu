@@ -14,7 +14,7 @@
 //     S[t] (+)= (1/w) max_{h in group} 2^(x_ht - m_h) / l_h.
 // Chain of launches: the prefix kernel; the decode, which needs nothing of it and
 // follows without a gap; the kernel that joins the records; the score.  8 sequences
-// behind 2k tokens 16 us, 64 behind 32k 59, scored 256 behind 4k 145 (bf16, 32 q and 8
+// behind 2k tokens 16 us, 64 behind 32k 60, scored 256 behind 4k 147 (bf16, 32 q and 8
 // kv heads of 128).  With the decode starting from the joined prefix instead, and its
 // own cooperative merge and score, the first two took 24 and 73.
 //
@@ -48,10 +48,11 @@ __device__ __forceinline__ void load_vec(const float *p, float *o) {
 // 64 query rows x 64 prefix tokens per tile, everything in fp32 in shared
 // memory; a thread holds 4 rows x 4 tokens of the logits and 4 rows x d/16 dims
 // of the accumulator, and the 16 threads of a row (a half-warp) share its
-// softmax statistics by shuffles.  Bound by the fp32 pipe and shared memory: eight
-// 16-byte loads per 64 FMAs.  The next tile waits in registers while one is computed.
-// (61 sequences in 7 groups behind 672 tokens, 16 q and 4 kv heads of 64: 10 us for two
-// tiles per CTA, scored in all 39 us.)
+// softmax statistics by shuffles: eight 16-byte loads per 64 FMAs.  The next tile waits
+// in registers while one is computed.  With few tiles per CTA bound by latency, the plan's
+// scan, the queries and the first tile one after another: 61 sequences in 7 groups behind
+// 672 tokens, 16 q and 4 kv heads of 64, two tiles per CTA, 10 us and scored in all 40 us
+// (4.4 TFLOP/s); of this kernel's cycles 28 % issue and 12 % use the fp32 pipe.
 template <int D>
 struct PfxSmem {
     float q[kPfxRows][D + 4];
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_part_kernel(const PfxArgs 
 // Window score of the prefix tokens from the final statistics: the logits again,
 // the maximum of x - (m + log2 l) over the q heads of the kv head, one
 // exponential per (sequence, kv head, token).  The first tile's logits do not wait for
-// the statistics (39 us where all of it waits: 45).
+// the statistics (40 us where all of it waits: 45).
 template <int D, int G>
 __global__ void __launch_bounds__(kPfxThreads) prefix_score_kernel(const PfxArgs a) {
     extern __shared__ __align__(16) unsigned char pfx_raw[];

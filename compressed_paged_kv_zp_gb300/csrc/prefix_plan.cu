@@ -18,8 +18,9 @@
 // are listed together), and the first CTA numbers the groups.  Bound by
 // latency (four cluster barriers and the gather of the first column); the rows
 // are read only up to their first difference.  256 entries behind a prefix of 64
-// blocks: 11.5 us; 2048 behind 16 prefixes of up to 256: 28.6 us, of which hashing 3.4,
-// the rows 7.5, counting and ranking 5.
+// blocks: 11.7 us; 2048 behind 16 prefixes of up to 256: 28.8 us, of which hashing 3.4,
+// the rows 7.5, counting and ranking 5 (the launch, the gather, the barriers and the first
+// CTA's numbering were not timed apart).
 #include <cooperative_groups.h>
 
 #include "zp_common.cuh"

@@ -27,7 +27,8 @@
 // 589, twice each), a tile of 256 rows 3150 to 3600.  64 sequences behind 32k tokens
 // (2048 query rows, 34 GFLOP, 134 MB of keys and values, 13.5 tiles per CTA): 35 us, of
 // which 5 until the first logits, 25 the tiles (1.4 PFLOP/s, 5.3 TB/s), 4.6 the 20 MB
-// of records.  Raising the maximum at every tile costs 1 us there.
+// of records.  Raising the maximum at every tile costs 1 us there, the test for a maximum
+// so far from zero that its rounding would count 0.2 us.
 #include <math.h>
 
 #include "prefix_common.cuh"
@@ -485,10 +486,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 // a kv head's q heads is taken in registers and consecutive lanes write
 // consecutive tokens of a score row.  Accumulators of two tiles (256 columns
 // each); per (token, sequence) one exponential of max_h (x_h - c_h),
-// c = m + log2 l.  Bound by the scores' bytes: 253 sequences behind 4k tokens 12 us
-// from the statistics on for 33 MB read and 33 MB written (5.5 TB/s; packed products and
-// three-way maxima in the epilogue change nothing), then 7 us for the 17 MB of logits of
-// the private tokens.  With eight epilogue warps, not sixteen, 4 us more in all.
+// c = m + log2 l.  253 sequences behind 4k tokens, all on the first row of their window:
+// 12 us from the statistics on for 33 MB of scores written, then 7 us for the 17 MB of
+// logits of the private tokens; on a later row, 33 MB read as well, 3 us more.  No unit is
+// full (over the kernel DRAM 14 % of its peak, L1 49 %, instructions in 48 % of the cycles):
+// bound by the latency of the epilogue's chain from tensor memory to the stores.  Packed
+// products and three-way maxima in it change nothing, with eight epilogue warps, not
+// sixteen, the call takes 4 us more.
 template <int D>
 struct PsCfg {
     static constexpr int KH = D / 64;

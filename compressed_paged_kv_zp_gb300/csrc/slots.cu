@@ -17,7 +17,8 @@
 // in distributed shared memory.  Latency bound: the redundant scan and count cost
 // less than a second launch (512 sequences of a token each 6.0 us, 16 prompts of 32k
 // tokens, half a million slots, 12.6 us).  In place (table_out = block_table) there is one
-// cluster, since the counts read entries that other clusters would write.
+// cluster, since the counts read entries that other clusters would write (in place, every
+// block placed already: 7.8 and 48.6 us).
 #include <cooperative_groups.h>
 
 #include "zp_common.cuh"
