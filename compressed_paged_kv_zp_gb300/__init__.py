@@ -349,14 +349,17 @@ def zp_write_kv(desc, k_new, v_new, slots, k_cache, v_cache, stream=None) -> Non
         raise ValueError("k_new, v_new, k_cache and v_cache must have the cache's type")
     if k_new.get_device() != dev or v_new.get_device() != dev:
         raise ValueError("k_new and v_new must be CUDA tensors on the current device")
-    strides = k_new.stride()
-    if n and (strides[-2:] != (d, 1) or v_new.stride() != strides):
+    # (layer, token, head, element); a stride along a dimension of one entry means nothing
+    row = h_kv * d
+    strides = [(x.stride(0) if layers > 1 else 0, x.stride(-3) if n > 1 else row, x.stride(-2) if h_kv > 1 else d, x.stride(-1))
+               for x in (k_new, v_new)]
+    if n and (strides[0][2:] != (d, 1) or strides[1] != strides[0]):
         raise ValueError("the row [h_kv][d] of a token must be contiguous, and k_new and v_new must have the same strides")
     _check_cache(desc, k_cache, v_cache, layers)
     if n == 0:
         return
-    rc = lib.zp_write_kv(desc, k_new.data_ptr(), v_new.data_ptr(), strides[-3] if n > 1 else max(strides[-3], h_kv * d),
-                         strides[0] if layers > 1 else 0, _ints(slots, dev, "slots"), n, _ptr_on(k_cache, dev, "k_cache"),
+    rc = lib.zp_write_kv(desc, k_new.data_ptr(), v_new.data_ptr(), strides[0][1], strides[0][0], _ints(slots, dev, "slots"), n,
+                         _ptr_on(k_cache, dev, "k_cache"),
                          _ptr_on(v_cache, dev, "v_cache"), k_cache.stride(0) if layers > 1 else 0, layers,
                          _raw_stream(stream, dev))
     if rc:

@@ -96,3 +96,37 @@ def test_default_workspace(zp, monkeypatch):
         zp.zp_prefix_decode_attn(zp.cache_desc(32, 8, 128, 16, 10, torch.bfloat16), q, K, K, i(2, 4), i(2), plan,
                                  torch.zeros_like(q), stream=Stream())
     assert log == [("alloc", 1000, -1, 77), ("call", (4096, 1000, 77)), ("delete", 4096)]
+
+
+def test_write_kv_strides_that_mean_nothing(zp, monkeypatch):
+    """One token, one kv head or one layer: the stride along that dimension is any number, and differs between k and v."""
+    got = []
+
+    class Lib:
+        def zp_write_kv(self, desc, k, v, token_stride, layer_stride, slots, n, K, V, cache_layer_stride, layers, stream):
+            got.append((token_stride, layer_stride, n, layers))
+            return 0
+
+    monkeypatch.setattr(zp, "lib", Lib())
+    monkeypatch.setattr(zp, "_device", lambda: -1)  # (tensors of the host)
+    monkeypatch.setattr(zp, "_raw_stream", lambda stream, dev: 0)
+    bf, i = torch.bfloat16, lambda n: torch.zeros(n, dtype=torch.int32)  # noqa: E731
+    d = 64
+
+    def call(k, v, n, h_kv, layers=None):
+        K = torch.zeros(*([layers] if layers else []), 3, 16, h_kv, d, dtype=bf)
+        zp.zp_write_kv(zp.cache_desc(8, h_kv, d, 16, 3, bf), k, v, i(n), K, K.clone())
+        return got.pop()
+
+    fused = torch.zeros(1, 12, d, dtype=bf)
+    assert call(fused[:, 8:10], torch.zeros(1, 2, d, dtype=bf), 1, 2) == (2 * d, 0, 1, 1)            # one token
+    assert call(torch.zeros(5, 1027, dtype=bf)[1:2, :2 * d].view(1, 2, d), torch.zeros(1, 2, d, dtype=bf), 1, 2)[0] == 2 * d
+    swapped = torch.zeros(1, 7, d, dtype=bf).transpose(0, 1)                                          # one head
+    assert call(swapped, torch.zeros(7, 1, d, dtype=bf), 7, 1) == (d, 0, 7, 1)
+    assert call(torch.zeros(4, 7, 2, d, dtype=bf)[2:3], torch.zeros(7, 1, 2, d, dtype=bf).transpose(0, 1), 7, 2, 1) == (2 * d, 0, 7, 1)
+    assert call(torch.zeros(2, 7, 6, d, dtype=bf)[:, :, :2], torch.zeros(2, 7, 6, d, dtype=bf)[:, :, 4:], 7, 2, 2) == (6 * d, 42 * d, 7, 2)
+    for k, v in ((torch.zeros(7, 2, 2 * d, dtype=bf)[..., ::2], torch.zeros(7, 2, d, dtype=bf)),          # elements apart
+                 (torch.zeros(2, 7, d, dtype=bf).transpose(0, 1), torch.zeros(2, 7, d, dtype=bf).transpose(0, 1)),  # heads apart
+                 (torch.zeros(7, 4, d, dtype=bf)[:, :2], torch.zeros(7, 2, d, dtype=bf))):                 # other strides
+        with pytest.raises(ValueError):
+            call(k, v, 7, 2)
