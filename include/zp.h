@@ -315,8 +315,8 @@ zp_status zp_prefix_plan(const zp_cache_desc *D, const int32_t *block_table, int
  * zp_paged_decode_attn keeps them in 32 bits).  For the score, the maximum and the
  * logarithm of the sum are held as one 32-bit number, and an addition to a row of S
  * whose sum is subnormal leaves 0.  Two calls that may overlap need a workspace each.
- * Limits: those of zp_paged_decode_attn and h_q/h_kv in {1,2,4,8} (1 and 2 with
- * bf16 caches). */
+ * Limits: those of zp_paged_decode_attn; with bf16 caches of 1, 2, 4 or 8 kv heads
+ * also h_q/h_kv of 1 and 2. */
 size_t zp_prefix_decode_workspace_size(const zp_cache_desc *D, int32_t B, int32_t table_stride);
 zp_status zp_prefix_decode_attn(const zp_cache_desc *D, const void *q, const void *k_cache, const void *v_cache,
                                 const int32_t *block_table, int32_t table_stride, const int32_t *seq_lens, int32_t B,
