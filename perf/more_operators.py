@@ -103,7 +103,7 @@ def _quantise(x, group):
     x = x.float().unflatten(-1, (-1, group))
     lo, hi = x.amin(-1, keepdim=True), x.amax(-1, keepdim=True)
     lo = _bf16_below(lo)
-    step = -_bf16_below(-((hi - lo) / 15))
+    step = -_bf16_below(-((hi - lo) / hi.new_full((), 15.0)))  # (by a host number torch multiplies by 1/15)
     step = step.clamp(min=2.0 ** -126)
     code = torch.floor((x - lo).double() / step.double() + 0.5).float()
     return code, step, lo
@@ -512,7 +512,7 @@ def _kept(x, group):
         return (trunc + away * 65536).int().view(torch.float32)
 
     lo = cut(lo, False)
-    step = torch.maximum(cut((hi - lo) / 15, True), torch.tensor(2.0 ** -126, device=DEV))
+    step = torch.maximum(cut((hi - lo) / hi.new_full((), 15.0), True), hi.new_full((), 2.0 ** -126))
     code = torch.floor((g - lo[..., None]).double() / step[..., None].double() + 0.5)
     return (lo[..., None].double() + code * step[..., None].double()).reshape(x.shape)
 
