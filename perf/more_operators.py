@@ -278,9 +278,10 @@ def _prepare_compact(case, rng, gen):
     lens = np.full(n, L)
     lens[1::3] -= rng.integers(0, min(b, L - k + 1), size=len(lens[1::3]))
     targets = -(-k // b)
-    table, total, fresh = _tables(rng, lens, b, L, n * targets)  # targets of their own, as behind a shared prompt
+    # targets of their own, as behind a shared prompt; as many blocks in all whatever the lengths drawn
+    table, total, fresh = _tables(rng, lens, b, L, n * (targets + -(-L // b)) - int((-(-lens // b)).sum()))
     K, V = _make_cache(case, total, gen, l)
-    dst = fresh.reshape(n, targets)
+    dst = fresh[:n * targets].reshape(n, targets)
     # keep sets: k of the L positions, ascending
     score = torch.rand(l, n, h_kv, L, device=DEV, generator=gen)
     score = torch.where(torch.arange(L, device=DEV) < _dev(lens)[:, None, None], score, -1.0)
