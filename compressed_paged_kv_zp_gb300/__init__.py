@@ -39,6 +39,8 @@ EXPORTS = [
     "zp_pool_create", "zp_pool_destroy", "zp_pool_num_free", "zp_pool_refcount", "zp_pool_alloc",
     "zp_pool_incref", "zp_pool_release", "zp_plan_compaction", "zp_plan_compaction_batch",
     "zp_plan_capacity",
+    "zp_q4_tile_bytes", "zp_q4_write_kv", "zp_q4_append_kv", "zp_q4_read_kv", "zp_q4_decode_workspace_size",
+    "zp_q4_decode_attn", "zp_q4_compact_pages",
     # include/zp_sched.h
     "zp_sched_create", "zp_sched_destroy", "zp_sched_add_request", "zp_sched_schedule", "zp_sched_commit",
     "zp_sched_take_compressions", "zp_sched_compression_done", "zp_sched_counts", "zp_sched_request_info",
@@ -155,6 +157,15 @@ def _load() -> ctypes.CDLL:
     lib.zp_compress_rho_supported.argtypes = [D, ctypes.POINTER(ScoreParams), I32, I32]
     lib.zp_compress_layers_rho.argtypes = [D, ctypes.POINTER(ScoreParams), P, P, I64, I32, P, I32, P, P, I32, P,
                                            P, I64, P, I32, I32, P, P, P, P, I32, P, P]
+    lib.zp_q4_tile_bytes.restype = SZ
+    lib.zp_q4_tile_bytes.argtypes = [D, I32]
+    lib.zp_q4_write_kv.argtypes = [D, I32, P, P, I64, I64, P, I32, P, P, I64, I32, P]
+    lib.zp_q4_append_kv.argtypes = [D, I32, P, P, P, P, P, I32, P, I32, P]
+    lib.zp_q4_read_kv.argtypes = [D, I32, P, P, I64, P, I32, P, P, I64, I64, I32, P]
+    lib.zp_q4_decode_workspace_size.restype = SZ
+    lib.zp_q4_decode_workspace_size.argtypes = [D, I32, I32, I32, I32]
+    lib.zp_q4_decode_attn.argtypes = [D, I32, P, P, P, P, I32, P, I32, P, P, P, I32, I32, P, SZ, P]
+    lib.zp_q4_compact_pages.argtypes = [D, I32, P, P, I64, I32, P, I64, P, P, I32, P, I32, P, P, I32, P, I32, P]
     lib.zp_pool_create.restype = P
     lib.zp_pool_create.argtypes = [I32]
     lib.zp_pool_destroy.argtypes = [P]
@@ -455,6 +466,178 @@ def zp_prefix_decode_attn(desc, q, k_cache, v_cache, block_table, seq_lens, plan
             torch.cuda.caching_allocator_delete(at)
     else:
         rc = lib.zp_prefix_decode_attn(*args, _ptr_on(workspace, dev, "workspace"), workspace.nbytes, on)
+    if rc:
+        _check(rc)
+
+
+# ----------------------------------------------------------------------------- 4-bit cache
+def zp_q4_tile_bytes(desc: CacheDesc, group: int = 32) -> int:
+    """Bytes of a tile (16 tokens of one kv head) of a 4-bit cache."""
+    n = lib.zp_q4_tile_bytes(desc, group)
+    if n == 0:
+        raise ZPError(2, lib.zp_last_error().decode())
+    return n
+
+
+def zp_q4_cache(desc: CacheDesc, group: int = 32, layers=None, device="cuda"):
+    """An empty 4-bit cache (all values 0): k_cache, v_cache uint8 [N_total][h_kv][b/16][tile], with a
+    leading dimension of `layers` where given."""
+    shape = (desc.n_total_blocks, desc.h_kv, desc.block_size // 16, zp_q4_tile_bytes(desc, group))
+    if layers is not None:
+        shape = (layers,) + shape
+    return torch.zeros(shape, dtype=torch.uint8, device=device), torch.zeros(shape, dtype=torch.uint8, device=device)
+
+
+def _q4_caches(desc, group, k_cache, v_cache, dev, several=None):
+    """(address, address, layers, bytes between layers) of a 4-bit cache of one layer or, with a fifth
+    dimension, of several (`several`: which of the two the call wants)."""
+    shape = (desc.n_total_blocks, desc.h_kv, desc.block_size // 16, zp_q4_tile_bytes(desc, group))
+    layers = k_cache.shape[0] if k_cache.dim() == 5 and several is not False else None
+    want = shape if layers is None else (layers,) + shape
+    if k_cache.shape != want or v_cache.shape != want or not (k_cache.dtype is v_cache.dtype is torch.uint8):
+        raise ValueError("k_cache and v_cache must be uint8 [N_total][h_kv][b/16][tile] = %s%s, are %s and %s"
+                         % (shape, "" if several is False else " (or one of these per layer)", tuple(k_cache.shape),
+                            tuple(v_cache.shape)))
+    return (_ptr_on(k_cache, dev, "k_cache"), _ptr_on(v_cache, dev, "v_cache"), layers,
+            0 if layers is None else k_cache.numel() // max(layers, 1))
+
+
+def _q4_rows(desc, k, v, n, layers, dev, names):
+    """(address, address, token stride, layer stride) of rows [n][h_kv][d] or [layers][n][h_kv][d]."""
+    h_kv, d = desc.h_kv, desc.head_dim
+    shape = (n, h_kv, d) if layers is None else (layers, n, h_kv, d)
+    if k.shape != shape or v.shape != shape:
+        raise ValueError("%s and %s must be %s, are %s and %s" % (*names, shape, tuple(k.shape), tuple(v.shape)))
+    if not (k.dtype is v.dtype is _TORCH.get(desc.dtype)):
+        raise ValueError("%s and %s must have the descriptor's type" % names)
+    if k.get_device() != dev or v.get_device() != dev:
+        raise ValueError("%s and %s must be CUDA tensors on the current device" % names)
+    # (layer, token, head, element); a stride along a dimension of one entry means nothing
+    row = h_kv * d
+    strides = [(x.stride(0) if layers and layers > 1 else 0, x.stride(-3) if n > 1 else row, x.stride(-2) if h_kv > 1 else d,
+                x.stride(-1)) for x in (k, v)]
+    if n and (strides[0][2:] != (d, 1) or strides[1] != strides[0]):
+        raise ValueError("the row [h_kv][d] of a token must be contiguous, and %s and %s must have the same strides" % names)
+    return k.data_ptr(), v.data_ptr(), strides[0][1], strides[0][0]
+
+
+def zp_q4_write_kv(desc, k_new, v_new, slots, k_cache, v_cache, group=32, stream=None) -> None:
+    """zp_write_kv into a 4-bit cache: rows [n][h_kv][d] (or [layers][n][h_kv][d]) quantised into their
+    slots (int32 [n]; negative: skipped)."""
+    dev, n = _device(), slots.numel()
+    K, V, layers, layer_bytes = _q4_caches(desc, group, k_cache, v_cache, dev)
+    k, v, token, layer = _q4_rows(desc, k_new, v_new, n, layers, dev, ("k_new", "v_new"))
+    rc = lib.zp_q4_write_kv(desc, group, k, v, token, layer, _ints(slots, dev, "slots"), n, K, V, layer_bytes,
+                            1 if layers is None else layers, _raw_stream(stream, dev))
+    if rc:
+        _check(rc)
+
+
+def zp_q4_append_kv(desc, k_new, v_new, k_cache, v_cache, block_table, seq_lens, group=32, stream=None) -> None:
+    """zp_append_kv into a 4-bit cache: k_new, v_new [B][h_kv][d], one token per sequence."""
+    B, table_stride = _table(block_table)
+    dev = _device()
+    K, V, _, _ = _q4_caches(desc, group, k_cache, v_cache, dev, several=False)
+    shape = (B, desc.h_kv, desc.head_dim)
+    if k_new.shape != shape or v_new.shape != shape or not (k_new.dtype is v_new.dtype is _TORCH.get(desc.dtype)):
+        raise ValueError("k_new and v_new must be [B][h_kv][d] = %s of the descriptor's type" % (shape,))
+    rc = lib.zp_q4_append_kv(desc, group, _ptr_on(k_new, dev, "k_new"), _ptr_on(v_new, dev, "v_new"), K, V,
+                             _ints(block_table, dev, "block_table"), table_stride, _ints(seq_lens, dev, "seq_lens", B), B,
+                             _raw_stream(stream, dev))
+    if rc:
+        _check(rc)
+
+
+def zp_q4_read_kv(desc, k_cache, v_cache, slots, k_out, v_out, group=32, stream=None) -> None:
+    """Rows of a 4-bit cache as bf16 or fp32: k_out, v_out [n][h_kv][d] (or [layers][n][h_kv][d]) receive
+    the rows at `slots` (int32 [n]; negative: the row is left as it was)."""
+    dev, n = _device(), slots.numel()
+    K, V, layers, layer_bytes = _q4_caches(desc, group, k_cache, v_cache, dev)
+    k, v, token, layer = _q4_rows(desc, k_out, v_out, n, layers, dev, ("k_out", "v_out"))
+    rc = lib.zp_q4_read_kv(desc, group, K, V, layer_bytes, _ints(slots, dev, "slots"), n, k, v, token, layer,
+                           1 if layers is None else layers, _raw_stream(stream, dev))
+    if rc:
+        _check(rc)
+
+
+def zp_q4_decode_workspace_size(desc: CacheDesc, B: int, table_stride: int, group: int = 32, scored: bool = True) -> int:
+    n = lib.zp_q4_decode_workspace_size(desc, group, B, table_stride, scored)
+    if n == 0:
+        raise ZPError(2, lib.zp_last_error().decode() or "unsupported decode shape")
+    return n
+
+
+def zp_q4_decode_attn(desc, q, k_cache, v_cache, block_table, seq_lens, out, score_accum=None, window=0, workspace=None,
+                      stream=None, score_rows=None, group=32) -> None:
+    """zp_paged_decode_attn over a 4-bit cache."""
+    B, table_stride = _table(block_table)
+    dev = _device()
+    shape, dt = (B, desc.h_q, desc.head_dim), _TORCH.get(desc.dtype)
+    if q.shape != shape or out.shape != shape:
+        raise ValueError("q and out must be [B][h_q][d] = %s, are %s and %s" % (shape, tuple(q.shape), tuple(out.shape)))
+    if not (q.dtype is out.dtype is dt):
+        raise ValueError("q and out must have the descriptor's type")
+    K, V, _, _ = _q4_caches(desc, group, k_cache, v_cache, dev, several=False)
+    n_rows = 0
+    if score_accum is not None:
+        n_rows = score_accum.shape[0]
+        if (score_accum.dtype is not torch.float32 or score_accum.dim() != 3 or (score_rows is None and n_rows < B) or
+                score_accum.shape[1:] != (desc.h_kv, table_stride * desc.block_size)):
+            raise ValueError("score_accum must be float32 [R][h_kv][table_stride*b] with a row per batch entry or a slot map")
+    elif score_rows is not None:
+        raise ValueError("score_rows needs score_accum")
+    args = (desc, group, _ptr_on(q, dev, "q"), K, V, _ints(block_table, dev, "block_table"), table_stride,
+            _ints(seq_lens, dev, "seq_lens", B), B, _ptr_on(out, dev, "out"), _ptr_on(score_accum, dev, "score_accum"),
+            _ints(score_rows, dev, "score_rows", B), n_rows, window)
+    on = _raw_stream(stream, dev)
+    if workspace is None:
+        # memory of the stream that the work runs on, given back behind it
+        n = max(zp_q4_decode_workspace_size(desc, B, table_stride, group, score_accum is not None), 16)
+        at = torch.cuda.caching_allocator_alloc(n, dev, on)
+        try:
+            rc = lib.zp_q4_decode_attn(*args, at, n, on)
+        finally:
+            torch.cuda.caching_allocator_delete(at)
+    else:
+        rc = lib.zp_q4_decode_attn(*args, _ptr_on(workspace, dev, "workspace"), workspace.nbytes, on)
+    if rc:
+        _check(rc)
+
+
+def zp_q4_compact_pages(desc, k_cache, v_cache, src_table, dst_targets, seq_lens, keep_idx, global_F=None, scores=None,
+                        rows=None, k_seq=None, group=32, stream=None) -> None:
+    """zp_compact_pages of a 4-bit cache of one or several layers: keep_idx int32 [n][h_kv][k] or
+    [layers][n][h_kv][k]; global_F float32 like the slots, [N_total][b][h_kv] (or one per layer), with the
+    score rows `scores` that zp_score_tokens left."""
+    n, table_stride = _table(src_table)
+    dev = _device()
+    K, V, layers, layer_bytes = _q4_caches(desc, group, k_cache, v_cache, dev)
+    lead = () if layers is None else (layers,)
+    k = keep_idx.shape[-1]
+    if keep_idx.shape != lead + (n, desc.h_kv, k):
+        raise ValueError("keep_idx must be %s, is %s" % (lead + (n, desc.h_kv, "k"), tuple(keep_idx.shape)))
+    if dst_targets.dim() != 2 or dst_targets.shape[0] != n:
+        raise ValueError("dst_targets must be [n][target_stride]")
+    score = None
+    if global_F is not None:
+        if global_F.dtype is not torch.float32 or global_F.shape != lead + (desc.n_total_blocks, desc.block_size, desc.h_kv):
+            raise ValueError("global_F must be float32 [N_total][b][h_kv] (or one of these per layer)")
+        if scores is None:
+            raise ValueError("global_F needs the score rows")
+        if scores.dim() != 3 + len(lead) or scores.shape[-2] != desc.h_kv or (layers and scores.shape[0] != layers):
+            raise ValueError("scores must be float32 [R][h_kv][stride] (or one of these per layer)")
+        if rows is None and scores.shape[-3] < n:
+            raise ValueError("scores must have a row per sequence or a row map")
+        if rows is not None and rows.numel() != n:
+            raise ValueError("rows must have one entry per sequence")
+        _ptr_on(scores, dev, "scores")
+        score = _score_rows(scores, rows)
+    rc = lib.zp_q4_compact_pages(desc, group, K, V, layer_bytes, 1 if layers is None else layers,
+                                 _ptr_on(global_F, dev, "global_F"), 0 if global_F is None or not lead else global_F.stride(0),
+                                 score, _ints(src_table, dev, "src_table"), table_stride,
+                                 _ints(dst_targets, dev, "dst_targets"), dst_targets.shape[1],
+                                 _ints(seq_lens, dev, "seq_lens", n), _ints(keep_idx, dev, "keep_idx"), k,
+                                 _ints(k_seq, dev, "k_seq", n), n, _raw_stream(stream, dev))
     if rc:
         _check(rc)
 

@@ -488,6 +488,84 @@ zp_status zp_compress_layers_rho(const zp_cache_desc *D, const zp_score_params *
                                  const int32_t *k_seq, int32_t *keep_idx, int32_t *tie_count, float *scores_out,
                                  int32_t Lmax, const zp_rho_rows *rho, void *stream);
 
+/* ---- a cache held in 4 bits ------------------------------------------------ */
+
+/* K and V kept in 4 bits [Zipage §3 has the cache's blocks and slots; the paper's cache
+ * is 16 bits wide].  A row (one token, one kv head) is cut into groups of `group`
+ * consecutive elements (32, 64 or 128, at most head_dim), each with a step and a
+ * lowest value lo in bf16; an element is kept as a code c of 4 bits and stands for
+ * lo + c * step.
+ *   Tile     16 tokens (slots 16j .. 16j+15 of a block) of one kv head: 16 rows of d/2
+ *            bytes of codes, then 16 rows of d/group 32-bit words, step in the low half, lo in
+ *            the high half.  Element e of a row is nibble e (low nibble first), but the
+ *            row's 16-byte chunks are exchanged: chunk c of the row of token t (of 16)
+ *            lies at chunk c ^ ((t / 2) % 4) for d = 128, c ^ ((t / 4) % 2) for d = 64.
+ *   Layer    [N_total][h_kv][b/16][tile]; several layers lie layer_stride bytes apart.
+ *            zp_q4_tile_bytes gives the bytes of a tile (d = 128, group 32: 1280, 0.31 of
+ *            bf16).
+ *   Quantising a group of elements x (32-bit arithmetic): lo is the largest bf16
+ *            value <= min x; step the smallest bf16 value >= (max x - lo) / 15, at least
+ *            2^-126; c = floor((x - lo) / step + 1/2) with the quotient not rounded.  So
+ *            |x - (lo + c * step)| <= step / 2, and for bf16 rows lo is min x.  A group with a
+ *            NaN or an infinity, or with a spread past the largest float, reads as NaN.
+ * D is the descriptor of the rows (dtype: of q, of the rows given and taken, of the output).
+ * Limits of every call: d in {64, 128}, b a multiple of 16, h_kv <= 256, N_total * b
+ * below 2^31 (ZP_ERR_SHAPE); caches 16-byte aligned.  0 = refused. */
+size_t zp_q4_tile_bytes(const zp_cache_desc *D, int32_t group);
+
+/* zp_write_kv into a 4-bit cache: the rows of n_tokens tokens (dtype, token_stride and
+ * new_layer_stride in elements, as there) are quantised into their slots of
+ * layer_count layers.  A negative slot is skipped, one >= N_total * b recorded as
+ * ZP_ERR_DEVICE (detail 0x150) and skipped; a slot named twice receives either row or a mix.
+ * Other slots keep their rows bit for bit. */
+zp_status zp_q4_write_kv(const zp_cache_desc *D, int32_t group, const void *k_new, const void *v_new,
+                         int64_t token_stride, int64_t new_layer_stride, const int32_t *slots, int32_t n_tokens,
+                         void *k_base, void *v_base, int64_t layer_stride, int32_t layer_count, void *stream);
+
+/* zp_append_kv into a 4-bit cache: one token per sequence, k_new, v_new [B][h_kv][d] into
+ * slot (L-1) % b of block table[(L-1)/b]; L = 0 skips the sequence.  Recorded and skipped:
+ * L outside [0, table_stride * b] (detail 0x151), a block outside [0, N_total) (0x152). */
+zp_status zp_q4_append_kv(const zp_cache_desc *D, int32_t group, const void *k_new, const void *v_new, void *k_cache,
+                          void *v_cache, const int32_t *block_table, int32_t table_stride, const int32_t *seq_lens,
+                          int32_t B, void *stream);
+
+/* Reads rows back: k_out, v_out row i (contiguous [h_kv][d], dtype, rows token_stride and
+ * layers out_layer_stride elements apart) receives the values of slot slots[i], lo + c * step
+ * in 32 bits, rounded once to dtype.  The row of a negative slot is left as it was; a
+ * slot >= N_total * b is recorded (detail 0x153) and its row left too.  A slot may be named more than once. */
+zp_status zp_q4_read_kv(const zp_cache_desc *D, int32_t group, const void *k_base, const void *v_base,
+                        int64_t layer_stride, const int32_t *slots, int32_t n_tokens, void *k_out, void *v_out,
+                        int64_t token_stride, int64_t out_layer_stride, int32_t layer_count, void *stream);
+
+/* zp_paged_decode_attn over a 4-bit cache: the same output, window score, skipping
+ * of L = 0, slot map and arguments, with k_t and v_t the values the codes stand for (not
+ * rounded to dtype).  q and out are dtype.  Slots behind a sequence's last token may hold
+ * anything.  Recorded as ZP_ERR_DEVICE: a length outside [0, table_stride * b] (detail 0x158;
+ * taken as the nearer bound), a block outside [0, N_total) among a sequence's blocks (0x159; its
+ * tokens weigh nothing), a slot >= n_score_rows (0x15a; not scored).
+ * The workspace is scratch: any content on entry, nothing kept; two calls that may
+ * overlap need one each.  Its size with scored = 0 serves calls without score_accum.
+ * Limits: B <= 4096, h_q/h_kv <= 8, B * table_stride * b below 2^31 (ZP_ERR_SHAPE);
+ * buffers 16-byte aligned; score_accum float [rows][h_kv][table_stride * b]. */
+size_t zp_q4_decode_workspace_size(const zp_cache_desc *D, int32_t group, int32_t B, int32_t table_stride,
+                                   int32_t scored);
+zp_status zp_q4_decode_attn(const zp_cache_desc *D, int32_t group, const void *q, const void *k_cache,
+                            const void *v_cache, const int32_t *block_table, int32_t table_stride,
+                            const int32_t *seq_lens, int32_t B, void *out, float *score_accum,
+                            const int32_t *score_rows, int32_t n_score_rows, int32_t window, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/* zp_compact_pages of a 4-bit cache: the kept rows move as they are, codes and
+ * parameters (nothing is quantised again), global_F as there; layer_stride in bytes.
+ * In place under the same rule.  Recorded as ZP_ERR_DEVICE and skipped: a kept position or its
+ * block out of range (detail 0x154), a target block (0x155), a score row (0x156).
+ * Limits: n and layer_count <= 65535, N_total * b * h_kv below 2^31 (ZP_ERR_SHAPE). */
+zp_status zp_q4_compact_pages(const zp_cache_desc *D, int32_t group, void *k_base, void *v_base, int64_t layer_stride,
+                              int32_t layer_count, float *global_F, int64_t F_layer_stride,
+                              const zp_score_rows *scores, const int32_t *src_table, int32_t table_stride,
+                              const int32_t *dst_targets, int32_t target_stride, const int32_t *seq_lens,
+                              const int32_t *keep_idx, int32_t k, const int32_t *k_seq, int32_t n, void *stream);
+
 /* ---- host block pool and planner (no device work) ------------------------ */
 typedef struct zp_pool zp_pool;
 
