@@ -8,10 +8,12 @@
 // pairs are laid one after another and every warp takes an equal contiguous range, so
 // ragged lengths cannot unbalance the grid.  A warp copies the tiles of its range to a ring of
 // its own in shared memory (bulk copies, one mbarrier per stage) and runs an online softmax in
-// base 2 over them.  A pair that lies in one warp's range is written out by it; of the others
-// every warp leaves a record (maximum, sum, accumulator) that q4_merge_kernel joins.  On window
-// steps the logits (log2 units) go to scratch; with the final statistics q4_score_kernel turns
-// them into probabilities, takes the maximum over the q heads and adds 1/w of it.
+// base 2 over them.  A pair that lies in one warp's range is written out by it.  Of a pair cut
+// between warps each keeps a record (reference, sums, accumulator) in shared memory; at the end
+// the CTA joins them and writes the pair out, or one record of it to the workspace where it
+// goes on in other CTAs.  q4_finish_kernel joins those (at most one pair per CTA boundary) and,
+// on window steps, turns the logits that the attention left (log2 units) into probabilities
+// with the final sums, takes the maximum over the q heads and adds 1/w of it to the score.
 #include <math.h>
 
 #include "q4_format.cuh"
@@ -20,7 +22,8 @@ namespace zp {
 namespace {
 
 constexpr int kQ4MaxB = 4096;
-constexpr int kMinUnits = 4;  // units per warp below which fewer warps take part
+constexpr int kMinUnits = 4;   // units per warp below which fewer warps take part
+constexpr int kMaxStages = 6;  // tiles (of keys and of values) a warp has in flight, at most
 
 struct Q4Args {
     const void *q;
@@ -38,10 +41,10 @@ struct Q4Args {
     const int32_t *score_rows;
     int n_score_rows;
     int *prefix;    // [B+1] units before each sequence (of one kv head)
-    float2 *stats;  // [B][h_q] final (max, sum), log2 units
-    float *rec;     // [2 * warps][G * (D + 2)]: per head max and sum, then the accumulators
+    float *stats;   // [B][h_q] reference + log2(sum) of the pairs that one CTA saw whole
+    float *rec;     // [2 * CTAs][G * (d + 4)]: per head (reference, sum for the output, sum, 0), then accumulators
     float *logits;  // [units][16][G]
-    int grid, warps;  // CTAs of the attention kernel, warps of one
+    int grid, warps, stages;  // CTAs of the attention kernel, warps of one, tiles in a warp's ring
     unsigned *err;
 };
 
@@ -50,8 +53,9 @@ struct Split {
     long long U, W;  // units, ranges
     int per_cta;     // ranges of a CTA: its first warps take one each
     __device__ __forceinline__ long long start(long long g) const { return g * U / W; }
-    // the range that holds unit x: the largest g with start(g) <= x
-    __device__ __forceinline__ long long owner(long long x) const { return ((x + 1) * W - 1) / U; }
+    __device__ __forceinline__ long long cta_start(int c) const { return start((long long)c * per_cta); }
+    // the CTA whose ranges hold unit x: the largest range g with start(g) <= x is its
+    __device__ __forceinline__ int cta_of(long long x) const { return (int)((((x + 1) * W - 1) / U) / per_cta); }
 };
 
 __device__ __forceinline__ Split make_split(const Q4Args &a, int units) {
@@ -143,9 +147,6 @@ __device__ __forceinline__ int q4_score_row(const Q4Args &a, int s, int L) {
     return r < 0 ? -1 : r;
 }
 
-template <typename T> __device__ __forceinline__ float to_f(T x);
-template <> __device__ __forceinline__ float to_f(float x) { return x; }
-template <> __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 template <typename T> __device__ __forceinline__ T from_f(float x);
 template <> __device__ __forceinline__ float from_f(float x) { return x; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __float2bfloat16_rn(x); }
@@ -159,20 +160,34 @@ __device__ __noinline__ void drain(uint64_t *full, int stages, int i, int n) {
         }
 }
 
+// ---------------------------------------------------------------- records
+// One pair's part in one range: per head float4 (reference m, sum that divides the output,
+// sum, 0), then the accumulators [G][D], all relative to 2^m.
+__device__ __forceinline__ int rec_floats(const Q4Args &a, int d) { return a.G * (d + 4); }
+
+// Normaliser of the score: p = 2^(logit - c).  An empty sum gives no score.
+__device__ __forceinline__ float score_norm(float m, float l) { return l == 0.f ? INFINITY : m + log2f(l); }
+
 // ---------------------------------------------------------------- fp32 products
 // One warp, GP >= G heads.  Logits: lane t and lane t + 16 take half of the dimensions of
 // token t each; values: every lane takes D/32 dimensions of all tokens.
-template <typename T, int D, int GP>
+template <int D, int GP>
 struct ScalarWarp {
+    using T = float;
+    static constexpr int kD = D, kWarps = 8, kCtas = 2;
     static constexpr int kDims = D / 32;
-    static constexpr int kSharedFloats = GP * D + kQ4Tile * GP;
+    static constexpr int kSharedBytes = (GP * D + kQ4Tile * GP) * 4;
     float m[GP], l[GP], acc[GP][kDims];
     float *q_s, *p_s;
 
+    __device__ __forceinline__ void init(unsigned char *shared) {
+        q_s = reinterpret_cast<float *>(shared);
+        p_s = q_s + GP * D;
+    }
     __device__ __forceinline__ void begin(const Q4Args &a, int s, int h, int lane) {
-        const T *q = static_cast<const T *>(a.q) + ((size_t)s * a.h_q + (size_t)h * a.G) * D;
+        const float *q = static_cast<const float *>(a.q) + ((size_t)s * a.h_q + (size_t)h * a.G) * D;
         __syncwarp();
-        for (int i = lane; i < GP * D; i += 32) q_s[i] = i < a.G * D ? to_f(q[i]) : 0.f;
+        for (int i = lane; i < GP * D; i += 32) q_s[i] = i < a.G * D ? q[i] : 0.f;
         __syncwarp();
 #pragma unroll
         for (int g = 0; g < GP; ++g) {
@@ -184,8 +199,8 @@ struct ScalarWarp {
     }
 
     // one tile; tokens >= valid weigh nothing
-    __device__ __forceinline__ void tile(const Q4Args &a, const unsigned char *kt, const unsigned char *vt, int valid,
-                                         float *logits, int lane) {
+    __device__ __forceinline__ void tile(const Q4Args &a, unsigned char *kt, unsigned char *vt, int valid, float *logits,
+                                         int lane) {
         const int t = lane & 15, half = lane >> 4;
         const int words = D >> a.lg_group;
         float x[GP];
@@ -213,7 +228,6 @@ struct ScalarWarp {
                 }
             }
         }
-        float alpha[GP];
 #pragma unroll
         for (int g = 0; g < GP; ++g) {
             x[g] = (x[g] + __shfl_xor_sync(0xFFFFFFFFu, x[g], 16)) * a.qscale;
@@ -224,15 +238,15 @@ struct ScalarWarp {
             const float was = m[g];
             m[g] = fmaxf(was, top);
             const float base = m[g] == -INFINITY ? 0.f : m[g];
-            alpha[g] = ex2_approx(was - base);
+            const float alpha = ex2_approx(was - base);
             const float p = ex2_approx(x[g] - base);
-            l[g] = l[g] * alpha[g] + p;  // of token t only: the lanes' sums are added at the end
+            l[g] = l[g] * alpha + p;  // of token t only: the lanes' sums are added at the end
             if (half == 0) {
                 p_s[t * GP + g] = p;
                 if (logits && g < a.G) logits[t * a.G + g] = x[g];
             }
 #pragma unroll
-            for (int j = 0; j < kDims; ++j) acc[g][j] *= alpha[g];
+            for (int j = 0; j < kDims; ++j) acc[g][j] *= alpha;
         }
         __syncwarp();
         const int e0 = lane * kDims;
@@ -255,236 +269,627 @@ struct ScalarWarp {
     }
 
     // sums over the lanes (both halves hold the same tokens' sums)
-    __device__ __forceinline__ void end() {
+    __device__ __forceinline__ void end(int lane) {
 #pragma unroll
         for (int g = 0; g < GP; ++g)
 #pragma unroll
             for (int o = 8; o; o >>= 1) l[g] += __shfl_xor_sync(0xFFFFFFFFu, l[g], o);
     }
     __device__ __forceinline__ void write_out(const Q4Args &a, int s, int h, int lane) const {
-        T *out = static_cast<T *>(a.out) + ((size_t)s * a.h_q + (size_t)h * a.G) * D;
+        float *out = static_cast<float *>(a.out) + ((size_t)s * a.h_q + (size_t)h * a.G) * D;
 #pragma unroll
         for (int g = 0; g < GP; ++g) {
             if (g >= a.G) break;
             const float r = l[g] == 0.f ? 0.f : 1.f / l[g];
 #pragma unroll
-            for (int j = 0; j < kDims; ++j) out[g * D + lane * kDims + j] = from_f<T>(acc[g][j] * r);
-            if (a.want_score && lane == 0) a.stats[(size_t)s * a.h_q + h * a.G + g] = make_float2(m[g], l[g]);
+            for (int j = 0; j < kDims; ++j) out[g * D + lane * kDims + j] = acc[g][j] * r;
+            if (a.want_score && lane == 0) a.stats[(size_t)s * a.h_q + h * a.G + g] = score_norm(m[g], l[g]);
         }
     }
     __device__ __forceinline__ void write_record(const Q4Args &a, float *rec, int lane) const {
 #pragma unroll
         for (int g = 0; g < GP; ++g) {
             if (g >= a.G) break;
-            if (lane == 0) reinterpret_cast<float2 *>(rec)[g] = make_float2(m[g], l[g]);
+            if (lane == 0) reinterpret_cast<float4 *>(rec)[g] = make_float4(m[g], l[g], l[g], 0.f);
 #pragma unroll
-            for (int j = 0; j < kDims; ++j) rec[2 * a.G + g * D + lane * kDims + j] = acc[g][j];
+            for (int j = 0; j < kDims; ++j) rec[4 * a.G + g * D + lane * kDims + j] = acc[g][j];
+        }
+    }
+};
+
+// ---------------------------------------------------------------- tensor-core products
+// bf16 queries, up to 8 q heads as the 8 columns of mma.sync m16n8k16: logits[t][h] with
+// the key codes as the left operand, out^T[i][h] with the value codes.  (One kv head has 8
+// query rows at most: the 128 rows of a tcgen05 tile would stand empty, and its operands
+// would have to be written to shared memory at four times the size of the codes.)  A code
+// becomes a bf16 number in a register by one and-or: 0x4300 | c is 128 + c, exactly.
+//   logits:  sum_i q_i (lo + c_i step) = lo sum_i q_i + step sum_i q_i c_i  per group.  The
+//     accumulator starts at -128 sum q, so that the product of 128 + c leaves sum q c;
+//     the lo part is a product of its own, of the parameter words (step, lo) as they lie
+//     in the tile with (0, sum q), the sum in three bf16 parts of 8 bits.  Nothing is rounded to
+//     16 bits: the logits are those of 32-bit arithmetic.
+//   output:  sum_t p_t (lo_t + c_t step_t): p rounded to bf16 and transposed (movmatrix), p *
+//     step rounded to bf16 again per group, both with half a step of 2^-8 relative; the sum
+//     that divides is that of the rounded p, and the 128 is taken off with the rounded
+//     products (a product with -128, into the accumulator that also sums p lo and p), so that
+//     each token's weight is off by the two roundings and no more.
+// ldmatrix of a natural row of codes gives lane 4t + j the word j of a 16-byte chunk of
+// token t, the layout of the left operand; its transposed form gives the codes of two
+// adjacent tokens for 4 dimensions, the layout of the transposed values.
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t mul_bf2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// codes e and e + 4 of a word (or code e of two tokens) as 128 + c
+template <int E>
+__device__ __forceinline__ uint32_t codes(uint32_t w) {
+    return ((w >> (4 * E)) & 0x000F000Fu) | 0x43004300u;
+}
+// N words of shared memory, N of 1, 2, 4
+template <int N>
+__device__ __forceinline__ void lds(const uint32_t *p, uint32_t (&w)[N]) {
+    if constexpr (N == 4) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(p);
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    } else if constexpr (N == 2) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(p);
+        w[0] = x.x, w[1] = x.y;
+    } else {
+        w[0] = *p;
+    }
+}
+
+constexpr float kLazyMax = 8.f;  // the reference follows the maximum when it is passed by this much (log2)
+
+template <int D, int LG>
+struct TcWarp {
+    using T = __nv_bfloat16;
+    static constexpr int kD = D, kWarps = 16, kCtas = 1;
+    static constexpr int kSharedBytes = 0;
+    static constexpr int NG = D >> LG, kChunks = D / 32, kPerGroup = (1 << LG) / 32;  // chunks of a row, of a group
+    uint32_t qb[kChunks][2][2];  // queries as the right operand, by chunk and half of its words
+    uint32_t ob[3];              // sums of the queries of (head lane / 4, group lane % 4), in three parts
+    float start[NG][2];          // -128 * those of heads 2 (lane % 4), + 1
+    float acc[kChunks][2][4], off[4];
+    float thr[2], base[2], l[2];  // of those heads: m + kLazyMax (-inf: none yet), m, sum over this lane's tokens
+
+    __device__ __forceinline__ void init(unsigned char *) {}
+
+    __device__ __forceinline__ void begin(const Q4Args &a, int s, int h, int lane) {
+        const int n = lane >> 2, j = lane & 3;
+        const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
+                                                         ((size_t)s * a.h_q + (size_t)h * a.G + n) * D);
+        float sum[NG];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) sum[g] = 0.f;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (n < a.G) w = __ldg(q + c * 4 + j);
+            qb[c][0][0] = __byte_perm(w.x, w.z, 0x5410);
+            qb[c][0][1] = __byte_perm(w.x, w.z, 0x7632);
+            qb[c][1][0] = __byte_perm(w.y, w.w, 0x5410);
+            qb[c][1][1] = __byte_perm(w.y, w.w, 0x7632);
+            const float2 x0 = bf2_to_f2(w.x), x1 = bf2_to_f2(w.y), x2 = bf2_to_f2(w.z), x3 = bf2_to_f2(w.w);
+            sum[c / kPerGroup] += ((x0.x + x0.y) + (x1.x + x1.y)) + ((x2.x + x2.y) + (x3.x + x3.y));
+        }
+        float part = 0.f;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            sum[g] += __shfl_xor_sync(0xFFFFFFFFu, sum[g], 1);
+            sum[g] += __shfl_xor_sync(0xFFFFFFFFu, sum[g], 2);
+            start[g][0] = -128.f * __shfl_sync(0xFFFFFFFFu, sum[g], 8 * j);
+            start[g][1] = -128.f * __shfl_sync(0xFFFFFFFFu, sum[g], 8 * j + 4);
+            if (j == g) part = sum[g];
+        }
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const float x = __bfloat162float(__float2bfloat16_rn(part));
+            ob[i] = __float_as_uint(x);  // (the high half: the place of lo in a parameter word)
+            part -= x;
+        }
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[c][m][i] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) off[i] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) thr[i] = -INFINITY, base[i] = 0.f, l[i] = 0.f;
+    }
+
+    __device__ __forceinline__ void tile(const Q4Args &a, unsigned char *kt, unsigned char *vt, int valid, float *logits,
+                                         int lane) {
+        const int n = lane >> 2, j = lane & 3;
+        uint32_t *kp = reinterpret_cast<uint32_t *>(kt + q4_code_bytes(D)), *vp = reinterpret_cast<uint32_t *>(vt + q4_code_bytes(D));
+        if (valid < kQ4Tile) {  // the parameters of the other tokens may be anything
+            for (int i = valid * NG + lane; i < kQ4Tile * NG; i += 32) kp[i] = vp[i] = 0;
+            fence_proxy_async_smem();  // (before the next copy into this stage)
+            __syncwarp();
+        }
+        // rows and chunks of the four matrices of an ldmatrix: tokens 0-7 and 8-15 of one chunk, then of the next
+        const int row = (lane & 7) + ((lane >> 3) & 1) * 8;
+        const uint32_t at = row * (D / 2) + q4_chunk<D>(row, lane >> 4) * 16;
+        // ---- logits of tokens n, n + 8 and heads 2j, 2j + 1
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
+        {
+            const uint32_t p0 = NG == 4 || j < NG ? kp[n * NG + (NG == 4 ? j : j % NG)] : 0;
+            const uint32_t p1 = NG == 4 || j < NG ? kp[(n + 8) * NG + (NG == 4 ? j : j % NG)] : 0;
+            mma_bf16(y, p0, p1, p0, p1, ob[0], ob[1]);
+            mma_bf16(y, p0, p1, 0, 0, ob[2], 0);
+            uint32_t w0[NG], w1[NG];
+            lds<NG>(kp + n * NG, w0);
+            lds<NG>(kp + (n + 8) * NG, w1);
+            const uint32_t ka = smem_u32(kt) + at;
+            float d[4];
+#pragma unroll
+            for (int c = 0; c < kChunks; c += 2) {
+                uint32_t r[4];
+                ldsm_x4(ka ^ (c << 4), r[0], r[1], r[2], r[3]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int g = (c + i) / kPerGroup;
+                    if ((c + i) % kPerGroup == 0) d[0] = d[2] = start[g][0], d[1] = d[3] = start[g][1];
+                    mma_bf16(d, codes<0>(r[2 * i]), codes<0>(r[2 * i + 1]), codes<1>(r[2 * i]), codes<1>(r[2 * i + 1]),
+                             qb[c + i][0][0], qb[c + i][0][1]);
+                    mma_bf16(d, codes<2>(r[2 * i]), codes<2>(r[2 * i + 1]), codes<3>(r[2 * i]), codes<3>(r[2 * i + 1]),
+                             qb[c + i][1][0], qb[c + i][1][1]);
+                    if ((c + i + 1) % kPerGroup == 0) {
+                        const float s0 = __uint_as_float(w0[g] << 16), s1 = __uint_as_float(w1[g] << 16);
+                        y[0] = fmaf(s0, d[0], y[0]);
+                        y[1] = fmaf(s0, d[1], y[1]);
+                        y[2] = fmaf(s1, d[2], y[2]);
+                        y[3] = fmaf(s1, d[3], y[3]);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] *= a.qscale;
+        if (valid < kQ4Tile) {
+            if (n >= valid) y[0] = y[1] = -INFINITY;
+            if (n + 8 >= valid) y[2] = y[3] = -INFINITY;
+        }
+        if (logits) {
+            const int h = 2 * j;
+            if (h < a.G) {
+                logits[n * a.G + h] = y[0];
+                logits[(n + 8) * a.G + h] = y[2];
+            }
+            if (h + 1 < a.G) {
+                logits[n * a.G + h + 1] = y[1];
+                logits[(n + 8) * a.G + h + 1] = y[3];
+            }
+        }
+        // ---- softmax relative to a reference that is changed only when a logit passes it by far
+        const float top0 = fmaxf(y[0], y[2]), top1 = fmaxf(y[1], y[3]);
+        if (__any_sync(0xFFFFFFFFu, top0 > thr[0] || top1 > thr[1])) {
+            float top[2] = {top0, top1};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], o));
+                const float m = thr[i] == -INFINITY ? top[i] : fmaxf(base[i], top[i]);
+                const float now = m == -INFINITY ? 0.f : m;
+                const float alpha = thr[i] == -INFINITY ? 0.f : ex2_approx(base[i] - now);
+                base[i] = now;
+                thr[i] = m + kLazyMax;
+                l[i] *= alpha;
+                off[i] *= alpha;
+                off[i + 2] *= alpha;
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) acc[c][e][i] *= alpha, acc[c][e][i + 2] *= alpha;
+            }
+        }
+        float p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = ex2_approx(y[i] - base[i & 1]);
+        l[0] += p[0] + p[2];
+        l[1] += p[1] + p[3];
+        // right operand of the values' products: tokens 2j, 2j + 1 (and + 8) of head n
+        const uint32_t b0 = transpose8(f2_to_bf2(p[0], p[1])), b1 = transpose8(f2_to_bf2(p[2], p[3]));
+        {
+            // row g of `off`: sum of p lo of group g, less 128 times that of its rounded p step; row 8: sum of p
+            const bool in = n < NG;
+            const uint32_t *q0 = vp + 2 * j * NG + (in ? n : 0);
+            const uint32_t l0 = in ? __byte_perm(q0[0], q0[NG], 0x7632) : 0;
+            const uint32_t l1 = in ? __byte_perm(q0[8 * NG], q0[9 * NG], 0x7632) : 0;
+            const uint32_t one = n == 0 ? 0x3F803F80u : 0;
+            mma_bf16(off, l0, one, l1, one, b0, b1);
+        }
+        uint32_t w0[NG], w1[NG], w2[NG], w3[NG];
+        lds<NG>(vp + 2 * j * NG, w0);
+        lds<NG>(vp + (2 * j + 1) * NG, w1);
+        lds<NG>(vp + (2 * j + 8) * NG, w2);
+        lds<NG>(vp + (2 * j + 9) * NG, w3);
+        const uint32_t va = smem_u32(vt) + at;
+        uint32_t s0 = 0, s1 = 0;
+#pragma unroll
+        for (int c = 0; c < kChunks; c += 2) {
+            uint32_t r[4];
+            ldsm_x4_t(va ^ (c << 4), r[0], r[1], r[2], r[3]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int g = (c + i) / kPerGroup;
+                if ((c + i) % kPerGroup == 0) {
+                    s0 = mul_bf2(b0, __byte_perm(w0[g], w1[g], 0x5410));
+                    s1 = mul_bf2(b1, __byte_perm(w2[g], w3[g], 0x5410));
+                    const uint32_t minus = n == g ? 0xC300C300u : 0;  // -128
+                    mma_bf16(off, minus, 0, minus, 0, s0, s1);
+                }
+                mma_bf16(acc[c + i][0], codes<0>(r[2 * i]), codes<1>(r[2 * i]), codes<0>(r[2 * i + 1]), codes<1>(r[2 * i + 1]), s0, s1);
+                mma_bf16(acc[c + i][1], codes<2>(r[2 * i]), codes<3>(r[2 * i]), codes<2>(r[2 * i + 1]), codes<3>(r[2 * i + 1]), s0, s1);
+            }
+        }
+    }
+
+    // heads 2j, 2j + 1: dimensions 32c + 4n .. + 3 in acc[c], the sums in off[2..3] (rounded p) and l
+    __device__ __forceinline__ void end(int lane) {
+        const int j = lane & 3;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], o);
+            off[i + 2] = __shfl_sync(0xFFFFFFFFu, off[i + 2], j);
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                const float add = __shfl_sync(0xFFFFFFFFu, off[i], 4 * (c / kPerGroup) + j);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) acc[c][e][i] += add, acc[c][e][i + 2] += add;
+            }
+        }
+    }
+    __device__ __forceinline__ float reference(int i) const { return thr[i] == -INFINITY ? -INFINITY : base[i]; }
+    __device__ __forceinline__ void write_out(const Q4Args &a, int s, int h, int lane) const {
+        const int n = lane >> 2, j = lane & 3;
+        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + ((size_t)s * a.h_q + (size_t)h * a.G) * D;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int g = 2 * j + i;
+            if (g >= a.G) break;
+            const float r = off[i + 2] == 0.f ? 0.f : 1.f / off[i + 2];
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c)
+                *reinterpret_cast<uint2 *>(out + g * D + c * 32 + n * 4) =
+                    make_uint2(f2_to_bf2(acc[c][0][i] * r, acc[c][0][i + 2] * r), f2_to_bf2(acc[c][1][i] * r, acc[c][1][i + 2] * r));
+            if (a.want_score && n == 0) a.stats[(size_t)s * a.h_q + h * a.G + g] = score_norm(reference(i), l[i]);
+        }
+    }
+    __device__ __forceinline__ void write_record(const Q4Args &a, float *rec, int lane) const {
+        const int n = lane >> 2, j = lane & 3;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int g = 2 * j + i;
+            if (g >= a.G) break;
+            if (n == 0) reinterpret_cast<float4 *>(rec)[g] = make_float4(reference(i), off[i + 2], l[i], 0.f);
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c)
+                *reinterpret_cast<float4 *>(rec + 4 * a.G + g * D + c * 32 + n * 4) =
+                    make_float4(acc[c][0][i], acc[c][0][i + 2], acc[c][1][i], acc[c][1][i + 2]);
         }
     }
 };
 
 // ---------------------------------------------------------------- attention
-constexpr int kScalarWarps = 8, kScalarStages = 4;
+// Shared memory: rings (a warp's tiles; at its end the record of a pair that goes on
+// behind its range), records of pairs that began before a warp's range, the warps' own, prefix.
+template <class W>
+__host__ __device__ inline size_t attention_smem(int stages, int tile, int G, int B) {
+    return (size_t)W::kWarps * ((size_t)stages * 2 * tile + (size_t)G * (W::kD + 4) * 4 + W::kSharedBytes) + ((size_t)B + 1) * 4;
+}
 
-template <typename T, int D, int GP>
-__global__ void __launch_bounds__(kScalarWarps * 32) q4_scalar_kernel(const Q4Args a) {
-    using Warp = ScalarWarp<T, D, GP>;
+template <class W>
+__global__ void __launch_bounds__(W::kWarps * 32, W::kCtas) q4_attention_kernel(const Q4Args a) {
+    constexpr int D = W::kD, kWarps = W::kWarps;
+    using T = typename W::T;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ uint64_t full_s[kScalarWarps][kScalarStages];
-    __shared__ int bad_s[kScalarWarps][kScalarStages], sums_s[kScalarWarps];
+    __shared__ uint64_t full_s[kWarps][kMaxStages];
+    __shared__ int bad_s[kWarps][kMaxStages], sums_s[kWarps];
+    __shared__ int head_s[kWarps], tail_s[kWarps];  // pair of a warp's records, -1 = none; bit 30 of head: its last unit is in
     __shared__ int abort_s;
+    constexpr int kLast = 1 << 30;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    unsigned char *ring = smem + (size_t)warp * kScalarStages * 2 * a.tile;
-    float *mine = reinterpret_cast<float *>(smem + (size_t)kScalarWarps * kScalarStages * 2 * a.tile) + warp * Warp::kSharedFloats;
-    int *prefix = reinterpret_cast<int *>(reinterpret_cast<float *>(smem + (size_t)kScalarWarps * kScalarStages * 2 * a.tile) +
-                                          kScalarWarps * Warp::kSharedFloats);
-    if (lane < kScalarStages) mbar_init(&full_s[warp][lane], 1);
+    const int rec_n = rec_floats(a, D), stages = a.stages;
+    const size_t ring_bytes = (size_t)stages * 2 * a.tile;
+    unsigned char *ring = smem + warp * ring_bytes;
+    float *heads = reinterpret_cast<float *>(smem + kWarps * ring_bytes);
+    unsigned char *own = reinterpret_cast<unsigned char *>(heads + kWarps * rec_n) + warp * W::kSharedBytes;
+    int *prefix = reinterpret_cast<int *>(reinterpret_cast<unsigned char *>(heads + kWarps * rec_n) + kWarps * W::kSharedBytes);
+    if (lane < stages) mbar_init(&full_s[warp][lane], 1);
+    if (lane == 0) head_s[warp] = tail_s[warp] = -1;
     if (tid == 0) abort_s = 0;
     fence_barrier_init();
     unit_prefix(a, prefix, sums_s);  // (has the barrier behind the initialisation)
     if (blockIdx.x == 0)
         for (int s = tid; s <= a.B; s += blockDim.x) a.prefix[s] = prefix[s];
+    if (prefix[a.B] == 0) return;
     const Split split = make_split(a, prefix[a.B]);
-    if (warp >= split.per_cta || split.U == 0) return;
     const long long g = (long long)blockIdx.x * split.per_cta + warp;
     const long long x0 = split.start(g);
-    const int n = (int)(split.start(g + 1) - x0);
-    if (n == 0) return;
-    const uint64_t pol = l2_evict_first_policy();
-
-    Cursor put, get;
-    put.seek(prefix, a.B, a.h_kv, x0);
-    get = put;
-    int ids = 0, ids_of = -1, ids_at = 0;  // lane i: block of unit ids_at + i of sequence ids_of
-    const int tpb = a.b / kQ4Tile;
-    auto issue = [&](int i) {
-        if (put.s != ids_of || put.u < ids_at || put.u >= ids_at + 32) {
-            ids_of = put.s;
-            ids_at = put.u;
-            const int u = put.u + lane;
-            ids = u < put.n ? __ldg(a.table + (size_t)put.s * a.table_stride + u / tpb) : -1;
-        }
-        const int blk = __shfl_sync(0xFFFFFFFFu, ids, put.u - ids_at);
-        const int st = i % kScalarStages;
-        if (lane == 0) {
-            const bool ok = blk >= 0 && blk < a.n_total;
-            bad_s[warp][st] = !ok;
-            if (ok) {
-                const size_t off = (((size_t)blk * a.h_kv + put.h) * tpb + put.u % tpb) * a.tile;
-                mbar_arrive_expect_tx(&full_s[warp][st], 2 * a.tile);
-                bulk_g2s(ring + (size_t)st * 2 * a.tile, a.k + off, a.tile, &full_s[warp][st], pol);
-                bulk_g2s(ring + (size_t)st * 2 * a.tile + a.tile, a.v + off, a.tile, &full_s[warp][st], pol);
-            } else {
-                record_error(a.err, ZP_ERR_DEVICE, 0x159);
-                mbar_arrive(&full_s[warp][st]);
+    const int n = warp < split.per_cta ? (int)(split.start(g + 1) - x0) : 0;
+    if (n > 0) {
+        const uint64_t pol = l2_evict_first_policy();
+        Cursor put, get;
+        put.seek(prefix, a.B, a.h_kv, x0);
+        get = put;
+        int ids = 0, ids_of = -1, ids_at = 0;  // lane i: block of unit ids_at + i of sequence ids_of
+        const int tpb = a.b / kQ4Tile;
+        int put_st = 0;
+        auto issue = [&]() {
+            if (put.s != ids_of || put.u < ids_at || put.u >= ids_at + 32) {
+                ids_of = put.s;
+                ids_at = put.u;
+                const int u = put.u + lane;
+                ids = u < put.n ? __ldg(a.table + (size_t)put.s * a.table_stride + u / tpb) : -1;
             }
-        }
-        put.next(prefix, a.B, a.h_kv);
-    };
-    for (int i = 0; i < n && i < kScalarStages; ++i) issue(i);
-
-    Warp w;
-    w.q_s = mine;
-    w.p_s = mine + GP * D;
-    int L = 0;
-    bool scored = false;
-    for (int i = 0; i < n; ++i) {
-        if (i == 0 || get.u == 0) {
-            if (i == 0 || get.h == 0) {
-                L = q4_len(a, get.s);
-                scored = q4_score_row(a, get.s, L) >= 0;
+            const int blk = __shfl_sync(0xFFFFFFFFu, ids, put.u - ids_at);
+            if (lane == 0) {
+                const bool ok = blk >= 0 && blk < a.n_total;
+                bad_s[warp][put_st] = !ok;
+                uint64_t *bar = &full_s[warp][put_st];
+                if (ok) {
+                    const size_t from = (((size_t)blk * a.h_kv + put.h) * tpb + put.u % tpb) * a.tile;
+                    unsigned char *to = ring + (size_t)put_st * 2 * a.tile;
+                    mbar_arrive_expect_tx(bar, 2 * a.tile);
+                    bulk_g2s(to, a.k + from, a.tile, bar, pol);
+                    bulk_g2s(to + a.tile, a.v + from, a.tile, bar, pol);
+                } else {
+                    record_error(a.err, ZP_ERR_DEVICE, 0x159);
+                    mbar_arrive(bar);
+                }
             }
-            w.begin(a, get.s, get.h, lane);
-        }
-        const int st = i % kScalarStages;
-        if (!mbar_wait_bounded(&full_s[warp][st], (i / kScalarStages) & 1, a.err, &abort_s, 0x15b)) {
-            drain(full_s[warp], kScalarStages, i, n);
-            return;
-        }
-        const int valid = bad_s[warp][st] ? 0 : min(kQ4Tile, L - get.u * kQ4Tile);
-        const unsigned char *kt = ring + (size_t)st * 2 * a.tile;
-        w.tile(a, kt, kt + a.tile, valid, scored ? a.logits + (size_t)(x0 + i) * kQ4Tile * a.G : nullptr, lane);
-        __syncwarp();
-        if (i + kScalarStages < n) issue(i + kScalarStages);
-        const bool last = get.u == get.n - 1;
-        if (last || i == n - 1) {
-            w.end();
-            const bool from_start = i >= get.u;  // the pair's first unit is in this range
-            if (last && from_start) w.write_out(a, get.s, get.h, lane);
-            else w.write_record(a, a.rec + (size_t)(2 * g + (from_start ? 1 : 0)) * a.G * (D + 2), lane);
-        }
-        get.next(prefix, a.B, a.h_kv);
-    }
-}
+            put_st = put_st + 1 == stages ? 0 : put_st + 1;
+            put.next(prefix, a.B, a.h_kv);
+        };
+        for (int i = 0; i < n && i < stages; ++i) issue();
 
-// ---------------------------------------------------------------- joining the records
-// One CTA per pair that several ranges share: warp w takes every eighth record, then the
-// warps are joined.
-constexpr int kMergeWarps = 8;
-
-template <typename T, int D>
-__global__ void __launch_bounds__(kMergeWarps * 32) q4_merge_kernel(const Q4Args a) {
-    extern __shared__ float sm[];  // [warps][G][D], [warps][G] (max, sum)
-    pdl_wait();
-    const int s = blockIdx.x / a.h_kv, h = blockIdx.x % a.h_kv;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int n = a.prefix[s + 1] - a.prefix[s];
-    if (n == 0) return;
-    const Split split = make_split(a, a.prefix[a.B]);
-    const long long p0 = (long long)a.prefix[s] * a.h_kv + (long long)h * n;
-    const long long g0 = split.owner(p0), g1 = split.owner(p0 + n - 1);
-    if (g0 == g1) return;
-    const int stride = a.G * (D + 2);
-    constexpr int kDims = D / 32;
-    float *ml = sm + kMergeWarps * a.G * D;
-    for (int g = 0; g < a.G; ++g) {
-        float m = -INFINITY, l = 0.f, acc[kDims] = {};
-        for (long long r = g0 + warp; r <= g1; r += kMergeWarps) {
-            if (split.start(r) == split.start(r + 1)) continue;  // an empty range
-            const float *rec = a.rec + (size_t)(2 * r + (split.start(r) <= p0 ? 1 : 0)) * stride;
-            const float2 x = reinterpret_cast<const float2 *>(rec)[g];
-            const float top = fmaxf(m, x.x), base = top == -INFINITY ? 0.f : top;
-            const float was = ex2_approx(m - base), now = ex2_approx(x.x - base);
-            m = top;
-            l = l * was + x.y * now;
-#pragma unroll
-            for (int j = 0; j < kDims; ++j) acc[j] = acc[j] * was + rec[2 * a.G + g * D + lane * kDims + j] * now;
-        }
-#pragma unroll
-        for (int j = 0; j < kDims; ++j) sm[(warp * a.G + g) * D + lane * kDims + j] = acc[j];
-        if (lane == 0) {
-            ml[(warp * a.G + g) * 2] = m;
-            ml[(warp * a.G + g) * 2 + 1] = l;
+        W w;
+        w.init(own);
+        int L = 0, st = 0;
+        unsigned phase = 0;
+        bool scored = false;
+        for (int i = 0; i < n; ++i) {
+            if (i == 0 || get.u == 0) {
+                if (i == 0 || get.h == 0) {
+                    L = q4_len(a, get.s);
+                    scored = q4_score_row(a, get.s, L) >= 0;
+                }
+                w.begin(a, get.s, get.h, lane);
+            }
+            if (!mbar_wait_bounded(&full_s[warp][st], phase, a.err, &abort_s, 0x15b)) {
+                drain(full_s[warp], stages, i, n);
+                break;
+            }
+            unsigned char *kt = ring + (size_t)st * 2 * a.tile;
+            float *lg = scored ? a.logits + (size_t)(x0 + i) * kQ4Tile * a.G : nullptr;
+            if (!bad_s[warp][st]) w.tile(a, kt, kt + a.tile, min(kQ4Tile, L - get.u * kQ4Tile), lg, lane);
+            else if (lg)
+                for (int e = lane; e < kQ4Tile * a.G; e += 32) lg[e] = -INFINITY;
+            __syncwarp();
+            if (i + stages < n) issue();
+            if (++st == stages) st = 0, phase ^= 1;
+            const bool last = get.u == get.n - 1;
+            if (last || i == n - 1) {
+                w.end(lane);
+                const bool from_start = i >= get.u;  // the pair's first unit is in this range
+                if (last && from_start) {
+                    w.write_out(a, get.s, get.h, lane);
+                } else {
+                    // (a pair that goes on behind the range is its last: the ring is empty then)
+                    w.write_record(a, from_start ? reinterpret_cast<float *>(ring) : heads + warp * rec_n, lane);
+                    if (lane == 0) {
+                        const int pair = get.s * a.h_kv + get.h;
+                        if (from_start) tail_s[warp] = pair;
+                        else head_s[warp] = pair | (last ? kLast : 0);
+                    }
+                }
+            }
+            get.next(prefix, a.B, a.h_kv);
         }
     }
     __syncthreads();
-    T *out = static_cast<T *>(a.out) + ((size_t)s * a.h_q + (size_t)h * a.G) * D;
-    for (int i = threadIdx.x; i < a.G * D; i += blockDim.x) {
-        const int g = i / D;
-        float m = -INFINITY, l = 0.f, acc = 0.f;
-        for (int w = 0; w < kMergeWarps; ++w) m = fmaxf(m, ml[(w * a.G + g) * 2]);
-        const float base = m == -INFINITY ? 0.f : m;
-        for (int w = 0; w < kMergeWarps; ++w) {
-            const float now = ex2_approx(ml[(w * a.G + g) * 2] - base);
-            l += ml[(w * a.G + g) * 2 + 1] * now;
-            acc += sm[w * a.G * D + i] * now;
+    if (abort_s) return;
+    // ---- the records of this CTA, pair by pair: one begins in a warp's tail, or before the
+    // CTA in the first warp's head, and goes on in the heads of the next warps
+    for (int w0 = 0; w0 < split.per_cta; ++w0) {
+#pragma unroll 1
+        for (int side = 0; side < 2; ++side) {
+            const int id = side ? tail_s[w0] : head_s[w0];
+            if (id < 0 || (side == 0 && w0 > 0 && (head_s[w0 - 1] == (id & ~kLast) || tail_s[w0 - 1] == (id & ~kLast)))) continue;
+            const int pair = id & ~kLast;
+            bool done = side == 0 && (id & kLast);
+            int w1 = w0;  // the pair's last warp here
+            while (!done && w1 + 1 < split.per_cta && head_s[w1 + 1] >= 0 && (head_s[w1 + 1] & ~kLast) == pair) {
+                ++w1;
+                done = head_s[w1] & kLast;
+            }
+            auto rec = [&](int w) {
+                return w == w0 && side ? reinterpret_cast<const float *>(smem + w * ring_bytes) : heads + w * rec_n;
+            };
+            const int s = pair / a.h_kv, h = pair % a.h_kv;
+            float *to = a.rec + (size_t)(2 * blockIdx.x + side) * rec_n;
+            T *out = static_cast<T *>(a.out) + ((size_t)s * a.h_q + (size_t)h * a.G) * D;
+            for (int i = tid; i < a.G * D; i += kWarps * 32) {
+                const int q = i / D;
+                float m = -INFINITY;
+                for (int w = w0; w <= w1; ++w) m = fmaxf(m, rec(w)[4 * q]);
+                const float base = m == -INFINITY ? 0.f : m;
+                float x = 0.f, lo = 0.f, l = 0.f;
+                for (int w = w0; w <= w1; ++w) {
+                    const float4 r = *reinterpret_cast<const float4 *>(rec(w) + 4 * q);
+                    const float f = ex2_approx(r.x - base);
+                    lo = fmaf(r.y, f, lo);
+                    l = fmaf(r.z, f, l);
+                    x = fmaf(rec(w)[4 * a.G + i], f, x);
+                }
+                if (side && done) {
+                    out[i] = from_f<T>(lo == 0.f ? 0.f : x / lo);
+                    if (a.want_score && i % D == 0) a.stats[(size_t)s * a.h_q + h * a.G + q] = score_norm(m, l);
+                } else {
+                    to[4 * a.G + i] = x;
+                    if (i % D == 0) reinterpret_cast<float4 *>(to)[q] = make_float4(m, lo, l, 0.f);
+                }
+            }
         }
-        out[i] = from_f<T>(l == 0.f ? 0.f : acc / l);
-        if (a.want_score && i % D == 0) a.stats[(size_t)s * a.h_q + h * a.G + g] = make_float2(m, l);
     }
 }
 
-// ---------------------------------------------------------------- window score
-// The units are split as for the attention; a half-warp takes one at a time, a lane a token.
-constexpr int kScoreWarps = 8;
+// ---------------------------------------------------------------- what is left
+// CTA c joins the records of the pair that its counterpart of the attention kernel began and
+// did not finish, and forms the score of that one's units.
+constexpr int kFinishThreads = 512, kScoreUnroll = 4;
 
-__global__ void __launch_bounds__(kScoreWarps * 32) q4_score_kernel(const Q4Args a) {
+// records of a pair cut between CTAs: CTA c0 has its beginning (slot 1), the others slot 0
+__device__ __forceinline__ const float *cta_record(const Q4Args &a, const Split &p, int c0, int c, int rec_n) {
+    return c > c0 && p.cta_start(c) == p.cta_start(c + 1) ? nullptr : a.rec + (size_t)(2 * c + (c == c0 ? 1 : 0)) * rec_n;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kFinishThreads) q4_finish_kernel(const Q4Args a) {
+    extern __shared__ int prefix[];
     pdl_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane & 15, half = lane >> 4;
-    const long long U = (long long)a.prefix[a.B] * a.h_kv, W = (long long)gridDim.x * kScoreWarps;
-    const long long g = (long long)blockIdx.x * kScoreWarps + warp;
-    const long long x0 = g * U / W, x1 = (g + 1) * U / W;
-    if (x0 >= x1) return;
-    Cursor c;
-    c.seek(a.prefix, a.B, a.h_kv, x0);
-    for (long long x = x0; x < x1;) {
-        // the rest of this pair
-        const int units = (int)min((long long)(c.n - c.u), x1 - x);
-        const int L = q4_len(a, c.s), row = q4_score_row(a, c.s, L);
-        if (row >= 0) {
-            const int P = L - 1;
-            const bool first = P % a.b == a.b - a.window;
-            const float share = 1.f / (float)a.window;
-            float *S = a.score + ((size_t)row * a.h_kv + c.h) * a.score_stride;
-            const float2 *st = a.stats + (size_t)c.s * a.h_q + c.h * a.G;
-            for (int i = half; i < units; i += 2) {
-                const int tok = (c.u + i) * kQ4Tile + t;
-                if (tok > P) continue;
-                const float *lg = a.logits + ((size_t)(x + i) * kQ4Tile + t) * a.G;
-                float top = 0.f;
-                for (int q = 0; q < a.G; ++q) {
-                    const float2 ml = st[q];
-                    const float p = ml.y > 0.f ? ex2_approx(lg[q] - ml.x) / ml.y : 0.f;
-                    top = fmaxf(top, p);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rec_n = rec_floats(a, D);
+    for (int s = tid; s <= a.B; s += kFinishThreads) prefix[s] = a.prefix[s];
+    __syncthreads();
+    if (prefix[a.B] == 0) return;
+    const Split split = make_split(a, prefix[a.B]);
+    const int c0 = blockIdx.x;
+    const long long b0 = split.cta_start(c0), b1 = split.cta_start(c0 + 1);
+    if (b0 == b1) return;
+    {
+        Cursor cut;
+        cut.seek(prefix, a.B, a.h_kv, b1 - 1);
+        const long long first = b1 - 1 - cut.u, last = first + cut.n - 1;
+        if (first >= b0 && last >= b1) {
+            const int c1 = split.cta_of(last);
+            T *out = static_cast<T *>(a.out) + ((size_t)cut.s * a.h_q + (size_t)cut.h * a.G) * D;
+            for (int i = tid; i < a.G * D; i += kFinishThreads) {
+                const int q = i / D;
+                float m = -INFINITY, x = 0.f, lo = 0.f;
+                for (int c = c0; c <= c1; ++c) {
+                    const float *r = cta_record(a, split, c0, c, rec_n);
+                    if (!r) continue;
+                    const float4 hd = *reinterpret_cast<const float4 *>(r + 4 * q);
+                    const float top = fmaxf(m, hd.x), base = top == -INFINITY ? 0.f : top;
+                    const float was = ex2_approx(m - base), now = ex2_approx(hd.x - base);
+                    m = top;
+                    lo = lo * was + hd.y * now;
+                    x = x * was + r[4 * a.G + i] * now;
                 }
-                top *= share;
-                S[tok] = first || tok == P ? top : S[tok] + top;
+                out[i] = from_f<T>(lo == 0.f ? 0.f : x / lo);
+            }
+        }
+    }
+    if (!a.want_score) return;
+    // ---- the score: warps take equal parts of the CTA's units, a lane one token at a time
+    constexpr int kWarps = kFinishThreads / 32;
+    const long long x0 = b0 + (b1 - b0) * warp / kWarps, x1 = b0 + (b1 - b0) * (warp + 1) / kWarps;
+    if (x0 == x1) return;
+    Cursor cur;
+    cur.seek(prefix, a.B, a.h_kv, x0);
+    for (long long x = x0; x < x1;) {
+        const int units = (int)min((long long)(cur.n - cur.u), x1 - x);  // the rest of this pair
+        const int L = q4_len(a, cur.s), row = q4_score_row(a, cur.s, L);
+        if (row >= 0) {
+            // normalisers of the heads: lane q has head q's
+            const long long first = x - cur.u, last = first + cur.n - 1;
+            float norm = INFINITY;
+            if (first >= b0 && last < b1) {
+                if (lane < a.G) norm = __ldcg(a.stats + (size_t)cur.s * a.h_q + cur.h * a.G + lane);
+            } else {
+                const int k0 = split.cta_of(first), k1 = split.cta_of(last);
+                if (lane < a.G) {
+                    float m = -INFINITY, l = 0.f;
+                    for (int c = k0; c <= k1; ++c) {
+                        const float *r = cta_record(a, split, k0, c, rec_n);
+                        if (!r) continue;
+                        const float4 hd = *reinterpret_cast<const float4 *>(r + 4 * lane);
+                        const float top = fmaxf(m, hd.x), base = top == -INFINITY ? 0.f : top;
+                        l = l * ex2_approx(m - base) + hd.z * ex2_approx(hd.x - base);
+                        m = top;
+                    }
+                    norm = score_norm(m, l);
+                }
+            }
+            float c[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) c[q] = __shfl_sync(0xFFFFFFFFu, norm, q);
+            const int P = L - 1;
+            const bool fresh = P % a.b == a.b - a.window;
+            const float share = 1.f / (float)a.window;
+            float *S = a.score + ((size_t)row * a.h_kv + cur.h) * a.score_stride;
+            const int t0 = cur.u * kQ4Tile, t1 = min(t0 + units * kQ4Tile, L);
+            const float *lg = a.logits + (size_t)first * kQ4Tile * a.G;
+            for (int t = t0 + lane; t < t1; t += 32 * kScoreUnroll) {
+                float top[kScoreUnroll], old[kScoreUnroll];
+#pragma unroll
+                for (int k = 0; k < kScoreUnroll; ++k) {
+                    const int tok = t + 32 * k;
+                    top[k] = -INFINITY;
+                    old[k] = 0.f;
+                    if (tok < t1) {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            if (q < a.G) top[k] = fmaxf(top[k], lg[(size_t)tok * a.G + q] - c[q]);
+                        if (!fresh && tok != P) old[k] = S[tok];
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < kScoreUnroll; ++k) {
+                    const int tok = t + 32 * k;
+                    if (tok < t1) S[tok] = fmaf(ex2_approx(top[k]), share, old[k]);
+                }
             }
         }
         x += units;
-        c.u += units - 1;
-        c.next(a.prefix, a.B, a.h_kv);
+        cur.u += units - 1;
+        cur.next(prefix, a.B, a.h_kv);
     }
 }
 
 // ---------------------------------------------------------------- host
 struct Q4Plan {
-    int grid, warps;
+    int grid, warps, stages;
     size_t smem;
     size_t off_prefix, off_stats, off_rec, off_logits, total;
 };
 
 int padded_group(int G) { return G <= 1 ? 1 : G <= 2 ? 2 : G <= 4 ? 4 : 8; }
+
+// f(W) for the warp type of a cache
+template <typename F>
+auto with_warp(const zp_cache_desc *D, int group, F f) {
+    const bool wide = D->head_dim == 128;
+    if (D->dtype == ZP_BF16) {
+        if (wide && group == 32) return f(TcWarp<128, 5>());
+        if (wide && group == 64) return f(TcWarp<128, 6>());
+        if (wide) return f(TcWarp<128, 7>());
+        if (group == 32) return f(TcWarp<64, 5>());
+        return f(TcWarp<64, 6>());
+    }
+    switch (padded_group(D->h_q / D->h_kv)) {
+        case 1: return wide ? f(ScalarWarp<128, 1>()) : f(ScalarWarp<64, 1>());
+        case 2: return wide ? f(ScalarWarp<128, 2>()) : f(ScalarWarp<64, 2>());
+        case 4: return wide ? f(ScalarWarp<128, 4>()) : f(ScalarWarp<64, 4>());
+        default: return wide ? f(ScalarWarp<128, 8>()) : f(ScalarWarp<64, 8>());
+    }
+}
 
 zp_status q4_plan(const zp_cache_desc *D, int group, int B, int table_stride, int scored, const DeviceInfo &dev, Q4Plan *p) {
     zp_status rc = check_q4(D, group, "q4_decode");
@@ -495,54 +900,41 @@ zp_status q4_plan(const zp_cache_desc *D, int group, int B, int table_stride, in
     if ((long long)B * table_stride * D->block_size > INT32_MAX)
         return fail(ZP_ERR_SHAPE, "q4_decode: B=%d rows of %d blocks of %d tokens exceed 32 bits", B, table_stride,
                     D->block_size);
-    const int d = D->head_dim, GP = padded_group(G), tile = q4_tile_bytes(d, group);
-    p->warps = kScalarWarps;
-    p->smem = (size_t)kScalarWarps * kScalarStages * 2 * tile + (size_t)kScalarWarps * (GP * d + kQ4Tile * GP) * 4 +
-              ((size_t)B + 1) * 4;
-    const int per_sm = (int)(dev.smem_optin / p->smem);
-    p->grid = dev.sm_count * (per_sm < 1 ? 1 : per_sm > 2 ? 2 : per_sm);
+    const int d = D->head_dim, tile = q4_tile_bytes(d, group);
+    with_warp(D, group, [&](auto w) {
+        using W = decltype(w);
+        const size_t room = ((size_t)dev.smem_optin + 1024) / W::kCtas - 2048;  // (1 KB of a CTA is the system's, 1 KB static)
+        p->warps = W::kWarps;
+        p->grid = dev.sm_count * W::kCtas;
+        p->stages = kMaxStages;
+        while (p->stages > 2 && attention_smem<W>(p->stages, tile, G, B) > room) --p->stages;
+        p->smem = attention_smem<W>(p->stages, tile, G, B);
+        return 0;
+    });
     size_t off = 0;
     p->off_prefix = off;
     off = align_up(off + ((size_t)B + 1) * 4, 256);
     p->off_stats = off;
-    off = align_up(off + (size_t)B * D->h_q * 8, 256);
+    off = align_up(off + (size_t)B * D->h_q * 4, 256);
     p->off_rec = off;
-    off = align_up(off + (size_t)2 * p->grid * p->warps * G * (d + 2) * 4, 256);
+    off = align_up(off + (size_t)2 * p->grid * G * (d + 4) * 4, 256);
     p->off_logits = off;
     if (scored) off = align_up(off + (size_t)B * table_stride * D->block_size * D->h_q * 4, 256);
     p->total = off;
     return ZP_OK;
 }
 
-template <typename T, int D, int GP>
-zp_status launch_attention(const Q4Args &a, const Q4Plan &p, cudaStream_t st) {
-    const auto kernel = q4_scalar_kernel<T, D, GP>;
-    const zp_status rc = set_max_dynamic_smem(reinterpret_cast<const void *>(kernel), p.smem, "q4_decode: shared-memory attribute");
+template <class W>
+zp_status launch_q4(const Q4Args &a, const Q4Plan &p, cudaStream_t st) {
+    const auto kernel = q4_attention_kernel<W>;
+    zp_status rc = set_max_dynamic_smem(reinterpret_cast<const void *>(kernel), p.smem, "q4_decode: shared-memory attribute");
     if (rc != ZP_OK) return rc;
     kernel<<<p.grid, p.warps * 32, p.smem, st>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? ZP_OK : cuda_fail(e, "q4_decode: attention launch");
-}
-
-template <typename T, int D>
-zp_status launch_q4(const Q4Args &a, const Q4Plan &p, cudaStream_t st) {
-    zp_status rc;
-    switch (padded_group(a.G)) {
-        case 1: rc = launch_attention<T, D, 1>(a, p, st); break;
-        case 2: rc = launch_attention<T, D, 2>(a, p, st); break;
-        case 4: rc = launch_attention<T, D, 4>(a, p, st); break;
-        default: rc = launch_attention<T, D, 8>(a, p, st); break;
-    }
-    if (rc != ZP_OK) return rc;
-    const size_t smem = (size_t)kMergeWarps * a.G * (D + 2) * 4;
-    const auto merge = q4_merge_kernel<T, D>;
-    rc = set_max_dynamic_smem(reinterpret_cast<const void *>(merge), smem, "q4_decode: shared-memory attribute");
-    if (rc != ZP_OK) return rc;
-    cudaError_t e = launch_dependent(merge, dim3(a.B * a.h_kv), dim3(kMergeWarps * 32), smem, st, a);
-    if (e != cudaSuccess) return cuda_fail(e, "q4_decode: merge launch");
-    if (!a.want_score) return ok();
-    e = launch_dependent(q4_score_kernel, dim3(4 * p.grid), dim3(kScoreWarps * 32), 0, st, a);
-    if (e != cudaSuccess) return cuda_fail(e, "q4_decode: score launch");
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "q4_decode: attention launch");
+    const auto finish = q4_finish_kernel<typename W::T, W::kD>;
+    e = launch_dependent(finish, dim3(p.grid), dim3(kFinishThreads), ((size_t)a.B + 1) * 4, st, a);
+    if (e != cudaSuccess) return cuda_fail(e, "q4_decode: finish launch");
     return ok();
 }
 
@@ -616,14 +1008,13 @@ extern "C" zp_status zp_q4_decode_attn(const zp_cache_desc *D, int32_t group, co
     a.score_rows = score_accum ? score_rows : nullptr;
     a.n_score_rows = n_score_rows;
     a.prefix = reinterpret_cast<int *>(ws + p.off_prefix);
-    a.stats = reinterpret_cast<float2 *>(ws + p.off_stats);
+    a.stats = reinterpret_cast<float *>(ws + p.off_stats);
     a.rec = reinterpret_cast<float *>(ws + p.off_rec);
     a.logits = reinterpret_cast<float *>(ws + p.off_logits);
     a.grid = p.grid;
     a.warps = p.warps;
+    a.stages = p.stages;
     a.err = dev.error_word;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool wide = D->head_dim == 128;
-    if (D->dtype == ZP_BF16) return wide ? launch_q4<__nv_bfloat16, 128>(a, p, st) : launch_q4<__nv_bfloat16, 64>(a, p, st);
-    return wide ? launch_q4<float, 128>(a, p, st) : launch_q4<float, 64>(a, p, st);
+    return with_warp(D, group, [&](auto w) { return launch_q4<decltype(w)>(a, p, st); });
 }
