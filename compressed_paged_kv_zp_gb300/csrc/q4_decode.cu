@@ -4,7 +4,7 @@
 //     out[s][h] = sum_{t<L_s} softmax_t(q[s][h] . k_t / sqrt(d)) v_t,
 // k_t and v_t the values that the cache's codes stand for (q4_format.cuh).
 //
-// Work unit = one tile of 16 tokens of one kv head.  The units of all (sequence, kv head)
+// Work unit = two tiles (32 tokens) of one kv head.  The units of all (sequence, kv head)
 // pairs are laid one after another and every warp takes an equal contiguous range, so
 // ragged lengths cannot unbalance the grid.  A warp copies the tiles of its range to a ring of
 // its own in shared memory (bulk copies, one mbarrier per stage) and runs an online softmax in
@@ -22,8 +22,8 @@ namespace zp {
 namespace {
 
 constexpr int kQ4MaxB = 4096;
-constexpr int kMinUnits = 4;   // units per warp below which fewer warps take part
-constexpr int kMaxStages = 6;  // tiles (of keys and of values) a warp has in flight, at most
+constexpr int kUnit = 2 * kQ4Tile;  // tokens of a unit
+constexpr int kMaxStages = 4;       // units a warp has in flight, at most
 
 struct Q4Args {
     const void *q;
@@ -43,15 +43,15 @@ struct Q4Args {
     int *prefix;    // [B+1] units before each sequence (of one kv head)
     float *stats;   // [B][h_q] reference + log2(sum) of the pairs that one CTA saw whole
     float *rec;     // [2 * CTAs][G * (d + 4)]: per head (reference, sum for the output, sum, 0), then accumulators
-    float *logits;  // [units][16][G]
-    int grid, warps, stages;  // CTAs of the attention kernel, warps of one, tiles in a warp's ring
+    float *logits;  // [units][32][G]
+    int grid, warps, stages;  // CTAs of the attention kernel, warps of one, units in a warp's ring
     unsigned *err;
 };
 
 // ---------------------------------------------------------------- the split
 struct Split {
-    long long U, W;  // units, ranges
-    int per_cta;     // ranges of a CTA: its first warps take one each
+    long long U, W;     // units, ranges (no more than units: none is empty)
+    int per_cta, ctas;  // ranges of a CTA (its first warps take one each), CTAs that have some
     __device__ __forceinline__ long long start(long long g) const { return g * U / W; }
     __device__ __forceinline__ long long cta_start(int c) const { return start((long long)c * per_cta); }
     // the CTA whose ranges hold unit x: the largest range g with start(g) <= x is its
@@ -61,9 +61,11 @@ struct Split {
 __device__ __forceinline__ Split make_split(const Q4Args &a, int units) {
     Split p;
     p.U = (long long)units * a.h_kv;
-    const long long want = (p.U + (long long)kMinUnits * a.grid - 1) / ((long long)kMinUnits * a.grid);
+    const long long want = (p.U + a.grid - 1) / a.grid;
     p.per_cta = (int)(want < 1 ? 1 : want > a.warps ? a.warps : want);
-    p.W = (long long)p.per_cta * a.grid;
+    const long long most = p.U / p.per_cta;
+    p.ctas = (int)(most < a.grid ? most : a.grid);
+    p.W = (long long)p.per_cta * p.ctas;
     return p;
 }
 
@@ -84,7 +86,7 @@ __device__ void unit_prefix(const Q4Args &a, int *prefix, int *warp_sum) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int mine = 0;
     for (int s = s0; s < s1; ++s) {
-        const int n = (q4_len(a, s) + kQ4Tile - 1) / kQ4Tile;
+        const int n = (int)(((long long)q4_len(a, s) + kUnit - 1) / kUnit);
         prefix[s] = n;
         mine += n;
     }
@@ -174,7 +176,7 @@ __device__ __forceinline__ float score_norm(float m, float l) { return l == 0.f 
 template <int D, int GP>
 struct ScalarWarp {
     using T = float;
-    static constexpr int kD = D, kWarps = 8, kCtas = 2;
+    static constexpr int kD = D, kWarps = 12, kCtas = 1;
     static constexpr int kDims = D / 32;
     static constexpr int kSharedBytes = (GP * D + kQ4Tile * GP) * 4;
     float m[GP], l[GP], acc[GP][kDims];
@@ -198,9 +200,13 @@ struct ScalarWarp {
         }
     }
 
-    // one tile; tokens >= valid weigh nothing
-    __device__ __forceinline__ void tile(const Q4Args &a, unsigned char *kt, unsigned char *vt, int valid, float *logits,
-                                         int lane) {
+    // Key tiles, then value tiles; of tile i the tokens >= v0 (i = 0), v1 weigh nothing.
+    __device__ __forceinline__ void unit(const Q4Args &a, unsigned char *tiles, int v0, int v1, float *logits, int lane) {
+        tile(a, tiles, tiles + 2 * a.tile, v0, logits, lane);
+        if (v1 || logits) tile(a, tiles + a.tile, tiles + 3 * a.tile, v1, logits ? logits + kQ4Tile * a.G : nullptr, lane);
+    }
+    __device__ __forceinline__ void tile(const Q4Args &a, const unsigned char *kt, const unsigned char *vt, int valid,
+                                         float *logits, int lane) {
         const int t = lane & 15, half = lane >> 4;
         const int words = D >> a.lg_group;
         float x[GP];
@@ -303,11 +309,10 @@ struct ScalarWarp {
 // query rows at most: the 128 rows of a tcgen05 tile would stand empty, and its operands
 // would have to be written to shared memory at four times the size of the codes.)  A code
 // becomes a bf16 number in a register by one and-or: 0x4300 | c is 128 + c, exactly.
-//   logits:  sum_i q_i (lo + c_i step) = lo sum_i q_i + step sum_i q_i c_i  per group.  The
-//     accumulator starts at -128 sum q, so that the product of 128 + c leaves sum q c;
-//     the lo part is a product of its own, of the parameter words (step, lo) as they lie
-//     in the tile with (0, sum q), the sum in three bf16 parts of 8 bits.  Nothing is rounded to
-//     16 bits: the logits are those of 32-bit arithmetic.
+//   logits:  sum_i q_i (lo + c_i step) = (lo - 128 step) sum_i q_i + step sum_i q_i (128 + c_i)
+//     per group.  The first term is a product of its own, of the parameter words (step, lo) as
+//     they lie in the tile with (-128 sum q, sum q), the sum in three bf16 parts of 8 bits.
+//     Nothing is rounded to 16 bits: the logits are those of 32-bit arithmetic.
 //   output:  sum_t p_t (lo_t + c_t step_t): p rounded to bf16 and transposed (movmatrix), p *
 //     step rounded to bf16 again per group, both with half a step of 2^-8 relative; the sum
 //     that divides is that of the rounded p, and the 128 is taken off with the rounded
@@ -322,6 +327,13 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// d = a b
+__device__ __forceinline__ void mma_bf16_0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                           uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t r;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -335,7 +347,9 @@ __device__ __forceinline__ uint32_t mul_bf2(uint32_t a, uint32_t b) {
 // codes e and e + 4 of a word (or code e of two tokens) as 128 + c
 template <int E>
 __device__ __forceinline__ uint32_t codes(uint32_t w) {
-    return ((w >> (4 * E)) & 0x000F000Fu) | 0x43004300u;
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w >> (4 * E)), "r"(0x000F000Fu), "r"(0x43004300u));  // (a & b) | c
+    return r;
 }
 // N words of shared memory, N of 1, 2, 4
 template <int N>
@@ -356,12 +370,11 @@ constexpr float kLazyMax = 8.f;  // the reference follows the maximum when it is
 template <int D, int LG>
 struct TcWarp {
     using T = __nv_bfloat16;
-    static constexpr int kD = D, kWarps = 16, kCtas = 1;
-    static constexpr int kSharedBytes = 0;
+    static constexpr int kD = D, kWarps = 12, kCtas = 1;  // (16 warps would leave a thread 128 registers)
+    static constexpr int kSharedBytes = 0, kTile = q4_tile_bytes(D, 1 << LG);
     static constexpr int NG = D >> LG, kChunks = D / 32, kPerGroup = (1 << LG) / 32;  // chunks of a row, of a group
     uint32_t qb[kChunks][2][2];  // queries as the right operand, by chunk and half of its words
-    uint32_t ob[3];              // sums of the queries of (head lane / 4, group lane % 4), in three parts
-    float start[NG][2];          // -128 * those of heads 2 (lane % 4), + 1
+    uint32_t ob[3];  // (-128, 1) * sums of the queries of (head lane / 4, group lane % 4), in three parts
     float acc[kChunks][2][4], off[4];
     float thr[2], base[2], l[2];  // of those heads: m + kLazyMax (-inf: none yet), m, sum over this lane's tokens
 
@@ -390,14 +403,12 @@ struct TcWarp {
         for (int g = 0; g < NG; ++g) {
             sum[g] += __shfl_xor_sync(0xFFFFFFFFu, sum[g], 1);
             sum[g] += __shfl_xor_sync(0xFFFFFFFFu, sum[g], 2);
-            start[g][0] = -128.f * __shfl_sync(0xFFFFFFFFu, sum[g], 8 * j);
-            start[g][1] = -128.f * __shfl_sync(0xFFFFFFFFu, sum[g], 8 * j + 4);
             if (j == g) part = sum[g];
         }
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
             const float x = __bfloat162float(__float2bfloat16_rn(part));
-            ob[i] = __float_as_uint(x);  // (the high half: the place of lo in a parameter word)
+            ob[i] = f2_to_bf2(-128.f * x, x);
             part -= x;
         }
 #pragma unroll
@@ -412,29 +423,37 @@ struct TcWarp {
         for (int i = 0; i < 2; ++i) thr[i] = -INFINITY, base[i] = 0.f, l[i] = 0.f;
     }
 
-    __device__ __forceinline__ void tile(const Q4Args &a, unsigned char *kt, unsigned char *vt, int valid, float *logits,
-                                         int lane) {
+    // Two key tiles, then two value tiles; of tile i the tokens >= v0 (i = 0), v1 weigh nothing.
+    __device__ __forceinline__ void unit(const Q4Args &a, unsigned char *tiles, int v0, int v1, float *logits, int lane) {
         const int n = lane >> 2, j = lane & 3;
-        uint32_t *kp = reinterpret_cast<uint32_t *>(kt + q4_code_bytes(D)), *vp = reinterpret_cast<uint32_t *>(vt + q4_code_bytes(D));
-        if (valid < kQ4Tile) {  // the parameters of the other tokens may be anything
-            for (int i = valid * NG + lane; i < kQ4Tile * NG; i += 32) kp[i] = vp[i] = 0;
+        unsigned char *kt = tiles, *vt = tiles + 2 * kTile;
+        const bool part = v0 + v1 < kUnit;
+        if (part) {  // the parameters of the other tokens may be anything
+            for (int i = lane; i < kUnit * NG; i += 32) {
+                const int t = i / NG;
+                if ((t & 15) < (t < kQ4Tile ? v0 : v1)) continue;
+                const int at = t / kQ4Tile * kTile + q4_code_bytes(D) + (i % (kQ4Tile * NG)) * 4;
+                *reinterpret_cast<uint32_t *>(kt + at) = *reinterpret_cast<uint32_t *>(vt + at) = 0;
+            }
             fence_proxy_async_smem();  // (before the next copy into this stage)
             __syncwarp();
         }
         // rows and chunks of the four matrices of an ldmatrix: tokens 0-7 and 8-15 of one chunk, then of the next
         const int row = (lane & 7) + ((lane >> 3) & 1) * 8;
         const uint32_t at = row * (D / 2) + q4_chunk<D>(row, lane >> 4) * 16;
-        // ---- logits of tokens n, n + 8 and heads 2j, 2j + 1
-        float y[4] = {0.f, 0.f, 0.f, 0.f};
-        {
+        // ---- logits of tokens n, n + 8 (of each tile) and heads 2j, 2j + 1
+        float y[2][4];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const uint32_t *kp = reinterpret_cast<const uint32_t *>(kt + b * kTile + q4_code_bytes(D));
             const uint32_t p0 = NG == 4 || j < NG ? kp[n * NG + (NG == 4 ? j : j % NG)] : 0;
             const uint32_t p1 = NG == 4 || j < NG ? kp[(n + 8) * NG + (NG == 4 ? j : j % NG)] : 0;
-            mma_bf16(y, p0, p1, p0, p1, ob[0], ob[1]);
-            mma_bf16(y, p0, p1, 0, 0, ob[2], 0);
+            mma_bf16_0(y[b], p0, p1, p0, p1, ob[0], ob[1]);
+            mma_bf16(y[b], p0, p1, 0, 0, ob[2], 0);
             uint32_t w0[NG], w1[NG];
             lds<NG>(kp + n * NG, w0);
             lds<NG>(kp + (n + 8) * NG, w1);
-            const uint32_t ka = smem_u32(kt) + at;
+            const uint32_t ka = smem_u32(kt + b * kTile) + at;
             float d[4];
 #pragma unroll
             for (int c = 0; c < kChunks; c += 2) {
@@ -443,40 +462,46 @@ struct TcWarp {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int g = (c + i) / kPerGroup;
-                    if ((c + i) % kPerGroup == 0) d[0] = d[2] = start[g][0], d[1] = d[3] = start[g][1];
-                    mma_bf16(d, codes<0>(r[2 * i]), codes<0>(r[2 * i + 1]), codes<1>(r[2 * i]), codes<1>(r[2 * i + 1]),
-                             qb[c + i][0][0], qb[c + i][0][1]);
+                    if ((c + i) % kPerGroup == 0)
+                        mma_bf16_0(d, codes<0>(r[2 * i]), codes<0>(r[2 * i + 1]), codes<1>(r[2 * i]), codes<1>(r[2 * i + 1]),
+                                   qb[c + i][0][0], qb[c + i][0][1]);
+                    else
+                        mma_bf16(d, codes<0>(r[2 * i]), codes<0>(r[2 * i + 1]), codes<1>(r[2 * i]), codes<1>(r[2 * i + 1]),
+                                 qb[c + i][0][0], qb[c + i][0][1]);
                     mma_bf16(d, codes<2>(r[2 * i]), codes<2>(r[2 * i + 1]), codes<3>(r[2 * i]), codes<3>(r[2 * i + 1]),
                              qb[c + i][1][0], qb[c + i][1][1]);
                     if ((c + i + 1) % kPerGroup == 0) {
                         const float s0 = __uint_as_float(w0[g] << 16), s1 = __uint_as_float(w1[g] << 16);
-                        y[0] = fmaf(s0, d[0], y[0]);
-                        y[1] = fmaf(s0, d[1], y[1]);
-                        y[2] = fmaf(s1, d[2], y[2]);
-                        y[3] = fmaf(s1, d[3], y[3]);
+                        y[b][0] = fmaf(s0, d[0], y[b][0]);
+                        y[b][1] = fmaf(s0, d[1], y[b][1]);
+                        y[b][2] = fmaf(s1, d[2], y[b][2]);
+                        y[b][3] = fmaf(s1, d[3], y[b][3]);
                     }
                 }
             }
-        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] *= a.qscale;
-        if (valid < kQ4Tile) {
-            if (n >= valid) y[0] = y[1] = -INFINITY;
-            if (n + 8 >= valid) y[2] = y[3] = -INFINITY;
+            for (int i = 0; i < 4; ++i) y[b][i] *= a.qscale;
+        }
+        if (part) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int valid = b ? v1 : v0;
+                if (n >= valid) y[b][0] = y[b][1] = -INFINITY;
+                if (n + 8 >= valid) y[b][2] = y[b][3] = -INFINITY;
+            }
         }
         if (logits) {
             const int h = 2 * j;
-            if (h < a.G) {
-                logits[n * a.G + h] = y[0];
-                logits[(n + 8) * a.G + h] = y[2];
-            }
-            if (h + 1 < a.G) {
-                logits[n * a.G + h + 1] = y[1];
-                logits[(n + 8) * a.G + h + 1] = y[3];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                float *to = logits + (b * kQ4Tile + n) * a.G + h;
+                if (h < a.G) to[0] = y[b][0], to[8 * a.G] = y[b][2];
+                if (h + 1 < a.G) to[1] = y[b][1], to[8 * a.G + 1] = y[b][3];
             }
         }
         // ---- softmax relative to a reference that is changed only when a logit passes it by far
-        const float top0 = fmaxf(y[0], y[2]), top1 = fmaxf(y[1], y[3]);
+        const float top0 = fmaxf(fmaxf(y[0][0], y[0][2]), fmaxf(y[1][0], y[1][2]));
+        const float top1 = fmaxf(fmaxf(y[0][1], y[0][3]), fmaxf(y[1][1], y[1][3]));
         if (__any_sync(0xFFFFFFFFu, top0 > thr[0] || top1 > thr[1])) {
             float top[2] = {top0, top1};
 #pragma unroll
@@ -497,44 +522,50 @@ struct TcWarp {
                     for (int e = 0; e < 2; ++e) acc[c][e][i] *= alpha, acc[c][e][i + 2] *= alpha;
             }
         }
-        float p[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = ex2_approx(y[i] - base[i & 1]);
-        l[0] += p[0] + p[2];
-        l[1] += p[1] + p[3];
-        // right operand of the values' products: tokens 2j, 2j + 1 (and + 8) of head n
-        const uint32_t b0 = transpose8(f2_to_bf2(p[0], p[1])), b1 = transpose8(f2_to_bf2(p[2], p[3]));
-        {
-            // row g of `off`: sum of p lo of group g, less 128 times that of its rounded p step; row 8: sum of p
-            const bool in = n < NG;
-            const uint32_t *q0 = vp + 2 * j * NG + (in ? n : 0);
-            const uint32_t l0 = in ? __byte_perm(q0[0], q0[NG], 0x7632) : 0;
-            const uint32_t l1 = in ? __byte_perm(q0[8 * NG], q0[9 * NG], 0x7632) : 0;
-            const uint32_t one = n == 0 ? 0x3F803F80u : 0;
-            mma_bf16(off, l0, one, l1, one, b0, b1);
-        }
-        uint32_t w0[NG], w1[NG], w2[NG], w3[NG];
-        lds<NG>(vp + 2 * j * NG, w0);
-        lds<NG>(vp + (2 * j + 1) * NG, w1);
-        lds<NG>(vp + (2 * j + 8) * NG, w2);
-        lds<NG>(vp + (2 * j + 9) * NG, w3);
-        const uint32_t va = smem_u32(vt) + at;
-        uint32_t s0 = 0, s1 = 0;
+        for (int b = 0; b < 2; ++b) {
+            float p[4];
 #pragma unroll
-        for (int c = 0; c < kChunks; c += 2) {
-            uint32_t r[4];
-            ldsm_x4_t(va ^ (c << 4), r[0], r[1], r[2], r[3]);
+            for (int i = 0; i < 4; ++i) p[i] = ex2_approx(y[b][i] - base[i & 1]);
+            l[0] += p[0] + p[2];
+            l[1] += p[1] + p[3];
+            // right operand of the values' products: tokens 2j, 2j + 1 (and + 8) of head n
+            const uint32_t b0 = transpose8(f2_to_bf2(p[0], p[1])), b1 = transpose8(f2_to_bf2(p[2], p[3]));
+            const uint32_t *vp = reinterpret_cast<const uint32_t *>(vt + b * kTile + q4_code_bytes(D));
+            {
+                // row g of `off`: sum of p lo of group g, less 128 times that of its rounded p step; row 8: sum of p
+                const bool in = n < NG;
+                const uint32_t *q0 = vp + 2 * j * NG + (in ? n : 0);
+                const uint32_t l0 = in ? __byte_perm(q0[0], q0[NG], 0x7632) : 0;
+                const uint32_t l1 = in ? __byte_perm(q0[8 * NG], q0[9 * NG], 0x7632) : 0;
+                const uint32_t one = n == 0 ? 0x3F803F80u : 0;
+                mma_bf16(off, l0, one, l1, one, b0, b1);
+            }
+            uint32_t w0[NG], w1[NG], w2[NG], w3[NG];
+            lds<NG>(vp + 2 * j * NG, w0);
+            lds<NG>(vp + (2 * j + 1) * NG, w1);
+            lds<NG>(vp + (2 * j + 8) * NG, w2);
+            lds<NG>(vp + (2 * j + 9) * NG, w3);
+            const uint32_t va = smem_u32(vt + b * kTile) + at;
+            uint32_t s0 = 0, s1 = 0;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int g = (c + i) / kPerGroup;
-                if ((c + i) % kPerGroup == 0) {
-                    s0 = mul_bf2(b0, __byte_perm(w0[g], w1[g], 0x5410));
-                    s1 = mul_bf2(b1, __byte_perm(w2[g], w3[g], 0x5410));
-                    const uint32_t minus = n == g ? 0xC300C300u : 0;  // -128
-                    mma_bf16(off, minus, 0, minus, 0, s0, s1);
+            for (int c = 0; c < kChunks; c += 2) {
+                uint32_t r[4];
+                ldsm_x4_t(va ^ (c << 4), r[0], r[1], r[2], r[3]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int g = (c + i) / kPerGroup;
+                    if ((c + i) % kPerGroup == 0) {
+                        s0 = mul_bf2(b0, __byte_perm(w0[g], w1[g], 0x5410));
+                        s1 = mul_bf2(b1, __byte_perm(w2[g], w3[g], 0x5410));
+                        const uint32_t minus = n == g ? 0xC300C300u : 0;  // -128
+                        mma_bf16(off, minus, 0, minus, 0, s0, s1);
+                    }
+                    mma_bf16(acc[c + i][0], codes<0>(r[2 * i]), codes<1>(r[2 * i]), codes<0>(r[2 * i + 1]), codes<1>(r[2 * i + 1]),
+                             s0, s1);
+                    mma_bf16(acc[c + i][1], codes<2>(r[2 * i]), codes<3>(r[2 * i]), codes<2>(r[2 * i + 1]), codes<3>(r[2 * i + 1]),
+                             s0, s1);
                 }
-                mma_bf16(acc[c + i][0], codes<0>(r[2 * i]), codes<1>(r[2 * i]), codes<0>(r[2 * i + 1]), codes<1>(r[2 * i + 1]), s0, s1);
-                mma_bf16(acc[c + i][1], codes<2>(r[2 * i]), codes<3>(r[2 * i]), codes<2>(r[2 * i + 1]), codes<3>(r[2 * i + 1]), s0, s1);
             }
         }
     }
@@ -591,7 +622,7 @@ struct TcWarp {
 // behind its range), records of pairs that began before a warp's range, the warps' own, prefix.
 template <class W>
 __host__ __device__ inline size_t attention_smem(int stages, int tile, int G, int B) {
-    return (size_t)W::kWarps * ((size_t)stages * 2 * tile + (size_t)G * (W::kD + 4) * 4 + W::kSharedBytes) + ((size_t)B + 1) * 4;
+    return (size_t)W::kWarps * ((size_t)stages * 4 * tile + (size_t)G * (W::kD + 4) * 4 + W::kSharedBytes) + ((size_t)B + 1) * 4;
 }
 
 template <class W>
@@ -600,18 +631,19 @@ __global__ void __launch_bounds__(W::kWarps * 32, W::kCtas) q4_attention_kernel(
     using T = typename W::T;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ uint64_t full_s[kWarps][kMaxStages];
-    __shared__ int bad_s[kWarps][kMaxStages], sums_s[kWarps];
-    __shared__ int head_s[kWarps], tail_s[kWarps];  // pair of a warp's records, -1 = none; bit 30 of head: its last unit is in
+    __shared__ int sums_s[kWarps];
+    __shared__ int head_s[kWarps], tail_s[kWarps];  // pair of a warp's records, -1 = none; kDone in head: its last unit is in
     __shared__ int abort_s;
-    constexpr int kLast = 1 << 30;
+    constexpr int kDone = 1 << 30;
+    constexpr int kFirst = 1 << 10, kLast = 1 << 11, kScored = 1 << 12;  // a unit's notes, above the tokens of its two tiles
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rec_n = rec_floats(a, D), stages = a.stages;
-    const size_t ring_bytes = (size_t)stages * 2 * a.tile;
+    const size_t ring_bytes = (size_t)stages * 4 * a.tile;
     unsigned char *ring = smem + warp * ring_bytes;
     float *heads = reinterpret_cast<float *>(smem + kWarps * ring_bytes);
     unsigned char *own = reinterpret_cast<unsigned char *>(heads + kWarps * rec_n) + warp * W::kSharedBytes;
     int *prefix = reinterpret_cast<int *>(reinterpret_cast<unsigned char *>(heads + kWarps * rec_n) + kWarps * W::kSharedBytes);
-    if (lane < stages) mbar_init(&full_s[warp][lane], 1);
+    if (lane < stages) mbar_init(&full_s[warp][lane], 2);
     if (lane == 0) head_s[warp] = tail_s[warp] = -1;
     if (tid == 0) abort_s = 0;
     fence_barrier_init();
@@ -620,131 +652,149 @@ __global__ void __launch_bounds__(W::kWarps * 32, W::kCtas) q4_attention_kernel(
         for (int s = tid; s <= a.B; s += blockDim.x) a.prefix[s] = prefix[s];
     if (prefix[a.B] == 0) return;
     const Split split = make_split(a, prefix[a.B]);
+    const bool mine = (int)blockIdx.x < split.ctas && warp < split.per_cta;
     const long long g = (long long)blockIdx.x * split.per_cta + warp;
-    const long long x0 = split.start(g);
-    const int n = warp < split.per_cta ? (int)(split.start(g + 1) - x0) : 0;
+    const long long x0 = mine ? split.start(g) : 0;
+    const int n = mine ? (int)(split.start(g + 1) - x0) : 0;
     if (n > 0) {
         const uint64_t pol = l2_evict_first_policy();
-        Cursor put, get;
-        put.seek(prefix, a.B, a.h_kv, x0);
-        get = put;
-        int ids = 0, ids_of = -1, ids_at = 0;  // lane i: block of unit ids_at + i of sequence ids_of
         const int tpb = a.b / kQ4Tile;
-        int put_st = 0;
-        auto issue = [&]() {
-            if (put.s != ids_of || put.u < ids_at || put.u >= ids_at + 32) {
-                ids_of = put.s;
-                ids_at = put.u;
-                const int u = put.u + lane;
-                ids = u < put.n ? __ldg(a.table + (size_t)put.s * a.table_stride + u / tpb) : -1;
-            }
-            const int blk = __shfl_sync(0xFFFFFFFFu, ids, put.u - ids_at);
-            if (lane == 0) {
-                const bool ok = blk >= 0 && blk < a.n_total;
-                bad_s[warp][put_st] = !ok;
-                uint64_t *bar = &full_s[warp][put_st];
-                if (ok) {
-                    const size_t from = (((size_t)blk * a.h_kv + put.h) * tpb + put.u % tpb) * a.tile;
-                    unsigned char *to = ring + (size_t)put_st * 2 * a.tile;
-                    mbar_arrive_expect_tx(bar, 2 * a.tile);
-                    bulk_g2s(to, a.k + from, a.tile, bar, pol);
-                    bulk_g2s(to + a.tile, a.v + from, a.tile, bar, pol);
+        // Units go in windows of 32: lane i finds out about unit i of the window that is
+        // being issued, and keeps it until the products get there.
+        int put_tile[2] = {-1, -1}, put_meta = 0, put_pair = 0, meta = 0, pair = 0;
+        auto look = [&](int i0) {
+            meta = put_meta;
+            pair = put_pair;
+            if (i0 + lane >= n) return;
+            Cursor c;
+            c.seek(prefix, a.B, a.h_kv, x0 + i0 + lane);
+            const int L = q4_len(a, c.s);
+            put_meta = (c.u == 0 ? kFirst : 0) | (c.u == c.n - 1 ? kLast : 0);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int t = 2 * c.u + b, valid = min(kQ4Tile, L - t * kQ4Tile);
+                put_tile[b] = -1;
+                if (valid <= 0) continue;
+                const int blk = __ldg(a.table + (size_t)c.s * a.table_stride + t / tpb);
+                if (blk >= 0 && blk < a.n_total) {
+                    put_tile[b] = (blk * a.h_kv + c.h) * tpb + t % tpb;
+                    put_meta |= valid << (5 * b);
                 } else {
-                    record_error(a.err, ZP_ERR_DEVICE, 0x159);
+                    record_error(a.err, ZP_ERR_DEVICE, 0x159);  // (its tokens weigh nothing)
+                }
+            }
+            if (a.want_score && q4_score_row(a, c.s, L) >= 0) put_meta |= kScored;
+            put_pair = c.s * a.h_kv + c.h;
+        };
+        int put_st = 0;
+        auto issue = [&](int i) {  // lanes 0 and 1: one tile of keys and values each
+            if ((i & 31) == 0) look(i);
+            const int t0 = __shfl_sync(0xFFFFFFFFu, put_tile[0], i & 31), t1 = __shfl_sync(0xFFFFFFFFu, put_tile[1], i & 31);
+            if (lane < 2) {
+                const int from = lane ? t1 : t0;
+                uint64_t *bar = &full_s[warp][put_st];
+                if (from >= 0) {
+                    unsigned char *to = ring + (put_st * 4 + lane) * a.tile;
+                    const size_t at = (size_t)(unsigned)from * (unsigned)a.tile;
+                    mbar_arrive_expect_tx(bar, 2 * a.tile);
+                    bulk_g2s(to, a.k + at, a.tile, bar, pol);
+                    bulk_g2s(to + 2 * a.tile, a.v + at, a.tile, bar, pol);
+                } else {
                     mbar_arrive(bar);
                 }
             }
             put_st = put_st + 1 == stages ? 0 : put_st + 1;
-            put.next(prefix, a.B, a.h_kv);
         };
-        for (int i = 0; i < n && i < stages; ++i) issue();
+        for (int i = 0; i < n && i < stages; ++i) issue(i);
+        meta = put_meta;
+        pair = put_pair;
 
         W w;
         w.init(own);
-        int L = 0, st = 0;
+        int st = 0;
         unsigned phase = 0;
-        bool scored = false;
+        bool began = false;  // the pair's first unit is in this range
         for (int i = 0; i < n; ++i) {
-            if (i == 0 || get.u == 0) {
-                if (i == 0 || get.h == 0) {
-                    L = q4_len(a, get.s);
-                    scored = q4_score_row(a, get.s, L) >= 0;
-                }
-                w.begin(a, get.s, get.h, lane);
+            // (units 32 and on were looked up stages before; `look` has then moved the window before on)
+            if (i && (i & 31) == 0) meta = put_meta, pair = put_pair;
+            const int now = __shfl_sync(0xFFFFFFFFu, meta, i & 31);
+            if (i == 0 || (now & kFirst)) {
+                const int id = __shfl_sync(0xFFFFFFFFu, pair, i & 31);
+                w.begin(a, id / a.h_kv, id % a.h_kv, lane);
+                began = now & kFirst;
             }
             if (!mbar_wait_bounded(&full_s[warp][st], phase, a.err, &abort_s, 0x15b)) {
                 drain(full_s[warp], stages, i, n);
                 break;
             }
-            unsigned char *kt = ring + (size_t)st * 2 * a.tile;
-            float *lg = scored ? a.logits + (size_t)(x0 + i) * kQ4Tile * a.G : nullptr;
-            if (!bad_s[warp][st]) w.tile(a, kt, kt + a.tile, min(kQ4Tile, L - get.u * kQ4Tile), lg, lane);
-            else if (lg)
-                for (int e = lane; e < kQ4Tile * a.G; e += 32) lg[e] = -INFINITY;
+            float *lg = now & kScored ? a.logits + (size_t)(x0 + i) * (kUnit * a.G) : nullptr;
+            w.unit(a, ring + st * 4 * a.tile, now & 31, now >> 5 & 31, lg, lane);
             __syncwarp();
-            if (i + stages < n) issue();
+            if (i + stages < n) issue(i + stages);
             if (++st == stages) st = 0, phase ^= 1;
-            const bool last = get.u == get.n - 1;
-            if (last || i == n - 1) {
+            if ((now & kLast) || i == n - 1) {
+                const bool last = now & kLast;
+                const int id = __shfl_sync(0xFFFFFFFFu, pair, i & 31);
                 w.end(lane);
-                const bool from_start = i >= get.u;  // the pair's first unit is in this range
-                if (last && from_start) {
-                    w.write_out(a, get.s, get.h, lane);
+                if (last && began) {
+                    w.write_out(a, id / a.h_kv, id % a.h_kv, lane);
                 } else {
                     // (a pair that goes on behind the range is its last: the ring is empty then)
-                    w.write_record(a, from_start ? reinterpret_cast<float *>(ring) : heads + warp * rec_n, lane);
+                    w.write_record(a, began ? reinterpret_cast<float *>(ring) : heads + warp * rec_n, lane);
                     if (lane == 0) {
-                        const int pair = get.s * a.h_kv + get.h;
-                        if (from_start) tail_s[warp] = pair;
-                        else head_s[warp] = pair | (last ? kLast : 0);
+                        if (began) tail_s[warp] = id;
+                        else head_s[warp] = id | (last ? kDone : 0);
                     }
                 }
             }
-            get.next(prefix, a.B, a.h_kv);
         }
     }
     __syncthreads();
     if (abort_s) return;
-    // ---- the records of this CTA, pair by pair: one begins in a warp's tail, or before the
-    // CTA in the first warp's head, and goes on in the heads of the next warps
-    for (int w0 = 0; w0 < split.per_cta; ++w0) {
-#pragma unroll 1
-        for (int side = 0; side < 2; ++side) {
-            const int id = side ? tail_s[w0] : head_s[w0];
-            if (id < 0 || (side == 0 && w0 > 0 && (head_s[w0 - 1] == (id & ~kLast) || tail_s[w0 - 1] == (id & ~kLast)))) continue;
-            const int pair = id & ~kLast;
-            bool done = side == 0 && (id & kLast);
-            int w1 = w0;  // the pair's last warp here
-            while (!done && w1 + 1 < split.per_cta && head_s[w1 + 1] >= 0 && (head_s[w1 + 1] & ~kLast) == pair) {
-                ++w1;
-                done = head_s[w1] & kLast;
+    // ---- the records of this CTA: a pair's chain begins in a warp's tail, or before the CTA in
+    // the first warp's head, and goes on in the heads of the next warps.  Its first warp joins it.
+    for (int side = warp == 0 ? 0 : 1; side < 2; ++side) {
+        const int id = warp >= split.per_cta ? -1 : side ? tail_s[warp] : head_s[warp];
+        if (id < 0) continue;
+        const int pair = id & ~kDone;
+        bool done = side == 0 && (id & kDone);
+        int w1 = warp;  // the pair's last warp here
+        while (!done && w1 + 1 < split.per_cta && head_s[w1 + 1] >= 0 && (head_s[w1 + 1] & ~kDone) == pair) {
+            ++w1;
+            done = head_s[w1] & kDone;
+        }
+        const float *rec0 = side ? reinterpret_cast<const float *>(ring) : heads + warp * rec_n;
+        auto rec = [&](int w) { return w == warp ? rec0 : heads + w * rec_n; };
+        const int s = pair / a.h_kv, h = pair % a.h_kv;
+        float *to = a.rec + (size_t)(2 * blockIdx.x + side) * rec_n;
+        T *out = static_cast<T *>(a.out) + ((size_t)s * a.h_q + (size_t)h * a.G) * D;
+        for (int i = lane * 4; i < a.G * D; i += 128) {
+            const int q = i / D;
+            float m = -INFINITY;
+#pragma unroll 4
+            for (int w = warp; w <= w1; ++w) m = fmaxf(m, rec(w)[4 * q]);
+            const float base = m == -INFINITY ? 0.f : m;
+            float x[4] = {}, lo = 0.f, l = 0.f;
+#pragma unroll 4
+            for (int w = warp; w <= w1; ++w) {
+                const float4 r = *reinterpret_cast<const float4 *>(rec(w) + 4 * q);
+                const float4 v = *reinterpret_cast<const float4 *>(rec(w) + 4 * a.G + i);
+                const float f = ex2_approx(r.x - base);
+                lo = fmaf(r.y, f, lo);
+                l = fmaf(r.z, f, l);
+                x[0] = fmaf(v.x, f, x[0]);
+                x[1] = fmaf(v.y, f, x[1]);
+                x[2] = fmaf(v.z, f, x[2]);
+                x[3] = fmaf(v.w, f, x[3]);
             }
-            auto rec = [&](int w) {
-                return w == w0 && side ? reinterpret_cast<const float *>(smem + w * ring_bytes) : heads + w * rec_n;
-            };
-            const int s = pair / a.h_kv, h = pair % a.h_kv;
-            float *to = a.rec + (size_t)(2 * blockIdx.x + side) * rec_n;
-            T *out = static_cast<T *>(a.out) + ((size_t)s * a.h_q + (size_t)h * a.G) * D;
-            for (int i = tid; i < a.G * D; i += kWarps * 32) {
-                const int q = i / D;
-                float m = -INFINITY;
-                for (int w = w0; w <= w1; ++w) m = fmaxf(m, rec(w)[4 * q]);
-                const float base = m == -INFINITY ? 0.f : m;
-                float x = 0.f, lo = 0.f, l = 0.f;
-                for (int w = w0; w <= w1; ++w) {
-                    const float4 r = *reinterpret_cast<const float4 *>(rec(w) + 4 * q);
-                    const float f = ex2_approx(r.x - base);
-                    lo = fmaf(r.y, f, lo);
-                    l = fmaf(r.z, f, l);
-                    x = fmaf(rec(w)[4 * a.G + i], f, x);
-                }
-                if (side && done) {
-                    out[i] = from_f<T>(lo == 0.f ? 0.f : x / lo);
-                    if (a.want_score && i % D == 0) a.stats[(size_t)s * a.h_q + h * a.G + q] = score_norm(m, l);
-                } else {
-                    to[4 * a.G + i] = x;
-                    if (i % D == 0) reinterpret_cast<float4 *>(to)[q] = make_float4(m, lo, l, 0.f);
-                }
+            if (side && done) {
+                const float r = lo == 0.f ? 0.f : 1.f / lo;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) out[i + e] = from_f<T>(x[e] * r);
+                if (a.want_score && i % D == 0) a.stats[(size_t)s * a.h_q + h * a.G + q] = score_norm(m, l);
+            } else {
+                *reinterpret_cast<float4 *>(to + 4 * a.G + i) = make_float4(x[0], x[1], x[2], x[3]);
+                if (i % D == 0) reinterpret_cast<float4 *>(to)[q] = make_float4(m, lo, l, 0.f);
             }
         }
     }
@@ -753,11 +803,11 @@ __global__ void __launch_bounds__(W::kWarps * 32, W::kCtas) q4_attention_kernel(
 // ---------------------------------------------------------------- what is left
 // CTA c joins the records of the pair that its counterpart of the attention kernel began and
 // did not finish, and forms the score of that one's units.
-constexpr int kFinishThreads = 512, kScoreUnroll = 4;
+constexpr int kFinishThreads = 1024, kScoreUnroll = 4;
 
-// records of a pair cut between CTAs: CTA c0 has its beginning (slot 1), the others slot 0
-__device__ __forceinline__ const float *cta_record(const Q4Args &a, const Split &p, int c0, int c, int rec_n) {
-    return c > c0 && p.cta_start(c) == p.cta_start(c + 1) ? nullptr : a.rec + (size_t)(2 * c + (c == c0 ? 1 : 0)) * rec_n;
+// Record of CTA c of a pair cut between CTAs, which CTA c0 begins.
+__device__ __forceinline__ const float *cta_record(const Q4Args &a, int c0, int c, int rec_n) {
+    return a.rec + (size_t)(2 * c + (c == c0 ? 1 : 0)) * rec_n;
 }
 
 template <typename T, int D>
@@ -770,8 +820,8 @@ __global__ void __launch_bounds__(kFinishThreads) q4_finish_kernel(const Q4Args 
     if (prefix[a.B] == 0) return;
     const Split split = make_split(a, prefix[a.B]);
     const int c0 = blockIdx.x;
+    if (c0 >= split.ctas) return;
     const long long b0 = split.cta_start(c0), b1 = split.cta_start(c0 + 1);
-    if (b0 == b1) return;
     {
         Cursor cut;
         cut.seek(prefix, a.B, a.h_kv, b1 - 1);
@@ -782,15 +832,16 @@ __global__ void __launch_bounds__(kFinishThreads) q4_finish_kernel(const Q4Args 
             for (int i = tid; i < a.G * D; i += kFinishThreads) {
                 const int q = i / D;
                 float m = -INFINITY, x = 0.f, lo = 0.f;
+#pragma unroll 8
+                for (int c = c0; c <= c1; ++c) m = fmaxf(m, cta_record(a, c0, c, rec_n)[4 * q]);
+                const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll 8
                 for (int c = c0; c <= c1; ++c) {
-                    const float *r = cta_record(a, split, c0, c, rec_n);
-                    if (!r) continue;
-                    const float4 hd = *reinterpret_cast<const float4 *>(r + 4 * q);
-                    const float top = fmaxf(m, hd.x), base = top == -INFINITY ? 0.f : top;
-                    const float was = ex2_approx(m - base), now = ex2_approx(hd.x - base);
-                    m = top;
-                    lo = lo * was + hd.y * now;
-                    x = x * was + r[4 * a.G + i] * now;
+                    const float *r = cta_record(a, c0, c, rec_n);
+                    const float2 hd = *reinterpret_cast<const float2 *>(r + 4 * q);
+                    const float f = ex2_approx(hd.x - base);
+                    lo = fmaf(hd.y, f, lo);
+                    x = fmaf(r[4 * a.G + i], f, x);
                 }
                 out[i] = from_f<T>(lo == 0.f ? 0.f : x / lo);
             }
@@ -816,13 +867,13 @@ __global__ void __launch_bounds__(kFinishThreads) q4_finish_kernel(const Q4Args 
                 const int k0 = split.cta_of(first), k1 = split.cta_of(last);
                 if (lane < a.G) {
                     float m = -INFINITY, l = 0.f;
+#pragma unroll 8
+                    for (int c = k0; c <= k1; ++c) m = fmaxf(m, cta_record(a, k0, c, rec_n)[4 * lane]);
+                    const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll 8
                     for (int c = k0; c <= k1; ++c) {
-                        const float *r = cta_record(a, split, k0, c, rec_n);
-                        if (!r) continue;
-                        const float4 hd = *reinterpret_cast<const float4 *>(r + 4 * lane);
-                        const float top = fmaxf(m, hd.x), base = top == -INFINITY ? 0.f : top;
-                        l = l * ex2_approx(m - base) + hd.z * ex2_approx(hd.x - base);
-                        m = top;
+                        const float4 hd = *reinterpret_cast<const float4 *>(cta_record(a, k0, c, rec_n) + 4 * lane);
+                        l = fmaf(hd.z, ex2_approx(hd.x - base), l);
                     }
                     norm = score_norm(m, l);
                 }
@@ -834,8 +885,8 @@ __global__ void __launch_bounds__(kFinishThreads) q4_finish_kernel(const Q4Args 
             const bool fresh = P % a.b == a.b - a.window;
             const float share = 1.f / (float)a.window;
             float *S = a.score + ((size_t)row * a.h_kv + cur.h) * a.score_stride;
-            const int t0 = cur.u * kQ4Tile, t1 = min(t0 + units * kQ4Tile, L);
-            const float *lg = a.logits + (size_t)first * kQ4Tile * a.G;
+            const int t0 = cur.u * kUnit, t1 = min(t0 + units * kUnit, L);
+            const float *lg = a.logits + (size_t)first * kUnit * a.G;
             for (int t = t0 + lane; t < t1; t += 32 * kScoreUnroll) {
                 float top[kScoreUnroll], old[kScoreUnroll];
 #pragma unroll
@@ -844,9 +895,20 @@ __global__ void __launch_bounds__(kFinishThreads) q4_finish_kernel(const Q4Args 
                     top[k] = -INFINITY;
                     old[k] = 0.f;
                     if (tok < t1) {
+                        const float *x = lg + (size_t)tok * a.G;
+                        if (a.G % 4 == 0) {
 #pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            if (q < a.G) top[k] = fmaxf(top[k], lg[(size_t)tok * a.G + q] - c[q]);
+                            for (int q = 0; q < 8; q += 4) {
+                                if (q >= a.G) continue;
+                                const float4 v = __ldcg(reinterpret_cast<const float4 *>(x + q));
+                                top[k] = fmaxf(fmaxf(top[k], fmaxf(v.x - c[q], v.y - c[q + 1])),
+                                               fmaxf(v.z - c[q + 2], v.w - c[q + 3]));
+                            }
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                if (q < a.G) top[k] = fmaxf(top[k], __ldcg(x + q) - c[q]);
+                        }
                         if (!fresh && tok != P) old[k] = S[tok];
                     }
                 }
@@ -900,6 +962,9 @@ zp_status q4_plan(const zp_cache_desc *D, int group, int B, int table_stride, in
     if ((long long)B * table_stride * D->block_size > INT32_MAX)
         return fail(ZP_ERR_SHAPE, "q4_decode: B=%d rows of %d blocks of %d tokens exceed 32 bits", B, table_stride,
                     D->block_size);
+    if ((long long)D->n_total_blocks * D->h_kv * (D->block_size / kQ4Tile) > INT32_MAX)
+        return fail(ZP_ERR_SHAPE, "q4_decode: %d blocks of %d tokens and %d heads exceed 32-bit tiles", D->n_total_blocks,
+                    D->block_size, D->h_kv);
     const int d = D->head_dim, tile = q4_tile_bytes(d, group);
     with_warp(D, group, [&](auto w) {
         using W = decltype(w);
@@ -919,7 +984,7 @@ zp_status q4_plan(const zp_cache_desc *D, int group, int B, int table_stride, in
     p->off_rec = off;
     off = align_up(off + (size_t)2 * p->grid * G * (d + 4) * 4, 256);
     p->off_logits = off;
-    if (scored) off = align_up(off + (size_t)B * table_stride * D->block_size * D->h_q * 4, 256);
+    if (scored) off += (size_t)B * align_up((size_t)table_stride * D->block_size, kUnit) * D->h_q * 4;
     p->total = off;
     return ZP_OK;
 }
