@@ -488,18 +488,29 @@ def zp_q4_cache(desc: CacheDesc, group: int = 32, layers=None, device="cuda"):
     return torch.zeros(shape, dtype=torch.uint8, device=device), torch.zeros(shape, dtype=torch.uint8, device=device)
 
 
-def _q4_caches(desc, group, k_cache, v_cache, dev, several=None):
-    """(address, address, layers, bytes between layers) of a 4-bit cache of one layer or, with a fifth
-    dimension, of several (`several`: which of the two the call wants)."""
-    shape = (desc.n_total_blocks, desc.h_kv, desc.block_size // 16, zp_q4_tile_bytes(desc, group))
-    layers = k_cache.shape[0] if k_cache.dim() == 5 and several is not False else None
-    want = shape if layers is None else (layers,) + shape
-    if k_cache.shape != want or v_cache.shape != want or not (k_cache.dtype is v_cache.dtype is torch.uint8):
-        raise ValueError("k_cache and v_cache must be uint8 [N_total][h_kv][b/16][tile] = %s%s, are %s and %s"
-                         % (shape, "" if several is False else " (or one of these per layer)", tuple(k_cache.shape),
-                            tuple(v_cache.shape)))
-    return (_ptr_on(k_cache, dev, "k_cache"), _ptr_on(v_cache, dev, "v_cache"), layers,
-            0 if layers is None else k_cache.numel() // max(layers, 1))
+def _q4_shape(desc, group):
+    """Shape of one layer of a 4-bit cache.  (The library refuses the groups and head sizes it does not know.)"""
+    d = desc.head_dim
+    return desc.n_total_blocks, desc.h_kv, desc.block_size >> 4, (d << 3) + 64 * (d // group if group > 0 else 0)
+
+
+def _q4_cache_of(t, shape, dev: int, name: str):
+    """Address of a cache tensor of `shape`."""
+    if t.shape != shape or t.dtype is not torch.uint8:
+        raise ValueError("%s must be uint8 [N_total][h_kv][b/16][tile] = %s, is %s %s" % (name, shape, t.dtype, tuple(t.shape)))
+    return _ptr_on(t, dev, name)
+
+
+def _q4_caches(desc, group, k_cache, v_cache, dev):
+    """(address, address, layers, bytes between layers) of a 4-bit cache of one layer (layers: None) or, with a
+    fifth dimension, of several."""
+    shape = _q4_shape(desc, group)
+    layers = None
+    if k_cache.dim() == 5:
+        layers = k_cache.shape[0]
+        shape = (layers,) + shape
+    return (_q4_cache_of(k_cache, shape, dev, "k_cache"), _q4_cache_of(v_cache, shape, dev, "v_cache"), layers,
+            0 if layers is None else k_cache.stride(0))
 
 
 def _q4_rows(desc, k, v, n, layers, dev, names):
@@ -514,11 +525,11 @@ def _q4_rows(desc, k, v, n, layers, dev, names):
         raise ValueError("%s and %s must be CUDA tensors on the current device" % names)
     # (layer, token, head, element); a stride along a dimension of one entry means nothing
     row = h_kv * d
-    strides = [(x.stride(0) if layers and layers > 1 else 0, x.stride(-3) if n > 1 else row, x.stride(-2) if h_kv > 1 else d,
-                x.stride(-1)) for x in (k, v)]
-    if n and (strides[0][2:] != (d, 1) or strides[1] != strides[0]):
+    ks, vs = k.stride(), v.stride()
+    if n and (ks[-1] != 1 or vs[-1] != 1 or (h_kv > 1 and (ks[-2] != d or vs[-2] != d)) or (n > 1 and ks[-3] != vs[-3]) or
+              (layers is not None and layers > 1 and ks[0] != vs[0])):
         raise ValueError("the row [h_kv][d] of a token must be contiguous, and %s and %s must have the same strides" % names)
-    return k.data_ptr(), v.data_ptr(), strides[0][1], strides[0][0]
+    return k.data_ptr(), v.data_ptr(), ks[-3] if n > 1 else row, ks[0] if layers is not None and layers > 1 else 0
 
 
 def zp_q4_write_kv(desc, k_new, v_new, slots, k_cache, v_cache, group=32, stream=None) -> None:
@@ -537,7 +548,8 @@ def zp_q4_append_kv(desc, k_new, v_new, k_cache, v_cache, block_table, seq_lens,
     """zp_append_kv into a 4-bit cache: k_new, v_new [B][h_kv][d], one token per sequence."""
     B, table_stride = _table(block_table)
     dev = _device()
-    K, V, _, _ = _q4_caches(desc, group, k_cache, v_cache, dev, several=False)
+    cache = _q4_shape(desc, group)
+    K, V = _q4_cache_of(k_cache, cache, dev, "k_cache"), _q4_cache_of(v_cache, cache, dev, "v_cache")
     shape = (B, desc.h_kv, desc.head_dim)
     if k_new.shape != shape or v_new.shape != shape or not (k_new.dtype is v_new.dtype is _TORCH.get(desc.dtype)):
         raise ValueError("k_new and v_new must be [B][h_kv][d] = %s of the descriptor's type" % (shape,))
@@ -567,6 +579,9 @@ def zp_q4_decode_workspace_size(desc: CacheDesc, B: int, table_stride: int, grou
     return n
 
 
+_Q4_SIZES = {}  # workspace sizes by shape and device
+
+
 def zp_q4_decode_attn(desc, q, k_cache, v_cache, block_table, seq_lens, out, score_accum=None, window=0, workspace=None,
                       stream=None, score_rows=None, group=32) -> None:
     """zp_paged_decode_attn over a 4-bit cache."""
@@ -577,7 +592,8 @@ def zp_q4_decode_attn(desc, q, k_cache, v_cache, block_table, seq_lens, out, sco
         raise ValueError("q and out must be [B][h_q][d] = %s, are %s and %s" % (shape, tuple(q.shape), tuple(out.shape)))
     if not (q.dtype is out.dtype is dt):
         raise ValueError("q and out must have the descriptor's type")
-    K, V, _, _ = _q4_caches(desc, group, k_cache, v_cache, dev, several=False)
+    cache = _q4_shape(desc, group)
+    K, V = _q4_cache_of(k_cache, cache, dev, "k_cache"), _q4_cache_of(v_cache, cache, dev, "v_cache")
     n_rows = 0
     if score_accum is not None:
         n_rows = score_accum.shape[0]
@@ -592,7 +608,12 @@ def zp_q4_decode_attn(desc, q, k_cache, v_cache, block_table, seq_lens, out, sco
     on = _raw_stream(stream, dev)
     if workspace is None:
         # memory of the stream that the work runs on, given back behind it
-        n = max(zp_q4_decode_workspace_size(desc, B, table_stride, group, score_accum is not None), 16)
+        key = (bytes(desc), group, B, table_stride, score_accum is not None, dev)
+        n = _Q4_SIZES.get(key)
+        if n is None:
+            if len(_Q4_SIZES) > 1000:
+                _Q4_SIZES.clear()
+            n = _Q4_SIZES[key] = zp_q4_decode_workspace_size(desc, B, table_stride, group, score_accum is not None)
         at = torch.cuda.caching_allocator_alloc(n, dev, on)
         try:
             rc = lib.zp_q4_decode_attn(*args, at, n, on)

@@ -50,22 +50,26 @@ struct Q4Args {
 
 // ---------------------------------------------------------------- the split
 struct Split {
-    long long U, W;     // units, ranges (no more than units: none is empty)
+    int U, W;           // units, ranges (no more than units: none is empty)
     int per_cta, ctas;  // ranges of a CTA (its first warps take one each), CTAs that have some
-    __device__ __forceinline__ long long start(long long g) const { return g * U / W; }
-    __device__ __forceinline__ long long cta_start(int c) const { return start((long long)c * per_cta); }
+    int quot, rest;     // U / W, U % W
+    // the first unit of range g: floor(g U / W)  (W is below 2^15: 32 bits hold g * rest)
+    __device__ __forceinline__ int start(int g) const { return g * quot + (int)((unsigned)g * (unsigned)rest / (unsigned)W); }
+    __device__ __forceinline__ int cta_start(int c) const { return start(c * per_cta); }
     // the CTA whose ranges hold unit x: the largest range g with start(g) <= x is its
-    __device__ __forceinline__ int cta_of(long long x) const { return (int)((((x + 1) * W - 1) / U) / per_cta); }
+    __device__ __forceinline__ int cta_of(int x) const { return (int)(((x + 1ll) * W - 1) / U) / per_cta; }
 };
 
 __device__ __forceinline__ Split make_split(const Q4Args &a, int units) {
     Split p;
-    p.U = (long long)units * a.h_kv;
-    const long long want = (p.U + a.grid - 1) / a.grid;
-    p.per_cta = (int)(want < 1 ? 1 : want > a.warps ? a.warps : want);
-    const long long most = p.U / p.per_cta;
-    p.ctas = (int)(most < a.grid ? most : a.grid);
-    p.W = (long long)p.per_cta * p.ctas;
+    p.U = units * a.h_kv;
+    const int want = (int)(((unsigned)p.U + a.grid - 1) / (unsigned)a.grid);
+    p.per_cta = want < 1 ? 1 : want > a.warps ? a.warps : want;
+    const int most = p.U / p.per_cta;
+    p.ctas = most < a.grid ? most : a.grid;
+    p.W = p.per_cta * p.ctas;
+    p.quot = p.U / p.W;
+    p.rest = p.U - p.quot * p.W;
     return p;
 }
 
@@ -112,16 +116,16 @@ __device__ void unit_prefix(const Q4Args &a, int *prefix, int *warp_sum) {
 // A place in the sequence of units.
 struct Cursor {
     int s, h, u, n;  // unit u of the n of (sequence s, kv head h)
-    __device__ __forceinline__ void seek(const int *prefix, int B, int h_kv, long long x) {
+    __device__ __forceinline__ void seek(const int *prefix, int B, int h_kv, int x) {
         int lo = 0, hi = B - 1;
         while (lo < hi) {  // the last s with prefix[s] * h_kv <= x (it has units)
             const int mid = (lo + hi + 1) >> 1;
-            if ((long long)prefix[mid] * h_kv <= x) lo = mid;
+            if (prefix[mid] * h_kv <= x) lo = mid;
             else hi = mid - 1;
         }
         s = lo;
         n = prefix[s + 1] - prefix[s];
-        const int in = (int)(x - (long long)prefix[s] * h_kv);
+        const int in = x - prefix[s] * h_kv;
         h = in / n;
         u = in - h * n;
     }
@@ -179,6 +183,9 @@ struct ScalarWarp {
     static constexpr int kD = D, kWarps = 12, kCtas = 1;
     static constexpr int kDims = D / 32;
     static constexpr int kSharedBytes = (GP * D + kQ4Tile * GP) * 4;
+    struct Query {
+        float q[GP * kDims];
+    };
     float m[GP], l[GP], acc[GP][kDims];
     float *q_s, *p_s;
 
@@ -186,10 +193,17 @@ struct ScalarWarp {
         q_s = reinterpret_cast<float *>(shared);
         p_s = q_s + GP * D;
     }
-    __device__ __forceinline__ void begin(const Q4Args &a, int s, int h, int lane) {
+    static __device__ __forceinline__ Query fetch(const Q4Args &a, int s, int h, int lane) {
         const float *q = static_cast<const float *>(a.q) + ((size_t)s * a.h_q + (size_t)h * a.G) * D;
+        Query x;
+#pragma unroll
+        for (int i = 0; i < GP * kDims; ++i) x.q[i] = lane + 32 * i < a.G * D ? __ldg(q + lane + 32 * i) : 0.f;
+        return x;
+    }
+    __device__ __forceinline__ void begin(const Q4Args &a, const Query &x, int lane) {
         __syncwarp();
-        for (int i = lane; i < GP * D; i += 32) q_s[i] = i < a.G * D ? q[i] : 0.f;
+#pragma unroll
+        for (int i = 0; i < GP * kDims; ++i) q_s[lane + 32 * i] = x.q[i];
         __syncwarp();
 #pragma unroll
         for (int g = 0; g < GP; ++g) {
@@ -380,17 +394,26 @@ struct TcWarp {
 
     __device__ __forceinline__ void init(unsigned char *) {}
 
-    __device__ __forceinline__ void begin(const Q4Args &a, int s, int h, int lane) {
+    struct Query {
+        uint4 w[kChunks];
+    };
+    static __device__ __forceinline__ Query fetch(const Q4Args &a, int s, int h, int lane) {
         const int n = lane >> 2, j = lane & 3;
         const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
                                                          ((size_t)s * a.h_q + (size_t)h * a.G + n) * D);
+        Query x;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) x.w[c] = n < a.G ? __ldg(q + c * 4 + j) : make_uint4(0, 0, 0, 0);
+        return x;
+    }
+    __device__ __forceinline__ void begin(const Q4Args &a, const Query &x, int lane) {
+        const int j = lane & 3;
         float sum[NG];
 #pragma unroll
         for (int g = 0; g < NG; ++g) sum[g] = 0.f;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (n < a.G) w = __ldg(q + c * 4 + j);
+            const uint4 w = x.w[c];
             qb[c][0][0] = __byte_perm(w.x, w.z, 0x5410);
             qb[c][0][1] = __byte_perm(w.x, w.z, 0x7632);
             qb[c][1][0] = __byte_perm(w.y, w.w, 0x5410);
@@ -653,10 +676,14 @@ __global__ void __launch_bounds__(W::kWarps * 32, W::kCtas) q4_attention_kernel(
     if (prefix[a.B] == 0) return;
     const Split split = make_split(a, prefix[a.B]);
     const bool mine = (int)blockIdx.x < split.ctas && warp < split.per_cta;
-    const long long g = (long long)blockIdx.x * split.per_cta + warp;
-    const long long x0 = mine ? split.start(g) : 0;
-    const int n = mine ? (int)(split.start(g + 1) - x0) : 0;
+    const int g = blockIdx.x * split.per_cta + warp;
+    const int x0 = mine ? split.start(g) : 0;
+    const int n = mine ? split.start(g + 1) - x0 : 0;
     if (n > 0) {
+        // the queries of the first pair, ahead of the tiles of all warps
+        Cursor begin;
+        begin.seek(prefix, a.B, a.h_kv, x0);
+        const typename W::Query query = W::fetch(a, begin.s, begin.h, lane);
         const uint64_t pol = l2_evict_first_policy();
         const int tpb = a.b / kQ4Tile;
         // Units go in windows of 32: lane i finds out about unit i of the window that is
@@ -668,6 +695,12 @@ __global__ void __launch_bounds__(W::kWarps * 32, W::kCtas) q4_attention_kernel(
             if (i0 + lane >= n) return;
             Cursor c;
             c.seek(prefix, a.B, a.h_kv, x0 + i0 + lane);
+            int blk[2];  // (read beside the length: a row of the table has an entry for every token below its stride)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int col = (2 * c.u + b) / tpb;
+                blk[b] = col < a.table_stride ? __ldg(a.table + (size_t)c.s * a.table_stride + col) : -1;
+            }
             const int L = q4_len(a, c.s);
             put_meta = (c.u == 0 ? kFirst : 0) | (c.u == c.n - 1 ? kLast : 0);
 #pragma unroll
@@ -675,14 +708,14 @@ __global__ void __launch_bounds__(W::kWarps * 32, W::kCtas) q4_attention_kernel(
                 const int t = 2 * c.u + b, valid = min(kQ4Tile, L - t * kQ4Tile);
                 put_tile[b] = -1;
                 if (valid <= 0) continue;
-                const int blk = __ldg(a.table + (size_t)c.s * a.table_stride + t / tpb);
-                if (blk >= 0 && blk < a.n_total) {
-                    put_tile[b] = (blk * a.h_kv + c.h) * tpb + t % tpb;
+                if (blk[b] >= 0 && blk[b] < a.n_total) {
+                    put_tile[b] = (blk[b] * a.h_kv + c.h) * tpb + t % tpb;
                     put_meta |= valid << (5 * b);
                 } else {
                     record_error(a.err, ZP_ERR_DEVICE, 0x159);  // (its tokens weigh nothing)
                 }
             }
+
             if (a.want_score && q4_score_row(a, c.s, L) >= 0) put_meta |= kScored;
             put_pair = c.s * a.h_kv + c.h;
         };
@@ -711,6 +744,7 @@ __global__ void __launch_bounds__(W::kWarps * 32, W::kCtas) q4_attention_kernel(
 
         W w;
         w.init(own);
+        w.begin(a, query, lane);
         int st = 0;
         unsigned phase = 0;
         bool began = false;  // the pair's first unit is in this range
@@ -718,10 +752,12 @@ __global__ void __launch_bounds__(W::kWarps * 32, W::kCtas) q4_attention_kernel(
             // (units 32 and on were looked up stages before; `look` has then moved the window before on)
             if (i && (i & 31) == 0) meta = put_meta, pair = put_pair;
             const int now = __shfl_sync(0xFFFFFFFFu, meta, i & 31);
-            if (i == 0 || (now & kFirst)) {
-                const int id = __shfl_sync(0xFFFFFFFFu, pair, i & 31);
-                w.begin(a, id / a.h_kv, id % a.h_kv, lane);
-                began = now & kFirst;
+            if (now & kFirst) {
+                began = true;
+                if (i) {
+                    const int id = __shfl_sync(0xFFFFFFFFu, pair, i & 31);
+                    w.begin(a, W::fetch(a, id / a.h_kv, id % a.h_kv, lane), lane);
+                }
             }
             if (!mbar_wait_bounded(&full_s[warp][st], phase, a.err, &abort_s, 0x15b)) {
                 drain(full_s[warp], stages, i, n);
@@ -821,11 +857,11 @@ __global__ void __launch_bounds__(kFinishThreads) q4_finish_kernel(const Q4Args 
     const Split split = make_split(a, prefix[a.B]);
     const int c0 = blockIdx.x;
     if (c0 >= split.ctas) return;
-    const long long b0 = split.cta_start(c0), b1 = split.cta_start(c0 + 1);
+    const int b0 = split.cta_start(c0), b1 = split.cta_start(c0 + 1);
     {
         Cursor cut;
         cut.seek(prefix, a.B, a.h_kv, b1 - 1);
-        const long long first = b1 - 1 - cut.u, last = first + cut.n - 1;
+        const int first = b1 - 1 - cut.u, last = first + cut.n - 1;
         if (first >= b0 && last >= b1) {
             const int c1 = split.cta_of(last);
             T *out = static_cast<T *>(a.out) + ((size_t)cut.s * a.h_q + (size_t)cut.h * a.G) * D;
@@ -850,16 +886,16 @@ __global__ void __launch_bounds__(kFinishThreads) q4_finish_kernel(const Q4Args 
     if (!a.want_score) return;
     // ---- the score: warps take equal parts of the CTA's units, a lane one token at a time
     constexpr int kWarps = kFinishThreads / 32;
-    const long long x0 = b0 + (b1 - b0) * warp / kWarps, x1 = b0 + (b1 - b0) * (warp + 1) / kWarps;
+    const int x0 = b0 + (int)((long long)(b1 - b0) * warp / kWarps), x1 = b0 + (int)((long long)(b1 - b0) * (warp + 1) / kWarps);
     if (x0 == x1) return;
     Cursor cur;
     cur.seek(prefix, a.B, a.h_kv, x0);
-    for (long long x = x0; x < x1;) {
-        const int units = (int)min((long long)(cur.n - cur.u), x1 - x);  // the rest of this pair
+    for (int x = x0; x < x1;) {
+        const int units = min(cur.n - cur.u, x1 - x);  // the rest of this pair
         const int L = q4_len(a, cur.s), row = q4_score_row(a, cur.s, L);
         if (row >= 0) {
             // normalisers of the heads: lane q has head q's
-            const long long first = x - cur.u, last = first + cur.n - 1;
+            const int first = x - cur.u, last = first + cur.n - 1;
             float norm = INFINITY;
             if (first >= b0 && last < b1) {
                 if (lane < a.G) norm = __ldcg(a.stats + (size_t)cur.s * a.h_q + cur.h * a.G + lane);
@@ -962,6 +998,8 @@ zp_status q4_plan(const zp_cache_desc *D, int group, int B, int table_stride, in
     if ((long long)B * table_stride * D->block_size > INT32_MAX)
         return fail(ZP_ERR_SHAPE, "q4_decode: B=%d rows of %d blocks of %d tokens exceed 32 bits", B, table_stride,
                     D->block_size);
+    if (((long long)table_stride * D->block_size / kUnit + 1) * B * D->h_kv > INT32_MAX / 2)
+        return fail(ZP_ERR_SHAPE, "q4_decode: B=%d rows of %d blocks and %d heads exceed 32-bit units", B, table_stride, D->h_kv);
     if ((long long)D->n_total_blocks * D->h_kv * (D->block_size / kQ4Tile) > INT32_MAX)
         return fail(ZP_ERR_SHAPE, "q4_decode: %d blocks of %d tokens and %d heads exceed 32-bit tiles", D->n_total_blocks,
                     D->block_size, D->h_kv);

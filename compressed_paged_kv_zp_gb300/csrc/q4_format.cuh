@@ -29,43 +29,65 @@ __host__ __device__ __forceinline__ int q4_chunk(int t, int c) {
     return D == 128 ? (c ^ ((t >> 1) & 3)) : (c ^ ((t >> 2) & 1));
 }
 
-// bf16 bits of the largest bf16 value not above x, and of the smallest not below it
-// (x not NaN; a result past the largest finite value is an infinity).
+// bf16 bits of the largest bf16 value not above x (x not NaN).
 __device__ __forceinline__ uint32_t bf16_below(float x) {
     const uint32_t u = __float_as_uint(x);
     return ((u & 0xFFFFu) && (u >> 31) ? u + 0x10000u : u) >> 16;
 }
-__device__ __forceinline__ uint32_t bf16_above(float x) {
-    const uint32_t u = __float_as_uint(x);
-    return ((u & 0xFFFFu) && !(u >> 31) ? u + 0x10000u : u) >> 16;
-}
 
 // The word (step, lo) of a group whose smallest and largest element are mn and mx
 // (NaN if one of its elements is): lo is the bf16 value at or below mn, the step the
-// bf16 value at or above a fifteenth of mx - lo, so that fifteen steps reach mx and no
-// element is further than half a step from its code's value.  For bf16 elements lo is
-// mn itself.  The step is at least 2^-126 (its reciprocal is finite).
+// smallest bf16 value of which fifteen reach from lo to mx, so that no element is further than
+// half a step from its code's value.  For bf16 elements lo is mn itself.  The step is at
+// least 2^-126 (its reciprocal is finite).
 __device__ __forceinline__ uint32_t q4_params(float mn, float mx) {
     const uint32_t lo = bf16_below(mn);
-    const float flo = __uint_as_float(lo << 16);
-    const float step = fmaxf(__uint_as_float(bf16_above(__fdiv_rn(mx - flo, 15.f)) << 16), __uint_as_float(0x00800000u));
-    const bool finite = fabsf(flo) < INFINITY && step < INFINITY && mx - flo < INFINITY;  // (a NaN compares false)
+    const float flo = __uint_as_float(lo << 16), spread = mx - flo;
+    // a fifteenth, a little too large (0x3D88888B is 2.8e-7 above 1/15), cut to bf16: the answer or the value below it
+    uint32_t s = __float_as_uint(spread * __uint_as_float(0x3D88888Bu)) & 0xFFFF0000u;
+    if (15.f * __uint_as_float(s) < spread) s += 0x10000u;  // (15 s has 12 bits)
+    const float step = fmaxf(__uint_as_float(s), __uint_as_float(0x00800000u));
+    const bool finite = fabsf(flo) < INFINITY && spread < INFINITY;  // (a NaN compares false)
     return finite ? (__float_as_uint(step) >> 16) | (lo << 16) : kQ4NaN;
 }
 
-// Code of x in a group with (step, lo): floor((x - lo) / step + 1/2), the quotient not
-// rounded.  r is a reciprocal of the step a little too small, so that t's integer k is
-// the code or one less; x - lo - k * step is exact (k * step has 12 bits, the difference
-// at most half a step) and tells which.  half = step / 2.
-__device__ __forceinline__ uint32_t q4_code(float x, float lo, float step, float r, float half) {
-    const float d = x - lo;
-    const float t = fmaf(d, r, 12582912.f);  // 1.5 * 2^23: the integer in the low bits
-    const float rest = fmaf(-(t - 12582912.f), step, d);
-    return __float_as_uint(t) + (rest >= half ? 1u : 0u);  // the caller keeps the low 4 bits
+// ---- codes: of x in a group with (step, lo), floor((x - lo) / step + 1/2), the quotient not
+// rounded.  r is a reciprocal of the step too small by 2^-20 or so, so that k, (x - lo) * r
+// rounded, is the code or one less; (k + 1/2) * step is exact (13 bits) and tells which.
+__device__ __forceinline__ float q4_small_reciprocal(float step) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(step));  // off by 2^-23 at most
+    return r * (1.f - 9.5367431640625e-7f);
 }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
+    return *reinterpret_cast<float2 *>(&r);
+}
+__device__ __forceinline__ float at_least(float a, float b) {  // 1 where a >= b, else 0
+    float r;
+    asm("set.ge.f32.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-__device__ __forceinline__ float q4_shrunk_reciprocal(float step) {
-    return __fmul_rn(__frcp_rn(step), 1.f - 9.5367431640625e-7f);  // 1 - 2^-20
+// Codes of two elements, as floats.
+__device__ __forceinline__ float2 q4_code2(float2 x, float lo, float step, float r, float half) {
+    const float2 d = add2(x, both(-lo));
+    const float2 k = add2(ffma2(d, both(r), both(12582912.f)), both(-12582912.f));  // 1.5 * 2^23: rounds to a whole number
+    const float2 edge = ffma2(k, both(step), both(half));
+    return add2(k, make_float2(at_least(d.x, edge.x), at_least(d.y, edge.y)));
+}
+// Eight whole numbers of 0 to 15, of two words, as the nibbles of those (four make a
+// number below 2^16, which 2^23 shows as the low bits).
+__device__ __forceinline__ uint2 q4_join(const float2 (&k)[8]) {
+    float2 x[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        x[h] = add2(ffma2(k[4 * h + 3], both(4096.f), ffma2(k[4 * h + 2], both(256.f), ffma2(k[4 * h + 1], both(16.f), k[4 * h]))),
+                    both(8388608.f));
+    return make_uint2(__byte_perm(__float_as_uint(x[0].x), __float_as_uint(x[1].x), 0x5410),
+                      __byte_perm(__float_as_uint(x[0].y), __float_as_uint(x[1].y), 0x5410));
 }
 
 // Host: arguments that every call on a 4-bit cache has.

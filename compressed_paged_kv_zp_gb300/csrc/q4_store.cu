@@ -10,10 +10,11 @@ namespace zp {
 namespace {
 
 // ---------------------------------------------------------------- rows in
-// Eight elements of a row per thread (one 16-byte load in bf16, two in fp32): a group of
-// 32 is four lanes, its extremes two shuffles away, and a thread's eight codes are one
-// 32-bit word, so the 16 lanes of a row of 128 write its 64 bytes side by side.
-constexpr int kStoreThreads = 256, kStoreUnroll = 2;
+// Sixteen elements of a row per thread (32 bytes in bf16, 64 in fp32): a group of 32 is two
+// lanes, its extremes one shuffle away, its parameters are worked out for 16 elements at a
+// time, and a thread's codes are 8 bytes, so the 8 lanes of a row of 128 write its 64 bytes
+// side by side.  A thread keeps its place in the row and walks over tokens.
+constexpr int kStoreThreads = 256, kPiece = 16;
 
 __device__ __forceinline__ float min_nan(float a, float b) {
     float r;
@@ -25,76 +26,146 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
+__device__ __forceinline__ uint32_t min_nan2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t max_nan2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 
-template <typename T> struct Piece;  // eight elements
-template <> struct Piece<__nv_bfloat16> {
-    uint4 w;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { w = __ldg(reinterpret_cast<const uint4 *>(p)); }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = bf2_to_f2(u[i]);
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
-        }
+// 32 bytes; in one access where the rows are 32-byte aligned
+__device__ __forceinline__ void load32(uint32_t (&w)[8], const void *p, bool wide) {
+    if (wide) {
+        asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+            : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+            : "l"(p));
+    } else {
+        const uint4 x = __ldg(static_cast<const uint4 *>(p)), y = __ldg(static_cast<const uint4 *>(p) + 1);
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w, w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
     }
-    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&x)[8]) {
-        *reinterpret_cast<uint4 *>(p) = make_uint4(f2_to_bf2(x[0], x[1]), f2_to_bf2(x[2], x[3]), f2_to_bf2(x[4], x[5]),
-                                                   f2_to_bf2(x[6], x[7]));
+}
+__device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8], bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        static_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+template <typename T> struct Piece;  // sixteen elements
+template <> struct Piece<__nv_bfloat16> {
+    uint32_t w[8];
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p, bool wide) { load32(w, p, wide); }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ float get(int i) const {
+        return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    }
+    __device__ __forceinline__ void extremes(float &mn, float &mx) const {
+        uint32_t a = w[0], b = w[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) a = min_nan2(a, w[i]), b = max_nan2(b, w[i]);
+        const float2 x = bf2_to_f2(a), y = bf2_to_f2(b);
+        mn = min_nan(x.x, x.y);
+        mx = max_nan(y.x, y.y);
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&x)[16], bool wide) {
+        uint32_t o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = f2_to_bf2(x[2 * i], x[2 * i + 1]);
+        store32(p, o, wide);
     }
 };
 template <> struct Piece<float> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const float *p) {
-        a = __ldg(reinterpret_cast<const float4 *>(p));
-        b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    uint32_t a[8], b[8];
+    __device__ __forceinline__ void load(const float *p, bool wide) {
+        load32(a, p, wide);
+        load32(b, p + 8, wide);
     }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[i] = b[i] = 0;
     }
-    static __device__ __forceinline__ void store(float *p, const float (&x)[8]) {
-        reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-        reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    __device__ __forceinline__ float get(int i) const { return __uint_as_float(i < 8 ? a[i & 7] : b[i & 7]); }
+    __device__ __forceinline__ void extremes(float &mn, float &mx) const {
+        mn = mx = get(0);
+#pragma unroll
+        for (int i = 1; i < 16; ++i) mn = min_nan(mn, get(i)), mx = max_nan(mx, get(i));
+    }
+    static __device__ __forceinline__ void store(float *p, const float (&x)[16], bool wide) {
+        uint32_t o[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(x[8 * h + i]);
+            store32(p + 8 * h, o, wide);
+        }
     }
 };
 
-struct StoreArgs {
-    const void *k, *v;                       // rows given
-    long long token_stride, new_layer_stride;  // elements
-    unsigned char *K, *V;
-    long long layer_bytes;
-    const int32_t *slots;                    // write; append: nullptr
-    const int32_t *table, *seq_lens;         // append
-    int table_stride;
-    int n_tokens, tokens_per_cta;
-    int h_kv, b, lg_group, tile;
-    int row_pieces;                          // h_kv * d / 8
-    unsigned inv_row;                        // ceil(2^32 / row_pieces)
+// What the calls that go over rows share.  A CTA has lanes_n threads for each of `at_once`
+// tokens at a time (a thread for every kPiece elements of a row, or fewer where a row has more
+// than kStoreThreads of them) and takes tokens_per_cta in all.
+struct RowArgs {
+    int n_tokens, tokens_per_cta, at_once, lanes_n;
+    int h_kv, lg_group, tile;
+    int row_pieces;                   // h_kv * d / kPiece
+    int tpb;                          // tiles per block and kv head
+    unsigned inv_lanes, inv_tpb;      // reciprocals, rounded up, of 2^32 (0: the divisor is 1)
     long long n_slots;
+    bool wide;                        // rows aligned to 32 bytes
     unsigned *err;
 };
 
-// slot of token i (-1: none); the caller's token is within range
+// Tile of slot's row of kv head h: ((slot / b) * h_kv + h) * (b / 16) + slot % b / 16.
+__device__ __forceinline__ size_t tile_offset(const RowArgs &a, int slot, int h) {
+    const unsigned t = (unsigned)slot / kQ4Tile;  // below 2^27; the reciprocal is exact as far as that
+    unsigned blk = t;
+    if (a.inv_tpb) {
+        blk = __umulhi(t, a.inv_tpb);
+        if (blk * a.tpb > t) --blk;  // (rounded up: one too many at most)
+    }
+    return (((size_t)blk * a.h_kv + h) * a.tpb + (t - blk * a.tpb)) * a.tile;
+}
+
+struct StoreArgs : RowArgs {
+    const void *k, *v;                         // rows given
+    long long token_stride, new_layer_stride;  // elements
+    unsigned char *K, *V;
+    long long layer_bytes;
+    const int32_t *slots;             // write; append: nullptr
+    const int32_t *table, *seq_lens;  // append
+    int table_stride;
+};
+
+// slot of token i, -1: none
 template <bool APPEND>
-__device__ __forceinline__ long long store_slot(const StoreArgs &a, int i) {
+__device__ __forceinline__ int store_slot(const StoreArgs &a, int i) {
     if constexpr (APPEND) {
-        const int L = __ldg(a.seq_lens + i);
+        const int L = __ldg(a.seq_lens + i), b = a.tpb * kQ4Tile;
         if (L == 0) return -1;  // no token for this sequence in this step
-        if (L < 0 || L > (long long)a.table_stride * a.b) {
+        if (L < 0 || L > (long long)a.table_stride * b) {
             record_error(a.err, ZP_ERR_DEVICE, 0x151);
             return -1;
         }
         const int P = L - 1;
-        const long long blk = __ldg(a.table + (size_t)i * a.table_stride + P / a.b);
-        if (blk < 0 || (blk + 1) * a.b > a.n_slots) {
+        const long long blk = __ldg(a.table + (size_t)i * a.table_stride + P / b);
+        if (blk < 0 || (blk + 1) * b > a.n_slots) {
             record_error(a.err, ZP_ERR_DEVICE, 0x152);
             return -1;
         }
-        return blk * a.b + P % a.b;
+        return (int)(blk * b + P % b);
     } else {
-        const long long slot = __ldg(a.slots + i);
+        const int slot = __ldg(a.slots + i);
         if (slot >= a.n_slots) {
             record_error(a.err, ZP_ERR_DEVICE, 0x150);
             return -1;
@@ -103,135 +174,138 @@ __device__ __forceinline__ long long store_slot(const StoreArgs &a, int i) {
     }
 }
 
-// tile of (slot, kv head), and the row inside it
-__device__ __forceinline__ size_t tile_offset(long long slot, int h, int h_kv, int b, int tile) {
-    const int sl = (int)slot, blk = sl / b, in = sl - blk * b;
-    return (((size_t)blk * h_kv + h) * (b / kQ4Tile) + in / kQ4Tile) * tile;
-}
-
-template <typename T, int D, bool APPEND>
+template <typename T, int D, bool APPEND, int U>
 __global__ void __launch_bounds__(kStoreThreads) q4_store_kernel(const StoreArgs a) {
-    constexpr int kPieces = D / 8;  // per row
+    constexpr int kPieces = D / kPiece;  // per row of a head
     const T *src = static_cast<const T *>(blockIdx.z ? a.v : a.k) + (long long)blockIdx.y * a.new_layer_stride;
     unsigned char *dst = (blockIdx.z ? a.V : a.K) + (long long)blockIdx.y * a.layer_bytes;
-    const int first = blockIdx.x * a.tokens_per_cta;
-    const int n = min(a.tokens_per_cta, a.n_tokens - first) * a.row_pieces;
-    const int group_lanes = 1 << (a.lg_group - 3);
-    for (int base = 0; base < n; base += kStoreThreads * kStoreUnroll) {
-        Piece<T> in[kStoreUnroll];
-        long long slot[kStoreUnroll];
-        int head[kStoreUnroll], piece[kStoreUnroll];
+    const int tok = a.inv_lanes ? (int)__umulhi(threadIdx.x, a.inv_lanes) : (int)threadIdx.x;
+    const int first = blockIdx.x * a.tokens_per_cta + tok, last = min(a.n_tokens, ((int)blockIdx.x + 1) * a.tokens_per_cta);
+    const int group_lanes = 1 << (a.lg_group - 4);
+    // (every thread goes as often round as the first: the shuffles are the whole warp's)
+    for (int c0 = 0; c0 < a.row_pieces; c0 += a.lanes_n) {
+        const int c = c0 + threadIdx.x - tok * a.lanes_n, head = c / kPieces, piece = c % kPieces;
+        const bool works = tok < a.at_once && c < a.row_pieces;
+        for (int i0 = first; i0 - tok < last; i0 += U * a.at_once) {
+            Piece<T> in[U];
+            int slot[U];
 #pragma unroll
-        for (int u = 0; u < kStoreUnroll; ++u) {
-            const int v = base + u * kStoreThreads + threadIdx.x;
-            slot[u] = -1;
-            if (v < n) {
-                const int i = __umulhi((unsigned)v, a.inv_row);
-                const int c = v - i * a.row_pieces;
-                in[u].load(src + (long long)(first + i) * a.token_stride + c * 8);
-                slot[u] = store_slot<APPEND>(a, first + i);
-                head[u] = c / kPieces;
-                piece[u] = c % kPieces;
-            } else {
-                in[u] = Piece<T>{};
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * a.at_once;
+                slot[u] = -1;
+                if (works && i < last) {
+                    in[u].load(src + (long long)i * a.token_stride + c * kPiece, a.wide);
+                    slot[u] = store_slot<APPEND>(a, i);
+                } else {
+                    in[u].clear();
+                }
             }
-        }
 #pragma unroll
-        for (int u = 0; u < kStoreUnroll; ++u) {
-            float x[8];
-            in[u].get(x);
-            float mn = min_nan(min_nan(min_nan(x[0], x[1]), min_nan(x[2], x[3])), min_nan(min_nan(x[4], x[5]), min_nan(x[6], x[7])));
-            float mx = max_nan(max_nan(max_nan(x[0], x[1]), max_nan(x[2], x[3])), max_nan(max_nan(x[4], x[5]), max_nan(x[6], x[7])));
-            for (int o = 1; o < group_lanes; o <<= 1) {
-                mn = min_nan(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, o));
-                mx = max_nan(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-            }
-            const uint32_t par = q4_params(mn, mx);
-            const float step = __uint_as_float(par << 16), lo = __uint_as_float(par & 0xFFFF0000u);
-            const float r = q4_shrunk_reciprocal(step), half = 0.5f * step;
-            uint32_t word = 0;
+            for (int u = 0; u < U; ++u) {
+                float mn, mx;
+                in[u].extremes(mn, mx);
+                for (int o = 1; o < group_lanes; o <<= 1) {
+                    mn = min_nan(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, o));
+                    mx = max_nan(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+                }
+                const uint32_t par = q4_params(mn, mx);
+                const float step = __uint_as_float(par << 16), lo = __uint_as_float(par & 0xFFFF0000u);
+                const float r = q4_small_reciprocal(step), half = 0.5f * step;
+                float2 k[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) word |= (q4_code(x[j], lo, step, r, half) & 15u) << (4 * j);
-            if (par == kQ4NaN) word = 0;
-            if (slot[u] >= 0) {
-                const int t = (int)slot[u] % kQ4Tile;
-                unsigned char *tile = dst + tile_offset(slot[u], head[u], a.h_kv, a.b, a.tile);
-                *reinterpret_cast<uint32_t *>(tile + t * (D / 2) + q4_chunk<D>(t, piece[u] / 4) * 16 + piece[u] % 4 * 4) = word;
-                if (piece[u] % group_lanes == 0)
-                    reinterpret_cast<uint32_t *>(tile + q4_code_bytes(D))[t * (D >> a.lg_group) + (piece[u] * 8 >> a.lg_group)] = par;
+                for (int j = 0; j < 8; ++j) k[j] = q4_code2(make_float2(in[u].get(j), in[u].get(j + 8)), lo, step, r, half);
+                uint2 word = q4_join(k);
+                if (par == kQ4NaN) word = make_uint2(0, 0);
+                if (slot[u] < 0) continue;
+                const int t = slot[u] % kQ4Tile;
+                unsigned char *tile = dst + tile_offset(a, slot[u], head);
+                *reinterpret_cast<uint2 *>(tile + t * (D / 2) + q4_chunk<D>(t, piece / 2) * 16 + piece % 2 * 8) = word;
+                if (piece % group_lanes == 0)
+                    reinterpret_cast<uint32_t *>(tile + q4_code_bytes(D))[t * (D >> a.lg_group) + (piece * kPiece >> a.lg_group)] = par;
             }
         }
     }
 }
 
 // ---------------------------------------------------------------- rows out
-constexpr int kReadUnroll = 4;
-
-struct ReadArgs {
+struct ReadArgs : RowArgs {
     const unsigned char *K, *V;
     long long layer_bytes;
     const int32_t *slots;
     void *k, *v;
     long long token_stride, out_layer_stride;  // elements
-    int n_tokens, tokens_per_cta;
-    int h_kv, b, lg_group, tile;
-    int row_pieces;
-    unsigned inv_row;
-    long long n_slots;
-    unsigned *err;
 };
 
-template <typename T, int D>
+template <typename T, int D, int U>
 __global__ void __launch_bounds__(kStoreThreads) q4_read_kernel(const ReadArgs a) {
-    constexpr int kPieces = D / 8;
+    constexpr int kPieces = D / kPiece;
     const unsigned char *src = (blockIdx.z ? a.V : a.K) + (long long)blockIdx.y * a.layer_bytes;
     T *dst = static_cast<T *>(blockIdx.z ? a.v : a.k) + (long long)blockIdx.y * a.out_layer_stride;
-    const int first = blockIdx.x * a.tokens_per_cta;
-    const int n = min(a.tokens_per_cta, a.n_tokens - first) * a.row_pieces;
-    for (int base = 0; base < n; base += kStoreThreads * kReadUnroll) {
-        uint32_t word[kReadUnroll], par[kReadUnroll];
-        T *to[kReadUnroll];
+    const int tok = a.inv_lanes ? (int)__umulhi(threadIdx.x, a.inv_lanes) : (int)threadIdx.x;
+    if (tok >= a.at_once) return;
+    const int first = blockIdx.x * a.tokens_per_cta + tok, last = min(a.n_tokens, ((int)blockIdx.x + 1) * a.tokens_per_cta);
+    for (int c = threadIdx.x - tok * a.lanes_n; c < a.row_pieces; c += a.lanes_n) {
+        const int head = c / kPieces, piece = c % kPieces;
+        for (int i0 = first; i0 < last; i0 += U * a.at_once) {
+            uint2 word[U];
+            uint32_t par[U];
+            int slot[U];
 #pragma unroll
-        for (int u = 0; u < kReadUnroll; ++u) {
-            const int v = base + u * kStoreThreads + threadIdx.x;
-            to[u] = nullptr;
-            if (v < n) {
-                const int i = __umulhi((unsigned)v, a.inv_row);
-                const int c = v - i * a.row_pieces;
-                const long long slot = __ldg(a.slots + first + i);
-                if (slot >= 0 && slot < a.n_slots) {
-                    const int piece = c % kPieces, t = (int)slot % kQ4Tile;
-                    const unsigned char *tile = src + tile_offset(slot, c / kPieces, a.h_kv, a.b, a.tile);
-                    word[u] = __ldg(reinterpret_cast<const uint32_t *>(tile + t * (D / 2) + q4_chunk<D>(t, piece / 4) * 16 +
-                                                                       piece % 4 * 4));
-                    par[u] = __ldg(reinterpret_cast<const uint32_t *>(tile + q4_code_bytes(D)) + t * (D >> a.lg_group) +
-                                   (piece * 8 >> a.lg_group));
-                    to[u] = dst + (long long)(first + i) * a.token_stride + c * 8;
-                } else if (slot >= 0) {
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * a.at_once;
+                slot[u] = i < last ? __ldg(a.slots + i) : -1;
+                if (slot[u] >= a.n_slots) {
                     record_error(a.err, ZP_ERR_DEVICE, 0x153);
+                    slot[u] = -1;
                 }
             }
-        }
 #pragma unroll
-        for (int u = 0; u < kReadUnroll; ++u) {
-            if (!to[u]) continue;
-            const float step = __uint_as_float(par[u] << 16), lo = __uint_as_float(par[u] & 0xFFFF0000u);
-            float x[8];
+            for (int u = 0; u < U; ++u) {
+                if (slot[u] < 0) continue;
+                const int t = slot[u] % kQ4Tile;
+                const unsigned char *tile = src + tile_offset(a, slot[u], head);
+                word[u] = __ldg(reinterpret_cast<const uint2 *>(tile + t * (D / 2) + q4_chunk<D>(t, piece / 2) * 16 + piece % 2 * 8));
+                par[u] = __ldg(reinterpret_cast<const uint32_t *>(tile + q4_code_bytes(D)) + t * (D >> a.lg_group) +
+                               (piece * kPiece >> a.lg_group));
+            }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = fmaf((float)(word[u] >> (4 * j) & 15u), step, lo);
-            Piece<T>::store(to[u], x);
+            for (int u = 0; u < U; ++u) {
+                if (slot[u] < 0) continue;
+                const float step = __uint_as_float(par[u] << 16), lo = __uint_as_float(par[u] & 0xFFFF0000u);
+                float x[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const uint32_t w = j < 8 ? word[u].x : word[u].y;
+                    const float code = __uint_as_float((w >> (4 * (j & 7)) & 15u) | 0x4B000000u) - 8388608.f;  // 2^23 + c, exact
+                    x[j] = fmaf(code, step, lo);
+                }
+                Piece<T>::store(dst + (long long)(i0 + u * a.at_once) * a.token_stride + c * kPiece, x, a.wide);
+            }
         }
     }
 }
 
 // ---------------------------------------------------------------- moves
-// One CTA per (tensor, kv head, sequence, layer), as in compact.cu: the CTA resolves every
-// rank's source and target, then moves up to kMoveChunk ranks at a time: all its row
-// pieces (16-byte chunks of codes, 4-byte words of parameters) into registers, a barrier,
-// all out.  A chunk reads positions >= its first rank and earlier chunks wrote slots below
-// it, and a slot that a source and a target share has the same index in both (the
-// target rule): the move is right in place too.
-constexpr int kMoveThreads = 1024, kMoveChunk = 2048;
+// One CTA per (tensor, kv head, sequence, layer) moves its ranks in rounds of kMoveRanks (a thread each) through
+// a ring in shared memory: asynchronous copies in, kMoveStages - 1 rounds ahead, plain stores out.
+// Round i is stored once all of its copies have arrived.  Its stores go to slots below the ranks of
+// later rounds, whose sources are at or above those ranks, and a slot that a source and a
+// target share has the same index in both (the target rule): later rounds may be read ahead of
+// earlier stores, and the move is right in place too.  A row in flight costs no registers that way,
+// and the look-ups (position, then block) run a round or two ahead of the copies.
+constexpr int kMoveStages = 4;
+
+__device__ __forceinline__ void copy_async(void *to, const void *from, int bytes) {  // 4, 8 or 16
+    const uint32_t at = smem_u32(to);
+    if (bytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+    else if (bytes == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at), "l"(from) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 struct MoveArgs {
     unsigned char *K, *V;
@@ -251,17 +325,23 @@ struct MoveArgs {
     unsigned *err;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kMoveThreads, 1) q4_compact_kernel(const MoveArgs a) {
-    constexpr int kChunks = D / 32, kPer = kMoveChunk * kChunks / kMoveThreads;  // 16-byte pieces per thread and round
-    __shared__ int s_from[kMoveChunk], s_to[kMoveChunk];  // tile * 16 + row, -1: skipped
-    const int kvh = blockIdx.x >> 1, tensor = blockIdx.x & 1, s = blockIdx.y, layer = blockIdx.z, tid = threadIdx.x;
+// A stage: codes [ranks][d/2], parameters [ranks][words], F values [ranks], 1 where the rank moves [ranks].
+__host__ __device__ constexpr int move_stage_bytes(int ranks, int d, int words) { return ranks * (d / 2 + 4 * words + 8); }
+
+template <int D, int kMoveRanks>
+__global__ void __launch_bounds__(kMoveRanks) q4_compact_kernel(const MoveArgs a) {
+    constexpr int kChunks = D / 32, kRows = 32 / kChunks;  // rows that a warp copies at a time
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int kvh = blockIdx.x >> 1, tensor = blockIdx.x & 1, s = blockIdx.y, layer = blockIdx.z;
+    const int tid = threadIdx.x, lane = tid & 31, warp0 = tid & ~31;
+    const int words = 1 << a.lg_words, stage_bytes = move_stage_bytes(kMoveRanks, D, words), tpb = a.b / kQ4Tile;
     const int32_t *kp = a.keep + (((size_t)layer * a.n + s) * a.h_kv + kvh) * a.k;
+    const int32_t *table = a.src_table + (size_t)s * a.table_stride, *dst = a.dst + (size_t)s * a.target_stride;
     unsigned char *X = (tensor ? a.V : a.K) + layer * a.layer_bytes;
     float *F = a.F && tensor == 0 ? a.F + layer * a.F_layer_stride : nullptr;
     const float *Srow = nullptr;
-    int L = __ldg(a.seq_lens + s);
-    if (L > (long long)a.table_stride * a.b) L = a.table_stride * a.b;
+    int pos_b = tid < a.k ? __ldg(kp + tid) : -1, pos_c = tid + kMoveRanks < a.k ? __ldg(kp + tid + kMoveRanks) : -1;
+    int L = (int)min((long long)__ldg(a.seq_lens + s), (long long)a.table_stride * a.b);
     if (F) {
         const int row = a.S_rows ? __ldg(a.S_rows + s) : s;
         if (row < 0) {
@@ -273,60 +353,74 @@ __global__ void __launch_bounds__(kMoveThreads, 1) q4_compact_kernel(const MoveA
         }
     }
     const int kk = min(a.k_seq ? min(__ldg(a.k_seq + s), a.k) : a.k, L);
-    const int tpb = a.b / kQ4Tile;
-    for (int r0 = 0; r0 < kk; r0 += kMoveChunk) {
-        const int nr = min(kMoveChunk, kk - r0);
-        for (int i = tid; i < nr; i += kMoveThreads) {
-            const int r = r0 + i, pos = __ldg(kp + r);
-            int from = -1, to = -1, blk = -1;
-            if (pos >= 0 && pos < L) blk = __ldg(a.src_table + (size_t)s * a.table_stride + pos / a.b);
-            const int target = __ldg(a.dst + (size_t)s * a.target_stride + r / a.b);
-            if (blk < 0 || blk >= a.n_total) record_error(a.err, ZP_ERR_DEVICE, 0x154);
-            else from = ((blk * a.h_kv + kvh) * tpb + pos % a.b / kQ4Tile) * kQ4Tile + pos % kQ4Tile;
-            if (target < 0 || target >= a.n_total) record_error(a.err, ZP_ERR_DEVICE, 0x155);
-            else to = ((target * a.h_kv + kvh) * tpb + r % a.b / kQ4Tile) * kQ4Tile + r % kQ4Tile;
-            if (to < 0) from = -1;
-            s_from[i] = from;
-            s_to[i] = to;
-            if (F && from >= 0) F[((size_t)target * a.b + r % a.b) * a.h_kv + kvh] = Srow[pos];
-        }
-        __syncthreads();
-        uint4 code[kPer];
-        uint32_t par[kMoveChunk * kQ4MaxGroups / kMoveThreads];
+    const int rounds = (kk + kMoveRanks - 1) / kMoveRanks;
+    auto block_of = [&](int pos) { return pos >= 0 && pos < L ? __ldg(table + pos / a.b) : -1; };
+    int pos = pos_b, blk = block_of(pos_b);  // of the next round to copy
+    pos_b = pos_c;                           // of the one behind it
+    // the copies of round i: lane l looks rank r up, kChunks lanes copy a row's codes
+    auto copy = [&](int i) {
+        if (i < rounds) {
+            unsigned char *stage = smem + (i % kMoveStages) * stage_bytes;
+            unsigned char *par = stage + kMoveRanks * (D / 2);
+            float *f = reinterpret_cast<float *>(par + kMoveRanks * 4 * words);
+            int *moves = reinterpret_cast<int *>(f + kMoveRanks);
+            const int r = i * kMoveRanks + tid;
+            int from = -1;  // tile * 16 + row
+            if (r < kk) {
+                if (blk < 0 || blk >= a.n_total) record_error(a.err, ZP_ERR_DEVICE, 0x154);
+                else from = ((blk * a.h_kv + kvh) * tpb + pos % a.b / kQ4Tile) * kQ4Tile + pos % kQ4Tile;
+            }
+            moves[tid] = from >= 0;
+            if (from >= 0) {
+                copy_async(par + tid * 4 * words, X + (size_t)(from / kQ4Tile) * a.tile + q4_code_bytes(D) + from % kQ4Tile * 4 * words,
+                           4 * words);
+                if (F) copy_async(f + tid, Srow + pos, 4);
+            }
 #pragma unroll
-        for (int u = 0; u < kPer; ++u) {
-            const int it = tid + u * kMoveThreads, i = it / kChunks;
-            if (i < nr && s_from[i] >= 0) {
-                const int t = s_from[i] % kQ4Tile;
-                code[u] = *reinterpret_cast<const uint4 *>(X + (size_t)(s_from[i] / kQ4Tile) * a.tile + t * (D / 2) +
-                                                           q4_chunk<D>(t, it % kChunks) * 16);
+            for (int u = 0; u < kChunks; ++u) {
+                const int row = u * kRows + lane / kChunks, x = __shfl_sync(0xFFFFFFFFu, from, row), c = lane % kChunks;
+                if (x >= 0)
+                    copy_async(stage + (warp0 + row) * (D / 2) + c * 16,
+                               X + (size_t)(x / kQ4Tile) * a.tile + x % kQ4Tile * (D / 2) + q4_chunk<D>(x % kQ4Tile, c) * 16, 16);
+            }
+            pos = pos_b;
+            blk = block_of(pos_b);
+            const int far = r + 2 * kMoveRanks;
+            pos_b = far < a.k ? __ldg(kp + far) : -1;
+        }
+        copies_commit();
+    };
+    for (int i = 0; i < kMoveStages - 1; ++i) copy(i);
+    for (int i = 0; i < rounds; ++i) {
+        copies_wait<kMoveStages - 2>();
+        __syncthreads();  // round i is here, and round i - 1 has been stored: its stage is free
+        copy(i + kMoveStages - 1);
+        const unsigned char *stage = smem + (i % kMoveStages) * stage_bytes;
+        const unsigned char *par = stage + kMoveRanks * (D / 2);
+        const float *f = reinterpret_cast<const float *>(par + kMoveRanks * 4 * words);
+        const int *moves = reinterpret_cast<const int *>(f + kMoveRanks);
+        const int r = i * kMoveRanks + tid;
+        int to = -1;
+        if (r < kk) {
+            const int target = __ldg(dst + r / a.b);
+            if (target < 0 || target >= a.n_total) {
+                record_error(a.err, ZP_ERR_DEVICE, 0x155);
+            } else if (moves[tid]) {
+                to = ((target * a.h_kv + kvh) * tpb + r % a.b / kQ4Tile) * kQ4Tile + r % kQ4Tile;
+                unsigned char *at = X + (size_t)(to / kQ4Tile) * a.tile + q4_code_bytes(D) + to % kQ4Tile * 4 * words;
+                if (words == 4) *reinterpret_cast<uint4 *>(at) = reinterpret_cast<const uint4 *>(par)[tid];
+                else if (words == 2) *reinterpret_cast<uint2 *>(at) = reinterpret_cast<const uint2 *>(par)[tid];
+                else *reinterpret_cast<uint32_t *>(at) = reinterpret_cast<const uint32_t *>(par)[tid];
+                if (F) F[((size_t)target * a.b + r % a.b) * a.h_kv + kvh] = f[tid];
             }
         }
 #pragma unroll
-        for (int u = 0; u < kMoveChunk * kQ4MaxGroups / kMoveThreads; ++u) {
-            const int it = tid + u * kMoveThreads, i = it >> a.lg_words;
-            if (i < nr && s_from[i] >= 0)
-                par[u] = reinterpret_cast<const uint32_t *>(X + (size_t)(s_from[i] / kQ4Tile) * a.tile + q4_code_bytes(D))
-                    [((s_from[i] % kQ4Tile) << a.lg_words) + (it & ((1 << a.lg_words) - 1))];
+        for (int u = 0; u < kChunks; ++u) {
+            const int row = u * kRows + lane / kChunks, x = __shfl_sync(0xFFFFFFFFu, to, row), c = lane % kChunks;
+            if (x >= 0)
+                *reinterpret_cast<uint4 *>(X + (size_t)(x / kQ4Tile) * a.tile + x % kQ4Tile * (D / 2) + q4_chunk<D>(x % kQ4Tile, c) * 16) =
+                    *reinterpret_cast<const uint4 *>(stage + (warp0 + row) * (D / 2) + c * 16);
         }
-        __syncthreads();
-#pragma unroll
-        for (int u = 0; u < kPer; ++u) {
-            const int it = tid + u * kMoveThreads, i = it / kChunks;
-            if (i < nr && s_from[i] >= 0) {
-                const int t = s_to[i] % kQ4Tile;
-                *reinterpret_cast<uint4 *>(X + (size_t)(s_to[i] / kQ4Tile) * a.tile + t * (D / 2) +
-                                           q4_chunk<D>(t, it % kChunks) * 16) = code[u];
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kMoveChunk * kQ4MaxGroups / kMoveThreads; ++u) {
-            const int it = tid + u * kMoveThreads, i = it >> a.lg_words;
-            if (i < nr && s_from[i] >= 0)
-                reinterpret_cast<uint32_t *>(X + (size_t)(s_to[i] / kQ4Tile) * a.tile + q4_code_bytes(D))
-                    [((s_to[i] % kQ4Tile) << a.lg_words) + (it & ((1 << a.lg_words) - 1))] = par[u];
-        }
-        __syncthreads();  // the next round's loads follow this round's stores
     }
 }
 
@@ -335,9 +429,6 @@ int log2_of(int x) {
     while ((1 << n) < x) ++n;
     return n;
 }
-
-// Tokens per CTA so that one has about `pieces` pieces.
-int tokens_per_cta(int row_pieces, int pieces) { return row_pieces >= pieces ? 1 : pieces / row_pieces; }
 
 zp_status check_rows(const zp_cache_desc *D, int group, const char *what, const void *k, const void *v, int64_t token_stride,
                      int64_t rows_layer_stride, int32_t layer_count, const void *K, const void *V, int64_t layer_stride) {
@@ -356,30 +447,48 @@ zp_status check_rows(const zp_cache_desc *D, int group, const char *what, const 
     return ZP_OK;
 }
 
-template <typename A>
-void fill_shape(A &a, const zp_cache_desc *D, int group, int n_tokens, int pieces, const DeviceInfo &dev) {
+// Bits that the addresses of rows have in common with their strides.
+uintptr_t row_alignment(const zp_cache_desc *D, const void *k, const void *v, int64_t token_stride, int64_t layer_stride) {
+    const int64_t es = elem_bytes(D->dtype);
+    return (uintptr_t)k | (uintptr_t)v | (uintptr_t)(token_stride * es) | (uintptr_t)(layer_stride * es);
+}
+
+unsigned reciprocal(int x) { return x == 1 ? 0 : (unsigned)((0x100000000ull + x - 1) / x); }
+
+// The split of n_tokens rows (of `layers` layers, keys and values) over CTAs whose threads
+// take U tokens at a time.
+void fill_rows(RowArgs &a, const zp_cache_desc *D, int group, int n_tokens, int U, uintptr_t aligned, const DeviceInfo &dev) {
     a.n_tokens = n_tokens;
+    a.row_pieces = D->h_kv * D->head_dim / kPiece;
+    a.lanes_n = a.row_pieces < kStoreThreads ? a.row_pieces : kStoreThreads;
+    a.at_once = kStoreThreads / a.lanes_n;
+    a.tokens_per_cta = a.at_once * U;
     a.h_kv = D->h_kv;
-    a.b = D->block_size;
     a.lg_group = log2_of(group);
     a.tile = q4_tile_bytes(D->head_dim, group);
-    a.row_pieces = D->h_kv * D->head_dim / 8;
-    a.inv_row = (unsigned)((0x100000000ull + a.row_pieces - 1) / a.row_pieces);
-    a.tokens_per_cta = tokens_per_cta(a.row_pieces, pieces);
+    a.tpb = D->block_size / kQ4Tile;
+    a.inv_lanes = reciprocal(a.lanes_n);
+    a.inv_tpb = reciprocal(a.tpb);
     a.n_slots = (long long)D->n_total_blocks * D->block_size;
+    a.wide = aligned % 32 == 0;
     a.err = dev.error_word;
 }
+dim3 row_grid(const RowArgs &a, int layers) {
+    return dim3((unsigned)((a.n_tokens + (long long)a.tokens_per_cta - 1) / a.tokens_per_cta), (unsigned)layers, 2);
+}
+
+constexpr int kStoreUnroll = 2, kReadUnroll = 4;
 
 template <bool APPEND>
 zp_status launch_store(const zp_cache_desc *D, const StoreArgs &a, int layers, const char *what, cudaStream_t st) {
-    const dim3 grid((unsigned)((a.n_tokens + (long long)a.tokens_per_cta - 1) / a.tokens_per_cta), (unsigned)layers, 2);
+    const dim3 grid = row_grid(a, layers);
     const bool wide = D->head_dim == 128;
     if (D->dtype == ZP_BF16) {
-        if (wide) q4_store_kernel<__nv_bfloat16, 128, APPEND><<<grid, kStoreThreads, 0, st>>>(a);
-        else q4_store_kernel<__nv_bfloat16, 64, APPEND><<<grid, kStoreThreads, 0, st>>>(a);
+        if (wide) q4_store_kernel<__nv_bfloat16, 128, APPEND, kStoreUnroll><<<grid, kStoreThreads, 0, st>>>(a);
+        else q4_store_kernel<__nv_bfloat16, 64, APPEND, kStoreUnroll><<<grid, kStoreThreads, 0, st>>>(a);
     } else {
-        if (wide) q4_store_kernel<float, 128, APPEND><<<grid, kStoreThreads, 0, st>>>(a);
-        else q4_store_kernel<float, 64, APPEND><<<grid, kStoreThreads, 0, st>>>(a);
+        if (wide) q4_store_kernel<float, 128, APPEND, kStoreUnroll><<<grid, kStoreThreads, 0, st>>>(a);
+        else q4_store_kernel<float, 64, APPEND, kStoreUnroll><<<grid, kStoreThreads, 0, st>>>(a);
     }
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, what);
@@ -404,6 +513,7 @@ extern "C" zp_status zp_q4_write_kv(const zp_cache_desc *D, int32_t group, const
     if (rc != ZP_OK) return rc;
     if (n_tokens < 0 || layer_count < 0)
         return fail(ZP_ERR_INVALID_ARG, "q4_write_kv: n_tokens=%d layer_count=%d", n_tokens, layer_count);
+    if (n_tokens > 1 << 30) return fail(ZP_ERR_SHAPE, "q4_write_kv: %d tokens", n_tokens);
     if (n_tokens == 0 || layer_count == 0) return ok();
     if (!k_new || !v_new || !slots || !k_base || !v_base) return fail(ZP_ERR_INVALID_ARG, "q4_write_kv: NULL buffer");
     rc = check_rows(D, group, "q4_write_kv", k_new, v_new, token_stride, new_layer_stride, layer_count, k_base, v_base,
@@ -421,7 +531,7 @@ extern "C" zp_status zp_q4_write_kv(const zp_cache_desc *D, int32_t group, const
     a.V = static_cast<unsigned char *>(v_base);
     a.layer_bytes = layer_count > 1 ? layer_stride : 0;
     a.slots = slots;
-    fill_shape(a, D, group, n_tokens, kStoreThreads * kStoreUnroll, dev);
+    fill_rows(a, D, group, n_tokens, kStoreUnroll, row_alignment(D, k_new, v_new, token_stride, a.new_layer_stride), dev);
     return launch_store<false>(D, a, layer_count, "q4_write_kv: launch", static_cast<cudaStream_t>(stream));
 }
 
@@ -450,7 +560,7 @@ extern "C" zp_status zp_q4_append_kv(const zp_cache_desc *D, int32_t group, cons
     a.table = block_table;
     a.table_stride = table_stride;
     a.seq_lens = seq_lens;
-    fill_shape(a, D, group, B, kStoreThreads * kStoreUnroll, dev);
+    fill_rows(a, D, group, B, kStoreUnroll, row_alignment(D, k_new, v_new, row, 0), dev);
     return launch_store<true>(D, a, 1, "q4_append_kv: launch", static_cast<cudaStream_t>(stream));
 }
 
@@ -461,6 +571,7 @@ extern "C" zp_status zp_q4_read_kv(const zp_cache_desc *D, int32_t group, const 
     if (rc != ZP_OK) return rc;
     if (n_tokens < 0 || layer_count < 0)
         return fail(ZP_ERR_INVALID_ARG, "q4_read_kv: n_tokens=%d layer_count=%d", n_tokens, layer_count);
+    if (n_tokens > 1 << 30) return fail(ZP_ERR_SHAPE, "q4_read_kv: %d tokens", n_tokens);
     if (n_tokens == 0 || layer_count == 0) return ok();
     if (!k_base || !v_base || !slots || !k_out || !v_out) return fail(ZP_ERR_INVALID_ARG, "q4_read_kv: NULL buffer");
     rc = check_rows(D, group, "q4_read_kv", k_out, v_out, token_stride, out_layer_stride, layer_count, k_base, v_base,
@@ -478,16 +589,16 @@ extern "C" zp_status zp_q4_read_kv(const zp_cache_desc *D, int32_t group, const 
     a.v = v_out;
     a.token_stride = token_stride;
     a.out_layer_stride = layer_count > 1 ? out_layer_stride : 0;
-    fill_shape(a, D, group, n_tokens, kStoreThreads * kReadUnroll, dev);
-    const dim3 grid((unsigned)((n_tokens + (long long)a.tokens_per_cta - 1) / a.tokens_per_cta), (unsigned)layer_count, 2);
+    fill_rows(a, D, group, n_tokens, kReadUnroll, row_alignment(D, k_out, v_out, token_stride, a.out_layer_stride), dev);
+    const dim3 grid = row_grid(a, layer_count);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool wide = D->head_dim == 128;
     if (D->dtype == ZP_BF16) {
-        if (wide) q4_read_kernel<__nv_bfloat16, 128><<<grid, kStoreThreads, 0, st>>>(a);
-        else q4_read_kernel<__nv_bfloat16, 64><<<grid, kStoreThreads, 0, st>>>(a);
+        if (wide) q4_read_kernel<__nv_bfloat16, 128, kReadUnroll><<<grid, kStoreThreads, 0, st>>>(a);
+        else q4_read_kernel<__nv_bfloat16, 64, kReadUnroll><<<grid, kStoreThreads, 0, st>>>(a);
     } else {
-        if (wide) q4_read_kernel<float, 128><<<grid, kStoreThreads, 0, st>>>(a);
-        else q4_read_kernel<float, 64><<<grid, kStoreThreads, 0, st>>>(a);
+        if (wide) q4_read_kernel<float, 128, kReadUnroll><<<grid, kStoreThreads, 0, st>>>(a);
+        else q4_read_kernel<float, 64, kReadUnroll><<<grid, kStoreThreads, 0, st>>>(a);
     }
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "q4_read_kv: launch");
@@ -548,10 +659,17 @@ extern "C" zp_status zp_q4_compact_pages(const zp_cache_desc *D, int32_t group, 
     a.lg_words = log2_of(D->head_dim / group);
     a.tile = q4_tile_bytes(D->head_dim, group);
     a.err = dev.error_word;
+    // Rounds of 512 ranks where every CTA has an SM of its own (7 sequences of 2032 ranks 12.8 us,
+    // with 256 14.8), of 256 and two or more CTAs per SM where there are more (16 of 4080: 58 us, 69).
     const dim3 grid(2 * D->h_kv, n, layer_count);
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (D->head_dim == 128) q4_compact_kernel<128><<<grid, kMoveThreads, 0, st>>>(a);
-    else q4_compact_kernel<64><<<grid, kMoveThreads, 0, st>>>(a);
+    const bool few = (long long)grid.x * grid.y * grid.z <= dev.sm_count, wide = D->head_dim == 128;
+    const int ranks = few ? 512 : 256;
+    const auto kernel = wide ? (few ? q4_compact_kernel<128, 512> : q4_compact_kernel<128, 256>)
+                             : (few ? q4_compact_kernel<64, 512> : q4_compact_kernel<64, 256>);
+    const size_t smem = (size_t)kMoveStages * move_stage_bytes(ranks, D->head_dim, D->head_dim / group);
+    rc = set_max_dynamic_smem(reinterpret_cast<const void *>(kernel), smem, "q4_compact: shared-memory attribute");
+    if (rc != ZP_OK) return rc;
+    kernel<<<grid, ranks, smem, static_cast<cudaStream_t>(stream)>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "q4_compact: launch");
     return ok();

@@ -510,7 +510,8 @@ zp_status zp_compress_layers_rho(const zp_cache_desc *D, const zp_score_params *
  *            NaN or an infinity, or with a spread past the largest float, reads as NaN.
  * D is the descriptor of the rows (dtype: of q, of the rows given and taken, of the output).
  * Limits of every call: d in {64, 128}, b a multiple of 16, h_kv <= 256, N_total * b
- * below 2^31 (ZP_ERR_SHAPE); caches 16-byte aligned.  0 = refused. */
+ * below 2^31, at most 2^30 tokens in a call (ZP_ERR_SHAPE); caches 16-byte aligned.
+ * zp_q4_tile_bytes: 0 = refused. */
 size_t zp_q4_tile_bytes(const zp_cache_desc *D, int32_t group);
 
 /* zp_write_kv into a 4-bit cache: the rows of n_tokens tokens (dtype, token_stride and
@@ -545,8 +546,8 @@ zp_status zp_q4_read_kv(const zp_cache_desc *D, int32_t group, const void *k_bas
  * tokens weigh nothing), a slot >= n_score_rows (0x15a; not scored).
  * The workspace is scratch: any content on entry, nothing kept; two calls that may
  * overlap need one each.  Its size with scored = 0 serves calls without score_accum.
- * Limits: B <= 4096, h_q/h_kv <= 8, B * table_stride * b below 2^31 (ZP_ERR_SHAPE);
- * buffers 16-byte aligned; score_accum float [rows][h_kv][table_stride * b]. */
+ * Limits: B <= 4096, h_q/h_kv <= 8, B * table_stride * b below 2^31, N_total * h_kv * b/16
+ * below 2^31, B * h_kv * (table_stride * b / 32 + 1) below 2^30 (ZP_ERR_SHAPE); buffers 16-byte aligned; score_accum float [rows][h_kv][table_stride * b]. */
 size_t zp_q4_decode_workspace_size(const zp_cache_desc *D, int32_t group, int32_t B, int32_t table_stride,
                                    int32_t scored);
 zp_status zp_q4_decode_attn(const zp_cache_desc *D, int32_t group, const void *q, const void *k_cache,

@@ -65,7 +65,7 @@ def test_rows(zp, name):
                dict(ts=1023), dict(ts=1028), dict(k=_at(8)), dict(V=_at(8)), dict(layers=2, nl=4096, ls=layer - 16),
                dict(layers=2, nl=-8, ls=layer), dict(layers=2, nl=4, ls=layer), dict(layers=2, nl=4096, ls=layer + 8)):
         assert call(**kw) == 1, kw
-    assert call(layers=65536, nl=4096, ls=layer) == 2
+    assert call(layers=65536, nl=4096, ls=layer) == 2 and call(n=(1 << 30) + 1) == 2
     assert call(n=0, k=None) == 0 and call(layers=0, k=None) == 0
 
 
