@@ -14,6 +14,7 @@
 // goes on in other CTAs.  q4_finish_kernel joins those (at most one pair per CTA boundary) and,
 // on window steps, turns the logits that the attention left (log2 units) into probabilities
 // with the final sums, takes the maximum over the q heads and adds 1/w of it to the score.
+#include <cuda_fp16.h>
 #include <math.h>
 
 #include "q4_format.cuh"
@@ -42,7 +43,7 @@ struct Q4Args {
     int n_score_rows;
     int *prefix;    // [B+1] units before each sequence (of one kv head)
     float *stats;   // [B][h_q] reference + log2(sum) of the pairs that one CTA saw whole
-    float *rec;     // [2 * CTAs][G * (d + 4)]: per head (reference, sum for the output, sum, 0), then accumulators
+    float *rec;     // [2 * CTAs + warps][G * (d + 4)]: per head (reference, sum for the output, sum, 0), then accumulators
     float *logits;  // [units][32][G]
     int grid, warps, stages;  // CTAs of the attention kernel, warps of one, units in a warp's ring
     unsigned *err;
@@ -321,17 +322,21 @@ struct ScalarWarp {
 // bf16 queries, up to 8 q heads as the 8 columns of mma.sync m16n8k16: logits[t][h] with
 // the key codes as the left operand, out^T[i][h] with the value codes.  (One kv head has 8
 // query rows at most: the 128 rows of a tcgen05 tile would stand empty, and its operands
-// would have to be written to shared memory at four times the size of the codes.)  A code
-// becomes a bf16 number in a register by one and-or: 0x4300 | c is 128 + c, exactly.
-//   logits:  sum_i q_i (lo + c_i step) = (lo - 128 step) sum_i q_i + step sum_i q_i (128 + c_i)
-//     per group.  The first term is a product of its own, of the parameter words (step, lo) as
-//     they lie in the tile with (-128 sum q, sum q), the sum in three bf16 parts of 8 bits.
-//     Nothing is rounded to 16 bits: the logits are those of 32-bit arithmetic.
-//   output:  sum_t p_t (lo_t + c_t step_t): p rounded to bf16 and transposed (movmatrix), p *
-//     step rounded to bf16 again per group, both with half a step of 2^-8 relative; the sum
-//     that divides is that of the rounded p, and the 128 is taken off with the rounded
-//     products (a product with -128, into the accumulator that also sums p lo and p), so that
-//     each token's weight is off by the two roundings and no more.
+// would have to be written to shared memory at four times the size of the codes.)
+//   logits:  sum_i q_i (lo + c_i step) = lo sum_i q_i + step sum_i q_i c_i per group.  The codes
+//     go in as fp16 numbers without any arithmetic: the low nibble of a halfword, masked, is the
+//     subnormal c 2^-24 and the next one c 2^-20 (whose queries are 2^-4 times as large), so
+//     that a word of eight codes takes four masks and one shift.  The queries are scaled by a power
+//     of two to fill fp16's range; those of 8 bits that lie within 2^-24 of the largest stay exact.
+//     The lo term is a product of its own, of the parameter words (step, lo) as they lie in the
+//     tile with (0, sum q), the sum in three bf16 parts of 8 bits.  Nothing else is rounded to 16
+//     bits: the logits are those of 32-bit arithmetic.
+//   output:  sum_t p_t (lo_t + c_t step_t): the codes as bf16 numbers 128 + c (0x4300 | c, one and-or;
+//     p step needs bf16's range), p rounded to bf16 and transposed (movmatrix), p *
+//     step rounded to bf16 again per group, both by 2^-9 at most.  The second rounding is kept to
+//     the part c - 8 of a code: sum_t p (lo + 8 step) is a product of p with the parameters as they
+//     are, and 136 times the rounded p step is taken off again (a product with -136, into the
+//     same accumulator).  The sum that divides is that of the rounded p.
 // ldmatrix of a natural row of codes gives lane 4t + j the word j of a 16-byte chunk of
 // token t, the layout of the left operand; its transposed form gives the codes of two
 // adjacent tokens for 4 dimensions, the layout of the transposed values.
@@ -340,6 +345,19 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// the same in fp16
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 // d = a b
 __device__ __forceinline__ void mma_bf16_0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -358,7 +376,11 @@ __device__ __forceinline__ uint32_t mul_bf2(uint32_t a, uint32_t b) {
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-// codes e and e + 4 of a word (or code e of two tokens) as 128 + c
+__device__ __forceinline__ uint32_t f2_to_h2(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+// code e of two tokens as 128 + c
 template <int E>
 __device__ __forceinline__ uint32_t codes(uint32_t w) {
     uint32_t r;
@@ -384,13 +406,15 @@ constexpr float kLazyMax = 8.f;  // the reference follows the maximum when it is
 template <int D, int LG>
 struct TcWarp {
     using T = __nv_bfloat16;
-    static constexpr int kD = D, kWarps = 12, kCtas = 1;  // (16 warps would leave a thread 128 registers)
+    static constexpr int kD = D, kWarps = 16, kCtas = 1;
     static constexpr int kSharedBytes = 0, kTile = q4_tile_bytes(D, 1 << LG);
     static constexpr int NG = D >> LG, kChunks = D / 32, kPerGroup = (1 << LG) / 32;  // chunks of a row, of a group
     uint32_t qb[kChunks][2][2];  // queries as the right operand, by chunk and half of its words
-    uint32_t ob[3];  // (-128, 1) * sums of the queries of (head lane / 4, group lane % 4), in three parts
+    uint32_t ob[3];  // (0, sum of the queries) of (head lane / 4, group lane % 4), in three parts, scaled as the products
+    float unit_y[2], more_y[2];  // what a product is worth: log2(e) / sqrt(d) over the scale of heads 2 (lane % 4), + 1;
+                                 // more_y: a factor beyond it (1 but for queries past 2^100)
     float acc[kChunks][2][4], off[4];
-    float thr[2], base[2], l[2];  // of those heads: m + kLazyMax (-inf: none yet), m, sum over this lane's tokens
+    float thr[2], base[2], l[2];  // of those two heads: m + kLazyMax (-inf: none yet), m, sum over this lane's tokens
 
     __device__ __forceinline__ void init(unsigned char *) {}
 
@@ -408,31 +432,56 @@ struct TcWarp {
     }
     __device__ __forceinline__ void begin(const Q4Args &a, const Query &x, int lane) {
         const int j = lane & 3;
+        // the head's largest exponent (that of an infinity is one more than of any number)
+        uint32_t top = 0;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t w = (&x.w[c].x)[i];
+                top = max(top, max(w & 0x7F80u, (w >> 16) & 0x7F80u));
+            }
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        const int e = max((int)(top >> 7) - 127, -100);  // |q| < 2^(e + 1), scaled to below 2^15
+        const float scale = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
         float sum[NG];
 #pragma unroll
         for (int g = 0; g < NG; ++g) sum[g] = 0.f;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-            const uint4 w = x.w[c];
-            qb[c][0][0] = __byte_perm(w.x, w.z, 0x5410);
-            qb[c][0][1] = __byte_perm(w.x, w.z, 0x7632);
-            qb[c][1][0] = __byte_perm(w.y, w.w, 0x5410);
-            qb[c][1][1] = __byte_perm(w.y, w.w, 0x7632);
-            const float2 x0 = bf2_to_f2(w.x), x1 = bf2_to_f2(w.y), x2 = bf2_to_f2(w.z), x3 = bf2_to_f2(w.w);
-            sum[c / kPerGroup] += ((x0.x + x0.y) + (x1.x + x1.y)) + ((x2.x + x2.y) + (x3.x + x3.y));
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = bf2_to_f2((&x.w[c].x)[i]);
+                v[2 * i] = f.x * scale;
+                v[2 * i + 1] = f.y * scale;
+            }
+            qb[c][0][0] = f2_to_h2(v[0], v[4]);
+            qb[c][0][1] = f2_to_h2(v[1] * 0.0625f, v[5] * 0.0625f);
+            qb[c][1][0] = f2_to_h2(v[2], v[6]);
+            qb[c][1][1] = f2_to_h2(v[3] * 0.0625f, v[7] * 0.0625f);
+            sum[c / kPerGroup] += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
         }
         float part = 0.f;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             sum[g] += __shfl_xor_sync(0xFFFFFFFFu, sum[g], 1);
             sum[g] += __shfl_xor_sync(0xFFFFFFFFu, sum[g], 2);
-            if (j == g) part = sum[g];
+            if (j == g) part = sum[g] * 0x1p-24f;
         }
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
-            const float x = __bfloat162float(__float2bfloat16_rn(part));
-            ob[i] = f2_to_bf2(-128.f * x, x);
-            part -= x;
+            const float hi = __bfloat162float(__float2bfloat16_rn(part));
+            ob[i] = __float_as_uint(hi);  // (the high half: the place of lo in a parameter word)
+            part -= hi;
+        }
+        // 2^(24 - 14 + e) log2(e) / sqrt(d); above 2^117 it is not a float, and the rest is multiplied on
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int eh = __shfl_sync(0xFFFFFFFFu, e, 8 * j + 4 * i);
+            unit_y[i] = a.qscale * __uint_as_float((uint32_t)(127 + min(eh + 10, 110)) << 23);
+            more_y[i] = __uint_as_float((uint32_t)(127 + max(eh - 100, 0)) << 23);
         }
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
@@ -485,14 +534,13 @@ struct TcWarp {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int g = (c + i) / kPerGroup;
+                    const uint32_t x0 = r[2 * i], x1 = r[2 * i + 1], z0 = x0 >> 8, z1 = x1 >> 8;
+                    constexpr uint32_t lo4 = 0x000F000Fu, hi4 = 0x00F000F0u;
                     if ((c + i) % kPerGroup == 0)
-                        mma_bf16_0(d, codes<0>(r[2 * i]), codes<0>(r[2 * i + 1]), codes<1>(r[2 * i]), codes<1>(r[2 * i + 1]),
-                                   qb[c + i][0][0], qb[c + i][0][1]);
+                        mma_f16_0(d, x0 & lo4, x1 & lo4, x0 & hi4, x1 & hi4, qb[c + i][0][0], qb[c + i][0][1]);
                     else
-                        mma_bf16(d, codes<0>(r[2 * i]), codes<0>(r[2 * i + 1]), codes<1>(r[2 * i]), codes<1>(r[2 * i + 1]),
-                                 qb[c + i][0][0], qb[c + i][0][1]);
-                    mma_bf16(d, codes<2>(r[2 * i]), codes<2>(r[2 * i + 1]), codes<3>(r[2 * i]), codes<3>(r[2 * i + 1]),
-                             qb[c + i][1][0], qb[c + i][1][1]);
+                        mma_f16(d, x0 & lo4, x1 & lo4, x0 & hi4, x1 & hi4, qb[c + i][0][0], qb[c + i][0][1]);
+                    mma_f16(d, z0 & lo4, z1 & lo4, z0 & hi4, z1 & hi4, qb[c + i][1][0], qb[c + i][1][1]);
                     if ((c + i + 1) % kPerGroup == 0) {
                         const float s0 = __uint_as_float(w0[g] << 16), s1 = __uint_as_float(w1[g] << 16);
                         y[b][0] = fmaf(s0, d[0], y[b][0]);
@@ -503,7 +551,13 @@ struct TcWarp {
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[b][i] *= a.qscale;
+            for (int i = 0; i < 4; ++i) y[b][i] *= unit_y[i & 1];
+        }
+        if (more_y[0] != 1.f || more_y[1] != 1.f) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[b][i] *= more_y[i & 1];
         }
         if (part) {
 #pragma unroll
@@ -556,13 +610,15 @@ struct TcWarp {
             const uint32_t b0 = transpose8(f2_to_bf2(p[0], p[1])), b1 = transpose8(f2_to_bf2(p[2], p[3]));
             const uint32_t *vp = reinterpret_cast<const uint32_t *>(vt + b * kTile + q4_code_bytes(D));
             {
-                // row g of `off`: sum of p lo of group g, less 128 times that of its rounded p step; row 8: sum of p
+                // row g of `off`: sum of p (lo + 8 step) of group g, less 136 times that of its rounded p step;
+                // row 8: sum of p
                 const bool in = n < NG;
                 const uint32_t *q0 = vp + 2 * j * NG + (in ? n : 0);
-                const uint32_t l0 = in ? __byte_perm(q0[0], q0[NG], 0x7632) : 0;
-                const uint32_t l1 = in ? __byte_perm(q0[8 * NG], q0[9 * NG], 0x7632) : 0;
+                const uint32_t x0 = in ? q0[0] : 0, x1 = in ? q0[NG] : 0, x8 = in ? q0[8 * NG] : 0, x9 = in ? q0[9 * NG] : 0;
                 const uint32_t one = n == 0 ? 0x3F803F80u : 0;
-                mma_bf16(off, l0, one, l1, one, b0, b1);
+                mma_bf16(off, __byte_perm(x0, x1, 0x7632), one, __byte_perm(x8, x9, 0x7632), one, b0, b1);
+                mma_bf16(off, __byte_perm(x0, x1, 0x5410), 0, __byte_perm(x8, x9, 0x5410), 0, mul_bf2(b0, 0x41004100u),
+                         mul_bf2(b1, 0x41004100u));
             }
             uint32_t w0[NG], w1[NG], w2[NG], w3[NG];
             lds<NG>(vp + 2 * j * NG, w0);
@@ -581,7 +637,7 @@ struct TcWarp {
                     if ((c + i) % kPerGroup == 0) {
                         s0 = mul_bf2(b0, __byte_perm(w0[g], w1[g], 0x5410));
                         s1 = mul_bf2(b1, __byte_perm(w2[g], w3[g], 0x5410));
-                        const uint32_t minus = n == g ? 0xC300C300u : 0;  // -128
+                        const uint32_t minus = n == g ? 0xC308C308u : 0;  // -136
                         mma_bf16(off, minus, 0, minus, 0, s0, s1);
                     }
                     mma_bf16(acc[c + i][0], codes<0>(r[2 * i]), codes<1>(r[2 * i]), codes<0>(r[2 * i + 1]), codes<1>(r[2 * i + 1]),
@@ -642,10 +698,11 @@ struct TcWarp {
 
 // ---------------------------------------------------------------- attention
 // Shared memory: rings (a warp's tiles; at its end the record of a pair that goes on
-// behind its range), records of pairs that began before a warp's range, the warps' own, prefix.
+// behind its range), the warps' own, prefix.  The record of a pair that began before a warp's range is
+// written while the ring is in use, so to the workspace.
 template <class W>
-__host__ __device__ inline size_t attention_smem(int stages, int tile, int G, int B) {
-    return (size_t)W::kWarps * ((size_t)stages * 4 * tile + (size_t)G * (W::kD + 4) * 4 + W::kSharedBytes) + ((size_t)B + 1) * 4;
+__host__ __device__ inline size_t attention_smem(int stages, int tile, int B) {
+    return (size_t)W::kWarps * ((size_t)stages * 4 * tile + W::kSharedBytes) + ((size_t)B + 1) * 4;
 }
 
 template <class W>
@@ -663,13 +720,14 @@ __global__ void __launch_bounds__(W::kWarps * 32, W::kCtas) q4_attention_kernel(
     const int rec_n = rec_floats(a, D), stages = a.stages;
     const size_t ring_bytes = (size_t)stages * 4 * a.tile;
     unsigned char *ring = smem + warp * ring_bytes;
-    float *heads = reinterpret_cast<float *>(smem + kWarps * ring_bytes);
-    unsigned char *own = reinterpret_cast<unsigned char *>(heads + kWarps * rec_n) + warp * W::kSharedBytes;
-    int *prefix = reinterpret_cast<int *>(reinterpret_cast<unsigned char *>(heads + kWarps * rec_n) + kWarps * W::kSharedBytes);
+    unsigned char *own = smem + kWarps * ring_bytes + warp * W::kSharedBytes;
+    int *prefix = reinterpret_cast<int *>(smem + kWarps * (ring_bytes + W::kSharedBytes));
+    float *heads = a.rec + (size_t)(2 * a.grid + (int)blockIdx.x * kWarps) * rec_n;
     if (lane < stages) mbar_init(&full_s[warp][lane], 2);
     if (lane == 0) head_s[warp] = tail_s[warp] = -1;
     if (tid == 0) abort_s = 0;
     fence_barrier_init();
+    pdl_wait();
     unit_prefix(a, prefix, sums_s);  // (has the barrier behind the initialisation)
     if (blockIdx.x == 0)
         for (int s = tid; s <= a.B; s += blockDim.x) a.prefix[s] = prefix[s];
@@ -788,50 +846,54 @@ __global__ void __launch_bounds__(W::kWarps * 32, W::kCtas) q4_attention_kernel(
     __syncthreads();
     if (abort_s) return;
     // ---- the records of this CTA: a pair's chain begins in a warp's tail, or before the CTA in
-    // the first warp's head, and goes on in the heads of the next warps.  Its first warp joins it.
-    for (int side = warp == 0 ? 0 : 1; side < 2; ++side) {
-        const int id = warp >= split.per_cta ? -1 : side ? tail_s[warp] : head_s[warp];
-        if (id < 0) continue;
-        const int pair = id & ~kDone;
-        bool done = side == 0 && (id & kDone);
-        int w1 = warp;  // the pair's last warp here
-        while (!done && w1 + 1 < split.per_cta && head_s[w1 + 1] >= 0 && (head_s[w1 + 1] & ~kDone) == pair) {
-            ++w1;
-            done = head_s[w1] & kDone;
+    // the first warp's head, and goes on in the heads of the next warps.  A warp joins one head
+    // of one chain at a time.
+    const int my_head = lane < split.per_cta ? head_s[lane] : -1;
+    const unsigned tails = __ballot_sync(0xFFFFFFFFu, lane < split.per_cta && tail_s[lane] >= 0);
+    const int before = head_s[0] >= 0, chains = before + __popc(tails);
+    for (int task = warp; task < chains * a.G; task += kWarps) {
+        const int chain = task / a.G, q = task - chain * a.G;
+        const bool side = chain >= before;  // it begins in this CTA
+        int w0 = 0;
+        if (side) {
+            unsigned rest = tails;
+            for (int i = before; i < chain; ++i) rest &= rest - 1;
+            w0 = __ffs(rest) - 1;
         }
-        const float *rec0 = side ? reinterpret_cast<const float *>(ring) : heads + warp * rec_n;
-        auto rec = [&](int w) { return w == warp ? rec0 : heads + w * rec_n; };
+        const int pair = (side ? tail_s[w0] : head_s[0]) & ~kDone;
+        const unsigned same = __ballot_sync(0xFFFFFFFFu, lane > w0 && my_head >= 0 && (my_head & ~kDone) == pair);
+        const int w1 = w0 + __ffs(~(same >> (w0 + 1))) - 1;  // the pair's last warp here
+        const bool done = w1 > w0 || !side ? (head_s[w1] & kDone) != 0 : false;
+        const float *rec0 = side ? reinterpret_cast<const float *>(smem + w0 * ring_bytes) : heads;
+        auto rec = [&](int w) { return w == w0 ? rec0 : heads + w * rec_n; };
         const int s = pair / a.h_kv, h = pair % a.h_kv;
-        float *to = a.rec + (size_t)(2 * blockIdx.x + side) * rec_n;
-        T *out = static_cast<T *>(a.out) + ((size_t)s * a.h_q + (size_t)h * a.G) * D;
-        for (int i = lane * 4; i < a.G * D; i += 128) {
-            const int q = i / D;
-            float m = -INFINITY;
+        float m = -INFINITY;
 #pragma unroll 4
-            for (int w = warp; w <= w1; ++w) m = fmaxf(m, rec(w)[4 * q]);
-            const float base = m == -INFINITY ? 0.f : m;
-            float x[4] = {}, lo = 0.f, l = 0.f;
+        for (int w = w0; w <= w1; ++w) m = fmaxf(m, rec(w)[4 * q]);
+        const float base = m == -INFINITY ? 0.f : m;
+        constexpr int kOwn = D / 32;
+        float x[kOwn] = {}, lo = 0.f, l = 0.f;
 #pragma unroll 4
-            for (int w = warp; w <= w1; ++w) {
-                const float4 r = *reinterpret_cast<const float4 *>(rec(w) + 4 * q);
-                const float4 v = *reinterpret_cast<const float4 *>(rec(w) + 4 * a.G + i);
-                const float f = ex2_approx(r.x - base);
-                lo = fmaf(r.y, f, lo);
-                l = fmaf(r.z, f, l);
-                x[0] = fmaf(v.x, f, x[0]);
-                x[1] = fmaf(v.y, f, x[1]);
-                x[2] = fmaf(v.z, f, x[2]);
-                x[3] = fmaf(v.w, f, x[3]);
-            }
-            if (side && done) {
-                const float r = lo == 0.f ? 0.f : 1.f / lo;
+        for (int w = w0; w <= w1; ++w) {
+            const float4 r = *reinterpret_cast<const float4 *>(rec(w) + 4 * q);
+            const float *v = rec(w) + 4 * a.G + q * D + lane * kOwn;
+            const float f = ex2_approx(r.x - base);
+            lo = fmaf(r.y, f, lo);
+            l = fmaf(r.z, f, l);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) out[i + e] = from_f<T>(x[e] * r);
-                if (a.want_score && i % D == 0) a.stats[(size_t)s * a.h_q + h * a.G + q] = score_norm(m, l);
-            } else {
-                *reinterpret_cast<float4 *>(to + 4 * a.G + i) = make_float4(x[0], x[1], x[2], x[3]);
-                if (i % D == 0) reinterpret_cast<float4 *>(to)[q] = make_float4(m, lo, l, 0.f);
-            }
+            for (int e = 0; e < kOwn; ++e) x[e] = fmaf(v[e], f, x[e]);
+        }
+        if (side && done) {
+            const float r = lo == 0.f ? 0.f : 1.f / lo;
+            T *out = static_cast<T *>(a.out) + ((size_t)s * a.h_q + (size_t)h * a.G + q) * D + lane * kOwn;
+#pragma unroll
+            for (int e = 0; e < kOwn; ++e) out[e] = from_f<T>(x[e] * r);
+            if (a.want_score && lane == 0) a.stats[(size_t)s * a.h_q + h * a.G + q] = score_norm(m, l);
+        } else {
+            float *to = a.rec + (size_t)(2 * blockIdx.x + side) * rec_n;
+#pragma unroll
+            for (int e = 0; e < kOwn; ++e) to[4 * a.G + q * D + lane * kOwn + e] = x[e];
+            if (lane == 0) reinterpret_cast<float4 *>(to)[q] = make_float4(m, lo, l, 0.f);
         }
     }
 }
@@ -839,11 +901,57 @@ __global__ void __launch_bounds__(W::kWarps * 32, W::kCtas) q4_attention_kernel(
 // ---------------------------------------------------------------- what is left
 // CTA c joins the records of the pair that its counterpart of the attention kernel began and
 // did not finish, and forms the score of that one's units.
-constexpr int kFinishThreads = 1024, kScoreUnroll = 4;
+constexpr int kFinishThreads = 512, kScoreUnroll = 8;
 
 // Record of CTA c of a pair cut between CTAs, which CTA c0 begins.
 __device__ __forceinline__ const float *cta_record(const Q4Args &a, int c0, int c, int rec_n) {
     return a.rec + (size_t)(2 * c + (c == c0 ? 1 : 0)) * rec_n;
+}
+
+// Every 32nd token from t to t1 of a pair: S += share * 2^max_q (logit - c), or = where `fresh` and at P.
+// G4: vectors of four heads (0: any number of heads).  All loads of a round are under way at once.
+template <int G4>
+__device__ __forceinline__ void score_tokens(const Q4Args &a, const float *lg, const float (&c)[8], float *S, int t, int t1,
+                                             int P, bool fresh, float share) {
+    for (; t < t1; t += 32 * kScoreUnroll) {
+        float top[kScoreUnroll], old[kScoreUnroll];
+        if constexpr (G4 > 0) {
+            float4 v[kScoreUnroll][G4];
+#pragma unroll
+            for (int k = 0; k < kScoreUnroll; ++k)
+#pragma unroll
+                for (int i = 0; i < G4; ++i) {
+                    const int tok = min(t + 32 * k, t1 - 1);
+                    v[k][i] = __ldcg(reinterpret_cast<const float4 *>(lg) + (size_t)tok * G4 + i);
+                }
+#pragma unroll
+            for (int k = 0; k < kScoreUnroll; ++k) {
+                const int tok = min(t + 32 * k, t1 - 1);
+                old[k] = fresh || tok == P ? 0.f : S[tok];
+            }
+#pragma unroll
+            for (int k = 0; k < kScoreUnroll; ++k) {
+                top[k] = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < G4; ++i)
+                    top[k] = fmaxf(fmaxf(top[k], fmaxf(v[k][i].x - c[4 * i], v[k][i].y - c[4 * i + 1])),
+                                   fmaxf(v[k][i].z - c[4 * i + 2], v[k][i].w - c[4 * i + 3]));
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kScoreUnroll; ++k) {
+                const int tok = min(t + 32 * k, t1 - 1);
+                top[k] = -INFINITY;
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    if (q < a.G) top[k] = fmaxf(top[k], __ldcg(lg + (size_t)tok * a.G + q) - c[q]);
+                old[k] = fresh || tok == P ? 0.f : S[tok];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kScoreUnroll; ++k)
+            if (t + 32 * k < t1) S[t + 32 * k] = fmaf(ex2_approx(top[k]), share, old[k]);
+    }
 }
 
 template <typename T, int D>
@@ -923,37 +1031,9 @@ __global__ void __launch_bounds__(kFinishThreads) q4_finish_kernel(const Q4Args 
             float *S = a.score + ((size_t)row * a.h_kv + cur.h) * a.score_stride;
             const int t0 = cur.u * kUnit, t1 = min(t0 + units * kUnit, L);
             const float *lg = a.logits + (size_t)first * kUnit * a.G;
-            for (int t = t0 + lane; t < t1; t += 32 * kScoreUnroll) {
-                float top[kScoreUnroll], old[kScoreUnroll];
-#pragma unroll
-                for (int k = 0; k < kScoreUnroll; ++k) {
-                    const int tok = t + 32 * k;
-                    top[k] = -INFINITY;
-                    old[k] = 0.f;
-                    if (tok < t1) {
-                        const float *x = lg + (size_t)tok * a.G;
-                        if (a.G % 4 == 0) {
-#pragma unroll
-                            for (int q = 0; q < 8; q += 4) {
-                                if (q >= a.G) continue;
-                                const float4 v = __ldcg(reinterpret_cast<const float4 *>(x + q));
-                                top[k] = fmaxf(fmaxf(top[k], fmaxf(v.x - c[q], v.y - c[q + 1])),
-                                               fmaxf(v.z - c[q + 2], v.w - c[q + 3]));
-                            }
-                        } else {
-#pragma unroll
-                            for (int q = 0; q < 8; ++q)
-                                if (q < a.G) top[k] = fmaxf(top[k], __ldcg(x + q) - c[q]);
-                        }
-                        if (!fresh && tok != P) old[k] = S[tok];
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < kScoreUnroll; ++k) {
-                    const int tok = t + 32 * k;
-                    if (tok < t1) S[tok] = fmaf(ex2_approx(top[k]), share, old[k]);
-                }
-            }
+            if (a.G == 4) score_tokens<1>(a, lg, c, S, t0 + lane, t1, P, fresh, share);
+            else if (a.G == 8) score_tokens<2>(a, lg, c, S, t0 + lane, t1, P, fresh, share);
+            else score_tokens<0>(a, lg, c, S, t0 + lane, t1, P, fresh, share);
         }
         x += units;
         cur.u += units - 1;
@@ -1010,8 +1090,8 @@ zp_status q4_plan(const zp_cache_desc *D, int group, int B, int table_stride, in
         p->warps = W::kWarps;
         p->grid = dev.sm_count * W::kCtas;
         p->stages = kMaxStages;
-        while (p->stages > 2 && attention_smem<W>(p->stages, tile, G, B) > room) --p->stages;
-        p->smem = attention_smem<W>(p->stages, tile, G, B);
+        while (p->stages > 2 && attention_smem<W>(p->stages, tile, B) > room) --p->stages;
+        p->smem = attention_smem<W>(p->stages, tile, B);
         return 0;
     });
     size_t off = 0;
@@ -1020,7 +1100,7 @@ zp_status q4_plan(const zp_cache_desc *D, int group, int B, int table_stride, in
     p->off_stats = off;
     off = align_up(off + (size_t)B * D->h_q * 4, 256);
     p->off_rec = off;
-    off = align_up(off + (size_t)2 * p->grid * G * (d + 4) * 4, 256);
+    off = align_up(off + (size_t)(2 + p->warps) * p->grid * G * (d + 4) * 4, 256);
     p->off_logits = off;
     if (scored) off += (size_t)B * align_up((size_t)table_stride * D->block_size, kUnit) * D->h_q * 4;
     p->total = off;
@@ -1032,8 +1112,7 @@ zp_status launch_q4(const Q4Args &a, const Q4Plan &p, cudaStream_t st) {
     const auto kernel = q4_attention_kernel<W>;
     zp_status rc = set_max_dynamic_smem(reinterpret_cast<const void *>(kernel), p.smem, "q4_decode: shared-memory attribute");
     if (rc != ZP_OK) return rc;
-    kernel<<<p.grid, p.warps * 32, p.smem, st>>>(a);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_dependent(kernel, dim3(p.grid), dim3(p.warps * 32), p.smem, st, a);
     if (e != cudaSuccess) return cuda_fail(e, "q4_decode: attention launch");
     const auto finish = q4_finish_kernel<typename W::T, W::kD>;
     e = launch_dependent(finish, dim3(p.grid), dim3(kFinishThreads), ((size_t)a.B + 1) * 4, st, a);
