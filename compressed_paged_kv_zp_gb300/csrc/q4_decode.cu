@@ -331,12 +331,13 @@ struct ScalarWarp {
 //     The lo term is a product of its own, of the parameter words (step, lo) as they lie in the
 //     tile with (0, sum q), the sum in three bf16 parts of 8 bits.  Nothing else is rounded to 16
 //     bits: the logits are those of 32-bit arithmetic.
-//   output:  sum_t p_t (lo_t + c_t step_t): the codes as bf16 numbers 128 + c (0x4300 | c, one and-or;
-//     p step needs bf16's range), p rounded to bf16 and transposed (movmatrix), p *
-//     step rounded to bf16 again per group, both by 2^-9 at most.  The second rounding is kept to
-//     the part c - 8 of a code: sum_t p (lo + 8 step) is a product of p with the parameters as they
-//     are, and 136 times the rounded p step is taken off again (a product with -136, into the
-//     same accumulator).  The sum that divides is that of the rounded p.
+//   output:  sum_t p_t (lo_t + 8 step_t) + sum_t p_t step_t (c_t - 8).  p is rounded to bf16 and
+//     transposed (movmatrix); the first sum is a product of p with the parameters as they are, for
+//     the second p step is rounded to bf16 again per group (its products need that range).
+//     Both roundings are by 2^-9 at most, and the second touches the part about the middle of the
+//     codes only.  The codes become bf16 numbers c - 8 by one and-or (0x4300 | c is 128 + c) and one
+//     exact addition: taking the 128 off the sums instead would lose in their last places what
+//     the mean of many values has left.  The sum that divides is that of the rounded p.
 // ldmatrix of a natural row of codes gives lane 4t + j the word j of a 16-byte chunk of
 // token t, the layout of the left operand; its transposed form gives the codes of two
 // adjacent tokens for 4 dimensions, the layout of the transposed values.
@@ -359,12 +360,16 @@ __device__ __forceinline__ void mma_f16_0(float (&d)[4], uint32_t a0, uint32_t a
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-// d = a b
-__device__ __forceinline__ void mma_bf16_0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                           uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+// products over 8 instead of 16
+__device__ __forceinline__ void mma8_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(b0));
+}
+__device__ __forceinline__ void mma8_bf16_0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%7, %7, %7, %7};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+        : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t r;
@@ -380,11 +385,12 @@ __device__ __forceinline__ uint32_t f2_to_h2(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
 }
-// code e of two tokens as 128 + c
+// code e of two tokens as c - 8: (128 + c) - 136, both exact
 template <int E>
 __device__ __forceinline__ uint32_t codes(uint32_t w) {
     uint32_t r;
     asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w >> (4 * E)), "r"(0x000F000Fu), "r"(0x43004300u));  // (a & b) | c
+    asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(0xC308C308u));
     return r;
 }
 // N words of shared memory, N of 1, 2, 4
@@ -520,8 +526,9 @@ struct TcWarp {
             const uint32_t *kp = reinterpret_cast<const uint32_t *>(kt + b * kTile + q4_code_bytes(D));
             const uint32_t p0 = NG == 4 || j < NG ? kp[n * NG + (NG == 4 ? j : j % NG)] : 0;
             const uint32_t p1 = NG == 4 || j < NG ? kp[(n + 8) * NG + (NG == 4 ? j : j % NG)] : 0;
-            mma_bf16_0(y[b], p0, p1, p0, p1, ob[0], ob[1]);
-            mma_bf16(y[b], p0, p1, 0, 0, ob[2], 0);
+            mma8_bf16_0(y[b], p0, p1, ob[0]);
+            mma8_bf16(y[b], p0, p1, ob[1]);
+            mma8_bf16(y[b], p0, p1, ob[2]);
             uint32_t w0[NG], w1[NG];
             lds<NG>(kp + n * NG, w0);
             lds<NG>(kp + (n + 8) * NG, w1);
@@ -610,15 +617,13 @@ struct TcWarp {
             const uint32_t b0 = transpose8(f2_to_bf2(p[0], p[1])), b1 = transpose8(f2_to_bf2(p[2], p[3]));
             const uint32_t *vp = reinterpret_cast<const uint32_t *>(vt + b * kTile + q4_code_bytes(D));
             {
-                // row g of `off`: sum of p (lo + 8 step) of group g, less 136 times that of its rounded p step;
-                // row 8: sum of p
+                // rows g and 8 + g of `off`: sums of p lo and of p step of group g; row 7: the sum of p
                 const bool in = n < NG;
                 const uint32_t *q0 = vp + 2 * j * NG + (in ? n : 0);
-                const uint32_t x0 = in ? q0[0] : 0, x1 = in ? q0[NG] : 0, x8 = in ? q0[8 * NG] : 0, x9 = in ? q0[9 * NG] : 0;
-                const uint32_t one = n == 0 ? 0x3F803F80u : 0;
-                mma_bf16(off, __byte_perm(x0, x1, 0x7632), one, __byte_perm(x8, x9, 0x7632), one, b0, b1);
-                mma_bf16(off, __byte_perm(x0, x1, 0x5410), 0, __byte_perm(x8, x9, 0x5410), 0, mul_bf2(b0, 0x41004100u),
-                         mul_bf2(b1, 0x41004100u));
+                const uint32_t x0 = q0[0], x1 = q0[NG], x8 = q0[8 * NG], x9 = q0[9 * NG];
+                const uint32_t rest = n == 7 ? 0x3F803F80u : 0;  // 1
+                mma_bf16(off, in ? __byte_perm(x0, x1, 0x7632) : rest, __byte_perm(x0, x1, 0x5410),
+                         in ? __byte_perm(x8, x9, 0x7632) : rest, __byte_perm(x8, x9, 0x5410), b0, b1);
             }
             uint32_t w0[NG], w1[NG], w2[NG], w3[NG];
             lds<NG>(vp + 2 * j * NG, w0);
@@ -637,8 +642,6 @@ struct TcWarp {
                     if ((c + i) % kPerGroup == 0) {
                         s0 = mul_bf2(b0, __byte_perm(w0[g], w1[g], 0x5410));
                         s1 = mul_bf2(b1, __byte_perm(w2[g], w3[g], 0x5410));
-                        const uint32_t minus = n == g ? 0xC308C308u : 0;  // -136
-                        mma_bf16(off, minus, 0, minus, 0, s0, s1);
                     }
                     mma_bf16(acc[c + i][0], codes<0>(r[2 * i]), codes<1>(r[2 * i]), codes<0>(r[2 * i + 1]), codes<1>(r[2 * i + 1]),
                              s0, s1);
@@ -649,20 +652,21 @@ struct TcWarp {
         }
     }
 
-    // heads 2j, 2j + 1: dimensions 32c + 4n .. + 3 in acc[c], the sums in off[2..3] (rounded p) and l
+    // heads 2j, 2j + 1: dimensions 32c + 4n .. + 3 in acc[c], the sums of the rounded p in off[2..3] and of p in l
     __device__ __forceinline__ void end(int lane) {
         const int j = lane & 3;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], o);
-            off[i + 2] = __shfl_sync(0xFFFFFFFFu, off[i + 2], j);
+            const float both = fmaf(8.f, off[i + 2], off[i]);  // of group lane / 4
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
-                const float add = __shfl_sync(0xFFFFFFFFu, off[i], 4 * (c / kPerGroup) + j);
+                const float add = __shfl_sync(0xFFFFFFFFu, both, 4 * (c / kPerGroup) + j);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) acc[c][e][i] += add, acc[c][e][i + 2] += add;
             }
+            off[i + 2] = __shfl_sync(0xFFFFFFFFu, off[i], 28 + j);
         }
     }
     __device__ __forceinline__ float reference(int i) const { return thr[i] == -INFINITY ? -INFINITY : base[i]; }
