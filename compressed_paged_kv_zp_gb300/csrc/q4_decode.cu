@@ -175,152 +175,8 @@ __device__ __forceinline__ int rec_floats(const Q4Args &a, int d) { return a.G *
 // Normaliser of the score: p = 2^(logit - c).  An empty sum gives no score.
 __device__ __forceinline__ float score_norm(float m, float l) { return l == 0.f ? INFINITY : m + log2f(l); }
 
-// ---------------------------------------------------------------- fp32 products
-// One warp, GP >= G heads.  Logits: lane t and lane t + 16 take half of the dimensions of
-// token t each; values: every lane takes D/32 dimensions of all tokens.
-template <int D, int GP>
-struct ScalarWarp {
-    using T = float;
-    static constexpr int kD = D, kWarps = 12, kCtas = 1;
-    static constexpr int kDims = D / 32;
-    static constexpr int kSharedBytes = (GP * D + kQ4Tile * GP) * 4;
-    struct Query {
-        float q[GP * kDims];
-    };
-    float m[GP], l[GP], acc[GP][kDims];
-    float *q_s, *p_s;
-
-    __device__ __forceinline__ void init(unsigned char *shared) {
-        q_s = reinterpret_cast<float *>(shared);
-        p_s = q_s + GP * D;
-    }
-    static __device__ __forceinline__ Query fetch(const Q4Args &a, int s, int h, int lane) {
-        const float *q = static_cast<const float *>(a.q) + ((size_t)s * a.h_q + (size_t)h * a.G) * D;
-        Query x;
-#pragma unroll
-        for (int i = 0; i < GP * kDims; ++i) x.q[i] = lane + 32 * i < a.G * D ? __ldg(q + lane + 32 * i) : 0.f;
-        return x;
-    }
-    __device__ __forceinline__ void begin(const Q4Args &a, const Query &x, int lane) {
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < GP * kDims; ++i) q_s[lane + 32 * i] = x.q[i];
-        __syncwarp();
-#pragma unroll
-        for (int g = 0; g < GP; ++g) {
-            m[g] = -INFINITY;
-            l[g] = 0.f;
-#pragma unroll
-            for (int j = 0; j < kDims; ++j) acc[g][j] = 0.f;
-        }
-    }
-
-    // Key tiles, then value tiles; of tile i the tokens >= v0 (i = 0), v1 weigh nothing.
-    __device__ __forceinline__ void unit(const Q4Args &a, unsigned char *tiles, int v0, int v1, float *logits, int lane) {
-        tile(a, tiles, tiles + 2 * a.tile, v0, logits, lane);
-        if (v1 || logits) tile(a, tiles + a.tile, tiles + 3 * a.tile, v1, logits ? logits + kQ4Tile * a.G : nullptr, lane);
-    }
-    __device__ __forceinline__ void tile(const Q4Args &a, const unsigned char *kt, const unsigned char *vt, int valid,
-                                         float *logits, int lane) {
-        const int t = lane & 15, half = lane >> 4;
-        const int words = D >> a.lg_group;
-        float x[GP];
-#pragma unroll
-        for (int g = 0; g < GP; ++g) x[g] = 0.f;
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-            const int chunk = half * (D / 64) + c;
-            const uint4 w = *reinterpret_cast<const uint4 *>(kt + t * (D / 2) + q4_chunk<D>(t, chunk) * 16);
-            const uint32_t par = reinterpret_cast<const uint32_t *>(kt + q4_code_bytes(D))[t * words + (chunk * 32 >> a.lg_group)];
-            const float step = __uint_as_float(par << 16), lo = __uint_as_float(par & 0xFFFF0000u);
-            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                for (int j = 0; j < 8; j += 4) {
-                    float k[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) k[e] = fmaf((float)(ws[i] >> (4 * (j + e)) & 15u), step, lo);
-#pragma unroll
-                    for (int g = 0; g < GP; ++g) {
-                        const float4 q = *reinterpret_cast<const float4 *>(q_s + g * D + chunk * 32 + i * 8 + j);
-                        x[g] = fmaf(k[0], q.x, fmaf(k[1], q.y, fmaf(k[2], q.z, fmaf(k[3], q.w, x[g]))));
-                    }
-                }
-            }
-        }
-#pragma unroll
-        for (int g = 0; g < GP; ++g) {
-            x[g] = (x[g] + __shfl_xor_sync(0xFFFFFFFFu, x[g], 16)) * a.qscale;
-            if (t >= valid) x[g] = -INFINITY;
-            float top = x[g];
-#pragma unroll
-            for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-            const float was = m[g];
-            m[g] = fmaxf(was, top);
-            const float base = m[g] == -INFINITY ? 0.f : m[g];
-            const float alpha = ex2_approx(was - base);
-            const float p = ex2_approx(x[g] - base);
-            l[g] = l[g] * alpha + p;  // of token t only: the lanes' sums are added at the end
-            if (half == 0) {
-                p_s[t * GP + g] = p;
-                if (logits && g < a.G) logits[t * a.G + g] = x[g];
-            }
-#pragma unroll
-            for (int j = 0; j < kDims; ++j) acc[g][j] *= alpha;
-        }
-        __syncwarp();
-        const int e0 = lane * kDims;
-        for (int tt = 0; tt < valid; ++tt) {
-            const unsigned char *row = vt + tt * (D / 2) + q4_chunk<D>(tt, e0 / 32) * 16 + (e0 % 32) / 2;
-            const uint32_t w = kDims == 4 ? *reinterpret_cast<const uint16_t *>(row) : *row;
-            const uint32_t par = reinterpret_cast<const uint32_t *>(vt + q4_code_bytes(D))[tt * words + (e0 >> a.lg_group)];
-            const float step = __uint_as_float(par << 16), lo = __uint_as_float(par & 0xFFFF0000u);
-            float v[kDims];
-#pragma unroll
-            for (int j = 0; j < kDims; ++j) v[j] = fmaf((float)(w >> (4 * j) & 15u), step, lo);
-#pragma unroll
-            for (int g = 0; g < GP; ++g) {
-                const float p = p_s[tt * GP + g];
-#pragma unroll
-                for (int j = 0; j < kDims; ++j) acc[g][j] = fmaf(p, v[j], acc[g][j]);
-            }
-        }
-        __syncwarp();
-    }
-
-    // sums over the lanes (both halves hold the same tokens' sums)
-    __device__ __forceinline__ void end(int lane) {
-#pragma unroll
-        for (int g = 0; g < GP; ++g)
-#pragma unroll
-            for (int o = 8; o; o >>= 1) l[g] += __shfl_xor_sync(0xFFFFFFFFu, l[g], o);
-    }
-    __device__ __forceinline__ void write_out(const Q4Args &a, int s, int h, int lane) const {
-        float *out = static_cast<float *>(a.out) + ((size_t)s * a.h_q + (size_t)h * a.G) * D;
-#pragma unroll
-        for (int g = 0; g < GP; ++g) {
-            if (g >= a.G) break;
-            const float r = l[g] == 0.f ? 0.f : 1.f / l[g];
-#pragma unroll
-            for (int j = 0; j < kDims; ++j) out[g * D + lane * kDims + j] = acc[g][j] * r;
-            if (a.want_score && lane == 0) a.stats[(size_t)s * a.h_q + h * a.G + g] = score_norm(m[g], l[g]);
-        }
-    }
-    __device__ __forceinline__ void write_record(const Q4Args &a, float *rec, int lane) const {
-#pragma unroll
-        for (int g = 0; g < GP; ++g) {
-            if (g >= a.G) break;
-            if (lane == 0) reinterpret_cast<float4 *>(rec)[g] = make_float4(m[g], l[g], l[g], 0.f);
-#pragma unroll
-            for (int j = 0; j < kDims; ++j) rec[4 * a.G + g * D + lane * kDims + j] = acc[g][j];
-        }
-    }
-};
-
 // ---------------------------------------------------------------- tensor-core products
-// bf16 queries, up to 8 q heads as the 8 columns of mma.sync m16n8k16: logits[t][h] with
-// the key codes as the left operand, out^T[i][h] with the value codes.  (One kv head has 8
+// Up to 8 q heads as the 8 columns of mma.sync m16n8k16: logits[t][h] with the key codes as the left operand, out^T[i][h] with the value codes.  (One kv head has 8
 // query rows at most: the 128 rows of a tcgen05 tile would stand empty, and its operands
 // would have to be written to shared memory at four times the size of the codes.)
 //   logits:  sum_i q_i (lo + c_i step) = lo sum_i q_i + step sum_i q_i c_i per group.  The codes
@@ -338,6 +194,9 @@ struct ScalarWarp {
 //     codes only.  The codes become bf16 numbers c - 8 by one and-or (0x4300 | c is 128 + c) and one
 //     exact addition: taking the 128 off the sums instead would lose in their last places what
 //     the mean of many values has left.  The sum that divides is that of the rounded p.
+//   fp32 queries: two fp16 parts of the query (2 x 11 bits) for the logits; for the output p and
+//     p step in three bf16 parts each, and every unit's products are summed from zero and added to
+//     the accumulators in 32 bits, since the tensor core's own additions cut what they drop.
 // ldmatrix of a natural row of codes gives lane 4t + j the word j of a 16-byte chunk of
 // token t, the layout of the left operand; its transposed form gives the codes of two
 // adjacent tokens for 4 dimensions, the layout of the transposed values.
@@ -409,31 +268,50 @@ __device__ __forceinline__ void lds(const uint32_t *p, uint32_t (&w)[N]) {
 
 constexpr float kLazyMax = 8.f;  // the reference follows the maximum when it is passed by this much (log2)
 
-template <int D, int LG>
+// x, y as the sum of N bf16 pairs
+template <int N>
+__device__ __forceinline__ void split_bf2(float x, float y, uint32_t (&part)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        part[i] = f2_to_bf2(x, y);
+        const float2 f = bf2_to_f2(part[i]);
+        x -= f.x;
+        y -= f.y;
+    }
+}
+
+template <typename T_, int D, int LG>
 struct TcWarp {
-    using T = __nv_bfloat16;
-    static constexpr int kD = D, kWarps = 16, kCtas = 1;
-    static constexpr int kSharedBytes = 0, kTile = q4_tile_bytes(D, 1 << LG);
+    using T = T_;
+    static constexpr bool kF32 = sizeof(T) == 4;
+    static constexpr int kD = D, kWarps = kF32 ? 12 : 16;
+    static constexpr int kTile = q4_tile_bytes(D, 1 << LG);
     static constexpr int NG = D >> LG, kChunks = D / 32, kPerGroup = (1 << LG) / 32;  // chunks of a row, of a group
-    uint32_t qb[kChunks][2][2];  // queries as the right operand, by chunk and half of its words
+    static constexpr int kQ = kF32 ? 2 : 1;                                           // parts of a query
+    uint32_t qb[kQ][kChunks][2][2];  // queries as the right operand, by part, chunk and half of its words
     uint32_t ob[3];  // (0, sum of the queries) of (head lane / 4, group lane % 4), in three parts, scaled as the products
     float unit_y[2], more_y[2];  // what a product is worth: log2(e) / sqrt(d) over the scale of heads 2 (lane % 4), + 1;
                                  // more_y: a factor beyond it (1 but for queries past 2^100)
     float acc[kChunks][2][4], off[4];
     float thr[2], base[2], l[2];  // of those two heads: m + kLazyMax (-inf: none yet), m, sum over this lane's tokens
 
-    __device__ __forceinline__ void init(unsigned char *) {}
-
-    struct Query {
-        uint4 w[kChunks];
+    struct Query {  // eight elements of each chunk
+        uint4 w[kChunks][kF32 ? 2 : 1];
+        __device__ __forceinline__ float get(int c, int i) const {
+            if constexpr (kF32) return __uint_as_float((&w[c][i / 4].x)[i % 4]);
+            const uint32_t x = (&w[c][0].x)[i / 2];
+            return __uint_as_float(i % 2 ? x & 0xFFFF0000u : x << 16);
+        }
     };
     static __device__ __forceinline__ Query fetch(const Q4Args &a, int s, int h, int lane) {
         const int n = lane >> 2, j = lane & 3;
-        const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
-                                                         ((size_t)s * a.h_q + (size_t)h * a.G + n) * D);
+        const T *q = static_cast<const T *>(a.q) + ((size_t)s * a.h_q + (size_t)h * a.G + n) * D + j * 8;
         Query x;
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) x.w[c] = n < a.G ? __ldg(q + c * 4 + j) : make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+            for (int i = 0; i < (kF32 ? 2 : 1); ++i)
+                x.w[c][i] = n < a.G ? __ldg(reinterpret_cast<const uint4 *>(q + c * 32) + i) : make_uint4(0, 0, 0, 0);
         return x;
     }
     __device__ __forceinline__ void begin(const Q4Args &a, const Query &x, int lane) {
@@ -443,13 +321,10 @@ struct TcWarp {
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t w = (&x.w[c].x)[i];
-                top = max(top, max(w & 0x7F80u, (w >> 16) & 0x7F80u));
-            }
+            for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x.get(c, i)) & 0x7F800000u);
         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-        const int e = max((int)(top >> 7) - 127, -100);  // |q| < 2^(e + 1), scaled to below 2^15
+        const int e = max((int)(top >> 23) - 127, -100);  // |q| < 2^(e + 1), scaled to below 2^15
         const float scale = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
         float sum[NG];
 #pragma unroll
@@ -458,16 +333,22 @@ struct TcWarp {
         for (int c = 0; c < kChunks; ++c) {
             float v[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = bf2_to_f2((&x.w[c].x)[i]);
-                v[2 * i] = f.x * scale;
-                v[2 * i + 1] = f.y * scale;
-            }
-            qb[c][0][0] = f2_to_h2(v[0], v[4]);
-            qb[c][0][1] = f2_to_h2(v[1] * 0.0625f, v[5] * 0.0625f);
-            qb[c][1][0] = f2_to_h2(v[2], v[6]);
-            qb[c][1][1] = f2_to_h2(v[3] * 0.0625f, v[7] * 0.0625f);
+            for (int i = 0; i < 8; ++i) v[i] = x.get(c, i) * scale;
             sum[c / kPerGroup] += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+#pragma unroll
+            for (int i = 1; i < 8; i += 2) v[i] *= 0.0625f;  // the elements of the high nibbles
+#pragma unroll
+            for (int k = 0; k < kQ; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t w = f2_to_h2(v[i], v[i + 4]);
+                    qb[k][c][i / 2][i % 2] = w;
+                    if constexpr (kF32) {
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+                        v[i] -= f.x;
+                        v[i + 4] -= f.y;
+                    }
+                }
         }
         float part = 0.f;
 #pragma unroll
@@ -526,9 +407,9 @@ struct TcWarp {
             const uint32_t *kp = reinterpret_cast<const uint32_t *>(kt + b * kTile + q4_code_bytes(D));
             const uint32_t p0 = NG == 4 || j < NG ? kp[n * NG + (NG == 4 ? j : j % NG)] : 0;
             const uint32_t p1 = NG == 4 || j < NG ? kp[(n + 8) * NG + (NG == 4 ? j : j % NG)] : 0;
-            mma8_bf16_0(y[b], p0, p1, ob[0]);
+            mma8_bf16_0(y[b], p0, p1, ob[2]);  // (small parts first)
             mma8_bf16(y[b], p0, p1, ob[1]);
-            mma8_bf16(y[b], p0, p1, ob[2]);
+            mma8_bf16(y[b], p0, p1, ob[0]);
             uint32_t w0[NG], w1[NG];
             lds<NG>(kp + n * NG, w0);
             lds<NG>(kp + (n + 8) * NG, w1);
@@ -543,12 +424,21 @@ struct TcWarp {
                     const int g = (c + i) / kPerGroup;
                     const uint32_t x0 = r[2 * i], x1 = r[2 * i + 1], z0 = x0 >> 8, z1 = x1 >> 8;
                     constexpr uint32_t lo4 = 0x000F000Fu, hi4 = 0x00F000F0u;
-                    if ((c + i) % kPerGroup == 0)
-                        mma_f16_0(d, x0 & lo4, x1 & lo4, x0 & hi4, x1 & hi4, qb[c + i][0][0], qb[c + i][0][1]);
+                    const auto &q = qb[0][c + i];
+                    if (kF32 || (c + i) % kPerGroup == 0)
+                        mma_f16_0(d, x0 & lo4, x1 & lo4, x0 & hi4, x1 & hi4, q[0][0], q[0][1]);
                     else
-                        mma_f16(d, x0 & lo4, x1 & lo4, x0 & hi4, x1 & hi4, qb[c + i][0][0], qb[c + i][0][1]);
-                    mma_f16(d, z0 & lo4, z1 & lo4, z0 & hi4, z1 & hi4, qb[c + i][1][0], qb[c + i][1][1]);
-                    if ((c + i + 1) % kPerGroup == 0) {
+                        mma_f16(d, x0 & lo4, x1 & lo4, x0 & hi4, x1 & hi4, q[0][0], q[0][1]);
+                    mma_f16(d, z0 & lo4, z1 & lo4, z0 & hi4, z1 & hi4, q[1][0], q[1][1]);
+                    if constexpr (kF32) {  // the second part's products by themselves, chunk by chunk
+                        const auto &q1 = qb[kQ - 1][c + i];
+                        float d1[4];
+                        mma_f16_0(d1, x0 & lo4, x1 & lo4, x0 & hi4, x1 & hi4, q1[0][0], q1[0][1]);
+                        mma_f16(d1, z0 & lo4, z1 & lo4, z0 & hi4, z1 & hi4, q1[1][0], q1[1][1]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) d[e] += d1[e];
+                    }
+                    if (kF32 || (c + i + 1) % kPerGroup == 0) {
                         const float s0 = __uint_as_float(w0[g] << 16), s1 = __uint_as_float(w1[g] << 16);
                         y[b][0] = fmaf(s0, d[0], y[b][0]);
                         y[b][1] = fmaf(s0, d[1], y[b][1]);
@@ -606,6 +496,29 @@ struct TcWarp {
                     for (int e = 0; e < 2; ++e) acc[c][e][i] *= alpha, acc[c][e][i + 2] *= alpha;
             }
         }
+        if constexpr (kF32) values_f32(vt, y, at, lane);
+        else values_bf16(vt, y, at, lane);
+    }
+
+    // the left operand of the sums with the parameters: rows g and 8 + g (lo, step) of group g, row 7 ones
+    static __device__ __forceinline__ void parameter_rows(const uint32_t *vp, int n, int j, uint32_t (&w)[4]) {
+        const bool in = n < NG;
+        const uint32_t *q0 = vp + 2 * j * NG + (in ? n : 0);
+        const uint32_t x0 = q0[0], x1 = q0[NG], x8 = q0[8 * NG], x9 = q0[9 * NG];
+        const uint32_t rest = n == 7 ? 0x3F803F80u : 0;  // 1
+        w[0] = in ? __byte_perm(x0, x1, 0x7632) : rest;
+        w[1] = __byte_perm(x0, x1, 0x5410);
+        w[2] = in ? __byte_perm(x8, x9, 0x7632) : rest;
+        w[3] = __byte_perm(x8, x9, 0x5410);
+    }
+    // codes of tokens 2j, 2j + 1 (x0) and + 8 (x1), dimensions 4n + E and 4n + E + 1 of a chunk
+    template <int E>
+    static __device__ __forceinline__ void code_rows(uint32_t x0, uint32_t x1, uint32_t (&w)[4]) {
+        w[0] = codes<E>(x0), w[1] = codes<E + 1>(x0), w[2] = codes<E>(x1), w[3] = codes<E + 1>(x1);
+    }
+
+    __device__ __forceinline__ void values_bf16(const unsigned char *vt, const float (&y)[2][4], uint32_t at, int lane) {
+        const int n = lane >> 2, j = lane & 3;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             float p[4];
@@ -616,15 +529,9 @@ struct TcWarp {
             // right operand of the values' products: tokens 2j, 2j + 1 (and + 8) of head n
             const uint32_t b0 = transpose8(f2_to_bf2(p[0], p[1])), b1 = transpose8(f2_to_bf2(p[2], p[3]));
             const uint32_t *vp = reinterpret_cast<const uint32_t *>(vt + b * kTile + q4_code_bytes(D));
-            {
-                // rows g and 8 + g of `off`: sums of p lo and of p step of group g; row 7: the sum of p
-                const bool in = n < NG;
-                const uint32_t *q0 = vp + 2 * j * NG + (in ? n : 0);
-                const uint32_t x0 = q0[0], x1 = q0[NG], x8 = q0[8 * NG], x9 = q0[9 * NG];
-                const uint32_t rest = n == 7 ? 0x3F803F80u : 0;  // 1
-                mma_bf16(off, in ? __byte_perm(x0, x1, 0x7632) : rest, __byte_perm(x0, x1, 0x5410),
-                         in ? __byte_perm(x8, x9, 0x7632) : rest, __byte_perm(x8, x9, 0x5410), b0, b1);
-            }
+            uint32_t w[4];
+            parameter_rows(vp, n, j, w);
+            mma_bf16(off, w[0], w[1], w[2], w[3], b0, b1);
             uint32_t w0[NG], w1[NG], w2[NG], w3[NG];
             lds<NG>(vp + 2 * j * NG, w0);
             lds<NG>(vp + (2 * j + 1) * NG, w1);
@@ -643,12 +550,64 @@ struct TcWarp {
                         s0 = mul_bf2(b0, __byte_perm(w0[g], w1[g], 0x5410));
                         s1 = mul_bf2(b1, __byte_perm(w2[g], w3[g], 0x5410));
                     }
-                    mma_bf16(acc[c + i][0], codes<0>(r[2 * i]), codes<1>(r[2 * i]), codes<0>(r[2 * i + 1]), codes<1>(r[2 * i + 1]),
-                             s0, s1);
-                    mma_bf16(acc[c + i][1], codes<2>(r[2 * i]), codes<3>(r[2 * i]), codes<2>(r[2 * i + 1]), codes<3>(r[2 * i + 1]),
-                             s0, s1);
+                    code_rows<0>(r[2 * i], r[2 * i + 1], w);
+                    mma_bf16(acc[c + i][0], w[0], w[1], w[2], w[3], s0, s1);
+                    code_rows<2>(r[2 * i], r[2 * i + 1], w);
+                    mma_bf16(acc[c + i][1], w[0], w[1], w[2], w[3], s0, s1);
                 }
             }
+        }
+    }
+
+    __device__ __forceinline__ void values_f32(const unsigned char *vt, const float (&y)[2][4], uint32_t at, int lane) {
+        constexpr int kP = 3;  // parts of a probability
+        const int n = lane >> 2, j = lane & 3;
+        float p[2][4], d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[b][i] = ex2_approx(y[b][i] - base[i & 1]);
+            l[0] += p[b][0] + p[b][2];
+            l[1] += p[b][1] + p[b][3];
+            uint32_t w[4], u0[kP], u1[kP];
+            parameter_rows(reinterpret_cast<const uint32_t *>(vt + b * kTile + q4_code_bytes(D)), n, j, w);
+            split_bf2(p[b][0], p[b][1], u0);
+            split_bf2(p[b][2], p[b][3], u1);
+#pragma unroll
+            for (int k = kP - 1; k >= 0; --k) mma_bf16(d, w[0], w[1], w[2], w[3], transpose8(u0[k]), transpose8(u1[k]));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) off[i] += d[i];
+        const uint32_t va = smem_u32(vt) + at;
+        uint32_t r[2][4], s0[2][kP], s1[2][kP];
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            uint32_t w[2][2][4];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                if (c % 2 == 0) ldsm_x4_t((va + b * kTile) ^ (c << 4), r[b][0], r[b][1], r[b][2], r[b][3]);
+                if (c % kPerGroup == 0) {
+                    const uint32_t *vp = reinterpret_cast<const uint32_t *>(vt + b * kTile + q4_code_bytes(D)) + c / kPerGroup;
+                    const float t0 = __uint_as_float(vp[n * NG] << 16), t1 = __uint_as_float(vp[(n + 8) * NG] << 16);
+                    split_bf2(p[b][0] * t0, p[b][1] * t0, s0[b]);
+                    split_bf2(p[b][2] * t1, p[b][3] * t1, s1[b]);
+#pragma unroll
+                    for (int k = 0; k < kP; ++k) s0[b][k] = transpose8(s0[b][k]), s1[b][k] = transpose8(s1[b][k]);
+                }
+                code_rows<0>(r[b][2 * (c % 2)], r[b][2 * (c % 2) + 1], w[b][0]);
+                code_rows<2>(r[b][2 * (c % 2)], r[b][2 * (c % 2) + 1], w[b][1]);
+            }
+            float e[2][4] = {};
+#pragma unroll
+            for (int k = kP - 1; k >= 0; --k)  // small parts first
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) mma_bf16(e[m], w[b][m][0], w[b][m][1], w[b][m][2], w[b][m][3], s0[b][k], s1[b][k]);
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[c][m][i] += e[m][i];
         }
     }
 
@@ -672,16 +631,19 @@ struct TcWarp {
     __device__ __forceinline__ float reference(int i) const { return thr[i] == -INFINITY ? -INFINITY : base[i]; }
     __device__ __forceinline__ void write_out(const Q4Args &a, int s, int h, int lane) const {
         const int n = lane >> 2, j = lane & 3;
-        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + ((size_t)s * a.h_q + (size_t)h * a.G) * D;
+        T *out = static_cast<T *>(a.out) + ((size_t)s * a.h_q + (size_t)h * a.G) * D;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int g = 2 * j + i;
             if (g >= a.G) break;
             const float r = off[i + 2] == 0.f ? 0.f : 1.f / off[i + 2];
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c)
-                *reinterpret_cast<uint2 *>(out + g * D + c * 32 + n * 4) =
-                    make_uint2(f2_to_bf2(acc[c][0][i] * r, acc[c][0][i + 2] * r), f2_to_bf2(acc[c][1][i] * r, acc[c][1][i + 2] * r));
+            for (int c = 0; c < kChunks; ++c) {
+                const float4 x = make_float4(acc[c][0][i] * r, acc[c][0][i + 2] * r, acc[c][1][i] * r, acc[c][1][i + 2] * r);
+                T *to = out + g * D + c * 32 + n * 4;
+                if constexpr (kF32) *reinterpret_cast<float4 *>(to) = x;
+                else *reinterpret_cast<uint2 *>(to) = make_uint2(f2_to_bf2(x.x, x.y), f2_to_bf2(x.z, x.w));
+            }
             if (a.want_score && n == 0) a.stats[(size_t)s * a.h_q + h * a.G + g] = score_norm(reference(i), l[i]);
         }
     }
@@ -702,15 +664,15 @@ struct TcWarp {
 
 // ---------------------------------------------------------------- attention
 // Shared memory: rings (a warp's tiles; at its end the record of a pair that goes on
-// behind its range), the warps' own, prefix.  The record of a pair that began before a warp's range is
+// behind its range), prefix.  The record of a pair that began before a warp's range is
 // written while the ring is in use, so to the workspace.
 template <class W>
 __host__ __device__ inline size_t attention_smem(int stages, int tile, int B) {
-    return (size_t)W::kWarps * ((size_t)stages * 4 * tile + W::kSharedBytes) + ((size_t)B + 1) * 4;
+    return (size_t)W::kWarps * stages * 4 * tile + ((size_t)B + 1) * 4;
 }
 
 template <class W>
-__global__ void __launch_bounds__(W::kWarps * 32, W::kCtas) q4_attention_kernel(const Q4Args a) {
+__global__ void __launch_bounds__(W::kWarps * 32, 1) q4_attention_kernel(const Q4Args a) {
     constexpr int D = W::kD, kWarps = W::kWarps;
     using T = typename W::T;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -724,8 +686,7 @@ __global__ void __launch_bounds__(W::kWarps * 32, W::kCtas) q4_attention_kernel(
     const int rec_n = rec_floats(a, D), stages = a.stages;
     const size_t ring_bytes = (size_t)stages * 4 * a.tile;
     unsigned char *ring = smem + warp * ring_bytes;
-    unsigned char *own = smem + kWarps * ring_bytes + warp * W::kSharedBytes;
-    int *prefix = reinterpret_cast<int *>(smem + kWarps * (ring_bytes + W::kSharedBytes));
+    int *prefix = reinterpret_cast<int *>(smem + kWarps * ring_bytes);
     float *heads = a.rec + (size_t)(2 * a.grid + (int)blockIdx.x * kWarps) * rec_n;
     if (lane < stages) mbar_init(&full_s[warp][lane], 2);
     if (lane == 0) head_s[warp] = tail_s[warp] = -1;
@@ -805,7 +766,6 @@ __global__ void __launch_bounds__(W::kWarps * 32, W::kCtas) q4_attention_kernel(
         pair = put_pair;
 
         W w;
-        w.init(own);
         w.begin(a, query, lane);
         int st = 0;
         unsigned phase = 0;
@@ -1052,25 +1012,18 @@ struct Q4Plan {
     size_t off_prefix, off_stats, off_rec, off_logits, total;
 };
 
-int padded_group(int G) { return G <= 1 ? 1 : G <= 2 ? 2 : G <= 4 ? 4 : 8; }
-
 // f(W) for the warp type of a cache
+template <typename T, typename F>
+auto with_group(const zp_cache_desc *D, int group, F f) {
+    if (D->head_dim == 128 && group == 32) return f(TcWarp<T, 128, 5>());
+    if (D->head_dim == 128 && group == 64) return f(TcWarp<T, 128, 6>());
+    if (D->head_dim == 128) return f(TcWarp<T, 128, 7>());
+    if (group == 32) return f(TcWarp<T, 64, 5>());
+    return f(TcWarp<T, 64, 6>());
+}
 template <typename F>
 auto with_warp(const zp_cache_desc *D, int group, F f) {
-    const bool wide = D->head_dim == 128;
-    if (D->dtype == ZP_BF16) {
-        if (wide && group == 32) return f(TcWarp<128, 5>());
-        if (wide && group == 64) return f(TcWarp<128, 6>());
-        if (wide) return f(TcWarp<128, 7>());
-        if (group == 32) return f(TcWarp<64, 5>());
-        return f(TcWarp<64, 6>());
-    }
-    switch (padded_group(D->h_q / D->h_kv)) {
-        case 1: return wide ? f(ScalarWarp<128, 1>()) : f(ScalarWarp<64, 1>());
-        case 2: return wide ? f(ScalarWarp<128, 2>()) : f(ScalarWarp<64, 2>());
-        case 4: return wide ? f(ScalarWarp<128, 4>()) : f(ScalarWarp<64, 4>());
-        default: return wide ? f(ScalarWarp<128, 8>()) : f(ScalarWarp<64, 8>());
-    }
+    return D->dtype == ZP_BF16 ? with_group<__nv_bfloat16>(D, group, f) : with_group<float>(D, group, f);
 }
 
 zp_status q4_plan(const zp_cache_desc *D, int group, int B, int table_stride, int scored, const DeviceInfo &dev, Q4Plan *p) {
@@ -1090,9 +1043,9 @@ zp_status q4_plan(const zp_cache_desc *D, int group, int B, int table_stride, in
     const int d = D->head_dim, tile = q4_tile_bytes(d, group);
     with_warp(D, group, [&](auto w) {
         using W = decltype(w);
-        const size_t room = ((size_t)dev.smem_optin + 1024) / W::kCtas - 2048;  // (1 KB of a CTA is the system's, 1 KB static)
+        const size_t room = (size_t)dev.smem_optin - 1024;  // (beside 1 KB static)
         p->warps = W::kWarps;
-        p->grid = dev.sm_count * W::kCtas;
+        p->grid = dev.sm_count;
         p->stages = kMaxStages;
         while (p->stages > 2 && attention_smem<W>(p->stages, tile, B) > room) --p->stages;
         p->smem = attention_smem<W>(p->stages, tile, B);
