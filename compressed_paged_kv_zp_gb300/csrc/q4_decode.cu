@@ -34,8 +34,9 @@ struct Q4Args {
     int table_stride;
     const int32_t *seq_lens;
     int B, h_q, h_kv, G, b, n_total;
-    int lg_group, tile;
-    float qscale;  // log2(e) / sqrt(d)
+    int tile, tpb;  // bytes of a tile, tiles of a block and kv head
+    unsigned inv_tpb, inv_ranges;  // reciprocals (div_by) of tpb and of grid * warps
+    float qscale;   // log2(e) / sqrt(d)
     int want_score, window;
     float *score;
     long long score_stride;
@@ -46,16 +47,26 @@ struct Q4Args {
     float *rec;     // [2 * CTAs + warps][G * (d + 4)]: per head (reference, sum for the output, sum, 0), then accumulators
     float *logits;  // [units][32][G]
     int grid, warps, stages;  // CTAs of the attention kernel, warps of one, units in a warp's ring
+    bool heads_here;          // records of pairs that began before a warp's range: in shared memory
     unsigned *err;
 };
 
 // ---------------------------------------------------------------- the split
+// n / d for n below 2^31, inv = 2^32 / d rounded up (d > 1) or 0 (d = 1): the product is one
+// too large at most.
+__device__ __forceinline__ int div_by(int n, int d, unsigned inv) {
+    if (!inv) return n;
+    const int q = (int)__umulhi((unsigned)n, inv);
+    return q - (q * d > n);
+}
+
 struct Split {
     int U, W;           // units, ranges (no more than units: none is empty)
     int per_cta, ctas;  // ranges of a CTA (its first warps take one each), CTAs that have some
     int quot, rest;     // U / W, U % W
-    // the first unit of range g: floor(g U / W)  (W is below 2^15: 32 bits hold g * rest)
-    __device__ __forceinline__ int start(int g) const { return g * quot + (int)((unsigned)g * (unsigned)rest / (unsigned)W); }
+    unsigned inv_W;
+    // the first unit of range g: floor(g U / W)  (W is below 2^15: g * rest below 2^30)
+    __device__ __forceinline__ int start(int g) const { return g * quot + div_by(g * rest, W, inv_W); }
     __device__ __forceinline__ int cta_start(int c) const { return start(c * per_cta); }
     // the CTA whose ranges hold unit x: the largest range g with start(g) <= x is its
     __device__ __forceinline__ int cta_of(int x) const { return (int)(((x + 1ll) * W - 1) / U) / per_cta; }
@@ -64,12 +75,20 @@ struct Split {
 __device__ __forceinline__ Split make_split(const Q4Args &a, int units) {
     Split p;
     p.U = units * a.h_kv;
-    const int want = (int)(((unsigned)p.U + a.grid - 1) / (unsigned)a.grid);
-    p.per_cta = want < 1 ? 1 : want > a.warps ? a.warps : want;
-    const int most = p.U / p.per_cta;
-    p.ctas = most < a.grid ? most : a.grid;
+    if (p.U >= a.grid * a.warps) {
+        p.per_cta = a.warps;
+        p.ctas = a.grid;
+        p.inv_W = a.inv_ranges;
+    } else {
+        const int want = (int)(((unsigned)p.U + a.grid - 1) / (unsigned)a.grid);
+        p.per_cta = want < 1 ? 1 : want;
+        const int most = p.U / p.per_cta;
+        p.ctas = most < a.grid ? most : a.grid;
+        const int W = p.per_cta * p.ctas;
+        p.inv_W = W <= 1 ? 0u : 0xFFFFFFFFu / (unsigned)W + 1;
+    }
     p.W = p.per_cta * p.ctas;
-    p.quot = p.U / p.W;
+    p.quot = div_by(p.U, p.W, p.inv_W);
     p.rest = p.U - p.quot * p.W;
     return p;
 }
@@ -664,11 +683,11 @@ struct TcWarp {
 
 // ---------------------------------------------------------------- attention
 // Shared memory: rings (a warp's tiles; at its end the record of a pair that goes on
-// behind its range), prefix.  The record of a pair that began before a warp's range is
-// written while the ring is in use, so to the workspace.
+// behind its range), records of pairs that began before a warp's range (written while the ring is in
+// use; in the workspace where there is no room), prefix.
 template <class W>
-__host__ __device__ inline size_t attention_smem(int stages, int tile, int B) {
-    return (size_t)W::kWarps * stages * 4 * tile + ((size_t)B + 1) * 4;
+__host__ __device__ inline size_t attention_smem(int stages, int tile, int B, int G, bool heads_here) {
+    return (size_t)W::kWarps * ((size_t)stages * 4 * tile + (heads_here ? (size_t)G * (W::kD + 4) * 4 : 0)) + ((size_t)B + 1) * 4;
 }
 
 template <class W>
@@ -686,8 +705,9 @@ __global__ void __launch_bounds__(W::kWarps * 32, 1) q4_attention_kernel(const Q
     const int rec_n = rec_floats(a, D), stages = a.stages;
     const size_t ring_bytes = (size_t)stages * 4 * a.tile;
     unsigned char *ring = smem + warp * ring_bytes;
-    int *prefix = reinterpret_cast<int *>(smem + kWarps * ring_bytes);
-    float *heads = a.rec + (size_t)(2 * a.grid + (int)blockIdx.x * kWarps) * rec_n;
+    float *heads = a.heads_here ? reinterpret_cast<float *>(smem + kWarps * ring_bytes)
+                                : a.rec + (size_t)(2 * a.grid + (int)blockIdx.x * kWarps) * rec_n;
+    int *prefix = reinterpret_cast<int *>(smem + kWarps * (ring_bytes + (a.heads_here ? (size_t)rec_n * 4 : 0)));
     if (lane < stages) mbar_init(&full_s[warp][lane], 2);
     if (lane == 0) head_s[warp] = tail_s[warp] = -1;
     if (tid == 0) abort_s = 0;
@@ -703,12 +723,7 @@ __global__ void __launch_bounds__(W::kWarps * 32, 1) q4_attention_kernel(const Q
     const int x0 = mine ? split.start(g) : 0;
     const int n = mine ? split.start(g + 1) - x0 : 0;
     if (n > 0) {
-        // the queries of the first pair, ahead of the tiles of all warps
-        Cursor begin;
-        begin.seek(prefix, a.B, a.h_kv, x0);
-        const typename W::Query query = W::fetch(a, begin.s, begin.h, lane);
         const uint64_t pol = l2_evict_first_policy();
-        const int tpb = a.b / kQ4Tile;
         // Units go in windows of 32: lane i finds out about unit i of the window that is
         // being issued, and keeps it until the products get there.
         int put_tile[2] = {-1, -1}, put_meta = 0, put_pair = 0, meta = 0, pair = 0;
@@ -718,10 +733,12 @@ __global__ void __launch_bounds__(W::kWarps * 32, 1) q4_attention_kernel(const Q
             if (i0 + lane >= n) return;
             Cursor c;
             c.seek(prefix, a.B, a.h_kv, x0 + i0 + lane);
-            int blk[2];  // (read beside the length: a row of the table has an entry for every token below its stride)
+            put_pair = c.s * a.h_kv + c.h;
+            int blk[2], sub[2];  // (read beside the length: a row of the table has an entry for every token below its stride)
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const int col = (2 * c.u + b) / tpb;
+                const int col = div_by(2 * c.u + b, a.tpb, a.inv_tpb);
+                sub[b] = 2 * c.u + b - col * a.tpb;
                 blk[b] = col < a.table_stride ? __ldg(a.table + (size_t)c.s * a.table_stride + col) : -1;
             }
             const int L = q4_len(a, c.s);
@@ -732,7 +749,7 @@ __global__ void __launch_bounds__(W::kWarps * 32, 1) q4_attention_kernel(const Q
                 put_tile[b] = -1;
                 if (valid <= 0) continue;
                 if (blk[b] >= 0 && blk[b] < a.n_total) {
-                    put_tile[b] = (blk[b] * a.h_kv + c.h) * tpb + t % tpb;
+                    put_tile[b] = (blk[b] * a.h_kv + c.h) * a.tpb + sub[b];
                     put_meta |= valid << (5 * b);
                 } else {
                     record_error(a.err, ZP_ERR_DEVICE, 0x159);  // (its tokens weigh nothing)
@@ -740,11 +757,10 @@ __global__ void __launch_bounds__(W::kWarps * 32, 1) q4_attention_kernel(const Q
             }
 
             if (a.want_score && q4_score_row(a, c.s, L) >= 0) put_meta |= kScored;
-            put_pair = c.s * a.h_kv + c.h;
         };
         int put_st = 0;
         auto issue = [&](int i) {  // lanes 0 and 1: one tile of keys and values each
-            if ((i & 31) == 0) look(i);
+            if (i && (i & 31) == 0) look(i);
             const int t0 = __shfl_sync(0xFFFFFFFFu, put_tile[0], i & 31), t1 = __shfl_sync(0xFFFFFFFFu, put_tile[1], i & 31);
             if (lane < 2) {
                 const int from = lane ? t1 : t0;
@@ -761,6 +777,10 @@ __global__ void __launch_bounds__(W::kWarps * 32, 1) q4_attention_kernel(const Q
             }
             put_st = put_st + 1 == stages ? 0 : put_st + 1;
         };
+        look(0);
+        // the queries of the first pair, ahead of the tiles
+        const int first = __shfl_sync(0xFFFFFFFFu, put_pair, 0);
+        const typename W::Query query = W::fetch(a, first / a.h_kv, first % a.h_kv, lane);
         for (int i = 0; i < n && i < stages; ++i) issue(i);
         meta = put_meta;
         pair = put_pair;
@@ -1008,6 +1028,7 @@ __global__ void __launch_bounds__(kFinishThreads) q4_finish_kernel(const Q4Args 
 // ---------------------------------------------------------------- host
 struct Q4Plan {
     int grid, warps, stages;
+    bool heads_here;
     size_t smem;
     size_t off_prefix, off_stats, off_rec, off_logits, total;
 };
@@ -1046,9 +1067,11 @@ zp_status q4_plan(const zp_cache_desc *D, int group, int B, int table_stride, in
         const size_t room = (size_t)dev.smem_optin - 1024;  // (beside 1 KB static)
         p->warps = W::kWarps;
         p->grid = dev.sm_count;
+        // two units in flight at least; the records' place before a third
+        p->heads_here = attention_smem<W>(2, tile, B, G, true) <= room;
         p->stages = kMaxStages;
-        while (p->stages > 2 && attention_smem<W>(p->stages, tile, B) > room) --p->stages;
-        p->smem = attention_smem<W>(p->stages, tile, B);
+        while (p->stages > 2 && attention_smem<W>(p->stages, tile, B, G, p->heads_here) > room) --p->stages;
+        p->smem = attention_smem<W>(p->stages, tile, B, G, p->heads_here);
         return 0;
     });
     size_t off = 0;
@@ -1137,8 +1160,10 @@ extern "C" zp_status zp_q4_decode_attn(const zp_cache_desc *D, int32_t group, co
     a.G = D->h_q / D->h_kv;
     a.b = D->block_size;
     a.n_total = D->n_total_blocks;
-    a.lg_group = group == 32 ? 5 : group == 64 ? 6 : 7;
     a.tile = q4_tile_bytes(D->head_dim, group);
+    a.tpb = D->block_size / kQ4Tile;
+    a.inv_tpb = a.tpb == 1 ? 0u : 0xFFFFFFFFu / (unsigned)a.tpb + 1;
+    a.inv_ranges = 0xFFFFFFFFu / (unsigned)(p.grid * p.warps) + 1;
     a.qscale = (float)(1.4426950408889634 / sqrt((double)D->head_dim));
     a.want_score = score_accum != nullptr;
     a.window = window;
@@ -1153,6 +1178,7 @@ extern "C" zp_status zp_q4_decode_attn(const zp_cache_desc *D, int32_t group, co
     a.grid = p.grid;
     a.warps = p.warps;
     a.stages = p.stages;
+    a.heads_here = p.heads_here;
     a.err = dev.error_word;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     return with_warp(D, group, [&](auto w) { return launch_q4<decltype(w)>(a, p, st); });
