@@ -21,7 +21,10 @@ The host side of the hot path around the libzp kernels:
   * with prefix_decode, sequences whose tables share leading blocks (§4.4) attend
     to those once per group: the groups are found on the device whenever tables
     or blocks change, for all layers (the compression then forms the row sums
-    itself).
+    itself);
+  * with kv_bits=4 the cache is held in 4 bits: tokens are quantised as they are
+    appended, the decode and its window score read the codes, and a compression
+    moves the kept rows as they are.
 All device work is libzp calls; torch provides memory, streams and events.
 """
 from __future__ import annotations
@@ -31,7 +34,9 @@ import torch
 
 from . import (Pool, cache_desc, prefix_plan, score_params, zp_append_kv, zp_compress_layers, zp_compress_rho_supported,
                zp_compress_workspace_size, zp_needs_compression_batch, zp_decode_workspace_size,
-               zp_paged_decode_attn, zp_prefix_decode_attn, zp_prefix_decode_workspace_size, zp_prefix_plan)
+               zp_paged_decode_attn, zp_prefix_decode_attn, zp_prefix_decode_workspace_size, zp_prefix_plan,
+               zp_q4_append_kv, zp_q4_cache, zp_q4_compact_pages, zp_q4_decode_attn, zp_q4_decode_workspace_size,
+               zp_score_tokens, zp_score_workspace_size, zp_select_topk)
 
 
 def upload(arr: np.ndarray, dev) -> torch.Tensor:
@@ -68,11 +73,16 @@ class DecodeLoop:
     decode_rho, which is then off (`use_rho` tells): behind a prefix a decode does
     not read the shared keys sequence by sequence and forms no row sums of them, so
     a compression reads its sequence's keys itself, as with decode_rho=False.
+
+    kv_bits=4: K and V are 4-bit caches with parameters per group of kv_group
+    elements (zp_q4_cache; the caller fills them with zp_q4_write_kv).  The key
+    redundancy, which compares keys as they are kept in 16 or 32 bits, is off:
+    params must not ask for it; nor is prefix_decode offered.
     """
 
     def __init__(self, h_q, h_kv, d, b, n_total, max_blocks, table_stride, layers=1, dtype=torch.bfloat16,
                  window=None, params=None, async_compress=False, layer_stride=None, device="cuda",
-                 decode_rho=True, prefix_decode=False, prefix_min_blocks=4):
+                 decode_rho=True, prefix_decode=False, prefix_min_blocks=4, kv_bits=16, kv_group=32):
         self.h_q, self.h_kv, self.d, self.b = h_q, h_kv, d, b
         self.n_total, self.N_max, self.stride, self.layers = n_total, max_blocks, table_stride, layers
         self.k = (max_blocks - 1) * b
@@ -80,15 +90,23 @@ class DecodeLoop:
         self.dtype = dtype
         self.dev = torch.device(device)
         self.desc = cache_desc(h_q, h_kv, d, b, n_total, dtype)
-        self.params = params or score_params(window=self.window)
+        if kv_bits not in (4, 16):
+            raise ValueError("kv_bits must be 16 (the cache in dtype) or 4")
+        self.q4, self.group = kv_bits == 4, kv_group
+        self.params = params or score_params(window=self.window, use_similarity=not self.q4)
+        if self.q4 and (self.params.use_similarity or prefix_decode):
+            raise ValueError("a 4-bit cache has neither the key redundancy (use_similarity) nor prefix_decode")
         self.async_compress = async_compress
         self.prefix_decode, self.prefix_min_blocks = prefix_decode, prefix_min_blocks
-        self.decode_rho = decode_rho and not prefix_decode
+        self.decode_rho = decode_rho and not prefix_decode and not self.q4
         # layers compressed per call (App. C.1's layer stride): bounds the
         # scoring scratch to layer_stride layers
         self.layer_stride = max(1, min(layer_stride or layers, layers))
-        self.K = torch.zeros(layers, n_total, b, h_kv, d, dtype=dtype, device=self.dev)
-        self.V = torch.zeros_like(self.K)
+        if self.q4:
+            self.K, self.V = zp_q4_cache(self.desc, kv_group, layers, device=self.dev)
+        else:
+            self.K = torch.zeros(layers, n_total, b, h_kv, d, dtype=dtype, device=self.dev)
+            self.V = torch.zeros_like(self.K)
         # global score cache F: paged like K (it moves with the kept tokens)
         self.F = torch.zeros(layers, n_total, b, h_kv, dtype=torch.float32, device=self.dev)
         self.pool = Pool(n_total)
@@ -146,16 +164,20 @@ class DecodeLoop:
         # position, so sequences sharing prefix blocks keep their own scores
         self.S = torch.zeros(self.layers, B, self.h_kv, self.stride * self.b, dtype=torch.float32,
                              device=self.dev)
-        ws_size = zp_prefix_decode_workspace_size if self.prefix_decode else zp_decode_workspace_size
-        self.ws = torch.empty(ws_size(self.desc, B, self.stride), dtype=torch.uint8, device=self.dev)
+        if self.q4:
+            size = zp_q4_decode_workspace_size(self.desc, B, self.stride, self.group)
+        else:
+            ws_size = zp_prefix_decode_workspace_size if self.prefix_decode else zp_decode_workspace_size
+            size = ws_size(self.desc, B, self.stride)
+        self.ws = torch.empty(size, dtype=torch.uint8, device=self.dev)
         self.plan = prefix_plan(B, self.dev) if self.prefix_decode else None
         self._plan_stale = True
         Lmax = self.stride * self.b
         self.Lmax = Lmax
         self.use_rho = bool(self.decode_rho and zp_compress_rho_supported(self.desc, self.params, Lmax, self.k))
-        self.score_ws = None if self.use_rho else torch.empty(
-            max(zp_compress_workspace_size(self.desc, B, Lmax, self.layer_stride), 1), dtype=torch.uint8,
-            device=self.dev)
+        need = (zp_score_workspace_size(self.desc, B, Lmax) if self.q4 else
+                zp_compress_workspace_size(self.desc, B, Lmax, self.layer_stride))
+        self.score_ws = None if self.use_rho else torch.empty(max(need, 1), dtype=torch.uint8, device=self.dev)
         self.out = torch.zeros(self.layers, B, self.h_q, self.d, dtype=self.dtype, device=self.dev)
 
     def layer_stride(self):
@@ -200,6 +222,11 @@ class DecodeLoop:
             rho = buf["rho"][: self.layers * n * self.h_kv * Lr].view(self.layers, n, self.h_kv, Lr)
             extra = dict(rho_rows=buf["rows"], rho_threshold=self.params.threshold)
         for l in range(self.layers):
+            if self.q4:
+                zp_q4_append_kv(self.desc, k_new[l], v_new[l], self.K[l], self.V[l], self.table_dev, step_lens, group=self.group)
+                zp_q4_decode_attn(self.desc, q[l], self.K[l], self.V[l], self.table_dev, step_lens, self.out[l],
+                                  score_accum=self.S[l], window=self.window, workspace=self.ws, group=self.group)
+                continue
             zp_append_kv(self.desc, k_new[l], v_new[l], self.K[l], self.V[l], self.table_dev, step_lens)
             if self.prefix_decode:
                 zp_prefix_decode_attn(self.desc, q[l], self.K[l], self.V[l], self.table_dev, step_lens, self.plan,
@@ -247,6 +274,9 @@ class DecodeLoop:
             keep = torch.empty(self.layers, n, self.h_kv, self.k, dtype=torch.int32, device=self.dev)
             for l0 in range(0, self.layers, self.layer_stride):  # scores, keep sets, moves of a layer group
                 l1 = min(l0 + self.layer_stride, self.layers)
+                if self.q4:
+                    self._compress_q4(l0, l1, n, tables_dev, lens_dev, rows_dev, targets_dev, first_dev, k_seq, keep)
+                    continue
                 zp_compress_layers(self.desc, self.params, self.K[l0:l1], self.V[l0:l1], tables_dev, lens_dev,
                                    first_dev, self.S[l0:l1], self.F[l0:l1], targets_dev, self.k, keep[l0:l1],
                                    self.Lmax, rows=rows_dev, workspace=self.score_ws, k_seq=k_seq,
@@ -261,6 +291,16 @@ class DecodeLoop:
         if not self.async_compress:
             main.wait_event(done)
         return done
+
+    def _compress_q4(self, l0, l1, n, tables, lens, rows, targets, first, k_seq, keep):
+        """The scores and keep sets of layers [l0, l1), one after another, then their moves in one call."""
+        scores = torch.empty(n, self.h_kv, self.Lmax, dtype=torch.float32, device=self.dev)
+        for l in range(l0, l1):
+            zp_score_tokens(self.desc, self.params, self.K[l], tables, lens, first, self.S[l], self.F[l], scores, rows=rows,
+                            workspace=self.score_ws)  # (without the redundancy the keys are not read)
+            zp_select_topk(scores, lens, self.k, keep[l], k_seq=k_seq)
+        zp_q4_compact_pages(self.desc, self.K[l0:l1], self.V[l0:l1], tables, targets, lens, keep[l0:l1],
+                            global_F=self.F[l0:l1], scores=self.S[l0:l1], rows=rows, k_seq=k_seq, group=self.group)
 
     def _retire(self, block=False):
         """Apply the compressions that have finished: new tables, lengths and
