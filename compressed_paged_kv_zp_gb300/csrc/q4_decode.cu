@@ -1137,6 +1137,9 @@ extern "C" zp_status zp_q4_decode_attn(const zp_cache_desc *D, int32_t group, co
     if (((uintptr_t)q | (uintptr_t)k_cache | (uintptr_t)v_cache | (uintptr_t)out | (uintptr_t)score_accum |
          (uintptr_t)workspace) % 16)
         return fail(ZP_ERR_INVALID_ARG, "q4_decode: buffers must be 16-byte aligned");
+    const uintptr_t q0 = (uintptr_t)q, o0 = (uintptr_t)out, q_bytes = (uintptr_t)B * D->h_q * D->head_dim * elem_bytes(D->dtype);
+    if (q0 < o0 + q_bytes && o0 < q0 + q_bytes)
+        return fail(ZP_ERR_INVALID_ARG, "q4_decode: out overlaps q (queries are read after outputs are written)");
     DeviceInfo dev;
     rc = device_info(&dev);
     if (rc != ZP_OK) return rc;

@@ -93,6 +93,92 @@ def test_write_and_read(zp, dtype, h_kv, d, group, b, n, layers, fused):
     assert bool((got[:, :, :, h_kv] == 7.0).all())
 
 
+@pytest.mark.parametrize("dtype,h_kv,d,group", [("bf16", 40, 128, 32), ("bf16", 65, 64, 64), ("f32", 33, 128, 128)])
+def test_many_heads(zp, dtype, h_kv, d, group):
+    """Rows of more pieces than a CTA has threads, a multiple of those or not."""
+    rng = np.random.default_rng(h_kv)
+    desc = zp.cache_desc(h_kv, h_kv, d, 16, 2, torch.bfloat16 if dtype == "bf16" else torch.float32)
+    ref = q4.random_cache(rng, 2, h_kv, d, group, 16)
+    K, V = _dev(ref), _dev(ref)
+    k = _rows(rng, (11, h_kv, d), dtype)
+    slots = rng.permutation(32)[:11].astype(np.int32)
+    zp.zp_q4_write_kv(desc, k.cuda(), k.cuda(), _dev(slots), K, V, group=group)
+    _ref_write(ref, k, slots, group, 16)
+    assert np.array_equal(K.cpu().numpy(), ref) and np.array_equal(V.cpu().numpy(), ref)
+    out = torch.empty(2, 11, h_kv, d, dtype=k.dtype, device="cuda")
+    zp.zp_q4_read_kv(desc, K, V, _dev(slots), out[0], out[1], group=group)
+    want = torch.from_numpy(q4.values(*q4.get_rows(ref, slots, d, group, 16), group)).float().to(k.dtype)
+    assert torch.equal(out[0].cpu(), want) and torch.equal(out[1].cpu(), want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_on_16_bytes(zp, dtype):
+    """Rows and layers that begin on 16 but not on 32 bytes, for both directions."""
+    rng = np.random.default_rng(3)
+    t = torch.bfloat16 if dtype == "bf16" else torch.float32
+    n, h_kv, d, layers, pad = 21, 3, 64, 2, 8 if dtype == "bf16" else 4
+    desc = zp.cache_desc(h_kv, h_kv, d, 16, 3, t)
+    ref = np.stack([q4.random_cache(rng, 3, h_kv, d, 32, 16) for _ in range(layers)])
+    K, V = _dev(ref), _dev(ref)
+    k = _rows(rng, (layers, n, h_kv, d), dtype)
+    place = lambda: torch.zeros(pad + layers * n * (h_kv * d + pad), dtype=t, device="cuda").as_strided(  # noqa: E731
+        (layers, n, h_kv, d), (n * (h_kv * d + pad), h_kv * d + pad, d, 1), pad)
+    kd, vd = place(), place()
+    kd.copy_(k)
+    vd.copy_(k)
+    assert kd.data_ptr() % 32 == 16
+    slots = rng.permutation(48)[:n].astype(np.int32)
+    zp.zp_q4_write_kv(desc, kd, vd, _dev(slots), K, V)
+    for l in range(layers):
+        _ref_write(ref[l], k[l], slots, 32, 16)
+    assert np.array_equal(K.cpu().numpy(), ref) and np.array_equal(V.cpu().numpy(), ref)
+    ko, vo = place(), place()
+    zp.zp_q4_read_kv(desc, K, V, _dev(slots), ko, vo)
+    for l in range(layers):
+        want = torch.from_numpy(q4.values(*q4.get_rows(ref[l], slots, d, 32, 16), 32)).float().to(t)
+        assert torch.equal(ko[l].cpu(), want) and torch.equal(vo[l].cpu(), want)
+
+
+def test_far_blocks(zp):
+    """A cache of more than 4 GB: its last blocks are written, read, moved and attended to."""
+    h_q, h_kv, d, group, b = 8, 4, 128, 32, 16
+    n_total = (1 << 32) // (h_kv * q4.tile_bytes(d, group)) + 40
+    desc = zp.cache_desc(h_q, h_kv, d, b, n_total, torch.float32)
+    K, V = zp.zp_q4_cache(desc, group)
+    assert K.numel() > 1 << 32
+    rng = np.random.default_rng(4)
+    L = 100
+    table = np.full((1, 9), -1, np.int32)
+    table[0, :7] = n_total - 1 - rng.permutation(30)[:7]
+    slots = (table[0, np.arange(L) // b].astype(np.int64) * b + np.arange(L) % b).astype(np.int32)
+    k, v = _rows(rng, (L, h_kv, d), "f32"), torch.from_numpy(rng.standard_normal((L, h_kv, d)).astype(np.float32))
+    k = torch.where(k.abs() < 10, k, 0.5)
+    lens = torch.tensor([L], dtype=torch.int32, device="cuda")
+    zp.zp_q4_write_kv(desc, k[:L - 1].cuda(), v[:L - 1].cuda(), _dev(slots[:L - 1]), K, V, group=group)
+    zp.zp_q4_append_kv(desc, k[L - 1:].cuda(), v[L - 1:].cuda(), K, V, _dev(table), lens, group=group)
+    want = []
+    for x in (k, v):
+        code, word = q4.quantise(x.numpy(), group)
+        want.append(torch.from_numpy(q4.values(code, q4.bf16_value(word & 0xFFFF), q4.bf16_value(word >> 16), group)))
+    ko, vo = torch.empty(L, h_kv, d, device="cuda"), torch.empty(L, h_kv, d, device="cuda")
+    zp.zp_q4_read_kv(desc, K, V, _dev(slots), ko, vo, group=group)
+    assert torch.equal(ko.cpu(), want[0].float()) and torch.equal(vo.cpu(), want[1].float())
+    assert int(K[:64].max()) == 0 and int(V[:64].max()) == 0   # nothing where a 32-bit offset would have gone
+    q = torch.randn(1, h_q, d, device="cuda")
+    out = torch.empty_like(q)
+    zp.zp_q4_decode_attn(desc, q, K, V, _dev(table), lens, out, group=group)
+    x = torch.einsum("hgd,thd->hgt", q.cpu().double().view(h_kv, 2, d), want[0]) / d ** 0.5
+    ref = torch.einsum("hgt,thd->hgd", torch.softmax(x, -1), want[1]).reshape(1, h_q, d)
+    # logits of up to 64 in 32 bits (2^-24 of the 128 terms' magnitudes, at most 2^11 in all): 2^-13 in a weight
+    assert (out.cpu().double() - ref).abs().max() < 2.0 ** -13 * want[1].abs().max()
+    keep = torch.from_numpy(np.stack([np.sort(rng.permutation(L)[:40]) for _ in range(h_kv)])[None].astype(np.int32)).cuda()
+    zp.zp_q4_compact_pages(desc, K, V, _dev(table), _dev(table[:, :3].copy()), lens, keep, group=group)
+    zp.zp_q4_read_kv(desc, K, V, _dev(slots[:40]), ko[:40], vo[:40], group=group)
+    for h in range(h_kv):
+        at = keep[0, h].cpu().long()
+        assert torch.equal(ko[:40, h].cpu(), want[0].float()[at, h]) and torch.equal(vo[:40, h].cpu(), want[1].float()[at, h])
+
+
 def test_not_finite(zp):
     """A NaN, an infinity or a spread past the largest float takes its group, and no other."""
     d, group, b = 128, 32, 16
@@ -194,6 +280,32 @@ def test_compact(zp, dtype, h_kv, d, group, b, L, k, in_place):
                             F[l, slot // b, slot % b, h] = S[l, rows[i], h, pos[r]]
     assert np.array_equal(K.cpu().numpy(), ref[0]) and np.array_equal(V.cpu().numpy(), ref[1])
     assert np.array_equal(Fd.cpu().numpy(), F)
+
+
+def test_compact_under_budget(zp):
+    """Sequences shorter than k (their keep lists padded with -1), budgets of 0 and sequences of no tokens."""
+    rng = np.random.default_rng(12)
+    h_kv, d, group, b, k = 2, 64, 32, 16, 40
+    lens = np.array([25, 0, 64, 17], np.int32)
+    k_seq = np.array([40, 40, 0, 16], np.int32)
+    table = rng.permutation(40)[:20].reshape(4, 5).astype(np.int32)
+    dst = np.setdiff1d(np.arange(60), table)[:12].reshape(4, 3).astype(np.int32)
+    keep = np.full((4, h_kv, k), -1, np.int32)
+    keep[0, :, :25] = np.arange(25)
+    keep[3, 0, :16], keep[3, 1, :16] = np.arange(16), np.arange(1, 17)
+    desc = zp.cache_desc(h_kv, h_kv, d, b, 60, torch.bfloat16)
+    ref = q4.random_cache(rng, 60, h_kv, d, group, b)
+    K, V = _dev(ref), _dev(ref)
+    zp.zp_q4_compact_pages(desc, K, V, _dev(table), _dev(dst), _dev(lens), _dev(keep), k_seq=_dev(k_seq), group=group)
+    old = ref.copy()
+    for i, m in ((0, 25), (3, 16)):
+        for h in range(h_kv):
+            pos = keep[i, h, :m]
+            code, step, lo = q4.get_rows(old[:, h:h + 1], table[i, pos // b] * b + pos % b, d, group, b)
+            word = (step.view(np.uint32) >> 16) | lo.view(np.uint32)
+            for r in range(m):
+                q4.put_row(ref, int(dst[i, r // b]) * b + r % b, h, code[r, 0], word[r, 0], b)
+    assert np.array_equal(K.cpu().numpy(), ref) and np.array_equal(V.cpu().numpy(), ref)
 
 
 def test_bad_indices(zp):

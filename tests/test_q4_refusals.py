@@ -81,14 +81,17 @@ def test_append(zp):
 
 
 def test_decode(zp):
-    def call(desc=None, group=32, q=P, k=P, v=P, table=P, stride=4, lens=P, B=2, out=P, S=None, rows=None, nr=0, w=0, ws=P):
+    O = _at(1 << 20)
+
+    def call(desc=None, group=32, q=P, k=P, v=P, table=P, stride=4, lens=P, B=2, out=O, S=None, rows=None, nr=0, w=0, ws=P):
         return zp.lib.zp_q4_decode_attn(desc or _desc(zp), group, q, k, v, table, stride, lens, B, out, S, rows, nr, w, ws,
                                         1 << 40, None)
 
     _common(zp, call)
     for kw in (dict(B=-1), dict(stride=-1), dict(stride=0), dict(q=None), dict(k=None), dict(v=None), dict(table=None),
                dict(lens=None), dict(out=None), dict(ws=None), dict(S=P, w=0), dict(S=P, w=17), dict(S=P, w=4, rows=P, nr=0),
-               dict(q=_at(8)), dict(k=_at(8)), dict(S=_at(4), w=4), dict(ws=_at(4)), dict(out=_at(2))):
+               dict(q=_at(8)), dict(k=_at(8)), dict(S=_at(4), w=4), dict(ws=_at(4)), dict(out=_at(2)),
+               dict(out=P), dict(out=_at(2 * 32 * 128 * 2 - 16)), dict(q=_at(16), out=P)):
         assert call(**kw) == 1, kw
     assert call(B=0, q=None) == 0
 
