@@ -213,7 +213,7 @@ __device__ __forceinline__ float score_norm(float m, float l) { return l == 0.f 
 //     codes only.  The codes become bf16 numbers c - 8 by one and-or (0x4300 | c is 128 + c) and one
 //     exact addition: taking the 128 off the sums instead would lose in their last places what
 //     the mean of many values has left.  The sum that divides is that of the rounded p.
-//   fp32 queries: two fp16 parts of the query (2 x 11 bits) for the logits; for the output p and
+//   fp32 queries: three parts of 8 bits of the query for the logits; for the output p and
 //     p step in three bf16 parts each, and every unit's products are summed from zero and added to
 //     the accumulators in 32 bits, since the tensor core's own additions cut what they drop.
 // ldmatrix of a natural row of codes gives lane 4t + j the word j of a 16-byte chunk of
@@ -306,7 +306,7 @@ struct TcWarp {
     static constexpr int kD = D, kWarps = kF32 ? 12 : 16;
     static constexpr int kTile = q4_tile_bytes(D, 1 << LG);
     static constexpr int NG = D >> LG, kChunks = D / 32, kPerGroup = (1 << LG) / 32;  // chunks of a row, of a group
-    static constexpr int kQ = kF32 ? 2 : 1;                                           // parts of a query
+    static constexpr int kQ = kF32 ? 3 : 1;                                           // parts of a query
     uint32_t qb[kQ][kChunks][2][2];  // queries as the right operand, by part, chunk and half of its words
     uint32_t ob[3];  // (0, sum of the queries) of (head lane / 4, group lane % 4), in three parts, scaled as the products
     float unit_y[2], more_y[2];  // what a product is worth: log2(e) / sqrt(d) over the scale of heads 2 (lane % 4), + 1;
@@ -360,13 +360,14 @@ struct TcWarp {
             for (int k = 0; k < kQ; ++k)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint32_t w = f2_to_h2(v[i], v[i + 4]);
-                    qb[k][c][i / 2][i % 2] = w;
-                    if constexpr (kF32) {
-                        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
-                        v[i] -= f.x;
-                        v[i + 4] -= f.y;
+                    float x0 = v[i], x1 = v[i + 4];
+                    if constexpr (kF32) {  // 8 bits, whose products with the codes add up exactly
+                        const float2 f = bf2_to_f2(f2_to_bf2(x0, x1));
+                        x0 = f.x, x1 = f.y;
+                        v[i] -= x0;
+                        v[i + 4] -= x1;
                     }
+                    qb[k][c][i / 2][i % 2] = f2_to_h2(x0, x1);
                 }
         }
         float part = 0.f;
@@ -379,7 +380,7 @@ struct TcWarp {
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
             const float hi = __bfloat162float(__float2bfloat16_rn(part));
-            ob[i] = __float_as_uint(hi);  // (the high half: the place of lo in a parameter word)
+            ob[i] = f2_to_bf2(0.f, hi);  // (lo is the high half of a parameter word, step the low one)
             part -= hi;
         }
         // 2^(24 - 14 + e) log2(e) / sqrt(d); above 2^117 it is not a float, and the rest is multiplied on
@@ -441,21 +442,26 @@ struct TcWarp {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int g = (c + i) / kPerGroup;
-                    const uint32_t x0 = r[2 * i], x1 = r[2 * i + 1], z0 = x0 >> 8, z1 = x1 >> 8;
-                    constexpr uint32_t lo4 = 0x000F000Fu, hi4 = 0x00F000F0u;
+                    uint32_t u[4], v[4];  // codes of words 0 and 1, 2 and 3 (nibbles) of tokens n, n + 8
+                    nibbles(r[2 * i], u[0], u[2], v[0], v[2]);
+                    nibbles(r[2 * i + 1], u[1], u[3], v[1], v[3]);
                     const auto &q = qb[0][c + i];
-                    if (kF32 || (c + i) % kPerGroup == 0)
-                        mma_f16_0(d, x0 & lo4, x1 & lo4, x0 & hi4, x1 & hi4, q[0][0], q[0][1]);
-                    else
-                        mma_f16(d, x0 & lo4, x1 & lo4, x0 & hi4, x1 & hi4, q[0][0], q[0][1]);
-                    mma_f16(d, z0 & lo4, z1 & lo4, z0 & hi4, z1 & hi4, q[1][0], q[1][1]);
-                    if constexpr (kF32) {  // the second part's products by themselves, chunk by chunk
-                        const auto &q1 = qb[kQ - 1][c + i];
-                        float d1[4];
-                        mma_f16_0(d1, x0 & lo4, x1 & lo4, x0 & hi4, x1 & hi4, q1[0][0], q1[0][1]);
-                        mma_f16(d1, z0 & lo4, z1 & lo4, z0 & hi4, z1 & hi4, q1[1][0], q1[1][1]);
+                    if constexpr (kF32) {
+                        // the small parts together, then the two halves of the first by themselves: the tensor core's
+                        // own additions cut what they drop
+                        float d1[4], d2[4];
+                        mma_f16_0(d, u[0], u[1], u[2], u[3], qb[kQ - 1][c + i][0][0], qb[kQ - 1][c + i][0][1]);
+                        mma_f16(d, v[0], v[1], v[2], v[3], qb[kQ - 1][c + i][1][0], qb[kQ - 1][c + i][1][1]);
+                        mma_f16(d, u[0], u[1], u[2], u[3], qb[kQ / 2][c + i][0][0], qb[kQ / 2][c + i][0][1]);
+                        mma_f16(d, v[0], v[1], v[2], v[3], qb[kQ / 2][c + i][1][0], qb[kQ / 2][c + i][1][1]);
+                        mma_f16_0(d1, u[0], u[1], u[2], u[3], q[0][0], q[0][1]);
+                        mma_f16_0(d2, v[0], v[1], v[2], v[3], q[1][0], q[1][1]);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) d[e] += d1[e];
+                        for (int e = 0; e < 4; ++e) d[e] += d1[e] + d2[e];
+                    } else {
+                        if ((c + i) % kPerGroup == 0) mma_f16_0(d, u[0], u[1], u[2], u[3], q[0][0], q[0][1]);
+                        else mma_f16(d, u[0], u[1], u[2], u[3], q[0][0], q[0][1]);
+                        mma_f16(d, v[0], v[1], v[2], v[3], q[1][0], q[1][1]);
                     }
                     if (kF32 || (c + i + 1) % kPerGroup == 0) {
                         const float s0 = __uint_as_float(w0[g] << 16), s1 = __uint_as_float(w1[g] << 16);
@@ -519,6 +525,13 @@ struct TcWarp {
         else values_bf16(vt, y, at, lane);
     }
 
+    // The nibbles of a word as fp16 pairs: c 2^-24 of nibbles 0, 4 and 2, 6 (a, c), c 2^-20 of 1, 5 and 3, 7 (b, d).
+    static __device__ __forceinline__ void nibbles(uint32_t w, uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d) {
+        a = w & 0x000F000Fu;
+        b = w & 0x00F000F0u;
+        c = w >> 8 & 0x000F000Fu;
+        d = w >> 8 & 0x00F000F0u;
+    }
     // the left operand of the sums with the parameters: rows g and 8 + g (lo, step) of group g, row 7 ones
     static __device__ __forceinline__ void parameter_rows(const uint32_t *vp, int n, int j, uint32_t (&w)[4]) {
         const bool in = n < NG;
