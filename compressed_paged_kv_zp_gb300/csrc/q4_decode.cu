@@ -206,15 +206,14 @@ __device__ __forceinline__ float score_norm(float m, float l) { return l == 0.f 
 //     The lo term is a product of its own, of the parameter words (step, lo) as they lie in the
 //     tile with (0, sum q), the sum in three bf16 parts of 8 bits.  Nothing else is rounded to 16
 //     bits: the logits are those of 32-bit arithmetic.
-//   output:  sum_t p_t (lo_t + 8 step_t) + sum_t p_t step_t (c_t - 8).  p is rounded to bf16 and
-//     transposed (movmatrix); the first sum is a product of p with the parameters as they are, for
-//     the second p step is rounded to bf16 again per group (its products need that range).
-//     Both roundings are by 2^-9 at most, and the second touches the part about the middle of the
-//     codes only.  The codes become bf16 numbers c - 8 by one and-or (0x4300 | c is 128 + c) and one
-//     exact addition: taking the 128 off the sums instead would lose in their last places what
-//     the mean of many values has left.  The sum that divides is that of the rounded p.
-//   fp32 queries: three parts of 8 bits of the query for the logits; for the output p and
-//     p step in three bf16 parts each, and every unit's products are summed from zero and added to
+//   output:  sum_t p_t lo_t + sum_t p_t step_t c_t.  The first is a product of p (two bf16 parts, transposed
+//     by movmatrix) with the parameters as they are.  For the second p goes to fp16 and its product with
+//     the step of a group to fp16 again, each rounded by 2^-12 at most; the codes are subnormals once more.  For
+//     that a step's exponent is moved by what suits the range's first unit.  A unit with steps far
+//     from those (p step needs bf16's range) takes its products in bf16, with codes 0x4300 | c = 128 + c less
+//     128; both roundings are then by 2^-9.  The sum that divides is that of p in two parts.
+//   fp32 queries: three parts of 8 bits of the query for the logits; for the output p and p step in
+//     three bf16 parts each, with codes c - 8 and the parameters' sum of lo + 8 step, and every unit's products are summed from zero and added to
 //     the accumulators in 32 bits, since the tensor core's own additions cut what they drop.
 // ldmatrix of a natural row of codes gives lane 4t + j the word j of a 16-byte chunk of
 // token t, the layout of the left operand; its transposed form gives the codes of two
@@ -263,12 +262,17 @@ __device__ __forceinline__ uint32_t f2_to_h2(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
 }
-// code e of two tokens as c - 8: (128 + c) - 136, both exact
-template <int E>
+__device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// code E of two tokens as the bf16 numbers c - CENTRE (0 or 8): (128 + c) - (128 + CENTRE), all exact
+template <int E, int CENTRE>
 __device__ __forceinline__ uint32_t codes(uint32_t w) {
     uint32_t r;
     asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w >> (4 * E)), "r"(0x000F000Fu), "r"(0x43004300u));  // (a & b) | c
-    asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(0xC308C308u));
+    asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(CENTRE ? 0xC308C308u : 0xC300C300u));
     return r;
 }
 // N words of shared memory, N of 1, 2, 4
@@ -285,7 +289,13 @@ __device__ __forceinline__ void lds(const uint32_t *p, uint32_t (&w)[N]) {
     }
 }
 
-constexpr float kLazyMax = 8.f;  // the reference follows the maximum when it is passed by this much (log2)
+// Probabilities are kept relative to 2^(m - kScale), and m follows the maximum when that passes it by
+// kLazyMax: below 2^15, so that fp16 holds them, with 11 bits down to 2^-25 and no zero above 2^-36 of 2^m.
+constexpr float kLazyMax = 4.f, kScale = 11.f;
+// Steps that a range's value products take in fp16: exponents from kBelow under the largest of the range's first unit
+// to kWindow - 1 - kBelow above it.  (p step is then below 2^16; the smallest step is still a normal number.)
+constexpr int kBelow = 10, kWindow = 14;
+constexpr uint32_t kNoWindow = 0xFFFFFFFFu;
 
 // x, y as the sum of N bf16 pairs
 template <int N>
@@ -312,7 +322,8 @@ struct TcWarp {
     float unit_y[2], more_y[2];  // what a product is worth: log2(e) / sqrt(d) over the scale of heads 2 (lane % 4), + 1;
                                  // more_y: a factor beyond it (1 but for queries past 2^100)
     float acc[kChunks][2][4], off[4];
-    float thr[2], base[2], l[2];  // of those two heads: m + kLazyMax (-inf: none yet), m, sum over this lane's tokens
+    float thr[2], base[2], l[2];  // of those two heads: m + kLazyMax (-inf: none yet), m - kScale, sum over this lane's tokens
+    uint32_t win[NG];  // bf16 queries: lowest exponent, less 1, of the group's steps taken in fp16; kNoWindow: none yet
 
     struct Query {  // eight elements of each chunk
         uint4 w[kChunks][kF32 ? 2 : 1];
@@ -400,6 +411,8 @@ struct TcWarp {
         for (int i = 0; i < 4; ++i) off[i] = 0.f;
 #pragma unroll
         for (int i = 0; i < 2; ++i) thr[i] = -INFINITY, base[i] = 0.f, l[i] = 0.f;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) win[g] = kNoWindow;
     }
 
     // Two key tiles, then two value tiles; of tile i the tokens >= v0 (i = 0), v1 weigh nothing.
@@ -507,8 +520,8 @@ struct TcWarp {
             for (int i = 0; i < 2; ++i) {
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], o));
-                const float m = thr[i] == -INFINITY ? top[i] : fmaxf(base[i], top[i]);
-                const float now = m == -INFINITY ? 0.f : m;
+                const float m = thr[i] == -INFINITY ? top[i] : fmaxf(base[i] + kScale, top[i]);
+                const float now = m == -INFINITY ? 0.f : m - kScale;
                 const float alpha = thr[i] == -INFINITY ? 0.f : ex2_approx(base[i] - now);
                 base[i] = now;
                 thr[i] = m + kLazyMax;
@@ -522,7 +535,7 @@ struct TcWarp {
             }
         }
         if constexpr (kF32) values_f32(vt, y, at, lane);
-        else values_bf16(vt, y, at, lane);
+        else values_bf16(vt, y, v0, v1, at, lane);
     }
 
     // The nibbles of a word as fp16 pairs: c 2^-24 of nibbles 0, 4 and 2, 6 (a, c), c 2^-20 of 1, 5 and 3, 7 (b, d).
@@ -544,26 +557,83 @@ struct TcWarp {
         w[3] = __byte_perm(x8, x9, 0x5410);
     }
     // codes of tokens 2j, 2j + 1 (x0) and + 8 (x1), dimensions 4n + E and 4n + E + 1 of a chunk
-    template <int E>
+    template <int E, int CENTRE>
     static __device__ __forceinline__ void code_rows(uint32_t x0, uint32_t x1, uint32_t (&w)[4]) {
-        w[0] = codes<E>(x0), w[1] = codes<E + 1>(x0), w[2] = codes<E>(x1), w[3] = codes<E + 1>(x1);
+        w[0] = codes<E, CENTRE>(x0), w[1] = codes<E + 1, CENTRE>(x0);
+        w[2] = codes<E, CENTRE>(x1), w[3] = codes<E + 1, CENTRE>(x1);
     }
 
-    __device__ __forceinline__ void values_bf16(const unsigned char *vt, const float (&y)[2][4], uint32_t at, int lane) {
+    // The accumulators of the value products in fp16 hold 2^(89 - e) times the sums of p step c (e: the window's
+    // lowest exponent), 16 times that for odd dimensions; to and from sums of p step c.  (In two factors:
+    // the power may be past the largest float.)
+    __device__ __forceinline__ void rescale(bool plain) {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            const int e = (int)win[c / kPerGroup] + 1 - 89, e0 = plain ? e : -e, half = e0 / 2;
+            const float f = __uint_as_float((uint32_t)(127 + half) << 23), f2 = __uint_as_float((uint32_t)(127 + e0 - half) << 23);
+            const float odd = plain ? 0.0625f * f2 : 16.f * f2;
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[c][m][i] = acc[c][m][i] * f * (i < 2 ? f2 : odd);
+        }
+    }
+
+    __device__ __forceinline__ void values_bf16(unsigned char *vt, const float (&y)[2][4], int v0, int v1, uint32_t at,
+                                                int lane) {
         const int n = lane >> 2, j = lane & 3;
+        // ---- do the steps of all tokens lie in the window?  (lane t looks at token t)
+        bool wild;
+        {
+            uint32_t w[NG], *own = reinterpret_cast<uint32_t *>(vt + (lane >> 4) * kTile + q4_code_bytes(D)) + (lane & 15) * NG;
+            lds<NG>(own, w);
+            const bool live = (lane & 15) < (lane < kQ4Tile ? v0 : v1);
+            if (win[0] == kNoWindow) {
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const int top = (int)__reduce_max_sync(0xFFFFFFFFu, live ? w[g] & 0x7F80u : 0u) >> 7;
+                    win[g] = min(max(top - kBelow, 1), 255 - kWindow) - 1;
+                }
+            }
+            bool out = false;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) out |= (w[g] & 0xFFFFu) - ((win[g] + 1) << 7) >= (uint32_t)kWindow << 7;
+            wild = __any_sync(0xFFFFFFFFu, live && out);
+            if (v0 + v1 < kUnit) {  // the other tokens (p = 0): a step of the window too, whose fp16 form is a number
+                if (!live) {
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) own[g] = (win[g] + 1) << 7;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+        }
+        float p[2][4];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            float p[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) p[i] = ex2_approx(y[b][i] - base[i & 1]);
-            l[0] += p[0] + p[2];
-            l[1] += p[1] + p[3];
+            for (int i = 0; i < 4; ++i) p[b][i] = ex2_approx(y[b][i] - base[i & 1]);
+            l[0] += p[b][0] + p[b][2];
+            l[1] += p[b][1] + p[b][3];
+            // the sums with the parameters, p in two bf16 parts
+            uint32_t w[4], u0[2], u1[2];
+            parameter_rows(reinterpret_cast<const uint32_t *>(vt + b * kTile + q4_code_bytes(D)), n, j, w);
+            split_bf2(p[b][0], p[b][1], u0);
+            split_bf2(p[b][2], p[b][3], u1);
+#pragma unroll
+            for (int k = 1; k >= 0; --k) mma_bf16(off, w[0], w[0], w[2], w[2], transpose8(u0[k]), transpose8(u1[k]));
+        }
+        if (wild) {
+            rescale(true);
+            values_wide(vt, p, at, lane);
+            rescale(false);
+            return;
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
             // right operand of the values' products: tokens 2j, 2j + 1 (and + 8) of head n
-            const uint32_t b0 = transpose8(f2_to_bf2(p[0], p[1])), b1 = transpose8(f2_to_bf2(p[2], p[3]));
+            const uint32_t b0 = transpose8(f2_to_h2(p[b][0], p[b][1])), b1 = transpose8(f2_to_h2(p[b][2], p[b][3]));
             const uint32_t *vp = reinterpret_cast<const uint32_t *>(vt + b * kTile + q4_code_bytes(D));
-            uint32_t w[4];
-            parameter_rows(vp, n, j, w);
-            mma_bf16(off, w[0], w[1], w[2], w[3], b0, b1);
             uint32_t w0[NG], w1[NG], w2[NG], w3[NG];
             lds<NG>(vp + 2 * j * NG, w0);
             lds<NG>(vp + (2 * j + 1) * NG, w1);
@@ -578,13 +648,42 @@ struct TcWarp {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int g = (c + i) / kPerGroup;
-                    if ((c + i) % kPerGroup == 0) {
-                        s0 = mul_bf2(b0, __byte_perm(w0[g], w1[g], 0x5410));
-                        s1 = mul_bf2(b1, __byte_perm(w2[g], w3[g], 0x5410));
+                    if ((c + i) % kPerGroup == 0) {  // (bf16 to fp16 bits: the exponent moved, three zeros behind)
+                        const uint32_t down = win[g] * (0x10001u << 10);
+                        s0 = mul_h2(b0, __byte_perm(w0[g], w1[g], 0x5410) * 8 - down);
+                        s1 = mul_h2(b1, __byte_perm(w2[g], w3[g], 0x5410) * 8 - down);
                     }
-                    code_rows<0>(r[2 * i], r[2 * i + 1], w);
+                    uint32_t x[4], z[4];
+                    nibbles(r[2 * i], x[0], x[1], z[0], z[1]);
+                    nibbles(r[2 * i + 1], x[2], x[3], z[2], z[3]);
+                    mma_f16(acc[c + i][0], x[0], x[1], x[2], x[3], s0, s1);
+                    mma_f16(acc[c + i][1], z[0], z[1], z[2], z[3], s0, s1);
+                }
+            }
+        }
+    }
+
+    // The values' products where steps of any size meet: p, and p step, rounded to bf16, the codes as bf16 numbers.
+    __device__ __forceinline__ void values_wide(const unsigned char *vt, const float (&p)[2][4], uint32_t at, int lane) {
+        const int j = lane & 3;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const uint32_t b0 = transpose8(f2_to_bf2(p[b][0], p[b][1])), b1 = transpose8(f2_to_bf2(p[b][2], p[b][3]));
+            const uint32_t *vp = reinterpret_cast<const uint32_t *>(vt + b * kTile + q4_code_bytes(D)) + 2 * j * NG;
+            const uint32_t va = smem_u32(vt + b * kTile) + at;
+#pragma unroll
+            for (int c = 0; c < kChunks; c += 2) {
+                uint32_t r[4];
+                ldsm_x4_t(va ^ (c << 4), r[0], r[1], r[2], r[3]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int g = (c + i) / kPerGroup;
+                    const uint32_t s0 = mul_bf2(b0, __byte_perm(vp[g], vp[NG + g], 0x5410));
+                    const uint32_t s1 = mul_bf2(b1, __byte_perm(vp[8 * NG + g], vp[9 * NG + g], 0x5410));
+                    uint32_t w[4];
+                    code_rows<0, 0>(r[2 * i], r[2 * i + 1], w);
                     mma_bf16(acc[c + i][0], w[0], w[1], w[2], w[3], s0, s1);
-                    code_rows<2>(r[2 * i], r[2 * i + 1], w);
+                    code_rows<2, 0>(r[2 * i], r[2 * i + 1], w);
                     mma_bf16(acc[c + i][1], w[0], w[1], w[2], w[3], s0, s1);
                 }
             }
@@ -626,8 +725,8 @@ struct TcWarp {
 #pragma unroll
                     for (int k = 0; k < kP; ++k) s0[b][k] = transpose8(s0[b][k]), s1[b][k] = transpose8(s1[b][k]);
                 }
-                code_rows<0>(r[b][2 * (c % 2)], r[b][2 * (c % 2) + 1], w[b][0]);
-                code_rows<2>(r[b][2 * (c % 2)], r[b][2 * (c % 2) + 1], w[b][1]);
+                code_rows<0, 8>(r[b][2 * (c % 2)], r[b][2 * (c % 2) + 1], w[b][0]);
+                code_rows<2, 8>(r[b][2 * (c % 2)], r[b][2 * (c % 2) + 1], w[b][1]);
             }
             float e[2][4] = {};
 #pragma unroll
@@ -646,11 +745,12 @@ struct TcWarp {
     // heads 2j, 2j + 1: dimensions 32c + 4n .. + 3 in acc[c], the sums of the rounded p in off[2..3] and of p in l
     __device__ __forceinline__ void end(int lane) {
         const int j = lane & 3;
+        if constexpr (!kF32) rescale(true);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], o);
-            const float both = fmaf(8.f, off[i + 2], off[i]);  // of group lane / 4
+            const float both = kF32 ? fmaf(8.f, off[i + 2], off[i]) : off[i];  // of group lane / 4
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
                 const float add = __shfl_sync(0xFFFFFFFFu, both, 4 * (c / kPerGroup) + j);

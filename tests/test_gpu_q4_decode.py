@@ -137,6 +137,41 @@ def test_peaked(zp, dtype):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["spread", "late", "flat", "tiny", "huge", "groups"])
+def test_step_sizes(zp, dtype, kind):
+    """Steps of very different sizes: among all tokens, larger ones from some token on, flat groups (the
+    smallest step) here and there, all tiny, all huge, and groups of sizes of their own."""
+    rng = np.random.default_rng(7)
+    c = Case(zp, [300, 1, 45, 1000], dtype, 32, 8, 128, 32, 16, seed=3)
+    for cache in (c.V, c.K):
+        word = np.ascontiguousarray(cache[..., 8 * 128:]).view(np.uint32).reshape(c.n_total, 8, 1, 16, 4)
+        live = word != 0x7FC07FC0
+        step = q4.bf16_value(word & 0xFFFF).copy()
+        lo = q4.bf16_value(word >> 16).copy()
+        if kind == "spread":
+            f = np.exp2(rng.integers(-40, 6, size=step.shape))
+        elif kind == "late":
+            late = np.zeros((c.n_total, 16), bool)
+            for s in range(c.B):
+                p = np.arange(c.lens[s] // 2, c.lens[s])
+                late[c.table[s, p // 16], p % 16] = True
+            f = np.where(late[:, None, None, :, None], 64.0, 1.0) * np.ones(step.shape)
+        elif kind == "flat":
+            f = np.where(rng.random(step.shape) < 0.02, 0.0, 1.0)
+        elif kind == "groups":
+            f = np.exp2(np.array([-30.0, 0.0, 9.0, -100.0])) * np.ones(step.shape)
+        else:
+            f = np.full(step.shape, 2.0 ** -110 if kind == "tiny" else 2.0 ** 90)
+        if cache is c.K:   # keys: sizes that leave the logits within reach
+            f = np.where(f > 4, 4.0, f)
+        step = np.maximum(step * f, 2.0 ** -126).astype(np.float32)
+        lo = (lo * f).astype(np.float32)
+        new = (q4.bf16_bits(step, True).astype(np.uint32) | q4.bf16_bits(lo, False).astype(np.uint32) << 16)
+        cache[..., 8 * 128:] = np.where(live, new, word).astype(np.uint32).reshape(c.n_total, 8, 1, 64).view(np.uint8)
+    c.check(c.run())
+
+
 def test_batch_limit(zp):
     rng = np.random.default_rng(2)
     lens = rng.integers(0, 20, size=4096)
