@@ -314,16 +314,17 @@ struct TcWarp {
     using T = T_;
     static constexpr bool kF32 = sizeof(T) == 4;
     static constexpr int kD = D, kWarps = kF32 ? 12 : 16;
-    static constexpr int kTile = q4_tile_bytes(D, 1 << LG);
+    static constexpr int kTile = q4_tile_bytes(D, 1 << LG), kSharedBytes = kF32 ? 0 : 512;
     static constexpr int NG = D >> LG, kChunks = D / 32, kPerGroup = (1 << LG) / 32;  // chunks of a row, of a group
     static constexpr int kQ = kF32 ? 3 : 1;                                           // parts of a query
     uint32_t qb[kQ][kChunks][2][2];  // queries as the right operand, by part, chunk and half of its words
     uint32_t ob[3];  // (0, sum of the queries) of (head lane / 4, group lane % 4), in three parts, scaled as the products
-    float unit_y[2], more_y[2];  // what a product is worth: log2(e) / sqrt(d) over the scale of heads 2 (lane % 4), + 1;
-                                 // more_y: a factor beyond it (1 but for queries past 2^100)
+    float unit_y[2];  // what a product is worth: log2(e) / sqrt(d) over the scale of heads 2 (lane % 4), + 1
     float acc[kChunks][2][4], off[4];
     float thr[2], base[2], l[2];  // of those two heads: m + kLazyMax (-inf: none yet), m - kScale, sum over this lane's tokens
-    uint32_t win[NG];  // bf16 queries: lowest exponent, less 1, of the group's steps taken in fp16; kNoWindow: none yet
+    uint4 *params;     // bf16 queries: of a unit's values, by two tokens: steps in fp16 and lo in bf16, by group
+    uint32_t wins;     // bf16 queries: by group a byte, lowest exponent, less 1, of the steps taken in fp16; kNoWindow: none yet
+    __device__ __forceinline__ uint32_t window(int g) const { return wins >> (8 * g) & 0xFFu; }
 
     struct Query {  // eight elements of each chunk
         uint4 w[kChunks][kF32 ? 2 : 1];
@@ -394,12 +395,11 @@ struct TcWarp {
             ob[i] = f2_to_bf2(0.f, hi);  // (lo is the high half of a parameter word, step the low one)
             part -= hi;
         }
-        // 2^(24 - 14 + e) log2(e) / sqrt(d); above 2^117 it is not a float, and the rest is multiplied on
+        // 2^(24 - 14 + e) log2(e) / sqrt(d); an infinity (and the outputs NaN) for queries of 2^118 and more
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int eh = __shfl_sync(0xFFFFFFFFu, e, 8 * j + 4 * i);
-            unit_y[i] = a.qscale * __uint_as_float((uint32_t)(127 + min(eh + 10, 110)) << 23);
-            more_y[i] = __uint_as_float((uint32_t)(127 + max(eh - 100, 0)) << 23);
+            unit_y[i] = a.qscale * __uint_as_float((uint32_t)min(127 + eh + 10, 255) << 23);
         }
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
@@ -411,8 +411,7 @@ struct TcWarp {
         for (int i = 0; i < 4; ++i) off[i] = 0.f;
 #pragma unroll
         for (int i = 0; i < 2; ++i) thr[i] = -INFINITY, base[i] = 0.f, l[i] = 0.f;
-#pragma unroll
-        for (int g = 0; g < NG; ++g) win[g] = kNoWindow;
+        wins = kNoWindow;
     }
 
     // Two key tiles, then two value tiles; of tile i the tokens >= v0 (i = 0), v1 weigh nothing.
@@ -488,12 +487,6 @@ struct TcWarp {
 #pragma unroll
             for (int i = 0; i < 4; ++i) y[b][i] *= unit_y[i & 1];
         }
-        if (more_y[0] != 1.f || more_y[1] != 1.f) {
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) y[b][i] *= more_y[i & 1];
-        }
         if (part) {
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
@@ -507,6 +500,13 @@ struct TcWarp {
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 float *to = logits + (b * kQ4Tile + n) * a.G + h;
+                if (a.G % 2 == 0) {
+                    if (h < a.G) {
+                        *reinterpret_cast<float2 *>(to) = make_float2(y[b][0], y[b][1]);
+                        *reinterpret_cast<float2 *>(to + 8 * a.G) = make_float2(y[b][2], y[b][3]);
+                    }
+                    continue;
+                }
                 if (h < a.G) to[0] = y[b][0], to[8 * a.G] = y[b][2];
                 if (h + 1 < a.G) to[1] = y[b][1], to[8 * a.G + 1] = y[b][3];
             }
@@ -569,7 +569,7 @@ struct TcWarp {
     __device__ __forceinline__ void rescale(bool plain) {
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-            const int e = (int)win[c / kPerGroup] + 1 - 89, e0 = plain ? e : -e, half = e0 / 2;
+            const int e = (int)window(c / kPerGroup) + 1 - 89, e0 = plain ? e : -e, half = e0 / 2;
             const float f = __uint_as_float((uint32_t)(127 + half) << 23), f2 = __uint_as_float((uint32_t)(127 + e0 - half) << 23);
             const float odd = plain ? 0.0625f * f2 : 16.f * f2;
 #pragma unroll
@@ -579,34 +579,40 @@ struct TcWarp {
         }
     }
 
-    __device__ __forceinline__ void values_bf16(unsigned char *vt, const float (&y)[2][4], int v0, int v1, uint32_t at,
+    __device__ __forceinline__ void values_bf16(const unsigned char *vt, const float (&y)[2][4], int v0, int v1, uint32_t at,
                                                 int lane) {
         const int n = lane >> 2, j = lane & 3;
-        // ---- do the steps of all tokens lie in the window?  (lane t looks at token t)
+        // ---- lane t looks at token t: do the steps of all tokens lie in the window?  Two lanes then lay out their
+        // two tokens' parameters, by group: steps in fp16 (bf16's bits with the exponent moved and three zeros
+        // behind), lo as it is.
         bool wild;
         {
-            uint32_t w[NG], *own = reinterpret_cast<uint32_t *>(vt + (lane >> 4) * kTile + q4_code_bytes(D)) + (lane & 15) * NG;
-            lds<NG>(own, w);
+            uint32_t w[NG];
+            lds<NG>(reinterpret_cast<const uint32_t *>(vt + (lane >> 4) * kTile + q4_code_bytes(D)) + (lane & 15) * NG, w);
             const bool live = (lane & 15) < (lane < kQ4Tile ? v0 : v1);
-            if (win[0] == kNoWindow) {
+            if (wins == kNoWindow) {
+                wins = 0;
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     const int top = (int)__reduce_max_sync(0xFFFFFFFFu, live ? w[g] & 0x7F80u : 0u) >> 7;
-                    win[g] = min(max(top - kBelow, 1), 255 - kWindow) - 1;
+                    wins |= (uint32_t)(min(max(top - kBelow, 1), 255 - kWindow) - 1) << (8 * g);
                 }
             }
             bool out = false;
 #pragma unroll
-            for (int g = 0; g < NG; ++g) out |= (w[g] & 0xFFFFu) - ((win[g] + 1) << 7) >= (uint32_t)kWindow << 7;
+            for (int g = 0; g < NG; ++g) out |= (w[g] & 0xFFFFu) - ((window(g) + 1) << 7) >= (uint32_t)kWindow << 7;
             wild = __any_sync(0xFFFFFFFFu, live && out);
-            if (v0 + v1 < kUnit) {  // the other tokens (p = 0): a step of the window too, whose fp16 form is a number
-                if (!live) {
+            uint32_t pair[4];
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) own[g] = (win[g] + 1) << 7;
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
+            for (int g = 0; g < NG; ++g) {
+                if (!live) w[g] = (window(g) + 1) << 7;  // (p = 0: any step whose fp16 form is a number)
+                const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, w[g], 1);
+                pair[g] = lane & 1 ? __byte_perm(w[g], other, 0x3276) : __byte_perm(w[g], other, 0x5410) * 8 - window(g) * (0x10001u << 10);
             }
+            if constexpr (NG == 4) params[lane] = make_uint4(pair[0], pair[1], pair[2], pair[3]);
+            else if constexpr (NG == 2) *reinterpret_cast<uint2 *>(params + lane) = make_uint2(pair[0], pair[1]);
+            else *reinterpret_cast<uint32_t *>(params + lane) = pair[0];
+            __syncwarp();
         }
         float p[2][4];
 #pragma unroll
@@ -615,13 +621,15 @@ struct TcWarp {
             for (int i = 0; i < 4; ++i) p[b][i] = ex2_approx(y[b][i] - base[i & 1]);
             l[0] += p[b][0] + p[b][2];
             l[1] += p[b][1] + p[b][3];
-            // the sums with the parameters, p in two bf16 parts
-            uint32_t w[4], u0[2], u1[2];
-            parameter_rows(reinterpret_cast<const uint32_t *>(vt + b * kTile + q4_code_bytes(D)), n, j, w);
+            // the sums with lo, p in two bf16 parts: rows g of the left operand lo of group g, row 7 ones
+            const uint32_t *q0 = reinterpret_cast<const uint32_t *>(params + b * 16 + 2 * j + 1) + (n < NG ? n : 0);
+            const uint32_t rest = n == 7 ? 0x3F803F80u : 0;
+            const uint32_t l0 = n < NG ? q0[0] : rest, l1 = n < NG ? q0[32] : rest;
+            uint32_t u0[2], u1[2];
             split_bf2(p[b][0], p[b][1], u0);
             split_bf2(p[b][2], p[b][3], u1);
 #pragma unroll
-            for (int k = 1; k >= 0; --k) mma_bf16(off, w[0], w[0], w[2], w[2], transpose8(u0[k]), transpose8(u1[k]));
+            for (int k = 1; k >= 0; --k) mma_bf16(off, l0, l0, l1, l1, transpose8(u0[k]), transpose8(u1[k]));
         }
         if (wild) {
             rescale(true);
@@ -633,12 +641,9 @@ struct TcWarp {
         for (int b = 0; b < 2; ++b) {
             // right operand of the values' products: tokens 2j, 2j + 1 (and + 8) of head n
             const uint32_t b0 = transpose8(f2_to_h2(p[b][0], p[b][1])), b1 = transpose8(f2_to_h2(p[b][2], p[b][3]));
-            const uint32_t *vp = reinterpret_cast<const uint32_t *>(vt + b * kTile + q4_code_bytes(D));
-            uint32_t w0[NG], w1[NG], w2[NG], w3[NG];
-            lds<NG>(vp + 2 * j * NG, w0);
-            lds<NG>(vp + (2 * j + 1) * NG, w1);
-            lds<NG>(vp + (2 * j + 8) * NG, w2);
-            lds<NG>(vp + (2 * j + 9) * NG, w3);
+            uint32_t w0[NG], w1[NG];
+            lds<NG>(reinterpret_cast<const uint32_t *>(params + b * 16 + 2 * j), w0);
+            lds<NG>(reinterpret_cast<const uint32_t *>(params + b * 16 + 2 * j + 8), w1);
             const uint32_t va = smem_u32(vt + b * kTile) + at;
             uint32_t s0 = 0, s1 = 0;
 #pragma unroll
@@ -648,10 +653,9 @@ struct TcWarp {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int g = (c + i) / kPerGroup;
-                    if ((c + i) % kPerGroup == 0) {  // (bf16 to fp16 bits: the exponent moved, three zeros behind)
-                        const uint32_t down = win[g] * (0x10001u << 10);
-                        s0 = mul_h2(b0, __byte_perm(w0[g], w1[g], 0x5410) * 8 - down);
-                        s1 = mul_h2(b1, __byte_perm(w2[g], w3[g], 0x5410) * 8 - down);
+                    if ((c + i) % kPerGroup == 0) {
+                        s0 = mul_h2(b0, w0[g]);
+                        s1 = mul_h2(b1, w1[g]);
                     }
                     uint32_t x[4], z[4];
                     nibbles(r[2 * i], x[0], x[1], z[0], z[1]);
@@ -796,11 +800,11 @@ struct TcWarp {
 
 // ---------------------------------------------------------------- attention
 // Shared memory: rings (a warp's tiles; at its end the record of a pair that goes on
-// behind its range), records of pairs that began before a warp's range (written while the ring is in
+// behind its range), what a warp lays out for itself, records of pairs that began before a warp's range (written while the ring is in
 // use; in the workspace where there is no room), prefix.
 template <class W>
 __host__ __device__ inline size_t attention_smem(int stages, int tile, int B, int G, bool heads_here) {
-    return (size_t)W::kWarps * ((size_t)stages * 4 * tile + (heads_here ? (size_t)G * (W::kD + 4) * 4 : 0)) + ((size_t)B + 1) * 4;
+    return (size_t)W::kWarps * ((size_t)stages * 4 * tile + W::kSharedBytes + (heads_here ? (size_t)G * (W::kD + 4) * 4 : 0)) + ((size_t)B + 1) * 4;
 }
 
 template <class W>
@@ -818,9 +822,10 @@ __global__ void __launch_bounds__(W::kWarps * 32, 1) q4_attention_kernel(const Q
     const int rec_n = rec_floats(a, D), stages = a.stages;
     const size_t ring_bytes = (size_t)stages * 4 * a.tile;
     unsigned char *ring = smem + warp * ring_bytes;
-    float *heads = a.heads_here ? reinterpret_cast<float *>(smem + kWarps * ring_bytes)
+    unsigned char *own = smem + kWarps * ring_bytes + warp * W::kSharedBytes, *behind = smem + kWarps * (ring_bytes + W::kSharedBytes);
+    float *heads = a.heads_here ? reinterpret_cast<float *>(behind)
                                 : a.rec + (size_t)(2 * a.grid + (int)blockIdx.x * kWarps) * rec_n;
-    int *prefix = reinterpret_cast<int *>(smem + kWarps * (ring_bytes + (a.heads_here ? (size_t)rec_n * 4 : 0)));
+    int *prefix = reinterpret_cast<int *>(behind + (a.heads_here ? (size_t)kWarps * rec_n * 4 : 0));
     if (lane < stages) mbar_init(&full_s[warp][lane], 2);
     if (lane == 0) head_s[warp] = tail_s[warp] = -1;
     if (tid == 0) abort_s = 0;
@@ -899,6 +904,7 @@ __global__ void __launch_bounds__(W::kWarps * 32, 1) q4_attention_kernel(const Q
         pair = put_pair;
 
         W w;
+        w.params = reinterpret_cast<uint4 *>(own);
         w.begin(a, query, lane);
         int st = 0;
         unsigned phase = 0;

@@ -541,10 +541,11 @@ zp_status zp_q4_read_kv(const zp_cache_desc *D, int32_t group, const void *k_bas
 /* zp_paged_decode_attn over a 4-bit cache: the same output, window score, skipping
  * of L = 0, slot map and arguments, with k_t and v_t the values the codes stand for (not
  * rounded to dtype).  q and out are dtype and do not overlap (ZP_ERR_INVALID_ARG).  Slots behind a
- * sequence's last token may hold anything.  bf16: a token's probability, and its product
- * with a group's step, are each rounded to bf16 for the output; logits, softmax statistics and
- * scores are those of 32-bit arithmetic.  fp32: parts of the queries and products that hold 22 bits
- * or more.  A call with the same arguments gives the same bits.  Recorded as ZP_ERR_DEVICE: a length outside [0, table_stride * b] (detail 0x158;
+ * sequence's last token may hold anything.  bf16: for the output a token's probability, and
+ * its product with a group's step, are each rounded to 11 bits (to 8 in runs of 32 tokens whose value
+ * steps differ by more than 2^10 from the first run's); logits, softmax statistics and scores are
+ * those of 32-bit arithmetic.  fp32: three parts of 8 bits or more of each factor.  Queries of 2^117
+ * and more in size give NaN.  A call with the same arguments gives the same bits.  Recorded as ZP_ERR_DEVICE: a length outside [0, table_stride * b] (detail 0x158;
  * taken as the nearer bound), a block outside [0, N_total) among a sequence's blocks (0x159; its
  * tokens weigh nothing), a slot >= n_score_rows (0x15a; not scored).
  * The workspace is scratch: any content on entry, nothing kept; two calls that may
