@@ -93,8 +93,8 @@ __device__ __forceinline__ Split make_split(const Q4Args &a, int units) {
     return p;
 }
 
-__device__ __forceinline__ int q4_len(const Q4Args &a, int s) {
-    const int L = __ldg(a.seq_lens + s);
+// A length as it is taken, the nearer bound where it lies outside [0, table_stride * b].
+__device__ __forceinline__ int checked_len(const Q4Args &a, int L) {
     const long long cap = (long long)a.table_stride * a.b;
     if (L < 0 || L > cap) {
         record_error(a.err, ZP_ERR_DEVICE, 0x158);
@@ -102,6 +102,7 @@ __device__ __forceinline__ int q4_len(const Q4Args &a, int s) {
     }
     return L;
 }
+__device__ __forceinline__ int q4_len(const Q4Args &a, int s) { return checked_len(a, __ldg(a.seq_lens + s)); }
 
 // prefix[s] = units of the sequences before s; blockDim.x threads, a multiple of 32.
 __device__ void unit_prefix(const Q4Args &a, int *prefix, int *warp_sum) {
@@ -161,12 +162,11 @@ struct Cursor {
     }
 };
 
-// Row of S that entry s scores into on this step, -1 = none.
-__device__ __forceinline__ int q4_score_row(const Q4Args &a, int s, int L) {
+// Row of S that entry s, with entry r of the slot map (without one: s), scores into on this step, -1 = none.
+__device__ __forceinline__ int slot_of(const Q4Args &a, int s) { return a.score_rows ? __ldg(a.score_rows + s) : s; }
+__device__ __forceinline__ int q4_score_row(const Q4Args &a, int r, int L) {
     if (!a.want_score || L < 1 || (L - 1) % a.b < a.b - a.window) return -1;
-    if (!a.score_rows) return s;
-    const int r = __ldg(a.score_rows + s);
-    if (r >= a.n_score_rows) {
+    if (a.score_rows && r >= a.n_score_rows) {
         record_error(a.err, ZP_ERR_DEVICE, 0x15a);
         return -1;
     }
@@ -859,6 +859,7 @@ __global__ void __launch_bounds__(W::kWarps * 32, 1) q4_attention_kernel(const Q
                 sub[b] = 2 * c.u + b - col * a.tpb;
                 blk[b] = col < a.table_stride ? __ldg(a.table + (size_t)c.s * a.table_stride + col) : -1;
             }
+            const int slot = a.want_score ? slot_of(a, c.s) : -1;
             const int L = q4_len(a, c.s);
             put_meta = (c.u == 0 ? kFirst : 0) | (c.u == c.n - 1 ? kLast : 0);
 #pragma unroll
@@ -874,7 +875,7 @@ __global__ void __launch_bounds__(W::kWarps * 32, 1) q4_attention_kernel(const Q
                 }
             }
 
-            if (a.want_score && q4_score_row(a, c.s, L) >= 0) put_meta |= kScored;
+            if (a.want_score && q4_score_row(a, slot, L) >= 0) put_meta |= kScored;
         };
         int put_st = 0;
         auto issue = [&](int i) {  // lanes 0 and 1: one tile of keys and values each
@@ -1004,7 +1005,7 @@ __global__ void __launch_bounds__(W::kWarps * 32, 1) q4_attention_kernel(const Q
 // ---------------------------------------------------------------- what is left
 // CTA c joins the records of the pair that its counterpart of the attention kernel began and
 // did not finish, and forms the score of that one's units.
-constexpr int kFinishThreads = 512, kScoreUnroll = 8;
+constexpr int kFinishThreads = 512, kScoreUnroll = 4;
 
 // Record of CTA c of a pair cut between CTAs, which CTA c0 begins.
 __device__ __forceinline__ const float *cta_record(const Q4Args &a, int c0, int c, int rec_n) {
@@ -1058,7 +1059,7 @@ __device__ __forceinline__ void score_tokens(const Q4Args &a, const float *lg, c
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kFinishThreads) q4_finish_kernel(const Q4Args a) {
+__global__ void __launch_bounds__(kFinishThreads, 1) q4_finish_kernel(const Q4Args a) {
     extern __shared__ int prefix[];
     pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rec_n = rec_floats(a, D);
@@ -1103,14 +1104,12 @@ __global__ void __launch_bounds__(kFinishThreads) q4_finish_kernel(const Q4Args 
     cur.seek(prefix, a.B, a.h_kv, x0);
     for (int x = x0; x < x1;) {
         const int units = min(cur.n - cur.u, x1 - x);  // the rest of this pair
-        const int L = q4_len(a, cur.s), row = q4_score_row(a, cur.s, L);
+        // three loads at once; normalisers of the heads: lane q has head q's
+        float norm = lane < a.G ? __ldcg(a.stats + (size_t)cur.s * a.h_q + cur.h * a.G + lane) : INFINITY;
+        const int slot = slot_of(a, cur.s), L = q4_len(a, cur.s), row = q4_score_row(a, slot, L);
         if (row >= 0) {
-            // normalisers of the heads: lane q has head q's
             const int first = x - cur.u, last = first + cur.n - 1;
-            float norm = INFINITY;
-            if (first >= b0 && last < b1) {
-                if (lane < a.G) norm = __ldcg(a.stats + (size_t)cur.s * a.h_q + cur.h * a.G + lane);
-            } else {
+            if (first < b0 || last >= b1) {  // a pair that several CTAs share
                 const int k0 = split.cta_of(first), k1 = split.cta_of(last);
                 if (lane < a.G) {
                     float m = -INFINITY, l = 0.f;
