@@ -18,7 +18,6 @@
 namespace zp {
 
 constexpr int kQ4Tile = 16;         // tokens per tile
-constexpr int kQ4MaxGroups = 4;     // groups per row: d/group
 constexpr uint32_t kQ4NaN = 0x7FC07FC0u;  // step and lo of a group that holds anything not finite
 
 __host__ __device__ constexpr int q4_code_bytes(int d) { return kQ4Tile * d / 2; }
@@ -88,6 +87,13 @@ __device__ __forceinline__ uint2 q4_join(const float2 (&k)[8]) {
                     both(8388608.f));
     return make_uint2(__byte_perm(__float_as_uint(x[0].x), __float_as_uint(x[1].x), 0x5410),
                       __byte_perm(__float_as_uint(x[0].y), __float_as_uint(x[1].y), 0x5410));
+}
+
+// Code j of a word as a float.  Nibbles 0 to 4 stay where they are: under the exponent of 2^(23 - 4j) the bits
+// from 4j on count ones.
+__device__ __forceinline__ float q4_code_at(uint32_t w, int j) {
+    if (j > 4) w >>= 20, j -= 5;
+    return __uint_as_float((w & 15u << (4 * j)) | (uint32_t)(150 - 4 * j) << 23) - (float)(1 << (23 - 4 * j));
 }
 
 // Host: arguments that every call on a 4-bit cache has.

@@ -14,6 +14,10 @@ namespace {
 // lanes, its extremes one shuffle away, its parameters are worked out for 16 elements at a
 // time, and a thread's codes are 8 bytes, so the 8 lanes of a row of 128 write its 64 bytes
 // side by side.  A thread keeps its place in the row and walks over tokens.
+// Bound: for many rows the instructions, about 14 per element and lane, issued in three quarters of all cycles:
+// 64k tokens of 8 heads of 128 in bf16, 352 MB, take 69 us (5.1 TB/s, 0.76 of a plain copy's rate); for few
+// the launch (512 tokens 2.7 us).  One row at a time per thread: with two the registers cost what the second
+// load in flight gains (64k tokens 70 us), and 512 tokens take longer.
 constexpr int kStoreThreads = 256, kPiece = 16;
 
 __device__ __forceinline__ float min_nan(float a, float b) {
@@ -121,20 +125,21 @@ struct RowArgs {
     int row_pieces;                   // h_kv * d / kPiece
     int tpb;                          // tiles per block and kv head
     unsigned inv_lanes, inv_tpb;      // reciprocals, rounded up, of 2^32 (0: the divisor is 1)
-    long long n_slots;
+    int n_slots;
     bool wide;                        // rows aligned to 32 bytes
     unsigned *err;
 };
 
-// Tile of slot's row of kv head h: ((slot / b) * h_kv + h) * (b / 16) + slot % b / 16.
-__device__ __forceinline__ size_t tile_offset(const RowArgs &a, int slot, int h) {
+// Byte offset of the tile of a slot from that of its kv head's first tile: the tiles of a head and block lie
+// tpb apart times h_kv, so ((slot / b) * h_kv * tpb + slot % b / 16) * tile, in 32-bit factors.
+__device__ __forceinline__ size_t tile_offset(const RowArgs &a, int slot) {
     const unsigned t = (unsigned)slot / kQ4Tile;  // below 2^27; the reciprocal is exact as far as that
-    unsigned blk = t;
+    unsigned m = t;                               // the first tile of the block
     if (a.inv_tpb) {
-        blk = __umulhi(t, a.inv_tpb);
-        if (blk * a.tpb > t) --blk;  // (rounded up: one too many at most)
+        m = __umulhi(t, a.inv_tpb) * a.tpb;
+        if (m > t) m -= a.tpb;  // (rounded up: one too many at most)
     }
-    return (((size_t)blk * a.h_kv + h) * a.tpb + (t - blk * a.tpb)) * a.tile;
+    return (size_t)m * (unsigned)((a.h_kv - 1) * a.tile) + (size_t)t * (unsigned)a.tile;
 }
 
 struct StoreArgs : RowArgs {
@@ -181,11 +186,15 @@ __global__ void __launch_bounds__(kStoreThreads) q4_store_kernel(const StoreArgs
     unsigned char *dst = (blockIdx.z ? a.V : a.K) + (long long)blockIdx.y * a.layer_bytes;
     const int tok = a.inv_lanes ? (int)__umulhi(threadIdx.x, a.inv_lanes) : (int)threadIdx.x;
     const int first = blockIdx.x * a.tokens_per_cta + tok, last = min(a.n_tokens, ((int)blockIdx.x + 1) * a.tokens_per_cta);
-    const int group_lanes = 1 << (a.lg_group - 4);
+    const int group_lanes = 1 << (a.lg_group - 4), lg_row = 2 + (D == 128 ? 7 : 6) - a.lg_group;  // log2 of a row's parameter bytes
+    const long long step_rows = a.at_once * a.token_stride;
     // (every thread goes as often round as the first: the shuffles are the whole warp's)
     for (int c0 = 0; c0 < a.row_pieces; c0 += a.lanes_n) {
         const int c = c0 + threadIdx.x - tok * a.lanes_n, head = c / kPieces, piece = c % kPieces;
         const bool works = tok < a.at_once && c < a.row_pieces;
+        const T *from = src + (long long)first * a.token_stride + c * kPiece;
+        unsigned char *base = dst + (size_t)head * a.tpb * a.tile;
+        const int par_at = q4_code_bytes(D) + (piece * kPiece >> a.lg_group) * 4;
         for (int i0 = first; i0 - tok < last; i0 += U * a.at_once) {
             Piece<T> in[U];
             int slot[U];
@@ -194,11 +203,12 @@ __global__ void __launch_bounds__(kStoreThreads) q4_store_kernel(const StoreArgs
                 const int i = i0 + u * a.at_once;
                 slot[u] = -1;
                 if (works && i < last) {
-                    in[u].load(src + (long long)i * a.token_stride + c * kPiece, a.wide);
+                    in[u].load(from, a.wide);
                     slot[u] = store_slot<APPEND>(a, i);
                 } else {
                     in[u].clear();
                 }
+                from += step_rows;
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -218,16 +228,18 @@ __global__ void __launch_bounds__(kStoreThreads) q4_store_kernel(const StoreArgs
                 if (par == kQ4NaN) word = make_uint2(0, 0);
                 if (slot[u] < 0) continue;
                 const int t = slot[u] % kQ4Tile;
-                unsigned char *tile = dst + tile_offset(a, slot[u], head);
+                unsigned char *tile = base + tile_offset(a, slot[u]);
                 *reinterpret_cast<uint2 *>(tile + t * (D / 2) + q4_chunk<D>(t, piece / 2) * 16 + piece % 2 * 8) = word;
-                if (piece % group_lanes == 0)
-                    reinterpret_cast<uint32_t *>(tile + q4_code_bytes(D))[t * (D >> a.lg_group) + (piece * kPiece >> a.lg_group)] = par;
+                if (piece % group_lanes == 0) *reinterpret_cast<uint32_t *>(tile + (t << lg_row) + par_at) = par;
             }
         }
     }
 }
 
 // ---------------------------------------------------------------- rows out
+// The same threads and walk, the other way, two rows at a time: 64k tokens of 8 heads of 128 into
+// bf16 take 60 us (5.8 TB/s, 0.87 of a plain copy's rate: bound by memory), 512 tokens 2.9; with
+// four rows 59 and 3.6, with one 64 and 2.8.
 struct ReadArgs : RowArgs {
     const unsigned char *K, *V;
     long long layer_bytes;
@@ -244,8 +256,13 @@ __global__ void __launch_bounds__(kStoreThreads) q4_read_kernel(const ReadArgs a
     const int tok = a.inv_lanes ? (int)__umulhi(threadIdx.x, a.inv_lanes) : (int)threadIdx.x;
     if (tok >= a.at_once) return;
     const int first = blockIdx.x * a.tokens_per_cta + tok, last = min(a.n_tokens, ((int)blockIdx.x + 1) * a.tokens_per_cta);
+    const int lg_row = 2 + (D == 128 ? 7 : 6) - a.lg_group;  // log2 of a row's parameter bytes
+    const long long step_rows = a.at_once * a.token_stride;
     for (int c = threadIdx.x - tok * a.lanes_n; c < a.row_pieces; c += a.lanes_n) {
         const int head = c / kPieces, piece = c % kPieces;
+        T *to = dst + (long long)first * a.token_stride + c * kPiece;
+        const unsigned char *base = src + (size_t)head * a.tpb * a.tile;
+        const int par_at = q4_code_bytes(D) + (piece * kPiece >> a.lg_group) * 4;
         for (int i0 = first; i0 < last; i0 += U * a.at_once) {
             uint2 word[U];
             uint32_t par[U];
@@ -263,36 +280,37 @@ __global__ void __launch_bounds__(kStoreThreads) q4_read_kernel(const ReadArgs a
             for (int u = 0; u < U; ++u) {
                 if (slot[u] < 0) continue;
                 const int t = slot[u] % kQ4Tile;
-                const unsigned char *tile = src + tile_offset(a, slot[u], head);
+                const unsigned char *tile = base + tile_offset(a, slot[u]);
                 word[u] = __ldg(reinterpret_cast<const uint2 *>(tile + t * (D / 2) + q4_chunk<D>(t, piece / 2) * 16 + piece % 2 * 8));
-                par[u] = __ldg(reinterpret_cast<const uint32_t *>(tile + q4_code_bytes(D)) + t * (D >> a.lg_group) +
-                               (piece * kPiece >> a.lg_group));
+                par[u] = __ldg(reinterpret_cast<const uint32_t *>(tile + (t << lg_row) + par_at));
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (slot[u] < 0) continue;
-                const float step = __uint_as_float(par[u] << 16), lo = __uint_as_float(par[u] & 0xFFFF0000u);
-                float x[16];
+                if (slot[u] >= 0) {
+                    const float step = __uint_as_float(par[u] << 16), lo = __uint_as_float(par[u] & 0xFFFF0000u);
+                    float x[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const uint32_t w = j < 8 ? word[u].x : word[u].y;
-                    const float code = __uint_as_float((w >> (4 * (j & 7)) & 15u) | 0x4B000000u) - 8388608.f;  // 2^23 + c, exact
-                    x[j] = fmaf(code, step, lo);
+                    for (int j = 0; j < 16; ++j) x[j] = fmaf(q4_code_at(j < 8 ? word[u].x : word[u].y, j & 7), step, lo);
+                    Piece<T>::store(to, x, a.wide);
                 }
-                Piece<T>::store(dst + (long long)(i0 + u * a.at_once) * a.token_stride + c * kPiece, x, a.wide);
+                to += step_rows;
             }
         }
     }
 }
 
 // ---------------------------------------------------------------- moves
-// One CTA per (tensor, kv head, sequence, layer) moves its ranks in rounds of kMoveRanks (a thread each) through
-// a ring in shared memory: asynchronous copies in, kMoveStages - 1 rounds ahead, plain stores out.
-// Round i is stored once all of its copies have arrived.  Its stores go to slots below the ranks of
-// later rounds, whose sources are at or above those ranks, and a slot that a source and a
-// target share has the same index in both (the target rule): later rounds may be read ahead of
-// earlier stores, and the move is right in place too.  A row in flight costs no registers that way,
-// and the look-ups (position, then block) run a round or two ahead of the copies.
+// One CTA per (tensor, kv head, sequence, layer) moves its ranks in rounds of kMoveRanks (a thread
+// each) through a ring in shared memory: asynchronous copies in, kMoveStages - 1 rounds ahead,
+// plain stores out.  Round i is stored once all of its copies have arrived.  Its stores go to slots
+// below the ranks of later rounds, whose sources are at or above those ranks, and a slot that a
+// source and a target share has the same index in both (the target rule): later rounds may be read
+// ahead of earlier stores, and the move is right in place too.  A row in flight costs no registers
+// that way, and the look-ups (position, then block) run a round or two ahead of the copies.
+// Bound: memory, where a row has 64 bytes of codes and 16 of parameters far from them.  16 sequences, 4080 of 32k
+// tokens each, 8 heads of 128: 51 us for 84 MB of rows, for which 232 MB are read and 49 MB written (5.5 TB/s);
+// 7 sequences of 2032 rows 12.8 us, a chain of five latencies (length, position, block, row, store).
+// Rows that went through registers, a round's loads before its stores, took 104 us with the read-back that takes 57.
 constexpr int kMoveStages = 4;
 
 __device__ __forceinline__ void copy_async(void *to, const void *from, int bytes) {  // 4, 8 or 16
@@ -457,19 +475,24 @@ unsigned reciprocal(int x) { return x == 1 ? 0 : (unsigned)((0x100000000ull + x 
 
 // The split of n_tokens rows (of `layers` layers, keys and values) over CTAs whose threads
 // take U tokens at a time.
-void fill_rows(RowArgs &a, const zp_cache_desc *D, int group, int n_tokens, int U, uintptr_t aligned, const DeviceInfo &dev) {
+void fill_rows(RowArgs &a, const zp_cache_desc *D, int group, int n_tokens, int layers, int U, uintptr_t aligned,
+               const DeviceInfo &dev) {
     a.n_tokens = n_tokens;
     a.row_pieces = D->h_kv * D->head_dim / kPiece;
     a.lanes_n = a.row_pieces < kStoreThreads ? a.row_pieces : kStoreThreads;
     a.at_once = kStoreThreads / a.lanes_n;
-    a.tokens_per_cta = a.at_once * U;
+    // Where there are far more CTAs than the SMs hold, each goes round up to 8 times (what a thread works out
+    // once is then spread over more rows) as long as several CTAs per SM and place remain to even the end out.
+    const long long ctas = ((long long)n_tokens + a.at_once * U - 1) / (a.at_once * U) * layers * 2;
+    const long long rounds = ctas / (dev.sm_count * 20);
+    a.tokens_per_cta = a.at_once * U * (int)(rounds < 1 ? 1 : rounds > 8 ? 8 : rounds);
     a.h_kv = D->h_kv;
     a.lg_group = log2_of(group);
     a.tile = q4_tile_bytes(D->head_dim, group);
     a.tpb = D->block_size / kQ4Tile;
     a.inv_lanes = reciprocal(a.lanes_n);
     a.inv_tpb = reciprocal(a.tpb);
-    a.n_slots = (long long)D->n_total_blocks * D->block_size;
+    a.n_slots = D->n_total_blocks * D->block_size;
     a.wide = aligned % 32 == 0;
     a.err = dev.error_word;
 }
@@ -477,7 +500,7 @@ dim3 row_grid(const RowArgs &a, int layers) {
     return dim3((unsigned)((a.n_tokens + (long long)a.tokens_per_cta - 1) / a.tokens_per_cta), (unsigned)layers, 2);
 }
 
-constexpr int kStoreUnroll = 2, kReadUnroll = 4;
+constexpr int kStoreUnroll = 1, kReadUnroll = 2;
 
 template <bool APPEND>
 zp_status launch_store(const zp_cache_desc *D, const StoreArgs &a, int layers, const char *what, cudaStream_t st) {
@@ -531,7 +554,7 @@ extern "C" zp_status zp_q4_write_kv(const zp_cache_desc *D, int32_t group, const
     a.V = static_cast<unsigned char *>(v_base);
     a.layer_bytes = layer_count > 1 ? layer_stride : 0;
     a.slots = slots;
-    fill_rows(a, D, group, n_tokens, kStoreUnroll, row_alignment(D, k_new, v_new, token_stride, a.new_layer_stride), dev);
+    fill_rows(a, D, group, n_tokens, layer_count, kStoreUnroll, row_alignment(D, k_new, v_new, token_stride, a.new_layer_stride), dev);
     return launch_store<false>(D, a, layer_count, "q4_write_kv: launch", static_cast<cudaStream_t>(stream));
 }
 
@@ -560,7 +583,7 @@ extern "C" zp_status zp_q4_append_kv(const zp_cache_desc *D, int32_t group, cons
     a.table = block_table;
     a.table_stride = table_stride;
     a.seq_lens = seq_lens;
-    fill_rows(a, D, group, B, kStoreUnroll, row_alignment(D, k_new, v_new, row, 0), dev);
+    fill_rows(a, D, group, B, 1, kStoreUnroll, row_alignment(D, k_new, v_new, row, 0), dev);
     return launch_store<true>(D, a, 1, "q4_append_kv: launch", static_cast<cudaStream_t>(stream));
 }
 
@@ -589,7 +612,7 @@ extern "C" zp_status zp_q4_read_kv(const zp_cache_desc *D, int32_t group, const 
     a.v = v_out;
     a.token_stride = token_stride;
     a.out_layer_stride = layer_count > 1 ? out_layer_stride : 0;
-    fill_rows(a, D, group, n_tokens, kReadUnroll, row_alignment(D, k_out, v_out, token_stride, a.out_layer_stride), dev);
+    fill_rows(a, D, group, n_tokens, layer_count, kReadUnroll, row_alignment(D, k_out, v_out, token_stride, a.out_layer_stride), dev);
     const dim3 grid = row_grid(a, layer_count);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool wide = D->head_dim == 128;
@@ -623,7 +646,8 @@ extern "C" zp_status zp_q4_compact_pages(const zp_cache_desc *D, int32_t group, 
         return fail(ZP_ERR_INVALID_ARG, "q4_compact: global_F needs the score rows");
     if ((long long)target_stride * D->block_size < k)
         return fail(ZP_ERR_CAPACITY, "q4_compact: %d target blocks hold fewer than k=%d rows", target_stride, k);
-    if (n > 65535 || layer_count > 65535) return fail(ZP_ERR_SHAPE, "q4_compact: n=%d layer_count=%d", n, layer_count);
+    if (n > 65535 || layer_count > 65535 || k > 1 << 30)
+        return fail(ZP_ERR_SHAPE, "q4_compact: n=%d layer_count=%d k=%d", n, layer_count, k);
     if ((long long)D->n_total_blocks * D->block_size * D->h_kv > INT32_MAX)
         return fail(ZP_ERR_SHAPE, "q4_compact: %d blocks of %d tokens and %d heads exceed 32-bit rows", D->n_total_blocks,
                     D->block_size, D->h_kv);

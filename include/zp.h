@@ -564,7 +564,7 @@ zp_status zp_q4_decode_attn(const zp_cache_desc *D, int32_t group, const void *q
  * parameters (nothing is quantised again), global_F as there; layer_stride in bytes.
  * In place under the same rule.  Recorded as ZP_ERR_DEVICE and skipped: a kept position or its
  * block out of range (detail 0x154), a target block (0x155), a score row (0x156).
- * Limits: n and layer_count <= 65535, N_total * b * h_kv below 2^31 (ZP_ERR_SHAPE). */
+ * Limits: n and layer_count <= 65535, k <= 2^30, N_total * b * h_kv below 2^31 (ZP_ERR_SHAPE). */
 zp_status zp_q4_compact_pages(const zp_cache_desc *D, int32_t group, void *k_base, void *v_base, int64_t layer_stride,
                               int32_t layer_count, float *global_F, int64_t F_layer_stride,
                               const zp_score_rows *scores, const int32_t *src_table, int32_t table_stride,

@@ -154,3 +154,9 @@ def test_plain_form(d, group):
     assert np.array_equal(got, code)
     err = np.abs(q4.values(got, step, lo, group) - x).reshape(40, 2, -1, group)
     assert (err <= step[..., None] * 0.5 + 2.0 ** -22).all()
+
+
+def test_compact_ranks(zp):
+    """Ranks are counted in 32 bits, a few rounds ahead."""
+    args = (_desc(zp), 32, P, P, 0, 1, None, 0, None, P, 4, P, 1 << 30, P, P)
+    assert zp.lib.zp_q4_compact_pages(*args, (1 << 30) + 1, None, 1, None) == 2
