@@ -14,6 +14,16 @@
 // goes on in other CTAs.  q4_finish_kernel joins those (at most one pair per CTA boundary) and,
 // on window steps, turns the logits that the attention left (log2 units) into probabilities
 // with the final sums, takes the maximum over the q heads and adds 1/w of it to the score.
+//
+// Bound: a 4-bit row of 128 elements is 80 bytes, for which each of 4 q heads asks 512
+// multiplications: with many tokens the issue of instructions (about 375 per tile and scheduler,
+// of which every second one goes to the half-rate integer pipe) and the memory are near one
+// another, below that the time before the first copy and after the last product.  Of keys and values,
+// 32 q and 8 kv heads of 128, groups of 32, with a copy's rate as 1:
+//     512 sequences of 1k to 4k tokens   319 us  5.2 TB/s  0.78
+//      64 of 4k at most                   51      4.1      0.62   (first copy at 4.3 us, last product at 43)
+//     256 of 4k at most, scored          174      4.0      0.59   (logits written and read besides)
+//       1 of 32k                          22      1.9      0.29   (3.4 units per warp: latencies)
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -187,34 +197,39 @@ __device__ __noinline__ void drain(uint64_t *full, int stages, int i, int n) {
 }
 
 // ---------------------------------------------------------------- records
-// One pair's part in one range: per head float4 (reference m, sum that divides the output,
-// sum, 0), then the accumulators [G][D], all relative to 2^m.
+// One pair's part in one range: per head float4 (reference, sum that divides the output, sum, 0),
+// then the accumulators [G][D], all relative to 2^reference.  (Joined by the last CTA to arrive at a pair
+// instead of by a second kernel, 1 x 32k took 28 us: 19 CTAs meet on its counter.)
 __device__ __forceinline__ int rec_floats(const Q4Args &a, int d) { return a.G * (d + 4); }
 
 // Normaliser of the score: p = 2^(logit - c).  An empty sum gives no score.
 __device__ __forceinline__ float score_norm(float m, float l) { return l == 0.f ? INFINITY : m + log2f(l); }
 
 // ---------------------------------------------------------------- tensor-core products
-// Up to 8 q heads as the 8 columns of mma.sync m16n8k16: logits[t][h] with the key codes as the left operand, out^T[i][h] with the value codes.  (One kv head has 8
-// query rows at most: the 128 rows of a tcgen05 tile would stand empty, and its operands
-// would have to be written to shared memory at four times the size of the codes.)
+// Up to 8 q heads as the 8 columns of mma.sync m16n8k16: logits[t][h] with the key codes as the
+// left operand, out^T[i][h] with the value codes.  (One kv head has 8 query rows at most: the 128
+// rows of a tcgen05 tile would stand empty, and its operands would have to be written to shared
+// memory at four times the size of the codes.)
 //   logits:  sum_i q_i (lo + c_i step) = lo sum_i q_i + step sum_i q_i c_i per group.  The codes
 //     go in as fp16 numbers without any arithmetic: the low nibble of a halfword, masked, is the
-//     subnormal c 2^-24 and the next one c 2^-20 (whose queries are 2^-4 times as large), so
-//     that a word of eight codes takes four masks and one shift.  The queries are scaled by a power
-//     of two to fill fp16's range; those of 8 bits that lie within 2^-24 of the largest stay exact.
-//     The lo term is a product of its own, of the parameter words (step, lo) as they lie in the
-//     tile with (0, sum q), the sum in three bf16 parts of 8 bits.  Nothing else is rounded to 16
-//     bits: the logits are those of 32-bit arithmetic.
-//   output:  sum_t p_t lo_t + sum_t p_t step_t c_t.  The first is a product of p (two bf16 parts, transposed
-//     by movmatrix) with the parameters as they are.  For the second p goes to fp16 and its product with
-//     the step of a group to fp16 again, each rounded by 2^-12 at most; the codes are subnormals once more.  For
-//     that a step's exponent is moved by what suits the range's first unit.  A unit with steps far
-//     from those (p step needs bf16's range) takes its products in bf16, with codes 0x4300 | c = 128 + c less
-//     128; both roundings are then by 2^-9.  The sum that divides is that of p in two parts.
+//     subnormal c 2^-24 and the next one c 2^-20 (whose queries are 2^-4 times as large), so that a
+//     word of eight codes takes four masks and one shift.  The queries are scaled by a power of two
+//     to fill fp16's range; those of 8 bits that lie within 2^-24 of the largest stay exact.  The
+//     lo term is a product of its own, of the parameter words (step, lo) as they lie in the tile
+//     with (0, sum q), the sum in three bf16 parts of 8 bits.  Nothing else is rounded to 16 bits:
+//     the logits are those of 32-bit arithmetic.
+//   output:  sum_t p_t lo_t + sum_t p_t step_t c_t.  The first is a product of p (two bf16 parts,
+//     transposed by movmatrix) with the parameters as they are.  For the second p goes to fp16 and
+//     its product with the step of a group to fp16 again, each rounded by 2^-12 at most; the codes
+//     are subnormals once more.  For that a step's exponent is moved by what suits the range's
+//     first unit.  A unit with steps far from those (p step needs bf16's range) takes its products
+//     in bf16, with codes 0x4300 | c = 128 + c less 128; both roundings are then by 2^-9.  The sum
+//     that divides is that of p in two parts.
 //   fp32 queries: three parts of 8 bits of the query for the logits; for the output p and p step in
-//     three bf16 parts each, with codes c - 8 and the parameters' sum of lo + 8 step, and every unit's products are summed from zero and added to
-//     the accumulators in 32 bits, since the tensor core's own additions cut what they drop.
+//     three bf16 parts each, with codes c - 8 and the parameters' sum of lo + 8 step, and every
+//     unit's products are summed from zero and added to the accumulators in 32 bits, since the
+//     tensor core's own additions cut what they drop.  (64 sequences of 2k tokens at most: 57 us,
+//     with 32-bit FMAs 98.)
 // ldmatrix of a natural row of codes gives lane 4t + j the word j of a 16-byte chunk of
 // token t, the layout of the left operand; its transposed form gives the codes of two
 // adjacent tokens for 4 dimensions, the layout of the transposed values.
@@ -289,11 +304,12 @@ __device__ __forceinline__ void lds(const uint32_t *p, uint32_t (&w)[N]) {
     }
 }
 
-// Probabilities are kept relative to 2^(m - kScale), and m follows the maximum when that passes it by
-// kLazyMax: below 2^15, so that fp16 holds them, with 11 bits down to 2^-25 and no zero above 2^-36 of 2^m.
+// Probabilities are kept relative to 2^(m - kScale), and m follows the maximum when that passes
+// it by kLazyMax: they stay below 2^15, so that fp16 holds them, with 11 bits down to 2^-14, that
+// is 2^-25 of 2^m's, and nothing above 2^-36 of that goes to zero.
 constexpr float kLazyMax = 4.f, kScale = 11.f;
-// Steps that a range's value products take in fp16: exponents from kBelow under the largest of the range's first unit
-// to kWindow - 1 - kBelow above it.  (p step is then below 2^16; the smallest step is still a normal number.)
+// Steps that a range's value products take in fp16: exponents from kBelow under the largest of the
+// range's first unit to kWindow - 1 - kBelow above it.
 constexpr int kBelow = 10, kWindow = 14;
 constexpr uint32_t kNoWindow = 0xFFFFFFFFu;
 
@@ -459,8 +475,8 @@ struct TcWarp {
                     nibbles(r[2 * i + 1], u[1], u[3], v[1], v[3]);
                     const auto &q = qb[0][c + i];
                     if constexpr (kF32) {
-                        // the small parts together, then the two halves of the first by themselves: the tensor core's
-                        // own additions cut what they drop
+                        // the small parts together, then the two halves of the first by themselves:
+                        // the tensor core's own additions cut what they drop
                         float d1[4], d2[4];
                         mma_f16_0(d, u[0], u[1], u[2], u[3], qb[kQ - 1][c + i][0][0], qb[kQ - 1][c + i][0][1]);
                         mma_f16(d, v[0], v[1], v[2], v[3], qb[kQ - 1][c + i][1][0], qb[kQ - 1][c + i][1][1]);
@@ -538,7 +554,8 @@ struct TcWarp {
         else values_bf16(vt, y, v0, v1, at, lane);
     }
 
-    // The nibbles of a word as fp16 pairs: c 2^-24 of nibbles 0, 4 and 2, 6 (a, c), c 2^-20 of 1, 5 and 3, 7 (b, d).
+    // The nibbles of a word as fp16 pairs: c 2^-24 of nibbles 0, 4 and 2, 6 (a, c), c 2^-20 of 1, 5
+    // and 3, 7 (b, d).
     static __device__ __forceinline__ void nibbles(uint32_t w, uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d) {
         a = w & 0x000F000Fu;
         b = w & 0x00F000F0u;
@@ -563,9 +580,9 @@ struct TcWarp {
         w[2] = codes<E, CENTRE>(x1), w[3] = codes<E + 1, CENTRE>(x1);
     }
 
-    // The accumulators of the value products in fp16 hold 2^(89 - e) times the sums of p step c (e: the window's
-    // lowest exponent), 16 times that for odd dimensions; to and from sums of p step c.  (In two factors:
-    // the power may be past the largest float.)
+    // The accumulators of the value products in fp16 hold 2^(89 - e) times the sums of p step c (e:
+    // the window's lowest exponent), 16 times that for odd dimensions; to and from sums of p step c.
+    // (In two factors: the power may be past the largest float.)
     __device__ __forceinline__ void rescale(bool plain) {
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
@@ -582,9 +599,10 @@ struct TcWarp {
     __device__ __forceinline__ void values_bf16(const unsigned char *vt, const float (&y)[2][4], int v0, int v1, uint32_t at,
                                                 int lane) {
         const int n = lane >> 2, j = lane & 3;
-        // ---- lane t looks at token t: do the steps of all tokens lie in the window?  Two lanes then lay out their
-        // two tokens' parameters, by group: steps in fp16 (bf16's bits with the exponent moved and three zeros
-        // behind), lo as it is.
+        // ---- lane t looks at token t: do the steps of all tokens lie in the window?  Two lanes then
+        // lay out their two tokens' parameters, by group: steps in fp16 (bf16's bits with the exponent
+        // moved and three zeros behind), lo as it is.  (Once per unit, not by each lane that needs them:
+        // 512 sequences 340 -> 319 us.)
         bool wild;
         {
             uint32_t w[NG];
@@ -667,7 +685,8 @@ struct TcWarp {
         }
     }
 
-    // The values' products where steps of any size meet: p, and p step, rounded to bf16, the codes as bf16 numbers.
+    // The values' products where steps of any size meet: p, and p step, rounded to bf16, the codes
+    // as bf16 numbers.
     __device__ __forceinline__ void values_wide(const unsigned char *vt, const float (&p)[2][4], uint32_t at, int lane) {
         const int j = lane & 3;
 #pragma unroll
@@ -799,9 +818,12 @@ struct TcWarp {
 };
 
 // ---------------------------------------------------------------- attention
-// Shared memory: rings (a warp's tiles; at its end the record of a pair that goes on
-// behind its range), what a warp lays out for itself, records of pairs that began before a warp's range (written while the ring is in
-// use; in the workspace where there is no room), prefix.
+// Shared memory: rings (a warp's tiles; at its end the record of a pair that goes on behind its
+// range), what a warp lays out for itself, records of pairs that began before a warp's range
+// (written while the ring is in use; in the workspace where there is no room), prefix.
+// Sixteen warps of 128 registers in bf16, twelve of 168 in fp32 (10, 13 and 14 were slower for
+// either), each with a ring of its own: no barrier between them, and 2 to 4 units (5 KB each at
+// d = 128 and groups of 32) in flight per warp are 160 KB and more per SM.
 template <class W>
 __host__ __device__ inline size_t attention_smem(int stages, int tile, int B, int G, bool heads_here) {
     return (size_t)W::kWarps * ((size_t)stages * 4 * tile + W::kSharedBytes + (heads_here ? (size_t)G * (W::kD + 4) * 4 : 0)) + ((size_t)B + 1) * 4;
@@ -1004,7 +1026,9 @@ __global__ void __launch_bounds__(W::kWarps * 32, 1) q4_attention_kernel(const Q
 
 // ---------------------------------------------------------------- what is left
 // CTA c joins the records of the pair that its counterpart of the attention kernel began and
-// did not finish, and forms the score of that one's units.
+// did not finish, and forms the score of that one's units.  Bound by latencies: about 3 us behind the
+// attention kernel without a score, 20 for 256 sequences of 4k tokens, whose logits (60 MB) and
+// scores it reads; four tokens per lane at a time, and its statistics, length and slot in one go.
 constexpr int kFinishThreads = 512, kScoreUnroll = 4;
 
 // Record of CTA c of a pair cut between CTAs, which CTA c0 begins.
@@ -1012,8 +1036,8 @@ __device__ __forceinline__ const float *cta_record(const Q4Args &a, int c0, int 
     return a.rec + (size_t)(2 * c + (c == c0 ? 1 : 0)) * rec_n;
 }
 
-// Every 32nd token from t to t1 of a pair: S += share * 2^max_q (logit - c), or = where `fresh` and at P.
-// G4: vectors of four heads (0: any number of heads).  All loads of a round are under way at once.
+// Every 32nd token from t to t1 of a pair: S += share * 2^max_q (logit - c), or = where `fresh` and
+// at P.  G4: vectors of four heads (0: any number of heads).  All loads of a round are under way at once.
 template <int G4>
 __device__ __forceinline__ void score_tokens(const Q4Args &a, const float *lg, const float (&c)[8], float *S, int t, int t1,
                                              int P, bool fresh, float share) {

@@ -545,13 +545,16 @@ zp_status zp_q4_read_kv(const zp_cache_desc *D, int32_t group, const void *k_bas
  * its product with a group's step, are each rounded to 11 bits (to 8 in runs of 32 tokens whose value
  * steps differ by more than 2^10 from the first run's); logits, softmax statistics and scores are
  * those of 32-bit arithmetic.  fp32: three parts of 8 bits or more of each factor.  Queries of 2^117
- * and more in size give NaN.  A call with the same arguments gives the same bits.  Recorded as ZP_ERR_DEVICE: a length outside [0, table_stride * b] (detail 0x158;
- * taken as the nearer bound), a block outside [0, N_total) among a sequence's blocks (0x159; its
- * tokens weigh nothing), a slot >= n_score_rows (0x15a; not scored).
+ * and more in size give NaN, values of 2^92 and more may (weights are held up to 2^15 times too
+ * large until the end).  A call with the same arguments gives the same bits.  Recorded as
+ * ZP_ERR_DEVICE: a length outside [0, table_stride * b] (detail 0x158; taken as the nearer bound), a
+ * block outside [0, N_total) among a sequence's blocks (0x159; its tokens weigh nothing), a slot
+ * >= n_score_rows (0x15a; not scored); as ZP_ERR_TIMEOUT: copies that did not arrive (0x15b).
  * The workspace is scratch: any content on entry, nothing kept; two calls that may
  * overlap need one each.  Its size with scored = 0 serves calls without score_accum.
  * Limits: B <= 4096, h_q/h_kv <= 8, B * table_stride * b below 2^31, N_total * h_kv * b/16
- * below 2^31, B * h_kv * (table_stride * b / 32 + 1) below 2^30 (ZP_ERR_SHAPE); buffers 16-byte aligned; score_accum float [rows][h_kv][table_stride * b]. */
+ * below 2^31, B * h_kv * (table_stride * b / 32 + 1) below 2^30 (ZP_ERR_SHAPE); buffers 16-byte
+ * aligned; score_accum float [rows][h_kv][table_stride * b]. */
 size_t zp_q4_decode_workspace_size(const zp_cache_desc *D, int32_t group, int32_t B, int32_t table_stride,
                                    int32_t scored);
 zp_status zp_q4_decode_attn(const zp_cache_desc *D, int32_t group, const void *q, const void *k_cache,
