@@ -303,7 +303,9 @@ def _ints(t, dev: int, name: str, numel=None):
 
 
 def _device() -> int:
-    return torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -2
+    if torch.cuda.is_initialized():
+        return torch._C._cuda_getDevice()
+    return torch.cuda.current_device() if torch.cuda.is_available() else -2
 
 
 def _raw_stream(stream, dev: int) -> int:
@@ -494,11 +496,25 @@ def _q4_shape(desc, group):
     return desc.n_total_blocks, desc.h_kv, desc.block_size >> 4, (d << 3) + 64 * (d // group if group > 0 else 0)
 
 
-def _q4_cache_of(t, shape, dev: int, name: str):
-    """Address of a cache tensor of `shape`."""
-    if t.shape != shape or t.dtype is not torch.uint8:
-        raise ValueError("%s must be uint8 [N_total][h_kv][b/16][tile] = %s, is %s %s" % (name, shape, t.dtype, tuple(t.shape)))
-    return _ptr_on(t, dev, name)
+def _q4_check(k_cache, v_cache, shape):
+    """Refuses cache tensors of other types or shapes."""
+    if not (k_cache.dtype is v_cache.dtype is torch.uint8 and k_cache.shape == shape and v_cache.shape == shape):
+        raise ValueError("k_cache and v_cache must be uint8 [N_total][h_kv][b/16][tile] = %s, are %s %s and %s %s"
+                         % (shape, k_cache.dtype, tuple(k_cache.shape), v_cache.dtype, tuple(v_cache.shape)))
+
+
+def _q4_here(dev: int, tensors, names) -> None:
+    """Refuses tensors that are not contiguous on CUDA device `dev`, the current one.  (One loop for all:
+    a call's checks are a good part of its time where the batch is small.)"""
+    for t in tensors:
+        if t.get_device() != dev or not t.is_contiguous():
+            for t, name in zip(tensors, names):
+                _ptr_on(t, dev, name)
+
+
+def _q4_ints(block_table, seq_lens, B) -> None:
+    if not (block_table.dtype is seq_lens.dtype is torch.int32 and seq_lens.numel() == B):
+        raise ValueError("block_table and seq_lens must be int32, with an entry of seq_lens per row of block_table")
 
 
 def _q4_caches(desc, group, k_cache, v_cache, dev):
@@ -509,8 +525,9 @@ def _q4_caches(desc, group, k_cache, v_cache, dev):
     if k_cache.dim() == 5:
         layers = k_cache.shape[0]
         shape = (layers,) + shape
-    return (_q4_cache_of(k_cache, shape, dev, "k_cache"), _q4_cache_of(v_cache, shape, dev, "v_cache"), layers,
-            0 if layers is None else k_cache.stride(0))
+    _q4_check(k_cache, v_cache, shape)
+    _q4_here(dev, (k_cache, v_cache), ("k_cache", "v_cache"))
+    return k_cache.data_ptr(), v_cache.data_ptr(), layers, 0 if layers is None else k_cache.stride(0)
 
 
 def _q4_rows(desc, k, v, n, layers, dev, names):
@@ -544,18 +561,21 @@ def zp_q4_write_kv(desc, k_new, v_new, slots, k_cache, v_cache, group=32, stream
         _check(rc)
 
 
+_Q4_APPEND = ("k_new", "v_new", "k_cache", "v_cache", "block_table", "seq_lens")
+
+
 def zp_q4_append_kv(desc, k_new, v_new, k_cache, v_cache, block_table, seq_lens, group=32, stream=None) -> None:
     """zp_append_kv into a 4-bit cache: k_new, v_new [B][h_kv][d], one token per sequence."""
     B, table_stride = _table(block_table)
     dev = _device()
-    cache = _q4_shape(desc, group)
-    K, V = _q4_cache_of(k_cache, cache, dev, "k_cache"), _q4_cache_of(v_cache, cache, dev, "v_cache")
+    _q4_check(k_cache, v_cache, _q4_shape(desc, group))
     shape = (B, desc.h_kv, desc.head_dim)
     if k_new.shape != shape or v_new.shape != shape or not (k_new.dtype is v_new.dtype is _TORCH.get(desc.dtype)):
         raise ValueError("k_new and v_new must be [B][h_kv][d] = %s of the descriptor's type" % (shape,))
-    rc = lib.zp_q4_append_kv(desc, group, _ptr_on(k_new, dev, "k_new"), _ptr_on(v_new, dev, "v_new"), K, V,
-                             _ints(block_table, dev, "block_table"), table_stride, _ints(seq_lens, dev, "seq_lens", B), B,
-                             _raw_stream(stream, dev))
+    _q4_ints(block_table, seq_lens, B)
+    _q4_here(dev, (k_new, v_new, k_cache, v_cache, block_table, seq_lens), _Q4_APPEND)
+    rc = lib.zp_q4_append_kv(desc, group, k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                             block_table.data_ptr(), table_stride, seq_lens.data_ptr(), B, _raw_stream(stream, dev))
     if rc:
         _check(rc)
 
@@ -580,6 +600,7 @@ def zp_q4_decode_workspace_size(desc: CacheDesc, B: int, table_stride: int, grou
 
 
 _Q4_SIZES = {}  # workspace sizes by shape and device
+_Q4_DECODE = ("q", "out", "k_cache", "v_cache", "block_table", "seq_lens")
 
 
 def zp_q4_decode_attn(desc, q, k_cache, v_cache, block_table, seq_lens, out, score_accum=None, window=0, workspace=None,
@@ -592,19 +613,20 @@ def zp_q4_decode_attn(desc, q, k_cache, v_cache, block_table, seq_lens, out, sco
         raise ValueError("q and out must be [B][h_q][d] = %s, are %s and %s" % (shape, tuple(q.shape), tuple(out.shape)))
     if not (q.dtype is out.dtype is dt):
         raise ValueError("q and out must have the descriptor's type")
-    cache = _q4_shape(desc, group)
-    K, V = _q4_cache_of(k_cache, cache, dev, "k_cache"), _q4_cache_of(v_cache, cache, dev, "v_cache")
-    n_rows = 0
+    _q4_check(k_cache, v_cache, _q4_shape(desc, group))
+    _q4_ints(block_table, seq_lens, B)
+    _q4_here(dev, (q, out, k_cache, v_cache, block_table, seq_lens), _Q4_DECODE)
+    n_rows, S, rows = 0, None, None
     if score_accum is not None:
         n_rows = score_accum.shape[0]
         if (score_accum.dtype is not torch.float32 or score_accum.dim() != 3 or (score_rows is None and n_rows < B) or
                 score_accum.shape[1:] != (desc.h_kv, table_stride * desc.block_size)):
             raise ValueError("score_accum must be float32 [R][h_kv][table_stride*b] with a row per batch entry or a slot map")
+        S, rows = _ptr_on(score_accum, dev, "score_accum"), _ints(score_rows, dev, "score_rows", B)
     elif score_rows is not None:
         raise ValueError("score_rows needs score_accum")
-    args = (desc, group, _ptr_on(q, dev, "q"), K, V, _ints(block_table, dev, "block_table"), table_stride,
-            _ints(seq_lens, dev, "seq_lens", B), B, _ptr_on(out, dev, "out"), _ptr_on(score_accum, dev, "score_accum"),
-            _ints(score_rows, dev, "score_rows", B), n_rows, window)
+    args = (desc, group, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), table_stride,
+            seq_lens.data_ptr(), B, out.data_ptr(), S, rows, n_rows, window)
     on = _raw_stream(stream, dev)
     if workspace is None:
         # memory of the stream that the work runs on, given back behind it
@@ -614,11 +636,11 @@ def zp_q4_decode_attn(desc, q, k_cache, v_cache, block_table, seq_lens, out, sco
             if len(_Q4_SIZES) > 1000:
                 _Q4_SIZES.clear()
             n = _Q4_SIZES[key] = zp_q4_decode_workspace_size(desc, B, table_stride, group, score_accum is not None)
-        at = torch.cuda.caching_allocator_alloc(n, dev, on)
+        at = torch._C._cuda_cudaCachingAllocator_raw_alloc(n, on)
         try:
             rc = lib.zp_q4_decode_attn(*args, at, n, on)
         finally:
-            torch.cuda.caching_allocator_delete(at)
+            torch._C._cuda_cudaCachingAllocator_raw_delete(at)
     else:
         rc = lib.zp_q4_decode_attn(*args, _ptr_on(workspace, dev, "workspace"), workspace.nbytes, on)
     if rc:
