@@ -14,6 +14,8 @@
 // goes on in other CTAs.  q4_finish_kernel joins those (at most one pair per CTA boundary) and,
 // on window steps, turns the logits that the attention left (log2 units) into probabilities
 // with the final sums, takes the maximum over the q heads and adds 1/w of it to the score.
+// With few pairs a pair's units are cut between the CTAs of a cluster instead, and nothing else is
+// launched (pick_cluster).
 //
 // Bound: a 4-bit row of 128 elements is 80 bytes, for which each of 4 q heads asks 512
 // multiplications: with many tokens the issue of instructions (about 375 per tile and scheduler,
@@ -24,8 +26,14 @@
 //      64 of 4k at most                   51      4.1      0.62   (first copy at 4.3 us, last product at 43)
 //     256 of 4k at most, scored          174      4.0      0.59   (logits written and read besides)
 //       1 of 32k                          22      1.9      0.29   (3.4 units per warp: latencies)
+//       4 of 2k                           10.6                    (latencies: lengths, table, tiles, join)
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <math.h>
+
+#include <map>
+#include <mutex>
+#include <utility>
 
 #include "q4_format.cuh"
 
@@ -45,7 +53,7 @@ struct Q4Args {
     const int32_t *seq_lens;
     int B, h_q, h_kv, G, b, n_total;
     int tile, tpb;  // bytes of a tile, tiles of a block and kv head
-    unsigned inv_tpb, inv_ranges;  // reciprocals (div_by) of tpb and of grid * warps
+    unsigned inv_tpb, inv_ranges;  // reciprocals (div_by) of tpb and of the CTAs * warps that share a split
     float qscale;   // log2(e) / sqrt(d)
     int want_score, window;
     float *score;
@@ -57,6 +65,7 @@ struct Q4Args {
     float *rec;     // [2 * CTAs + warps][G * (d + 4)]: per head (reference, sum for the output, sum, 0), then accumulators
     float *logits;  // [units][32][G]
     int grid, warps, stages;  // CTAs of the attention kernel, warps of one, units in a warp's ring
+    int cluster;              // 0: all pairs are one line, cut evenly; else the CTAs (a cluster) of every pair
     bool heads_here;          // records of pairs that began before a warp's range: in shared memory
     unsigned *err;
 };
@@ -82,18 +91,18 @@ struct Split {
     __device__ __forceinline__ int cta_of(int x) const { return (int)(((x + 1ll) * W - 1) / U) / per_cta; }
 };
 
-__device__ __forceinline__ Split make_split(const Q4Args &a, int units) {
+__device__ __forceinline__ Split make_split(const Q4Args &a, int units, int grid) {
     Split p;
-    p.U = units * a.h_kv;
-    if (p.U >= a.grid * a.warps) {
+    p.U = units;
+    if (p.U >= grid * a.warps) {
         p.per_cta = a.warps;
-        p.ctas = a.grid;
+        p.ctas = grid;
         p.inv_W = a.inv_ranges;
     } else {
-        const int want = (int)(((unsigned)p.U + a.grid - 1) / (unsigned)a.grid);
+        const int want = (int)(((unsigned)p.U + grid - 1) / (unsigned)grid);
         p.per_cta = want < 1 ? 1 : want;
         const int most = p.U / p.per_cta;
-        p.ctas = most < a.grid ? most : a.grid;
+        p.ctas = most < grid ? most : grid;
         const int W = p.per_cta * p.ctas;
         p.inv_W = W <= 1 ? 0u : 0xFFFFFFFFu / (unsigned)W + 1;
     }
@@ -112,6 +121,7 @@ __device__ __forceinline__ int checked_len(const Q4Args &a, int L) {
     }
     return L;
 }
+__device__ __forceinline__ int units_of(int L) { return (int)(((long long)L + kUnit - 1) / kUnit); }
 __device__ __forceinline__ int q4_len(const Q4Args &a, int s) { return checked_len(a, __ldg(a.seq_lens + s)); }
 
 // prefix[s] = units of the sequences before s; blockDim.x threads, a multiple of 32.
@@ -121,7 +131,7 @@ __device__ void unit_prefix(const Q4Args &a, int *prefix, int *warp_sum) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int mine = 0;
     for (int s = s0; s < s1; ++s) {
-        const int n = (int)(((long long)q4_len(a, s) + kUnit - 1) / kUnit);
+        const int n = units_of(q4_len(a, s));
         prefix[s] = n;
         mine += n;
     }
@@ -159,6 +169,14 @@ struct Cursor {
         const int in = x - prefix[s] * h_kv;
         h = in / n;
         u = in - h * n;
+    }
+    // unit x of the pair that the CTA's cluster has
+    __device__ __forceinline__ void at(const Q4Args &a, int x) {
+        const int pair = (int)blockIdx.x / a.cluster;
+        s = pair / a.h_kv;
+        h = pair - s * a.h_kv;
+        u = x;
+        n = units_of(q4_len(a, s));
     }
     __device__ __forceinline__ void next(const int *prefix, int B, int h_kv) {
         if (++u < n) return;
@@ -829,7 +847,7 @@ __host__ __device__ inline size_t attention_smem(int stages, int tile, int B, in
     return (size_t)W::kWarps * ((size_t)stages * 4 * tile + W::kSharedBytes + (heads_here ? (size_t)G * (W::kD + 4) * 4 : 0)) + ((size_t)B + 1) * 4;
 }
 
-template <class W>
+template <class W, bool CLUSTER>
 __global__ void __launch_bounds__(W::kWarps * 32, 1) q4_attention_kernel(const Q4Args a) {
     constexpr int D = W::kD, kWarps = W::kWarps;
     using T = typename W::T;
@@ -853,13 +871,23 @@ __global__ void __launch_bounds__(W::kWarps * 32, 1) q4_attention_kernel(const Q
     if (tid == 0) abort_s = 0;
     fence_barrier_init();
     pdl_wait();
-    unit_prefix(a, prefix, sums_s);  // (has the barrier behind the initialisation)
-    if (blockIdx.x == 0)
-        for (int s = tid; s <= a.B; s += blockDim.x) a.prefix[s] = prefix[s];
-    if (prefix[a.B] == 0) return;
-    const Split split = make_split(a, prefix[a.B]);
-    const bool mine = (int)blockIdx.x < split.ctas && warp < split.per_cta;
-    const int g = blockIdx.x * split.per_cta + warp;
+    // the units that are cut: of all pairs, or (cluster) of the one that this CTA's cluster has
+    int units, cta = blockIdx.x;
+    if constexpr (CLUSTER) {
+        const int pair = cta / a.cluster;
+        cta -= pair * a.cluster;
+        units = units_of(q4_len(a, pair / a.h_kv));
+        __syncthreads();  // (the initialisation)
+    } else {
+        unit_prefix(a, prefix, sums_s);  // (has the barrier behind the initialisation)
+        if (blockIdx.x == 0)
+            for (int s = tid; s <= a.B; s += blockDim.x) a.prefix[s] = prefix[s];
+        units = prefix[a.B] * a.h_kv;
+    }
+    if (units == 0) return;
+    const Split split = make_split(a, units, CLUSTER ? a.cluster : a.grid);
+    const bool mine = cta < split.ctas && warp < split.per_cta;
+    const int g = cta * split.per_cta + warp;
     const int x0 = mine ? split.start(g) : 0;
     const int n = mine ? split.start(g + 1) - x0 : 0;
     if (n > 0) {
@@ -872,7 +900,8 @@ __global__ void __launch_bounds__(W::kWarps * 32, 1) q4_attention_kernel(const Q
             pair = put_pair;
             if (i0 + lane >= n) return;
             Cursor c;
-            c.seek(prefix, a.B, a.h_kv, x0 + i0 + lane);
+            if constexpr (CLUSTER) c.at(a, x0 + i0 + lane);
+            else c.seek(prefix, a.B, a.h_kv, x0 + i0 + lane);
             put_pair = c.s * a.h_kv + c.h;
             int blk[2], sub[2];  // (read beside the length: a row of the table has an entry for every token below its stride)
 #pragma unroll
@@ -970,13 +999,15 @@ __global__ void __launch_bounds__(W::kWarps * 32, 1) q4_attention_kernel(const Q
         }
     }
     __syncthreads();
-    if (abort_s) return;
+    if (!CLUSTER && abort_s) return;  // (the others of a cluster read this CTA's shared memory: it stays)
     // ---- the records of this CTA: a pair's chain begins in a warp's tail, or before the CTA in
     // the first warp's head, and goes on in the heads of the next warps.  A warp joins one head
     // of one chain at a time.
     const int my_head = lane < split.per_cta ? head_s[lane] : -1;
     const unsigned tails = __ballot_sync(0xFFFFFFFFu, lane < split.per_cta && tail_s[lane] >= 0);
     const int before = head_s[0] >= 0, chains = before + __popc(tails);
+    // a cluster's CTA leaves its record in the last ring (empty by now; the one tail there is lies in the first)
+    float *joined = reinterpret_cast<float *>(smem + (kWarps - 1) * ring_bytes);
     for (int task = warp; task < chains * a.G; task += kWarps) {
         const int chain = task / a.G, q = task - chain * a.G;
         const bool side = chain >= before;  // it begins in this CTA
@@ -1016,11 +1047,41 @@ __global__ void __launch_bounds__(W::kWarps * 32, 1) q4_attention_kernel(const Q
             for (int e = 0; e < kOwn; ++e) out[e] = from_f<T>(x[e] * r);
             if (a.want_score && lane == 0) a.stats[(size_t)s * a.h_q + h * a.G + q] = score_norm(m, l);
         } else {
-            float *to = a.rec + (size_t)(2 * blockIdx.x + side) * rec_n;
+            float *to = CLUSTER ? joined : a.rec + (size_t)(2 * blockIdx.x + side) * rec_n;
 #pragma unroll
             for (int e = 0; e < kOwn; ++e) to[4 * a.G + q * D + lane * kOwn + e] = x[e];
             if (lane == 0) reinterpret_cast<float4 *>(to)[q] = make_float4(m, lo, l, 0.f);
         }
+    }
+    if constexpr (CLUSTER) {
+        if (split.ctas < 2) return;
+        // ---- the records of the cluster's CTAs, a warp per head
+        const auto cluster = cooperative_groups::this_cluster();
+        cluster.sync();
+        const int pair = (int)blockIdx.x / a.cluster, rank = (int)blockIdx.x % a.cluster;
+        for (int q = rank + a.cluster * warp; q < a.G; q += a.cluster * kWarps) {
+            constexpr int kOwn = D / 32;
+            float4 r = make_float4(-INFINITY, 0.f, 0.f, 0.f);  // lane c: CTA c's
+            if (lane < split.ctas) r = reinterpret_cast<const float4 *>(cluster.map_shared_rank(joined, lane))[q];
+            float m = r.x;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            const float f = ex2_approx(r.x - (m == -INFINITY ? 0.f : m));
+            float lo = 0.f, x[kOwn] = {};
+#pragma unroll 4
+            for (int c = 0; c < split.ctas; ++c) {
+                const float *v = cluster.map_shared_rank(joined, c) + 4 * a.G + q * D + lane * kOwn;
+                const float fc = __shfl_sync(0xFFFFFFFFu, f, c);
+                lo = fmaf(__shfl_sync(0xFFFFFFFFu, r.y, c), fc, lo);
+#pragma unroll
+                for (int e = 0; e < kOwn; ++e) x[e] = fmaf(v[e], fc, x[e]);
+            }
+            const float by = lo == 0.f ? 0.f : 1.f / lo;
+            T *out = static_cast<T *>(a.out) + ((size_t)(pair / a.h_kv) * a.h_q + (size_t)(pair % a.h_kv) * a.G + q) * D + lane * kOwn;
+#pragma unroll
+            for (int e = 0; e < kOwn; ++e) out[e] = from_f<T>(x[e] * by);
+        }
+        cluster.sync();  // (no CTA goes while its record is read)
     }
 }
 
@@ -1090,7 +1151,7 @@ __global__ void __launch_bounds__(kFinishThreads, 1) q4_finish_kernel(const Q4Ar
     for (int s = tid; s <= a.B; s += kFinishThreads) prefix[s] = a.prefix[s];
     __syncthreads();
     if (prefix[a.B] == 0) return;
-    const Split split = make_split(a, prefix[a.B]);
+    const Split split = make_split(a, prefix[a.B] * a.h_kv, a.grid);
     const int c0 = blockIdx.x;
     if (c0 >= split.ctas) return;
     const int b0 = split.cta_start(c0), b1 = split.cta_start(c0 + 1);
@@ -1229,13 +1290,85 @@ zp_status q4_plan(const zp_cache_desc *D, int group, int B, int table_stride, in
     return ZP_OK;
 }
 
+// With few pairs of few tokens at most (by the table's width; the lengths are on the GPU) every
+// pair gets a cluster of CTAs of its own, which join their records in each other's shared memory: no
+// look at the other lengths, no second kernel.  A cluster is as large as gives its warps a unit each, or as fits
+// the GPU, and pairs that may have more than three units per warp take the even cut: a long one
+// among short ones would hold the others up.  Measured, cluster and even cut, with 8 kv heads of 128 in bf16:
+//     16 sequences of 100 tokens       6.3 and  9.6 us,  of 500 9.0 and 14.5
+//      1 of 1k 10.0, 11.2;  4 of 2k 10.6, 15.7;  1 of 4k 10.7, 14.1;  4 of 4k 13.1, 17.2
+//     16 of 2k (four units per warp)  16.8 and 20.2, but one of 2k in one CTA 15.2, cut evenly 11.4.
+constexpr int kMaxCluster = 16, kClusterUnits = 3;
+
+// Clusters of `size` CTAs that the GPU runs at once, 0 where it cannot.
 template <class W>
-zp_status launch_q4(const Q4Args &a, const Q4Plan &p, cudaStream_t st) {
-    const auto kernel = q4_attention_kernel<W>;
+int clusters_at_once(int size, size_t smem, int device) {
+    static std::mutex mutex;
+    static std::map<std::pair<int, int>, int> known;
+    const auto kernel = q4_attention_kernel<W, true>;
+    std::lock_guard<std::mutex> lock(mutex);
+    const auto at = known.find({device, size});
+    if (at != known.end()) return at->second;
+    int n = 0;
+    if (set_max_dynamic_smem(reinterpret_cast<const void *>(kernel), smem, "q4_decode: shared-memory attribute") != ZP_OK) return 0;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(size);
+        cfg.blockDim = dim3(W::kWarps * 32);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = size;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    }
+    if (e != cudaSuccess) {
+        n = 0;
+        cudaGetLastError();
+    }
+    known[{device, size}] = n;
+    return n;
+}
+
+// CTAs that each pair gets, 0 where the units of all pairs are better cut evenly.
+template <class W>
+int pick_cluster(const Q4Args &a, const Q4Plan &p, int device) {
+    const long long pairs = (long long)a.B * a.h_kv, units = ((long long)a.table_stride * a.b + kUnit - 1) / kUnit;
+    if (a.want_score || pairs > p.grid) return 0;
+    int size = 1;
+    while (size < kMaxCluster && units > (long long)size * W::kWarps && pairs * 2 * size <= p.grid &&
+           pairs <= clusters_at_once<W>(2 * size, p.smem, device))
+        size *= 2;
+    const long long most = (long long)size * W::kWarps * kClusterUnits;
+    return units <= most ? size : 0;
+}
+
+template <class W>
+zp_status launch_q4(Q4Args a, const Q4Plan &p, int device, cudaStream_t st) {
+    a.cluster = pick_cluster<W>(a, p, device);
+    a.inv_ranges = 0xFFFFFFFFu / (unsigned)((a.cluster ? a.cluster : p.grid) * p.warps) + 1;
+    const auto kernel = a.cluster ? q4_attention_kernel<W, true> : q4_attention_kernel<W, false>;
     zp_status rc = set_max_dynamic_smem(reinterpret_cast<const void *>(kernel), p.smem, "q4_decode: shared-memory attribute");
     if (rc != ZP_OK) return rc;
-    cudaError_t e = launch_dependent(kernel, dim3(p.grid), dim3(p.warps * 32), p.smem, st, a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.cluster ? a.B * a.h_kv * a.cluster : p.grid);
+    cfg.blockDim = dim3(p.warps * 32);
+    cfg.dynamicSmemBytes = p.smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = a.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.cluster > 1 ? 2 : 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
     if (e != cudaSuccess) return cuda_fail(e, "q4_decode: attention launch");
+    if (a.cluster) return ok();
     const auto finish = q4_finish_kernel<typename W::T, W::kD>;
     e = launch_dependent(finish, dim3(p.grid), dim3(kFinishThreads), ((size_t)a.B + 1) * 4, st, a);
     if (e != cudaSuccess) return cuda_fail(e, "q4_decode: finish launch");
@@ -1308,7 +1441,6 @@ extern "C" zp_status zp_q4_decode_attn(const zp_cache_desc *D, int32_t group, co
     a.tile = q4_tile_bytes(D->head_dim, group);
     a.tpb = D->block_size / kQ4Tile;
     a.inv_tpb = a.tpb == 1 ? 0u : 0xFFFFFFFFu / (unsigned)a.tpb + 1;
-    a.inv_ranges = 0xFFFFFFFFu / (unsigned)(p.grid * p.warps) + 1;
     a.qscale = (float)(1.4426950408889634 / sqrt((double)D->head_dim));
     a.want_score = score_accum != nullptr;
     a.window = window;
@@ -1326,5 +1458,5 @@ extern "C" zp_status zp_q4_decode_attn(const zp_cache_desc *D, int32_t group, co
     a.heads_here = p.heads_here;
     a.err = dev.error_word;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return with_warp(D, group, [&](auto w) { return launch_q4<decltype(w)>(a, p, st); });
+    return with_warp(D, group, [&](auto w) { return launch_q4<decltype(w)>(a, p, dev.device, st); });
 }
