@@ -65,6 +65,7 @@ struct Q4Args {
     float *rec;     // [2 * CTAs + warps][G * (d + 4)]: per head (reference, sum for the output, sum, 0), then accumulators
     float *logits;  // [units][32][G]
     int grid, warps, stages;  // CTAs of the attention kernel, warps of one, units in a warp's ring
+    int pair_units;           // units that the table has room for (cluster: the logits of a pair)
     int cluster;              // 0: all pairs are one line, cut evenly; else the CTAs (a cluster) of every pair
     bool heads_here;          // records of pairs that began before a warp's range: in shared memory
     unsigned *err;
@@ -835,6 +836,71 @@ struct TcWarp {
     }
 };
 
+// ---------------------------------------------------------------- the score
+constexpr int kScoreUnroll = 4;
+
+// Every 32nd token from t to t1 of a pair: S += share * 2^max_q (logit - c), or = where `fresh` and
+// at P.  G4: vectors of four heads (0: any number of heads).  All loads of a round are under way at once.
+template <int G4>
+__device__ __forceinline__ void score_tokens(const Q4Args &a, const float *lg, const float (&c)[8], float *S, int t, int t1,
+                                             int P, bool fresh, float share) {
+    for (; t < t1; t += 32 * kScoreUnroll) {
+        float top[kScoreUnroll], old[kScoreUnroll];
+        if constexpr (G4 > 0) {
+            float4 v[kScoreUnroll][G4];
+#pragma unroll
+            for (int k = 0; k < kScoreUnroll; ++k)
+#pragma unroll
+                for (int i = 0; i < G4; ++i) {
+                    const int tok = min(t + 32 * k, t1 - 1);
+                    v[k][i] = __ldcg(reinterpret_cast<const float4 *>(lg) + (size_t)tok * G4 + i);
+                }
+#pragma unroll
+            for (int k = 0; k < kScoreUnroll; ++k) {
+                const int tok = min(t + 32 * k, t1 - 1);
+                old[k] = fresh || tok == P ? 0.f : S[tok];
+            }
+#pragma unroll
+            for (int k = 0; k < kScoreUnroll; ++k) {
+                top[k] = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < G4; ++i)
+                    top[k] = fmaxf(fmaxf(top[k], fmaxf(v[k][i].x - c[4 * i], v[k][i].y - c[4 * i + 1])),
+                                   fmaxf(v[k][i].z - c[4 * i + 2], v[k][i].w - c[4 * i + 3]));
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kScoreUnroll; ++k) {
+                const int tok = min(t + 32 * k, t1 - 1);
+                top[k] = -INFINITY;
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    if (q < a.G) top[k] = fmaxf(top[k], __ldcg(lg + (size_t)tok * a.G + q) - c[q]);
+                old[k] = fresh || tok == P ? 0.f : S[tok];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kScoreUnroll; ++k)
+            if (t + 32 * k < t1) S[t + 32 * k] = fmaf(ex2_approx(top[k]), share, old[k]);
+    }
+}
+
+// The score of tokens t0 to t1 of the pair (a sequence of L tokens, kv head h), whose logits are lg, in row `row` of
+// S; lane q's norm is head q's normaliser.
+__device__ __forceinline__ void score_part(const Q4Args &a, int h, int L, int row, const float *lg, float norm, int t0,
+                                           int t1, int lane) {
+    float c[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) c[q] = __shfl_sync(0xFFFFFFFFu, norm, q);
+    const int P = L - 1;
+    const bool fresh = P % a.b == a.b - a.window;
+    const float share = 1.f / (float)a.window;
+    float *S = a.score + ((size_t)row * a.h_kv + h) * a.score_stride;
+    if (a.G == 4) score_tokens<1>(a, lg, c, S, t0 + lane, t1, P, fresh, share);
+    else if (a.G == 8) score_tokens<2>(a, lg, c, S, t0 + lane, t1, P, fresh, share);
+    else score_tokens<0>(a, lg, c, S, t0 + lane, t1, P, fresh, share);
+}
+
 // ---------------------------------------------------------------- attention
 // Shared memory: rings (a warp's tiles; at its end the record of a pair that goes on behind its
 // range), what a warp lays out for itself, records of pairs that began before a warp's range
@@ -976,7 +1042,9 @@ __global__ void __launch_bounds__(W::kWarps * 32, 1) q4_attention_kernel(const Q
                 drain(full_s[warp], stages, i, n);
                 break;
             }
-            float *lg = now & kScored ? a.logits + (size_t)(x0 + i) * (kUnit * a.G) : nullptr;
+            float *lg = nullptr;
+            if (now & kScored)
+                lg = a.logits + ((CLUSTER ? (size_t)((int)blockIdx.x / a.cluster) * a.pair_units : 0) + x0 + i) * (kUnit * a.G);
             w.unit(a, ring + st * 4 * a.tile, now & 31, now >> 5 & 31, lg, lane);
             __syncwarp();
             if (i + stages < n) issue(i + stages);
@@ -1054,34 +1122,56 @@ __global__ void __launch_bounds__(W::kWarps * 32, 1) q4_attention_kernel(const Q
         }
     }
     if constexpr (CLUSTER) {
-        if (split.ctas < 2) return;
-        // ---- the records of the cluster's CTAs, a warp per head
-        const auto cluster = cooperative_groups::this_cluster();
-        cluster.sync();
-        const int pair = (int)blockIdx.x / a.cluster, rank = (int)blockIdx.x % a.cluster;
-        for (int q = rank + a.cluster * warp; q < a.G; q += a.cluster * kWarps) {
-            constexpr int kOwn = D / 32;
-            float4 r = make_float4(-INFINITY, 0.f, 0.f, 0.f);  // lane c: CTA c's
-            if (lane < split.ctas) r = reinterpret_cast<const float4 *>(cluster.map_shared_rank(joined, lane))[q];
-            float m = r.x;
+        const int pair = (int)blockIdx.x / a.cluster, rank = (int)blockIdx.x % a.cluster, s = pair / a.h_kv, h = pair % a.h_kv;
+        __shared__ float norm_s[8];
+        float norm = INFINITY;  // of head `lane`
+        if (split.ctas > 1) {
+            // ---- the records of the cluster's CTAs, a warp per head; for a score every CTA needs every head's sum
+            const auto cluster = cooperative_groups::this_cluster();
+            cluster.sync();
+            for (int q = warp; q < a.G; q += kWarps) {
+                constexpr int kOwn = D / 32;
+                const bool mine = q % a.cluster == rank;
+                if (!mine && !a.want_score) continue;
+                float4 r = make_float4(-INFINITY, 0.f, 0.f, 0.f);  // lane c: CTA c's
+                if (lane < split.ctas) r = reinterpret_cast<const float4 *>(cluster.map_shared_rank(joined, lane))[q];
+                float m = r.x;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-            const float f = ex2_approx(r.x - (m == -INFINITY ? 0.f : m));
-            float lo = 0.f, x[kOwn] = {};
+                for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+                const float f = ex2_approx(r.x - (m == -INFINITY ? 0.f : m));
+                if (a.want_score) {
+                    float l = r.z * f;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+                    if (lane == 0) norm_s[q] = score_norm(m, l);
+                }
+                if (!mine) continue;
+                float lo = 0.f, x[kOwn] = {};
 #pragma unroll 4
-            for (int c = 0; c < split.ctas; ++c) {
-                const float *v = cluster.map_shared_rank(joined, c) + 4 * a.G + q * D + lane * kOwn;
-                const float fc = __shfl_sync(0xFFFFFFFFu, f, c);
-                lo = fmaf(__shfl_sync(0xFFFFFFFFu, r.y, c), fc, lo);
+                for (int c = 0; c < split.ctas; ++c) {
+                    const float *v = cluster.map_shared_rank(joined, c) + 4 * a.G + q * D + lane * kOwn;
+                    const float fc = __shfl_sync(0xFFFFFFFFu, f, c);
+                    lo = fmaf(__shfl_sync(0xFFFFFFFFu, r.y, c), fc, lo);
 #pragma unroll
-                for (int e = 0; e < kOwn; ++e) x[e] = fmaf(v[e], fc, x[e]);
+                    for (int e = 0; e < kOwn; ++e) x[e] = fmaf(v[e], fc, x[e]);
+                }
+                const float by = lo == 0.f ? 0.f : 1.f / lo;
+                T *out = static_cast<T *>(a.out) + ((size_t)s * a.h_q + (size_t)h * a.G + q) * D + lane * kOwn;
+#pragma unroll
+                for (int e = 0; e < kOwn; ++e) out[e] = from_f<T>(x[e] * by);
             }
-            const float by = lo == 0.f ? 0.f : 1.f / lo;
-            T *out = static_cast<T *>(a.out) + ((size_t)(pair / a.h_kv) * a.h_q + (size_t)(pair % a.h_kv) * a.G + q) * D + lane * kOwn;
-#pragma unroll
-            for (int e = 0; e < kOwn; ++e) out[e] = from_f<T>(x[e] * by);
+            cluster.sync();  // (no CTA goes while its record is read)
+            if (lane < a.G) norm = norm_s[lane];
+        } else if (a.want_score) {
+            __syncthreads();  // (this CTA has left the sums of all heads)
+            if (lane < a.G) norm = __ldcg(a.stats + (size_t)s * a.h_q + h * a.G + lane);
         }
-        cluster.sync();  // (no CTA goes while its record is read)
+        if (!a.want_score || n <= 0 || abort_s) return;
+        const int slot = slot_of(a, s), L = q4_len(a, s), row = q4_score_row(a, slot, L);
+        if (row < 0) return;
+        // ---- the score of the warp's own units
+        score_part(a, h, L, row, a.logits + (size_t)pair * a.pair_units * (kUnit * a.G), norm, x0 * kUnit, min((x0 + n) * kUnit, L),
+                   lane);
     }
 }
 
@@ -1090,57 +1180,11 @@ __global__ void __launch_bounds__(W::kWarps * 32, 1) q4_attention_kernel(const Q
 // did not finish, and forms the score of that one's units.  Bound by latencies: about 3 us behind the
 // attention kernel without a score, 20 for 256 sequences of 4k tokens, whose logits (60 MB) and
 // scores it reads; four tokens per lane at a time, and its statistics, length and slot in one go.
-constexpr int kFinishThreads = 512, kScoreUnroll = 4;
+constexpr int kFinishThreads = 512;
 
 // Record of CTA c of a pair cut between CTAs, which CTA c0 begins.
 __device__ __forceinline__ const float *cta_record(const Q4Args &a, int c0, int c, int rec_n) {
     return a.rec + (size_t)(2 * c + (c == c0 ? 1 : 0)) * rec_n;
-}
-
-// Every 32nd token from t to t1 of a pair: S += share * 2^max_q (logit - c), or = where `fresh` and
-// at P.  G4: vectors of four heads (0: any number of heads).  All loads of a round are under way at once.
-template <int G4>
-__device__ __forceinline__ void score_tokens(const Q4Args &a, const float *lg, const float (&c)[8], float *S, int t, int t1,
-                                             int P, bool fresh, float share) {
-    for (; t < t1; t += 32 * kScoreUnroll) {
-        float top[kScoreUnroll], old[kScoreUnroll];
-        if constexpr (G4 > 0) {
-            float4 v[kScoreUnroll][G4];
-#pragma unroll
-            for (int k = 0; k < kScoreUnroll; ++k)
-#pragma unroll
-                for (int i = 0; i < G4; ++i) {
-                    const int tok = min(t + 32 * k, t1 - 1);
-                    v[k][i] = __ldcg(reinterpret_cast<const float4 *>(lg) + (size_t)tok * G4 + i);
-                }
-#pragma unroll
-            for (int k = 0; k < kScoreUnroll; ++k) {
-                const int tok = min(t + 32 * k, t1 - 1);
-                old[k] = fresh || tok == P ? 0.f : S[tok];
-            }
-#pragma unroll
-            for (int k = 0; k < kScoreUnroll; ++k) {
-                top[k] = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < G4; ++i)
-                    top[k] = fmaxf(fmaxf(top[k], fmaxf(v[k][i].x - c[4 * i], v[k][i].y - c[4 * i + 1])),
-                                   fmaxf(v[k][i].z - c[4 * i + 2], v[k][i].w - c[4 * i + 3]));
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < kScoreUnroll; ++k) {
-                const int tok = min(t + 32 * k, t1 - 1);
-                top[k] = -INFINITY;
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    if (q < a.G) top[k] = fmaxf(top[k], __ldcg(lg + (size_t)tok * a.G + q) - c[q]);
-                old[k] = fresh || tok == P ? 0.f : S[tok];
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < kScoreUnroll; ++k)
-            if (t + 32 * k < t1) S[t + 32 * k] = fmaf(ex2_approx(top[k]), share, old[k]);
-    }
 }
 
 template <typename T, int D>
@@ -1209,18 +1253,8 @@ __global__ void __launch_bounds__(kFinishThreads, 1) q4_finish_kernel(const Q4Ar
                     norm = score_norm(m, l);
                 }
             }
-            float c[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) c[q] = __shfl_sync(0xFFFFFFFFu, norm, q);
-            const int P = L - 1;
-            const bool fresh = P % a.b == a.b - a.window;
-            const float share = 1.f / (float)a.window;
-            float *S = a.score + ((size_t)row * a.h_kv + cur.h) * a.score_stride;
-            const int t0 = cur.u * kUnit, t1 = min(t0 + units * kUnit, L);
-            const float *lg = a.logits + (size_t)first * kUnit * a.G;
-            if (a.G == 4) score_tokens<1>(a, lg, c, S, t0 + lane, t1, P, fresh, share);
-            else if (a.G == 8) score_tokens<2>(a, lg, c, S, t0 + lane, t1, P, fresh, share);
-            else score_tokens<0>(a, lg, c, S, t0 + lane, t1, P, fresh, share);
+            const int t0 = cur.u * kUnit;
+            score_part(a, cur.h, L, row, a.logits + (size_t)first * kUnit * a.G, norm, t0, min(t0 + units * kUnit, L), lane);
         }
         x += units;
         cur.u += units - 1;
@@ -1291,12 +1325,13 @@ zp_status q4_plan(const zp_cache_desc *D, int group, int B, int table_stride, in
 }
 
 // With few pairs of few tokens at most (by the table's width; the lengths are on the GPU) every
-// pair gets a cluster of CTAs of its own, which join their records in each other's shared memory: no
-// look at the other lengths, no second kernel.  A cluster is as large as gives its warps a unit each, or as fits
+// pair gets a cluster of CTAs of its own, which join their records in each other's shared memory and
+// form the scores of their own units: no look at the other lengths, no second kernel.  A cluster is as large as gives its warps a unit each, or as fits
 // the GPU, and pairs that may have more than three units per warp take the even cut: a long one
 // among short ones would hold the others up.  Measured, cluster and even cut, with 8 kv heads of 128 in bf16:
 //     16 sequences of 100 tokens       6.3 and  9.6 us,  of 500 9.0 and 14.5
 //      1 of 1k 10.0, 11.2;  4 of 2k 10.6, 15.7;  1 of 4k 10.7, 14.1;  4 of 4k 13.1, 17.2
+//     scored: 16 of 100 8.4, 11.0;  4 of 2k 12.5, 18.2;  16 of 500 in fp32 14.2, 18.6
 //     16 of 2k (four units per warp)  16.8 and 20.2, but one of 2k in one CTA 15.2, cut evenly 11.4.
 constexpr int kMaxCluster = 16, kClusterUnits = 3;
 
@@ -1336,8 +1371,8 @@ int clusters_at_once(int size, size_t smem, int device) {
 // CTAs that each pair gets, 0 where the units of all pairs are better cut evenly.
 template <class W>
 int pick_cluster(const Q4Args &a, const Q4Plan &p, int device) {
-    const long long pairs = (long long)a.B * a.h_kv, units = ((long long)a.table_stride * a.b + kUnit - 1) / kUnit;
-    if (a.want_score || pairs > p.grid) return 0;
+    const long long pairs = (long long)a.B * a.h_kv, units = a.pair_units;
+    if (pairs > p.grid) return 0;
     int size = 1;
     while (size < kMaxCluster && units > (long long)size * W::kWarps && pairs * 2 * size <= p.grid &&
            pairs <= clusters_at_once<W>(2 * size, p.smem, device))
@@ -1456,6 +1491,7 @@ extern "C" zp_status zp_q4_decode_attn(const zp_cache_desc *D, int32_t group, co
     a.warps = p.warps;
     a.stages = p.stages;
     a.heads_here = p.heads_here;
+    a.pair_units = (int)(((long long)table_stride * D->block_size + kUnit - 1) / kUnit);
     a.err = dev.error_word;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     return with_warp(D, group, [&](auto w) { return launch_q4<decltype(w)>(a, p, dev.device, st); });

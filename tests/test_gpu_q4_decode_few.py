@@ -91,3 +91,46 @@ def test_streams_and_graph(zp):  # noqa: F811
         c.lens = np.array([l0, l1])
         c.check(a.cpu())
 
+
+
+@pytest.mark.parametrize("extra", [0, 60, WIDE])
+@pytest.mark.parametrize("dtype,h_q,h_kv,d,group,b", SHAPES)
+@pytest.mark.parametrize("window", [4, 0])
+def test_score(zp, dtype, h_q, h_kv, d, group, b, window, extra):  # noqa: F811
+    """Written on the first step of the window, added on the others, left alone without a row, off the window and
+    behind the newest token."""
+    w = window or b
+    lens = np.array([b - w + 1, 12 * b, 2 * b - w, 8 * b])
+    c = Case(zp, lens, dtype, h_q, h_kv, d, group, b, seed=w, extra=extra)
+    rows = np.array([3, 1, 2, -1], dtype=np.int32)
+    S0 = np.random.default_rng(1).uniform(0.5, 1.0, size=(4, h_kv, c.table.shape[1] * b)).astype(np.float32)
+    S = torch.from_numpy(S0).cuda()
+    c.check(c.run(w, S, torch.from_numpy(rows).cuda()))
+    got, want, tol = S.cpu().numpy().astype(np.float64), S0.astype(np.float64), np.zeros(S0.shape)
+    for s, L in enumerate(lens):
+        P = int(L) - 1
+        if rows[s] < 0 or P % b < b - w:
+            continue
+        _, _, prob, ptol = c.reference(s)
+        new = prob.reshape(h_kv, -1, L).max(1) / w
+        rel = ptol.reshape(h_kv, -1).max(1)[:, None] + 2.0 ** -21
+        old = np.where((P % b == b - w) | (np.arange(L) == P), 0.0, want[rows[s], :, :L])
+        want[rows[s], :, :L] = old + new
+        tol[rows[s], :, :L] = rel * new + 2.0 ** -24 * (old + new) * (old > 0)
+    assert (np.abs(got - want) <= tol).all(), float((np.abs(got - want) - tol).max())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("L", [16, 512, 1040, 2048, 9008])
+def test_score_of_one(zp, dtype, L):  # noqa: F811
+    """Clusters of every size; the same scores from the even cut, to rounding."""
+    S = []
+    for extra in (0, WIDE):
+        c = Case(zp, [L], dtype, 8, 1, 128, 32, 16, seed=L, extra=extra)
+        S.append(torch.full((1, 1, c.table.shape[1] * 16), 7.0, device="cuda"))
+        c.check(c.run(1, S[-1]))
+        assert (S[-1][..., L:] == 7.0).all()
+    _, _, prob, ptol = c.reference(0)
+    for x in S:
+        got = x[0, 0, :L].cpu().double().numpy()
+        assert (np.abs(got - prob.max(0)) <= (ptol.max() + 2.0 ** -21) * prob.max(0)).all()
