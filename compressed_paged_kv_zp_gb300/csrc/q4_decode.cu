@@ -18,9 +18,8 @@
 // launched (pick_cluster).
 //
 // Bound: a 4-bit row of 128 elements is 80 bytes, for which each of 4 q heads asks 512
-// multiplications: with many tokens the issue of instructions (about 375 per tile and scheduler,
-// of which every second one goes to the half-rate integer pipe) and the memory are near one
-// another, below that the time before the first copy and after the last product.  Of keys and values,
+// multiplications: with many tokens the issue of instructions (390 of a warp for 16 tokens, nearly
+// half of them on the half-rate integer pipe) and the memory are near one another, below that the time before the first copy and after the last product.  Of keys and values,
 // 32 q and 8 kv heads of 128, groups of 32, with a copy's rate as 1:
 //     512 sequences of 1k to 4k tokens   319 us  5.2 TB/s  0.78
 //      64 of 4k at most                   51      4.1      0.62   (first copy at 4.3 us, last product at 43)
