@@ -17,14 +17,15 @@
 // With few pairs a pair's units are cut between the CTAs of a cluster instead, and nothing else is
 // launched (pick_cluster).
 //
-// Bound: a 4-bit row of 128 elements is 80 bytes, for which each of 4 q heads asks 512
-// multiplications: with many tokens the issue of instructions (390 of a warp for 16 tokens, nearly
-// half of them on the half-rate integer pipe) and the memory are near one another, below that the time before the first copy and after the last product.  Of keys and values,
-// 32 q and 8 kv heads of 128, groups of 32, with a copy's rate as 1:
-//     512 sequences of 1k to 4k tokens   319 us  5.2 TB/s  0.78
+// Bound: a 4-bit row of 128 elements is 80 bytes, for which every q head asks 128 multiplications:
+// with many tokens the issue of instructions (390 of a warp for 16 tokens, nearly half of them on
+// the half-rate integer pipe) and the memory are near one another, below that the time before the
+// first copy and after the last product.  Of keys and values, 32 q and 8 kv heads of 128, groups of
+// 32, with a copy's rate as 1:
+//     512 sequences of 1k to 4k tokens   321 us  5.2 TB/s  0.78
 //      64 of 4k at most                   51      4.1      0.62   (first copy at 4.3 us, last product at 43)
-//     256 of 4k at most, scored          174      4.0      0.59   (logits written and read besides)
-//       1 of 32k                          22      1.9      0.29   (3.4 units per warp: latencies)
+//     256 of 4k at most, scored          172      4.0      0.60   (logits written and read besides)
+//       1 of 32k                          20.5    2.0      0.31   (3.4 units per warp: latencies)
 //       4 of 2k                           10.6                    (latencies: lengths, table, tiles, join)
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
@@ -1203,21 +1204,29 @@ __global__ void __launch_bounds__(kFinishThreads, 1) q4_finish_kernel(const Q4Ar
         cut.seek(prefix, a.B, a.h_kv, b1 - 1);
         const int first = b1 - 1 - cut.u, last = first + cut.n - 1;
         if (first >= b0 && last >= b1) {
-            const int c1 = split.cta_of(last);
+            const int c1 = split.cta_of(last), n = c1 - c0 + 1;
             T *out = static_cast<T *>(a.out) + ((size_t)cut.s * a.h_q + (size_t)cut.h * a.G) * D;
             for (int i = tid; i < a.G * D; i += kFinishThreads) {
-                const int q = i / D;
+                const int q = i / D;  // the warp's: lane c has the statistics of record c (of 32 at a time)
                 float m = -INFINITY, x = 0.f, lo = 0.f;
+                for (int at = 0; at < n; at += 32) {
+                    const int c = c0 + at + lane;
+                    float2 hd = make_float2(-INFINITY, 0.f);
+                    if (c <= c1) hd = *reinterpret_cast<const float2 *>(cta_record(a, c0, c, rec_n) + 4 * q);
+                    float top = fmaxf(hd.x, m);
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                    const float base = top == -INFINITY ? 0.f : top, keep = ex2_approx(m - base), f = ex2_approx(hd.x - base);
+                    m = top;
+                    x *= keep;
+                    lo *= keep;
+                    const int most = min(32, n - at);
 #pragma unroll 8
-                for (int c = c0; c <= c1; ++c) m = fmaxf(m, cta_record(a, c0, c, rec_n)[4 * q]);
-                const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll 8
-                for (int c = c0; c <= c1; ++c) {
-                    const float *r = cta_record(a, c0, c, rec_n);
-                    const float2 hd = *reinterpret_cast<const float2 *>(r + 4 * q);
-                    const float f = ex2_approx(hd.x - base);
-                    lo = fmaf(hd.y, f, lo);
-                    x = fmaf(r[4 * a.G + i], f, x);
+                    for (int k = 0; k < most; ++k) {
+                        const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
+                        lo = fmaf(__shfl_sync(0xFFFFFFFFu, hd.y, k), fk, lo);
+                        x = fmaf(cta_record(a, c0, c0 + at + k, rec_n)[4 * a.G + i], fk, x);
+                    }
                 }
                 out[i] = from_f<T>(lo == 0.f ? 0.f : x / lo);
             }
