@@ -600,6 +600,8 @@ extern "C" zp_status zp_q4_read_kv(const zp_cache_desc *D, int32_t group, const 
     rc = check_rows(D, group, "q4_read_kv", k_out, v_out, token_stride, out_layer_stride, layer_count, k_base, v_base,
                     layer_stride);
     if (rc != ZP_OK) return rc;
+    if (layer_count > 1 && out_layer_stride < (int64_t)D->h_kv * D->head_dim)
+        return fail(ZP_ERR_INVALID_ARG, "q4_read_kv: layers of the output %lld elements apart overlap", (long long)out_layer_stride);
     DeviceInfo dev;
     rc = device_info(&dev);
     if (rc != ZP_OK) return rc;

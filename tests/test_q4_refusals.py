@@ -160,3 +160,11 @@ def test_compact_ranks(zp):
     """Ranks are counted in 32 bits, a few rounds ahead."""
     args = (_desc(zp), 32, P, P, 0, 1, None, 0, None, P, 4, P, 1 << 30, P, P)
     assert zp.lib.zp_q4_compact_pages(*args, (1 << 30) + 1, None, 1, None) == 2
+
+
+def test_read_into_one_layer(zp):
+    """Outputs of several layers that lie on one another are refused; the same rows stored into several layers are not."""
+    size = 100 * 8 * 1280
+    args = (_desc(zp), 32, P, P, size, P, 4, P, P, 1024)
+    assert zp.lib.zp_q4_read_kv(*args, 0, 2, None) == 1
+    assert zp.lib.zp_q4_read_kv(*args, 1016, 2, None) == 1
