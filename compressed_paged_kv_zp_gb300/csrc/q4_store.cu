@@ -16,7 +16,7 @@ namespace {
 // side by side.  A thread keeps its place in the row and walks over tokens.
 // Bound: for many rows the instructions, about 14 per element and lane, issued in three quarters of all cycles:
 // 64k tokens of 8 heads of 128 in bf16, 352 MB, take 69 us (5.1 TB/s, 0.76 of a plain copy's rate); for few
-// the launch (512 tokens 2.7 us).  One row at a time per thread: with two the registers cost what the second
+// the launch (512 tokens 2.5 us).  One row at a time per thread: with two the registers cost what the second
 // load in flight gains (64k tokens 70 us), and 512 tokens take longer.
 constexpr int kStoreThreads = 256, kPiece = 16;
 
@@ -188,6 +188,7 @@ __global__ void __launch_bounds__(kStoreThreads) q4_store_kernel(const StoreArgs
     const int first = blockIdx.x * a.tokens_per_cta + tok, last = min(a.n_tokens, ((int)blockIdx.x + 1) * a.tokens_per_cta);
     const int group_lanes = 1 << (a.lg_group - 4), lg_row = 2 + (D == 128 ? 7 : 6) - a.lg_group;  // log2 of a row's parameter bytes
     const long long step_rows = a.at_once * a.token_stride;
+    pdl_wait();
     // (every thread goes as often round as the first: the shuffles are the whole warp's)
     for (int c0 = 0; c0 < a.row_pieces; c0 += a.lanes_n) {
         const int c = c0 + threadIdx.x - tok * a.lanes_n, head = c / kPieces, piece = c % kPieces;
@@ -238,8 +239,8 @@ __global__ void __launch_bounds__(kStoreThreads) q4_store_kernel(const StoreArgs
 
 // ---------------------------------------------------------------- rows out
 // The same threads and walk, the other way, two rows at a time: 64k tokens of 8 heads of 128 into
-// bf16 take 60 us (5.8 TB/s, 0.87 of a plain copy's rate: bound by memory), 512 tokens 2.9; with
-// four rows 59 and 3.6, with one 64 and 2.8.
+// bf16 take 60 us (5.8 TB/s, 0.87 of a plain copy's rate: bound by memory), 512 tokens 2.5; with
+// four rows 1 us less and 0.7 more, with one 4 more and the same.
 struct ReadArgs : RowArgs {
     const unsigned char *K, *V;
     long long layer_bytes;
@@ -254,6 +255,7 @@ __global__ void __launch_bounds__(kStoreThreads) q4_read_kernel(const ReadArgs a
     const unsigned char *src = (blockIdx.z ? a.V : a.K) + (long long)blockIdx.y * a.layer_bytes;
     T *dst = static_cast<T *>(blockIdx.z ? a.v : a.k) + (long long)blockIdx.y * a.out_layer_stride;
     const int tok = a.inv_lanes ? (int)__umulhi(threadIdx.x, a.inv_lanes) : (int)threadIdx.x;
+    pdl_wait();
     if (tok >= a.at_once) return;
     const int first = blockIdx.x * a.tokens_per_cta + tok, last = min(a.n_tokens, ((int)blockIdx.x + 1) * a.tokens_per_cta);
     const int lg_row = 2 + (D == 128 ? 7 : 6) - a.lg_group;  // log2 of a row's parameter bytes
@@ -358,6 +360,7 @@ __global__ void __launch_bounds__(kMoveRanks) q4_compact_kernel(const MoveArgs a
     unsigned char *X = (tensor ? a.V : a.K) + layer * a.layer_bytes;
     float *F = a.F && tensor == 0 ? a.F + layer * a.F_layer_stride : nullptr;
     const float *Srow = nullptr;
+    pdl_wait();
     int pos_b = tid < a.k ? __ldg(kp + tid) : -1, pos_c = tid + kMoveRanks < a.k ? __ldg(kp + tid + kMoveRanks) : -1;
     int L = (int)min((long long)__ldg(a.seq_lens + s), (long long)a.table_stride * a.b);
     if (F) {
@@ -504,16 +507,11 @@ constexpr int kStoreUnroll = 1, kReadUnroll = 2;
 
 template <bool APPEND>
 zp_status launch_store(const zp_cache_desc *D, const StoreArgs &a, int layers, const char *what, cudaStream_t st) {
-    const dim3 grid = row_grid(a, layers);
     const bool wide = D->head_dim == 128;
-    if (D->dtype == ZP_BF16) {
-        if (wide) q4_store_kernel<__nv_bfloat16, 128, APPEND, kStoreUnroll><<<grid, kStoreThreads, 0, st>>>(a);
-        else q4_store_kernel<__nv_bfloat16, 64, APPEND, kStoreUnroll><<<grid, kStoreThreads, 0, st>>>(a);
-    } else {
-        if (wide) q4_store_kernel<float, 128, APPEND, kStoreUnroll><<<grid, kStoreThreads, 0, st>>>(a);
-        else q4_store_kernel<float, 64, APPEND, kStoreUnroll><<<grid, kStoreThreads, 0, st>>>(a);
-    }
-    const cudaError_t e = cudaGetLastError();
+    const auto kernel = D->dtype == ZP_BF16
+                            ? (wide ? q4_store_kernel<__nv_bfloat16, 128, APPEND, kStoreUnroll> : q4_store_kernel<__nv_bfloat16, 64, APPEND, kStoreUnroll>)
+                            : (wide ? q4_store_kernel<float, 128, APPEND, kStoreUnroll> : q4_store_kernel<float, 64, APPEND, kStoreUnroll>);
+    const cudaError_t e = launch_dependent(kernel, row_grid(a, layers), dim3(kStoreThreads), 0, st, a);
     if (e != cudaSuccess) return cuda_fail(e, what);
     return ok();
 }
@@ -615,17 +613,11 @@ extern "C" zp_status zp_q4_read_kv(const zp_cache_desc *D, int32_t group, const 
     a.token_stride = token_stride;
     a.out_layer_stride = layer_count > 1 ? out_layer_stride : 0;
     fill_rows(a, D, group, n_tokens, layer_count, kReadUnroll, row_alignment(D, k_out, v_out, token_stride, a.out_layer_stride), dev);
-    const dim3 grid = row_grid(a, layer_count);
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool wide = D->head_dim == 128;
-    if (D->dtype == ZP_BF16) {
-        if (wide) q4_read_kernel<__nv_bfloat16, 128, kReadUnroll><<<grid, kStoreThreads, 0, st>>>(a);
-        else q4_read_kernel<__nv_bfloat16, 64, kReadUnroll><<<grid, kStoreThreads, 0, st>>>(a);
-    } else {
-        if (wide) q4_read_kernel<float, 128, kReadUnroll><<<grid, kStoreThreads, 0, st>>>(a);
-        else q4_read_kernel<float, 64, kReadUnroll><<<grid, kStoreThreads, 0, st>>>(a);
-    }
-    const cudaError_t e = cudaGetLastError();
+    const auto kernel = D->dtype == ZP_BF16
+                            ? (wide ? q4_read_kernel<__nv_bfloat16, 128, kReadUnroll> : q4_read_kernel<__nv_bfloat16, 64, kReadUnroll>)
+                            : (wide ? q4_read_kernel<float, 128, kReadUnroll> : q4_read_kernel<float, 64, kReadUnroll>);
+    const cudaError_t e = launch_dependent(kernel, row_grid(a, layer_count), dim3(kStoreThreads), 0, static_cast<cudaStream_t>(stream), a);
     if (e != cudaSuccess) return cuda_fail(e, "q4_read_kv: launch");
     return ok();
 }
@@ -695,8 +687,7 @@ extern "C" zp_status zp_q4_compact_pages(const zp_cache_desc *D, int32_t group, 
     const size_t smem = (size_t)kMoveStages * move_stage_bytes(ranks, D->head_dim, D->head_dim / group);
     rc = set_max_dynamic_smem(reinterpret_cast<const void *>(kernel), smem, "q4_compact: shared-memory attribute");
     if (rc != ZP_OK) return rc;
-    kernel<<<grid, ranks, smem, static_cast<cudaStream_t>(stream)>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_dependent(kernel, grid, dim3(ranks), smem, static_cast<cudaStream_t>(stream), a);
     if (e != cudaSuccess) return cuda_fail(e, "q4_compact: launch");
     return ok();
 }
