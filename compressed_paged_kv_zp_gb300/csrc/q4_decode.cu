@@ -325,7 +325,10 @@ __device__ __forceinline__ void lds(const uint32_t *p, uint32_t (&w)[N]) {
 
 // Probabilities are kept relative to 2^(m - kScale), and m follows the maximum when that passes
 // it by kLazyMax: they stay below 2^15, so that fp16 holds them, with 11 bits down to 2^-14, that
-// is 2^-25 of 2^m's, and nothing above 2^-36 of that goes to zero.
+// is 2^-25 of 2^m's, and nothing above 2^-36 of that goes to zero.  Far from zero, where a float's
+// step is some units, m - kScale is rounded up and m + kLazyMax down: their distance, the exponent of
+// the largest weight, is never above 15.  (m = base + kScale rounded down is m again, or a step above
+// at a power of two, for which base is the same.)
 constexpr float kLazyMax = 4.f, kScale = 11.f;
 // Steps that a range's value products take in fp16: exponents from kBelow under the largest of the
 // range's first unit to kWindow - 1 - kBelow above it.
@@ -555,11 +558,11 @@ struct TcWarp {
             for (int i = 0; i < 2; ++i) {
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], o));
-                const float m = thr[i] == -INFINITY ? top[i] : fmaxf(base[i] + kScale, top[i]);
-                const float now = m == -INFINITY ? 0.f : m - kScale;
+                const float m = thr[i] == -INFINITY ? top[i] : fmaxf(__fadd_rd(base[i], kScale), top[i]);
+                const float now = m == -INFINITY ? 0.f : __fsub_ru(m, kScale);
                 const float alpha = thr[i] == -INFINITY ? 0.f : ex2_approx(base[i] - now);
                 base[i] = now;
-                thr[i] = m + kLazyMax;
+                thr[i] = __fadd_rd(m, kLazyMax);
                 l[i] *= alpha;
                 off[i] *= alpha;
                 off[i + 2] *= alpha;
