@@ -61,7 +61,7 @@ struct Q4Args {
     const int32_t *score_rows;
     int n_score_rows;
     int *prefix;    // [B+1] units before each sequence (of one kv head)
-    float *stats;   // [B][h_q] reference + log2(sum) of the pairs that one CTA saw whole
+    float2 *stats;  // [B][h_q] reference and log2(sum) of the pairs that one CTA saw whole
     float *rec;     // [2 * CTAs + warps][G * (d + 4)]: per head (reference, sum for the output, sum, 0), then accumulators
     float *logits;  // [units][32][G]
     int grid, warps, stages;  // CTAs of the attention kernel, warps of one, units in a warp's ring
@@ -221,8 +221,11 @@ __device__ __noinline__ void drain(uint64_t *full, int stages, int i, int n) {
 // instead of by a second kernel, 1 x 32k took 28 us: 19 CTAs meet on its counter.)
 __device__ __forceinline__ int rec_floats(const Q4Args &a, int d) { return a.G * (d + 4); }
 
-// Normaliser of the score: p = 2^(logit - c).  An empty sum gives no score.
-__device__ __forceinline__ float score_norm(float m, float l) { return l == 0.f ? INFINITY : m + log2f(l); }
+// Normaliser of the score: p = 2^((logit - x) - y).  (Not in one number: far from zero the
+// reference's step is larger than the logarithm.)  An empty sum gives no score.
+__device__ __forceinline__ float2 score_norm(float m, float l) {
+    return l == 0.f ? make_float2(INFINITY, 0.f) : make_float2(m, log2f(l));
+}
 
 // ---------------------------------------------------------------- tensor-core products
 // Up to 8 q heads as the 8 columns of mma.sync m16n8k16: logits[t][h] with the key codes as the
@@ -842,10 +845,12 @@ struct TcWarp {
 // ---------------------------------------------------------------- the score
 constexpr int kScoreUnroll = 4;
 
-// Every 32nd token from t to t1 of a pair: S += share * 2^max_q (logit - c), or = where `fresh` and
+__device__ __forceinline__ float less(float logit, float2 c) { return (logit - c.x) - c.y; }
+
+// Every 32nd token from t to t1 of a pair: S += share * 2^max_q ((logit - c.x) - c.y), or = where `fresh` and
 // at P.  G4: vectors of four heads (0: any number of heads).  All loads of a round are under way at once.
 template <int G4>
-__device__ __forceinline__ void score_tokens(const Q4Args &a, const float *lg, const float (&c)[8], float *S, int t, int t1,
+__device__ __forceinline__ void score_tokens(const Q4Args &a, const float *lg, const float2 (&c)[8], float *S, int t, int t1,
                                              int P, bool fresh, float share) {
     for (; t < t1; t += 32 * kScoreUnroll) {
         float top[kScoreUnroll], old[kScoreUnroll];
@@ -868,8 +873,8 @@ __device__ __forceinline__ void score_tokens(const Q4Args &a, const float *lg, c
                 top[k] = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < G4; ++i)
-                    top[k] = fmaxf(fmaxf(top[k], fmaxf(v[k][i].x - c[4 * i], v[k][i].y - c[4 * i + 1])),
-                                   fmaxf(v[k][i].z - c[4 * i + 2], v[k][i].w - c[4 * i + 3]));
+                    top[k] = fmaxf(fmaxf(top[k], fmaxf(less(v[k][i].x, c[4 * i]), less(v[k][i].y, c[4 * i + 1]))),
+                                   fmaxf(less(v[k][i].z, c[4 * i + 2]), less(v[k][i].w, c[4 * i + 3])));
             }
         } else {
 #pragma unroll
@@ -878,7 +883,7 @@ __device__ __forceinline__ void score_tokens(const Q4Args &a, const float *lg, c
                 top[k] = -INFINITY;
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
-                    if (q < a.G) top[k] = fmaxf(top[k], __ldcg(lg + (size_t)tok * a.G + q) - c[q]);
+                    if (q < a.G) top[k] = fmaxf(top[k], less(__ldcg(lg + (size_t)tok * a.G + q), c[q]));
                 old[k] = fresh || tok == P ? 0.f : S[tok];
             }
         }
@@ -890,11 +895,11 @@ __device__ __forceinline__ void score_tokens(const Q4Args &a, const float *lg, c
 
 // The score of tokens t0 to t1 of the pair (a sequence of L tokens, kv head h), whose logits are lg, in row `row` of
 // S; lane q's norm is head q's normaliser.
-__device__ __forceinline__ void score_part(const Q4Args &a, int h, int L, int row, const float *lg, float norm, int t0,
+__device__ __forceinline__ void score_part(const Q4Args &a, int h, int L, int row, const float *lg, float2 norm, int t0,
                                            int t1, int lane) {
-    float c[8];
+    float2 c[8];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) c[q] = __shfl_sync(0xFFFFFFFFu, norm, q);
+    for (int q = 0; q < 8; ++q) c[q] = make_float2(__shfl_sync(0xFFFFFFFFu, norm.x, q), __shfl_sync(0xFFFFFFFFu, norm.y, q));
     const int P = L - 1;
     const bool fresh = P % a.b == a.b - a.window;
     const float share = 1.f / (float)a.window;
@@ -1126,8 +1131,8 @@ __global__ void __launch_bounds__(W::kWarps * 32, 1) q4_attention_kernel(const Q
     }
     if constexpr (CLUSTER) {
         const int pair = (int)blockIdx.x / a.cluster, rank = (int)blockIdx.x % a.cluster, s = pair / a.h_kv, h = pair % a.h_kv;
-        __shared__ float norm_s[8];
-        float norm = INFINITY;  // of head `lane`
+        __shared__ float2 norm_s[8];
+        float2 norm = make_float2(INFINITY, 0.f);  // of head `lane`
         if (split.ctas > 1) {
             // ---- the records of the cluster's CTAs, a warp per head; for a score every CTA needs every head's sum
             const auto cluster = cooperative_groups::this_cluster();
@@ -1245,7 +1250,7 @@ __global__ void __launch_bounds__(kFinishThreads, 1) q4_finish_kernel(const Q4Ar
     for (int x = x0; x < x1;) {
         const int units = min(cur.n - cur.u, x1 - x);  // the rest of this pair
         // three loads at once; normalisers of the heads: lane q has head q's
-        float norm = lane < a.G ? __ldcg(a.stats + (size_t)cur.s * a.h_q + cur.h * a.G + lane) : INFINITY;
+        float2 norm = lane < a.G ? __ldcg(a.stats + (size_t)cur.s * a.h_q + cur.h * a.G + lane) : make_float2(INFINITY, 0.f);
         const int slot = slot_of(a, cur.s), L = q4_len(a, cur.s), row = q4_score_row(a, slot, L);
         if (row >= 0) {
             const int first = x - cur.u, last = first + cur.n - 1;
@@ -1326,7 +1331,7 @@ zp_status q4_plan(const zp_cache_desc *D, int group, int B, int table_stride, in
     p->off_prefix = off;
     off = align_up(off + ((size_t)B + 1) * 4, 256);
     p->off_stats = off;
-    off = align_up(off + (size_t)B * D->h_q * 4, 256);
+    off = align_up(off + (size_t)B * D->h_q * 8, 256);
     p->off_rec = off;
     off = align_up(off + (size_t)(2 + p->warps) * p->grid * G * (d + 4) * 4, 256);
     p->off_logits = off;
@@ -1495,7 +1500,7 @@ extern "C" zp_status zp_q4_decode_attn(const zp_cache_desc *D, int32_t group, co
     a.score_rows = score_accum ? score_rows : nullptr;
     a.n_score_rows = n_score_rows;
     a.prefix = reinterpret_cast<int *>(ws + p.off_prefix);
-    a.stats = reinterpret_cast<float *>(ws + p.off_stats);
+    a.stats = reinterpret_cast<float2 *>(ws + p.off_stats);
     a.rec = reinterpret_cast<float *>(ws + p.off_rec);
     a.logits = reinterpret_cast<float *>(ws + p.off_logits);
     a.grid = p.grid;

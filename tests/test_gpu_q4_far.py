@@ -82,3 +82,36 @@ def test_one_value(zp, dtype, scale, extra):  # noqa: F811
         each, L = 2.0 ** -11 if dtype == "bf16" else 2.0 ** -22, int(c.lens[s])
         tol = (2 * each + L * 2.0 ** -23) * a + torch.finfo(out_type(dtype)).eps / 2 * 1.01 * np.abs(want)
         assert (np.abs(out[s] - want) <= tol).all(), (s, float((np.abs(out[s] - want) / tol).max()))
+
+
+@BOTH
+@DTYPES
+@pytest.mark.parametrize("top", [0.0, 3e4, 3e7, 1.5e8, 1e12, -3e4, -3e7, -1.5e8, -1e12])
+def test_score_of_equal_logits(zp, dtype, top, extra):  # noqa: F811
+    """Scored on the first step of the window: each of L tokens has a share of 1 / L."""
+    c = Case(zp, [289, 33, 1, 4097], dtype, 8, 2, 64, 32, 16, seed=5, extra=extra)
+    code = np.zeros(64, np.uint8)
+    word = _words(np.full(2, 0.25, np.float32), np.array([top / (32 / 8 * np.log2(np.e)), -1.0], np.float32))
+    _set_live(c, c.K, lambda s, t, h: (code, word))
+    c.q[..., :32] = 1.0
+    S = torch.full((4, 2, c.table.shape[1] * 16), 9.0, device="cuda")
+    c.run(16, S)
+    for s in range(c.B):
+        L = int(c.lens[s])
+        got = S[s, :, :L].cpu().double().numpy() * 16 * L
+        # two differences of at most 32 rounded to 32 bits (2^-20 each), a logarithm, an exponential and a product
+        assert (np.abs(got - 1) <= 2.0 ** -18 + L * 2.0 ** -24).all(), (s, float(np.abs(got - 1).max()))
+        assert (S[s, :, L:] == 9.0).all()
+
+
+@BOTH
+@DTYPES
+@pytest.mark.parametrize("scale", [1.0, 1e3, 3e6, 2.5e7, 1e8, 1e10])
+def test_scores_add_up(zp, dtype, scale, extra):  # noqa: F811
+    """One q head per kv head: the scores of a sequence are its probabilities, whatever the logits are."""
+    c = Case(zp, [289, 33, 1, 1025], dtype, 2, 2, 64, 32, 16, seed=11, extra=extra, q_scale=scale)
+    S = torch.zeros(4, 2, c.table.shape[1] * 16, device="cuda")
+    c.run(16, S)
+    for s in range(c.B):
+        total = S[s].cpu().double().numpy().sum(-1) * 16
+        assert (np.abs(total - 1) <= 2.0 ** -18 + int(c.lens[s]) * 2.0 ** -24).all(), (s, total)
