@@ -333,10 +333,14 @@ __device__ __forceinline__ void lds(const uint32_t *p, uint32_t (&w)[N]) {
 // the largest weight, is never above 15.  (m = base + kScale rounded down is m again, or a step above
 // at a power of two, for which base is the same.)
 constexpr float kLazyMax = 4.f, kScale = 11.f;
-// Steps that a range's value products take in fp16: exponents from kBelow under the largest of the
-// range's first unit to kWindow - 1 - kBelow above it.
-constexpr int kBelow = 10, kWindow = 14;
+// Steps that a group's value products take in fp16: kWindow exponents, from kBelow under the largest step
+// of the range's first unit on, but none below 2^-34 (kLowest): the accumulators then hold no more than the
+// sums they stand for (rescale).  Where a later unit has steps past the window, and all of its steps fit a
+// window of its own, the window moves up to that.
+constexpr int kBelow = 10, kWindow = 14, kLowest = 127 - 34;
 constexpr uint32_t kNoWindow = 0xFFFFFFFFu;
+// byte g of `wins` for a largest step of exponent `top`
+__device__ __forceinline__ uint32_t window_for(int top) { return min(max(top - kBelow, kLowest), 255 - kWindow) - 1; }
 
 // x, y as the sum of N bf16 pairs
 template <int N>
@@ -605,8 +609,24 @@ struct TcWarp {
         w[2] = codes<E, CENTRE>(x1), w[3] = codes<E + 1, CENTRE>(x1);
     }
 
+    // Moves windows up to the steps of a unit that were not in them.
+    __device__ __forceinline__ void raise_windows(const unsigned char *vt, int v0, int v1, int lane) {
+        uint32_t w[NG];
+        lds<NG>(reinterpret_cast<const uint32_t *>(vt + (lane >> 4) * kTile + q4_code_bytes(D)) + (lane & 15) * NG, w);
+        const bool live = (lane & 15) < (lane < kQ4Tile ? v0 : v1);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const uint32_t exponent = (w[g] & 0x7F80u) >> 7;
+            const uint32_t to = window_for((int)__reduce_max_sync(0xFFFFFFFFu, live ? exponent : 0u));
+            if (to > window(g) && !__any_sync(0xFFFFFFFFu, live && exponent - (to + 1) >= (uint32_t)kWindow))
+                wins += (to - window(g)) << (8 * g);
+        }
+    }
+
     // The accumulators of the value products in fp16 hold 2^(89 - e) times the sums of p step c (e:
-    // the window's lowest exponent), 16 times that for odd dimensions; to and from sums of p step c.
+    // the window's lowest exponent, kLowest = 93 or more), 16 times that for odd dimensions; to and
+    // from sums of p step c.  Neither is larger than those sums, which are finite for values below 2^92:
+    // windows of any lower exponent had let ordinary values pass the largest float after units of flat groups.
     // (In two factors: the power may be past the largest float.)
     __device__ __forceinline__ void rescale(bool plain) {
 #pragma unroll
@@ -638,7 +658,7 @@ struct TcWarp {
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     const int top = (int)__reduce_max_sync(0xFFFFFFFFu, live ? w[g] & 0x7F80u : 0u) >> 7;
-                    wins |= (uint32_t)(min(max(top - kBelow, 1), 255 - kWindow) - 1) << (8 * g);
+                    wins |= window_for(top) << (8 * g);
                 }
             }
             bool out = false;
@@ -677,6 +697,7 @@ struct TcWarp {
         if (wild) {
             rescale(true);
             values_wide(vt, p, at, lane);
+            raise_windows(vt, v0, v1, lane);
             rescale(false);
             return;
         }
