@@ -242,11 +242,13 @@ __device__ __forceinline__ float2 score_norm(float m, float l) {
 //     the logits are those of 32-bit arithmetic.
 //   output:  sum_t p_t lo_t + sum_t p_t step_t c_t.  The first is a product of p (two bf16 parts,
 //     transposed by movmatrix) with the parameters as they are.  For the second p goes to fp16 and
-//     its product with the step of a group to fp16 again, each rounded by 2^-12 at most; the codes
-//     are subnormals once more.  For that a step's exponent is moved by what suits the range's
-//     first unit.  A unit with steps far from those (p step needs bf16's range) takes its products
-//     in bf16, with codes 0x4300 | c = 128 + c less 128; both roundings are then by 2^-9.  The sum
-//     that divides is that of p in two parts.
+//     its product with the step of a group to fp16 again, each off by 2^-11 of itself at most; the codes
+//     are subnormals once more.  (Both in two fp16 parts: 64 sequences of 4k at most 56 us instead of
+//     51, 512 365 instead of 319.  The output's own rounding is by up to 2^-8.)  For that a step's exponent
+//     is moved by what suits the first unit of a run.  A unit with steps far from those (p step needs
+//     bf16's range) takes its products in bf16, p step in two parts that are off by 2^-15 at most, with
+//     codes 0x4300 | c = 128 + c less 128, and the run ends there.  The sum that divides is that of p in
+//     two bf16 parts (2^-17).
 //   fp32 queries: three parts of 8 bits of the query for the logits; for the output p and p step in
 //     three bf16 parts each, with codes c - 8 and the parameters' sum of lo + 8 step, and every
 //     unit's products are summed from zero and added to the accumulators in 32 bits, since the
@@ -295,6 +297,11 @@ __device__ __forceinline__ uint32_t mul_bf2(uint32_t a, uint32_t b) {
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+__device__ __forceinline__ uint32_t fma_bf2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
 __device__ __forceinline__ uint32_t f2_to_h2(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
@@ -334,11 +341,10 @@ __device__ __forceinline__ void lds(const uint32_t *p, uint32_t (&w)[N]) {
 // at a power of two, for which base is the same.)
 constexpr float kLazyMax = 4.f, kScale = 11.f;
 // Steps that a group's value products take in fp16: kWindow exponents, from kBelow under the largest step
-// of the range's first unit on, but none below 2^-34 (kLowest): the accumulators then hold no more than the
-// sums they stand for (rescale).  Where a later unit has steps past the window, and all of its steps fit a
-// window of its own, the window moves up to that.
+// of a run's first unit on, but none below 2^-34 (kLowest): the accumulators then hold no more than the
+// sums they stand for (rescale).  A run of units ends with the first that has a live step outside.
 constexpr int kBelow = 10, kWindow = 14, kLowest = 127 - 34;
-constexpr uint32_t kNoWindow = 0xFFFFFFFFu;
+constexpr uint32_t kNoWindow = 0xFFFFFFFFu, kPlain = 0xFFFFFFFEu;  // no unit yet; the accumulators are plain sums
 // byte g of `wins` for a largest step of exponent `top`
 __device__ __forceinline__ uint32_t window_for(int top) { return min(max(top - kBelow, kLowest), 255 - kWindow) - 1; }
 
@@ -368,7 +374,7 @@ struct TcWarp {
     float acc[kChunks][2][4], off[4];
     float thr[2], base[2], l[2];  // of those two heads: m + kLazyMax (-inf: none yet), m - kScale, sum over this lane's tokens
     uint4 *params;     // bf16 queries: of a unit's values, by two tokens: steps in fp16 and lo in bf16, by group
-    uint32_t wins;     // bf16 queries: by group a byte, lowest exponent, less 1, of the steps taken in fp16; kNoWindow: none yet
+    uint32_t wins;     // bf16 queries: by group a byte, lowest exponent, less 1, of the steps taken in fp16; or kNoWindow, kPlain
     __device__ __forceinline__ uint32_t window(int g) const { return wins >> (8 * g) & 0xFFu; }
 
     struct Query {  // eight elements of each chunk
@@ -609,20 +615,6 @@ struct TcWarp {
         w[2] = codes<E, CENTRE>(x1), w[3] = codes<E + 1, CENTRE>(x1);
     }
 
-    // Moves windows up to the steps of a unit that were not in them.
-    __device__ __forceinline__ void raise_windows(const unsigned char *vt, int v0, int v1, int lane) {
-        uint32_t w[NG];
-        lds<NG>(reinterpret_cast<const uint32_t *>(vt + (lane >> 4) * kTile + q4_code_bytes(D)) + (lane & 15) * NG, w);
-        const bool live = (lane & 15) < (lane < kQ4Tile ? v0 : v1);
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            const uint32_t exponent = (w[g] & 0x7F80u) >> 7;
-            const uint32_t to = window_for((int)__reduce_max_sync(0xFFFFFFFFu, live ? exponent : 0u));
-            if (to > window(g) && !__any_sync(0xFFFFFFFFu, live && exponent - (to + 1) >= (uint32_t)kWindow))
-                wins += (to - window(g)) << (8 * g);
-        }
-    }
-
     // The accumulators of the value products in fp16 hold 2^(89 - e) times the sums of p step c (e:
     // the window's lowest exponent, kLowest = 93 or more), 16 times that for odd dimensions; to and
     // from sums of p step c.  Neither is larger than those sums, which are finite for values below 2^92:
@@ -653,13 +645,15 @@ struct TcWarp {
             uint32_t w[NG];
             lds<NG>(reinterpret_cast<const uint32_t *>(vt + (lane >> 4) * kTile + q4_code_bytes(D)) + (lane & 15) * NG, w);
             const bool live = (lane & 15) < (lane < kQ4Tile ? v0 : v1);
-            if (wins == kNoWindow) {
+            if (wins >= kPlain) {
+                const bool again = wins == kPlain;
                 wins = 0;
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     const int top = (int)__reduce_max_sync(0xFFFFFFFFu, live ? w[g] & 0x7F80u : 0u) >> 7;
                     wins |= window_for(top) << (8 * g);
                 }
+                if (again) rescale(false);
             }
             bool out = false;
 #pragma unroll
@@ -697,8 +691,7 @@ struct TcWarp {
         if (wild) {
             rescale(true);
             values_wide(vt, p, at, lane);
-            raise_windows(vt, v0, v1, lane);
-            rescale(false);
+            wins = kPlain;
             return;
         }
 #pragma unroll
@@ -731,13 +724,15 @@ struct TcWarp {
         }
     }
 
-    // The values' products where steps of any size meet: p, and p step, rounded to bf16, the codes
-    // as bf16 numbers.
+    // The values' products where steps of any size meet: p step in two bf16 parts, the codes as bf16 numbers.
     __device__ __forceinline__ void values_wide(const unsigned char *vt, const float (&p)[2][4], uint32_t at, int lane) {
         const int j = lane & 3;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            const uint32_t b0 = transpose8(f2_to_bf2(p[b][0], p[b][1])), b1 = transpose8(f2_to_bf2(p[b][2], p[b][3]));
+            uint32_t u0[2], u1[2];
+            split_bf2(p[b][0], p[b][1], u0);
+            split_bf2(p[b][2], p[b][3], u1);
+            const uint32_t b0 = transpose8(u0[0]), b1 = transpose8(u1[0]), e0 = transpose8(u0[1]), e1 = transpose8(u1[1]);
             const uint32_t *vp = reinterpret_cast<const uint32_t *>(vt + b * kTile + q4_code_bytes(D)) + 2 * j * NG;
             const uint32_t va = smem_u32(vt + b * kTile) + at;
 #pragma unroll
@@ -747,13 +742,19 @@ struct TcWarp {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int g = (c + i) / kPerGroup;
-                    const uint32_t s0 = mul_bf2(b0, __byte_perm(vp[g], vp[NG + g], 0x5410));
-                    const uint32_t s1 = mul_bf2(b1, __byte_perm(vp[8 * NG + g], vp[9 * NG + g], 0x5410));
-                    uint32_t w[4];
-                    code_rows<0, 0>(r[2 * i], r[2 * i + 1], w);
-                    mma_bf16(acc[c + i][0], w[0], w[1], w[2], w[3], s0, s1);
-                    code_rows<2, 0>(r[2 * i], r[2 * i + 1], w);
-                    mma_bf16(acc[c + i][1], w[0], w[1], w[2], w[3], s0, s1);
+                    const uint32_t w0 = __byte_perm(vp[g], vp[NG + g], 0x5410), w1 = __byte_perm(vp[8 * NG + g], vp[9 * NG + g], 0x5410);
+                    uint32_t s0 = mul_bf2(b0, w0), s1 = mul_bf2(b1, w1);
+#pragma unroll 1
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t w[4];
+                        code_rows<0, 0>(r[2 * i], r[2 * i + 1], w);
+                        mma_bf16(acc[c + i][0], w[0], w[1], w[2], w[3], s0, s1);
+                        code_rows<2, 0>(r[2 * i], r[2 * i + 1], w);
+                        mma_bf16(acc[c + i][1], w[0], w[1], w[2], w[3], s0, s1);
+                        // what is left (b w - s is a number of bf16); one copy of the code, seldom run
+                        s0 = fma_bf2(e0, w0, fma_bf2(b0, w0, s0 ^ 0x80008000u));
+                        s1 = fma_bf2(e1, w1, fma_bf2(b1, w1, s1 ^ 0x80008000u));
+                    }
                 }
             }
         }
@@ -814,7 +815,8 @@ struct TcWarp {
     // heads 2j, 2j + 1: dimensions 32c + 4n .. + 3 in acc[c], the sums of the rounded p in off[2..3] and of p in l
     __device__ __forceinline__ void end(int lane) {
         const int j = lane & 3;
-        if constexpr (!kF32) rescale(true);
+        if constexpr (!kF32)
+            if (wins != kPlain) rescale(true);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
