@@ -123,7 +123,7 @@ __device__ __forceinline__ int checked_len(const Q4Args &a, int L) {
     return L;
 }
 __device__ __forceinline__ int units_of(int L) { return (int)(((long long)L + kUnit - 1) / kUnit); }
-__device__ __forceinline__ int q4_len(const Q4Args &a, int s) { return checked_len(a, __ldg(a.seq_lens + s)); }
+__device__ __forceinline__ int q4_len(const Q4Args &a, int s) { return checked_len(a, __ldg(from_here(a.seq_lens) + s)); }
 
 // prefix[s] = units of the sequences before s; blockDim.x threads, a multiple of 32.
 __device__ void unit_prefix(const Q4Args &a, int *prefix, int *warp_sum) {
@@ -192,7 +192,7 @@ struct Cursor {
 };
 
 // Row of S that entry s, with entry r of the slot map (without one: s), scores into on this step, -1 = none.
-__device__ __forceinline__ int slot_of(const Q4Args &a, int s) { return a.score_rows ? __ldg(a.score_rows + s) : s; }
+__device__ __forceinline__ int slot_of(const Q4Args &a, int s) { return a.score_rows ? __ldg(from_here(a.score_rows) + s) : s; }
 __device__ __forceinline__ int q4_score_row(const Q4Args &a, int r, int L) {
     if (!a.want_score || L < 1 || (L - 1) % a.b < a.b - a.window) return -1;
     if (a.score_rows && r >= a.n_score_rows) {
@@ -387,7 +387,7 @@ struct TcWarp {
     };
     static __device__ __forceinline__ Query fetch(const Q4Args &a, int s, int h, int lane) {
         const int n = lane >> 2, j = lane & 3;
-        const T *q = static_cast<const T *>(a.q) + ((size_t)s * a.h_q + (size_t)h * a.G + n) * D + j * 8;
+        const T *q = from_here(static_cast<const T *>(a.q)) + ((size_t)s * a.h_q + (size_t)h * a.G + n) * D + j * 8;
         Query x;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
@@ -927,6 +927,7 @@ __device__ __forceinline__ void score_part(const Q4Args &a, int h, int L, int ro
     const bool fresh = P % a.b == a.b - a.window;
     const float share = 1.f / (float)a.window;
     float *S = a.score + ((size_t)row * a.h_kv + h) * a.score_stride;
+    lg = from_here(lg);
     if (a.G == 4) score_tokens<1>(a, lg, c, S, t0 + lane, t1, P, fresh, share);
     else if (a.G == 8) score_tokens<2>(a, lg, c, S, t0 + lane, t1, P, fresh, share);
     else score_tokens<0>(a, lg, c, S, t0 + lane, t1, P, fresh, share);
@@ -1005,7 +1006,7 @@ __global__ void __launch_bounds__(W::kWarps * 32, 1) q4_attention_kernel(const Q
             for (int b = 0; b < 2; ++b) {
                 const int col = div_by(2 * c.u + b, a.tpb, a.inv_tpb);
                 sub[b] = 2 * c.u + b - col * a.tpb;
-                blk[b] = col < a.table_stride ? __ldg(a.table + (size_t)c.s * a.table_stride + col) : -1;
+                blk[b] = col < a.table_stride ? __ldg(from_here(a.table) + (size_t)c.s * a.table_stride + col) : -1;
             }
             const int slot = a.want_score ? slot_of(a, c.s) : -1;
             const int L = q4_len(a, c.s);
@@ -1195,7 +1196,7 @@ __global__ void __launch_bounds__(W::kWarps * 32, 1) q4_attention_kernel(const Q
             if (lane < a.G) norm = norm_s[lane];
         } else if (a.want_score) {
             __syncthreads();  // (this CTA has left the sums of all heads)
-            if (lane < a.G) norm = __ldcg(a.stats + (size_t)s * a.h_q + h * a.G + lane);
+            if (lane < a.G) norm = __ldcg(from_here(a.stats) + (size_t)s * a.h_q + h * a.G + lane);
         }
         if (!a.want_score || n <= 0 || abort_s) return;
         const int slot = slot_of(a, s), L = q4_len(a, s), row = q4_score_row(a, slot, L);
@@ -1273,7 +1274,7 @@ __global__ void __launch_bounds__(kFinishThreads, 1) q4_finish_kernel(const Q4Ar
     for (int x = x0; x < x1;) {
         const int units = min(cur.n - cur.u, x1 - x);  // the rest of this pair
         // three loads at once; normalisers of the heads: lane q has head q's
-        float2 norm = lane < a.G ? __ldcg(a.stats + (size_t)cur.s * a.h_q + cur.h * a.G + lane) : make_float2(INFINITY, 0.f);
+        float2 norm = lane < a.G ? __ldcg(from_here(a.stats) + (size_t)cur.s * a.h_q + cur.h * a.G + lane) : make_float2(INFINITY, 0.f);
         const int slot = slot_of(a, cur.s), L = q4_len(a, cur.s), row = q4_score_row(a, slot, L);
         if (row >= 0) {
             const int first = x - cur.u, last = first + cur.n - 1;

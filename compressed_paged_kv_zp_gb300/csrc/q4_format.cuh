@@ -23,6 +23,19 @@ constexpr uint32_t kQ4NaN = 0x7FC07FC0u;  // step and lo of a group that holds a
 __host__ __device__ constexpr int q4_code_bytes(int d) { return kQ4Tile * d / 2; }
 __host__ __device__ constexpr int q4_tile_bytes(int d, int group) { return q4_code_bytes(d) + kQ4Tile * 4 * (d / group); }
 
+// The same value, which the compiler knows only from here on.  What is loaded from an address that comes from
+// it stays behind the waits and barriers before: they are volatile as this is, and a load without a memory
+// clobber (a read-only or cached one) is otherwise free to pass them.  Costs no instruction.
+template <typename T>
+__device__ __forceinline__ T *from_here(T *p) {
+    asm volatile("" : "+l"(p));
+    return p;
+}
+__device__ __forceinline__ int from_here(int x) {
+    asm volatile("" : "+r"(x));
+    return x;
+}
+
 template <int D>
 __host__ __device__ __forceinline__ int q4_chunk(int t, int c) {
     return D == 128 ? (c ^ ((t >> 1) & 3)) : (c ^ ((t >> 2) & 1));

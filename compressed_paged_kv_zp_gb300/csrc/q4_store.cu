@@ -156,21 +156,21 @@ struct StoreArgs : RowArgs {
 template <bool APPEND>
 __device__ __forceinline__ int store_slot(const StoreArgs &a, int i) {
     if constexpr (APPEND) {
-        const int L = __ldg(a.seq_lens + i), b = a.tpb * kQ4Tile;
+        const int L = __ldg(from_here(a.seq_lens) + i), b = a.tpb * kQ4Tile;
         if (L == 0) return -1;  // no token for this sequence in this step
         if (L < 0 || L > (long long)a.table_stride * b) {
             record_error(a.err, ZP_ERR_DEVICE, 0x151);
             return -1;
         }
         const int P = L - 1;
-        const long long blk = __ldg(a.table + (size_t)i * a.table_stride + P / b);
+        const long long blk = __ldg(from_here(a.table) + (size_t)i * a.table_stride + P / b);
         if (blk < 0 || (blk + 1) * b > a.n_slots) {
             record_error(a.err, ZP_ERR_DEVICE, 0x152);
             return -1;
         }
         return (int)(blk * b + P % b);
     } else {
-        const int slot = __ldg(a.slots + i);
+        const int slot = __ldg(from_here(a.slots) + i);
         if (slot >= a.n_slots) {
             record_error(a.err, ZP_ERR_DEVICE, 0x150);
             return -1;
@@ -191,7 +191,8 @@ __global__ void __launch_bounds__(kStoreThreads) q4_store_kernel(const StoreArgs
     pdl_wait();
     // (every thread goes as often round as the first: the shuffles are the whole warp's)
     for (int c0 = 0; c0 < a.row_pieces; c0 += a.lanes_n) {
-        const int c = c0 + threadIdx.x - tok * a.lanes_n, head = c / kPieces, piece = c % kPieces;
+        const int c = from_here((int)(c0 + threadIdx.x - tok * a.lanes_n));  // (the rows' addresses come from it)
+        const int head = c / kPieces, piece = c % kPieces;
         const bool works = tok < a.at_once && c < a.row_pieces;
         const T *from = src + (long long)first * a.token_stride + c * kPiece;
         unsigned char *base = dst + (size_t)head * a.tpb * a.tile;
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(kStoreThreads) q4_read_kernel(const ReadArgs a
     for (int c = threadIdx.x - tok * a.lanes_n; c < a.row_pieces; c += a.lanes_n) {
         const int head = c / kPieces, piece = c % kPieces;
         T *to = dst + (long long)first * a.token_stride + c * kPiece;
-        const unsigned char *base = src + (size_t)head * a.tpb * a.tile;
+        const unsigned char *base = from_here(src) + (size_t)head * a.tpb * a.tile;
         const int par_at = q4_code_bytes(D) + (piece * kPiece >> a.lg_group) * 4;
         for (int i0 = first; i0 < last; i0 += U * a.at_once) {
             uint2 word[U];
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kStoreThreads) q4_read_kernel(const ReadArgs a
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int i = i0 + u * a.at_once;
-                slot[u] = i < last ? __ldg(a.slots + i) : -1;
+                slot[u] = i < last ? __ldg(from_here(a.slots) + i) : -1;
                 if (slot[u] >= a.n_slots) {
                     record_error(a.err, ZP_ERR_DEVICE, 0x153);
                     slot[u] = -1;
@@ -361,10 +362,11 @@ __global__ void __launch_bounds__(kMoveRanks) q4_compact_kernel(const MoveArgs a
     float *F = a.F && tensor == 0 ? a.F + layer * a.F_layer_stride : nullptr;
     const float *Srow = nullptr;
     pdl_wait();
+    kp = from_here(kp), table = from_here(table), dst = from_here(dst);
     int pos_b = tid < a.k ? __ldg(kp + tid) : -1, pos_c = tid + kMoveRanks < a.k ? __ldg(kp + tid + kMoveRanks) : -1;
-    int L = (int)min((long long)__ldg(a.seq_lens + s), (long long)a.table_stride * a.b);
+    int L = (int)min((long long)__ldg(from_here(a.seq_lens) + s), (long long)a.table_stride * a.b);
     if (F) {
-        const int row = a.S_rows ? __ldg(a.S_rows + s) : s;
+        const int row = a.S_rows ? __ldg(from_here(a.S_rows) + s) : s;
         if (row < 0) {
             if (tid == 0) record_error(a.err, ZP_ERR_DEVICE, 0x156);
             F = nullptr;
@@ -373,7 +375,7 @@ __global__ void __launch_bounds__(kMoveRanks) q4_compact_kernel(const MoveArgs a
             if (L > a.S_stride) L = (int)a.S_stride;
         }
     }
-    const int kk = min(a.k_seq ? min(__ldg(a.k_seq + s), a.k) : a.k, L);
+    const int kk = min(a.k_seq ? min(__ldg(from_here(a.k_seq) + s), a.k) : a.k, L);
     const int rounds = (kk + kMoveRanks - 1) / kMoveRanks;
     auto block_of = [&](int pos) { return pos >= 0 && pos < L ? __ldg(table + pos / a.b) : -1; };
     int pos = pos_b, blk = block_of(pos_b);  // of the next round to copy
