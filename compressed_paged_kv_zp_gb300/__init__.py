@@ -303,9 +303,7 @@ def _ints(t, dev: int, name: str, numel=None):
 
 
 def _device() -> int:
-    if torch.cuda.is_initialized():
-        return torch._C._cuda_getDevice()
-    return torch.cuda.current_device() if torch.cuda.is_available() else -2
+    return torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -2
 
 
 def _raw_stream(stream, dev: int) -> int:
@@ -636,11 +634,11 @@ def zp_q4_decode_attn(desc, q, k_cache, v_cache, block_table, seq_lens, out, sco
             if len(_Q4_SIZES) > 1000:
                 _Q4_SIZES.clear()
             n = _Q4_SIZES[key] = zp_q4_decode_workspace_size(desc, B, table_stride, group, score_accum is not None)
-        at = torch._C._cuda_cudaCachingAllocator_raw_alloc(n, on)
+        at = torch.cuda.caching_allocator_alloc(n, dev, on)
         try:
             rc = lib.zp_q4_decode_attn(*args, at, n, on)
         finally:
-            torch._C._cuda_cudaCachingAllocator_raw_delete(at)
+            torch.cuda.caching_allocator_delete(at)
     else:
         rc = lib.zp_q4_decode_attn(*args, _ptr_on(workspace, dev, "workspace"), workspace.nbytes, on)
     if rc:
