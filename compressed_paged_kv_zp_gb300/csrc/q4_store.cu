@@ -470,6 +470,27 @@ zp_status check_rows(const zp_cache_desc *D, int group, const char *what, const 
     return ZP_OK;
 }
 
+// Do rows of k and v, of any tokens and layers, have a byte in common?  (Tokens are a row apart at least.)
+bool rows_meet(const zp_cache_desc *D, const void *k, const void *v, int64_t n, int64_t token_stride, int64_t layer_stride,
+               int64_t layers) {
+    const int64_t es = elem_bytes(D->dtype), row = (int64_t)D->h_kv * D->head_dim * es, ts = token_stride * es;
+    const int64_t ls = layers > 1 ? layer_stride * es : 0, apart = (int64_t)((uintptr_t)v - (uintptr_t)k);
+    // two lines of n rows, one `by` bytes behind the other: the multiples of ts next to `by` decide
+    auto meet = [&](int64_t by) {
+        if (by < 0) by = -by;
+        const int64_t i = by / ts;
+        return (i < n && by - i * ts < row) || (i + 1 < n && (i + 1) * ts - by < row);
+    };
+    if (ls < (n - 1) * ts + row)  // (else every layer is behind the one before)
+        for (int64_t l = 1; l < layers; ++l)
+            if (meet(l * ls)) return true;
+    const int64_t all = (layers - 1) * ls + (n - 1) * ts + row;
+    if (apart < all && -apart < all)
+        for (int64_t l = 1 - layers; l < layers; ++l)
+            if (meet(apart + l * ls)) return true;
+    return false;
+}
+
 // Bits that the addresses of rows have in common with their strides.
 uintptr_t row_alignment(const zp_cache_desc *D, const void *k, const void *v, int64_t token_stride, int64_t layer_stride) {
     const int64_t es = elem_bytes(D->dtype);
@@ -600,8 +621,9 @@ extern "C" zp_status zp_q4_read_kv(const zp_cache_desc *D, int32_t group, const 
     rc = check_rows(D, group, "q4_read_kv", k_out, v_out, token_stride, out_layer_stride, layer_count, k_base, v_base,
                     layer_stride);
     if (rc != ZP_OK) return rc;
-    if (layer_count > 1 && out_layer_stride < (int64_t)D->h_kv * D->head_dim)
-        return fail(ZP_ERR_INVALID_ARG, "q4_read_kv: layers of the output %lld elements apart overlap", (long long)out_layer_stride);
+    if (rows_meet(D, k_out, v_out, n_tokens, token_stride, out_layer_stride, layer_count))
+        return fail(ZP_ERR_INVALID_ARG, "q4_read_kv: rows of the output lie on one another (token stride %lld, layer stride %lld)",
+                    (long long)token_stride, (long long)out_layer_stride);
     DeviceInfo dev;
     rc = device_info(&dev);
     if (rc != ZP_OK) return rc;

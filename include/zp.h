@@ -534,7 +534,8 @@ zp_status zp_q4_append_kv(const zp_cache_desc *D, int32_t group, const void *k_n
  * layers out_layer_stride elements apart) receives the values of slot slots[i], lo + c * step
  * in 32 bits, rounded once to dtype.  The row of a negative slot is left as it was; a
  * slot >= N_total * b is recorded (detail 0x153) and its row left too.  A slot may be named more than
- * once; layers less than a row apart are refused (ZP_ERR_INVALID_ARG). */
+ * once; rows of the output that lie on one another, of whichever tokens, layers and of k_out and v_out,
+ * are refused (ZP_ERR_INVALID_ARG). */
 zp_status zp_q4_read_kv(const zp_cache_desc *D, int32_t group, const void *k_base, const void *v_base,
                         int64_t layer_stride, const int32_t *slots, int32_t n_tokens, void *k_out, void *v_out,
                         int64_t token_stride, int64_t out_layer_stride, int32_t layer_count, void *stream);
