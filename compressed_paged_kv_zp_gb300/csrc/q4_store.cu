@@ -586,6 +586,7 @@ extern "C" zp_status zp_q4_append_kv(const zp_cache_desc *D, int32_t group, cons
     if (rc != ZP_OK) return rc;
     if (B < 0 || table_stride < 1)
         return fail(ZP_ERR_INVALID_ARG, "q4_append_kv: B=%d table_stride=%d", B, table_stride);
+    if (B > 1 << 30) return fail(ZP_ERR_SHAPE, "q4_append_kv: %d tokens", B);
     if (B == 0) return ok();
     if (!k_new || !v_new || !k_cache || !v_cache || !block_table || !seq_lens)
         return fail(ZP_ERR_INVALID_ARG, "q4_append_kv: NULL buffer");

@@ -87,3 +87,9 @@ def test_read_rows_on_one_another(zp):
                         assert _read(zp, FAR, FAR + dv, n, ts, ls, layers) == want, (n, ts, ls, layers, dv)
                         some.add((want, layers > 1, n > 1))
     assert len(some) == 8
+
+
+def test_append_tokens(zp):
+    """As every call: no more than 2^30 tokens."""
+    desc = ctypes.byref(zp.cache_desc(32, 8, 128, 16, 100, torch.bfloat16))
+    assert zp.lib.zp_q4_append_kv(desc, 32, P, P, P, P, P, 1, P, (1 << 30) + 1, None) == 2
