@@ -50,8 +50,8 @@ __device__ __forceinline__ uint32_t bf16_below(float x) {
 // The word (step, lo) of a group whose smallest and largest element are mn and mx
 // (NaN if one of its elements is): lo is the bf16 value at or below mn, the step the
 // smallest bf16 value of which fifteen reach from lo to mx, so that no element is further than
-// half a step from its code's value.  For bf16 elements lo is mn itself.  The step is at
-// least 2^-126 (its reciprocal is finite).
+// half a step, and what x - lo is rounded by, from its code's value.  For bf16 elements lo is mn
+// itself.  The step is at least 2^-126 (its reciprocal is finite).
 __device__ __forceinline__ uint32_t q4_params(float mn, float mx) {
     const uint32_t lo = bf16_below(mn);
     const float flo = __uint_as_float(lo << 16), spread = mx - flo;

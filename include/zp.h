@@ -506,7 +506,8 @@ zp_status zp_compress_layers_rho(const zp_cache_desc *D, const zp_score_params *
  *   Quantising a group of elements x (32-bit arithmetic): lo is the largest bf16
  *            value <= min x; step the smallest bf16 value >= (max x - lo) / 15, at least
  *            2^-126; c = floor((x - lo) / step + 1/2) with the quotient not rounded.  So
- *            |x - (lo + c * step)| <= step / 2, and for bf16 rows lo is min x.  A group with a
+ *            |x - (lo + c * step)| <= step / 2 + 2^-24 (x - lo), the latter for the rounding of
+ *            x - lo, and for bf16 rows lo is min x.  A group with a
  *            NaN or an infinity, or with a spread past the largest float, reads as NaN.
  * D is the descriptor of the rows (dtype: of q, of the rows given and taken, of the output).
  * Limits of every call: d in {64, 128}, b a multiple of 16, h_kv <= 256, N_total * b
