@@ -244,11 +244,11 @@ __device__ __forceinline__ float2 score_norm(float m, float l) {
 //     transposed by movmatrix) with the parameters as they are.  For the second p goes to fp16 and
 //     its product with the step of a group to fp16 again, each off by 2^-11 of itself at most; the codes
 //     are subnormals once more.  (Both in two fp16 parts: 64 sequences of 4k at most 56 us instead of
-//     51, 512 365 instead of 319.  The output's own rounding is by up to 2^-8.)  For that a step's exponent
-//     is moved by what suits the first unit of a run.  A unit with steps far from those (p step needs
+//     51, 512 365 instead of 324.  The output's own rounding is by up to 2^-8.)  For that a step's exponent
+//     is moved by what suits an earlier unit.  A unit with steps far from that one's (p step needs
 //     bf16's range) takes its products in bf16, p step in two parts that are off by 2^-15 at most, with
-//     codes 0x4300 | c = 128 + c less 128, and the run ends there.  The sum that divides is that of p in
-//     two bf16 parts (2^-17).
+//     codes 0x4300 | c = 128 + c less 128, and the next units' exponents are moved by what suits it.  The
+//     sum that divides is that of p in two bf16 parts (2^-17).
 //   fp32 queries: three parts of 8 bits of the query for the logits; for the output p and p step in
 //     three bf16 parts each, with codes c - 8 and the parameters' sum of lo + 8 step, and every
 //     unit's products are summed from zero and added to the accumulators in 32 bits, since the
@@ -341,10 +341,10 @@ __device__ __forceinline__ void lds(const uint32_t *p, uint32_t (&w)[N]) {
 // at a power of two, for which base is the same.)
 constexpr float kLazyMax = 4.f, kScale = 11.f;
 // Steps that a group's value products take in fp16: kWindow exponents, from kBelow under the largest step
-// of a run's first unit on, but none below 2^-34 (kLowest): the accumulators then hold no more than the
-// sums they stand for (rescale).  A run of units ends with the first that has a live step outside.
+// of some unit on, but none below 2^-34 (kLowest): the accumulators then hold no more than the sums
+// they stand for (rescale).  The unit is a range's first, then every one with a live step outside.
 constexpr int kBelow = 10, kWindow = 14, kLowest = 127 - 34;
-constexpr uint32_t kNoWindow = 0xFFFFFFFFu, kPlain = 0xFFFFFFFEu;  // no unit yet; the accumulators are plain sums
+constexpr uint32_t kNoWindow = 0xFFFFFFFFu;  // no unit yet
 // byte g of `wins` for a largest step of exponent `top`
 __device__ __forceinline__ uint32_t window_for(int top) { return min(max(top - kBelow, kLowest), 255 - kWindow) - 1; }
 
@@ -374,7 +374,7 @@ struct TcWarp {
     float acc[kChunks][2][4], off[4];
     float thr[2], base[2], l[2];  // of those two heads: m + kLazyMax (-inf: none yet), m - kScale, sum over this lane's tokens
     uint4 *params;     // bf16 queries: of a unit's values, by two tokens: steps in fp16 and lo in bf16, by group
-    uint32_t wins;     // bf16 queries: by group a byte, lowest exponent, less 1, of the steps taken in fp16; or kNoWindow, kPlain
+    uint32_t wins;     // bf16 queries: by group a byte, lowest exponent, less 1, of the steps taken in fp16; or kNoWindow
     __device__ __forceinline__ uint32_t window(int g) const { return wins >> (8 * g) & 0xFFu; }
 
     struct Query {  // eight elements of each chunk
@@ -615,6 +615,17 @@ struct TcWarp {
         w[2] = codes<E, CENTRE>(x1), w[3] = codes<E + 1, CENTRE>(x1);
     }
 
+    // (The first unit's are chosen beside its other look at the steps: 256 short sequences 0.7 us less.)
+    __device__ __forceinline__ void choose_windows(const unsigned char *vt, int v0, int v1, int lane) {
+        uint32_t w[NG];
+        lds<NG>(reinterpret_cast<const uint32_t *>(vt + (lane >> 4) * kTile + q4_code_bytes(D)) + (lane & 15) * NG, w);
+        const bool live = (lane & 15) < (lane < kQ4Tile ? v0 : v1);
+        wins = 0;
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+            wins |= window_for((int)__reduce_max_sync(0xFFFFFFFFu, live ? w[g] & 0x7F80u : 0u) >> 7) << (8 * g);
+    }
+
     // The accumulators of the value products in fp16 hold 2^(89 - e) times the sums of p step c (e:
     // the window's lowest exponent, kLowest = 93 or more), 16 times that for odd dimensions; to and
     // from sums of p step c.  Neither is larger than those sums, which are finite for values below 2^92:
@@ -645,15 +656,13 @@ struct TcWarp {
             uint32_t w[NG];
             lds<NG>(reinterpret_cast<const uint32_t *>(vt + (lane >> 4) * kTile + q4_code_bytes(D)) + (lane & 15) * NG, w);
             const bool live = (lane & 15) < (lane < kQ4Tile ? v0 : v1);
-            if (wins >= kPlain) {
-                const bool again = wins == kPlain;
+            if (wins == kNoWindow) {
                 wins = 0;
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     const int top = (int)__reduce_max_sync(0xFFFFFFFFu, live ? w[g] & 0x7F80u : 0u) >> 7;
                     wins |= window_for(top) << (8 * g);
                 }
-                if (again) rescale(false);
             }
             bool out = false;
 #pragma unroll
@@ -691,7 +700,8 @@ struct TcWarp {
         if (wild) {
             rescale(true);
             values_wide(vt, p, at, lane);
-            wins = kPlain;
+            choose_windows(vt, v0, v1, lane);
+            rescale(false);
             return;
         }
 #pragma unroll
@@ -816,7 +826,7 @@ struct TcWarp {
     __device__ __forceinline__ void end(int lane) {
         const int j = lane & 3;
         if constexpr (!kF32)
-            if (wins != kPlain) rescale(true);
+            rescale(true);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
