@@ -22,11 +22,11 @@
 // the half-rate integer pipe) and the memory are near one another, below that the time before the
 // first copy and after the last product.  Of keys and values, 32 q and 8 kv heads of 128, groups of
 // 32, with a copy's rate as 1:
-//     512 sequences of 1k to 4k tokens   321 us  5.2 TB/s  0.78
+//     512 sequences of 1k to 4k tokens   324 us  5.2 TB/s  0.78
 //      64 of 4k at most                   51      4.1      0.62   (first copy at 4.3 us, last product at 43)
 //     256 of 4k at most, scored          172      4.0      0.60   (logits written and read besides)
-//       1 of 32k                          20.5    2.0      0.31   (3.4 units per warp: latencies)
-//       4 of 2k                           10.6                    (latencies: lengths, table, tiles, join)
+//       1 of 32k                          20.7    2.0      0.31   (3.4 units per warp: latencies)
+//       4 of 2k                           12.6                    (latencies: lengths, table, tiles, join)
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -947,8 +947,8 @@ __device__ __forceinline__ void score_part(const Q4Args &a, int h, int L, int ro
 // Shared memory: rings (a warp's tiles; at its end the record of a pair that goes on behind its
 // range), what a warp lays out for itself, records of pairs that began before a warp's range
 // (written while the ring is in use; in the workspace where there is no room), prefix.
-// Sixteen warps of 128 registers in bf16, twelve of 168 in fp32 (10, 13 and 14 were slower for
-// either), each with a ring of its own: no barrier between them, and 2 to 4 units (5 KB each at
+// Sixteen warps of 128 registers in bf16 (12 bytes spilled at d = 128 and groups of 32), twelve of 168 in
+// fp32 (92) (10, 13 and 14 were slower for either), each with a ring of its own: no barrier between them, and 2 to 4 units (5 KB each at
 // d = 128 and groups of 32) in flight per warp are 160 KB and more per SM.
 template <class W>
 __host__ __device__ inline size_t attention_smem(int stages, int tile, int B, int G, bool heads_here) {
@@ -1379,10 +1379,10 @@ zp_status q4_plan(const zp_cache_desc *D, int group, int B, int table_stride, in
 // form the scores of their own units: no look at the other lengths, no second kernel.  A cluster is as large as gives its warps a unit each, or as fits
 // the GPU, and pairs that may have more than three units per warp take the even cut: a long one
 // among short ones would hold the others up.  Measured, cluster and even cut, with 8 kv heads of 128 in bf16:
-//     16 sequences of 100 tokens       6.3 and  9.6 us,  of 500 9.0 and 14.5
-//      1 of 1k 10.0, 11.2;  4 of 2k 10.6, 15.7;  1 of 4k 10.7, 14.1;  4 of 4k 13.1, 17.2
-//     scored: 16 of 100 8.4, 11.0;  4 of 2k 12.5, 18.2;  16 of 500 in fp32 14.2, 18.6
-//     16 of 2k (four units per warp)  16.8 and 20.2, but one of 2k in one CTA 15.2, cut evenly 11.4.
+//     16 sequences of 100 tokens       6.7 and  9.2 us,  of 500 9.6 and 13.8
+//      1 of 1k 10.3, 11.0;  4 of 2k 12.6, 13.5;  1 of 4k 12.6, 12.7;  4 of 4k 13.6, 16.0
+//     scored: 16 of 100 8.0, 11.1;  4 of 2k 14.5, 16.4;  16 of 500 in fp32 13.3, 18.5
+//     16 of 2k (four units per warp)  16.5 and 19.5, but one of 2k in one CTA 15.2, cut evenly 11.4.
 constexpr int kMaxCluster = 16, kClusterUnits = 3;
 
 // Clusters of `size` CTAs that the GPU runs at once, 0 where it cannot.

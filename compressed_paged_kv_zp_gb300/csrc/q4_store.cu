@@ -15,9 +15,9 @@ namespace {
 // time, and a thread's codes are 8 bytes, so the 8 lanes of a row of 128 write its 64 bytes
 // side by side.  A thread keeps its place in the row and walks over tokens.
 // Bound: for many rows the instructions, about 14 per element and lane, issued in three quarters of all cycles:
-// 64k tokens of 8 heads of 128 in bf16, 352 MB, take 69 us (5.1 TB/s, 0.76 of a plain copy's rate); for few
-// the launch (512 tokens 2.5 us).  One row at a time per thread: with two the registers cost what the second
-// load in flight gains (64k tokens 70 us), and 512 tokens take longer.
+// 64k tokens of 8 heads of 128 in bf16, 352 MB, take 67 us (5.2 TB/s, 0.78 of a plain copy's rate); for few
+// the launch (512 tokens 2.6 us).  One row at a time per thread: with two the registers cost what the second
+// load in flight gains (64k tokens 1 us more), and 512 tokens take longer.
 constexpr int kStoreThreads = 256, kPiece = 16;
 
 __device__ __forceinline__ float min_nan(float a, float b) {
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kStoreThreads) q4_store_kernel(const StoreArgs
 
 // ---------------------------------------------------------------- rows out
 // The same threads and walk, the other way, two rows at a time: 64k tokens of 8 heads of 128 into
-// bf16 take 60 us (5.8 TB/s, 0.87 of a plain copy's rate: bound by memory), 512 tokens 2.5; with
+// bf16 take 58 us (6.0 TB/s, 0.90 of a plain copy's rate: bound by memory), 1,024 tokens 2.8; with
 // four rows 1 us less and 0.7 more, with one 4 more and the same.
 struct ReadArgs : RowArgs {
     const unsigned char *K, *V;
@@ -311,9 +311,9 @@ __global__ void __launch_bounds__(kStoreThreads) q4_read_kernel(const ReadArgs a
 // ahead of earlier stores, and the move is right in place too.  A row in flight costs no registers
 // that way, and the look-ups (position, then block) run a round or two ahead of the copies.
 // Bound: memory, where a row has 64 bytes of codes and 16 of parameters far from them.  16 sequences, 4080 of 32k
-// tokens each, 8 heads of 128: 51 us for 84 MB of rows, for which 232 MB are read and 49 MB written (5.5 TB/s);
-// 7 sequences of 2032 rows 12.8 us, a chain of five latencies (length, position, block, row, store).
-// Rows that went through registers, a round's loads before its stores, took 104 us with the read-back that takes 57.
+// tokens each, 8 heads of 128: 56 us for 84 MB of rows, for which 232 MB are read and 49 MB written (5.0 TB/s);
+// 7 sequences of 2032 rows 12.5 us, a chain of five latencies (length, position, block, row, store).
+// Rows that went through registers, a round's loads before its stores, took 104 us where the ring took 58.
 constexpr int kMoveStages = 4;
 
 __device__ __forceinline__ void copy_async(void *to, const void *from, int bytes) {  // 4, 8 or 16
@@ -702,8 +702,8 @@ extern "C" zp_status zp_q4_compact_pages(const zp_cache_desc *D, int32_t group, 
     a.lg_words = log2_of(D->head_dim / group);
     a.tile = q4_tile_bytes(D->head_dim, group);
     a.err = dev.error_word;
-    // Rounds of 512 ranks where every CTA has an SM of its own (7 sequences of 2032 ranks 12.8 us,
-    // with 256 14.8), of 256 and two or more CTAs per SM where there are more (16 of 4080: 58 us, 69).
+    // Rounds of 512 ranks where every CTA has an SM of its own (7 sequences of 2032 ranks 12.5 us,
+    // with 256 16.5), of 256 and two or more CTAs per SM where there are more (16 of 4080: 56 us, 60).
     const dim3 grid(2 * D->h_kv, n, layer_count);
     const bool few = (long long)grid.x * grid.y * grid.z <= dev.sm_count, wide = D->head_dim == 128;
     const int ranks = few ? 512 : 256;

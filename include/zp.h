@@ -544,13 +544,13 @@ zp_status zp_q4_read_kv(const zp_cache_desc *D, int32_t group, const void *k_bas
 /* zp_paged_decode_attn over a 4-bit cache: the same output, window score, skipping
  * of L = 0, slot map and arguments, with k_t and v_t the values the codes stand for (not
  * rounded to dtype).  q and out are dtype and do not overlap (ZP_ERR_INVALID_ARG).  Slots behind a
- * sequence's last token may hold anything.  bf16: for the output a token's probability and
- * its product with a group's step are each rounded to 11 bits, and a probability below 2^-36 of the
- * largest may count as none; 32 tokens with a step more than 10 exponents below or 3 above the
- * largest of earlier ones, or below 2^-34 (a flat group's is 2^-126), are rounded to 15 bits instead.
- * Logits, softmax statistics and scores are those of 32-bit arithmetic.  fp32: three parts of 8 bits
- * or more of each factor.  Queries of 2^118
- * and more in size give NaN, values of 2^92 and more may (weights are held up to 2^15 times too
+ * sequence's last token may hold anything.  bf16: for the output a token's probability and its
+ * product with a group's step are each rounded to 11 bits, and a probability below 2^-36 of the
+ * largest (2^-25 with logits of 2^24 and more) may count as none; 32 tokens with a step more than 10
+ * exponents below or 3 above the largest of earlier ones, or below 2^-34 (a flat group's is 2^-126),
+ * are rounded to 15 bits instead.  Logits, softmax statistics and scores are those of 32-bit
+ * arithmetic.  fp32: three parts of 8 bits or more of each factor.  Queries of 2^118 and more in
+ * size give NaN, values of 2^92 and more may (weights are held up to 2^15 times too
  * large until the end).  A call with the same arguments gives the same bits.  Recorded as
  * ZP_ERR_DEVICE: a length outside [0, table_stride * b] (detail 0x158; taken as the nearer bound), a
  * block outside [0, N_total) among a sequence's blocks (0x159; its tokens weigh nothing), a slot
